@@ -14,6 +14,8 @@ LIB_PATH = os.path.join(HERE, "libwave.so")
 
 WAVE_OK, WAVE_EINVAL, WAVE_ECUDA, WAVE_ELAUNCH = 0, -1, -2, -3
 WAVE_ETIMEOUT, WAVE_EPOS, WAVE_EDEVICE, WAVE_ENOMEM = -4, -5, -6, -7
+WAVE_F32, WAVE_BF16, WAVE_F16 = 0, 1, 2
+WAVE_MAX_SEQS = 128
 
 
 class WaveConfig(ctypes.Structure):
@@ -54,7 +56,8 @@ EXPORTS = ("wave_create", "wave_destroy", "wave_weights_bytes", "wave_weight_off
            "wave_set_timeout_ns", "wave_debug_skip_barrier", "wave_debug_skip_signal", "wave_debug_dump_kv", "wave_debug_dump_acts",
            "wave_debug_act_record_floats", "wave_debug_phase_times", "wave_debug_arrival_times",
            "wave_grid_size", "wave_barriers_per_step", "wave_phases_per_step", "wave_hybrid_create", "wave_hybrid_step",
-           "wave_hybrid_weights_bytes", "wave_hybrid_layer_offset")
+           "wave_hybrid_weights_bytes", "wave_hybrid_layer_offset",
+           "wave_prompt_append", "wave_prompt_attention", "wave_hybrid_prompt_state", "wave_sessions_copy")
 
 
 def lib() -> ctypes.CDLL:
@@ -127,6 +130,15 @@ def lib() -> ctypes.CDLL:
         L.wave_barriers_per_step.restype = i32
         L.wave_phases_per_step.argtypes = [vp]
         L.wave_phases_per_step.restype = i32
+        i32p = ctypes.POINTER(ctypes.c_int32)
+        L.wave_prompt_append.argtypes = [vp, i32, i32, i32p, i32p, i32p, vp, i32, i64, vp, vp, vp, vp, vp, i32, vp]
+        L.wave_prompt_append.restype = i32
+        L.wave_prompt_attention.argtypes = [vp, i32, i32p, i32, i32, vp, i64, vp, i64, vp, i64, ctypes.c_float, vp, i64, vp]
+        L.wave_prompt_attention.restype = i32
+        L.wave_hybrid_prompt_state.argtypes = [vp, i32, vp, i32, i32p, i32p, i32p, vp, i64, vp, vp, vp, i64, vp]
+        L.wave_hybrid_prompt_state.restype = i32
+        L.wave_sessions_copy.argtypes = [vp, i32, i32p, i32p, i32, vp, vp, vp, vp, vp]
+        L.wave_sessions_copy.restype = i32
         _lib = L
     return _lib
 
@@ -141,6 +153,35 @@ def _ptr(t) -> int | None:
     if isinstance(t, int):
         return t
     return t.data_ptr()
+
+
+def _ints(values):
+    """A host array of int32 (any sequence of integers)."""
+    values = [int(v) for v in values]
+    return (ctypes.c_int32 * max(1, len(values)))(*values), len(values)
+
+
+def _type_of(t) -> int:
+    import torch
+    return {torch.float32: WAVE_F32, torch.bfloat16: WAVE_BF16, torch.float16: WAVE_F16}.get(t.dtype, -1)
+
+
+def _rows(t, heads: bool, what: str) -> int:
+    """The row stride in elements of a packed tensor [rows][H][D] (heads) or
+    [rows][values]; what lies inside a row has to be contiguous."""
+    inner = (t.shape[2], 1) if heads else (1,)
+    if t.dim() != len(inner) + 1 or (t.numel() and any(n > 1 and a != b for n, a, b in zip(t.shape[1:], t.stride()[1:], inner))):
+        raise ValueError(f"{what}: a packed tensor of rows, contiguous inside a row, is wanted")
+    width = 1
+    for n in t.shape[1:]:
+        width *= n
+    return t.stride(0) if t.shape[0] > 1 else width
+
+
+def _covered(cu, n_cu: int, what: str, *tensors) -> None:
+    """Every packed buffer has the rows that cu names."""
+    if n_cu < 2 or any(t is not None and t.shape[0] < cu[n_cu - 1] for t in tensors):
+        raise ValueError(f"{what}: cu_seqlens names more rows than a buffer has")
 
 
 def _stream(stream) -> int:
@@ -229,6 +270,63 @@ class Wave:
                              int(bool(advance)), _ptr(x), _ptr(y), _stream(stream))
         if check and rc != WAVE_OK:
             raise WaveError(rc, "wave_beat")
+        return rc
+
+    def prompt_append(self, layer, cu_seqlens, slots, starts, qkv, kv, kv_scales, q=None, k=None, v=None,
+                      stream=None, check=True) -> int:
+        """wave_prompt_append: RoPE, FP8 quantisation and append of packed
+        prompts to layer `layer`'s history.  cu_seqlens, slots and starts are
+        host integers; qkv is [rows][3*H*D] (fp32 or bf16, rows may be
+        strided); q, k, v (each optional) are contiguous [rows][H][D] outputs
+        of one 16-bit type: the rotated q and the k, v that the history now
+        holds."""
+        (cu, n_cu), (sl, n_sl), (s0, n_s0) = _ints(cu_seqlens), _ints(slots), _ints(starts)
+        if n_sl != n_cu - 1 or n_s0 != n_cu - 1:
+            raise ValueError("wave_prompt_append: one slot and one start for each sequence")
+        outs = [t for t in (q, k, v) if t is not None]
+        H, D = self.cfg.n_heads, self.cfg.head_dim
+        if any(tuple(t.shape[1:]) != (H, D) or not t.is_contiguous() or t.dtype != outs[0].dtype for t in outs):
+            raise ValueError("wave_prompt_append: q, k and v are contiguous [rows][H][D], of one type")
+        if qkv.dim() != 2 or qkv.shape[1] != 3 * H * D:
+            raise ValueError("wave_prompt_append: qkv is [rows][3*H*D]")
+        _covered(cu, n_cu, "wave_prompt_append", qkv, *outs)
+        rc = lib().wave_prompt_append(self.h, layer, n_cu - 1, cu, sl, s0, _ptr(qkv), _type_of(qkv),
+                                      _rows(qkv, False, "qkv"), _ptr(kv), _ptr(kv_scales), _ptr(q), _ptr(k), _ptr(v),
+                                      _type_of(outs[0]) if outs else WAVE_BF16, _stream(stream))
+        if check and rc != WAVE_OK:
+            raise WaveError(rc, "wave_prompt_append")
+        return rc
+
+    def prompt_attention(self, cu_seqlens, q, k, v, out, scale=None, stream=None, check=True) -> int:
+        """wave_prompt_attention: causal attention over packed prompts.  q and
+        out are [rows][n_heads][D], k and v [rows][n_kv_heads][D], all bf16 or
+        all fp16, rows may be strided; scale defaults to 1/sqrt(D)."""
+        cu, n_cu = _ints(cu_seqlens)
+        H, D = self.cfg.n_heads, self.cfg.head_dim
+        if any(t.dtype != q.dtype for t in (k, v, out)) or k.shape[1:] != v.shape[1:] or k.shape[-1] != D \
+                or tuple(q.shape[1:]) != (H, D) or tuple(out.shape[1:]) != (H, D):
+            raise ValueError("wave_prompt_attention: q, out [rows][n_heads][D] and k, v [rows][n_kv_heads][D] of one type")
+        strides = [_rows(t, True, "wave_prompt_attention") for t in (q, k, v, out)]
+        _covered(cu, n_cu, "wave_prompt_attention", q, k, v, out)
+        rc = lib().wave_prompt_attention(self.h, n_cu - 1, cu, k.shape[1], _type_of(q), _ptr(q), strides[0], _ptr(k),
+                                         strides[1], _ptr(v), strides[2], D ** -0.5 if scale is None else scale,
+                                         _ptr(out), strides[3], _stream(stream))
+        if check and rc != WAVE_OK:
+            raise WaveError(rc, "wave_prompt_attention")
+        return rc
+
+    def sessions_copy(self, src, dst, kv, kv_scales, positions, state=None, move=False, stream=None,
+                      check=True) -> int:
+        """wave_sessions_copy: sessions src (host integers) copied to slots dst:
+        history, position and, for a hybrid handle, the recurrent state.  With
+        move the sources are freed (position -1)."""
+        (s, n), (d, n_d) = _ints(src), _ints(dst)
+        if n != n_d:
+            raise ValueError("wave_sessions_copy: one destination for each source")
+        rc = lib().wave_sessions_copy(self.h, n, s, d, int(bool(move)), _ptr(kv), _ptr(kv_scales), _ptr(state),
+                                      _ptr(positions), _stream(stream))
+        if check and rc != WAVE_OK:
+            raise WaveError(rc, "wave_sessions_copy")
         return rc
 
     def status(self, sync: bool = True) -> int:
@@ -355,6 +453,28 @@ class HybridWave(Wave):
                                     _ptr(positions), _ptr(x), _ptr(y), _stream(stream))
         if check and rc != WAVE_OK:
             raise WaveError(rc, "wave_hybrid_step")
+        return rc
+
+    def prompt_state(self, layer, weights, cu_seqlens, slots, starts, zxbcdt, state_in, state_out, out, stream=None,
+                     check=True) -> int:
+        """wave_hybrid_prompt_state: the selective-state block `layer` over
+        packed prompts.  zxbcdt is bf16 [rows][in_rows] and out bf16
+        [rows][d_inner], rows may be strided; state_in (None when every start
+        is 0) and state_out are the fp32 state, which may be one buffer."""
+        (cu, n_cu), (sl, n_sl), (s0, n_s0) = _ints(cu_seqlens), _ints(slots), _ints(starts)
+        if n_sl != n_cu - 1 or n_s0 != n_cu - 1:
+            raise ValueError("wave_hybrid_prompt_state: one slot and one start for each sequence")
+        c = self.cfg
+        di = c.ssm_heads * c.ssm_head_dim
+        if zxbcdt.shape[1:] != (2 * di + 2 * c.ssm_state + c.ssm_heads,) or out.shape[1:] != (di,) \
+                or _type_of(zxbcdt) != WAVE_BF16 or _type_of(out) != WAVE_BF16:
+            raise ValueError("wave_hybrid_prompt_state: zxbcdt is bf16 [rows][in_rows], out bf16 [rows][d_inner]")
+        _covered(cu, n_cu, "wave_hybrid_prompt_state", zxbcdt, out)
+        rc = lib().wave_hybrid_prompt_state(self.h, layer, _ptr(weights), n_cu - 1, cu, sl, s0, _ptr(zxbcdt),
+                                            _rows(zxbcdt, False, "zxbcdt"), _ptr(state_in), _ptr(state_out), _ptr(out),
+                                            _rows(out, False, "out"), _stream(stream))
+        if check and rc != WAVE_OK:
+            raise WaveError(rc, "wave_hybrid_prompt_state")
         return rc
 
 

@@ -10,7 +10,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libwave.so")
-SOURCES = ["step.cu", "api.cu", "plan.cu", "pack.cu", "quant.cu", "noalloc.cu"]
+SOURCES = ["step.cu", "api.cu", "plan.cu", "pack.cu", "quant.cu", "noalloc.cu",
+           "prompt.cu", "prompt_attn.cu", "prompt_state.cu", "sessions.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v"]
 

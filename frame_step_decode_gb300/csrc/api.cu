@@ -11,33 +11,11 @@
 #include <vector>
 
 #include "../../include/wave.h"
+#include "ctx.h"
 #include "internal.h"
 #include "plan.h"
 
 using namespace wave;
-
-struct wave_ctx {
-  Plan pl;
-  int device = 0;
-  void* ws_block = nullptr;
-  Workspace ws;
-  int* err_host = nullptr;      // pinned host word the kernel mirrors the error bits into
-  int* err_host_dev = nullptr;  // its device-side address
-  // cached tensor maps and what they were encoded for
-  Maps maps;
-  const void* maps_weights = nullptr;
-  const void* maps_kv = nullptr;
-  const void* maps_sc = nullptr;
-  int maps_S = -1;
-  cudaStream_t last_stream = nullptr;
-  long long timeout_ns = 2000000000LL;
-  int skip_cta = -1, skip_bar = -1, skip_sig = -1, skip_sig_kind = -1;
-  float* kv_dump = nullptr;
-  float* act_dump = nullptr;
-  int act_dump_n = 0;
-  long long* phase_ts = nullptr;
-  long long* arrive_ts = nullptr;
-};
 
 extern "C" size_t wave_weights_bytes(const wave_config* cfg) {
   if (!decoder_shape_ok(cfg)) return 0;

@@ -45,6 +45,13 @@ extern "C" {
 #define WAVE_EDEVICE (-6)  /* the current device is not an sm_103 GPU */
 #define WAVE_ENOMEM (-7)   /* device allocation failed */
 
+/* Element types of the calls on packed prompts. */
+#define WAVE_F32 0
+#define WAVE_BF16 1
+#define WAVE_F16 2
+/* Sequences one call on packed prompts takes at most (the largest S_max). */
+#define WAVE_MAX_SEQS 128
+
 /* Decoder shape.  Constraints checked by wave_create: head_dim is 64 or 128;
  * d_model (at most 8192), n_heads*head_dim and ffn are multiples of 64, 64
  * and 8. */
@@ -280,6 +287,111 @@ int wave_kv_quantize(const float* v, int64_t rows, int D, uint8_t* codes, float*
 /* Element-wise E4M3 encoder of the step (round to nearest even, saturate to
  * +-448, sign kept): out[i] = E4M3(in[i]).  Asynchronous on `stream`. */
 int wave_fp8_encode(const float* in, int64_t n, uint8_t* out, void* stream);
+
+/* ---- sessions from prompts ------------------------------------------------
+ * A new session starts from a prompt (the persona and text prompts of the
+ * narilabs blog's sessions, "A server built around the conversation clock":
+ * free slots of the fixed-shape batch are filled by new sessions).  The
+ * calls below bring prompts of many sessions into the batch at once, between
+ * frames; the projections around them are plain matrix products of the
+ * caller's.  They are an interface addition of this library: the pages
+ * describe no prompt path.
+ *
+ * Packed prompts.  The tokens of all sequences lie one after another in each
+ * buffer: sequence i is rows cu_seqlens[i] .. cu_seqlens[i+1]-1.  cu_seqlens
+ * [n_seq + 1], slots [n_seq] and starts [n_seq] are HOST arrays (a server
+ * keeps its slots on the host), read before the call returns; a launch
+ * captured into a graph keeps the batch it was captured with.  slots[i] is
+ * the session the sequence belongs to (negative: the sequence is left out, as
+ * an empty slot of the step) and starts[i] the position of its first token (0
+ * for a new session, the session's position for a continuation).
+ * 1 <= n_seq <= WAVE_MAX_SEQS; sequences may be empty; no session may be named
+ * twice.  Rows outside every sequence are neither read nor written.  Buffers
+ * are 16-byte aligned and row strides (in elements) multiples of 8.  Every
+ * argument is checked on the host before anything is enqueued: WAVE_EINVAL,
+ * or WAVE_EPOS where a token's position would reach T_max; the handle's
+ * device has to be the current one.  The calls are asynchronous, allocate
+ * nothing, and use the handle as a step does (one stream at a time).
+ */
+
+/*
+ * Append prompts to the history of layer `layer` (the model's layer index; of
+ * a hybrid handle, an attention block's): per token and head, rotate q and k,
+ * quantise k and v as wave_step's append does, and write slot starts[i] + t
+ * of session slots[i].
+ *
+ *   qkv     [rows][row_stride], row = q (H*D) | k (H*D) | v (H*D); qkv_type
+ *           WAVE_F32 or WAVE_BF16.
+ *   kv_fp8, kv_scales   the history, as wave_step.
+ *   q       [rows][H][D] of out_type (WAVE_BF16 or WAVE_F16): the rotated q.
+ *   k, v    [rows][H][D] of out_type: what the history now holds (code *
+ *           scale), rounded once, so that attention over the prompt sees the
+ *           keys and values the later frames will read.
+ * q, k, v may each be NULL.  One launch, bound by HBM.
+ */
+int wave_prompt_append(wave_t* h, int layer, int n_seq, const int32_t* cu_seqlens, const int32_t* slots,
+                       const int32_t* starts, const void* qkv, int qkv_type, int64_t row_stride, uint8_t* kv_fp8,
+                       float* kv_scales, void* q, void* k, void* v, int out_type, void* stream);
+
+/*
+ * Causal attention over packed whole prompts: token t of a sequence attends
+ * to tokens 0..t of the same sequence,
+ *     out_t = sum_{j<=t} p_tj v_j / sum_{j<=t} p_tj,  p_tj = exp(scale q_t . k_j - max).
+ * q and out hold the handle's n_heads heads of head_dim per row, k and v
+ * n_kv_heads (a divisor of n_heads; head h reads K/V head h / (n_heads /
+ * n_kv_heads)); heads are contiguous in a row and rows are *_stride elements
+ * apart, so slices of a wider row can be passed.  type is WAVE_BF16 or
+ * WAVE_F16, of all four; scale is finite and > 0 (1/sqrt(D) in the step).
+ * Scores, the softmax's maximum and sum and the output are kept in fp32, the
+ * weights p are rounded to `type` for the second product.  Values at tokens
+ * that a row does not attend to never reach it, whatever they are (NaN and
+ * infinities included).  out must not overlap q, k or v.  Lengths are not
+ * tied to the handle's T_max.
+ */
+int wave_prompt_attention(wave_t* h, int n_seq, const int32_t* cu_seqlens, int n_kv_heads, int type, const void* q,
+                          int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                          float scale, void* out, int64_t out_stride, void* stream);
+
+/*
+ * The selective-state block `layer` (the model's layer index) of a hybrid
+ * handle over packed prompts: from zxbcdt, the block's in-projection of the
+ * normed tokens, to out, the input of its out-projection, with the same
+ * recurrence, gate and parameters as wave_hybrid_step (linear attention with
+ * a decay for each head), for any number of tokens at once.
+ *
+ *   weights   the hybrid packed blob (its A_log, dt_bias and D of the layer are read).
+ *   zxbcdt    bf16 [rows][zx_stride], row = z | x | B | C | dt; zx_stride a
+ *             multiple of 4 (a row of Hs heads may be no multiple of 8).
+ *   state_in  fp32 [Lm][S_max][Hs][64][128], the state before the first token
+ *             of every sequence with starts[i] > 0; a sequence with starts[i]
+ *             == 0 begins from zero.  May be NULL when all do.
+ *   state_out the same layout: the state after each sequence's last token.
+ *             May be state_in (sessions go on in place) or another buffer (a
+ *             continuation tried without giving up the state it began from;
+ *             the two may not overlap otherwise).  Sessions that the call does
+ *             not name, and those with an empty sequence, are not written.
+ *   out       bf16 [rows][out_stride]: bf16(y silu(z)).
+ */
+int wave_hybrid_prompt_state(wave_t* h, int layer, const void* weights, int n_seq, const int32_t* cu_seqlens,
+                             const int32_t* slots, const int32_t* starts, const void* zxbcdt, int64_t zx_stride,
+                             const float* state_in, float* state_out, void* out, int64_t out_stride, void* stream);
+
+/*
+ * Copy n sessions to other slots: for each pair, the history of all layers
+ * (slots 0..positions[src]-1 of K and V, codes and scales), the fp32 state of
+ * all selective-state layers (a hybrid handle's; ssm_state is NULL for a
+ * decoder handle) and the position (a negative one makes the destination an
+ * empty slot and nothing else is copied).  src and dst are HOST arrays of n
+ * slots in [0, S_max); positions is the device array [S_max] that the steps
+ * use.  A source may be given several destinations (a prepared session
+ * forked: it is read once); a destination appears once and is no source
+ * (WAVE_EINVAL otherwise).  With move != 0 the sources' positions are set to -1
+ * afterwards: sessions compacted into free slots, their old ones freed.  Slots
+ * at or beyond positions[src] of a destination keep what they held.
+ * Asynchronous, one launch (two with move).
+ */
+int wave_sessions_copy(wave_t* h, int n, const int32_t* src, const int32_t* dst, int move, uint8_t* kv_fp8,
+                       float* kv_scales, float* ssm_state, int32_t* positions, void* stream);
 
 /*
  * wave_step for callers that cannot allocate device memory (inside another
