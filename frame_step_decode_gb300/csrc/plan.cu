@@ -365,6 +365,16 @@ int encode_act_maps(const Plan& pl, const Workspace& ws, int S_pad, Maps* m) {
   return WAVE_OK;
 }
 
+int encode_rows_map(CUtensorMap* m, const void* base, int D, int heads, long long rows, long long stride,
+                    int box_rows) {
+  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)rows};
+  cuuint64_t str[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
+  cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, (void*)base, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B)
+             ? WAVE_OK
+             : WAVE_ECUDA;
+}
+
 int encode_kv_maps(const Plan& pl, uint8_t* kv, float* scales, Maps* m) {
   const wave_config& c = pl.cfg;
   const cuuint64_t D = c.head_dim, L = c.n_layers;

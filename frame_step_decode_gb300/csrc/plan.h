@@ -106,6 +106,11 @@ void fill_params(StepParams* p, const Plan& pl, const Workspace& ws, const Maps&
 // The inner depth loop's maps: W_p [d][d] as a one-layer weight stack, and
 // the outputs y [steps * S][d] read back S_pad rows at a time.
 int encode_proj_maps(const Plan& pl, const void* w_proj, void* y, int S, int steps, Maps* m);
+// A packed 16-bit tensor [rows][heads][D], rows `stride` elements apart, read
+// as tiles of 64 values x box_rows rows of one head (128-byte swizzle; rows
+// beyond the tensor read as zero).
+int encode_rows_map(CUtensorMap* m, const void* base, int D, int heads, long long rows, long long stride,
+                    int box_rows);
 // Floats per record of the activation dump (the testing hook of wave.h):
 // 5 d + max(3 H D, in_rows) + max(H D, d_inner) + F.
 long long act_record_floats(const Plan& pl);

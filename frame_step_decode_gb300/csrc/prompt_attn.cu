@@ -9,68 +9,511 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "../../include/wave.h"
 #include "ctx.h"
 #include "prompt.h"
-#include "ptx.cuh"
+#include "prompt_ptx.cuh"
 
 using namespace wave;
 
 namespace wave {
 
+constexpr int kRows = 128;         // query rows of one stream, and keys of one block
+constexpr int kAttnThreads = 384;  // 8 softmax warps (two streams), then copies, MMAs, guard, scheduler
+
 struct AttnParams {
-  SeqBatch b;
-  int Hq, group;  // query heads, and how many of them share a K/V head
-  const void *q, *k, *v;
-  void* out;
-  long long q_stride, k_stride, v_stride, out_stride;
-  float scale2;   // scale * log2(e)
+  CUtensorMap tm_q, tm_k, tm_v;
+  int n;                            // sequences, longest first
+  int32_t begin[WAVE_MAX_SEQS], len[WAVE_MAX_SEQS];
+  long long items;                  // (pairs of row tiles) x heads
+  int Hq, group;                    // query heads, and how many of them share a K/V head
+  const uint16_t* v;
+  uint16_t* out;
+  long long v_stride, out_stride;
+  float scale2;                     // scale * log2(e)
+  ErrSink sink;
 };
 
-template <typename T>
-__device__ __forceinline__ float to_f32(T v);
-template <>
-__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <>
-__device__ __forceinline__ float to_f32<__half>(__half v) { return __half2float(v); }
-template <typename T>
-__device__ __forceinline__ T from_f32(float v);
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
-template <>
-__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+// What the scheduler hands to the other warps.
+struct AttnItem {
+  int valid, head;
+  int row0, left;      // first query row of the pair, rows from there to the sequence's end
+  int kv0;             // the sequence's first row
+  int n0, n1;          // key blocks of stream 0 and 1 (0: no rows)
+  uint32_t bad[2][4];  // keys of the last two V blocks that hold a value which is not finite
+};
 
-// A warp per (token, head), a running maximum and sum over the keys.
-template <int D, typename T>
-__global__ void __launch_bounds__(256) k_prompt_attention_rows(const __grid_constant__ AttnParams p) {
-  constexpr int E = D / 32;
+// Shared memory: the two streams' Q tiles, a ring of K and V tiles, barriers, items.
+template <int D>
+struct AttnSmem {
+  static constexpr int kTile = kRows * D * 2;
+  static constexpr int kStages = D == 128 ? 5 : 10;
+  static constexpr int kRing = 2 * kTile;
+  static constexpr int kBars = kRing + kStages * kTile;
+  enum {
+    kFull = 0,
+    kEmpty = kFull + kStages,
+    kQFull = kEmpty + kStages,
+    kQEmpty,
+    kSFull,
+    kPFull = kSFull + 2,
+    kOFull = kPFull + 2,
+    kGo = kOFull + 2,
+    kOk,
+    kDone,
+    kItemFull,
+    kItemEmpty = kItemFull + 2,
+    kCount = kItemEmpty + 2
+  };
+  static constexpr int kItems = kBars + kCount * 8;
+  static constexpr int kMisc = kItems + 2 * (int)sizeof(AttnItem);
+  static constexpr int kTotal = kMisc + 16 + 1024;  // + alignment
+};
+
+template <bool kF16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  uint32_t r;
+  if constexpr (kF16)
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  else
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// The rank-th pair of row tiles in descending order of work: pairs with many
+// key blocks first, so that the last ones to start are the shortest.  The
+// level of a pair is its index in its sequence (its work is 2 level + 2 key
+// blocks); the sequences that reach a level are the first ones, as they are
+// sorted.  Called by a whole warp.
+__device__ __forceinline__ void pair_of_rank(const AttnParams& p, int rank, int& seq, int& level) {
   const int lane = threadIdx.x & 31;
-  const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int t = (int)(w / p.Hq), h = (int)(w % p.Hq);
-  if (t >= p.b.cum[p.b.n]) return;
-  const int i = seq_of(p.b, t), at = t - p.b.cum[i];
-  const size_t first = p.b.begin[i];
-  const T* q = (const T*)p.q + (first + at) * p.q_stride + h * D + lane * E;
-  const T* k = (const T*)p.k + first * p.k_stride + (h / p.group) * D + lane * E;
-  const T* v = (const T*)p.v + first * p.v_stride + (h / p.group) * D + lane * E;
-  float qv[E], o[E] = {}, m = -INFINITY, l = 0.f;
+  int np[4];
 #pragma unroll
-  for (int e = 0; e < E; ++e) qv[e] = to_f32<T>(q[e]) * p.scale2;
-  for (int j = 0; j <= at; ++j) {
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) s += qv[e] * to_f32<T>(k[(size_t)j * p.k_stride + e]);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    const float m2 = fmaxf(m, s), a = m == m2 ? 1.f : ex2(m - m2), w2 = ex2(s - m2);
-    m = m2;
-    l = l * a + w2;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * a + w2 * to_f32<T>(v[(size_t)j * p.v_stride + e]);
+  for (int i = 0; i < 4; ++i) {
+    const int s = lane + 32 * i;
+    np[i] = s < p.n ? (int)(((unsigned)p.len[s] + 2 * kRows - 1) / (2 * kRows)) : 0;
   }
-  T* out = (T*)p.out + (first + at) * p.out_stride + h * D + lane * E;
+  auto at_or_above = [&](int t) {  // pairs whose level is t or more
+    int c = 0;
 #pragma unroll
-  for (int e = 0; e < E; ++e) out[e] = from_f32<T>(o[e] / l);
+    for (int i = 0; i < 4; ++i) c += max(0, np[i] - t);
+    return (int)__reduce_add_sync(0xffffffffu, (unsigned)c);
+  };
+  int lo = 0, hi = (int)(((unsigned)p.len[0] + 2 * kRows - 1) / (2 * kRows)) - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (at_or_above(mid + 1) <= rank)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  level = lo;
+  seq = rank - at_or_above(lo + 1);
+}
+
+// Flash attention on the tensor cores, a pair of 128-row query tiles per work
+// item.  One pass over the keys with the softmax's running maximum and sum:
+// S = Q K^T by tcgen05 into TMEM, a thread per row turns S into the weights
+// P (16 bits, written over S), O += P V by tcgen05 with P read from TMEM.  The
+// two tiles are two streams: while one stream's weights are computed the
+// tensor core works for the other.
+//
+// MMAs issued by one thread run in issue order, which is what lets Q K^T of
+// block j + 1 be issued behind P V of block j although both use the same TMEM
+// columns; a commit covers every MMA issued before it, so s_full of block
+// j + 1 also says that P V of block j is complete.
+template <int D, bool kF16>
+__global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __grid_constant__ AttnParams p) {
+  using L = AttnSmem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t base_raw = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + ((1024 - (base_raw & 1023)) & 1023);
+  const uint32_t sb = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto bar = [&](int i) { return sb + L::kBars + i * 8; };
+  AttnItem* items = (AttnItem*)(smem + L::kItems);
+  uint32_t* tmem_word = (uint32_t*)(smem + L::kMisc);
+
+  if (warp == 9) {
+    if (lane == 0) {
+      for (int i = 0; i < L::kStages; ++i) {
+        mbar_init(bar(L::kFull + i), 1);
+        mbar_init(bar(L::kEmpty + i), 1);
+      }
+      mbar_init(bar(L::kQFull), 1);
+      mbar_init(bar(L::kQEmpty), 1);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(bar(L::kSFull + i), 1);
+        mbar_init(bar(L::kPFull + i), 128);
+        mbar_init(bar(L::kOFull + i), 1);
+        mbar_init(bar(L::kItemFull + i), 1);
+        mbar_init(bar(L::kItemEmpty + i), 11);  // 8 softmax warps, copies, MMAs, guard
+      }
+      mbar_init(bar(L::kGo), 1);
+      mbar_init(bar(L::kOk), 1);
+      mbar_init(bar(L::kDone), 1);
+      fence_mbar_init();
+      fence_proxy_async_smem();
+    }
+    __syncwarp();
+    tmem_alloc(smem_u32(tmem_word), 512);
+    tmem_relinquish();
+  }
+  if (warp == 8 && lane == 0) {
+    prefetch_tmap(&p.tm_q);
+    prefetch_tmap(&p.tm_k);
+    prefetch_tmap(&p.tm_v);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_word;
+  auto tS = [&](int st) { return tmem + st * 128; };
+  auto tO = [&](int st) { return tmem + 256 + st * D; };
+
+  // Every wait is bounded; a give-up sets the error word, which ends the
+  // other waits, and every warp leaves its loop.  wait: one thread;
+  // wait_warp: a whole warp, which stays together.
+  bool ok = true;
+  auto wait = [&](int b, uint32_t parity) { return ok = wait_or_flag(bar(b), parity, p.sink, kErrTimeout); };
+  auto wait_warp = [&](int b, uint32_t parity) {
+    return ok = __all_sync(0xffffffffu, wait_or_flag(bar(b), parity, p.sink, kErrTimeout));
+  };
+
+  if (warp < 8) {
+    // ---------------------------------------------------------------- softmax
+    regs_take<216>();
+    const int st = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    uint32_t s_it = 0, o_it = 0;
+    for (uint32_t k = 0; ok; ++k) {
+      if (!wait_warp(L::kItemFull + (k & 1), (k >> 1) & 1)) break;
+      const AttnItem& it = items[k & 1];
+      const bool live = it.valid != 0;
+      const int n = st ? it.n1 : it.n0;
+      if (live && n > 0) {
+        float m = -INFINITY, l = 0.f;
+        for (int j = 0; j < n; ++j, ++s_it) {
+          if (!wait_warp(L::kSFull + st, s_it & 1)) break;
+          tc_fence_after();
+          uint32_t s[128];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(tS(st) + lanes + 32 * c, s + 32 * c);
+          tmem_ld_wait();
+          if (j == n - 1) {  // the diagonal block
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+              if (c > row) s[c] = __float_as_uint(-INFINITY);
+          }
+          float mx[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) mx[c] = __uint_as_float(s[c]);
+#pragma unroll
+          for (int c = 4; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c]));
+          const float bm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          // The maximum moves only when a weight would exceed 2^8 (the sums
+          // and the 16-bit weights have room for that): O is rescaled seldom.
+          if (j == 0) {
+            m = bm;
+          } else {
+            const bool up = (bm - m) * p.scale2 > 8.f;
+            if (__any_sync(0xffffffffu, up)) {
+              const float m2 = up ? bm : m;
+              const float a = up ? (m == -INFINITY ? 0.f : ex2((m - m2) * p.scale2)) : 1.f;
+              l *= a;
+              m = m2;
+#pragma unroll
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(tO(st) + lanes + 32 * c, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
+                tmem_st32(tO(st) + lanes + 32 * c, o);
+              }
+            }
+          }
+          const float neg = m == -INFINITY ? 0.f : -m * p.scale2;
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t w[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float x = ex2(fmaf(__uint_as_float(s[64 * c + 2 * i]), p.scale2, neg));
+              const float y = ex2(fmaf(__uint_as_float(s[64 * c + 2 * i + 1]), p.scale2, neg));
+              sum[(2 * i) & 3] += x;
+              sum[(2 * i + 1) & 3] += y;
+              w[i] = pack16<kF16>(x, y);
+            }
+            tmem_st32(tS(st) + lanes + 32 * c, w);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_st_wait();
+          tc_fence_before();
+          mbar_arrive(bar(L::kPFull + st));
+        }
+        if (!ok || !wait_warp(L::kOFull + st, o_it & 1)) break;
+        ++o_it;
+        tc_fence_after();
+        const float inv = 1.f / l;
+        uint32_t bad = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) bad |= it.bad[0][i] | it.bad[1][i];
+        uint16_t* orow = p.out + (size_t)(it.row0 + st * kRows + row) * p.out_stride + it.head * D;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(tO(st) + lanes + 32 * c, o);
+          tmem_ld_wait();
+          if (bad) {
+            // values of the last blocks' keys that are not finite were left
+            // out of P V; the rows that attend to them get them here
+            for (int g = 0; g <= st; ++g)
+              for (int w = 0; w < 4; ++w)
+                for (uint32_t bits = it.bad[g][w]; bits; bits &= bits - 1) {
+                  const int key = w * 32 + __ffs(bits) - 1;
+                  const int kr = it.kv0 + (it.n0 - 1 + g) * kRows + key;
+                  if ((g == st && key > row) || kr >= it.row0 + it.left) continue;
+                  const uint16_t* vr = p.v + (size_t)kr * p.v_stride + (it.head / p.group) * D + 32 * c;
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) {
+                    const float v = kF16 ? __half2float(__ushort_as_half(vr[i])) : __uint_as_float((uint32_t)vr[i] << 16);
+                    if (!isfinite(v)) o[i] = __float_as_uint(__uint_as_float(o[i]) + v);
+                  }
+                }
+          }
+          if (st * kRows + row < it.left) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint4 w;
+              w.x = pack16<kF16>(__uint_as_float(o[8 * i]) * inv, __uint_as_float(o[8 * i + 1]) * inv);
+              w.y = pack16<kF16>(__uint_as_float(o[8 * i + 2]) * inv, __uint_as_float(o[8 * i + 3]) * inv);
+              w.z = pack16<kF16>(__uint_as_float(o[8 * i + 4]) * inv, __uint_as_float(o[8 * i + 5]) * inv);
+              w.w = pack16<kF16>(__uint_as_float(o[8 * i + 6]) * inv, __uint_as_float(o[8 * i + 7]) * inv);
+              *(uint4*)(orow + 32 * c + 8 * i) = w;
+            }
+          }
+          __syncwarp();
+        }
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::kItemEmpty + (k & 1)));
+      if (!live) break;
+    }
+  } else {
+    regs_give<64>();
+    if (warp == 8) {
+      // ------------------------------------------------------------- copies
+      if (lane == 0) {
+        uint32_t it_r = 0;  // tiles brought into the ring
+        auto tile = [&](const CUtensorMap* map, uint32_t dst, int head, int r, uint32_t b) {
+#pragma unroll
+          for (int i = 0; i < D / 64; ++i) tma_load_3d_plain(dst + i * (kRows * 128), map, 64 * i, head, r, b);
+        };
+        uint32_t q_it = 0;
+        for (uint32_t k = 0; ok; ++k) {
+          if (!wait(L::kItemFull + (k & 1), (k >> 1) & 1)) break;
+          const AttnItem& src = items[k & 1];
+          const int valid = src.valid, head = src.head, row0 = src.row0, kv0 = src.kv0, n0 = src.n0, n1 = src.n1;
+          mbar_arrive(bar(L::kItemEmpty + (k & 1)));
+          if (!valid) break;
+          if (!wait(L::kQEmpty, (k & 1) ^ 1)) break;
+          mbar_arrive_expect_tx(bar(L::kQFull), (n1 ? 2 : 1) * L::kTile);
+          tile(&p.tm_q, sb, head, row0, bar(L::kQFull));
+          if (n1) tile(&p.tm_q, sb + L::kTile, head, row0 + kRows, bar(L::kQFull));
+          ++q_it;
+          const int nb = max(n0, n1), kvh = head / p.group;
+          for (int j = 0; j < 2 * nb; ++j, ++it_r) {  // K_0, V_0, K_1, V_1, ...
+            const int slot = it_r % L::kStages;
+            if (!wait(L::kEmpty + slot, ((it_r / L::kStages) & 1) ^ 1)) break;
+            mbar_arrive_expect_tx(bar(L::kFull + slot), L::kTile);
+            tile(j & 1 ? &p.tm_v : &p.tm_k, sb + L::kRing + slot * L::kTile, kvh, kv0 + (j >> 1) * kRows,
+                 bar(L::kFull + slot));
+          }
+        }
+        if (!ok) {  // give-up: the copies in flight land before the shared memory is left
+          auto drain = [&](int b, uint32_t parity) {
+            for (int n = 0; n < (1 << 20) && !mbar_try_wait(bar(b), parity); ++n) {
+            }
+          };
+          if (q_it) drain(L::kQFull, (q_it - 1) & 1);
+          for (uint32_t i = it_r > L::kStages ? it_r - L::kStages : 0; i < it_r; ++i)
+            drain(L::kFull + i % L::kStages, (i / L::kStages) & 1);
+        }
+      }
+      __syncwarp();
+    } else if (warp == 9) {
+      // --------------------------------------------------------------- MMAs
+      if (lane == 0) {
+        constexpr uint32_t id_s = idesc_16(128, 128, kF16, false, false), id_o = idesc_16(128, D, kF16, false, true);
+        uint32_t it_r = 0, p_it[2] = {0, 0}, g_it = 0;
+        auto slot_of = [&](uint32_t i) { return (int)(i % L::kStages); };
+        auto full = [&](uint32_t i) { return wait(L::kFull + slot_of(i), (i / L::kStages) & 1); };
+        auto scores = [&](int st, uint32_t i) {  // S = Q K^T
+          const uint32_t q = sb + st * L::kTile, kt = sb + L::kRing + slot_of(i) * L::kTile;
+#pragma unroll
+          for (int e = 0; e < D / 16; ++e) {
+            const uint32_t o = (e / 4) * (kRows * 128) + (e % 4) * 32;
+            mma_ss(tS(st), sdesc_sw128(q + o), sdesc_sw128(kt + o), id_s, e > 0);
+          }
+          tc_commit(bar(L::kSFull + st));
+        };
+        auto values = [&](int st, uint32_t i, bool first) {  // O += P V
+          const uint32_t vt = sb + L::kRing + slot_of(i) * L::kTile;
+#pragma unroll
+          for (int e = 0; e < kRows / 16; ++e)
+            mma_ts(tO(st), tS(st) + 8 * e, sdesc_mn_sw128(vt + e * 2048, kRows * 128), id_o, !first || e > 0);
+        };
+        for (uint32_t k = 0; ok; ++k) {
+          if (!wait(L::kItemFull + (k & 1), (k >> 1) & 1)) break;
+          const int valid = items[k & 1].valid, n0 = items[k & 1].n0, n1 = items[k & 1].n1;
+          mbar_arrive(bar(L::kItemEmpty + (k & 1)));
+          if (!valid) break;
+          const int nb = max(n0, n1);
+          if (!wait(L::kQFull, k & 1) || !full(it_r)) break;
+          tc_fence_after();
+          scores(0, it_r);
+          if (n1) scores(1, it_r);
+          tc_commit(bar(L::kEmpty + slot_of(it_r)));
+          for (int j = 0; j < nb; ++j) {
+            const uint32_t kv = it_r + 2 * j + 1, kk = kv + 1;
+            const bool more = j + 1 < nb, guarded = j >= n0 - 1;
+            if (!full(kv)) break;
+            if (guarded) mbar_arrive(bar(L::kGo));
+            if (more && !full(kk)) break;
+            bool checked = !guarded;
+#pragma unroll
+            for (int st = 0; st < 2; ++st) {
+              const int n = st ? n1 : n0;
+              if (!ok || j >= n) continue;
+              if (!wait(L::kPFull + st, p_it[st] & 1)) continue;
+              ++p_it[st];
+              if (!checked) {
+                if (!wait(L::kOk, g_it & 1)) continue;
+                ++g_it;
+                checked = true;
+              }
+              tc_fence_after();
+              values(st, kv, j == 0);
+              if (j + 1 < n)
+                scores(st, kk);
+              else
+                tc_commit(bar(L::kOFull + st));
+            }
+            if (!ok) break;
+            tc_commit(bar(L::kEmpty + slot_of(kv)));
+            if (more) tc_commit(bar(L::kEmpty + slot_of(kk)));
+          }
+          if (!ok) break;
+          tc_commit(bar(L::kQEmpty));
+          it_r += 2 * nb;
+        }
+        if (!ok) {  // give-up: wait (bounded) for the MMAs issued so far
+          tc_commit(bar(L::kDone));
+          for (int n = 0; n < (1 << 20) && !mbar_try_wait(bar(L::kDone), 0); ++n) {
+          }
+        }
+      }
+      __syncwarp();
+    } else if (warp == 10) {
+      // -------------------------------------------------------------- guard
+      // A weight of zero times a value that is not finite is NaN, so the V
+      // tiles with keys that some of their rows do not attend to (the blocks
+      // on the diagonal; behind a sequence's end lie other sequences) are
+      // looked over first: such values become zero there, and the epilogue
+      // adds them to the rows that do attend to them.
+      uint32_t it_r = 0, g_it = 0;
+      for (uint32_t k = 0; ok; ++k) {
+        if (!wait_warp(L::kItemFull + (k & 1), (k >> 1) & 1)) break;
+        AttnItem& it = items[k & 1];
+        const int valid = it.valid, n0 = it.n0, nb = max(it.n0, it.n1);
+        for (int j = n0 - 1; valid && j < nb; ++j) {
+          if (!wait_warp(L::kGo, g_it & 1)) break;
+          ++g_it;
+          uint8_t* v = smem + L::kRing + ((it_r + 2 * j + 1) % L::kStages) * L::kTile;
+          uint32_t acc = 0;  // x * 0 is NaN exactly where x is not finite
+#pragma unroll 4
+          for (int o = lane * 16; o < L::kTile; o += 512) {
+            const uint4 x = *(const uint4*)(v + o);
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if constexpr (kF16)
+                asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(w[i]), "r"(0));
+              else
+                asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(w[i]), "r"(0));
+            }
+          }
+          if (__any_sync(0xffffffffu, (acc & 0x7fff7fffu) != 0)) {
+            constexpr uint32_t kExp = kF16 ? 0x7C00u : 0x7F80u;
+            for (int o = lane * 4; o < L::kTile; o += 128) {
+              uint32_t w = *(uint32_t*)(v + o);
+              const bool lo = (w & kExp) == kExp, hi = ((w >> 16) & kExp) == kExp;
+              if (lo || hi) {
+                if (lo) w &= 0xFFFF0000u;
+                if (hi) w &= 0x0000FFFFu;
+                *(uint32_t*)(v + o) = w;
+                const int key = (o / 128) % kRows;
+                atomicOr(&it.bad[j - (n0 - 1)][key >> 5], 1u << (key & 31));
+              }
+            }
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::kOk));
+        }
+        if (!ok) break;
+        it_r += 2 * nb;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::kItemEmpty + (k & 1)));
+        if (!valid) break;
+      }
+    } else {
+      // ---------------------------------------------------------- scheduler
+      for (uint32_t k = 0; ok; ++k) {
+        if (!wait_warp(L::kItemEmpty + (k & 1), ((k >> 1) & 1) ^ 1)) break;
+        // rows of gridDim items, every second one backwards: the CTA with the
+        // longest item of one row gets the shortest of the next
+        const long long idx = (long long)k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        const bool valid = idx < p.items;
+        int seq = 0, level = 0;
+        if (valid) pair_of_rank(p, (int)(idx / p.Hq), seq, level);
+        if (lane == 0) {
+          AttnItem& it = items[k & 1];
+          const int left = p.len[seq] - level * 2 * kRows;
+          it.valid = valid;
+          it.head = (int)(idx % p.Hq);
+          it.kv0 = p.begin[seq];
+          it.row0 = p.begin[seq] + level * 2 * kRows;
+          it.left = left;
+          it.n0 = 2 * level + 1;
+          it.n1 = left > kRows ? 2 * level + 2 : 0;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) it.bad[i / 4][i % 4] = 0;
+          mbar_arrive(bar(L::kItemFull + (k & 1)));
+        }
+        __syncwarp();
+        if (!valid) break;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+template <int D, bool kF16>
+static cudaError_t launch_attention(const AttnParams& p, int grid, cudaStream_t st) {
+  const cudaError_t set = cudaFuncSetAttribute(k_prompt_attention<D, kF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               AttnSmem<D>::kTotal);
+  if (set != cudaSuccess) return set;
+  k_prompt_attention<D, kF16><<<(unsigned)(p.items < grid ? p.items : grid), kAttnThreads, AttnSmem<D>::kTotal, st>>>(p);
+  return cudaGetLastError();
 }
 
 }  // namespace wave
@@ -89,36 +532,42 @@ extern "C" int wave_prompt_attention(wave_t* h, int n_seq, const int32_t* cu_seq
     if (strides[i] < least[i] || strides[i] % 8 || strides[i] >= (1LL << 31) || !aligned16(ptrs[i])) return WAVE_EINVAL;
   if (!on_device(h)) return WAVE_EINVAL;
   AttnParams p;
-  p.b.n = 0;
-  p.b.cum[0] = 0;
-  for (int i = 0; i < n_seq; ++i) {
-    const int len = cu_seqlens[i + 1] - cu_seqlens[i];
-    if (!len) continue;
-    p.b.begin[p.b.n] = cu_seqlens[i];
-    p.b.cum[p.b.n + 1] = p.b.cum[p.b.n] + len;
-    ++p.b.n;
+  // the sequences that have tokens, longest first
+  int order[WAVE_MAX_SEQS];
+  p.n = 0;
+  for (int i = 0; i < n_seq; ++i)
+    if (cu_seqlens[i + 1] > cu_seqlens[i]) order[p.n++] = i;
+  if (!p.n) return WAVE_OK;
+  std::stable_sort(order, order + p.n, [&](int a, int b) {
+    return cu_seqlens[a + 1] - cu_seqlens[a] > cu_seqlens[b + 1] - cu_seqlens[b];
+  });
+  long long pairs = 0;
+  for (int i = 0; i < p.n; ++i) {
+    p.begin[i] = cu_seqlens[order[i]];
+    p.len[i] = cu_seqlens[order[i] + 1] - cu_seqlens[order[i]];
+    pairs += (p.len[i] + 2LL * kRows - 1) / (2 * kRows);
   }
-  if (!p.b.n) return WAVE_OK;
+  const long long rows = cu_seqlens[n_seq];
+  if (encode_rows_map(&p.tm_q, q, D, H, rows, q_stride, kRows) ||
+      encode_rows_map(&p.tm_k, k, D, n_kv_heads, rows, k_stride, kRows) ||
+      encode_rows_map(&p.tm_v, v, D, n_kv_heads, rows, v_stride, kRows))
+    return WAVE_ECUDA;
+  p.items = pairs * H;
   p.Hq = H;
   p.group = H / n_kv_heads;
-  p.q = q;
-  p.k = k;
-  p.v = v;
-  p.out = out;
-  p.q_stride = q_stride;
-  p.k_stride = k_stride;
+  p.v = (const uint16_t*)v;
+  p.out = (uint16_t*)out;
   p.v_stride = v_stride;
   p.out_stride = out_stride;
   p.scale2 = scale * 1.44269504088896340736f;
+  p.sink = {h->ws.err, h->err_host_dev, h->timeout_ns};
   cudaStream_t st = (cudaStream_t)stream;
   h->last_stream = st;
-  const long long warps = (long long)p.b.cum[p.b.n] * H;
-  const unsigned grid = (unsigned)((warps + 7) / 8);
+  const int grid = h->pl.grid;
+  cudaError_t e;
   if (D == 128)
-    type == WAVE_BF16 ? k_prompt_attention_rows<128, __nv_bfloat16><<<grid, 256, 0, st>>>(p)
-                      : k_prompt_attention_rows<128, __half><<<grid, 256, 0, st>>>(p);
+    e = type == WAVE_F16 ? launch_attention<128, true>(p, grid, st) : launch_attention<128, false>(p, grid, st);
   else
-    type == WAVE_BF16 ? k_prompt_attention_rows<64, __nv_bfloat16><<<grid, 256, 0, st>>>(p)
-                      : k_prompt_attention_rows<64, __half><<<grid, 256, 0, st>>>(p);
-  return cudaGetLastError() == cudaSuccess ? WAVE_OK : WAVE_ECUDA;
+    e = type == WAVE_F16 ? launch_attention<64, true>(p, grid, st) : launch_attention<64, false>(p, grid, st);
+  return e == cudaSuccess ? WAVE_OK : WAVE_ECUDA;
 }
