@@ -24,6 +24,8 @@ constexpr int kRowTokens = 8;
 
 struct StateParams {
   SeqBatch b;
+  CUtensorMap tm;          // the rows of zx as tiles of 64 columns x 128 tokens
+  int tiled;               // whether tm is there: a row stride of a multiple of 16 bytes
   int Hs, S_max;
   const uint16_t* zx;      // [rows][zx_stride] bf16: z | x | B | C | dt
   const uint16_t* prm;     // A_log[Hs] | dt_bias[Hs] | D[Hs]
@@ -102,9 +104,17 @@ __global__ void __launch_bounds__(256) k_prompt_state_rows(const __grid_constant
 // over the whole sequence.  M and the H of C H^T are rounded to bf16 once
 // (the output is bf16); (w X)^T is split into a bf16 and the bf16 of its
 // remainder (2^-18), since the state is carried on in fp32.
+//
+// Five warpgroups: two in front (a head each: the decays, the state's pass
+// between chunks, M), two behind (the weights w, (w X)^T, the gated output),
+// and one warp each for the MMAs, the copies of B, C, x and those of z.  The
+// chain from chunk to chunk is the state's: its pass and its product.
 constexpr int kQ = 128;                 // tokens of a chunk
-constexpr int kStateThreads = 384;      // 8 compute warps, the MMA warp, 3 copy warps
-constexpr int kCopyThreads = 96;
+constexpr int kStateThreads = 640;
+// Registers: 640 threads are launched with 96 each (61440); the split is
+// 256 x 112 + 256 x 104 + 128 x 48, the same sum.
+constexpr int kRegsFront = 112, kRegsBehind = 104, kRegsRest = 48;
+static_assert(256 * kRegsFront + 256 * kRegsBehind + 128 * kRegsRest <= kStateThreads * 96, "registers");
 constexpr int kBC = kQ * kSsmN * 2;     // bytes of the B (or C) tile
 constexpr int kXT = kQ * kSsmP * 2;     // ... of one head's x (or z) tile
 
@@ -113,8 +123,9 @@ struct StateSmem {
   static constexpr int kH = 2 * kBuf;             // bf16 H of both heads: [2][n / 64][64 rows of 128 B]
   static constexpr int kA = kH + 2 * kXT;         // [head][128] c_j + log2 dt_j
   static constexpr int kW = kA + 2 * kQ * 4;      // [head][128] w_j
-  static constexpr int kTot = kW + 2 * kQ * 4;    // [chunk parity][head][warp] sums of the warps' 32 tokens
-  static constexpr int kBad = kTot + 2 * 2 * 4 * 4;  // [chunk parity][head][4] tokens with an x that is not finite
+  static constexpr int kTot = kW + 2 * kQ * 4;    // [chunk parity][head][warp] sums over the warps' 32 tokens
+  static constexpr int kAfter = kTot + 2 * 2 * 4 * 4;  // the same of the warpgroups behind
+  static constexpr int kBad = kAfter + 2 * 2 * 4 * 4;  // [chunk parity][head][4] tokens with an x that is not finite
   static constexpr int kBars = kBad + 2 * 2 * 4 * 4;
   enum { kFull = 0, kEmpty = 2, kZFull = 4, kG = 5, kY2 = 6, kHFull = 7, kMFull = 8, kYFull = 10, kWx = 12, kS = 13, kDone = 14, kCount = 15 };
   static constexpr int kMisc = kBars + kCount * 8;
@@ -122,77 +133,43 @@ struct StateSmem {
 };
 static_assert(StateSmem::kTotal <= 232448, "the chunked state form does not fit shared memory");
 
-// TMEM columns: G, then (w X)^T in its place (high parts, remainders); the
-// state; M and Y of each head.
-constexpr int kTG = 0, kTState = 128, kTM = 256, kTY = 384;
+// TMEM columns: G (the heads' M later, 64 each), (w X)^T (high parts, then
+// remainders), the state, Y of each head.
+constexpr int kTG = 0, kTWx = 128, kTState = 256, kTY = 384;
 
 __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 template <int kBytes>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool there) {  // zeros where it is not
-  const int n = there ? kBytes : 0;
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
   if constexpr (kBytes == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
   else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 // A tile of 128 tokens x kCols values at column `col` of the rows from `row0`
-// on (n of them are there), 128-byte swizzled blocks of 64 columns.
-template <int kCols, int kBytes>
-__device__ __forceinline__ void copy_tile(uint32_t dst, const uint16_t* zx, long long stride, int col, size_t row0, int n,
-                                          int tid) {
-  constexpr int kPer = kCols * 2 / kBytes;  // pieces of a row
-  for (int q = tid; q < kQ * kPer; q += kCopyThreads) {
-    const int r = q / kPer, b = (q % kPer) * kBytes, blk = b >> 7, c = (b >> 4) & 7;
-    const bool there = r < n;
-    copy_async<kBytes>(dst + blk * (kQ * 128) + r * 128 + ((c ^ (r & 7)) << 4) + (b & 15),
-                       zx + (row0 + (there ? r : 0)) * stride + col + b / 2, there);
+// on, 128-byte swizzled blocks of 64 columns, by one warp: for rows that no
+// tensor map can describe (a stride that is no multiple of 16 bytes).  Rows
+// from n on repeat row n - 1.
+template <int kCols>
+__device__ __forceinline__ void copy_tile(uint32_t dst, const uint16_t* zx, long long stride, int col, size_t row0, int n) {
+  constexpr int kPer = kCols * 2 / 8;  // pieces of a row
+#pragma unroll 8
+  for (int q = threadIdx.x & 31; q < kQ * kPer; q += 32) {
+    const int r = q / kPer, b = (q % kPer) * 8, blk = b >> 7, c = (b >> 4) & 7;
+    copy_async<8>(dst + blk * (kQ * 128) + r * 128 + ((c ^ (r & 7)) << 4) + (b & 15),
+                  zx + (row0 + min(r, n - 1)) * stride + col + b / 2);
   }
-}
-
-template <bool kWide>
-__device__ __forceinline__ void state_copies(const StateParams& p, uint32_t sb, size_t first, int len, int h0, int tid,
-                                             bool& ok) {
-  using L = StateSmem;
-  constexpr int kBytes = kWide ? 16 : 8;
-  auto bar = [&](int i) { return sb + L::kBars + i * 8; };
-  const int di = p.Hs * kSsmP, chunks = (len + kQ - 1) / kQ;
-  for (int c = 0; c <= chunks && ok; ++c) {
-    const uint32_t buf = sb + (c & 1) * L::kBuf;
-    const size_t row0 = first + (size_t)c * kQ;
-    const int n = min(kQ, len - c * kQ);
-    if (c < chunks) {
-      if (!(ok = wait_or_flag(bar(L::kEmpty + (c & 1)), ((c >> 1) & 1) ^ 1, p.sink, kErrTimeout))) break;
-      copy_tile<kSsmN, kBytes>(buf, p.zx, p.zx_stride, 2 * di, row0, n, tid);
-      copy_tile<kSsmN, kBytes>(buf + kBC, p.zx, p.zx_stride, 2 * di + kSsmN, row0, n, tid);
-      for (int h = 0; h < 2; ++h)
-        copy_tile<kSsmP, kBytes>(buf + 2 * kBC + h * kXT, p.zx, p.zx_stride, di + (h0 + h) * kSsmP, row0, n, tid);
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    if (c > 0) {  // z of the chunk before, over its C once C's products are done
-      if (!(ok = wait_or_flag(bar(L::kY2), (c - 1) & 1, p.sink, kErrTimeout))) break;
-      for (int h = 0; h < 2; ++h)
-        copy_tile<kSsmP, kBytes>(sb + ((c - 1) & 1) * L::kBuf + kBC + h * kXT, p.zx, p.zx_stride, (h0 + h) * kSsmP,
-                                 row0 - kQ, min(kQ, len - (c - 1) * kQ), tid);
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    if (c < chunks) {
-      asm volatile("cp.async.wait_group 1;" ::: "memory");
-      fence_proxy_async_smem();
-      mbar_arrive(bar(L::kFull + (c & 1)));
-    }
-    if (c > 0) {
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-      mbar_arrive(bar(L::kZFull));
-    }
-  }
-  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 __device__ __forceinline__ float lg2(float x) {
   float y;
   asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -201,15 +178,25 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
+// softplus and the log-decay of a token (in powers of two, positive).  2^-160
+// is zero in fp32: a larger step changes nothing, and the cap bounds the
+// rounding of the sums.
+__device__ __forceinline__ float step_of(float raw, float rate, float& lam) {
+  const float dt = raw > 0.f ? raw + log1pf(expf(-raw)) : log1pf(expf(raw));
+  lam = fminf(rate * dt, 160.f);
+  return dt;
+}
+
 __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_constant__ StateParams p) {
   using L = StateSmem;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int pairs = p.Hs / 2, i = blockIdx.x / pairs, h0 = (blockIdx.x % pairs) * 2;
-  const size_t first = p.b.begin[i];
-  const int len = p.b.len(i), chunks = (len + kQ - 1) / kQ;
-  const bool goes_on = p.b.start[i] > 0;  // the state begins as state_in, not as zero
+  const int pairs = p.Hs / 2, seq = blockIdx.x / pairs, h0 = (blockIdx.x % pairs) * 2;
+  const size_t first = p.b.begin[seq];
+  const int len = p.b.len(seq), chunks = (len + kQ - 1) / kQ;
+  const bool goes_on = p.b.start[seq] > 0;  // the state begins as state_in, not as zero
+  const int di = p.Hs * kSsmP;
   auto bar = [&](int b) { return sb + L::kBars + b * 8; };
   uint32_t* tmem_word = (uint32_t*)(smem + L::kMisc);
   if (sb & 1023) {  // the tiles' swizzle counts on it, and there is no room to align by hand
@@ -217,15 +204,16 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
     return;
   }
 
-  if (warp == 8) {
+  if (warp == 16) {
     if (lane == 0) {
+      const int copies = p.tiled ? 1 : 32;
       for (int b = 0; b < 2; ++b) {
-        mbar_init(bar(L::kFull + b), kCopyThreads);
-        mbar_init(bar(L::kEmpty + b), 257);  // the compute threads and the MMAs
+        mbar_init(bar(L::kFull + b), copies);
+        mbar_init(bar(L::kEmpty + b), 257);  // the 256 threads behind and the MMAs
         mbar_init(bar(L::kMFull + b), 128);
         mbar_init(bar(L::kYFull + b), 1);
       }
-      mbar_init(bar(L::kZFull), kCopyThreads);
+      mbar_init(bar(L::kZFull), copies);
       mbar_init(bar(L::kG), 1);
       mbar_init(bar(L::kY2), 1);
       mbar_init(bar(L::kHFull), 256);
@@ -239,75 +227,61 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
     tmem_alloc(smem_u32(tmem_word), 512);
     tmem_relinquish();
   }
+  if (threadIdx.x < 16) ((uint32_t*)(smem + L::kBad))[threadIdx.x] = 0;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_word;
 
+  // In the compute warps a wait that gives up leaves the rest of the loop
+  // without waits (the named barriers need every warp), with its results
+  // undefined; the other warps leave their loops.
   bool ok = true;
+  auto wait_warp = [&](int b, uint32_t parity) {
+    if (ok) ok = __all_sync(0xffffffffu, wait_or_flag(bar(b), parity, p.sink, kErrTimeout));
+  };
+  auto wait = [&](int b, uint32_t parity) { return ok = wait_or_flag(bar(b), parity, p.sink, kErrTimeout); };
+  const int h = (warp >> 2) & 1, quad = warp & 3, row = quad * 32 + lane;  // a thread per token of head h0 + h
+  const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+  const int hh = row >> 6, pp = row & 63;  // for the state: row (head hh, p), half h of the columns or tokens
+  const int head = h0 + h;
+  float* sa = (float*)(smem + L::kA);
+  float* sw = (float*)(smem + L::kW);
+  const uint16_t* dt_col = p.zx + first * p.zx_stride + 2 * di + 2 * kSsmN + head;
+  const size_t state_at = (((size_t)p.b.slot[seq] * p.Hs + h0) * kSsmP + row) * kSsmN + h * 64;
+
   if (warp < 8) {
-    // ------------------------------------------------------------- compute
-    // Warps 4h..4h+3 have head h0 + h, a thread per token.  For the state a
-    // thread has row (head hh, p) and half the columns.  A wait that gives up
-    // leaves the rest of the loop without waits (the barriers below need
-    // every warp), with its results undefined.
-    auto wait = [&](int b, uint32_t parity) {
-      if (ok) ok = __all_sync(0xffffffffu, wait_or_flag(bar(b), parity, p.sink, kErrTimeout));
-    };
-    const int h = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
-    const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-    const int hh = row >> 6, pp = row & 63;  // the state's row
-    const int head = h0 + h, di = p.Hs * kSsmP;
-    float* sa = (float*)(smem + L::kA);
-    float* sw = (float*)(smem + L::kW);
-    float* tot = (float*)(smem + L::kTot);
+    // -------------------------------------------------------------- in front
+    regs_take<kRegsFront>();
     const float rate = expf(bf(p.prm[head])) * 1.44269504088896340736f, bias = bf(p.prm[p.Hs + head]);
-    const float skip = bf(p.prm[2 * p.Hs + head]);
-    const size_t state_at = (((size_t)p.b.slot[i] * p.Hs + h0) * kSsmP + row) * kSsmN + h * 64;
-    const uint16_t* dt_col = p.zx + first * p.zx_stride + 2 * di + 2 * kSsmN + head;
     uint16_t dt_next = row < len ? dt_col[(size_t)row * p.zx_stride] : 0;
-    if (threadIdx.x < 16) ((uint32_t*)(smem + L::kBad))[threadIdx.x] = 0;
     for (int c = 0; c < chunks; ++c) {
-      const int b = c & 1, left = len - c * kQ;
-      uint32_t* bad = (uint32_t*)(smem + L::kBad) + b * 8;
-      uint8_t* buf = smem + b * L::kBuf;
-      // ---- the decays
-      float dt = 0.f;
-      if (row < left) {
-        const float raw = bf(dt_next) + bias;
-        dt = raw > 0.f ? raw + log1pf(expf(-raw)) : log1pf(expf(raw));
-      }
+      const int left = len - c * kQ;
+      // ---- the decays: c_i and its sums over the chunk's tokens
+      float dt = 0.f, lam = 0.f;
+      if (row < left) dt = step_of(bf(dt_next) + bias, rate, lam);
       if (row + kQ < left) dt_next = dt_col[(size_t)((c + 1) * kQ + row) * p.zx_stride];
-      // 2^-160 is zero in fp32: a larger step changes nothing, and bounds the sums' rounding
-      const float lam = fminf(rate * dt, 160.f);
-      float up = lam, down = lam;  // sums of the warp's tokens up to this one, and from it on
+      float ci = lam;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
-        const float u = __shfl_up_sync(0xffffffffu, up, d), v = __shfl_down_sync(0xffffffffu, down, d);
-        if (lane >= d) up += u;
-        if (lane + d < 32) down += v;
+        const float u = __shfl_up_sync(0xffffffffu, ci, d);
+        if (lane >= d) ci += u;
       }
-      float* tc = tot + b * 8;
-      if (lane == 31) tc[h * 4 + quad] = up;
-      bar_sync(1, 256);
-      float ci = up, after = __shfl_down_sync(0xffffffffu, down, 1);  // the sum behind this token
-      if (lane == 31) after = 0.f;
+      float* tot = (float*)(smem + L::kTot) + (c & 1) * 8;
+      if (lane == 31) tot[h * 4 + quad] = ci;
+      bar_sync(1, 256);  // also: every M of the last chunk is done with sa
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (q < quad) ci += tc[h * 4 + q];
-        if (q > quad) after += tc[h * 4 + q];
-      }
-      if (c > 0) wait(L::kS, (c - 1) & 1);  // also: nobody reads sa or sw of the last chunk any more
-      tc_fence_after();
+      for (int q = 0; q < 3; ++q)
+        if (q < quad) ci += tot[h * 4 + q];
       sa[h * kQ + row] = ci + lg2(dt);
-      sw[h * kQ + row] = dt * ex2(-after);
-      // every thread is past the last chunk: its flags are cleared for the next one
-      if (threadIdx.x < 8) ((uint32_t*)(smem + L::kBad))[(b ^ 1) * 8 + threadIdx.x] = 0;
       // ---- the state: its bf16 copy for C H^T, and the chunk's decay
+      if (c > 0) wait_warp(L::kS, (c - 1) & 1);
+      tc_fence_after();
       const bool zero = c == 0 && !goes_on;
       if (!zero) {
-        const float* th = tc + hh * 4;
+        const float* th = tot + hh * 4;
         const float dec = ex2(-((th[0] + th[1]) + (th[2] + th[3])));
+        const float2 dec2 = make_float2(dec, dec);
         uint8_t* hrow = smem + L::kH + hh * kXT + h * (64 * 128) + pp * 128;
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
@@ -334,7 +308,10 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
             *(uint4*)(hrow + (((q * 4 + e) ^ (pp & 7)) << 4)) = w;
           }
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * dec);
+          for (int e = 0; e < 16; ++e) {
+            const float2 r = mul2(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), dec2);
+            v[2 * e] = __float_as_uint(r.x), v[2 * e + 1] = __float_as_uint(r.y);
+          }
           tmem_st32(tmem + kTState + lanes + h * 64 + q * 32, v);
         }
         tmem_st_wait();
@@ -342,36 +319,14 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
       }
       tc_fence_before();
       mbar_arrive(bar(L::kHFull));
-      // ---- this token's x: a value that is not finite would reach earlier
-      // tokens as 0 * NaN, so it is set to zero here and put back below
-      wait(L::kFull + b, (c >> 1) & 1);
-      uint8_t* xrow = buf + 2 * kBC + h * kXT + row * 128;
-      {
-        uint32_t acc = 0;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint4 x = *(const uint4*)(xrow + (e << 4));
-          asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(x.x), "r"(0));
-          asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(x.y), "r"(0));
-          asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(x.z), "r"(0));
-          asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(x.w), "r"(0));
-        }
-        if (acc & 0x7fff7fffu) {
-          for (int e = 0; e < 64; ++e) {
-            uint16_t* x = (uint16_t*)xrow + e;
-            if ((*x & 0x7F80) == 0x7F80) *x = 0;
-          }
-          atomicOr(&bad[h * 4 + quad], 1u << lane);
-          fence_proxy_async_smem();
-        }
-      }
-      bar_sync(1, 256);  // sa, sw and bad are complete
-      // ---- M
-      wait(L::kG, c & 1);
+      bar_sync(2 + h, 128);  // the head's sa is complete
+      // ---- M, over G once both heads have read G
+      wait_warp(L::kG, c & 1);
       tc_fence_after();
+      uint32_t m[64];
+      const float2 nci = make_float2(-ci, -ci);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        uint32_t w[16];
         if (q <= quad) {
           uint32_t g[32];
           tmem_ld32(tmem + kTG + lanes + 32 * q, g);
@@ -380,75 +335,176 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float4 a4 = aj[e];
-            float m[4] = {__uint_as_float(g[4 * e]) * ex2(a4.x - ci), __uint_as_float(g[4 * e + 1]) * ex2(a4.y - ci),
-                          __uint_as_float(g[4 * e + 2]) * ex2(a4.z - ci), __uint_as_float(g[4 * e + 3]) * ex2(a4.w - ci)};
+            const float2 t0 = add2(make_float2(a4.x, a4.y), nci), t1 = add2(make_float2(a4.z, a4.w), nci);
+            float2 r0 = mul2(make_float2(__uint_as_float(g[4 * e]), __uint_as_float(g[4 * e + 1])),
+                             make_float2(ex2(t0.x), ex2(t0.y)));
+            float2 r1 = mul2(make_float2(__uint_as_float(g[4 * e + 2]), __uint_as_float(g[4 * e + 3])),
+                             make_float2(ex2(t1.x), ex2(t1.y)));
             if (q == quad) {
-#pragma unroll
-              for (int f = 0; f < 4; ++f)
-                if (4 * e + f > lane) m[f] = 0.f;
+              if (4 * e > lane) r0.x = 0.f;
+              if (4 * e + 1 > lane) r0.y = 0.f;
+              if (4 * e + 2 > lane) r1.x = 0.f;
+              if (4 * e + 3 > lane) r1.y = 0.f;
             }
-            w[2 * e] = pack_bf16(m[0], m[1]);
-            w[2 * e + 1] = pack_bf16(m[2], m[3]);
+            m[16 * q + 2 * e] = pack_bf16(r0.x, r0.y);
+            m[16 * q + 2 * e + 1] = pack_bf16(r1.x, r1.y);
           }
         } else {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) w[e] = 0;
+          for (int e = 0; e < 16; ++e) m[16 * q + e] = 0;
         }
-        tmem_st16(tmem + kTM + h * 64 + lanes + 16 * q, w);
       }
+      tc_fence_before();
+      bar_sync(1, 256);
+      tc_fence_after();
+      tmem_st32(tmem + kTG + h * 64 + lanes, m);
+      tmem_st32(tmem + kTG + h * 64 + lanes + 32, m + 32);
       // ---- C H^T, scaled in place: M X is added to it
-      wait(L::kY2, c & 1);
+      wait_warp(L::kY2, c & 1);
       tc_fence_after();
       if (!zero) {
         const float ei = ex2(-ci);
+        const float2 ei2 = make_float2(ei, ei);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           uint32_t v[32];
           tmem_ld32(tmem + kTY + h * 64 + lanes + 32 * q, v);
           tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * ei);
+          for (int e = 0; e < 16; ++e) {
+            const float2 r = mul2(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), ei2);
+            v[2 * e] = __float_as_uint(r.x), v[2 * e + 1] = __float_as_uint(r.y);
+          }
           tmem_st32(tmem + kTY + h * 64 + lanes + 32 * q, v);
         }
       }
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(bar(L::kMFull + h));
-      bar_sync(1, 256);  // G has been read: (w X)^T goes in its place
-      // ---- (w X)^T: row (hh, pp), tokens 64 h .. 64 h + 63
-      const uint32_t any_bad = (bad[0] | bad[1] | bad[2] | bad[3]) | (bad[4] | bad[5] | bad[6] | bad[7]);
-      {
-        const uint8_t* xt = buf + 2 * kBC + hh * kXT + (pp & 7) * 2;
-        const float* wj = sw + hh * kQ + h * 64;
-        uint32_t hi[32], lo[32];
+    }
+    // ---- the state after the last token
+    wait_warp(L::kS, (chunks - 1) & 1);
+    tc_fence_after();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) {
-          float v[2];
+    for (int q = 0; q < 2; ++q) {
+      uint32_t v[32];
+      tmem_ld32(tmem + kTState + lanes + h * 64 + q * 32, v);
+      tmem_ld_wait();
+      float4* dst = (float4*)(p.state_out + state_at + 32 * q);
 #pragma unroll
-          for (int f = 0; f < 2; ++f) {
-            const int j = h * 64 + 2 * e + f;
-            v[f] = wj[2 * e + f] * bf(*(const uint16_t*)(xt + j * 128 + (((pp >> 3) ^ (j & 7)) << 4)));
-          }
-          if (any_bad) {
+      for (int e = 0; e < 8; ++e)
+        dst[e] = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]), __uint_as_float(v[4 * e + 2]),
+                             __uint_as_float(v[4 * e + 3]));
+    }
+  } else if (warp < 16) {
+    // ---------------------------------------------------------------- behind
+    regs_take<kRegsBehind>();
+    const float rate = expf(bf(p.prm[head])) * 1.44269504088896340736f, bias = bf(p.prm[p.Hs + head]);
+    const float skip = bf(p.prm[2 * p.Hs + head]);
+    const float2 skip2 = make_float2(skip, skip);
+    uint16_t dt_next = row < len ? dt_col[(size_t)row * p.zx_stride] : 0;
+    for (int c = 0; c < chunks; ++c) {
+      const int b = c & 1, left = len - c * kQ;
+      uint8_t* buf = smem + b * L::kBuf;
+      uint32_t* bad = (uint32_t*)(smem + L::kBad) + b * 8;
+      // ---- w: the decays from behind each token to the chunk's end, summed from the end
+      float dt = 0.f, lam = 0.f;
+      if (row < left) dt = step_of(bf(dt_next) + bias, rate, lam);
+      if (row + kQ < left) dt_next = dt_col[(size_t)((c + 1) * kQ + row) * p.zx_stride];
+      float down = lam;
 #pragma unroll
-            for (int f = 0; f < 2; ++f) {
-              const int j = h * 64 + 2 * e + f;
-              if (bad[hh * 4 + (j >> 5)] >> (j & 31) & 1)
-                v[f] = wj[2 * e + f] * bf(p.zx[(first + (size_t)c * kQ + j) * p.zx_stride + di + (h0 + hh) * kSsmP + pp]);
-            }
-          }
-          hi[e] = pack_bf16(v[0], v[1]);
-          lo[e] = pack_bf16(v[0] - __uint_as_float(hi[e] << 16), v[1] - __uint_as_float(hi[e] & 0xFFFF0000u));
+      for (int d = 1; d < 32; d <<= 1) {
+        const float v = __shfl_down_sync(0xffffffffu, down, d);
+        if (lane + d < 32) down += v;
+      }
+      float after = __shfl_down_sync(0xffffffffu, down, 1);
+      if (lane == 31) after = 0.f;
+      float* tot = (float*)(smem + L::kAfter) + b * 8;
+      if (lane == 0) tot[h * 4 + quad] = down;
+      bar_sync(4, 256);  // also: every thread behind is done with the last chunk
+#pragma unroll
+      for (int q = 1; q < 4; ++q)
+        if (q > quad) after += tot[h * 4 + q];
+      sw[h * kQ + row] = dt * ex2(-after);
+      if ((threadIdx.x & 255) < 8) ((uint32_t*)(smem + L::kBad))[(b ^ 1) * 8 + (threadIdx.x & 255)] = 0;
+      // ---- this token's x and B.  Behind the sequence's end lie other rows:
+      // theirs become zero.  An x that is not finite would reach earlier
+      // tokens as 0 * NaN: it becomes zero here and is put back below.
+      wait_warp(L::kFull + b, (c >> 1) & 1);
+      uint8_t* xrow = buf + 2 * kBC + h * kXT + row * 128;
+      if (row >= left) {
+        uint8_t* brow = buf + h * (kQ * 128) + row * 128;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          *(uint4*)(xrow + (e << 4)) = make_uint4(0, 0, 0, 0);
+          *(uint4*)(brow + (e << 4)) = make_uint4(0, 0, 0, 0);
         }
-        tmem_st32(tmem + kTG + lanes + h * 32, hi);
-        tmem_st32(tmem + kTG + 64 + lanes + h * 32, lo);
+        fence_proxy_async_smem();
+      } else {
+        uint32_t acc[2] = {0, 0};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint4 x = *(const uint4*)(xrow + ((e ^ (lane & 7)) << 4));
+          asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[0]) : "r"(x.x), "r"(0));
+          asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[1]) : "r"(x.y), "r"(0));
+          asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[0]) : "r"(x.z), "r"(0));
+          asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[1]) : "r"(x.w), "r"(0));
+        }
+        if ((acc[0] | acc[1]) & 0x7fff7fffu) {
+#pragma unroll 1
+          for (int e = 0; e < 64; ++e) {
+            uint16_t* x = (uint16_t*)xrow + e;
+            if ((*x & 0x7F80) == 0x7F80) *x = 0;
+          }
+          atomicOr(&bad[h * 4 + quad], 1u << lane);
+          fence_proxy_async_smem();
+        }
+      }
+      bar_sync(4, 256);  // sw, x and bad are complete
+      const uint32_t any_bad = (bad[0] | bad[1] | bad[2] | bad[3]) | (bad[4] | bad[5] | bad[6] | bad[7]);
+      // ---- (w X)^T: row (hh, pp), tokens 64 h .. 64 h + 63
+      if (c > 0) wait_warp(L::kS, (c - 1) & 1);
+      tc_fence_after();
+      const uint8_t* xt = buf + 2 * kBC + hh * kXT + (pp & 7) * 2;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int j0 = h * 64 + 32 * q;
+        const float4* wj = (const float4*)(sw + hh * kQ + j0);
+        float v[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e)  // j0 is a multiple of 8
+          v[e] = bf(*(const uint16_t*)(xt + (j0 + e) * 128 + (((pp >> 3) ^ (e & 7)) << 4)));
+        if (any_bad) {
+#pragma unroll 1
+          for (uint32_t bits = bad[hh * 4 + (j0 >> 5)]; bits; bits &= bits - 1) {
+            const int e = __ffs(bits) - 1;
+            const float x = bf(p.zx[(first + (size_t)c * kQ + j0 + e) * p.zx_stride + di + (h0 + hh) * kSsmP + pp]);
+#pragma unroll
+            for (int f = 0; f < 32; ++f)
+              if (f == e) v[f] = x;
+          }
+        }
+        uint32_t hi[16], lo[16];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float4 w4 = wj[e];
+          const float2 r0 = mul2(make_float2(v[4 * e], v[4 * e + 1]), make_float2(w4.x, w4.y));
+          const float2 r1 = mul2(make_float2(v[4 * e + 2], v[4 * e + 3]), make_float2(w4.z, w4.w));
+          hi[2 * e] = pack_bf16(r0.x, r0.y);
+          hi[2 * e + 1] = pack_bf16(r1.x, r1.y);
+          lo[2 * e] = pack_bf16(r0.x - __uint_as_float(hi[2 * e] << 16), r0.y - __uint_as_float(hi[2 * e] & 0xFFFF0000u));
+          lo[2 * e + 1] =
+              pack_bf16(r1.x - __uint_as_float(hi[2 * e + 1] << 16), r1.y - __uint_as_float(hi[2 * e + 1] & 0xFFFF0000u));
+        }
+        tmem_st16(tmem + kTWx + lanes + h * 32 + q * 16, hi);
+        tmem_st16(tmem + kTWx + 64 + lanes + h * 32 + q * 16, lo);
       }
       tmem_st_wait();
       tc_fence_before();
       mbar_arrive(bar(L::kWx));
       // ---- the output: y + D x, gated, over z's row and from there to global
-      wait(L::kYFull + h, c & 1);
-      wait(L::kZFull, c & 1);
+      wait_warp(L::kZFull, c & 1);
+      wait_warp(L::kYFull + h, c & 1);
       tc_fence_after();
       uint8_t* ztile = buf + kBC + h * kXT;
 #pragma unroll
@@ -457,6 +513,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
         tmem_ld32(tmem + kTY + h * 64 + lanes + 32 * q, y);
         tmem_ld_wait();
         if (any_bad) {  // tokens up to this one whose x is not finite
+#pragma unroll 1
           for (int j = 0; j <= row; ++j) {
             if (!(bad[h * 4 + (j >> 5)] >> (j & 31) & 1)) continue;
             const uint16_t* x = p.zx + (first + (size_t)c * kQ + j) * p.zx_stride + di + head * kSsmP + 32 * q;
@@ -473,15 +530,14 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
           uint32_t o[4];
 #pragma unroll
           for (int f = 0; f < 4; ++f) {
-            float r[2];
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              const float x = __uint_as_float(g ? xw[f] & 0xFFFF0000u : xw[f] << 16);
-              const float z = __uint_as_float(g ? zw[f] & 0xFFFF0000u : zw[f] << 16);
-              const float yv = fmaf(skip, x, __uint_as_float(y[8 * e + 2 * f + g]));
-              r[g] = yv * __fdividef(z, 1.f + ex2(-1.44269504088896340736f * z));
-            }
-            o[f] = pack_bf16(r[0], r[1]);
+            const float2 x2 = make_float2(__uint_as_float(xw[f] << 16), __uint_as_float(xw[f] & 0xFFFF0000u));
+            const float2 z2 = make_float2(__uint_as_float(zw[f] << 16), __uint_as_float(zw[f] & 0xFFFF0000u));
+            const float2 y2 = make_float2(__uint_as_float(y[8 * e + 2 * f]), __uint_as_float(y[8 * e + 2 * f + 1]));
+            const float2 t = mul2(z2, make_float2(-1.44269504088896340736f, -1.44269504088896340736f));
+            const float2 d = add2(make_float2(ex2(t.x), ex2(t.y)), make_float2(1.f, 1.f));
+            const float2 g = mul2(z2, make_float2(rcp(d.x), rcp(d.y)));
+            const float2 r = mul2(fma2(skip2, x2, y2), g);
+            o[f] = pack_bf16(r.x, r.y);
           }
           *(uint4*)(ztile + row * 128 + at) = make_uint4(o[0], o[1], o[2], o[3]);
         }
@@ -494,86 +550,137 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
         const uint4 v = *(const uint4*)(ztile + r * 128 + ((at ^ (r & 7)) << 4));
         if (r < left) *(uint4*)(p.out + (first + (size_t)c * kQ + r) * p.out_stride + head * kSsmP + at * 8) = v;
       }
+      fence_proxy_async_smem();  // the next copies into this buffer come by the async proxy
       mbar_arrive(bar(L::kEmpty + b));
     }
-    // ---- the state after the last token
-    wait(L::kS, (chunks - 1) & 1);
-    tc_fence_after();
+  } else {
+    regs_give<kRegsRest>();
+    if (warp == 16) {
+      // ---------------------------------------------------------------- MMAs
+      if (lane == 0) {
+        constexpr uint32_t id_g = idesc_16(128, 128, false, false, false), id_y2 = idesc_16(128, 64, false, false, false),
+                           id_y = idesc_16(128, 64, false, false, true), id_s = idesc_16(128, 128, false, false, true);
+        for (int c = 0; c < chunks; ++c) {
+          const uint32_t buf = sb + (c & 1) * L::kBuf, cm = buf + kBC, x = buf + 2 * kBC;
+          const bool zero = c == 0 && !goes_on;
+          if (!wait(L::kFull + (c & 1), (c >> 1) & 1)) break;
+          tc_fence_after();
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      uint32_t v[32];
-      tmem_ld32(tmem + kTState + lanes + h * 64 + q * 32, v);
-      tmem_ld_wait();
-      float4* dst = (float4*)(p.state_out + state_at + 32 * q);
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        dst[e] = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]), __uint_as_float(v[4 * e + 2]),
-                             __uint_as_float(v[4 * e + 3]));
-    }
-  } else if (warp == 8) {
-    // ------------------------------------------------------------------ MMAs
-    if (lane == 0) {
-      auto wait = [&](int b, uint32_t parity) { return ok = wait_or_flag(bar(b), parity, p.sink, kErrTimeout); };
-      constexpr uint32_t id_g = idesc_16(128, 128, false, false, false), id_y2 = idesc_16(128, 64, false, false, false),
-                         id_y = idesc_16(128, 64, false, false, true), id_s = idesc_16(128, 128, false, false, true);
-      for (int c = 0; c < chunks; ++c) {
-        const uint32_t buf = sb + (c & 1) * L::kBuf, cm = buf + kBC, x = buf + 2 * kBC;
-        const bool zero = c == 0 && !goes_on;
-        if (!wait(L::kFull + (c & 1), (c >> 1) & 1)) break;
-        tc_fence_after();
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t o = (e / 4) * (kQ * 128) + (e % 4) * 32;
-          mma_ss(tmem + kTG, sdesc_sw128(cm + o), sdesc_sw128(buf + o), id_g, e > 0);
-        }
-        tc_commit(bar(L::kG));
-        if (!wait(L::kHFull, c & 1)) break;
-        tc_fence_after();
-        if (!zero) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t o = (e / 4) * (kQ * 128) + (e % 4) * 32;
+            mma_ss(tmem + kTG, sdesc_sw128(cm + o), sdesc_sw128(buf + o), id_g, e > 0);
+          }
+          tc_commit(bar(L::kG));
+          // the threads behind write (w X)^T of this chunk after they have read Y of the last one
+          if (!wait(L::kHFull, c & 1) || !wait(L::kWx, c & 1)) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int h = 0; h < 2 && !zero; ++h)
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               mma_ss(tmem + kTY + h * 64, sdesc_sw128(cm + (e / 4) * (kQ * 128) + (e % 4) * 32),
                      sdesc_sw128(sb + L::kH + h * kXT + (e / 4) * (64 * 128) + (e % 4) * 32), id_y2, e > 0);
+          tc_commit(bar(L::kY2));
+#pragma unroll
+          for (int e = 0; e < 16; ++e)  // the high parts, then the remainders
+            mma_ts(tmem + kTState, tmem + kTWx + 8 * e, sdesc_mn_sw128(buf + (e % 8) * 2048, kQ * 128), id_s, !zero || e > 0);
+          tc_commit(bar(L::kS));
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            if (!wait(L::kMFull + h, c & 1)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              mma_ts(tmem + kTY + h * 64, tmem + kTG + h * 64 + 8 * e, sdesc_mn_sw128(x + h * kXT + e * 2048, kQ * 128), id_y,
+                     !zero || e > 0);
+            tc_commit(bar(L::kYFull + h));
+          }
+          if (!ok) break;
+          tc_commit(bar(L::kEmpty + (c & 1)));
         }
-        tc_commit(bar(L::kY2));
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (!ok || !wait(L::kMFull + h, c & 1)) continue;
-          tc_fence_after();
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            mma_ts(tmem + kTY + h * 64, tmem + kTM + h * 64 + 8 * e, sdesc_mn_sw128(x + h * kXT + e * 2048, kQ * 128), id_y,
-                   !zero || e > 0);
-          tc_commit(bar(L::kYFull + h));
+        if (!ok) {  // give-up: wait (bounded) for the MMAs issued so far
+          tc_commit(bar(L::kDone));
+          for (int n = 0; n < (1 << 20) && !mbar_try_wait(bar(L::kDone), 0); ++n) {
+          }
         }
-        if (!ok || !wait(L::kWx, c & 1)) break;
-        tc_fence_after();
-#pragma unroll
-        for (int e = 0; e < 16; ++e)  // the high parts, then the remainders
-          mma_ts(tmem + kTState, tmem + kTG + 8 * e, sdesc_mn_sw128(buf + (e % 8) * 2048, kQ * 128), id_s, !zero || e > 0);
-        tc_commit(bar(L::kS));
-        tc_commit(bar(L::kEmpty + (c & 1)));
       }
-      if (!ok) {  // give-up: wait (bounded) for the MMAs issued so far
-        tc_commit(bar(L::kDone));
-        for (int n = 0; n < (1 << 20) && !mbar_try_wait(bar(L::kDone), 0); ++n) {
+      __syncwarp();
+    } else if (warp == 17) {
+      // ------------------------------------------------ copies of B, C and x
+      if (p.tiled) {
+        if (lane == 0) {
+          int c = 0;
+          for (; c < chunks; ++c) {
+            const uint32_t buf = sb + (c & 1) * L::kBuf, fb = bar(L::kFull + (c & 1));
+            const int r = (int)first + c * kQ;
+            if (!wait(L::kEmpty + (c & 1), ((c >> 1) & 1) ^ 1)) break;
+            mbar_arrive_expect_tx(fb, L::kBuf);
+            tma_load_3d_plain(buf, &p.tm, 2 * di, 0, r, fb);
+            tma_load_3d_plain(buf + kQ * 128, &p.tm, 2 * di + 64, 0, r, fb);
+            tma_load_3d_plain(buf + kBC, &p.tm, 2 * di + kSsmN, 0, r, fb);
+            tma_load_3d_plain(buf + kBC + kQ * 128, &p.tm, 2 * di + kSsmN + 64, 0, r, fb);
+            tma_load_3d_plain(buf + 2 * kBC, &p.tm, di + h0 * kSsmP, 0, r, fb);
+            tma_load_3d_plain(buf + 2 * kBC + kXT, &p.tm, di + (h0 + 1) * kSsmP, 0, r, fb);
+          }
+          if (!ok)  // give-up: the copies in flight land before the shared memory is left
+            for (int i = max(0, c - 2); i < c; ++i)
+              for (int n = 0; n < (1 << 20) && !mbar_try_wait(bar(L::kFull + (i & 1)), (i >> 1) & 1); ++n) {
+              }
+        }
+      } else {
+        for (int c = 0; c < chunks; ++c) {
+          const uint32_t buf = sb + (c & 1) * L::kBuf;
+          const size_t row0 = first + (size_t)c * kQ;
+          const int n = min(kQ, len - c * kQ);
+          wait_warp(L::kEmpty + (c & 1), ((c >> 1) & 1) ^ 1);
+          if (!ok) break;
+          copy_tile<kSsmN>(buf, p.zx, p.zx_stride, 2 * di, row0, n);
+          copy_tile<kSsmN>(buf + kBC, p.zx, p.zx_stride, 2 * di + kSsmN, row0, n);
+          copy_tile<kSsmP>(buf + 2 * kBC, p.zx, p.zx_stride, di + h0 * kSsmP, row0, n);
+          copy_tile<kSsmP>(buf + 2 * kBC + kXT, p.zx, p.zx_stride, di + (h0 + 1) * kSsmP, row0, n);
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          fence_proxy_async_smem();
+          mbar_arrive(bar(L::kFull + (c & 1)));
         }
       }
+      __syncwarp();
+    } else if (warp == 18) {
+      // ---------------------------- copies of z, over C once its products are done
+      if (p.tiled) {
+        if (lane == 0) {
+          int c = 0;
+          for (; c < chunks; ++c) {
+            const uint32_t dst = sb + (c & 1) * L::kBuf + kBC;
+            const int r = (int)first + c * kQ;
+            if (!wait(L::kY2, c & 1)) break;
+            mbar_arrive_expect_tx(bar(L::kZFull), 2 * kXT);
+            tma_load_3d_plain(dst, &p.tm, h0 * kSsmP, 0, r, bar(L::kZFull));
+            tma_load_3d_plain(dst + kXT, &p.tm, (h0 + 1) * kSsmP, 0, r, bar(L::kZFull));
+          }
+          if (!ok && c > 0)
+            for (int n = 0; n < (1 << 20) && !mbar_try_wait(bar(L::kZFull), (c - 1) & 1); ++n) {
+            }
+        }
+      } else {
+        for (int c = 0; c < chunks; ++c) {
+          const uint32_t dst = sb + (c & 1) * L::kBuf + kBC;
+          const size_t row0 = first + (size_t)c * kQ;
+          const int n = min(kQ, len - c * kQ);
+          wait_warp(L::kY2, c & 1);
+          if (!ok) break;
+          copy_tile<kSsmP>(dst, p.zx, p.zx_stride, h0 * kSsmP, row0, n);
+          copy_tile<kSsmP>(dst + kXT, p.zx, p.zx_stride, (h0 + 1) * kSsmP, row0, n);
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          mbar_arrive(bar(L::kZFull));
+        }
+      }
+      __syncwarp();
     }
-    __syncwarp();
-  } else {
-    const int tid = (int)threadIdx.x - 9 * 32;
-    if (p.zx_stride % 8 == 0)
-      state_copies<true>(p, sb, first, len, h0, tid, ok);
-    else
-      state_copies<false>(p, sb, first, len, h0, tid, ok);
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 8) tmem_dealloc(tmem, 512);
+  if (warp == 16) tmem_dealloc(tmem, 512);
 }
 
 }  // namespace wave
@@ -628,7 +735,9 @@ extern "C" int wave_hybrid_prompt_state(wave_t* h, int layer, const void* weight
     }
     return p.b.n;
   };
+  p.tiled = zx_stride % 8 == 0;
   if (take(true)) {
+    if (p.tiled && encode_rows_map(&p.tm, zxbcdt, pl.in_rows, 1, cu_seqlens[n_seq], zx_stride, kQ)) return WAVE_ECUDA;
     if (cudaFuncSetAttribute(k_prompt_state, cudaFuncAttributeMaxDynamicSharedMemorySize, StateSmem::kTotal) != cudaSuccess)
       return WAVE_ECUDA;
     k_prompt_state<<<p.b.n * (Hs / 2), kStateThreads, StateSmem::kTotal, st>>>(p);
