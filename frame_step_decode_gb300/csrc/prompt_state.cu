@@ -121,13 +121,27 @@ constexpr int kXT = kQ * kSsmP * 2;     // ... of one head's x (or z) tile
 struct StateSmem {
   static constexpr int kBuf = 2 * kBC + 2 * kXT;  // B, C (later z, then out, of both heads), x of both heads
   static constexpr int kH = 2 * kBuf;             // bf16 H of both heads: [2][n / 64][64 rows of 128 B]
-  static constexpr int kA = kH + 2 * kXT;         // [head][128] c_j + log2 dt_j
-  static constexpr int kW = kA + 2 * kQ * 4;      // [head][128] w_j
-  static constexpr int kTot = kW + 2 * kQ * 4;    // [chunk parity][head][warp] sums over the warps' 32 tokens
-  static constexpr int kAfter = kTot + 2 * 2 * 4 * 4;  // the same of the warpgroups behind
-  static constexpr int kBad = kAfter + 2 * 2 * 4 * 4;  // [chunk parity][head][4] tokens with an x that is not finite
-  static constexpr int kBars = kBad + 2 * 2 * 4 * 4;
-  enum { kFull = 0, kEmpty = 2, kZFull = 4, kG = 5, kY2 = 6, kHFull = 7, kMFull = 8, kYFull = 10, kWx = 12, kS = 13, kDone = 14, kCount = 15 };
+  static constexpr int kAfter = kH + 2 * kXT;     // [head][128] the decays behind token j, to the chunk's end
+  static constexpr int kV = kAfter + 2 * kQ * 4;  // [head][128] log2 dt_j - after_j
+  static constexpr int kLast = kV + 2 * kQ * 4;   // [head] the decays of the whole chunk
+  static constexpr int kBad = kLast + 16;         // [chunk % 4][head][4] tokens with an x that is not finite
+  static constexpr int kBars = kBad + 4 * 2 * 4 * 4;
+  enum {
+    kFull = 0,
+    kEmpty = 2,
+    kZFull = 4,
+    kG,
+    kY2,
+    kHFull,
+    kMFull,
+    kYFull = kMFull + 2,
+    kYFree = kYFull + 2,
+    kWx,
+    kS,
+    kScan,
+    kDone,
+    kCount
+  };
   static constexpr int kMisc = kBars + kCount * 8;
   static constexpr int kTotal = kMisc + 16;
 };
@@ -217,6 +231,8 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
       mbar_init(bar(L::kG), 1);
       mbar_init(bar(L::kY2), 1);
       mbar_init(bar(L::kHFull), 256);
+      mbar_init(bar(L::kYFree), 256);
+      mbar_init(bar(L::kScan), 1);
       mbar_init(bar(L::kWx), 256);
       mbar_init(bar(L::kS), 1);
       mbar_init(bar(L::kDone), 1);
@@ -227,7 +243,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
     tmem_alloc(smem_u32(tmem_word), 512);
     tmem_relinquish();
   }
-  if (threadIdx.x < 16) ((uint32_t*)(smem + L::kBad))[threadIdx.x] = 0;
+  if (threadIdx.x < 32) ((uint32_t*)(smem + L::kBad))[threadIdx.x] = 0;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -245,42 +261,22 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
   const uint32_t lanes = (uint32_t)(quad * 32) << 16;
   const int hh = row >> 6, pp = row & 63;  // for the state: row (head hh, p), half h of the columns or tokens
   const int head = h0 + h;
-  float* sa = (float*)(smem + L::kA);
-  float* sw = (float*)(smem + L::kW);
-  const uint16_t* dt_col = p.zx + first * p.zx_stride + 2 * di + 2 * kSsmN + head;
+  float* sv = (float*)(smem + L::kV);
+  float* saft = (float*)(smem + L::kAfter);
+  float* slast = (float*)(smem + L::kLast);
   const size_t state_at = (((size_t)p.b.slot[seq] * p.Hs + h0) * kSsmP + row) * kSsmN + h * 64;
 
   if (warp < 8) {
     // -------------------------------------------------------------- in front
     regs_take<kRegsFront>();
-    const float rate = expf(bf(p.prm[head])) * 1.44269504088896340736f, bias = bf(p.prm[p.Hs + head]);
-    uint16_t dt_next = row < len ? dt_col[(size_t)row * p.zx_stride] : 0;
     for (int c = 0; c < chunks; ++c) {
-      const int left = len - c * kQ;
-      // ---- the decays: c_i and its sums over the chunk's tokens
-      float dt = 0.f, lam = 0.f;
-      if (row < left) dt = step_of(bf(dt_next) + bias, rate, lam);
-      if (row + kQ < left) dt_next = dt_col[(size_t)((c + 1) * kQ + row) * p.zx_stride];
-      float ci = lam;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const float u = __shfl_up_sync(0xffffffffu, ci, d);
-        if (lane >= d) ci += u;
-      }
-      float* tot = (float*)(smem + L::kTot) + (c & 1) * 8;
-      if (lane == 31) tot[h * 4 + quad] = ci;
-      bar_sync(1, 256);  // also: every M of the last chunk is done with sa
-#pragma unroll
-      for (int q = 0; q < 3; ++q)
-        if (q < quad) ci += tot[h * 4 + q];
-      sa[h * kQ + row] = ci + lg2(dt);
       // ---- the state: its bf16 copy for C H^T, and the chunk's decay
+      wait_warp(L::kScan, c & 1);
       if (c > 0) wait_warp(L::kS, (c - 1) & 1);
       tc_fence_after();
       const bool zero = c == 0 && !goes_on;
       if (!zero) {
-        const float* th = tot + hh * 4;
-        const float dec = ex2(-((th[0] + th[1]) + (th[2] + th[3])));
+        const float dec = ex2(-slast[hh]);
         const float2 dec2 = make_float2(dec, dec);
         uint8_t* hrow = smem + L::kH + hh * kXT + h * (64 * 128) + pp * 128;
 #pragma unroll
@@ -319,23 +315,23 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
       }
       tc_fence_before();
       mbar_arrive(bar(L::kHFull));
-      bar_sync(2 + h, 128);  // the head's sa is complete
       // ---- M, over G once both heads have read G
       wait_warp(L::kG, c & 1);
       tc_fence_after();
       uint32_t m[64];
-      const float2 nci = make_float2(-ci, -ci);
+      const float after = saft[h * kQ + row];  // c_j - c_i = after_i - after_j
+      const float2 ai = make_float2(after, after);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         if (q <= quad) {
           uint32_t g[32];
           tmem_ld32(tmem + kTG + lanes + 32 * q, g);
           tmem_ld_wait();
-          const float4* aj = (const float4*)(sa + h * kQ + 32 * q);
+          const float4* vj = (const float4*)(sv + h * kQ + 32 * q);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float4 a4 = aj[e];
-            const float2 t0 = add2(make_float2(a4.x, a4.y), nci), t1 = add2(make_float2(a4.z, a4.w), nci);
+            const float4 v4 = vj[e];
+            const float2 t0 = add2(make_float2(v4.x, v4.y), ai), t1 = add2(make_float2(v4.z, v4.w), ai);
             float2 r0 = mul2(make_float2(__uint_as_float(g[4 * e]), __uint_as_float(g[4 * e + 1])),
                              make_float2(ex2(t0.x), ex2(t0.y)));
             float2 r1 = mul2(make_float2(__uint_as_float(g[4 * e + 2]), __uint_as_float(g[4 * e + 3])),
@@ -363,7 +359,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
       wait_warp(L::kY2, c & 1);
       tc_fence_after();
       if (!zero) {
-        const float ei = ex2(-ci);
+        const float ei = ex2(after - slast[h]);
         const float2 ei2 = make_float2(ei, ei);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
@@ -399,123 +395,125 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
   } else if (warp < 16) {
     // ---------------------------------------------------------------- behind
     regs_take<kRegsBehind>();
-    const float rate = expf(bf(p.prm[head])) * 1.44269504088896340736f, bias = bf(p.prm[p.Hs + head]);
     const float skip = bf(p.prm[2 * p.Hs + head]);
     const float2 skip2 = make_float2(skip, skip);
-    uint16_t dt_next = row < len ? dt_col[(size_t)row * p.zx_stride] : 0;
-    for (int c = 0; c < chunks; ++c) {
+    // (w X)^T of a chunk is made before the output of the chunk before it: the
+    // state's product does not wait for the gate
+    for (int c = -1; c < chunks; ++c) {
+      if (c + 1 < chunks) {
+        const int k = c + 1, b = k & 1, left = len - k * kQ;
+        uint8_t* buf = smem + b * L::kBuf;
+        uint32_t* bad = (uint32_t*)(smem + L::kBad) + (k & 3) * 8;
+        // ---- this token's x and B.  Behind the sequence's end lie other rows:
+        // theirs become zero.  An x that is not finite would reach earlier
+        // tokens as 0 * NaN: it becomes zero here and is put back below.
+        wait_warp(L::kFull + b, (k >> 1) & 1);
+        uint8_t* xrow = buf + 2 * kBC + h * kXT + row * 128;
+        if (row >= left) {
+          uint8_t* brow = buf + h * (kQ * 128) + row * 128;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            *(uint4*)(xrow + (e << 4)) = make_uint4(0, 0, 0, 0);
+            *(uint4*)(brow + (e << 4)) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        } else {
+          uint32_t acc[2] = {0, 0};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint4 x = *(const uint4*)(xrow + ((e ^ (lane & 7)) << 4));
+            asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[0]) : "r"(x.x), "r"(0));
+            asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[1]) : "r"(x.y), "r"(0));
+            asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[0]) : "r"(x.z), "r"(0));
+            asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[1]) : "r"(x.w), "r"(0));
+          }
+          if ((acc[0] | acc[1]) & 0x7fff7fffu) {
+#pragma unroll 1
+            for (int e = 0; e < 64; ++e) {
+              uint16_t* x = (uint16_t*)xrow + e;
+              if ((*x & 0x7F80) == 0x7F80) *x = 0;
+            }
+            atomicOr(&bad[h * 4 + quad], 1u << lane);
+            fence_proxy_async_smem();
+          }
+        }
+        bar_sync(4, 256);  // x and bad are complete; every thread here is done with chunk k - 2
+        // cleared two chunks ahead: nobody sets these before the next barrier
+        if ((threadIdx.x & 255) < 8) ((uint32_t*)(smem + L::kBad))[((k + 2) & 3) * 8 + (threadIdx.x & 255)] = 0;
+        const uint32_t* bh = bad + hh * 4 + h * 2;  // of the tokens below
+        // ---- (w X)^T: row (hh, pp), tokens 64 h .. 64 h + 63
+        wait_warp(L::kScan, k & 1);
+        if (k > 0) wait_warp(L::kS, (k - 1) & 1);
+        tc_fence_after();
+        const uint8_t* xt = buf + 2 * kBC + hh * kXT + (pp & 7) * 2;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int j0 = h * 64 + 32 * q;
+          const float4* vj = (const float4*)(sv + hh * kQ + j0);
+          float v[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e)  // j0 is a multiple of 8
+            v[e] = bf(*(const uint16_t*)(xt + (j0 + e) * 128 + (((pp >> 3) ^ (e & 7)) << 4)));
+          if (bh[q]) {
+#pragma unroll 1
+            for (uint32_t bits = bh[q]; bits; bits &= bits - 1) {
+              const int e = __ffs(bits) - 1;
+              const float x = bf(p.zx[(first + (size_t)k * kQ + j0 + e) * p.zx_stride + di + (h0 + hh) * kSsmP + pp]);
+#pragma unroll
+              for (int f = 0; f < 32; ++f)
+                if (f == e) v[f] = x;
+            }
+          }
+          uint32_t hi[16], lo[16];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float4 v4 = vj[e];
+            const float2 r0 = mul2(make_float2(v[4 * e], v[4 * e + 1]), make_float2(ex2(v4.x), ex2(v4.y)));
+            const float2 r1 = mul2(make_float2(v[4 * e + 2], v[4 * e + 3]), make_float2(ex2(v4.z), ex2(v4.w)));
+            hi[2 * e] = pack_bf16(r0.x, r0.y);
+            hi[2 * e + 1] = pack_bf16(r1.x, r1.y);
+            lo[2 * e] = pack_bf16(r0.x - __uint_as_float(hi[2 * e] << 16), r0.y - __uint_as_float(hi[2 * e] & 0xFFFF0000u));
+            lo[2 * e + 1] =
+                pack_bf16(r1.x - __uint_as_float(hi[2 * e + 1] << 16), r1.y - __uint_as_float(hi[2 * e + 1] & 0xFFFF0000u));
+          }
+          tmem_st16(tmem + kTWx + lanes + h * 32 + q * 16, hi);
+          tmem_st16(tmem + kTWx + 64 + lanes + h * 32 + q * 16, lo);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(bar(L::kWx));
+      }
+      if (c < 0) continue;
+      // ---- the output: y + D x, gated, over z's row and from there to global
       const int b = c & 1, left = len - c * kQ;
       uint8_t* buf = smem + b * L::kBuf;
-      uint32_t* bad = (uint32_t*)(smem + L::kBad) + b * 8;
-      // ---- w: the decays from behind each token to the chunk's end, summed from the end
-      float dt = 0.f, lam = 0.f;
-      if (row < left) dt = step_of(bf(dt_next) + bias, rate, lam);
-      if (row + kQ < left) dt_next = dt_col[(size_t)((c + 1) * kQ + row) * p.zx_stride];
-      float down = lam;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const float v = __shfl_down_sync(0xffffffffu, down, d);
-        if (lane + d < 32) down += v;
-      }
-      float after = __shfl_down_sync(0xffffffffu, down, 1);
-      if (lane == 31) after = 0.f;
-      float* tot = (float*)(smem + L::kAfter) + b * 8;
-      if (lane == 0) tot[h * 4 + quad] = down;
-      bar_sync(4, 256);  // also: every thread behind is done with the last chunk
-#pragma unroll
-      for (int q = 1; q < 4; ++q)
-        if (q > quad) after += tot[h * 4 + q];
-      sw[h * kQ + row] = dt * ex2(-after);
-      if ((threadIdx.x & 255) < 8) ((uint32_t*)(smem + L::kBad))[(b ^ 1) * 8 + (threadIdx.x & 255)] = 0;
-      // ---- this token's x and B.  Behind the sequence's end lie other rows:
-      // theirs become zero.  An x that is not finite would reach earlier
-      // tokens as 0 * NaN: it becomes zero here and is put back below.
-      wait_warp(L::kFull + b, (c >> 1) & 1);
-      uint8_t* xrow = buf + 2 * kBC + h * kXT + row * 128;
-      if (row >= left) {
-        uint8_t* brow = buf + h * (kQ * 128) + row * 128;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          *(uint4*)(xrow + (e << 4)) = make_uint4(0, 0, 0, 0);
-          *(uint4*)(brow + (e << 4)) = make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async_smem();
-      } else {
-        uint32_t acc[2] = {0, 0};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint4 x = *(const uint4*)(xrow + ((e ^ (lane & 7)) << 4));
-          asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[0]) : "r"(x.x), "r"(0));
-          asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[1]) : "r"(x.y), "r"(0));
-          asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[0]) : "r"(x.z), "r"(0));
-          asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[1]) : "r"(x.w), "r"(0));
-        }
-        if ((acc[0] | acc[1]) & 0x7fff7fffu) {
-#pragma unroll 1
-          for (int e = 0; e < 64; ++e) {
-            uint16_t* x = (uint16_t*)xrow + e;
-            if ((*x & 0x7F80) == 0x7F80) *x = 0;
-          }
-          atomicOr(&bad[h * 4 + quad], 1u << lane);
-          fence_proxy_async_smem();
-        }
-      }
-      bar_sync(4, 256);  // sw, x and bad are complete
-      const uint32_t any_bad = (bad[0] | bad[1] | bad[2] | bad[3]) | (bad[4] | bad[5] | bad[6] | bad[7]);
-      // ---- (w X)^T: row (hh, pp), tokens 64 h .. 64 h + 63
-      if (c > 0) wait_warp(L::kS, (c - 1) & 1);
-      tc_fence_after();
-      const uint8_t* xt = buf + 2 * kBC + hh * kXT + (pp & 7) * 2;
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int j0 = h * 64 + 32 * q;
-        const float4* wj = (const float4*)(sw + hh * kQ + j0);
-        float v[32];
-#pragma unroll
-        for (int e = 0; e < 32; ++e)  // j0 is a multiple of 8
-          v[e] = bf(*(const uint16_t*)(xt + (j0 + e) * 128 + (((pp >> 3) ^ (e & 7)) << 4)));
-        if (any_bad) {
-#pragma unroll 1
-          for (uint32_t bits = bad[hh * 4 + (j0 >> 5)]; bits; bits &= bits - 1) {
-            const int e = __ffs(bits) - 1;
-            const float x = bf(p.zx[(first + (size_t)c * kQ + j0 + e) * p.zx_stride + di + (h0 + hh) * kSsmP + pp]);
-#pragma unroll
-            for (int f = 0; f < 32; ++f)
-              if (f == e) v[f] = x;
-          }
-        }
-        uint32_t hi[16], lo[16];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float4 w4 = wj[e];
-          const float2 r0 = mul2(make_float2(v[4 * e], v[4 * e + 1]), make_float2(w4.x, w4.y));
-          const float2 r1 = mul2(make_float2(v[4 * e + 2], v[4 * e + 3]), make_float2(w4.z, w4.w));
-          hi[2 * e] = pack_bf16(r0.x, r0.y);
-          hi[2 * e + 1] = pack_bf16(r1.x, r1.y);
-          lo[2 * e] = pack_bf16(r0.x - __uint_as_float(hi[2 * e] << 16), r0.y - __uint_as_float(hi[2 * e] & 0xFFFF0000u));
-          lo[2 * e + 1] =
-              pack_bf16(r1.x - __uint_as_float(hi[2 * e + 1] << 16), r1.y - __uint_as_float(hi[2 * e + 1] & 0xFFFF0000u));
-        }
-        tmem_st16(tmem + kTWx + lanes + h * 32 + q * 16, hi);
-        tmem_st16(tmem + kTWx + 64 + lanes + h * 32 + q * 16, lo);
-      }
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(bar(L::kWx));
-      // ---- the output: y + D x, gated, over z's row and from there to global
+      const uint8_t* xrow = buf + 2 * kBC + h * kXT + row * 128;
+      uint8_t* ztile = buf + kBC + h * kXT;
+      const uint32_t* bad = (const uint32_t*)(smem + L::kBad) + (c & 3) * 8 + h * 4;
+      const uint32_t any_bad = (bad[0] | bad[1]) | (bad[2] | bad[3]);
       wait_warp(L::kZFull, c & 1);
       wait_warp(L::kYFull + h, c & 1);
       tc_fence_after();
-      uint8_t* ztile = buf + kBC + h * kXT;
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         uint32_t y[32];
         tmem_ld32(tmem + kTY + h * 64 + lanes + 32 * q, y);
+        uint4 xv[4], zv[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int at = ((q * 4 + e) ^ (row & 7)) << 4;
+          xv[e] = *(const uint4*)(xrow + at);
+          zv[e] = *(const uint4*)(ztile + row * 128 + at);
+        }
         tmem_ld_wait();
+        if (q == 1) {
+          tc_fence_before();
+          mbar_arrive(bar(L::kYFree));
+        }
         if (any_bad) {  // tokens up to this one whose x is not finite
 #pragma unroll 1
           for (int j = 0; j <= row; ++j) {
-            if (!(bad[h * 4 + (j >> 5)] >> (j & 31) & 1)) continue;
+            if (!(bad[j >> 5] >> (j & 31) & 1)) continue;
             const uint16_t* x = p.zx + (first + (size_t)c * kQ + j) * p.zx_stride + di + head * kSsmP + 32 * q;
 #pragma unroll
             for (int e = 0; e < 32; ++e)
@@ -524,9 +522,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int at = ((q * 4 + e) ^ (row & 7)) << 4;
-          const uint4 xv = *(const uint4*)(xrow + at), zv = *(const uint4*)(ztile + row * 128 + at);
-          const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w}, zw[4] = {zv.x, zv.y, zv.z, zv.w};
+          const uint32_t xw[4] = {xv[e].x, xv[e].y, xv[e].z, xv[e].w}, zw[4] = {zv[e].x, zv[e].y, zv[e].z, zv[e].w};
           uint32_t o[4];
 #pragma unroll
           for (int f = 0; f < 4; ++f) {
@@ -539,10 +535,9 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
             const float2 r = mul2(fma2(skip2, x2, y2), g);
             o[f] = pack_bf16(r.x, r.y);
           }
-          *(uint4*)(ztile + row * 128 + at) = make_uint4(o[0], o[1], o[2], o[3]);
+          *(uint4*)(ztile + row * 128 + (((q * 4 + e) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
         }
       }
-      tc_fence_before();
       __syncwarp();
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
@@ -571,8 +566,13 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
             mma_ss(tmem + kTG, sdesc_sw128(cm + o), sdesc_sw128(buf + o), id_g, e > 0);
           }
           tc_commit(bar(L::kG));
-          // the threads behind write (w X)^T of this chunk after they have read Y of the last one
           if (!wait(L::kHFull, c & 1) || !wait(L::kWx, c & 1)) break;
+          tc_fence_after();
+#pragma unroll
+          for (int e = 0; e < 16; ++e)  // the high parts, then the remainders
+            mma_ts(tmem + kTState, tmem + kTWx + 8 * e, sdesc_mn_sw128(buf + (e % 8) * 2048, kQ * 128), id_s, !zero || e > 0);
+          tc_commit(bar(L::kS));
+          if (c > 0 && !wait(L::kYFree, (c - 1) & 1)) break;
           tc_fence_after();
 #pragma unroll 1
           for (int h = 0; h < 2 && !zero; ++h)
@@ -581,10 +581,6 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
               mma_ss(tmem + kTY + h * 64, sdesc_sw128(cm + (e / 4) * (kQ * 128) + (e % 4) * 32),
                      sdesc_sw128(sb + L::kH + h * kXT + (e / 4) * (64 * 128) + (e % 4) * 32), id_y2, e > 0);
           tc_commit(bar(L::kY2));
-#pragma unroll
-          for (int e = 0; e < 16; ++e)  // the high parts, then the remainders
-            mma_ts(tmem + kTState, tmem + kTWx + 8 * e, sdesc_mn_sw128(buf + (e % 8) * 2048, kQ * 128), id_s, !zero || e > 0);
-          tc_commit(bar(L::kS));
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
             if (!wait(L::kMFull + h, c & 1)) break;
@@ -673,6 +669,71 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
           asm volatile("cp.async.wait_all;" ::: "memory");
           mbar_arrive(bar(L::kZFull));
         }
+      }
+      __syncwarp();
+    } else {
+      // ------------------------------ the decays, a chunk ahead: lane l has
+      // tokens 4 l .. 4 l + 3 of both heads.  They are summed from the chunk's
+      // end, so that the weights of the state's newest tokens are exact to
+      // fp32 whatever the sum over the chunk is.
+      float rate[2], bias[2];
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        rate[g] = expf(bf(p.prm[h0 + g])) * 1.44269504088896340736f;
+        bias[g] = bf(p.prm[p.Hs + h0 + g]);
+      }
+      const uint16_t* col = p.zx + first * p.zx_stride + 2 * di + 2 * kSsmN + h0;  // two heads: 4 bytes
+      uint32_t raw[4];
+      auto fetch = [&](int c) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int j = c * kQ + 4 * lane + t;
+          raw[t] = j < len ? *(const uint32_t*)(col + (size_t)j * p.zx_stride) : 0;
+        }
+      };
+      fetch(0);
+      for (int c = 0; c < chunks; ++c) {
+        const int left = len - c * kQ;
+        float dt[2][4], after[2][4], last[2];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          float lam[4];
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            dt[g][t] = step_of((g ? __uint_as_float(raw[t] & 0xFFFF0000u) : __uint_as_float(raw[t] << 16)) + bias[g], rate[g], lam[t]);
+            if (4 * lane + t >= left) dt[g][t] = lam[t] = 0.f;
+          }
+          float down = (lam[0] + lam[1]) + (lam[2] + lam[3]);  // this lane's and the later ones'
+#pragma unroll
+          for (int d = 1; d < 32; d <<= 1) {
+            const float v = __shfl_down_sync(0xffffffffu, down, d);
+            if (lane + d < 32) down += v;
+          }
+          float a = __shfl_down_sync(0xffffffffu, down, 1);
+          if (lane == 31) a = 0.f;
+          last[g] = __shfl_sync(0xffffffffu, down, 0);
+#pragma unroll
+          for (int t = 3; t >= 0; --t) {
+            after[g][t] = a;
+            a += lam[t];
+          }
+        }
+        if (c + 1 < chunks) fetch(c + 1);
+        if (c > 0) {  // the last chunk's have been read
+          wait_warp(L::kWx, (c - 1) & 1);
+          wait_warp(L::kMFull, (c - 1) & 1);
+          wait_warp(L::kMFull + 1, (c - 1) & 1);
+          if (!ok) break;
+        }
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          *(float4*)(saft + g * kQ + 4 * lane) = make_float4(after[g][0], after[g][1], after[g][2], after[g][3]);
+          *(float4*)(sv + g * kQ + 4 * lane) = make_float4(lg2(dt[g][0]) - after[g][0], lg2(dt[g][1]) - after[g][1],
+                                                           lg2(dt[g][2]) - after[g][2], lg2(dt[g][3]) - after[g][3]);
+          if (lane == 0) slast[g] = last[g];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::kScan));
       }
       __syncwarp();
     }
