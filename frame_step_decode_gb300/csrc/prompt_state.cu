@@ -123,13 +123,16 @@ struct StateSmem {
   static constexpr int kH = 2 * kBuf;             // bf16 H of both heads: [2][n / 64][64 rows of 128 B]
   static constexpr int kAfter = kH + 2 * kXT;     // [head][128] the decays behind token j, to the chunk's end
   static constexpr int kV = kAfter + 2 * kQ * 4;  // [head][128] log2 dt_j - after_j
-  static constexpr int kLast = kV + 2 * kQ * 4;   // [head] the decays of the whole chunk
-  static constexpr int kBad = kLast + 16;         // [chunk % 4][head][4] tokens with an x that is not finite
-  static constexpr int kBars = kBad + 4 * 2 * 4 * 4;
+  static constexpr int kU = kV + 2 * kQ * 4;      // [head][96] dt_j 2^-(the decays behind j in its 32 tokens)
+  static constexpr int kLast = kU + 2 * 96 * 4;   // [head] the decays of the whole chunk
+  static constexpr int kBad = kLast + 8;          // [chunk % 4] bit head * 4 + warp: an x that is not finite
+  static constexpr int kBars = kBad + 4 * 4;
   enum {
-    kFull = 0,
-    kEmpty = 2,
-    kZFull = 4,
+    kFull = 0,             // B and x
+    kEmpty = kFull + 2,
+    kCFull = kEmpty + 2,   // C
+    kCEmpty = kCFull + 2,  // ... and the z and out that follow it
+    kZFull = kCEmpty + 2,
     kG,
     kY2,
     kHFull,
@@ -192,6 +195,16 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
+template <int n>
+__device__ __forceinline__ void scale_regs(uint32_t* v, float f) {
+#pragma unroll
+  for (int e = 0; e < n; e += 2) {
+    const float2 r = mul2(make_float2(__uint_as_float(v[e]), __uint_as_float(v[e + 1])), make_float2(f, f));
+    v[e] = __float_as_uint(r.x);
+    v[e + 1] = __float_as_uint(r.y);
+  }
+}
+
 // softplus and the log-decay of a token (in powers of two, positive).  2^-160
 // is zero in fp32: a larger step changes nothing, and the cap bounds the
 // rounding of the sums.
@@ -223,7 +236,9 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
       const int copies = p.tiled ? 1 : 32;
       for (int b = 0; b < 2; ++b) {
         mbar_init(bar(L::kFull + b), copies);
-        mbar_init(bar(L::kEmpty + b), 257);  // the 256 threads behind and the MMAs
+        mbar_init(bar(L::kEmpty + b), 1);
+        mbar_init(bar(L::kCFull + b), copies);
+        mbar_init(bar(L::kCEmpty + b), 256);
         mbar_init(bar(L::kMFull + b), 128);
         mbar_init(bar(L::kYFull + b), 1);
       }
@@ -243,7 +258,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
     tmem_alloc(smem_u32(tmem_word), 512);
     tmem_relinquish();
   }
-  if (threadIdx.x < 32) ((uint32_t*)(smem + L::kBad))[threadIdx.x] = 0;
+  if (threadIdx.x < 4) ((uint32_t*)(smem + L::kBad))[threadIdx.x] = 0;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -263,12 +278,15 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
   const int head = h0 + h;
   float* sv = (float*)(smem + L::kV);
   float* saft = (float*)(smem + L::kAfter);
+  float* su = (float*)(smem + L::kU);
   float* slast = (float*)(smem + L::kLast);
+  uint32_t* sbad = (uint32_t*)(smem + L::kBad);
   const size_t state_at = (((size_t)p.b.slot[seq] * p.Hs + h0) * kSsmP + row) * kSsmN + h * 64;
 
   if (warp < 8) {
     // -------------------------------------------------------------- in front
     regs_take<kRegsFront>();
+    const float skip = bf(p.prm[2 * p.Hs + head]);
     for (int c = 0; c < chunks; ++c) {
       // ---- the state: its bf16 copy for C H^T, and the chunk's decay
       wait_warp(L::kScan, c & 1);
@@ -277,39 +295,33 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
       const bool zero = c == 0 && !goes_on;
       if (!zero) {
         const float dec = ex2(-slast[hh]);
-        const float2 dec2 = make_float2(dec, dec);
         uint8_t* hrow = smem + L::kH + hh * kXT + h * (64 * 128) + pp * 128;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t v[32];
-          if (c == 0) {
-            const float4* src = (const float4*)(p.state_in + state_at + 32 * q);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float4 f = src[e];
-              v[4 * e] = __float_as_uint(f.x), v[4 * e + 1] = __float_as_uint(f.y);
-              v[4 * e + 2] = __float_as_uint(f.z), v[4 * e + 3] = __float_as_uint(f.w);
-            }
-          } else {
-            tmem_ld32(tmem + kTState + lanes + h * 64 + q * 32, v);
-            tmem_ld_wait();
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint4 w;
-            w.x = pack_bf16(__uint_as_float(v[8 * e]), __uint_as_float(v[8 * e + 1]));
-            w.y = pack_bf16(__uint_as_float(v[8 * e + 2]), __uint_as_float(v[8 * e + 3]));
-            w.z = pack_bf16(__uint_as_float(v[8 * e + 4]), __uint_as_float(v[8 * e + 5]));
-            w.w = pack_bf16(__uint_as_float(v[8 * e + 6]), __uint_as_float(v[8 * e + 7]));
-            *(uint4*)(hrow + (((q * 4 + e) ^ (pp & 7)) << 4)) = w;
-          }
+        uint32_t v[64];
+        if (c == 0) {
+          const float4* src = (const float4*)(p.state_in + state_at);
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const float2 r = mul2(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), dec2);
-            v[2 * e] = __float_as_uint(r.x), v[2 * e + 1] = __float_as_uint(r.y);
+            const float4 f = src[e];
+            v[4 * e] = __float_as_uint(f.x), v[4 * e + 1] = __float_as_uint(f.y);
+            v[4 * e + 2] = __float_as_uint(f.z), v[4 * e + 3] = __float_as_uint(f.w);
           }
-          tmem_st32(tmem + kTState + lanes + h * 64 + q * 32, v);
+        } else {
+          tmem_ld32(tmem + kTState + lanes + h * 64, v);
+          tmem_ld32(tmem + kTState + lanes + h * 64 + 32, v + 32);
+          tmem_ld_wait();
         }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          uint4 w;
+          w.x = pack_bf16(__uint_as_float(v[8 * e]), __uint_as_float(v[8 * e + 1]));
+          w.y = pack_bf16(__uint_as_float(v[8 * e + 2]), __uint_as_float(v[8 * e + 3]));
+          w.z = pack_bf16(__uint_as_float(v[8 * e + 4]), __uint_as_float(v[8 * e + 5]));
+          w.w = pack_bf16(__uint_as_float(v[8 * e + 6]), __uint_as_float(v[8 * e + 7]));
+          *(uint4*)(hrow + ((e ^ (pp & 7)) << 4)) = w;
+        }
+        scale_regs<64>(v, dec);
+        tmem_st32(tmem + kTState + lanes + h * 64, v);
+        tmem_st32(tmem + kTState + lanes + h * 64 + 32, v + 32);
         tmem_st_wait();
         fence_proxy_async_smem();
       }
@@ -320,30 +332,50 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
       tc_fence_after();
       uint32_t m[64];
       const float after = saft[h * kQ + row];  // c_j - c_i = after_i - after_j
-      const float2 ai = make_float2(after, after);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        if (q <= quad) {
+        if (q < quad) {
+          // below the diagonal: the decay from token j's end of 32 tokens to i
+          // is a factor of the row, that from j to there is in u_j
           uint32_t g[32];
           tmem_ld32(tmem + kTG + lanes + 32 * q, g);
+          const float r = ex2(after - saft[h * kQ + 32 * q + 31]);
+          const float2 r2 = make_float2(r, r);
+          const float4* uj = (const float4*)(su + h * 96 + 32 * q);
           tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float4 u4 = uj[e];
+            const float2 m0 = mul2(mul2(make_float2(__uint_as_float(g[4 * e]), __uint_as_float(g[4 * e + 1])), r2),
+                                   make_float2(u4.x, u4.y));
+            const float2 m1 = mul2(mul2(make_float2(__uint_as_float(g[4 * e + 2]), __uint_as_float(g[4 * e + 3])), r2),
+                                   make_float2(u4.z, u4.w));
+            m[16 * q + 2 * e] = pack_bf16(m0.x, m0.y);
+            m[16 * q + 2 * e + 1] = pack_bf16(m1.x, m1.y);
+          }
+        } else if (q == quad) {
+          // on it: D x_i is added to y_i as D on the diagonal
+          uint32_t g[32];
+          tmem_ld32(tmem + kTG + lanes + 32 * q, g);
+          const float2 ai = make_float2(after, after);
           const float4* vj = (const float4*)(sv + h * kQ + 32 * q);
+          tmem_ld_wait();
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float4 v4 = vj[e];
             const float2 t0 = add2(make_float2(v4.x, v4.y), ai), t1 = add2(make_float2(v4.z, v4.w), ai);
-            float2 r0 = mul2(make_float2(__uint_as_float(g[4 * e]), __uint_as_float(g[4 * e + 1])),
-                             make_float2(ex2(t0.x), ex2(t0.y)));
-            float2 r1 = mul2(make_float2(__uint_as_float(g[4 * e + 2]), __uint_as_float(g[4 * e + 3])),
-                             make_float2(ex2(t1.x), ex2(t1.y)));
-            if (q == quad) {
-              if (4 * e > lane) r0.x = 0.f;
-              if (4 * e + 1 > lane) r0.y = 0.f;
-              if (4 * e + 2 > lane) r1.x = 0.f;
-              if (4 * e + 3 > lane) r1.y = 0.f;
+            const float2 m0 = mul2(make_float2(__uint_as_float(g[4 * e]), __uint_as_float(g[4 * e + 1])),
+                                   make_float2(ex2(t0.x), ex2(t0.y)));
+            const float2 m1 = mul2(make_float2(__uint_as_float(g[4 * e + 2]), __uint_as_float(g[4 * e + 3])),
+                                   make_float2(ex2(t1.x), ex2(t1.y)));
+            float f[4] = {m0.x, m0.y, m1.x, m1.y};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (4 * e + k > lane) f[k] = 0.f;
+              if (4 * e + k == lane) f[k] += skip;
             }
-            m[16 * q + 2 * e] = pack_bf16(r0.x, r0.y);
-            m[16 * q + 2 * e + 1] = pack_bf16(r1.x, r1.y);
+            m[16 * q + 2 * e] = pack_bf16(f[0], f[1]);
+            m[16 * q + 2 * e + 1] = pack_bf16(f[2], f[3]);
           }
         } else {
 #pragma unroll
@@ -359,20 +391,14 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
       wait_warp(L::kY2, c & 1);
       tc_fence_after();
       if (!zero) {
+        uint32_t v[64];
+        tmem_ld32(tmem + kTY + h * 64 + lanes, v);
+        tmem_ld32(tmem + kTY + h * 64 + lanes + 32, v + 32);
         const float ei = ex2(after - slast[h]);
-        const float2 ei2 = make_float2(ei, ei);
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          uint32_t v[32];
-          tmem_ld32(tmem + kTY + h * 64 + lanes + 32 * q, v);
-          tmem_ld_wait();
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float2 r = mul2(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), ei2);
-            v[2 * e] = __float_as_uint(r.x), v[2 * e + 1] = __float_as_uint(r.y);
-          }
-          tmem_st32(tmem + kTY + h * 64 + lanes + 32 * q, v);
-        }
+        tmem_ld_wait();
+        scale_regs<64>(v, ei);
+        tmem_st32(tmem + kTY + h * 64 + lanes, v);
+        tmem_st32(tmem + kTY + h * 64 + lanes + 32, v + 32);
       }
       tmem_st_wait();
       tc_fence_before();
@@ -395,15 +421,12 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
   } else if (warp < 16) {
     // ---------------------------------------------------------------- behind
     regs_take<kRegsBehind>();
-    const float skip = bf(p.prm[2 * p.Hs + head]);
-    const float2 skip2 = make_float2(skip, skip);
     // (w X)^T of a chunk is made before the output of the chunk before it: the
     // state's product does not wait for the gate
     for (int c = -1; c < chunks; ++c) {
       if (c + 1 < chunks) {
         const int k = c + 1, b = k & 1, left = len - k * kQ;
         uint8_t* buf = smem + b * L::kBuf;
-        uint32_t* bad = (uint32_t*)(smem + L::kBad) + (k & 3) * 8;
         // ---- this token's x and B.  Behind the sequence's end lie other rows:
         // theirs become zero.  An x that is not finite would reach earlier
         // tokens as 0 * NaN: it becomes zero here and is put back below.
@@ -433,14 +456,14 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
               uint16_t* x = (uint16_t*)xrow + e;
               if ((*x & 0x7F80) == 0x7F80) *x = 0;
             }
-            atomicOr(&bad[h * 4 + quad], 1u << lane);
+            atomicOr(&sbad[k & 3], 1u << (h * 4 + quad));
             fence_proxy_async_smem();
           }
         }
         bar_sync(4, 256);  // x and bad are complete; every thread here is done with chunk k - 2
         // cleared two chunks ahead: nobody sets these before the next barrier
-        if ((threadIdx.x & 255) < 8) ((uint32_t*)(smem + L::kBad))[((k + 2) & 3) * 8 + (threadIdx.x & 255)] = 0;
-        const uint32_t* bh = bad + hh * 4 + h * 2;  // of the tokens below
+        if ((threadIdx.x & 255) == 0) sbad[(k + 2) & 3] = 0;
+        const uint32_t bad = sbad[k & 3] >> (hh * 4 + h * 2);  // of the tokens below
         // ---- (w X)^T: row (hh, pp), tokens 64 h .. 64 h + 63
         wait_warp(L::kScan, k & 1);
         if (k > 0) wait_warp(L::kS, (k - 1) & 1);
@@ -449,32 +472,46 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           const int j0 = h * 64 + 32 * q;
-          const float4* vj = (const float4*)(sv + hh * kQ + j0);
           float v[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e)  // j0 is a multiple of 8
             v[e] = bf(*(const uint16_t*)(xt + (j0 + e) * 128 + (((pp >> 3) ^ (e & 7)) << 4)));
-          if (bh[q]) {
-#pragma unroll 1
-            for (uint32_t bits = bh[q]; bits; bits &= bits - 1) {
-              const int e = __ffs(bits) - 1;
-              const float x = bf(p.zx[(first + (size_t)k * kQ + j0 + e) * p.zx_stride + di + (h0 + hh) * kSsmP + pp]);
+          if (bad >> q & 1) {
+            const uint16_t* x = p.zx + (first + (size_t)k * kQ + j0) * p.zx_stride + di + (h0 + hh) * kSsmP + pp;
 #pragma unroll
-              for (int f = 0; f < 32; ++f)
-                if (f == e) v[f] = x;
+            for (int e = 0; e < 32; ++e)
+              if (j0 + e < left) v[e] = bf(x[e * p.zx_stride]);
+          }
+          // w_j: u_j times the decay from its 32 tokens' end on (none after the last 32)
+          if (q == 0 || h == 0) {
+            const float tail = ex2(-saft[hh * kQ + j0 + 31]);
+            const float4* uj = (const float4*)(su + hh * 96 + j0);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float4 u4 = uj[e];
+              const float2 w0 = mul2(make_float2(u4.x, u4.y), make_float2(tail, tail));
+              const float2 w1 = mul2(make_float2(u4.z, u4.w), make_float2(tail, tail));
+              const float2 r0 = mul2(make_float2(v[4 * e], v[4 * e + 1]), w0);
+              const float2 r1 = mul2(make_float2(v[4 * e + 2], v[4 * e + 3]), w1);
+              v[4 * e] = r0.x, v[4 * e + 1] = r0.y, v[4 * e + 2] = r1.x, v[4 * e + 3] = r1.y;
+            }
+          } else {
+            const float4* vj = (const float4*)(sv + hh * kQ + j0);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float4 v4 = vj[e];
+              const float2 r0 = mul2(make_float2(v[4 * e], v[4 * e + 1]), make_float2(ex2(v4.x), ex2(v4.y)));
+              const float2 r1 = mul2(make_float2(v[4 * e + 2], v[4 * e + 3]), make_float2(ex2(v4.z), ex2(v4.w)));
+              v[4 * e] = r0.x, v[4 * e + 1] = r0.y, v[4 * e + 2] = r1.x, v[4 * e + 3] = r1.y;
             }
           }
           uint32_t hi[16], lo[16];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float4 v4 = vj[e];
-            const float2 r0 = mul2(make_float2(v[4 * e], v[4 * e + 1]), make_float2(ex2(v4.x), ex2(v4.y)));
-            const float2 r1 = mul2(make_float2(v[4 * e + 2], v[4 * e + 3]), make_float2(ex2(v4.z), ex2(v4.w)));
-            hi[2 * e] = pack_bf16(r0.x, r0.y);
-            hi[2 * e + 1] = pack_bf16(r1.x, r1.y);
-            lo[2 * e] = pack_bf16(r0.x - __uint_as_float(hi[2 * e] << 16), r0.y - __uint_as_float(hi[2 * e] & 0xFFFF0000u));
-            lo[2 * e + 1] =
-                pack_bf16(r1.x - __uint_as_float(hi[2 * e + 1] << 16), r1.y - __uint_as_float(hi[2 * e + 1] & 0xFFFF0000u));
+          for (int e = 0; e < 16; ++e) {
+            hi[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+            const float2 r = sub2(make_float2(v[2 * e], v[2 * e + 1]),
+                                  make_float2(__uint_as_float(hi[e] << 16), __uint_as_float(hi[e] & 0xFFFF0000u)));
+            lo[e] = pack_bf16(r.x, r.y);
           }
           tmem_st16(tmem + kTWx + lanes + h * 32 + q * 16, hi);
           tmem_st16(tmem + kTWx + 64 + lanes + h * 32 + q * 16, lo);
@@ -484,59 +521,54 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
         mbar_arrive(bar(L::kWx));
       }
       if (c < 0) continue;
-      // ---- the output: y + D x, gated, over z's row and from there to global
+      // ---- the output: y, gated, over z's row and from there to global
       const int b = c & 1, left = len - c * kQ;
       uint8_t* buf = smem + b * L::kBuf;
-      const uint8_t* xrow = buf + 2 * kBC + h * kXT + row * 128;
       uint8_t* ztile = buf + kBC + h * kXT;
-      const uint32_t* bad = (const uint32_t*)(smem + L::kBad) + (c & 3) * 8 + h * 4;
-      const uint32_t any_bad = (bad[0] | bad[1]) | (bad[2] | bad[3]);
+      const uint32_t any_bad = sbad[c & 3] >> (h * 4) & 15u;
       wait_warp(L::kZFull, c & 1);
       wait_warp(L::kYFull + h, c & 1);
       tc_fence_after();
+      uint32_t y[64];
+      tmem_ld32(tmem + kTY + h * 64 + lanes, y);
+      tmem_ld32(tmem + kTY + h * 64 + lanes + 32, y + 32);
+      tmem_ld_wait();
+      tc_fence_before();
+      mbar_arrive(bar(L::kYFree));
+      if (any_bad) {  // tokens up to this one whose x is not finite
+#pragma unroll 1
+        for (int j = 0; j <= row && j < left; ++j) {
+          if (!(any_bad >> (j >> 5) & 1)) continue;
+          const uint16_t* x = p.zx + (first + (size_t)c * kQ + j) * p.zx_stride + di + head * kSsmP;
+#pragma unroll
+          for (int e = 0; e < 64; ++e)
+            if ((x[e] & 0x7F80) == 0x7F80) y[e] = 0x7FC00000u;
+        }
+      }
+      uint8_t* zrow = ztile + row * 128;
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        uint32_t y[32];
-        tmem_ld32(tmem + kTY + h * 64 + lanes + 32 * q, y);
-        uint4 xv[4], zv[4];
+        uint4 zv[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) zv[e] = *(const uint4*)(zrow + (((q * 4 + e) ^ (row & 7)) << 4));
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int at = ((q * 4 + e) ^ (row & 7)) << 4;
-          xv[e] = *(const uint4*)(xrow + at);
-          zv[e] = *(const uint4*)(ztile + row * 128 + at);
-        }
-        tmem_ld_wait();
-        if (q == 1) {
-          tc_fence_before();
-          mbar_arrive(bar(L::kYFree));
-        }
-        if (any_bad) {  // tokens up to this one whose x is not finite
-#pragma unroll 1
-          for (int j = 0; j <= row; ++j) {
-            if (!(bad[j >> 5] >> (j & 31) & 1)) continue;
-            const uint16_t* x = p.zx + (first + (size_t)c * kQ + j) * p.zx_stride + di + head * kSsmP + 32 * q;
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if ((x[e] & 0x7F80) == 0x7F80) y[e] = 0x7FC00000u;
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const uint32_t xw[4] = {xv[e].x, xv[e].y, xv[e].z, xv[e].w}, zw[4] = {zv[e].x, zv[e].y, zv[e].z, zv[e].w};
+          const uint32_t zw[4] = {zv[e].x, zv[e].y, zv[e].z, zv[e].w};
           uint32_t o[4];
 #pragma unroll
           for (int f = 0; f < 4; ++f) {
-            const float2 x2 = make_float2(__uint_as_float(xw[f] << 16), __uint_as_float(xw[f] & 0xFFFF0000u));
+            const int i = 32 * q + 8 * e + 2 * f;
             const float2 z2 = make_float2(__uint_as_float(zw[f] << 16), __uint_as_float(zw[f] & 0xFFFF0000u));
-            const float2 y2 = make_float2(__uint_as_float(y[8 * e + 2 * f]), __uint_as_float(y[8 * e + 2 * f + 1]));
             const float2 t = mul2(z2, make_float2(-1.44269504088896340736f, -1.44269504088896340736f));
             const float2 d = add2(make_float2(ex2(t.x), ex2(t.y)), make_float2(1.f, 1.f));
             const float2 g = mul2(z2, make_float2(rcp(d.x), rcp(d.y)));
-            const float2 r = mul2(fma2(skip2, x2, y2), g);
+            const float2 r = mul2(make_float2(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), g);
             o[f] = pack_bf16(r.x, r.y);
           }
-          *(uint4*)(ztile + row * 128 + (((q * 4 + e) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+          zv[e] = make_uint4(o[0], o[1], o[2], o[3]);
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) *(uint4*)(zrow + (((q * 4 + e) ^ (row & 7)) << 4)) = zv[e];
       }
       __syncwarp();
 #pragma unroll
@@ -546,7 +578,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
         if (r < left) *(uint4*)(p.out + (first + (size_t)c * kQ + r) * p.out_stride + head * kSsmP + at * 8) = v;
       }
       fence_proxy_async_smem();  // the next copies into this buffer come by the async proxy
-      mbar_arrive(bar(L::kEmpty + b));
+      mbar_arrive(bar(L::kCEmpty + b));
     }
   } else {
     regs_give<kRegsRest>();
@@ -558,7 +590,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
         for (int c = 0; c < chunks; ++c) {
           const uint32_t buf = sb + (c & 1) * L::kBuf, cm = buf + kBC, x = buf + 2 * kBC;
           const bool zero = c == 0 && !goes_on;
-          if (!wait(L::kFull + (c & 1), (c >> 1) & 1)) break;
+          if (!wait(L::kFull + (c & 1), (c >> 1) & 1) || !wait(L::kCFull + (c & 1), (c >> 1) & 1)) break;
           tc_fence_after();
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
@@ -607,36 +639,51 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
         if (lane == 0) {
           int c = 0;
           for (; c < chunks; ++c) {
-            const uint32_t buf = sb + (c & 1) * L::kBuf, fb = bar(L::kFull + (c & 1));
+            const uint32_t buf = sb + (c & 1) * L::kBuf, fb = bar(L::kFull + (c & 1)), fc = bar(L::kCFull + (c & 1));
+            const uint32_t parity = ((c >> 1) & 1) ^ 1;
             const int r = (int)first + c * kQ;
-            if (!wait(L::kEmpty + (c & 1), ((c >> 1) & 1) ^ 1)) break;
-            mbar_arrive_expect_tx(fb, L::kBuf);
+            if (!wait(L::kEmpty + (c & 1), parity)) break;
+            mbar_arrive_expect_tx(fb, kBC + 2 * kXT);
             tma_load_3d_plain(buf, &p.tm, 2 * di, 0, r, fb);
             tma_load_3d_plain(buf + kQ * 128, &p.tm, 2 * di + 64, 0, r, fb);
-            tma_load_3d_plain(buf + kBC, &p.tm, 2 * di + kSsmN, 0, r, fb);
-            tma_load_3d_plain(buf + kBC + kQ * 128, &p.tm, 2 * di + kSsmN + 64, 0, r, fb);
             tma_load_3d_plain(buf + 2 * kBC, &p.tm, di + h0 * kSsmP, 0, r, fb);
             tma_load_3d_plain(buf + 2 * kBC + kXT, &p.tm, di + (h0 + 1) * kSsmP, 0, r, fb);
+            if (!wait(L::kCEmpty + (c & 1), parity)) {
+              ++c;
+              break;
+            }
+            mbar_arrive_expect_tx(fc, kBC);
+            tma_load_3d_plain(buf + kBC, &p.tm, 2 * di + kSsmN, 0, r, fc);
+            tma_load_3d_plain(buf + kBC + kQ * 128, &p.tm, 2 * di + kSsmN + 64, 0, r, fc);
           }
           if (!ok)  // give-up: the copies in flight land before the shared memory is left
-            for (int i = max(0, c - 2); i < c; ++i)
+            for (int i = max(0, c - 2); i < c; ++i) {
               for (int n = 0; n < (1 << 20) && !mbar_try_wait(bar(L::kFull + (i & 1)), (i >> 1) & 1); ++n) {
               }
+              for (int n = 0; n < (1 << 12) && !mbar_try_wait(bar(L::kCFull + (i & 1)), (i >> 1) & 1); ++n) {
+              }
+            }
         }
       } else {
         for (int c = 0; c < chunks; ++c) {
           const uint32_t buf = sb + (c & 1) * L::kBuf;
           const size_t row0 = first + (size_t)c * kQ;
           const int n = min(kQ, len - c * kQ);
-          wait_warp(L::kEmpty + (c & 1), ((c >> 1) & 1) ^ 1);
+          const uint32_t parity = ((c >> 1) & 1) ^ 1;
+          wait_warp(L::kEmpty + (c & 1), parity);
           if (!ok) break;
           copy_tile<kSsmN>(buf, p.zx, p.zx_stride, 2 * di, row0, n);
-          copy_tile<kSsmN>(buf + kBC, p.zx, p.zx_stride, 2 * di + kSsmN, row0, n);
           copy_tile<kSsmP>(buf + 2 * kBC, p.zx, p.zx_stride, di + h0 * kSsmP, row0, n);
           copy_tile<kSsmP>(buf + 2 * kBC + kXT, p.zx, p.zx_stride, di + (h0 + 1) * kSsmP, row0, n);
           asm volatile("cp.async.wait_all;" ::: "memory");
           fence_proxy_async_smem();
           mbar_arrive(bar(L::kFull + (c & 1)));
+          wait_warp(L::kCEmpty + (c & 1), parity);
+          if (!ok) break;
+          copy_tile<kSsmN>(buf + kBC, p.zx, p.zx_stride, 2 * di + kSsmN, row0, n);
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          fence_proxy_async_smem();
+          mbar_arrive(bar(L::kCFull + (c & 1)));
         }
       }
       __syncwarp();
@@ -730,6 +777,11 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
           *(float4*)(saft + g * kQ + 4 * lane) = make_float4(after[g][0], after[g][1], after[g][2], after[g][3]);
           *(float4*)(sv + g * kQ + 4 * lane) = make_float4(lg2(dt[g][0]) - after[g][0], lg2(dt[g][1]) - after[g][1],
                                                            lg2(dt[g][2]) - after[g][2], lg2(dt[g][3]) - after[g][3]);
+          const float end = __shfl_sync(0xffffffffu, after[g][3], lane | 7);  // behind these 32 tokens
+          if (lane < 24)
+            *(float4*)(su + g * 96 + 4 * lane) =
+                make_float4(dt[g][0] * ex2(end - after[g][0]), dt[g][1] * ex2(end - after[g][1]),
+                            dt[g][2] * ex2(end - after[g][2]), dt[g][3] * ex2(end - after[g][3]));
           if (lane == 0) slast[g] = last[g];
         }
         __syncwarp();
