@@ -296,32 +296,33 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
       if (!zero) {
         const float dec = ex2(-slast[hh]);
         uint8_t* hrow = smem + L::kH + hh * kXT + h * (64 * 128) + pp * 128;
-        uint32_t v[64];
-        if (c == 0) {
-          const float4* src = (const float4*)(p.state_in + state_at);
+#pragma unroll 1
+        for (int q = 0; q < 2; ++q) {
+          uint32_t v[32];
+          if (c == 0) {
+            const float4* src = (const float4*)(p.state_in + state_at + 32 * q);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float4 f = src[e];
-            v[4 * e] = __float_as_uint(f.x), v[4 * e + 1] = __float_as_uint(f.y);
-            v[4 * e + 2] = __float_as_uint(f.z), v[4 * e + 3] = __float_as_uint(f.w);
+            for (int e = 0; e < 8; ++e) {
+              const float4 f = src[e];
+              v[4 * e] = __float_as_uint(f.x), v[4 * e + 1] = __float_as_uint(f.y);
+              v[4 * e + 2] = __float_as_uint(f.z), v[4 * e + 3] = __float_as_uint(f.w);
+            }
+          } else {
+            tmem_ld32(tmem + kTState + lanes + h * 64 + 32 * q, v);
+            tmem_ld_wait();
           }
-        } else {
-          tmem_ld32(tmem + kTState + lanes + h * 64, v);
-          tmem_ld32(tmem + kTState + lanes + h * 64 + 32, v + 32);
-          tmem_ld_wait();
-        }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          uint4 w;
-          w.x = pack_bf16(__uint_as_float(v[8 * e]), __uint_as_float(v[8 * e + 1]));
-          w.y = pack_bf16(__uint_as_float(v[8 * e + 2]), __uint_as_float(v[8 * e + 3]));
-          w.z = pack_bf16(__uint_as_float(v[8 * e + 4]), __uint_as_float(v[8 * e + 5]));
-          w.w = pack_bf16(__uint_as_float(v[8 * e + 6]), __uint_as_float(v[8 * e + 7]));
-          *(uint4*)(hrow + ((e ^ (pp & 7)) << 4)) = w;
+          for (int e = 0; e < 4; ++e) {
+            uint4 w;
+            w.x = pack_bf16(__uint_as_float(v[8 * e]), __uint_as_float(v[8 * e + 1]));
+            w.y = pack_bf16(__uint_as_float(v[8 * e + 2]), __uint_as_float(v[8 * e + 3]));
+            w.z = pack_bf16(__uint_as_float(v[8 * e + 4]), __uint_as_float(v[8 * e + 5]));
+            w.w = pack_bf16(__uint_as_float(v[8 * e + 6]), __uint_as_float(v[8 * e + 7]));
+            *(uint4*)(hrow + (((4 * q + e) ^ (pp & 7)) << 4)) = w;
+          }
+          scale_regs<32>(v, dec);
+          tmem_st32(tmem + kTState + lanes + h * 64 + 32 * q, v);
         }
-        scale_regs<64>(v, dec);
-        tmem_st32(tmem + kTState + lanes + h * 64, v);
-        tmem_st32(tmem + kTState + lanes + h * 64 + 32, v + 32);
         tmem_st_wait();
         fence_proxy_async_smem();
       }
@@ -330,75 +331,82 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
       // ---- M, over G once both heads have read G
       wait_warp(L::kG, c & 1);
       tc_fence_after();
-      uint32_t m[64];
       const float after = saft[h * kQ + row];  // c_j - c_i = after_i - after_j
+      // 32 tokens at a time, from the diagonal down: m[16 t ..] is block quad - t
+      uint32_t m[64];
+      {
+        // on the diagonal; D x_i is added to y_i as D on the diagonal
+        uint32_t g[32];
+        tmem_ld32(tmem + kTG + lanes + 32 * quad, g);
+        const float2 ai = make_float2(after, after);
+        const float4* vj = (const float4*)(sv + h * kQ + 32 * quad);
+        tmem_ld_wait();
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (q < quad) {
-          // below the diagonal: the decay from token j's end of 32 tokens to i
-          // is a factor of the row, that from j to there is in u_j
-          uint32_t g[32];
-          tmem_ld32(tmem + kTG + lanes + 32 * q, g);
-          const float r = ex2(after - saft[h * kQ + 32 * q + 31]);
-          const float2 r2 = make_float2(r, r);
-          const float4* uj = (const float4*)(su + h * 96 + 32 * q);
-          tmem_ld_wait();
+        for (int e = 0; e < 8; ++e) {
+          const float4 v4 = vj[e];
+          const float2 t0 = add2(make_float2(v4.x, v4.y), ai), t1 = add2(make_float2(v4.z, v4.w), ai);
+          const float2 m0 = mul2(make_float2(__uint_as_float(g[4 * e]), __uint_as_float(g[4 * e + 1])),
+                                 make_float2(ex2(t0.x), ex2(t0.y)));
+          const float2 m1 = mul2(make_float2(__uint_as_float(g[4 * e + 2]), __uint_as_float(g[4 * e + 3])),
+                                 make_float2(ex2(t1.x), ex2(t1.y)));
+          float f[4] = {m0.x, m0.y, m1.x, m1.y};
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float4 u4 = uj[e];
-            const float2 m0 = mul2(mul2(make_float2(__uint_as_float(g[4 * e]), __uint_as_float(g[4 * e + 1])), r2),
-                                   make_float2(u4.x, u4.y));
-            const float2 m1 = mul2(mul2(make_float2(__uint_as_float(g[4 * e + 2]), __uint_as_float(g[4 * e + 3])), r2),
-                                   make_float2(u4.z, u4.w));
-            m[16 * q + 2 * e] = pack_bf16(m0.x, m0.y);
-            m[16 * q + 2 * e + 1] = pack_bf16(m1.x, m1.y);
+          for (int k = 0; k < 4; ++k) {
+            if (4 * e + k > lane) f[k] = 0.f;
+            if (4 * e + k == lane) f[k] += skip;
           }
-        } else if (q == quad) {
-          // on it: D x_i is added to y_i as D on the diagonal
-          uint32_t g[32];
-          tmem_ld32(tmem + kTG + lanes + 32 * q, g);
-          const float2 ai = make_float2(after, after);
-          const float4* vj = (const float4*)(sv + h * kQ + 32 * q);
-          tmem_ld_wait();
+          m[2 * e] = pack_bf16(f[0], f[1]);
+          m[2 * e + 1] = pack_bf16(f[2], f[3]);
+        }
+      }
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float4 v4 = vj[e];
-            const float2 t0 = add2(make_float2(v4.x, v4.y), ai), t1 = add2(make_float2(v4.z, v4.w), ai);
-            const float2 m0 = mul2(make_float2(__uint_as_float(g[4 * e]), __uint_as_float(g[4 * e + 1])),
-                                   make_float2(ex2(t0.x), ex2(t0.y)));
-            const float2 m1 = mul2(make_float2(__uint_as_float(g[4 * e + 2]), __uint_as_float(g[4 * e + 3])),
-                                   make_float2(ex2(t1.x), ex2(t1.y)));
-            float f[4] = {m0.x, m0.y, m1.x, m1.y};
+      for (int t = 1; t < 4; ++t) {
+        if (t > quad) continue;
+        // below: the decay from the end of token j's block to i is a factor
+        // of the row, that from j to there is in u_j
+        const int q = quad - t;
+        uint32_t g[32];
+        tmem_ld32(tmem + kTG + lanes + 32 * q, g);
+        const float r = ex2(after - saft[h * kQ + 32 * q + 31]);
+        const float2 r2 = make_float2(r, r);
+        const float4* uj = (const float4*)(su + h * 96 + 32 * q);
+        tmem_ld_wait();
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              if (4 * e + k > lane) f[k] = 0.f;
-              if (4 * e + k == lane) f[k] += skip;
-            }
-            m[16 * q + 2 * e] = pack_bf16(f[0], f[1]);
-            m[16 * q + 2 * e + 1] = pack_bf16(f[2], f[3]);
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) m[16 * q + e] = 0;
+        for (int e = 0; e < 8; ++e) {
+          const float4 u4 = uj[e];
+          const float2 m0 = mul2(mul2(make_float2(__uint_as_float(g[4 * e]), __uint_as_float(g[4 * e + 1])), r2),
+                                 make_float2(u4.x, u4.y));
+          const float2 m1 = mul2(mul2(make_float2(__uint_as_float(g[4 * e + 2]), __uint_as_float(g[4 * e + 3])), r2),
+                                 make_float2(u4.z, u4.w));
+          m[16 * t + 2 * e] = pack_bf16(m0.x, m0.y);
+          m[16 * t + 2 * e + 1] = pack_bf16(m1.x, m1.y);
         }
       }
       tc_fence_before();
-      bar_sync(1, 256);
+      bar_sync(1, 256);  // both heads have read G
       tc_fence_after();
-      tmem_st32(tmem + kTG + h * 64 + lanes, m);
-      tmem_st32(tmem + kTG + h * 64 + lanes + 32, m + 32);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        if (t <= quad) {
+          tmem_st16(tmem + kTG + h * 64 + lanes + 16 * (quad - t), m + 16 * t);
+        } else {  // above the diagonal
+          uint32_t none[16] = {};
+          tmem_st16(tmem + kTG + h * 64 + lanes + 16 * t, none);
+        }
+      }
       // ---- C H^T, scaled in place: M X is added to it
       wait_warp(L::kY2, c & 1);
       tc_fence_after();
       if (!zero) {
-        uint32_t v[64];
-        tmem_ld32(tmem + kTY + h * 64 + lanes, v);
-        tmem_ld32(tmem + kTY + h * 64 + lanes + 32, v + 32);
         const float ei = ex2(after - slast[h]);
-        tmem_ld_wait();
-        scale_regs<64>(v, ei);
-        tmem_st32(tmem + kTY + h * 64 + lanes, v);
-        tmem_st32(tmem + kTY + h * 64 + lanes + 32, v + 32);
+#pragma unroll 1
+        for (int q = 0; q < 2; ++q) {
+          uint32_t v[32];
+          tmem_ld32(tmem + kTY + h * 64 + lanes + 32 * q, v);
+          tmem_ld_wait();
+          scale_regs<32>(v, ei);
+          tmem_st32(tmem + kTY + h * 64 + lanes + 32 * q, v);
+        }
       }
       tmem_st_wait();
       tc_fence_before();
@@ -407,7 +415,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
     // ---- the state after the last token
     wait_warp(L::kS, (chunks - 1) & 1);
     tc_fence_after();
-#pragma unroll
+#pragma unroll 1
     for (int q = 0; q < 2; ++q) {
       uint32_t v[32];
       tmem_ld32(tmem + kTState + lanes + h * 64 + q * 32, v);
@@ -429,12 +437,14 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
         uint8_t* buf = smem + b * L::kBuf;
         // ---- this token's x and B.  Behind the sequence's end lie other rows:
         // theirs become zero.  An x that is not finite would reach earlier
-        // tokens as 0 * NaN: it becomes zero here and is put back below.
+        // tokens as 0 * NaN in M X: it is noted here, becomes zero once the
+        // state's weights have been made of it, and is put back at the output.
         wait_warp(L::kFull + b, (k >> 1) & 1);
         uint8_t* xrow = buf + 2 * kBC + h * kXT + row * 128;
+        bool odd = false;
         if (row >= left) {
           uint8_t* brow = buf + h * (kQ * 128) + row * 128;
-#pragma unroll
+#pragma unroll 4
           for (int e = 0; e < 8; ++e) {
             *(uint4*)(xrow + (e << 4)) = make_uint4(0, 0, 0, 0);
             *(uint4*)(brow + (e << 4)) = make_uint4(0, 0, 0, 0);
@@ -450,38 +460,24 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
             asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[0]) : "r"(x.z), "r"(0));
             asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[1]) : "r"(x.w), "r"(0));
           }
-          if ((acc[0] | acc[1]) & 0x7fff7fffu) {
-#pragma unroll 1
-            for (int e = 0; e < 64; ++e) {
-              uint16_t* x = (uint16_t*)xrow + e;
-              if ((*x & 0x7F80) == 0x7F80) *x = 0;
-            }
-            atomicOr(&sbad[k & 3], 1u << (h * 4 + quad));
-            fence_proxy_async_smem();
-          }
+          odd = ((acc[0] | acc[1]) & 0x7fff7fffu) != 0;
+          if (odd) atomicOr(&sbad[k & 3], 1u << (h * 4 + quad));
         }
-        bar_sync(4, 256);  // x and bad are complete; every thread here is done with chunk k - 2
+        bar_sync(4, 256);  // x and its flags are complete; every thread here is done with chunk k - 2
         // cleared two chunks ahead: nobody sets these before the next barrier
         if ((threadIdx.x & 255) == 0) sbad[(k + 2) & 3] = 0;
-        const uint32_t bad = sbad[k & 3] >> (hh * 4 + h * 2);  // of the tokens below
         // ---- (w X)^T: row (hh, pp), tokens 64 h .. 64 h + 63
         wait_warp(L::kScan, k & 1);
         if (k > 0) wait_warp(L::kS, (k - 1) & 1);
         tc_fence_after();
         const uint8_t* xt = buf + 2 * kBC + hh * kXT + (pp & 7) * 2;
-#pragma unroll
+#pragma unroll 1
         for (int q = 0; q < 2; ++q) {
           const int j0 = h * 64 + 32 * q;
           float v[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e)  // j0 is a multiple of 8
             v[e] = bf(*(const uint16_t*)(xt + (j0 + e) * 128 + (((pp >> 3) ^ (e & 7)) << 4)));
-          if (bad >> q & 1) {
-            const uint16_t* x = p.zx + (first + (size_t)k * kQ + j0) * p.zx_stride + di + (h0 + hh) * kSsmP + pp;
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (j0 + e < left) v[e] = bf(x[e * p.zx_stride]);
-          }
           // w_j: u_j times the decay from its 32 tokens' end on (none after the last 32)
           if (q == 0 || h == 0) {
             const float tail = ex2(-saft[hh * kQ + j0 + 31]);
@@ -517,6 +513,17 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
           tmem_st16(tmem + kTWx + 64 + lanes + h * 32 + q * 16, lo);
         }
         tmem_st_wait();
+        if (sbad[k & 3]) {  // seen by every thread or none
+          bar_sync(4, 256);
+          if (odd) {
+#pragma unroll 1
+            for (int e = 0; e < 64; ++e) {
+              uint16_t* x = (uint16_t*)xrow + e;
+              if ((*x & 0x7F80) == 0x7F80) *x = 0;
+            }
+            fence_proxy_async_smem();
+          }
+        }
         tc_fence_before();
         mbar_arrive(bar(L::kWx));
       }
@@ -529,35 +536,22 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
       wait_warp(L::kZFull, c & 1);
       wait_warp(L::kYFull + h, c & 1);
       tc_fence_after();
-      uint32_t y[64];
-      tmem_ld32(tmem + kTY + h * 64 + lanes, y);
-      tmem_ld32(tmem + kTY + h * 64 + lanes + 32, y + 32);
-      tmem_ld_wait();
-      tc_fence_before();
-      mbar_arrive(bar(L::kYFree));
-      if (any_bad) {  // tokens up to this one whose x is not finite
-#pragma unroll 1
-        for (int j = 0; j <= row && j < left; ++j) {
-          if (!(any_bad >> (j >> 5) & 1)) continue;
-          const uint16_t* x = p.zx + (first + (size_t)c * kQ + j) * p.zx_stride + di + head * kSsmP;
-#pragma unroll
-          for (int e = 0; e < 64; ++e)
-            if ((x[e] & 0x7F80) == 0x7F80) y[e] = 0x7FC00000u;
-        }
-      }
       uint8_t* zrow = ztile + row * 128;
-#pragma unroll
+#pragma unroll 1
       for (int q = 0; q < 2; ++q) {
+        uint32_t y[32];
+        tmem_ld32(tmem + kTY + h * 64 + lanes + 32 * q, y);
         uint4 zv[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) zv[e] = *(const uint4*)(zrow + (((q * 4 + e) ^ (row & 7)) << 4));
+        tmem_ld_wait();
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const uint32_t zw[4] = {zv[e].x, zv[e].y, zv[e].z, zv[e].w};
           uint32_t o[4];
 #pragma unroll
           for (int f = 0; f < 4; ++f) {
-            const int i = 32 * q + 8 * e + 2 * f;
+            const int i = 8 * e + 2 * f;
             const float2 z2 = make_float2(__uint_as_float(zw[f] << 16), __uint_as_float(zw[f] & 0xFFFF0000u));
             const float2 t = mul2(z2, make_float2(-1.44269504088896340736f, -1.44269504088896340736f));
             const float2 d = add2(make_float2(ex2(t.x), ex2(t.y)), make_float2(1.f, 1.f));
@@ -565,10 +559,20 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
             const float2 r = mul2(make_float2(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), g);
             o[f] = pack_bf16(r.x, r.y);
           }
-          zv[e] = make_uint4(o[0], o[1], o[2], o[3]);
+          *(uint4*)(zrow + (((q * 4 + e) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
         }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) *(uint4*)(zrow + (((q * 4 + e) ^ (row & 7)) << 4)) = zv[e];
+      }
+      tc_fence_before();
+      mbar_arrive(bar(L::kYFree));
+      if (any_bad) {  // tokens up to this one whose x is not finite
+#pragma unroll 1
+        for (int j = 0; j <= row && j < left; ++j) {
+          if (!(any_bad >> (j >> 5) & 1)) continue;
+          const uint16_t* x = p.zx + (first + (size_t)c * kQ + j) * p.zx_stride + di + head * kSsmP;
+#pragma unroll 1
+          for (int e = 0; e < 64; ++e)
+            if ((x[e] & 0x7F80) == 0x7F80) *(uint16_t*)(zrow + (((e >> 3) ^ (row & 7)) << 4) + (e & 7) * 2) = 0x7FC0;
+        }
       }
       __syncwarp();
 #pragma unroll
@@ -592,35 +596,41 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
           const bool zero = c == 0 && !goes_on;
           if (!wait(L::kFull + (c & 1), (c >> 1) & 1) || !wait(L::kCFull + (c & 1), (c >> 1) & 1)) break;
           tc_fence_after();
+#pragma unroll 1
+          for (int k = 0; k < 2; ++k) {
+            const uint64_t a = sdesc_sw128(cm + k * (kQ * 128)), b = sdesc_sw128(buf + k * (kQ * 128));
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint32_t o = (e / 4) * (kQ * 128) + (e % 4) * 32;
-            mma_ss(tmem + kTG, sdesc_sw128(cm + o), sdesc_sw128(buf + o), id_g, e > 0);
+            for (int e = 0; e < 4; ++e) mma_ss(tmem + kTG, a + 2 * e, b + 2 * e, id_g, k + e > 0);
           }
           tc_commit(bar(L::kG));
           if (!wait(L::kHFull, c & 1) || !wait(L::kWx, c & 1)) break;
           tc_fence_after();
+#pragma unroll 1
+          for (int k = 0; k < 4; ++k) {  // the high parts, then the remainders
+            const uint64_t b = sdesc_mn_sw128(buf + (k & 1) * (4 * 2048), kQ * 128);
 #pragma unroll
-          for (int e = 0; e < 16; ++e)  // the high parts, then the remainders
-            mma_ts(tmem + kTState, tmem + kTWx + 8 * e, sdesc_mn_sw128(buf + (e % 8) * 2048, kQ * 128), id_s, !zero || e > 0);
+            for (int e = 0; e < 4; ++e)
+              mma_ts(tmem + kTState, tmem + kTWx + 32 * k + 8 * e, b + (2048 >> 4) * e, id_s, !zero || k + e > 0);
+          }
           tc_commit(bar(L::kS));
           if (c > 0 && !wait(L::kYFree, (c - 1) & 1)) break;
           tc_fence_after();
 #pragma unroll 1
-          for (int h = 0; h < 2 && !zero; ++h)
+          for (int k = 0; k < 4 && !zero; ++k) {  // half of n of a head
+            const uint64_t a = sdesc_sw128(cm + (k & 1) * (kQ * 128)),
+                           b = sdesc_sw128(sb + L::kH + (k >> 1) * kXT + (k & 1) * (64 * 128));
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              mma_ss(tmem + kTY + h * 64, sdesc_sw128(cm + (e / 4) * (kQ * 128) + (e % 4) * 32),
-                     sdesc_sw128(sb + L::kH + h * kXT + (e / 4) * (64 * 128) + (e % 4) * 32), id_y2, e > 0);
+            for (int e = 0; e < 4; ++e) mma_ss(tmem + kTY + (k >> 1) * 64, a + 2 * e, b + 2 * e, id_y2, (k & 1) + e > 0);
+          }
           tc_commit(bar(L::kY2));
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
             if (!wait(L::kMFull + h, c & 1)) break;
             tc_fence_after();
+            const uint64_t b = sdesc_mn_sw128(x + h * kXT, kQ * 128);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              mma_ts(tmem + kTY + h * 64, tmem + kTG + h * 64 + 8 * e, sdesc_mn_sw128(x + h * kXT + e * 2048, kQ * 128), id_y,
-                     !zero || e > 0);
+              mma_ts(tmem + kTY + h * 64, tmem + kTG + h * 64 + 8 * e, b + (2048 >> 4) * e, id_y, !zero || e > 0);
             tc_commit(bar(L::kYFull + h));
           }
           if (!ok) break;
