@@ -177,9 +177,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __gr
   // other waits, and every warp leaves its loop.  wait: one thread;
   // wait_warp: a whole warp, which stays together.
   bool ok = true;
-  auto wait = [&](int b, uint32_t parity) { return ok = wait_or_flag(bar(b), parity, p.sink, kErrTimeout); };
+  auto wait = [&](int b, uint32_t parity) { return ok = wait_bar(bar(b), parity, p.sink); };
   auto wait_warp = [&](int b, uint32_t parity) {
-    return ok = __all_sync(0xffffffffu, wait_or_flag(bar(b), parity, p.sink, kErrTimeout));
+    return ok = __all_sync(0xffffffffu, wait_bar(bar(b), parity, p.sink));
   };
 
   if (warp < 8) {
@@ -560,7 +560,7 @@ extern "C" int wave_prompt_attention(wave_t* h, int n_seq, const int32_t* cu_seq
   p.v_stride = v_stride;
   p.out_stride = out_stride;
   p.scale2 = scale * 1.44269504088896340736f;
-  p.sink = {h->ws.err, h->err_host_dev, h->timeout_ns};
+  p.sink = make_sink(h->ws.err, h->err_host_dev, h->timeout_ns);
   cudaStream_t st = (cudaStream_t)stream;
   h->last_stream = st;
   const int grid = h->pl.grid;

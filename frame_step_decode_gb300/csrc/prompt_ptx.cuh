@@ -64,6 +64,20 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld16_nowait(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // MN-major operand: rows of 128 bytes along M/N (64 elements), one row per k,
@@ -123,16 +137,34 @@ __device__ __forceinline__ void regs_give() {
 }
 
 // What a kernel with bounded waits reports to: the handle's error word and
-// its mirror on the host (see wave_status).
+// its mirror on the host (see wave_status); and how often a wait is tried.
 struct ErrSink {
   int* err;
   int* err_out;
-  long long timeout_ns;
+  int tries;
 };
-__device__ __forceinline__ bool wait_or_flag(uint32_t bar, uint32_t parity, const ErrSink& e, int bits) {
-  if (mbar_wait(bar, parity, e.timeout_ns, e.err)) return true;
-  const int now = atomicOr(e.err, bits) | bits;
-  *(volatile int*)e.err_out = now;
+constexpr uint32_t kTryNs = 1000;  // how long one try may sleep
+inline ErrSink make_sink(int* err, int* err_out, long long timeout_ns) {
+  const long long n = timeout_ns / kTryNs + 1;
+  return {err, err_out, n > 0x7fffffff ? 0x7fffffff : (int)n};
+}
+// Wait for the phase with the given parity; false, and the timeout noted,
+// after about timeout_ns.  Kept short: it is inlined at every wait, and longer
+// waits made the kernels' code outgrow the instruction cache.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, const ErrSink& e) {
+#pragma unroll 1
+  for (int n = 0; n < e.tries; ++n) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(kTryNs)
+        : "memory");
+    if (ok) return true;
+  }
+  *(volatile int*)e.err_out = atomicOr(e.err, 1) | 1;  // kErrTimeout
   return false;
 }
 

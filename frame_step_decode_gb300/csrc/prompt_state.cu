@@ -171,7 +171,7 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
 template <int kCols>
 __device__ __forceinline__ void copy_tile(uint32_t dst, const uint16_t* zx, long long stride, int col, size_t row0, int n) {
   constexpr int kPer = kCols * 2 / 8;  // pieces of a row
-#pragma unroll 8
+#pragma unroll 4
   for (int q = threadIdx.x & 31; q < kQ * kPer; q += 32) {
     const int r = q / kPer, b = (q % kPer) * 8, blk = b >> 7, c = (b >> 4) & 7;
     copy_async<8>(dst + blk * (kQ * 128) + r * 128 + ((c ^ (r & 7)) << 4) + (b & 15),
@@ -205,13 +205,21 @@ __device__ __forceinline__ void scale_regs(uint32_t* v, float f) {
   }
 }
 
-// softplus and the log-decay of a token (in powers of two, positive).  2^-160
-// is zero in fp32: a larger step changes nothing, and the cap bounds the
-// rounding of the sums.
-__device__ __forceinline__ float step_of(float raw, float rate, float& lam) {
-  const float dt = raw > 0.f ? raw + log1pf(expf(-raw)) : log1pf(expf(raw));
-  lam = fminf(rate * dt, 160.f);
-  return dt;
+// log(1 + e^raw) = max(raw, 0) + log1p(t), t = e^-|raw|, by the series
+// log1p(t) = 2 (s + s^3/3 + s^5/5 + ...), s = t / (2 + t) <= 1/3: terms to
+// s^13 leave 2^-27.  Short and without branches: it runs eight times per lane
+// and chunk, and the library's expf and log1pf together did not fit the
+// instruction cache beside the other warps' code.
+__device__ __forceinline__ float softplus(float raw) {
+  const float t = ex2(-1.44269504088896340736f * fabsf(raw));
+  const float s = __fdividef(t, 2.f + t), s2 = s * s;
+  float q = fmaf(s2, 2.f / 13.f, 2.f / 11.f);
+  q = fmaf(s2, q, 2.f / 9.f);
+  q = fmaf(s2, q, 2.f / 7.f);
+  q = fmaf(s2, q, 2.f / 5.f);
+  q = fmaf(s2, q, 2.f / 3.f);
+  q = fmaf(s2, q, 2.f);
+  return fmaxf(raw, 0.f) + s * q;
 }
 
 __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_constant__ StateParams p) {
@@ -269,9 +277,9 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
   // undefined; the other warps leave their loops.
   bool ok = true;
   auto wait_warp = [&](int b, uint32_t parity) {
-    if (ok) ok = __all_sync(0xffffffffu, wait_or_flag(bar(b), parity, p.sink, kErrTimeout));
+    if (ok) ok = __all_sync(0xffffffffu, wait_bar(bar(b), parity, p.sink));
   };
-  auto wait = [&](int b, uint32_t parity) { return ok = wait_or_flag(bar(b), parity, p.sink, kErrTimeout); };
+  auto wait = [&](int b, uint32_t parity) { return ok = wait_bar(bar(b), parity, p.sink); };
   const int h = (warp >> 2) & 1, quad = warp & 3, row = quad * 32 + lane;  // a thread per token of head h0 + h
   const uint32_t lanes = (uint32_t)(quad * 32) << 16;
   const int hh = row >> 6, pp = row & 63;  // for the state: row (head hh, p), half h of the columns or tokens
@@ -297,31 +305,31 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
         const float dec = ex2(-slast[hh]);
         uint8_t* hrow = smem + L::kH + hh * kXT + h * (64 * 128) + pp * 128;
 #pragma unroll 1
-        for (int q = 0; q < 2; ++q) {
-          uint32_t v[32];
+        for (int q = 0; q < 4; ++q) {
+          uint32_t v[16];
           if (c == 0) {
-            const float4* src = (const float4*)(p.state_in + state_at + 32 * q);
+            const float4* src = (const float4*)(p.state_in + state_at + 16 * q);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
+            for (int e = 0; e < 4; ++e) {
               const float4 f = src[e];
               v[4 * e] = __float_as_uint(f.x), v[4 * e + 1] = __float_as_uint(f.y);
               v[4 * e + 2] = __float_as_uint(f.z), v[4 * e + 3] = __float_as_uint(f.w);
             }
           } else {
-            tmem_ld32(tmem + kTState + lanes + h * 64 + 32 * q, v);
+            tmem_ld16_nowait(tmem + kTState + lanes + h * 64 + 16 * q, v);
             tmem_ld_wait();
           }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
+          for (int e = 0; e < 2; ++e) {
             uint4 w;
             w.x = pack_bf16(__uint_as_float(v[8 * e]), __uint_as_float(v[8 * e + 1]));
             w.y = pack_bf16(__uint_as_float(v[8 * e + 2]), __uint_as_float(v[8 * e + 3]));
             w.z = pack_bf16(__uint_as_float(v[8 * e + 4]), __uint_as_float(v[8 * e + 5]));
             w.w = pack_bf16(__uint_as_float(v[8 * e + 6]), __uint_as_float(v[8 * e + 7]));
-            *(uint4*)(hrow + (((4 * q + e) ^ (pp & 7)) << 4)) = w;
+            *(uint4*)(hrow + (((2 * q + e) ^ (pp & 7)) << 4)) = w;
           }
-          scale_regs<32>(v, dec);
-          tmem_st32(tmem + kTState + lanes + h * 64 + 32 * q, v);
+          scale_regs<16>(v, dec);
+          tmem_st16(tmem + kTState + lanes + h * 64 + 16 * q, v);
         }
         tmem_st_wait();
         fence_proxy_async_smem();
@@ -472,45 +480,34 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
         tc_fence_after();
         const uint8_t* xt = buf + 2 * kBC + hh * kXT + (pp & 7) * 2;
 #pragma unroll 1
-        for (int q = 0; q < 2; ++q) {
-          const int j0 = h * 64 + 32 * q;
-          float v[32];
+        for (int q = 0; q < 4; ++q) {
+          const int j0 = h * 64 + 16 * q;
+          float v[16];
 #pragma unroll
-          for (int e = 0; e < 32; ++e)  // j0 is a multiple of 8
+          for (int e = 0; e < 16; ++e)  // j0 is a multiple of 8
             v[e] = bf(*(const uint16_t*)(xt + (j0 + e) * 128 + (((pp >> 3) ^ (e & 7)) << 4)));
-          // w_j: u_j times the decay from its 32 tokens' end on (none after the last 32)
-          if (q == 0 || h == 0) {
-            const float tail = ex2(-saft[hh * kQ + j0 + 31]);
-            const float4* uj = (const float4*)(su + hh * 96 + j0);
+          // w_j: u_j times the decay from its 32 tokens' end on; the last 32 have v_j only
+          const bool tail_block = j0 >= 96;
+          const float tail = tail_block ? 1.f : ex2(-saft[hh * kQ + (j0 | 31)]);
+          const float4* uj = (const float4*)((tail_block ? sv + hh * kQ : su + hh * 96) + j0);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float4 u4 = uj[e];
-              const float2 w0 = mul2(make_float2(u4.x, u4.y), make_float2(tail, tail));
-              const float2 w1 = mul2(make_float2(u4.z, u4.w), make_float2(tail, tail));
-              const float2 r0 = mul2(make_float2(v[4 * e], v[4 * e + 1]), w0);
-              const float2 r1 = mul2(make_float2(v[4 * e + 2], v[4 * e + 3]), w1);
-              v[4 * e] = r0.x, v[4 * e + 1] = r0.y, v[4 * e + 2] = r1.x, v[4 * e + 3] = r1.y;
-            }
-          } else {
-            const float4* vj = (const float4*)(sv + hh * kQ + j0);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float4 v4 = vj[e];
-              const float2 r0 = mul2(make_float2(v[4 * e], v[4 * e + 1]), make_float2(ex2(v4.x), ex2(v4.y)));
-              const float2 r1 = mul2(make_float2(v[4 * e + 2], v[4 * e + 3]), make_float2(ex2(v4.z), ex2(v4.w)));
-              v[4 * e] = r0.x, v[4 * e + 1] = r0.y, v[4 * e + 2] = r1.x, v[4 * e + 3] = r1.y;
-            }
+          for (int e = 0; e < 4; ++e) {
+            float4 u4 = uj[e];
+            if (tail_block) u4 = make_float4(ex2(u4.x), ex2(u4.y), ex2(u4.z), ex2(u4.w));
+            const float2 r0 = mul2(make_float2(v[4 * e], v[4 * e + 1]), mul2(make_float2(u4.x, u4.y), make_float2(tail, tail)));
+            const float2 r1 = mul2(make_float2(v[4 * e + 2], v[4 * e + 3]), mul2(make_float2(u4.z, u4.w), make_float2(tail, tail)));
+            v[4 * e] = r0.x, v[4 * e + 1] = r0.y, v[4 * e + 2] = r1.x, v[4 * e + 3] = r1.y;
           }
-          uint32_t hi[16], lo[16];
+          uint32_t hi[8], lo[8];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
+          for (int e = 0; e < 8; ++e) {
             hi[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
             const float2 r = sub2(make_float2(v[2 * e], v[2 * e + 1]),
                                   make_float2(__uint_as_float(hi[e] << 16), __uint_as_float(hi[e] & 0xFFFF0000u)));
             lo[e] = pack_bf16(r.x, r.y);
           }
-          tmem_st16(tmem + kTWx + lanes + h * 32 + q * 16, hi);
-          tmem_st16(tmem + kTWx + 64 + lanes + h * 32 + q * 16, lo);
+          tmem_st8(tmem + kTWx + lanes + h * 32 + q * 8, hi);
+          tmem_st8(tmem + kTWx + 64 + lanes + h * 32 + q * 8, lo);
         }
         tmem_st_wait();
         if (sbad[k & 3]) {  // seen by every thread or none
@@ -538,15 +535,15 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
       tc_fence_after();
       uint8_t* zrow = ztile + row * 128;
 #pragma unroll 1
-      for (int q = 0; q < 2; ++q) {
-        uint32_t y[32];
-        tmem_ld32(tmem + kTY + h * 64 + lanes + 32 * q, y);
-        uint4 zv[4];
+      for (int q = 0; q < 4; ++q) {
+        uint32_t y[16];
+        tmem_ld16_nowait(tmem + kTY + h * 64 + lanes + 16 * q, y);
+        uint4 zv[2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) zv[e] = *(const uint4*)(zrow + (((q * 4 + e) ^ (row & 7)) << 4));
+        for (int e = 0; e < 2; ++e) zv[e] = *(const uint4*)(zrow + (((q * 2 + e) ^ (row & 7)) << 4));
         tmem_ld_wait();
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < 2; ++e) {
           const uint32_t zw[4] = {zv[e].x, zv[e].y, zv[e].z, zv[e].w};
           uint32_t o[4];
 #pragma unroll
@@ -559,7 +556,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
             const float2 r = mul2(make_float2(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), g);
             o[f] = pack_bf16(r.x, r.y);
           }
-          *(uint4*)(zrow + (((q * 4 + e) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+          *(uint4*)(zrow + (((q * 2 + e) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
         }
       }
       tc_fence_before();
@@ -575,11 +572,15 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
         }
       }
       __syncwarp();
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const int r = quad * 32 + q * 4 + (lane >> 3), at = lane & 7;
-        const uint4 v = *(const uint4*)(ztile + r * 128 + ((at ^ (r & 7)) << 4));
-        if (r < left) *(uint4*)(p.out + (first + (size_t)c * kQ + r) * p.out_stride + head * kSsmP + at * 8) = v;
+      {
+        const int r0 = quad * 32 + (lane >> 3), at = lane & 7;  // four rows at a time
+        uint16_t* dst = p.out + (first + (size_t)c * kQ + r0) * p.out_stride + head * kSsmP + at * 8;
+#pragma unroll 4
+        for (int q = 0; q < 8; ++q, dst += 4 * p.out_stride) {
+          const int r = r0 + 4 * q;
+          const uint4 v = *(const uint4*)(ztile + r * 128 + ((at ^ (r & 7)) << 4));
+          if (r < left) *(uint4*)dst = v;
+        }
       }
       fence_proxy_async_smem();  // the next copies into this buffer come by the async proxy
       mbar_arrive(bar(L::kCEmpty + b));
@@ -757,8 +758,11 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
           float lam[4];
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
-            dt[g][t] = step_of((g ? __uint_as_float(raw[t] & 0xFFFF0000u) : __uint_as_float(raw[t] << 16)) + bias[g], rate[g], lam[t]);
-            if (4 * lane + t >= left) dt[g][t] = lam[t] = 0.f;
+            dt[g][t] = softplus((g ? __uint_as_float(raw[t] & 0xFFFF0000u) : __uint_as_float(raw[t] << 16)) + bias[g]);
+            if (4 * lane + t >= left) dt[g][t] = 0.f;
+            // the token's decay in powers of two; 2^-160 is zero in fp32: a larger
+            // step changes nothing, and the cap bounds the rounding of the sums
+            lam[t] = fminf(rate[g] * dt[g][t], 160.f);
           }
           float down = (lam[0] + lam[1]) + (lam[2] + lam[3]);  // this lane's and the later ones'
 #pragma unroll
@@ -839,7 +843,7 @@ extern "C" int wave_hybrid_prompt_state(wave_t* h, int layer, const void* weight
   p.out_stride = out_stride;
   cudaStream_t st = (cudaStream_t)stream;
   h->last_stream = st;
-  p.sink = {h->ws.err, h->err_host_dev, h->timeout_ns};
+  p.sink = make_sink(h->ws.err, h->err_host_dev, h->timeout_ns);
   // short sequences go token by token, the others in chunks, longest first
   SeqBatch all = p.b;
   int order[WAVE_MAX_SEQS];
