@@ -157,25 +157,19 @@ constexpr int kTG = 0, kTWx = 128, kTState = 256, kTY = 384;
 __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
-template <int kBytes>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
-  if constexpr (kBytes == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
-// A tile of 128 tokens x kCols values at column `col` of the rows from `row0`
-// on, 128-byte swizzled blocks of 64 columns, by one warp: for rows that no
-// tensor map can describe (a stride that is no multiple of 16 bytes).  Rows
-// from n on repeat row n - 1.
+// Rows that no tensor map can describe (a stride that is no multiple of 16
+// bytes) are copied by the 256 threads behind, 8 bytes at a time: 128 tokens x
+// kCols values at column `col` of the rows from row0 on, as the same 128-byte
+// swizzled blocks of 64 columns.  Rows from n on repeat row n - 1.
 template <int kCols>
 __device__ __forceinline__ void copy_tile(uint32_t dst, const uint16_t* zx, long long stride, int col, size_t row0, int n) {
   constexpr int kPer = kCols * 2 / 8;  // pieces of a row
 #pragma unroll 4
-  for (int q = threadIdx.x & 31; q < kQ * kPer; q += 32) {
+  for (int q = threadIdx.x & 255; q < kQ * kPer; q += 256) {
     const int r = q / kPer, b = (q % kPer) * 8, blk = b >> 7, c = (b >> 4) & 7;
-    copy_async<8>(dst + blk * (kQ * 128) + r * 128 + ((c ^ (r & 7)) << 4) + (b & 15),
-                  zx + (row0 + min(r, n - 1)) * stride + col + b / 2);
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst + blk * (kQ * 128) + r * 128 + ((c ^ (r & 7)) << 4) + (b & 15)),
+                 "l"(zx + (row0 + min(r, n - 1)) * stride + col + b / 2)
+                 : "memory");
   }
 }
 
@@ -241,7 +235,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
 
   if (warp == 16) {
     if (lane == 0) {
-      const int copies = p.tiled ? 1 : 32;
+      const int copies = p.tiled ? 1 : 256;
       for (int b = 0; b < 2; ++b) {
         mbar_init(bar(L::kFull + b), copies);
         mbar_init(bar(L::kEmpty + b), 1);
@@ -437,99 +431,110 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
   } else if (warp < 16) {
     // ---------------------------------------------------------------- behind
     regs_take<kRegsBehind>();
-    // (w X)^T of a chunk is made before the output of the chunk before it: the
-    // state's product does not wait for the gate
-    for (int c = -1; c < chunks; ++c) {
-      if (c + 1 < chunks) {
-        const int k = c + 1, b = k & 1, left = len - k * kQ;
-        uint8_t* buf = smem + b * L::kBuf;
-        // ---- this token's x and B.  Behind the sequence's end lie other rows:
-        // theirs become zero.  An x that is not finite would reach earlier
-        // tokens as 0 * NaN in M X: it is noted here, becomes zero once the
-        // state's weights have been made of it, and is put back at the output.
-        wait_warp(L::kFull + b, (k >> 1) & 1);
-        uint8_t* xrow = buf + 2 * kBC + h * kXT + row * 128;
-        bool odd = false;
-        if (row >= left) {
-          uint8_t* brow = buf + h * (kQ * 128) + row * 128;
-#pragma unroll 4
-          for (int e = 0; e < 8; ++e) {
-            *(uint4*)(xrow + (e << 4)) = make_uint4(0, 0, 0, 0);
-            *(uint4*)(brow + (e << 4)) = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async_smem();
-        } else {
-          uint32_t acc[2] = {0, 0};
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint4 x = *(const uint4*)(xrow + ((e ^ (lane & 7)) << 4));
-            asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[0]) : "r"(x.x), "r"(0));
-            asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[1]) : "r"(x.y), "r"(0));
-            asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[0]) : "r"(x.z), "r"(0));
-            asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[1]) : "r"(x.w), "r"(0));
-          }
-          odd = ((acc[0] | acc[1]) & 0x7fff7fffu) != 0;
-          if (odd) atomicOr(&sbad[k & 3], 1u << (h * 4 + quad));
-        }
-        bar_sync(4, 256);  // x and its flags are complete; every thread here is done with chunk k - 2
-        // cleared two chunks ahead: nobody sets these before the next barrier
-        if ((threadIdx.x & 255) == 0) sbad[(k + 2) & 3] = 0;
-        // ---- (w X)^T: row (hh, pp), tokens 64 h .. 64 h + 63
-        wait_warp(L::kScan, k & 1);
-        if (k > 0) wait_warp(L::kS, (k - 1) & 1);
-        tc_fence_after();
-        const uint8_t* xt = buf + 2 * kBC + hh * kXT + (pp & 7) * 2;
-#pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-          const int j0 = h * 64 + 16 * q;
-          float v[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e)  // j0 is a multiple of 8
-            v[e] = bf(*(const uint16_t*)(xt + (j0 + e) * 128 + (((pp >> 3) ^ (e & 7)) << 4)));
-          // w_j: u_j times the decay from its 32 tokens' end on; the last 32 have v_j only
-          const bool tail_block = j0 >= 96;
-          const float tail = tail_block ? 1.f : ex2(-saft[hh * kQ + (j0 | 31)]);
-          const float4* uj = (const float4*)((tail_block ? sv + hh * kQ : su + hh * 96) + j0);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float4 u4 = uj[e];
-            if (tail_block) u4 = make_float4(ex2(u4.x), ex2(u4.y), ex2(u4.z), ex2(u4.w));
-            const float2 r0 = mul2(make_float2(v[4 * e], v[4 * e + 1]), mul2(make_float2(u4.x, u4.y), make_float2(tail, tail)));
-            const float2 r1 = mul2(make_float2(v[4 * e + 2], v[4 * e + 3]), mul2(make_float2(u4.z, u4.w), make_float2(tail, tail)));
-            v[4 * e] = r0.x, v[4 * e + 1] = r0.y, v[4 * e + 2] = r1.x, v[4 * e + 3] = r1.y;
-          }
-          uint32_t hi[8], lo[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            hi[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
-            const float2 r = sub2(make_float2(v[2 * e], v[2 * e + 1]),
-                                  make_float2(__uint_as_float(hi[e] << 16), __uint_as_float(hi[e] & 0xFFFF0000u)));
-            lo[e] = pack_bf16(r.x, r.y);
-          }
-          tmem_st8(tmem + kTWx + lanes + h * 32 + q * 8, hi);
-          tmem_st8(tmem + kTWx + 64 + lanes + h * 32 + q * 8, lo);
-        }
-        tmem_st_wait();
-        if (sbad[k & 3]) {  // seen by every thread or none
-          bar_sync(4, 256);
-          if (odd) {
-#pragma unroll 1
-            for (int e = 0; e < 64; ++e) {
-              uint16_t* x = (uint16_t*)xrow + e;
-              if ((*x & 0x7F80) == 0x7F80) *x = 0;
-            }
-            fence_proxy_async_smem();
-          }
-        }
-        tc_fence_before();
-        mbar_arrive(bar(L::kWx));
-      }
-      if (c < 0) continue;
-      // ---- the output: y, gated, over z's row and from there to global
+    for (int c = 0; c < chunks; ++c) {
       const int b = c & 1, left = len - c * kQ;
       uint8_t* buf = smem + b * L::kBuf;
+      // ---- this token's x and B.  Behind the sequence's end lie other rows:
+      // theirs become zero.  An x that is not finite would reach earlier
+      // tokens as 0 * NaN in M X: it is noted here, becomes zero once the
+      // state's weights have been made of it, and is put back at the output.
+      if (!p.tiled) {
+        const size_t row0 = first + (size_t)c * kQ;
+        const int n = min(kQ, left);
+        wait_warp(L::kEmpty + b, ((c >> 1) & 1) ^ 1);
+        wait_warp(L::kCEmpty + b, ((c >> 1) & 1) ^ 1);
+        copy_tile<2 * kSsmN>(sb + b * L::kBuf, p.zx, p.zx_stride, 2 * di, row0, n);  // B, then C
+        copy_tile<2 * kSsmP>(sb + b * L::kBuf + 2 * kBC, p.zx, p.zx_stride, di + h0 * kSsmP, row0, n);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_proxy_async_smem();
+        mbar_arrive(bar(L::kFull + b));
+        mbar_arrive(bar(L::kCFull + b));
+      }
+      wait_warp(L::kFull + b, (c >> 1) & 1);
+      uint8_t* xrow = buf + 2 * kBC + h * kXT + row * 128;
+      bool odd = false;
+      if (row >= left) {
+        uint8_t* brow = buf + h * (kQ * 128) + row * 128;
+#pragma unroll 4
+        for (int e = 0; e < 8; ++e) {
+          *(uint4*)(xrow + (e << 4)) = make_uint4(0, 0, 0, 0);
+          *(uint4*)(brow + (e << 4)) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+      } else {
+        uint32_t acc[2] = {0, 0};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint4 x = *(const uint4*)(xrow + ((e ^ (lane & 7)) << 4));
+          asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[0]) : "r"(x.x), "r"(0));
+          asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[1]) : "r"(x.y), "r"(0));
+          asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[0]) : "r"(x.z), "r"(0));
+          asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[1]) : "r"(x.w), "r"(0));
+        }
+        odd = ((acc[0] | acc[1]) & 0x7fff7fffu) != 0;
+        if (odd) atomicOr(&sbad[c & 3], 1u << (h * 4 + quad));
+      }
+      bar_sync(4, 256);  // x and its flags are complete; every thread here is done with chunk c - 2
+      // cleared two chunks ahead: nobody sets these before the next barrier
+      if ((threadIdx.x & 255) == 0) sbad[(c + 2) & 3] = 0;
+      // ---- (w X)^T: row (hh, pp), tokens 64 h .. 64 h + 63
+      wait_warp(L::kScan, c & 1);
+      if (c > 0) wait_warp(L::kS, (c - 1) & 1);
+      tc_fence_after();
+      const uint8_t* xt = buf + 2 * kBC + hh * kXT + (pp & 7) * 2;
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        const int j0 = h * 64 + 16 * q;
+        float v[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e)  // j0 is a multiple of 8
+          v[e] = bf(*(const uint16_t*)(xt + (j0 + e) * 128 + (((pp >> 3) ^ (e & 7)) << 4)));
+        // w_j: u_j times the decay from its 32 tokens' end on; the last 32 have v_j only
+        const bool tail_block = j0 >= 96;
+        const float tail = tail_block ? 1.f : ex2(-saft[hh * kQ + (j0 | 31)]);
+        const float4* uj = (const float4*)((tail_block ? sv + hh * kQ : su + hh * 96) + j0);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float4 u4 = uj[e];
+          if (tail_block) u4 = make_float4(ex2(u4.x), ex2(u4.y), ex2(u4.z), ex2(u4.w));
+          const float2 r0 = mul2(make_float2(v[4 * e], v[4 * e + 1]), mul2(make_float2(u4.x, u4.y), make_float2(tail, tail)));
+          const float2 r1 = mul2(make_float2(v[4 * e + 2], v[4 * e + 3]), mul2(make_float2(u4.z, u4.w), make_float2(tail, tail)));
+          v[4 * e] = r0.x, v[4 * e + 1] = r0.y, v[4 * e + 2] = r1.x, v[4 * e + 3] = r1.y;
+        }
+        uint32_t hi[8], lo[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          hi[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+          const float2 r = sub2(make_float2(v[2 * e], v[2 * e + 1]),
+                                make_float2(__uint_as_float(hi[e] << 16), __uint_as_float(hi[e] & 0xFFFF0000u)));
+          lo[e] = pack_bf16(r.x, r.y);
+        }
+        tmem_st8(tmem + kTWx + lanes + h * 32 + q * 8, hi);
+        tmem_st8(tmem + kTWx + 64 + lanes + h * 32 + q * 8, lo);
+      }
+      tmem_st_wait();
+      if (sbad[c & 3]) {  // seen by every thread or none
+        bar_sync(4, 256);
+        if (odd) {
+#pragma unroll 1
+          for (int e = 0; e < 64; ++e) {
+            uint16_t* x = (uint16_t*)xrow + e;
+            if ((*x & 0x7F80) == 0x7F80) *x = 0;
+          }
+          fence_proxy_async_smem();
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(bar(L::kWx));
+      // ---- the output: y, gated, over z's row and from there to global
       uint8_t* ztile = buf + kBC + h * kXT;
       const uint32_t any_bad = sbad[c & 3] >> (h * 4) & 15u;
+      if (!p.tiled) {
+        wait_warp(L::kY2, c & 1);
+        copy_tile<2 * kSsmP>(sb + b * L::kBuf + kBC, p.zx, p.zx_stride, h0 * kSsmP, first + (size_t)c * kQ, min(kQ, left));
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        mbar_arrive(bar(L::kZFull));
+      }
       wait_warp(L::kZFull, c & 1);
       wait_warp(L::kYFull + h, c & 1);
       tc_fence_after();
@@ -604,16 +609,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
             for (int e = 0; e < 4; ++e) mma_ss(tmem + kTG, a + 2 * e, b + 2 * e, id_g, k + e > 0);
           }
           tc_commit(bar(L::kG));
-          if (!wait(L::kHFull, c & 1) || !wait(L::kWx, c & 1)) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int k = 0; k < 4; ++k) {  // the high parts, then the remainders
-            const uint64_t b = sdesc_mn_sw128(buf + (k & 1) * (4 * 2048), kQ * 128);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              mma_ts(tmem + kTState, tmem + kTWx + 32 * k + 8 * e, b + (2048 >> 4) * e, id_s, !zero || k + e > 0);
-          }
-          tc_commit(bar(L::kS));
+          if (!wait(L::kHFull, c & 1)) break;
           if (c > 0 && !wait(L::kYFree, (c - 1) & 1)) break;
           tc_fence_after();
 #pragma unroll 1
@@ -624,6 +620,16 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
             for (int e = 0; e < 4; ++e) mma_ss(tmem + kTY + (k >> 1) * 64, a + 2 * e, b + 2 * e, id_y2, (k & 1) + e > 0);
           }
           tc_commit(bar(L::kY2));
+          if (!wait(L::kWx, c & 1)) break;
+          tc_fence_after();
+#pragma unroll 1
+          for (int k = 0; k < 4; ++k) {  // the high parts, then the remainders
+            const uint64_t b = sdesc_mn_sw128(buf + (k & 1) * (4 * 2048), kQ * 128);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              mma_ts(tmem + kTState, tmem + kTWx + 32 * k + 8 * e, b + (2048 >> 4) * e, id_s, !zero || k + e > 0);
+          }
+          tc_commit(bar(L::kS));
 #pragma unroll 1
           for (int h = 0; h < 2; ++h) {
             if (!wait(L::kMFull + h, c & 1)) break;
@@ -675,27 +681,6 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
               }
             }
         }
-      } else {
-        for (int c = 0; c < chunks; ++c) {
-          const uint32_t buf = sb + (c & 1) * L::kBuf;
-          const size_t row0 = first + (size_t)c * kQ;
-          const int n = min(kQ, len - c * kQ);
-          const uint32_t parity = ((c >> 1) & 1) ^ 1;
-          wait_warp(L::kEmpty + (c & 1), parity);
-          if (!ok) break;
-          copy_tile<kSsmN>(buf, p.zx, p.zx_stride, 2 * di, row0, n);
-          copy_tile<kSsmP>(buf + 2 * kBC, p.zx, p.zx_stride, di + h0 * kSsmP, row0, n);
-          copy_tile<kSsmP>(buf + 2 * kBC + kXT, p.zx, p.zx_stride, di + (h0 + 1) * kSsmP, row0, n);
-          asm volatile("cp.async.wait_all;" ::: "memory");
-          fence_proxy_async_smem();
-          mbar_arrive(bar(L::kFull + (c & 1)));
-          wait_warp(L::kCEmpty + (c & 1), parity);
-          if (!ok) break;
-          copy_tile<kSsmN>(buf + kBC, p.zx, p.zx_stride, 2 * di + kSsmN, row0, n);
-          asm volatile("cp.async.wait_all;" ::: "memory");
-          fence_proxy_async_smem();
-          mbar_arrive(bar(L::kCFull + (c & 1)));
-        }
       }
       __syncwarp();
     } else if (warp == 18) {
@@ -714,18 +699,6 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
           if (!ok && c > 0)
             for (int n = 0; n < (1 << 20) && !mbar_try_wait(bar(L::kZFull), (c - 1) & 1); ++n) {
             }
-        }
-      } else {
-        for (int c = 0; c < chunks; ++c) {
-          const uint32_t dst = sb + (c & 1) * L::kBuf + kBC;
-          const size_t row0 = first + (size_t)c * kQ;
-          const int n = min(kQ, len - c * kQ);
-          wait_warp(L::kY2, c & 1);
-          if (!ok) break;
-          copy_tile<kSsmP>(dst, p.zx, p.zx_stride, h0 * kSsmP, row0, n);
-          copy_tile<kSsmP>(dst + kXT, p.zx, p.zx_stride, (h0 + 1) * kSsmP, row0, n);
-          asm volatile("cp.async.wait_all;" ::: "memory");
-          mbar_arrive(bar(L::kZFull));
         }
       }
       __syncwarp();
