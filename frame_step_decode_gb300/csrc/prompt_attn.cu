@@ -348,52 +348,66 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __gr
       __syncwarp();
     } else if (warp == 9) {
       // --------------------------------------------------------------- MMAs
-      if (lane == 0) {
+      {
         constexpr uint32_t id_s = idesc_16(128, 128, kF16, false, false), id_o = idesc_16(128, D, kF16, false, true);
         uint32_t it_r = 0, p_it[2] = {0, 0}, g_it = 0;
         auto slot_of = [&](uint32_t i) { return (int)(i % L::kStages); };
-        auto full = [&](uint32_t i) { return wait(L::kFull + slot_of(i), (i / L::kStages) & 1); };
+        auto full = [&](uint32_t i) { return wait_warp(L::kFull + slot_of(i), (i / L::kStages) & 1); };
+        auto commit = [&](int b) {
+          if (elect_one()) tc_commit(bar(b));
+          __syncwarp();
+        };
         auto scores = [&](int st, uint32_t i) {  // S = Q K^T
-          const uint32_t q = sb + st * L::kTile, kt = sb + L::kRing + slot_of(i) * L::kTile;
+          if (elect_one()) {
+            const uint32_t q = sdesc_lo(sb + st * L::kTile), kt = sdesc_lo(sb + L::kRing + slot_of(i) * L::kTile);
 #pragma unroll
-          for (int e = 0; e < D / 16; ++e) {
-            const uint32_t o = (e / 4) * (kRows * 128) + (e % 4) * 32;
-            mma_ss(tS(st), sdesc_sw128(q + o), sdesc_sw128(kt + o), id_s, e > 0);
+            for (int e = 0; e < D / 16; ++e) {
+              const uint32_t o = ((e / 4) * (kRows * 128) + (e % 4) * 32) >> 4;
+              if (e == 0)
+                mma_ss<false>(tS(st), q, kt, id_s);
+              else
+                mma_ss<true>(tS(st), q + o, kt + o, id_s);
+            }
+            tc_commit(bar(L::kSFull + st));
           }
-          tc_commit(bar(L::kSFull + st));
+          __syncwarp();
         };
         auto values = [&](int st, uint32_t i, bool first) {  // O += P V
-          const uint32_t vt = sb + L::kRing + slot_of(i) * L::kTile;
+          if (elect_one()) {
+            const uint32_t vt = sdesc_lo(sb + L::kRing + slot_of(i) * L::kTile, kRows * 128);
 #pragma unroll
-          for (int e = 0; e < kRows / 16; ++e)
-            mma_ts(tO(st), tS(st) + 8 * e, sdesc_mn_sw128(vt + e * 2048, kRows * 128), id_o, !first || e > 0);
+            for (int e = 0; e < kRows / 16; ++e)
+              mma_ts(tO(st), tS(st) + 8 * e, vt + e * (2048 >> 4), id_o, e > 0 ? 1u : first ? 0u : 1u);
+          }
+          __syncwarp();
         };
         for (uint32_t k = 0; ok; ++k) {
-          if (!wait(L::kItemFull + (k & 1), (k >> 1) & 1)) break;
+          if (!wait_warp(L::kItemFull + (k & 1), (k >> 1) & 1)) break;
           const int valid = items[k & 1].valid, n0 = items[k & 1].n0, n1 = items[k & 1].n1;
-          mbar_arrive(bar(L::kItemEmpty + (k & 1)));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::kItemEmpty + (k & 1)));
           if (!valid) break;
           const int nb = max(n0, n1);
-          if (!wait(L::kQFull, k & 1) || !full(it_r)) break;
+          if (!wait_warp(L::kQFull, k & 1) || !full(it_r)) break;
           tc_fence_after();
           scores(0, it_r);
           if (n1) scores(1, it_r);
-          tc_commit(bar(L::kEmpty + slot_of(it_r)));
+          commit(L::kEmpty + slot_of(it_r));
           for (int j = 0; j < nb; ++j) {
             const uint32_t kv = it_r + 2 * j + 1, kk = kv + 1;
             const bool more = j + 1 < nb, guarded = j >= n0 - 1;
             if (!full(kv)) break;
-            if (guarded) mbar_arrive(bar(L::kGo));
+            if (guarded && lane == 0) mbar_arrive(bar(L::kGo));
             if (more && !full(kk)) break;
             bool checked = !guarded;
 #pragma unroll
             for (int st = 0; st < 2; ++st) {
               const int n = st ? n1 : n0;
               if (!ok || j >= n) continue;
-              if (!wait(L::kPFull + st, p_it[st] & 1)) continue;
+              if (!wait_warp(L::kPFull + st, p_it[st] & 1)) continue;
               ++p_it[st];
               if (!checked) {
-                if (!wait(L::kOk, g_it & 1)) continue;
+                if (!wait_warp(L::kOk, g_it & 1)) continue;
                 ++g_it;
                 checked = true;
               }
@@ -402,18 +416,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __gr
               if (j + 1 < n)
                 scores(st, kk);
               else
-                tc_commit(bar(L::kOFull + st));
+                commit(L::kOFull + st);
             }
             if (!ok) break;
-            tc_commit(bar(L::kEmpty + slot_of(kv)));
-            if (more) tc_commit(bar(L::kEmpty + slot_of(kk)));
+            commit(L::kEmpty + slot_of(kv));
+            if (more) commit(L::kEmpty + slot_of(kk));
           }
           if (!ok) break;
-          tc_commit(bar(L::kQEmpty));
+          commit(L::kQEmpty);
           it_r += 2 * nb;
         }
         if (!ok) {  // give-up: wait (bounded) for the MMAs issued so far
-          tc_commit(bar(L::kDone));
+          commit(L::kDone);
           for (int n = 0; n < (1 << 20) && !mbar_try_wait(bar(L::kDone), 0); ++n) {
           }
         }

@@ -17,19 +17,40 @@ __device__ __forceinline__ void tma_load_3d_plain(uint32_t dst, const CUtensorMa
       : "memory");
 }
 
-// D[tmem] (+)= A * B, kind::f16; both operands from shared memory, or A from TMEM.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+// One lane of a converged warp.  The branch around single-thread work (copies,
+// MMAs, commits) is taken with this and not with lane == 0: the compiler then
+// keeps descriptors and addresses in uniform registers, where a tcgen05.mma
+// wants them; issued from a lane == 0 branch an MMA took ~75 cycles (six moves
+// into uniform registers each), more than the tensor core needs for it.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// D[tmem] (+)= A * B, kind::f16; both operands from shared memory, or A from
+// TMEM.  A descriptor is its low word (the address, see sdesc_lo) and a high
+// word that is the same for every tile used here.
+constexpr uint32_t kDescHi = (1024 >> 4) | (1u << 14) | (2u << 29);  // stride offset 1024 B, version, 128-byte swizzle
+__device__ __forceinline__ uint32_t sdesc_lo(uint32_t addr, uint32_t lead = 16) {  // lead: bytes to the next 64 of M/N
+  return ((addr >> 4) & 0x3FFFu) | ((lead >> 4) << 16);
+}
+template <bool kAcc>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .b64 a, b;\n\t.reg .pred p;\n\tmov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "n"((int)kAcc), "r"(kDescHi)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+      "{\n\t.reg .b64 b;\n\t.reg .pred p;\n\tmov.b64 b, {%2, %5};\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(acc), "r"(kDescHi)
       : "memory");
 }
 
@@ -80,18 +101,9 @@ __device__ __forceinline__ void tmem_ld16_nowait(uint32_t taddr, uint32_t* r) {
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// MN-major operand: rows of 128 bytes along M/N (64 elements), one row per k,
-// 8 rows a swizzle atom (stride-dimension offset 1024 B); the next 64 elements
-// of M/N are `lead` bytes away (leading-dimension offset).
-__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t addr, uint32_t lead) {
-  uint64_t d = 0;
-  d |= (uint64_t)((addr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(lead >> 4) << 16;
-  d |= (uint64_t)(1024 >> 4) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
-}
+// Operand tiles are rows of 128 bytes (64 values), 8 rows a swizzle atom.  K-major
+// (a row per m or n): the next 64 of K are another tile.  MN-major (a row per
+// k): the next 64 of M or N are `lead` bytes away.
 // Instruction descriptor of kind::f16 with fp32 accumulation: fp16 or bf16
 // operands, A K-major, B K-major or (b_mn) MN-major.
 __host__ __device__ constexpr uint32_t idesc_16(int M, int N, bool f16, bool a_mn, bool b_mn) {

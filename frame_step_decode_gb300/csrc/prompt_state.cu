@@ -594,59 +594,76 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
     regs_give<kRegsRest>();
     if (warp == 16) {
       // ---------------------------------------------------------------- MMAs
-      if (lane == 0) {
-        constexpr uint32_t id_g = idesc_16(128, 128, false, false, false), id_y2 = idesc_16(128, 64, false, false, false),
-                           id_y = idesc_16(128, 64, false, false, true), id_s = idesc_16(128, 128, false, false, true);
-        for (int c = 0; c < chunks; ++c) {
-          const uint32_t buf = sb + (c & 1) * L::kBuf, cm = buf + kBC, x = buf + 2 * kBC;
-          const bool zero = c == 0 && !goes_on;
-          if (!wait(L::kFull + (c & 1), (c >> 1) & 1) || !wait(L::kCFull + (c & 1), (c >> 1) & 1)) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int k = 0; k < 2; ++k) {
-            const uint64_t a = sdesc_sw128(cm + k * (kQ * 128)), b = sdesc_sw128(buf + k * (kQ * 128));
+      constexpr uint32_t id_g = idesc_16(128, 128, false, false, false), id_y2 = idesc_16(128, 64, false, false, false),
+                         id_y = idesc_16(128, 64, false, false, true), id_s = idesc_16(128, 128, false, false, true);
+      constexpr uint32_t kBlk = (kQ * 128) >> 4;  // the next 64 columns of a tile, as a descriptor counts
+      for (int c = 0; c < chunks; ++c) {
+        const uint32_t buf = sb + (c & 1) * L::kBuf;
+        const bool zero = c == 0 && !goes_on;
+        wait_warp(L::kFull + (c & 1), (c >> 1) & 1);
+        wait_warp(L::kCFull + (c & 1), (c >> 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {  // G = C B^T
+          const uint32_t cm = sdesc_lo(buf + kBC), bm = sdesc_lo(buf);
+          mma_ss<false>(tmem + kTG, cm, bm, id_g);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) mma_ss(tmem + kTG, a + 2 * e, b + 2 * e, id_g, k + e > 0);
-          }
+          for (int e = 1; e < 8; ++e)
+            mma_ss<true>(tmem + kTG, cm + (e / 4) * kBlk + (e % 4) * 2, bm + (e / 4) * kBlk + (e % 4) * 2, id_g);
           tc_commit(bar(L::kG));
-          if (!wait(L::kHFull, c & 1)) break;
-          if (c > 0 && !wait(L::kYFree, (c - 1) & 1)) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int k = 0; k < 4 && !zero; ++k) {  // half of n of a head
-            const uint64_t a = sdesc_sw128(cm + (k & 1) * (kQ * 128)),
-                           b = sdesc_sw128(sb + L::kH + (k >> 1) * kXT + (k & 1) * (64 * 128));
+        }
+        __syncwarp();
+        wait_warp(L::kHFull, c & 1);
+        if (c > 0) wait_warp(L::kYFree, (c - 1) & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {  // Y = C H^T
+          if (!zero) {
+            const uint32_t cm = sdesc_lo(buf + kBC), hm = sdesc_lo(sb + L::kH);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) mma_ss(tmem + kTY + (k >> 1) * 64, a + 2 * e, b + 2 * e, id_y2, (k & 1) + e > 0);
+            for (int h = 0; h < 2; ++h) {
+              mma_ss<false>(tmem + kTY + h * 64, cm, hm + h * (kXT >> 4), id_y2);
+#pragma unroll
+              for (int e = 1; e < 8; ++e)
+                mma_ss<true>(tmem + kTY + h * 64, cm + (e / 4) * kBlk + (e % 4) * 2,
+                             hm + ((h * kXT + (e / 4) * (64 * 128)) >> 4) + (e % 4) * 2, id_y2);
+            }
           }
           tc_commit(bar(L::kY2));
-          if (!wait(L::kWx, c & 1)) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int k = 0; k < 4; ++k) {  // the high parts, then the remainders
-            const uint64_t b = sdesc_mn_sw128(buf + (k & 1) * (4 * 2048), kQ * 128);
+        }
+        __syncwarp();
+        wait_warp(L::kWx, c & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {  // the state += (w X)^T B: the high parts, then the remainders
+          const uint32_t bm = sdesc_lo(buf, kQ * 128);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              mma_ts(tmem + kTState, tmem + kTWx + 32 * k + 8 * e, b + (2048 >> 4) * e, id_s, !zero || k + e > 0);
-          }
+          for (int e = 0; e < 16; ++e)
+            mma_ts(tmem + kTState, tmem + kTWx + 8 * e, bm + (e % 8) * (2048 >> 4), id_s, e > 0 ? 1u : zero ? 0u : 1u);
           tc_commit(bar(L::kS));
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            if (!wait(L::kMFull + h, c & 1)) break;
-            tc_fence_after();
-            const uint64_t b = sdesc_mn_sw128(x + h * kXT, kQ * 128);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {  // Y += M X
+          wait_warp(L::kMFull + h, c & 1);
+          tc_fence_after();
+          if (ok && elect_one()) {
+            const uint32_t xm = sdesc_lo(buf + 2 * kBC + h * kXT, kQ * 128);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              mma_ts(tmem + kTY + h * 64, tmem + kTG + h * 64 + 8 * e, b + (2048 >> 4) * e, id_y, !zero || e > 0);
+              mma_ts(tmem + kTY + h * 64, tmem + kTG + h * 64 + 8 * e, xm + e * (2048 >> 4), id_y, e > 0 ? 1u : zero ? 0u : 1u);
             tc_commit(bar(L::kYFull + h));
           }
-          if (!ok) break;
-          tc_commit(bar(L::kEmpty + (c & 1)));
+          __syncwarp();
         }
-        if (!ok) {  // give-up: wait (bounded) for the MMAs issued so far
-          tc_commit(bar(L::kDone));
-          for (int n = 0; n < (1 << 20) && !mbar_try_wait(bar(L::kDone), 0); ++n) {
-          }
+        if (!ok) break;
+        if (elect_one()) tc_commit(bar(L::kEmpty + (c & 1)));
+        __syncwarp();
+      }
+      if (!ok) {  // give-up: wait (bounded) for the MMAs issued so far
+        if (elect_one()) tc_commit(bar(L::kDone));
+        __syncwarp();
+        for (int n = 0; n < (1 << 20) && !mbar_try_wait(bar(L::kDone), 0); ++n) {
         }
       }
       __syncwarp();
