@@ -121,11 +121,11 @@ constexpr int kXT = kQ * kSsmP * 2;     // ... of one head's x (or z) tile
 struct StateSmem {
   static constexpr int kBuf = 2 * kBC + 2 * kXT;  // B, C (later z, then out, of both heads), x of both heads
   static constexpr int kH = 2 * kBuf;             // bf16 H of both heads: [2][n / 64][64 rows of 128 B]
-  static constexpr int kAfter = kH + 2 * kXT;     // [head][128] the decays behind token j, to the chunk's end
-  static constexpr int kV = kAfter + 2 * kQ * 4;  // [head][128] log2 dt_j - after_j
+  static constexpr int kV = kH + 2 * kXT;         // [head][128] log2 dt_j - (the decays behind j, to the chunk's end)
   static constexpr int kU = kV + 2 * kQ * 4;      // [head][96] dt_j 2^-(the decays behind j in its 32 tokens)
-  static constexpr int kLast = kU + 2 * 96 * 4;   // [head] the decays of the whole chunk
-  static constexpr int kBad = kLast + 8;          // [chunk % 4] bit head * 4 + warp: an x that is not finite
+  static constexpr int kW = kU + 2 * 96 * 4;      // [head][128] w_j
+  static constexpr int kTot = kW + 2 * kQ * 4;    // [in front, behind][head][32 tokens] sums of decays
+  static constexpr int kBad = kTot + 2 * 2 * 4 * 4;  // [chunk % 4] bit head * 4 + warp: an x that is not finite
   static constexpr int kBars = kBad + 4 * 4;
   enum {
     kFull = 0,             // B and x
@@ -141,7 +141,6 @@ struct StateSmem {
     kYFree = kYFull + 2,
     kWx,
     kS,
-    kScan,
     kDone,
     kCount
   };
@@ -249,7 +248,6 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
       mbar_init(bar(L::kY2), 1);
       mbar_init(bar(L::kHFull), 256);
       mbar_init(bar(L::kYFree), 256);
-      mbar_init(bar(L::kScan), 1);
       mbar_init(bar(L::kWx), 256);
       mbar_init(bar(L::kS), 1);
       mbar_init(bar(L::kDone), 1);
@@ -279,24 +277,59 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
   const int hh = row >> 6, pp = row & 63;  // for the state: row (head hh, p), half h of the columns or tokens
   const int head = h0 + h;
   float* sv = (float*)(smem + L::kV);
-  float* saft = (float*)(smem + L::kAfter);
   float* su = (float*)(smem + L::kU);
-  float* slast = (float*)(smem + L::kLast);
+  float* sw = (float*)(smem + L::kW);
   uint32_t* sbad = (uint32_t*)(smem + L::kBad);
+  // the decays: this token's dt of chunk c (0 behind the sequence's end), the
+  // sum of the later tokens' log-decays among its 32 (in powers of two), and
+  // the sum of all 32 for the others.  Summed from the end: the state's newest
+  // tokens are exact to fp32 whatever the sum over the chunk is.
+  const uint16_t* dt_col = p.zx + first * p.zx_stride + 2 * di + 2 * kSsmN + head;
+  const float rate = warp < 16 ? ex2(bf(p.prm[head]) * 1.44269504088896340736f) * 1.44269504088896340736f : 0.f;
+  const float bias = warp < 16 ? bf(p.prm[p.Hs + head]) : 0.f;
+  auto dt_at = [&](int c) { return c * kQ + row < len ? dt_col[(size_t)(c * kQ + row) * p.zx_stride] : (uint16_t)0; };
+  auto decays = [&](int c, uint16_t raw, float& dt, float& inner) {
+    dt = c * kQ + row < len ? softplus(bf(raw) + bias) : 0.f;
+    // 2^-160 is zero in fp32: a larger step changes nothing, and the cap bounds the sums' rounding
+    float down = fminf(rate * dt, 160.f);
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const float v = __shfl_down_sync(0xffffffffu, down, d);
+      if (lane + d < 32) down += v;
+    }
+    inner = __shfl_down_sync(0xffffffffu, down, 1);
+    if (lane == 31) inner = 0.f;
+    return down;  // lane 0: the sum of all 32
+  };
   const size_t state_at = (((size_t)p.b.slot[seq] * p.Hs + h0) * kSsmP + row) * kSsmN + h * 64;
 
   if (warp < 8) {
     // -------------------------------------------------------------- in front
     regs_take<kRegsFront>();
     const float skip = bf(p.prm[2 * p.Hs + head]);
+    uint16_t dt_next = dt_at(0);
     for (int c = 0; c < chunks; ++c) {
+      // ---- the decays
+      float dt, inner;
+      const float sum = decays(c, dt_next, dt, inner);
+      dt_next = dt_at(c + 1);
+      float* tot = (float*)(smem + L::kTot);
+      if (lane == 0) tot[h * 4 + quad] = sum;
+      bar_sync(1, 256);  // also: the last chunk's sv and su have been read
+      float end[4];  // behind each 32 tokens
+      end[3] = 0.f;
+#pragma unroll
+      for (int q = 2; q >= 0; --q) end[q] = end[q + 1] + tot[h * 4 + q + 1];
+      const float after = inner + (quad == 0 ? end[0] : quad == 1 ? end[1] : quad == 2 ? end[2] : 0.f);
+      const float last = end[0] + tot[h * 4];
+      sv[h * kQ + row] = lg2(dt) - after;
+      if (row < 96) su[h * 96 + row] = dt * ex2(-inner);
       // ---- the state: its bf16 copy for C H^T, and the chunk's decay
-      wait_warp(L::kScan, c & 1);
       if (c > 0) wait_warp(L::kS, (c - 1) & 1);
       tc_fence_after();
       const bool zero = c == 0 && !goes_on;
       if (!zero) {
-        const float dec = ex2(-slast[hh]);
+        const float dec = ex2(-((tot[hh * 4] + tot[hh * 4 + 1]) + (tot[hh * 4 + 2] + tot[hh * 4 + 3])));
         uint8_t* hrow = smem + L::kH + hh * kXT + h * (64 * 128) + pp * 128;
 #pragma unroll 1
         for (int q = 0; q < 4; ++q) {
@@ -330,10 +363,10 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
       }
       tc_fence_before();
       mbar_arrive(bar(L::kHFull));
+      bar_sync(2 + h, 128);  // the head's sv and su are complete
       // ---- M, over G once both heads have read G
       wait_warp(L::kG, c & 1);
       tc_fence_after();
-      const float after = saft[h * kQ + row];  // c_j - c_i = after_i - after_j
       // 32 tokens at a time, from the diagonal down: m[16 t ..] is block quad - t
       uint32_t m[64];
       {
@@ -369,7 +402,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
         const int q = quad - t;
         uint32_t g[32];
         tmem_ld32(tmem + kTG + lanes + 32 * q, g);
-        const float r = ex2(after - saft[h * kQ + 32 * q + 31]);
+        const float r = ex2(after - (q == 0 ? end[0] : q == 1 ? end[1] : end[2]));
         const float2 r2 = make_float2(r, r);
         const float4* uj = (const float4*)(su + h * 96 + 32 * q);
         tmem_ld_wait();
@@ -400,7 +433,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
       wait_warp(L::kY2, c & 1);
       tc_fence_after();
       if (!zero) {
-        const float ei = ex2(after - slast[h]);
+        const float ei = ex2(after - last);
 #pragma unroll 1
         for (int q = 0; q < 2; ++q) {
           uint32_t v[32];
@@ -431,101 +464,117 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
   } else if (warp < 16) {
     // ---------------------------------------------------------------- behind
     regs_take<kRegsBehind>();
-    for (int c = 0; c < chunks; ++c) {
-      const int b = c & 1, left = len - c * kQ;
-      uint8_t* buf = smem + b * L::kBuf;
-      // ---- this token's x and B.  Behind the sequence's end lie other rows:
-      // theirs become zero.  An x that is not finite would reach earlier
-      // tokens as 0 * NaN in M X: it is noted here, becomes zero once the
-      // state's weights have been made of it, and is put back at the output.
-      if (!p.tiled) {
-        const size_t row0 = first + (size_t)c * kQ;
-        const int n = min(kQ, left);
-        wait_warp(L::kEmpty + b, ((c >> 1) & 1) ^ 1);
-        wait_warp(L::kCEmpty + b, ((c >> 1) & 1) ^ 1);
-        copy_tile<2 * kSsmN>(sb + b * L::kBuf, p.zx, p.zx_stride, 2 * di, row0, n);  // B, then C
-        copy_tile<2 * kSsmP>(sb + b * L::kBuf + 2 * kBC, p.zx, p.zx_stride, di + h0 * kSsmP, row0, n);
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        fence_proxy_async_smem();
-        mbar_arrive(bar(L::kFull + b));
-        mbar_arrive(bar(L::kCFull + b));
-      }
-      wait_warp(L::kFull + b, (c >> 1) & 1);
-      uint8_t* xrow = buf + 2 * kBC + h * kXT + row * 128;
-      bool odd = false;
-      if (row >= left) {
-        uint8_t* brow = buf + h * (kQ * 128) + row * 128;
+    // (w X)^T of a chunk is made before the output of the chunk before it: the
+    // state's product does not wait for the gate
+    uint16_t dt_next = dt_at(0);
+    for (int c = -1; c < chunks; ++c) {
+      if (c + 1 < chunks) {
+        const int k = c + 1, b = k & 1, left = len - k * kQ;
+        uint8_t* buf = smem + b * L::kBuf;
+        // ---- this token's x and B.  Behind the sequence's end lie other rows:
+        // theirs become zero.  An x that is not finite would reach earlier
+        // tokens as 0 * NaN in M X: it is noted here, becomes zero once the
+        // state's weights have been made of it, and is put back at the output.
+        if (!p.tiled) {
+          const size_t row0 = first + (size_t)k * kQ;
+          const int n = min(kQ, left);
+          wait_warp(L::kEmpty + b, ((k >> 1) & 1) ^ 1);
+          wait_warp(L::kCEmpty + b, ((k >> 1) & 1) ^ 1);
+          copy_tile<2 * kSsmN>(sb + b * L::kBuf, p.zx, p.zx_stride, 2 * di, row0, n);  // B, then C
+          copy_tile<2 * kSsmP>(sb + b * L::kBuf + 2 * kBC, p.zx, p.zx_stride, di + h0 * kSsmP, row0, n);
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          fence_proxy_async_smem();
+          mbar_arrive(bar(L::kFull + b));
+          mbar_arrive(bar(L::kCFull + b));
+        }
+        float dt, inner;
+        const float sum = decays(k, dt_next, dt, inner);
+        dt_next = dt_at(k + 1);
+        float* tot = (float*)(smem + L::kTot) + 8;
+        if (lane == 0) tot[h * 4 + quad] = sum;
+        wait_warp(L::kFull + b, (k >> 1) & 1);
+        uint8_t* xrow = buf + 2 * kBC + h * kXT + row * 128;
+        bool odd = false;
+        if (row >= left) {
+          uint8_t* brow = buf + h * (kQ * 128) + row * 128;
 #pragma unroll 4
-        for (int e = 0; e < 8; ++e) {
-          *(uint4*)(xrow + (e << 4)) = make_uint4(0, 0, 0, 0);
-          *(uint4*)(brow + (e << 4)) = make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async_smem();
-      } else {
-        uint32_t acc[2] = {0, 0};
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint4 x = *(const uint4*)(xrow + ((e ^ (lane & 7)) << 4));
-          asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[0]) : "r"(x.x), "r"(0));
-          asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[1]) : "r"(x.y), "r"(0));
-          asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[0]) : "r"(x.z), "r"(0));
-          asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[1]) : "r"(x.w), "r"(0));
-        }
-        odd = ((acc[0] | acc[1]) & 0x7fff7fffu) != 0;
-        if (odd) atomicOr(&sbad[c & 3], 1u << (h * 4 + quad));
-      }
-      bar_sync(4, 256);  // x and its flags are complete; every thread here is done with chunk c - 2
-      // cleared two chunks ahead: nobody sets these before the next barrier
-      if ((threadIdx.x & 255) == 0) sbad[(c + 2) & 3] = 0;
-      // ---- (w X)^T: row (hh, pp), tokens 64 h .. 64 h + 63
-      wait_warp(L::kScan, c & 1);
-      if (c > 0) wait_warp(L::kS, (c - 1) & 1);
-      tc_fence_after();
-      const uint8_t* xt = buf + 2 * kBC + hh * kXT + (pp & 7) * 2;
-#pragma unroll 1
-      for (int q = 0; q < 4; ++q) {
-        const int j0 = h * 64 + 16 * q;
-        float v[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e)  // j0 is a multiple of 8
-          v[e] = bf(*(const uint16_t*)(xt + (j0 + e) * 128 + (((pp >> 3) ^ (e & 7)) << 4)));
-        // w_j: u_j times the decay from its 32 tokens' end on; the last 32 have v_j only
-        const bool tail_block = j0 >= 96;
-        const float tail = tail_block ? 1.f : ex2(-saft[hh * kQ + (j0 | 31)]);
-        const float4* uj = (const float4*)((tail_block ? sv + hh * kQ : su + hh * 96) + j0);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float4 u4 = uj[e];
-          if (tail_block) u4 = make_float4(ex2(u4.x), ex2(u4.y), ex2(u4.z), ex2(u4.w));
-          const float2 r0 = mul2(make_float2(v[4 * e], v[4 * e + 1]), mul2(make_float2(u4.x, u4.y), make_float2(tail, tail)));
-          const float2 r1 = mul2(make_float2(v[4 * e + 2], v[4 * e + 3]), mul2(make_float2(u4.z, u4.w), make_float2(tail, tail)));
-          v[4 * e] = r0.x, v[4 * e + 1] = r0.y, v[4 * e + 2] = r1.x, v[4 * e + 3] = r1.y;
-        }
-        uint32_t hi[8], lo[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          hi[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
-          const float2 r = sub2(make_float2(v[2 * e], v[2 * e + 1]),
-                                make_float2(__uint_as_float(hi[e] << 16), __uint_as_float(hi[e] & 0xFFFF0000u)));
-          lo[e] = pack_bf16(r.x, r.y);
-        }
-        tmem_st8(tmem + kTWx + lanes + h * 32 + q * 8, hi);
-        tmem_st8(tmem + kTWx + 64 + lanes + h * 32 + q * 8, lo);
-      }
-      tmem_st_wait();
-      if (sbad[c & 3]) {  // seen by every thread or none
-        bar_sync(4, 256);
-        if (odd) {
-#pragma unroll 1
-          for (int e = 0; e < 64; ++e) {
-            uint16_t* x = (uint16_t*)xrow + e;
-            if ((*x & 0x7F80) == 0x7F80) *x = 0;
+          for (int e = 0; e < 8; ++e) {
+            *(uint4*)(xrow + (e << 4)) = make_uint4(0, 0, 0, 0);
+            *(uint4*)(brow + (e << 4)) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();
+        } else {
+          uint32_t acc[2] = {0, 0};
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint4 x = *(const uint4*)(xrow + ((e ^ (lane & 7)) << 4));
+            asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[0]) : "r"(x.x), "r"(0));
+            asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[1]) : "r"(x.y), "r"(0));
+            asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[0]) : "r"(x.z), "r"(0));
+            asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[1]) : "r"(x.w), "r"(0));
+          }
+          odd = ((acc[0] | acc[1]) & 0x7fff7fffu) != 0;
+          if (odd) atomicOr(&sbad[k & 3], 1u << (h * 4 + quad));
         }
+        bar_sync(4, 256);  // x and its flags are complete; every thread here is done with chunk k - 2
+        // cleared two chunks ahead: nobody sets these before the next barrier
+        if ((threadIdx.x & 255) == 0) sbad[(k + 2) & 3] = 0;
+        // ---- (w X)^T: row (hh, pp), tokens 64 h .. 64 h + 63
+        {
+          float after = inner;
+#pragma unroll
+          for (int q = 1; q < 4; ++q)
+            if (q > quad) after += tot[h * 4 + q];
+          sw[h * kQ + row] = dt * ex2(-after);
+        }
+        if (k > 0) wait_warp(L::kS, (k - 1) & 1);
+        bar_sync(4, 256);  // sw is complete
+        tc_fence_after();
+        const uint8_t* xt = buf + 2 * kBC + hh * kXT + (pp & 7) * 2;
+#pragma unroll 1
+        for (int q = 0; q < 4; ++q) {
+          const int j0 = h * 64 + 16 * q;
+          float v[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e)  // j0 is a multiple of 8
+            v[e] = bf(*(const uint16_t*)(xt + (j0 + e) * 128 + (((pp >> 3) ^ (e & 7)) << 4)));
+          const float4* wj = (const float4*)(sw + hh * kQ + j0);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float4 w4 = wj[e];
+            const float2 r0 = mul2(make_float2(v[4 * e], v[4 * e + 1]), make_float2(w4.x, w4.y));
+            const float2 r1 = mul2(make_float2(v[4 * e + 2], v[4 * e + 3]), make_float2(w4.z, w4.w));
+            v[4 * e] = r0.x, v[4 * e + 1] = r0.y, v[4 * e + 2] = r1.x, v[4 * e + 3] = r1.y;
+          }
+          uint32_t hi[8], lo[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            hi[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+            const float2 r = sub2(make_float2(v[2 * e], v[2 * e + 1]),
+                                  make_float2(__uint_as_float(hi[e] << 16), __uint_as_float(hi[e] & 0xFFFF0000u)));
+            lo[e] = pack_bf16(r.x, r.y);
+          }
+          tmem_st8(tmem + kTWx + lanes + h * 32 + q * 8, hi);
+          tmem_st8(tmem + kTWx + 64 + lanes + h * 32 + q * 8, lo);
+        }
+        tmem_st_wait();
+        if (sbad[k & 3]) {  // seen by every thread or none
+          bar_sync(4, 256);
+          if (odd) {
+#pragma unroll 1
+            for (int e = 0; e < 64; ++e) {
+              uint16_t* x = (uint16_t*)xrow + e;
+              if ((*x & 0x7F80) == 0x7F80) *x = 0;
+            }
+            fence_proxy_async_smem();
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(bar(L::kWx));
       }
-      tc_fence_before();
-      mbar_arrive(bar(L::kWx));
+      if (c < 0) continue;
+      const int b = c & 1, left = len - c * kQ;
+      uint8_t* buf = smem + b * L::kBuf;
       // ---- the output: y, gated, over z's row and from there to global
       uint8_t* ztile = buf + kBC + h * kXT;
       const uint32_t any_bad = sbad[c & 3] >> (h * 4) & 15u;
@@ -614,6 +663,17 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
         }
         __syncwarp();
         wait_warp(L::kHFull, c & 1);
+        wait_warp(L::kWx, c & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {  // the state += (w X)^T B: the high parts, then the remainders
+          const uint32_t bm = sdesc_lo(buf, kQ * 128);
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            mma_ts(tmem + kTState, tmem + kTWx + 8 * e, bm + (e % 8) * (2048 >> 4), id_s, e > 0 ? 1u : zero ? 0u : 1u);
+          tc_commit(bar(L::kS));
+        }
+        __syncwarp();
         if (c > 0) wait_warp(L::kYFree, (c - 1) & 1);
         if (!ok) break;
         tc_fence_after();
@@ -630,17 +690,6 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
             }
           }
           tc_commit(bar(L::kY2));
-        }
-        __syncwarp();
-        wait_warp(L::kWx, c & 1);
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {  // the state += (w X)^T B: the high parts, then the remainders
-          const uint32_t bm = sdesc_lo(buf, kQ * 128);
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            mma_ts(tmem + kTState, tmem + kTWx + 8 * e, bm + (e % 8) * (2048 >> 4), id_s, e > 0 ? 1u : zero ? 0u : 1u);
-          tc_commit(bar(L::kS));
         }
         __syncwarp();
 #pragma unroll
@@ -717,79 +766,6 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
             for (int n = 0; n < (1 << 20) && !mbar_try_wait(bar(L::kZFull), (c - 1) & 1); ++n) {
             }
         }
-      }
-      __syncwarp();
-    } else {
-      // ------------------------------ the decays, a chunk ahead: lane l has
-      // tokens 4 l .. 4 l + 3 of both heads.  They are summed from the chunk's
-      // end, so that the weights of the state's newest tokens are exact to
-      // fp32 whatever the sum over the chunk is.
-      float rate[2], bias[2];
-#pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        rate[g] = expf(bf(p.prm[h0 + g])) * 1.44269504088896340736f;
-        bias[g] = bf(p.prm[p.Hs + h0 + g]);
-      }
-      const uint16_t* col = p.zx + first * p.zx_stride + 2 * di + 2 * kSsmN + h0;  // two heads: 4 bytes
-      uint32_t raw[4];
-      auto fetch = [&](int c) {
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const int j = c * kQ + 4 * lane + t;
-          raw[t] = j < len ? *(const uint32_t*)(col + (size_t)j * p.zx_stride) : 0;
-        }
-      };
-      fetch(0);
-      for (int c = 0; c < chunks; ++c) {
-        const int left = len - c * kQ;
-        float dt[2][4], after[2][4], last[2];
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          float lam[4];
-#pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            dt[g][t] = softplus((g ? __uint_as_float(raw[t] & 0xFFFF0000u) : __uint_as_float(raw[t] << 16)) + bias[g]);
-            if (4 * lane + t >= left) dt[g][t] = 0.f;
-            // the token's decay in powers of two; 2^-160 is zero in fp32: a larger
-            // step changes nothing, and the cap bounds the rounding of the sums
-            lam[t] = fminf(rate[g] * dt[g][t], 160.f);
-          }
-          float down = (lam[0] + lam[1]) + (lam[2] + lam[3]);  // this lane's and the later ones'
-#pragma unroll
-          for (int d = 1; d < 32; d <<= 1) {
-            const float v = __shfl_down_sync(0xffffffffu, down, d);
-            if (lane + d < 32) down += v;
-          }
-          float a = __shfl_down_sync(0xffffffffu, down, 1);
-          if (lane == 31) a = 0.f;
-          last[g] = __shfl_sync(0xffffffffu, down, 0);
-#pragma unroll
-          for (int t = 3; t >= 0; --t) {
-            after[g][t] = a;
-            a += lam[t];
-          }
-        }
-        if (c + 1 < chunks) fetch(c + 1);
-        if (c > 0) {  // the last chunk's have been read
-          wait_warp(L::kWx, (c - 1) & 1);
-          wait_warp(L::kMFull, (c - 1) & 1);
-          wait_warp(L::kMFull + 1, (c - 1) & 1);
-          if (!ok) break;
-        }
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          *(float4*)(saft + g * kQ + 4 * lane) = make_float4(after[g][0], after[g][1], after[g][2], after[g][3]);
-          *(float4*)(sv + g * kQ + 4 * lane) = make_float4(lg2(dt[g][0]) - after[g][0], lg2(dt[g][1]) - after[g][1],
-                                                           lg2(dt[g][2]) - after[g][2], lg2(dt[g][3]) - after[g][3]);
-          const float end = __shfl_sync(0xffffffffu, after[g][3], lane | 7);  // behind these 32 tokens
-          if (lane < 24)
-            *(float4*)(su + g * 96 + 4 * lane) =
-                make_float4(dt[g][0] * ex2(end - after[g][0]), dt[g][1] * ex2(end - after[g][1]),
-                            dt[g][2] * ex2(end - after[g][2]), dt[g][3] * ex2(end - after[g][3]));
-          if (lane == 0) slast[g] = last[g];
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::kScan));
       }
       __syncwarp();
     }
