@@ -105,47 +105,55 @@ __global__ void __launch_bounds__(256) k_prompt_state_rows(const __grid_constant
 // (the output is bf16); (w X)^T is split into a bf16 and the bf16 of its
 // remainder (2^-18), since the state is carried on in fp32.
 //
-// Five warpgroups: two in front (a head each: the decays, the state's pass
-// between chunks, M), two behind (the weights w, (w X)^T, the gated output),
+// Seven warpgroups: two in front (a head each: the decays, the state's pass
+// between chunks, M), four behind (the weights w, (w X)^T, the gated output),
 // and one warp each for the MMAs, the copies of B, C, x and those of z.  The
 // chain from chunk to chunk is the state's: its pass and its product.
 constexpr int kQ = 128;                 // tokens of a chunk
-constexpr int kStateThreads = 640;
-// Registers: 640 threads are launched with 96 each (61440); the split is
-// 256 x 112 + 256 x 104 + 128 x 48, the same sum.
-constexpr int kRegsFront = 112, kRegsBehind = 104, kRegsRest = 48;
-static_assert(256 * kRegsFront + 256 * kRegsBehind + 128 * kRegsRest <= kStateThreads * 96, "registers");
+constexpr int kStateThreads = 896;      // 2 warpgroups in front, 4 behind, 4 single warps
+constexpr int kBehind = 512;
+// Registers: 896 threads are launched with 72 each (64512).
+constexpr int kRegsFront = 96, kRegsBehind = 64, kRegsRest = 48;
+static_assert(256 * kRegsFront + kBehind * kRegsBehind + 128 * kRegsRest <= kStateThreads * 72, "registers");
 constexpr int kBC = kQ * kSsmN * 2;     // bytes of the B (or C) tile
 constexpr int kXT = kQ * kSsmP * 2;     // ... of one head's x (or z) tile
 
 struct StateSmem {
-  static constexpr int kBuf = 2 * kBC + 2 * kXT;  // B, C (later z, then out, of both heads), x of both heads
-  static constexpr int kH = 2 * kBuf;             // bf16 H of both heads: [2][n / 64][64 rows of 128 B]
+  // One B; x of two chunks (both heads); three tiles that C and z take turns
+  // with: C_0, z_0, C_1, ...  C's tile is free once its two products are done,
+  // z's once the output has left it (z becomes out in place), so that z is
+  // there a chunk before it is needed and neither waits for the other.
+  static constexpr int kB = 0;
+  static constexpr int kX = kB + kBC;
+  static constexpr int kRing = kX + 2 * 2 * kXT;
+  static constexpr int kH = kRing + 3 * kBC;      // bf16 H of both heads: [2][n / 64][64 rows of 128 B]
   static constexpr int kV = kH + 2 * kXT;         // [head][128] log2 dt_j - (the decays behind j, to the chunk's end)
   static constexpr int kU = kV + 2 * kQ * 4;      // [head][96] dt_j 2^-(the decays behind j in its 32 tokens)
   static constexpr int kW = kU + 2 * 96 * 4;      // [head][128] w_j
   static constexpr int kTot = kW + 2 * kQ * 4;    // [in front, behind][head][32 tokens] sums of decays
-  static constexpr int kBad = kTot + 2 * 2 * 4 * 4;  // [chunk % 4] bit head * 4 + warp: an x that is not finite
-  static constexpr int kBars = kBad + 4 * 4;
+  static constexpr int kBad = kTot + 2 * 2 * 4 * 4;  // byte chunk % 4, bit head * 4 + warp: an x that is not finite
+  static constexpr int kMisc = kBad + 4;          // TMEM's address
+  static constexpr int kBars = kMisc + 4;
   enum {
-    kFull = 0,             // B and x
-    kEmpty = kFull + 2,
-    kCFull = kEmpty + 2,   // C
-    kCEmpty = kCFull + 2,  // ... and the z and out that follow it
-    kZFull = kCEmpty + 2,
-    kG,
+    kBFull = 0,
+    kBEmpty,
+    kXFull,
+    kXEmpty = kXFull + 2,
+    kCFull = kXEmpty + 2,
+    kZFull = kCFull + 2,
+    kOut = kZFull + 2,  // the output has left z's tile
+    kG = kOut + 2,
     kY2,
-    kHFull,
+    kHFull = kY2 + 2,
     kMFull,
-    kYFull = kMFull + 2,
+    kYFull,
     kYFree = kYFull + 2,
     kWx,
     kS,
     kDone,
     kCount
   };
-  static constexpr int kMisc = kBars + kCount * 8;
-  static constexpr int kTotal = kMisc + 16;
+  static constexpr int kTotal = kBars + kCount * 8;
 };
 static_assert(StateSmem::kTotal <= 232448, "the chunked state form does not fit shared memory");
 
@@ -157,14 +165,14 @@ __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 // Rows that no tensor map can describe (a stride that is no multiple of 16
-// bytes) are copied by the 256 threads behind, 8 bytes at a time: 128 tokens x
+// bytes) are copied by the 512 threads behind, 8 bytes at a time: 128 tokens x
 // kCols values at column `col` of the rows from row0 on, as the same 128-byte
 // swizzled blocks of 64 columns.  Rows from n on repeat row n - 1.
 template <int kCols>
 __device__ __forceinline__ void copy_tile(uint32_t dst, const uint16_t* zx, long long stride, int col, size_t row0, int n) {
   constexpr int kPer = kCols * 2 / 8;  // pieces of a row
 #pragma unroll 4
-  for (int q = threadIdx.x & 255; q < kQ * kPer; q += 256) {
+  for (int q = (int)threadIdx.x - 256; q < kQ * kPer; q += kBehind) {
     const int r = q / kPer, b = (q % kPer) * 8, blk = b >> 7, c = (b >> 4) & 7;
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst + blk * (kQ * 128) + r * 128 + ((c ^ (r & 7)) << 4) + (b & 15)),
                  "l"(zx + (row0 + min(r, n - 1)) * stride + col + b / 2)
@@ -232,23 +240,25 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
     return;
   }
 
-  if (warp == 16) {
+  if (warp == 24) {
     if (lane == 0) {
-      const int copies = p.tiled ? 1 : 256;
+      const int copies = p.tiled ? 1 : kBehind;
       for (int b = 0; b < 2; ++b) {
-        mbar_init(bar(L::kFull + b), copies);
-        mbar_init(bar(L::kEmpty + b), 1);
+        mbar_init(bar(L::kXFull + b), copies);
+        mbar_init(bar(L::kXEmpty + b), 1);
         mbar_init(bar(L::kCFull + b), copies);
-        mbar_init(bar(L::kCEmpty + b), 256);
-        mbar_init(bar(L::kMFull + b), 128);
+        mbar_init(bar(L::kZFull + b), copies);
+        mbar_init(bar(L::kOut + b), kBehind);
+        mbar_init(bar(L::kY2 + b), 1);
         mbar_init(bar(L::kYFull + b), 1);
       }
-      mbar_init(bar(L::kZFull), copies);
+      mbar_init(bar(L::kBFull), copies);
+      mbar_init(bar(L::kBEmpty), 1);
+      mbar_init(bar(L::kMFull), 256);
       mbar_init(bar(L::kG), 1);
-      mbar_init(bar(L::kY2), 1);
       mbar_init(bar(L::kHFull), 256);
-      mbar_init(bar(L::kYFree), 256);
-      mbar_init(bar(L::kWx), 256);
+      mbar_init(bar(L::kYFree), kBehind);
+      mbar_init(bar(L::kWx), kBehind);
       mbar_init(bar(L::kS), 1);
       mbar_init(bar(L::kDone), 1);
       fence_mbar_init();
@@ -258,7 +268,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
     tmem_alloc(smem_u32(tmem_word), 512);
     tmem_relinquish();
   }
-  if (threadIdx.x < 4) ((uint32_t*)(smem + L::kBad))[threadIdx.x] = 0;
+  if (threadIdx.x == 0) *(uint32_t*)(smem + L::kBad) = 0;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -271,10 +281,11 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
   auto wait_warp = [&](int b, uint32_t parity) {
     if (ok) ok = __all_sync(0xffffffffu, wait_bar(bar(b), parity, p.sink));
   };
-  auto wait = [&](int b, uint32_t parity) { return ok = wait_bar(bar(b), parity, p.sink); };
+  auto c_tile = [&](int c) { return L::kRing + (2 * c) % 3 * kBC; };
+  auto z_tile = [&](int c) { return L::kRing + (2 * c + 1) % 3 * kBC; };
   const int h = (warp >> 2) & 1, quad = warp & 3, row = quad * 32 + lane;  // a thread per token of head h0 + h
   const uint32_t lanes = (uint32_t)(quad * 32) << 16;
-  const int hh = row >> 6, pp = row & 63;  // for the state: row (head hh, p), half h of the columns or tokens
+  const int hh = row >> 6, pp = row & 63;  // for the state: row (head hh, p)
   const int head = h0 + h;
   float* sv = (float*)(smem + L::kV);
   float* su = (float*)(smem + L::kU);
@@ -285,8 +296,8 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
   // the sum of all 32 for the others.  Summed from the end: the state's newest
   // tokens are exact to fp32 whatever the sum over the chunk is.
   const uint16_t* dt_col = p.zx + first * p.zx_stride + 2 * di + 2 * kSsmN + head;
-  const float rate = warp < 16 ? ex2(bf(p.prm[head]) * 1.44269504088896340736f) * 1.44269504088896340736f : 0.f;
-  const float bias = warp < 16 ? bf(p.prm[p.Hs + head]) : 0.f;
+  const float rate = warp < 24 ? ex2(bf(p.prm[head]) * 1.44269504088896340736f) * 1.44269504088896340736f : 0.f;
+  const float bias = warp < 24 ? bf(p.prm[p.Hs + head]) : 0.f;
   auto dt_at = [&](int c) { return c * kQ + row < len ? dt_col[(size_t)(c * kQ + row) * p.zx_stride] : (uint16_t)0; };
   auto decays = [&](int c, uint16_t raw, float& dt, float& inner) {
     dt = c * kQ + row < len ? softplus(bf(raw) + bias) : 0.f;
@@ -367,70 +378,69 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
       // ---- M, over G once both heads have read G
       wait_warp(L::kG, c & 1);
       tc_fence_after();
-      // 32 tokens at a time, from the diagonal down: m[16 t ..] is block quad - t
-      uint32_t m[64];
-      {
-        // on the diagonal; D x_i is added to y_i as D on the diagonal
-        uint32_t g[32];
-        tmem_ld32(tmem + kTG + lanes + 32 * quad, g);
-        const float2 ai = make_float2(after, after);
-        const float4* vj = (const float4*)(sv + h * kQ + 32 * quad);
-        tmem_ld_wait();
+      // Tokens 64..127 first, then 0..63: once both heads have read that half
+      // of G, its 64 columns take the same half of both heads' M.
+#pragma unroll 1
+      for (int half = 1; half >= 0; --half) {
+        uint32_t m[32];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float4 v4 = vj[e];
-          const float2 t0 = add2(make_float2(v4.x, v4.y), ai), t1 = add2(make_float2(v4.z, v4.w), ai);
-          const float2 m0 = mul2(make_float2(__uint_as_float(g[4 * e]), __uint_as_float(g[4 * e + 1])),
-                                 make_float2(ex2(t0.x), ex2(t0.y)));
-          const float2 m1 = mul2(make_float2(__uint_as_float(g[4 * e + 2]), __uint_as_float(g[4 * e + 3])),
-                                 make_float2(ex2(t1.x), ex2(t1.y)));
-          float f[4] = {m0.x, m0.y, m1.x, m1.y};
+        for (int t = 0; t < 2; ++t) {
+          const int q = 2 * half + t;  // 32 tokens
+          if (q > quad) {              // above the diagonal
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (4 * e + k > lane) f[k] = 0.f;
-            if (4 * e + k == lane) f[k] += skip;
+            for (int e = 0; e < 16; ++e) m[16 * t + e] = 0;
+            continue;
           }
-          m[2 * e] = pack_bf16(f[0], f[1]);
-          m[2 * e + 1] = pack_bf16(f[2], f[3]);
-        }
-      }
+          uint32_t g[32];
+          tmem_ld32(tmem + kTG + lanes + 32 * q, g);
+          if (q < quad) {
+            // below: the decay from the end of token j's 32 to i is a factor
+            // of the row, that from j to there is in u_j
+            const float r = ex2(after - (q == 0 ? end[0] : q == 1 ? end[1] : end[2]));
+            const float2 r2 = make_float2(r, r);
+            const float4* uj = (const float4*)(su + h * 96 + 32 * q);
+            tmem_ld_wait();
 #pragma unroll
-      for (int t = 1; t < 4; ++t) {
-        if (t > quad) continue;
-        // below: the decay from the end of token j's block to i is a factor
-        // of the row, that from j to there is in u_j
-        const int q = quad - t;
-        uint32_t g[32];
-        tmem_ld32(tmem + kTG + lanes + 32 * q, g);
-        const float r = ex2(after - (q == 0 ? end[0] : q == 1 ? end[1] : end[2]));
-        const float2 r2 = make_float2(r, r);
-        const float4* uj = (const float4*)(su + h * 96 + 32 * q);
-        tmem_ld_wait();
+            for (int e = 0; e < 8; ++e) {
+              const float4 u4 = uj[e];
+              const float2 m0 = mul2(mul2(make_float2(__uint_as_float(g[4 * e]), __uint_as_float(g[4 * e + 1])), r2),
+                                     make_float2(u4.x, u4.y));
+              const float2 m1 = mul2(mul2(make_float2(__uint_as_float(g[4 * e + 2]), __uint_as_float(g[4 * e + 3])), r2),
+                                     make_float2(u4.z, u4.w));
+              m[16 * t + 2 * e] = pack_bf16(m0.x, m0.y);
+              m[16 * t + 2 * e + 1] = pack_bf16(m1.x, m1.y);
+            }
+          } else {
+            // on it; D x_i is added to y_i as D on the diagonal
+            const float2 ai = make_float2(after, after);
+            const float4* vj = (const float4*)(sv + h * kQ + 32 * q);
+            tmem_ld_wait();
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float4 u4 = uj[e];
-          const float2 m0 = mul2(mul2(make_float2(__uint_as_float(g[4 * e]), __uint_as_float(g[4 * e + 1])), r2),
-                                 make_float2(u4.x, u4.y));
-          const float2 m1 = mul2(mul2(make_float2(__uint_as_float(g[4 * e + 2]), __uint_as_float(g[4 * e + 3])), r2),
-                                 make_float2(u4.z, u4.w));
-          m[16 * t + 2 * e] = pack_bf16(m0.x, m0.y);
-          m[16 * t + 2 * e + 1] = pack_bf16(m1.x, m1.y);
-        }
-      }
-      tc_fence_before();
-      bar_sync(1, 256);  // both heads have read G
-      tc_fence_after();
+            for (int e = 0; e < 8; ++e) {
+              const float4 v4 = vj[e];
+              const float2 t0 = add2(make_float2(v4.x, v4.y), ai), t1 = add2(make_float2(v4.z, v4.w), ai);
+              const float2 m0 = mul2(make_float2(__uint_as_float(g[4 * e]), __uint_as_float(g[4 * e + 1])),
+                                     make_float2(ex2(t0.x), ex2(t0.y)));
+              const float2 m1 = mul2(make_float2(__uint_as_float(g[4 * e + 2]), __uint_as_float(g[4 * e + 3])),
+                                     make_float2(ex2(t1.x), ex2(t1.y)));
+              float f[4] = {m0.x, m0.y, m1.x, m1.y};
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        if (t <= quad) {
-          tmem_st16(tmem + kTG + h * 64 + lanes + 16 * (quad - t), m + 16 * t);
-        } else {  // above the diagonal
-          uint32_t none[16] = {};
-          tmem_st16(tmem + kTG + h * 64 + lanes + 16 * t, none);
+              for (int k = 0; k < 4; ++k) {
+                if (4 * e + k > lane) f[k] = 0.f;
+                if (4 * e + k == lane) f[k] += skip;
+              }
+              m[16 * t + 2 * e] = pack_bf16(f[0], f[1]);
+              m[16 * t + 2 * e + 1] = pack_bf16(f[2], f[3]);
+            }
+          }
         }
+        tc_fence_before();
+        bar_sync(1, 256);  // both heads have read this half of G
+        tc_fence_after();
+        tmem_st32(tmem + kTG + half * 64 + h * 32 + lanes, m);
       }
       // ---- C H^T, scaled in place: M X is added to it
-      wait_warp(L::kY2, c & 1);
+      wait_warp(L::kY2 + (c & 1), (c >> 1) & 1);
       tc_fence_after();
       if (!zero) {
         const float ei = ex2(after - last);
@@ -445,7 +455,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
       }
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(bar(L::kMFull + h));
+      mbar_arrive(bar(L::kMFull));
     }
     // ---- the state after the last token
     wait_warp(L::kS, (chunks - 1) & 1);
@@ -461,66 +471,69 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
         dst[e] = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]), __uint_as_float(v[4 * e + 2]),
                              __uint_as_float(v[4 * e + 3]));
     }
-  } else if (warp < 16) {
+  } else if (warp < 24) {
     // ---------------------------------------------------------------- behind
-    regs_take<kRegsBehind>();
+    regs_give<kRegsBehind>();
+    const int part = (warp - 8) >> 2, half = part >> 1;  // 32 tokens of (w X)^T; half of a token's values
+    const int at0 = half * 4;                            // the first of this half's 16-byte pieces (before the swizzle)
     // (w X)^T of a chunk is made before the output of the chunk before it: the
     // state's product does not wait for the gate
     uint16_t dt_next = dt_at(0);
     for (int c = -1; c < chunks; ++c) {
       if (c + 1 < chunks) {
         const int k = c + 1, b = k & 1, left = len - k * kQ;
-        uint8_t* buf = smem + b * L::kBuf;
         // ---- this token's x and B.  Behind the sequence's end lie other rows:
         // theirs become zero.  An x that is not finite would reach earlier
         // tokens as 0 * NaN in M X: it is noted here, becomes zero once the
         // state's weights have been made of it, and is put back at the output.
+        const uint32_t parity = (k >> 1) & 1;
         if (!p.tiled) {
           const size_t row0 = first + (size_t)k * kQ;
           const int n = min(kQ, left);
-          wait_warp(L::kEmpty + b, ((k >> 1) & 1) ^ 1);
-          wait_warp(L::kCEmpty + b, ((k >> 1) & 1) ^ 1);
-          copy_tile<2 * kSsmN>(sb + b * L::kBuf, p.zx, p.zx_stride, 2 * di, row0, n);  // B, then C
-          copy_tile<2 * kSsmP>(sb + b * L::kBuf + 2 * kBC, p.zx, p.zx_stride, di + h0 * kSsmP, row0, n);
+          wait_warp(L::kXEmpty + b, parity ^ 1);
+          copy_tile<2 * kSsmP>(sb + L::kX + b * 2 * kXT, p.zx, p.zx_stride, di + h0 * kSsmP, row0, n);
+          wait_warp(L::kOut + b, parity ^ 1);
+          copy_tile<kSsmN>(sb + c_tile(k), p.zx, p.zx_stride, 2 * di + kSsmN, row0, n);
+          wait_warp(L::kBEmpty, (k & 1) ^ 1);
+          copy_tile<kSsmN>(sb + L::kB, p.zx, p.zx_stride, 2 * di, row0, n);
           asm volatile("cp.async.wait_all;" ::: "memory");
           fence_proxy_async_smem();
-          mbar_arrive(bar(L::kFull + b));
+          mbar_arrive(bar(L::kXFull + b));
           mbar_arrive(bar(L::kCFull + b));
+          mbar_arrive(bar(L::kBFull));
         }
         float dt, inner;
-        const float sum = decays(k, dt_next, dt, inner);
-        dt_next = dt_at(k + 1);
         float* tot = (float*)(smem + L::kTot) + 8;
-        if (lane == 0) tot[h * 4 + quad] = sum;
-        wait_warp(L::kFull + b, (k >> 1) & 1);
-        uint8_t* xrow = buf + 2 * kBC + h * kXT + row * 128;
+        if (half == 0) {
+          const float sum = decays(k, dt_next, dt, inner);
+          dt_next = dt_at(k + 1);
+          if (lane == 0) tot[h * 4 + quad] = sum;
+        }
+        wait_warp(L::kXFull + b, parity);
+        uint8_t* xrow = smem + L::kX + (b * 2 + h) * kXT + row * 128;
         bool odd = false;
         if (row >= left) {
-          uint8_t* brow = buf + h * (kQ * 128) + row * 128;
-#pragma unroll 4
-          for (int e = 0; e < 8; ++e) {
-            *(uint4*)(xrow + (e << 4)) = make_uint4(0, 0, 0, 0);
-            *(uint4*)(brow + (e << 4)) = make_uint4(0, 0, 0, 0);
-          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) *(uint4*)(xrow + ((at0 + e) << 4)) = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
         } else {
           uint32_t acc[2] = {0, 0};
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint4 x = *(const uint4*)(xrow + ((e ^ (lane & 7)) << 4));
+          for (int e = 0; e < 4; ++e) {
+            const uint4 x = *(const uint4*)(xrow + (((at0 + e) ^ (row & 7)) << 4));
             asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[0]) : "r"(x.x), "r"(0));
             asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[1]) : "r"(x.y), "r"(0));
             asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[0]) : "r"(x.z), "r"(0));
             asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[1]) : "r"(x.w), "r"(0));
           }
           odd = ((acc[0] | acc[1]) & 0x7fff7fffu) != 0;
-          if (odd) atomicOr(&sbad[k & 3], 1u << (h * 4 + quad));
+          if (odd) atomicOr(sbad, 1u << ((k & 3) * 8 + h * 4 + quad));
         }
-        bar_sync(4, 256);  // x and its flags are complete; every thread here is done with chunk k - 2
+        bar_sync(4, kBehind);  // x and its flags are complete; every thread here is done with chunk k - 2
         // cleared two chunks ahead: nobody sets these before the next barrier
-        if ((threadIdx.x & 255) == 0) sbad[(k + 2) & 3] = 0;
-        // ---- (w X)^T: row (hh, pp), tokens 64 h .. 64 h + 63
-        {
+        if (threadIdx.x == 256) atomicAnd(sbad, ~(0xFFu << (((k + 2) & 3) * 8)));
+        // ---- (w X)^T: row (hh, pp), tokens 32 part .. 32 part + 31
+        if (half == 0) {
           float after = inner;
 #pragma unroll
           for (int q = 1; q < 4; ++q)
@@ -528,12 +541,21 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
           sw[h * kQ + row] = dt * ex2(-after);
         }
         if (k > 0) wait_warp(L::kS, (k - 1) & 1);
-        bar_sync(4, 256);  // sw is complete
+        if (left < kQ) {  // B's phase before this one is over: the last state has been made of it
+          wait_warp(L::kBFull, k & 1);
+          if (row >= left) {
+            uint8_t* brow = smem + L::kB + h * (kQ * 128) + row * 128;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) *(uint4*)(brow + ((at0 + e) << 4)) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+          }
+        }
+        bar_sync(4, kBehind);  // sw is complete
         tc_fence_after();
-        const uint8_t* xt = buf + 2 * kBC + hh * kXT + (pp & 7) * 2;
+        const uint8_t* xt = smem + L::kX + (b * 2 + hh) * kXT + (pp & 7) * 2;
 #pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-          const int j0 = h * 64 + 16 * q;
+        for (int q = 0; q < 2; ++q) {
+          const int j0 = part * 32 + 16 * q;
           float v[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e)  // j0 is a multiple of 8
@@ -554,16 +576,16 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
                                   make_float2(__uint_as_float(hi[e] << 16), __uint_as_float(hi[e] & 0xFFFF0000u)));
             lo[e] = pack_bf16(r.x, r.y);
           }
-          tmem_st8(tmem + kTWx + lanes + h * 32 + q * 8, hi);
-          tmem_st8(tmem + kTWx + 64 + lanes + h * 32 + q * 8, lo);
+          tmem_st8(tmem + kTWx + lanes + part * 16 + q * 8, hi);
+          tmem_st8(tmem + kTWx + 64 + lanes + part * 16 + q * 8, lo);
         }
         tmem_st_wait();
-        if (sbad[k & 3]) {  // seen by every thread or none
-          bar_sync(4, 256);
+        if (*(volatile uint32_t*)sbad >> ((k & 3) * 8) & 0xFFu) {  // seen by every thread or none
+          bar_sync(4, kBehind);
           if (odd) {
 #pragma unroll 1
-            for (int e = 0; e < 64; ++e) {
-              uint16_t* x = (uint16_t*)xrow + e;
+            for (int e = 0; e < 32; ++e) {
+              uint16_t* x = (uint16_t*)(xrow + (((at0 + (e >> 3)) ^ (row & 7)) << 4)) + (e & 7);
               if ((*x & 0x7F80) == 0x7F80) *x = 0;
             }
             fence_proxy_async_smem();
@@ -574,87 +596,82 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
       }
       if (c < 0) continue;
       const int b = c & 1, left = len - c * kQ;
-      uint8_t* buf = smem + b * L::kBuf;
       // ---- the output: y, gated, over z's row and from there to global
-      uint8_t* ztile = buf + kBC + h * kXT;
-      const uint32_t any_bad = sbad[c & 3] >> (h * 4) & 15u;
+      uint8_t* ztile = smem + z_tile(c) + h * kXT;
+      const uint32_t any_bad = *(volatile uint32_t*)sbad >> ((c & 3) * 8 + h * 4) & 15u;
       if (!p.tiled) {
-        wait_warp(L::kY2, c & 1);
-        copy_tile<2 * kSsmP>(sb + b * L::kBuf + kBC, p.zx, p.zx_stride, h0 * kSsmP, first + (size_t)c * kQ, min(kQ, left));
+        if (c > 0) wait_warp(L::kY2 + ((c - 1) & 1), ((c - 1) >> 1) & 1);
+        copy_tile<2 * kSsmP>(sb + z_tile(c), p.zx, p.zx_stride, h0 * kSsmP, first + (size_t)c * kQ, min(kQ, left));
         asm volatile("cp.async.wait_all;" ::: "memory");
-        mbar_arrive(bar(L::kZFull));
+        mbar_arrive(bar(L::kZFull + b));
       }
-      wait_warp(L::kZFull, c & 1);
+      wait_warp(L::kZFull + b, (c >> 1) & 1);
       wait_warp(L::kYFull + h, c & 1);
       tc_fence_after();
       uint8_t* zrow = ztile + row * 128;
-#pragma unroll 1
-      for (int q = 0; q < 4; ++q) {
-        uint32_t y[16];
-        tmem_ld16_nowait(tmem + kTY + h * 64 + lanes + 16 * q, y);
-        uint4 zv[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) zv[e] = *(const uint4*)(zrow + (((q * 2 + e) ^ (row & 7)) << 4));
-        tmem_ld_wait();
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t zw[4] = {zv[e].x, zv[e].y, zv[e].z, zv[e].w};
-          uint32_t o[4];
-#pragma unroll
-          for (int f = 0; f < 4; ++f) {
-            const int i = 8 * e + 2 * f;
-            const float2 z2 = make_float2(__uint_as_float(zw[f] << 16), __uint_as_float(zw[f] & 0xFFFF0000u));
-            const float2 t = mul2(z2, make_float2(-1.44269504088896340736f, -1.44269504088896340736f));
-            const float2 d = add2(make_float2(ex2(t.x), ex2(t.y)), make_float2(1.f, 1.f));
-            const float2 g = mul2(z2, make_float2(rcp(d.x), rcp(d.y)));
-            const float2 r = mul2(make_float2(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), g);
-            o[f] = pack_bf16(r.x, r.y);
-          }
-          *(uint4*)(zrow + (((q * 2 + e) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-        }
-      }
+      uint32_t y[32];
+      tmem_ld32(tmem + kTY + h * 64 + lanes + 32 * half, y);
+      tmem_ld_wait();
       tc_fence_before();
       mbar_arrive(bar(L::kYFree));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint4* zp = (uint4*)(zrow + (((at0 + e) ^ (row & 7)) << 4));
+        const uint4 zv = *zp;
+        const uint32_t zw[4] = {zv.x, zv.y, zv.z, zv.w};
+        uint32_t o[4];
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+          const int i = 8 * e + 2 * f;
+          const float2 z2 = make_float2(__uint_as_float(zw[f] << 16), __uint_as_float(zw[f] & 0xFFFF0000u));
+          const float2 t = mul2(z2, make_float2(-1.44269504088896340736f, -1.44269504088896340736f));
+          const float2 d = add2(make_float2(ex2(t.x), ex2(t.y)), make_float2(1.f, 1.f));
+          const float2 g = mul2(z2, make_float2(rcp(d.x), rcp(d.y)));
+          const float2 r = mul2(make_float2(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), g);
+          o[f] = pack_bf16(r.x, r.y);
+        }
+        *zp = make_uint4(o[0], o[1], o[2], o[3]);
+      }
       if (any_bad) {  // tokens up to this one whose x is not finite
 #pragma unroll 1
         for (int j = 0; j <= row && j < left; ++j) {
           if (!(any_bad >> (j >> 5) & 1)) continue;
           const uint16_t* x = p.zx + (first + (size_t)c * kQ + j) * p.zx_stride + di + head * kSsmP;
 #pragma unroll 1
-          for (int e = 0; e < 64; ++e)
+          for (int e = half * 32; e < half * 32 + 32; ++e)
             if ((x[e] & 0x7F80) == 0x7F80) *(uint16_t*)(zrow + (((e >> 3) ^ (row & 7)) << 4) + (e & 7) * 2) = 0x7FC0;
         }
       }
       __syncwarp();
       {
-        const int r0 = quad * 32 + (lane >> 3), at = lane & 7;  // four rows at a time
+        const int r0 = quad * 32 + (lane >> 2), at = at0 + (lane & 3);  // eight rows at a time
         uint16_t* dst = p.out + (first + (size_t)c * kQ + r0) * p.out_stride + head * kSsmP + at * 8;
-#pragma unroll 4
-        for (int q = 0; q < 8; ++q, dst += 4 * p.out_stride) {
-          const int r = r0 + 4 * q;
+#pragma unroll
+        for (int q = 0; q < 4; ++q, dst += 8 * p.out_stride) {
+          const int r = r0 + 8 * q;
           const uint4 v = *(const uint4*)(ztile + r * 128 + ((at ^ (r & 7)) << 4));
           if (r < left) *(uint4*)dst = v;
         }
       }
       fence_proxy_async_smem();  // the next copies into this buffer come by the async proxy
-      mbar_arrive(bar(L::kCEmpty + b));
+      mbar_arrive(bar(L::kOut + b));
     }
   } else {
     regs_give<kRegsRest>();
-    if (warp == 16) {
+    if (warp == 24) {
       // ---------------------------------------------------------------- MMAs
       constexpr uint32_t id_g = idesc_16(128, 128, false, false, false), id_y2 = idesc_16(128, 64, false, false, false),
                          id_y = idesc_16(128, 64, false, false, true), id_s = idesc_16(128, 128, false, false, true);
       constexpr uint32_t kBlk = (kQ * 128) >> 4;  // the next 64 columns of a tile, as a descriptor counts
       for (int c = 0; c < chunks; ++c) {
-        const uint32_t buf = sb + (c & 1) * L::kBuf;
+        const uint32_t ct = sb + c_tile(c), bt = sb + L::kB;
         const bool zero = c == 0 && !goes_on;
-        wait_warp(L::kFull + (c & 1), (c >> 1) & 1);
+        wait_warp(L::kBFull, c & 1);
         wait_warp(L::kCFull + (c & 1), (c >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {  // G = C B^T
-          const uint32_t cm = sdesc_lo(buf + kBC), bm = sdesc_lo(buf);
+          const uint32_t cm = sdesc_lo(ct), bm = sdesc_lo(bt);
           mma_ss<false>(tmem + kTG, cm, bm, id_g);
 #pragma unroll
           for (int e = 1; e < 8; ++e)
@@ -667,11 +684,12 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {  // the state += (w X)^T B: the high parts, then the remainders
-          const uint32_t bm = sdesc_lo(buf, kQ * 128);
+          const uint32_t bm = sdesc_lo(bt, kQ * 128);
 #pragma unroll
           for (int e = 0; e < 16; ++e)
             mma_ts(tmem + kTState, tmem + kTWx + 8 * e, bm + (e % 8) * (2048 >> 4), id_s, e > 0 ? 1u : zero ? 0u : 1u);
           tc_commit(bar(L::kS));
+          tc_commit(bar(L::kBEmpty));
         }
         __syncwarp();
         if (c > 0) wait_warp(L::kYFree, (c - 1) & 1);
@@ -679,7 +697,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
         tc_fence_after();
         if (elect_one()) {  // Y = C H^T
           if (!zero) {
-            const uint32_t cm = sdesc_lo(buf + kBC), hm = sdesc_lo(sb + L::kH);
+            const uint32_t cm = sdesc_lo(ct), hm = sdesc_lo(sb + L::kH);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
               mma_ss<false>(tmem + kTY + h * 64, cm, hm + h * (kXT >> 4), id_y2);
@@ -689,24 +707,25 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
                              hm + ((h * kXT + (e / 4) * (64 * 128)) >> 4) + (e % 4) * 2, id_y2);
             }
           }
-          tc_commit(bar(L::kY2));
+          tc_commit(bar(L::kY2 + (c & 1)));
         }
         __syncwarp();
+        wait_warp(L::kMFull, c & 1);
+        if (!ok) break;
+        tc_fence_after();
 #pragma unroll
         for (int h = 0; h < 2; ++h) {  // Y += M X
-          wait_warp(L::kMFull + h, c & 1);
-          tc_fence_after();
-          if (ok && elect_one()) {
-            const uint32_t xm = sdesc_lo(buf + 2 * kBC + h * kXT, kQ * 128);
+          if (elect_one()) {
+            const uint32_t xm = sdesc_lo(sb + L::kX + ((c & 1) * 2 + h) * kXT, kQ * 128);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-              mma_ts(tmem + kTY + h * 64, tmem + kTG + h * 64 + 8 * e, xm + e * (2048 >> 4), id_y, e > 0 ? 1u : zero ? 0u : 1u);
+              mma_ts(tmem + kTY + h * 64, tmem + kTG + (e / 4) * 64 + h * 32 + (e % 4) * 8, xm + e * (2048 >> 4), id_y,
+                     e > 0 ? 1u : zero ? 0u : 1u);
             tc_commit(bar(L::kYFull + h));
           }
           __syncwarp();
         }
-        if (!ok) break;
-        if (elect_one()) tc_commit(bar(L::kEmpty + (c & 1)));
+        if (elect_one()) tc_commit(bar(L::kXEmpty + (c & 1)));
         __syncwarp();
       }
       if (!ok) {  // give-up: wait (bounded) for the MMAs issued so far
@@ -716,56 +735,47 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
         }
       }
       __syncwarp();
-    } else if (warp == 17) {
-      // ------------------------------------------------ copies of B, C and x
-      if (p.tiled) {
-        if (lane == 0) {
-          int c = 0;
-          for (; c < chunks; ++c) {
-            const uint32_t buf = sb + (c & 1) * L::kBuf, fb = bar(L::kFull + (c & 1)), fc = bar(L::kCFull + (c & 1));
-            const uint32_t parity = ((c >> 1) & 1) ^ 1;
-            const int r = (int)first + c * kQ;
-            if (!wait(L::kEmpty + (c & 1), parity)) break;
-            mbar_arrive_expect_tx(fb, kBC + 2 * kXT);
-            tma_load_3d_plain(buf, &p.tm, 2 * di, 0, r, fb);
-            tma_load_3d_plain(buf + kQ * 128, &p.tm, 2 * di + 64, 0, r, fb);
-            tma_load_3d_plain(buf + 2 * kBC, &p.tm, di + h0 * kSsmP, 0, r, fb);
-            tma_load_3d_plain(buf + 2 * kBC + kXT, &p.tm, di + (h0 + 1) * kSsmP, 0, r, fb);
-            if (!wait(L::kCEmpty + (c & 1), parity)) {
-              ++c;
-              break;
-            }
-            mbar_arrive_expect_tx(fc, kBC);
-            tma_load_3d_plain(buf + kBC, &p.tm, 2 * di + kSsmN, 0, r, fc);
-            tma_load_3d_plain(buf + kBC + kQ * 128, &p.tm, 2 * di + kSsmN + 64, 0, r, fc);
-          }
-          if (!ok)  // give-up: the copies in flight land before the shared memory is left
-            for (int i = max(0, c - 2); i < c; ++i) {
-              for (int n = 0; n < (1 << 20) && !mbar_try_wait(bar(L::kFull + (i & 1)), (i >> 1) & 1); ++n) {
-              }
-              for (int n = 0; n < (1 << 12) && !mbar_try_wait(bar(L::kCFull + (i & 1)), (i >> 1) & 1); ++n) {
-              }
-            }
+    } else if (p.tiled) {
+      // -------------------------- copies by tensor maps: x and C, z, B, a warp each
+      const int col = warp == 25 ? di + h0 * kSsmP : warp == 26 ? h0 * kSsmP : 2 * di;
+      auto copy = [&](uint32_t dst, int column, int c, int b) {  // two blocks of 64 columns
+        if (elect_one()) {
+          mbar_arrive_expect_tx(bar(b), kBC);
+          tma_load_3d_plain(dst, &p.tm, column, 0, (int)first + c * kQ, bar(b));
+          tma_load_3d_plain(dst + kQ * 128, &p.tm, column + 64, 0, (int)first + c * kQ, bar(b));
+        }
+        __syncwarp();
+      };
+      int c = 0;
+      for (; c < chunks; ++c) {
+        const uint32_t parity = ((c >> 1) & 1) ^ 1;
+        if (warp == 25) {
+          wait_warp(L::kXEmpty + (c & 1), parity);
+          if (!ok) break;
+          copy(sb + L::kX + (c & 1) * 2 * kXT, col, c, L::kXFull + (c & 1));
+          wait_warp(L::kOut + (c & 1), parity);  // z of two chunks before
+          if (!ok) break;
+          copy(sb + c_tile(c), 2 * di + kSsmN, c, L::kCFull + (c & 1));
+        } else if (warp == 26) {
+          if (c > 0) wait_warp(L::kY2 + ((c - 1) & 1), ((c - 1) >> 1) & 1);  // C of the chunk before
+          if (!ok) break;
+          copy(sb + z_tile(c), col, c, L::kZFull + (c & 1));
+        } else {
+          wait_warp(L::kBEmpty, (c & 1) ^ 1);
+          if (!ok) break;
+          copy(sb + L::kB, col, c, L::kBFull);
         }
       }
-      __syncwarp();
-    } else if (warp == 18) {
-      // ---------------------------- copies of z, over C once its products are done
-      if (p.tiled) {
-        if (lane == 0) {
-          int c = 0;
-          for (; c < chunks; ++c) {
-            const uint32_t dst = sb + (c & 1) * L::kBuf + kBC;
-            const int r = (int)first + c * kQ;
-            if (!wait(L::kY2, c & 1)) break;
-            mbar_arrive_expect_tx(bar(L::kZFull), 2 * kXT);
-            tma_load_3d_plain(dst, &p.tm, h0 * kSsmP, 0, r, bar(L::kZFull));
-            tma_load_3d_plain(dst + kXT, &p.tm, (h0 + 1) * kSsmP, 0, r, bar(L::kZFull));
+      if (!ok) {  // give-up: the copies in flight land before the shared memory is left
+        const int from = max(0, c - 2);
+        for (int i = from; i <= c; ++i)
+          for (int n = 0; n < (1 << 12); ++n) {
+            const bool x = warp == 25 ? mbar_try_wait(bar(L::kXFull + (i & 1)), (i >> 1) & 1) &&
+                                            mbar_try_wait(bar(L::kCFull + (i & 1)), (i >> 1) & 1)
+                                      : warp == 26 ? mbar_try_wait(bar(L::kZFull + (i & 1)), (i >> 1) & 1)
+                                                   : mbar_try_wait(bar(L::kBFull), i & 1);
+            if (x) break;
           }
-          if (!ok && c > 0)
-            for (int n = 0; n < (1 << 20) && !mbar_try_wait(bar(L::kZFull), (c - 1) & 1); ++n) {
-            }
-        }
       }
       __syncwarp();
     }
@@ -773,7 +783,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 16) tmem_dealloc(tmem, 512);
+  if (warp == 24) tmem_dealloc(tmem, 512);
 }
 
 }  // namespace wave
