@@ -33,6 +33,7 @@ struct AttnParams {
   uint16_t* out;
   long long v_stride, out_stride;
   float scale2;                     // scale * log2(e)
+  int wide;                         // out's rows are 32-byte aligned
   ErrSink sink;
 };
 
@@ -146,7 +147,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __gr
       mbar_init(bar(L::kQEmpty), 1);
       for (int i = 0; i < 2; ++i) {
         mbar_init(bar(L::kSFull + i), 1);
-        mbar_init(bar(L::kPFull + i), 128);
+        mbar_init(bar(L::kPFull + i), 4);  // a stream's softmax warps
         mbar_init(bar(L::kOFull + i), 1);
         mbar_init(bar(L::kItemFull + i), 1);
         mbar_init(bar(L::kItemEmpty + i), 11);  // 8 softmax warps, copies, MMAs, guard
@@ -184,7 +185,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __gr
 
   if (warp < 8) {
     // ---------------------------------------------------------------- softmax
-    regs_take<216>();
+    regs_take<208>();
     const int st = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     uint32_t s_it = 0, o_it = 0;
@@ -211,7 +212,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __gr
 #pragma unroll
           for (int c = 0; c < 4; ++c) mx[c] = __uint_as_float(s[c]);
 #pragma unroll
-          for (int c = 4; c < 128; ++c) mx[c & 3] = fmaxf(mx[c & 3], __uint_as_float(s[c]));
+          for (int c = 4; c < 124; c += 8) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mx[i] = max3(mx[i], __uint_as_float(s[c + 2 * i]), __uint_as_float(s[c + 2 * i + 1]));
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], __uint_as_float(s[124 + i]));
           const float bm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
           // The maximum moves only when a weight would exceed 2^8 (the sums
           // and the 16-bit weights have room for that): O is rescaled seldom.
@@ -236,24 +242,26 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __gr
             }
           }
           const float neg = m == -INFINITY ? 0.f : -m * p.scale2;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          const float2 scale = make_float2(p.scale2, p.scale2), neg2 = make_float2(neg, neg);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             uint32_t w[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-              const float x = ex2(fmaf(__uint_as_float(s[64 * c + 2 * i]), p.scale2, neg));
-              const float y = ex2(fmaf(__uint_as_float(s[64 * c + 2 * i + 1]), p.scale2, neg));
-              sum[(2 * i) & 3] += x;
-              sum[(2 * i + 1) & 3] += y;
-              w[i] = pack16<kF16>(x, y);
+              const float2 t =
+                  fma2(make_float2(__uint_as_float(s[64 * c + 2 * i]), __uint_as_float(s[64 * c + 2 * i + 1])), scale, neg2);
+              const float2 e = make_float2(ex2(t.x), ex2(t.y));
+              sum[i & 1] = add2(sum[i & 1], e);
+              w[i] = pack16<kF16>(e.x, e.y);
             }
             tmem_st32(tS(st) + lanes + 32 * c, w);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           tmem_st_wait();
           tc_fence_before();
-          mbar_arrive(bar(L::kPFull + st));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::kPFull + st));
         }
         if (!ok || !wait_warp(L::kOFull + st, o_it & 1)) break;
         ++o_it;
@@ -286,14 +294,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __gr
                 }
           }
           if (st * kRows + row < it.left) {
+            uint32_t w[16];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint4 w;
-              w.x = pack16<kF16>(__uint_as_float(o[8 * i]) * inv, __uint_as_float(o[8 * i + 1]) * inv);
-              w.y = pack16<kF16>(__uint_as_float(o[8 * i + 2]) * inv, __uint_as_float(o[8 * i + 3]) * inv);
-              w.z = pack16<kF16>(__uint_as_float(o[8 * i + 4]) * inv, __uint_as_float(o[8 * i + 5]) * inv);
-              w.w = pack16<kF16>(__uint_as_float(o[8 * i + 6]) * inv, __uint_as_float(o[8 * i + 7]) * inv);
-              *(uint4*)(orow + 32 * c + 8 * i) = w;
+            for (int i = 0; i < 16; ++i) {
+              const float2 v = mul2(make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), make_float2(inv, inv));
+              w[i] = pack16<kF16>(v.x, v.y);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (p.wide)
+                store32(orow + 32 * c + 16 * i, w + 8 * i);
+              else
+#pragma unroll
+                for (int f = 0; f < 2; ++f)
+                  *(uint4*)(orow + 32 * c + 16 * i + 8 * f) =
+                      make_uint4(w[8 * i + 4 * f], w[8 * i + 4 * f + 1], w[8 * i + 4 * f + 2], w[8 * i + 4 * f + 3]);
             }
           }
           __syncwarp();
@@ -305,7 +320,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __gr
       if (!live) break;
     }
   } else {
-    regs_give<64>();
+    regs_give<80>();
     if (warp == 8) {
       // ------------------------------------------------------------- copies
       if (lane == 0) {
@@ -449,20 +464,25 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __gr
           if (!wait_warp(L::kGo, g_it & 1)) break;
           ++g_it;
           uint8_t* v = smem + L::kRing + ((it_r + 2 * j + 1) % L::kStages) * L::kTile;
-          uint32_t acc = 0;  // x * 0 is NaN exactly where x is not finite
-#pragma unroll 4
-          for (int o = lane * 16; o < L::kTile; o += 512) {
-            const uint4 x = *(const uint4*)(v + o);
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+          uint32_t acc[4] = {0, 0, 0, 0};  // x * 0 is NaN exactly where x is not finite
+#pragma unroll 1
+          for (int o = lane * 16; o < L::kTile; o += 8 * 512) {
+            uint4 x[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if constexpr (kF16)
-                asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(w[i]), "r"(0));
-              else
-                asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc) : "r"(w[i]), "r"(0));
+            for (int i = 0; i < 8; ++i) x[i] = *(const uint4*)(v + o + i * 512);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+              for (int f = 0; f < 4; ++f) {
+                if constexpr (kF16)
+                  asm("fma.rn.f16x2 %0, %1, %2, %0;" : "+r"(acc[f]) : "r"(w[f]), "r"(0));
+                else
+                  asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[f]) : "r"(w[f]), "r"(0));
+              }
             }
           }
-          if (__any_sync(0xffffffffu, (acc & 0x7fff7fffu) != 0)) {
+          if (__any_sync(0xffffffffu, (((acc[0] | acc[1]) | (acc[2] | acc[3])) & 0x7fff7fffu) != 0)) {
             constexpr uint32_t kExp = kF16 ? 0x7C00u : 0x7F80u;
             for (int o = lane * 4; o < L::kTile; o += 128) {
               uint32_t w = *(uint32_t*)(v + o);
@@ -573,6 +593,7 @@ extern "C" int wave_prompt_attention(wave_t* h, int n_seq, const int32_t* cu_seq
   p.out = (uint16_t*)out;
   p.v_stride = v_stride;
   p.out_stride = out_stride;
+  p.wide = ((uintptr_t)out & 31) == 0 && out_stride % 16 == 0;
   p.scale2 = scale * 1.44269504088896340736f;
   p.sink = make_sink(h->ws.err, h->err_host_dev, h->timeout_ns);
   cudaStream_t st = (cudaStream_t)stream;
