@@ -57,8 +57,8 @@ struct AttnSmem {
     kFull = 0,
     kEmpty = kFull + kStages,
     kQFull = kEmpty + kStages,
-    kQEmpty,
-    kSFull,
+    kQEmpty = kQFull + 2,
+    kSFull = kQEmpty + 2,
     kPFull = kSFull + 2,
     kOFull = kPFull + 2,
     kGo = kOFull + 2,
@@ -143,9 +143,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __gr
         mbar_init(bar(L::kFull + i), 1);
         mbar_init(bar(L::kEmpty + i), 1);
       }
-      mbar_init(bar(L::kQFull), 1);
-      mbar_init(bar(L::kQEmpty), 1);
       for (int i = 0; i < 2; ++i) {
+        mbar_init(bar(L::kQFull + i), 1);
+        mbar_init(bar(L::kQEmpty + i), 1);
         mbar_init(bar(L::kSFull + i), 1);
         mbar_init(bar(L::kPFull + i), 4);  // a stream's softmax warps
         mbar_init(bar(L::kOFull + i), 1);
@@ -329,25 +329,28 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __gr
 #pragma unroll
           for (int i = 0; i < D / 64; ++i) tma_load_3d_plain(dst + i * (kRows * 128), map, 64 * i, head, r, b);
         };
-        uint32_t q_it = 0;
+        uint32_t q_it[2] = {0, 0};
         for (uint32_t k = 0; ok; ++k) {
           if (!wait(L::kItemFull + (k & 1), (k >> 1) & 1)) break;
           const AttnItem& src = items[k & 1];
           const int valid = src.valid, head = src.head, row0 = src.row0, kv0 = src.kv0, n0 = src.n0, n1 = src.n1;
           mbar_arrive(bar(L::kItemEmpty + (k & 1)));
           if (!valid) break;
-          if (!wait(L::kQEmpty, (k & 1) ^ 1)) break;
-          mbar_arrive_expect_tx(bar(L::kQFull), (n1 ? 2 : 1) * L::kTile);
-          tile(&p.tm_q, sb, head, row0, bar(L::kQFull));
-          if (n1) tile(&p.tm_q, sb + L::kTile, head, row0 + kRows, bar(L::kQFull));
-          ++q_it;
           const int nb = max(n0, n1), kvh = head / p.group;
-          for (int j = 0; j < 2 * nb; ++j, ++it_r) {  // K_0, V_0, K_1, V_1, ...
+          auto query = [&](int st) {
+            if (!wait(L::kQEmpty + st, (q_it[st] & 1) ^ 1)) return;
+            mbar_arrive_expect_tx(bar(L::kQFull + st), L::kTile);
+            tile(&p.tm_q, sb + st * L::kTile, head, row0 + st * kRows, bar(L::kQFull + st));
+            ++q_it[st];
+          };
+          query(0);
+          for (int j = 0; j < 2 * nb && ok; ++j, ++it_r) {  // K_0, V_0, K_1, V_1, ...
             const int slot = it_r % L::kStages;
             if (!wait(L::kEmpty + slot, ((it_r / L::kStages) & 1) ^ 1)) break;
             mbar_arrive_expect_tx(bar(L::kFull + slot), L::kTile);
             tile(j & 1 ? &p.tm_v : &p.tm_k, sb + L::kRing + slot * L::kTile, kvh, kv0 + (j >> 1) * kRows,
                  bar(L::kFull + slot));
+            if (j == 0 && n1) query(1);
           }
         }
         if (!ok) {  // give-up: the copies in flight land before the shared memory is left
@@ -355,7 +358,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __gr
             for (int n = 0; n < (1 << 20) && !mbar_try_wait(bar(b), parity); ++n) {
             }
           };
-          if (q_it) drain(L::kQFull, (q_it - 1) & 1);
+          for (int st = 0; st < 2; ++st)
+            if (q_it[st]) drain(L::kQFull + st, (q_it[st] - 1) & 1);
           for (uint32_t i = it_r > L::kStages ? it_r - L::kStages : 0; i < it_r; ++i)
             drain(L::kFull + i % L::kStages, (i / L::kStages) & 1);
         }
@@ -396,18 +400,32 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __gr
           }
           __syncwarp();
         };
-        for (uint32_t k = 0; ok; ++k) {
-          if (!wait_warp(L::kItemFull + (k & 1), (k >> 1) & 1)) break;
-          const int valid = items[k & 1].valid, n0 = items[k & 1].n0, n1 = items[k & 1].n1;
+        uint32_t q_it[2] = {0, 0};
+        auto item = [&](uint32_t k, int& n0, int& n1) {  // its key blocks (0: no item)
+          const AttnItem& it = items[k & 1];
+          n0 = it.valid ? it.n0 : 0, n1 = it.valid ? it.n1 : 0;
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(L::kItemEmpty + (k & 1)));
-          if (!valid) break;
-          const int nb = max(n0, n1);
-          if (!wait_warp(L::kQFull, k & 1) || !full(it_r)) break;
+        };
+        // The first scores of an item, stream by stream: behind the stream's
+        // last P V of the item before, so that its epilogue is not waited for.
+        auto first = [&](int st, int n, bool last_reader) {
+          if (!wait_warp(L::kQFull + st, q_it[st] & 1) || !full(it_r)) return;
+          ++q_it[st];
           tc_fence_after();
-          scores(0, it_r);
-          if (n1) scores(1, it_r);
-          commit(L::kEmpty + slot_of(it_r));
+          scores(st, it_r);
+          if (n == 1) commit(L::kQEmpty + st);
+          if (last_reader) commit(L::kEmpty + slot_of(it_r));
+        };
+        int n0 = 0, n1 = 0;
+        if (wait_warp(L::kItemFull, 0)) {
+          item(0, n0, n1);
+          if (n0) first(0, n0, !n1);
+          if (ok && n1) first(1, n1, true);
+        }
+        for (uint32_t k = 0; ok && n0; ++k) {
+          const int nb = max(n0, n1);
+          int m0 = 0, m1 = 0;  // the next item
           for (int j = 0; j < nb; ++j) {
             const uint32_t kv = it_r + 2 * j + 1, kk = kv + 1;
             const bool more = j + 1 < nb, guarded = j >= n0 - 1;
@@ -428,18 +446,24 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __gr
               }
               tc_fence_after();
               values(st, kv, j == 0);
-              if (j + 1 < n)
+              if (j + 1 < n) {
                 scores(st, kk);
-              else
+                if (j + 2 == n) commit(L::kQEmpty + st);
+              } else {
                 commit(L::kOFull + st);
+              }
             }
             if (!ok) break;
             commit(L::kEmpty + slot_of(kv));
             if (more) commit(L::kEmpty + slot_of(kk));
           }
           if (!ok) break;
-          commit(L::kQEmpty);
           it_r += 2 * nb;
+          if (!wait_warp(L::kItemFull + ((k + 1) & 1), ((k + 1) >> 1) & 1)) break;
+          item(k + 1, m0, m1);
+          if (m0) first(0, m0, !m1);
+          if (ok && m1) first(1, m1, true);
+          n0 = m0, n1 = m1;
         }
         if (!ok) {  // give-up: wait (bounded) for the MMAs issued so far
           commit(L::kDone);
