@@ -368,17 +368,27 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __gr
     } else if (warp == 9) {
       // --------------------------------------------------------------- MMAs
       {
+        // A group of MMAs is issued hardly faster than it runs (some 400 cycles
+        // of them are queued), so what stands between two groups is short:
+        // waits for tiles are made while the group before them runs.
         constexpr uint32_t id_s = idesc_16(128, 128, kF16, false, false), id_o = idesc_16(128, D, kF16, false, true);
-        uint32_t it_r = 0, p_it[2] = {0, 0}, g_it = 0;
-        auto slot_of = [&](uint32_t i) { return (int)(i % L::kStages); };
-        auto full = [&](uint32_t i) { return wait_warp(L::kFull + slot_of(i), (i / L::kStages) & 1); };
+        uint32_t p_par[2] = {0, 0}, q_par[2] = {0, 0}, g_par = 0;
+        int at = 0;           // the next tile of the ring ...
+        uint32_t at_par = 0;  // ... and its parity
+        auto next_tile = [&]() {  // waits for it; its slot
+          wait_warp(L::kFull + at, at_par);
+          const int slot = at;
+          if (++at == L::kStages) at = 0, at_par ^= 1;
+          return slot;
+        };
         auto commit = [&](int b) {
           if (elect_one()) tc_commit(bar(b));
           __syncwarp();
         };
-        auto scores = [&](int st, uint32_t i) {  // S = Q K^T
+        auto scores = [&](int st, int slot) {  // S = Q K^T
+          tc_fence_after();
           if (elect_one()) {
-            const uint32_t q = sdesc_lo(sb + st * L::kTile), kt = sdesc_lo(sb + L::kRing + slot_of(i) * L::kTile);
+            const uint32_t q = sdesc_lo(sb + st * L::kTile), kt = sdesc_lo(sb + L::kRing + slot * L::kTile);
 #pragma unroll
             for (int e = 0; e < D / 16; ++e) {
               const uint32_t o = ((e / 4) * (kRows * 128) + (e % 4) * 32) >> 4;
@@ -391,79 +401,75 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __gr
           }
           __syncwarp();
         };
-        auto values = [&](int st, uint32_t i, bool first) {  // O += P V
+        auto values = [&](int st, int slot, bool first) {  // O += P V
+          tc_fence_after();
           if (elect_one()) {
-            const uint32_t vt = sdesc_lo(sb + L::kRing + slot_of(i) * L::kTile, kRows * 128);
+            const uint32_t vt = sdesc_lo(sb + L::kRing + slot * L::kTile, kRows * 128);
 #pragma unroll
             for (int e = 0; e < kRows / 16; ++e)
               mma_ts(tO(st), tS(st) + 8 * e, vt + e * (2048 >> 4), id_o, e > 0 ? 1u : first ? 0u : 1u);
           }
           __syncwarp();
         };
-        uint32_t q_it[2] = {0, 0};
-        auto item = [&](uint32_t k, int& n0, int& n1) {  // its key blocks (0: no item)
-          const AttnItem& it = items[k & 1];
-          n0 = it.valid ? it.n0 : 0, n1 = it.valid ? it.n1 : 0;
+        int n0 = 0, n1 = 0;  // key blocks of the streams (0: no item, or no second tile)
+        for (uint32_t k = 0; ok; ++k) {
+          if (!wait_warp(L::kItemFull + (k & 1), (k >> 1) & 1)) break;
+          {
+            const AttnItem& it = items[k & 1];
+            n0 = it.valid ? it.n0 : 0, n1 = it.valid ? it.n1 : 0;
+          }
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(L::kItemEmpty + (k & 1)));
-        };
-        // The first scores of an item, stream by stream: behind the stream's
-        // last P V of the item before, so that its epilogue is not waited for.
-        auto first = [&](int st, int n, bool last_reader) {
-          if (!wait_warp(L::kQFull + st, q_it[st] & 1) || !full(it_r)) return;
-          ++q_it[st];
-          tc_fence_after();
-          scores(st, it_r);
-          if (n == 1) commit(L::kQEmpty + st);
-          if (last_reader) commit(L::kEmpty + slot_of(it_r));
-        };
-        int n0 = 0, n1 = 0;
-        if (wait_warp(L::kItemFull, 0)) {
-          item(0, n0, n1);
-          if (n0) first(0, n0, !n1);
-          if (ok && n1) first(1, n1, true);
-        }
-        for (uint32_t k = 0; ok && n0; ++k) {
+          if (!n0) break;
           const int nb = max(n0, n1);
-          int m0 = 0, m1 = 0;  // the next item
-          for (int j = 0; j < nb; ++j) {
-            const uint32_t kv = it_r + 2 * j + 1, kk = kv + 1;
-            const bool more = j + 1 < nb, guarded = j >= n0 - 1;
-            if (!full(kv)) break;
-            if (guarded && lane == 0) mbar_arrive(bar(L::kGo));
-            if (more && !full(kk)) break;
-            bool checked = !guarded;
+          // the first scores, behind the last P V of the item before: its epilogue is not waited for
+          int ks = next_tile();
+#pragma unroll
+          for (int st = 0; st < 2; ++st) {
+            const int n = st ? n1 : n0;
+            if (!ok || !n || !wait_warp(L::kQFull + st, q_par[st])) continue;
+            q_par[st] ^= 1;
+            scores(st, ks);
+            if (n == 1) commit(L::kQEmpty + st);
+          }
+          if (!ok) break;
+          commit(L::kEmpty + ks);
+          int vs = next_tile();
+          if (n0 == 1 && lane == 0) mbar_arrive(bar(L::kGo));
+          for (int j = 0; j < nb && ok; ++j) {
+            const bool more = j + 1 < nb;
+            bool unchecked = j >= n0 - 1;  // the guard looks over V
+            int vnext = 0;
 #pragma unroll
             for (int st = 0; st < 2; ++st) {
               const int n = st ? n1 : n0;
-              if (!ok || j >= n) continue;
-              if (!wait_warp(L::kPFull + st, p_it[st] & 1)) continue;
-              ++p_it[st];
-              if (!checked) {
-                if (!wait_warp(L::kOk, g_it & 1)) continue;
-                ++g_it;
-                checked = true;
+              if (j < n) {
+                if (!wait_warp(L::kPFull + st, p_par[st])) break;
+                p_par[st] ^= 1;
+                if (unchecked) {
+                  if (!wait_warp(L::kOk, g_par)) break;
+                  g_par ^= 1;
+                  unchecked = false;
+                }
+                values(st, vs, j == 0);
               }
-              tc_fence_after();
-              values(st, kv, j == 0);
+              if (st == 1) commit(L::kEmpty + vs);
+              if (st == 0 && more) ks = next_tile();
+              if (!ok) break;
               if (j + 1 < n) {
-                scores(st, kk);
+                scores(st, ks);
                 if (j + 2 == n) commit(L::kQEmpty + st);
-              } else {
+              } else if (j < n) {
                 commit(L::kOFull + st);
               }
+              if (st == 0 && more) {
+                vnext = next_tile();
+                if (j + 1 >= n0 - 1 && lane == 0) mbar_arrive(bar(L::kGo));
+              }
             }
-            if (!ok) break;
-            commit(L::kEmpty + slot_of(kv));
-            if (more) commit(L::kEmpty + slot_of(kk));
+            if (ok && more) commit(L::kEmpty + ks);
+            vs = vnext;
           }
-          if (!ok) break;
-          it_r += 2 * nb;
-          if (!wait_warp(L::kItemFull + ((k + 1) & 1), ((k + 1) >> 1) & 1)) break;
-          item(k + 1, m0, m1);
-          if (m0) first(0, m0, !m1);
-          if (ok && m1) first(1, m1, true);
-          n0 = m0, n1 = m1;
         }
         if (!ok) {  // give-up: wait (bounded) for the MMAs issued so far
           commit(L::kDone);
