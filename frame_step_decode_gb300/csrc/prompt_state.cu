@@ -110,11 +110,11 @@ __global__ void __launch_bounds__(256) k_prompt_state_rows(const __grid_constant
 // and one warp each for the MMAs, the copies of B, C, x and those of z.  The
 // chain from chunk to chunk is the state's: its pass and its product.
 constexpr int kQ = 128;                 // tokens of a chunk
-constexpr int kStateThreads = 896;      // 2 warpgroups in front, 4 behind, 4 single warps
-constexpr int kBehind = 512;
-// Registers: 896 threads are launched with 72 each (64512).
-constexpr int kRegsFront = 96, kRegsBehind = 64, kRegsRest = 48;
-static_assert(256 * kRegsFront + kBehind * kRegsBehind + 128 * kRegsRest <= kStateThreads * 72, "registers");
+constexpr int kStateThreads = 640;      // 2 warpgroups in front, 2 behind, 4 single warps
+constexpr int kBehind = 256;
+// Registers: 640 threads are launched with 96 each (61440).
+constexpr int kRegsFront = 104, kRegsBehind = 104, kRegsRest = 64;
+static_assert(256 * kRegsFront + kBehind * kRegsBehind + 128 * kRegsRest <= kStateThreads * 96, "registers");
 constexpr int kBC = kQ * kSsmN * 2;     // bytes of the B (or C) tile
 constexpr int kXT = kQ * kSsmP * 2;     // ... of one head's x (or z) tile
 
@@ -127,11 +127,11 @@ struct StateSmem {
   static constexpr int kX = kB + kBC;
   static constexpr int kRing = kX + 2 * 2 * kXT;
   static constexpr int kH = kRing + 3 * kBC;      // bf16 H of both heads: [2][n / 64][64 rows of 128 B]
-  static constexpr int kV = kH + 2 * kXT;         // [head][128] log2 dt_j - (the decays behind j, to the chunk's end)
+  static constexpr int kAfter = kH + 2 * kXT;     // [head][128] the decays behind token j, to the chunk's end
+  static constexpr int kV = kAfter + 2 * kQ * 4;  // [head][128] log2 dt_j - after_j
   static constexpr int kU = kV + 2 * kQ * 4;      // [head][96] dt_j 2^-(the decays behind j in its 32 tokens)
-  static constexpr int kW = kU + 2 * 96 * 4;      // [head][128] w_j
-  static constexpr int kTot = kW + 2 * kQ * 4;    // [in front, behind][head][32 tokens] sums of decays
-  static constexpr int kBad = kTot + 2 * 2 * 4 * 4;  // byte chunk % 4, bit head * 4 + warp: an x that is not finite
+  static constexpr int kLast = kU + 2 * 96 * 4;   // [head] the decays of the whole chunk
+  static constexpr int kBad = kLast + 8;  // byte chunk % 4, bit head * 4 + warp: an x that is not finite
   static constexpr int kMisc = kBad + 4;          // TMEM's address
   static constexpr int kBars = kMisc + 4;
   enum {
@@ -150,6 +150,7 @@ struct StateSmem {
     kYFree = kYFull + 2,
     kWx,
     kS,
+    kScan,
     kDone,
     kCount
   };
@@ -165,7 +166,7 @@ __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 // Rows that no tensor map can describe (a stride that is no multiple of 16
-// bytes) are copied by the 512 threads behind, 8 bytes at a time: 128 tokens x
+// bytes) are copied by the 256 threads behind, 8 bytes at a time: 128 tokens x
 // kCols values at column `col` of the rows from row0 on, as the same 128-byte
 // swizzled blocks of 64 columns.  Rows from n on repeat row n - 1.
 template <int kCols>
@@ -240,25 +241,26 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
     return;
   }
 
-  if (warp == 24) {
+  if (warp == 16) {
     if (lane == 0) {
-      const int copies = p.tiled ? 1 : kBehind;
+      const int copies = p.tiled ? 1 : kBehind / 32;
       for (int b = 0; b < 2; ++b) {
         mbar_init(bar(L::kXFull + b), copies);
         mbar_init(bar(L::kXEmpty + b), 1);
         mbar_init(bar(L::kCFull + b), copies);
         mbar_init(bar(L::kZFull + b), copies);
-        mbar_init(bar(L::kOut + b), kBehind);
+        mbar_init(bar(L::kOut + b), kBehind / 32);
         mbar_init(bar(L::kY2 + b), 1);
         mbar_init(bar(L::kYFull + b), 1);
       }
       mbar_init(bar(L::kBFull), copies);
       mbar_init(bar(L::kBEmpty), 1);
-      mbar_init(bar(L::kMFull), 256);
+      mbar_init(bar(L::kMFull), 8);
       mbar_init(bar(L::kG), 1);
-      mbar_init(bar(L::kHFull), 256);
-      mbar_init(bar(L::kYFree), kBehind);
-      mbar_init(bar(L::kWx), kBehind);
+      mbar_init(bar(L::kHFull), 8);  // warps
+      mbar_init(bar(L::kYFree), kBehind / 32);
+      mbar_init(bar(L::kScan), 1);
+      mbar_init(bar(L::kWx), kBehind / 32);
       mbar_init(bar(L::kS), 1);
       mbar_init(bar(L::kDone), 1);
       fence_mbar_init();
@@ -281,6 +283,12 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
   auto wait_warp = [&](int b, uint32_t parity) {
     if (ok) ok = __all_sync(0xffffffffu, wait_bar(bar(b), parity, p.sink));
   };
+  // One arrival for the warp's 32 threads (as many arrivals on one barrier would
+  // go one after the other through the shared-memory pipe, 32 passes a warp).
+  auto arrive_warp = [&](int b) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(b));
+  };
   auto c_tile = [&](int c) { return L::kRing + (2 * c) % 3 * kBC; };
   auto z_tile = [&](int c) { return L::kRing + (2 * c + 1) % 3 * kBC; };
   const int h = (warp >> 2) & 1, quad = warp & 3, row = quad * 32 + lane;  // a thread per token of head h0 + h
@@ -289,58 +297,24 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
   const int head = h0 + h;
   float* sv = (float*)(smem + L::kV);
   float* su = (float*)(smem + L::kU);
-  float* sw = (float*)(smem + L::kW);
+  float* saft = (float*)(smem + L::kAfter);
+  float* slast = (float*)(smem + L::kLast);
   uint32_t* sbad = (uint32_t*)(smem + L::kBad);
-  // the decays: this token's dt of chunk c (0 behind the sequence's end), the
-  // sum of the later tokens' log-decays among its 32 (in powers of two), and
-  // the sum of all 32 for the others.  Summed from the end: the state's newest
-  // tokens are exact to fp32 whatever the sum over the chunk is.
-  const uint16_t* dt_col = p.zx + first * p.zx_stride + 2 * di + 2 * kSsmN + head;
-  const float rate = warp < 24 ? ex2(bf(p.prm[head]) * 1.44269504088896340736f) * 1.44269504088896340736f : 0.f;
-  const float bias = warp < 24 ? bf(p.prm[p.Hs + head]) : 0.f;
-  auto dt_at = [&](int c) { return c * kQ + row < len ? dt_col[(size_t)(c * kQ + row) * p.zx_stride] : (uint16_t)0; };
-  auto decays = [&](int c, uint16_t raw, float& dt, float& inner) {
-    dt = c * kQ + row < len ? softplus(bf(raw) + bias) : 0.f;
-    // 2^-160 is zero in fp32: a larger step changes nothing, and the cap bounds the sums' rounding
-    float down = fminf(rate * dt, 160.f);
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const float v = __shfl_down_sync(0xffffffffu, down, d);
-      if (lane + d < 32) down += v;
-    }
-    inner = __shfl_down_sync(0xffffffffu, down, 1);
-    if (lane == 31) inner = 0.f;
-    return down;  // lane 0: the sum of all 32
-  };
   const size_t state_at = (((size_t)p.b.slot[seq] * p.Hs + h0) * kSsmP + row) * kSsmN + h * 64;
 
   if (warp < 8) {
     // -------------------------------------------------------------- in front
     regs_take<kRegsFront>();
     const float skip = bf(p.prm[2 * p.Hs + head]);
-    uint16_t dt_next = dt_at(0);
     for (int c = 0; c < chunks; ++c) {
-      // ---- the decays
-      float dt, inner;
-      const float sum = decays(c, dt_next, dt, inner);
-      dt_next = dt_at(c + 1);
-      float* tot = (float*)(smem + L::kTot);
-      if (lane == 0) tot[h * 4 + quad] = sum;
-      bar_sync(1, 256);  // also: the last chunk's sv and su have been read
-      float end[4];  // behind each 32 tokens
-      end[3] = 0.f;
-#pragma unroll
-      for (int q = 2; q >= 0; --q) end[q] = end[q + 1] + tot[h * 4 + q + 1];
-      const float after = inner + (quad == 0 ? end[0] : quad == 1 ? end[1] : quad == 2 ? end[2] : 0.f);
-      const float last = end[0] + tot[h * 4];
-      sv[h * kQ + row] = lg2(dt) - after;
-      if (row < 96) su[h * 96 + row] = dt * ex2(-inner);
       // ---- the state: its bf16 copy for C H^T, and the chunk's decay
+      wait_warp(L::kScan, c & 1);
       if (c > 0) wait_warp(L::kS, (c - 1) & 1);
       tc_fence_after();
+      const float after = saft[h * kQ + row];  // c_j - c_i = after_i - after_j
       const bool zero = c == 0 && !goes_on;
       if (!zero) {
-        const float dec = ex2(-((tot[hh * 4] + tot[hh * 4 + 1]) + (tot[hh * 4 + 2] + tot[hh * 4 + 3])));
+        const float dec = ex2(-slast[hh]);
         uint8_t* hrow = smem + L::kH + hh * kXT + h * (64 * 128) + pp * 128;
 #pragma unroll 1
         for (int q = 0; q < 4; ++q) {
@@ -373,8 +347,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
         fence_proxy_async_smem();
       }
       tc_fence_before();
-      mbar_arrive(bar(L::kHFull));
-      bar_sync(2 + h, 128);  // the head's sv and su are complete
+      arrive_warp(L::kHFull);
       // ---- M, over G once both heads have read G
       wait_warp(L::kG, c & 1);
       tc_fence_after();
@@ -396,7 +369,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
           if (q < quad) {
             // below: the decay from the end of token j's 32 to i is a factor
             // of the row, that from j to there is in u_j
-            const float r = ex2(after - (q == 0 ? end[0] : q == 1 ? end[1] : end[2]));
+            const float r = ex2(after - saft[h * kQ + 32 * q + 31]);
             const float2 r2 = make_float2(r, r);
             const float4* uj = (const float4*)(su + h * 96 + 32 * q);
             tmem_ld_wait();
@@ -443,7 +416,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
       wait_warp(L::kY2 + (c & 1), (c >> 1) & 1);
       tc_fence_after();
       if (!zero) {
-        const float ei = ex2(after - last);
+        const float ei = ex2(after - slast[h]);
 #pragma unroll 1
         for (int q = 0; q < 2; ++q) {
           uint32_t v[32];
@@ -455,7 +428,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
       }
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(bar(L::kMFull));
+      arrive_warp(L::kMFull);
     }
     // ---- the state after the last token
     wait_warp(L::kS, (chunks - 1) & 1);
@@ -471,14 +444,11 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
         dst[e] = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]), __uint_as_float(v[4 * e + 2]),
                              __uint_as_float(v[4 * e + 3]));
     }
-  } else if (warp < 24) {
+  } else if (warp < 16) {
     // ---------------------------------------------------------------- behind
-    regs_give<kRegsBehind>();
-    const int part = (warp - 8) >> 2, half = part >> 1;  // 32 tokens of (w X)^T; half of a token's values
-    const int at0 = half * 4;                            // the first of this half's 16-byte pieces (before the swizzle)
+    regs_take<kRegsBehind>();
     // (w X)^T of a chunk is made before the output of the chunk before it: the
     // state's product does not wait for the gate
-    uint16_t dt_next = dt_at(0);
     for (int c = -1; c < chunks; ++c) {
       if (c + 1 < chunks) {
         const int k = c + 1, b = k & 1, left = len - k * kQ;
@@ -498,29 +468,22 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
           copy_tile<kSsmN>(sb + L::kB, p.zx, p.zx_stride, 2 * di, row0, n);
           asm volatile("cp.async.wait_all;" ::: "memory");
           fence_proxy_async_smem();
-          mbar_arrive(bar(L::kXFull + b));
-          mbar_arrive(bar(L::kCFull + b));
-          mbar_arrive(bar(L::kBFull));
-        }
-        float dt, inner;
-        float* tot = (float*)(smem + L::kTot) + 8;
-        if (half == 0) {
-          const float sum = decays(k, dt_next, dt, inner);
-          dt_next = dt_at(k + 1);
-          if (lane == 0) tot[h * 4 + quad] = sum;
+          arrive_warp(L::kXFull + b);
+          arrive_warp(L::kCFull + b);
+          arrive_warp(L::kBFull);
         }
         wait_warp(L::kXFull + b, parity);
         uint8_t* xrow = smem + L::kX + (b * 2 + h) * kXT + row * 128;
         bool odd = false;
         if (row >= left) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) *(uint4*)(xrow + ((at0 + e) << 4)) = make_uint4(0, 0, 0, 0);
+#pragma unroll 4
+          for (int e = 0; e < 8; ++e) *(uint4*)(xrow + (e << 4)) = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
         } else {
           uint32_t acc[2] = {0, 0};
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint4 x = *(const uint4*)(xrow + (((at0 + e) ^ (row & 7)) << 4));
+          for (int e = 0; e < 8; ++e) {
+            const uint4 x = *(const uint4*)(xrow + ((e ^ (row & 7)) << 4));
             asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[0]) : "r"(x.x), "r"(0));
             asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[1]) : "r"(x.y), "r"(0));
             asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[0]) : "r"(x.z), "r"(0));
@@ -532,40 +495,37 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
         bar_sync(4, kBehind);  // x and its flags are complete; every thread here is done with chunk k - 2
         // cleared two chunks ahead: nobody sets these before the next barrier
         if (threadIdx.x == 256) atomicAnd(sbad, ~(0xFFu << (((k + 2) & 3) * 8)));
-        // ---- (w X)^T: row (hh, pp), tokens 32 part .. 32 part + 31
-        if (half == 0) {
-          float after = inner;
-#pragma unroll
-          for (int q = 1; q < 4; ++q)
-            if (q > quad) after += tot[h * 4 + q];
-          sw[h * kQ + row] = dt * ex2(-after);
-        }
+        // ---- (w X)^T: row (hh, pp), tokens 64 h .. 64 h + 63
+        wait_warp(L::kScan, k & 1);
         if (k > 0) wait_warp(L::kS, (k - 1) & 1);
         if (left < kQ) {  // B's phase before this one is over: the last state has been made of it
           wait_warp(L::kBFull, k & 1);
           if (row >= left) {
             uint8_t* brow = smem + L::kB + h * (kQ * 128) + row * 128;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) *(uint4*)(brow + ((at0 + e) << 4)) = make_uint4(0, 0, 0, 0);
+            for (int e = 0; e < 8; ++e) *(uint4*)(brow + (e << 4)) = make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();
           }
         }
-        bar_sync(4, kBehind);  // sw is complete
         tc_fence_after();
         const uint8_t* xt = smem + L::kX + (b * 2 + hh) * kXT + (pp & 7) * 2;
 #pragma unroll 1
-        for (int q = 0; q < 2; ++q) {
-          const int j0 = part * 32 + 16 * q;
+        for (int q = 0; q < 4; ++q) {
+          const int j0 = h * 64 + 16 * q;
           float v[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e)  // j0 is a multiple of 8
             v[e] = bf(*(const uint16_t*)(xt + (j0 + e) * 128 + (((pp >> 3) ^ (e & 7)) << 4)));
-          const float4* wj = (const float4*)(sw + hh * kQ + j0);
+          // w_j: u_j times the decay from its 32 tokens' end on; the last 32 have v_j only
+          const bool tail_block = j0 >= 96;
+          const float tail = tail_block ? 1.f : ex2(-saft[hh * kQ + (j0 | 31)]);
+          const float4* uj = (const float4*)((tail_block ? sv + hh * kQ : su + hh * 96) + j0);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float4 w4 = wj[e];
-            const float2 r0 = mul2(make_float2(v[4 * e], v[4 * e + 1]), make_float2(w4.x, w4.y));
-            const float2 r1 = mul2(make_float2(v[4 * e + 2], v[4 * e + 3]), make_float2(w4.z, w4.w));
+            float4 u4 = uj[e];
+            if (tail_block) u4 = make_float4(ex2(u4.x), ex2(u4.y), ex2(u4.z), ex2(u4.w));
+            const float2 r0 = mul2(make_float2(v[4 * e], v[4 * e + 1]), mul2(make_float2(u4.x, u4.y), make_float2(tail, tail)));
+            const float2 r1 = mul2(make_float2(v[4 * e + 2], v[4 * e + 3]), mul2(make_float2(u4.z, u4.w), make_float2(tail, tail)));
             v[4 * e] = r0.x, v[4 * e + 1] = r0.y, v[4 * e + 2] = r1.x, v[4 * e + 3] = r1.y;
           }
           uint32_t hi[8], lo[8];
@@ -576,23 +536,23 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
                                   make_float2(__uint_as_float(hi[e] << 16), __uint_as_float(hi[e] & 0xFFFF0000u)));
             lo[e] = pack_bf16(r.x, r.y);
           }
-          tmem_st8(tmem + kTWx + lanes + part * 16 + q * 8, hi);
-          tmem_st8(tmem + kTWx + 64 + lanes + part * 16 + q * 8, lo);
+          tmem_st8(tmem + kTWx + lanes + h * 32 + q * 8, hi);
+          tmem_st8(tmem + kTWx + 64 + lanes + h * 32 + q * 8, lo);
         }
         tmem_st_wait();
         if (*(volatile uint32_t*)sbad >> ((k & 3) * 8) & 0xFFu) {  // seen by every thread or none
           bar_sync(4, kBehind);
           if (odd) {
 #pragma unroll 1
-            for (int e = 0; e < 32; ++e) {
-              uint16_t* x = (uint16_t*)(xrow + (((at0 + (e >> 3)) ^ (row & 7)) << 4)) + (e & 7);
+            for (int e = 0; e < 64; ++e) {
+              uint16_t* x = (uint16_t*)xrow + e;
               if ((*x & 0x7F80) == 0x7F80) *x = 0;
             }
             fence_proxy_async_smem();
           }
         }
         tc_fence_before();
-        mbar_arrive(bar(L::kWx));
+        arrive_warp(L::kWx);
       }
       if (c < 0) continue;
       const int b = c & 1, left = len - c * kQ;
@@ -603,34 +563,39 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
         if (c > 0) wait_warp(L::kY2 + ((c - 1) & 1), ((c - 1) >> 1) & 1);
         copy_tile<2 * kSsmP>(sb + z_tile(c), p.zx, p.zx_stride, h0 * kSsmP, first + (size_t)c * kQ, min(kQ, left));
         asm volatile("cp.async.wait_all;" ::: "memory");
-        mbar_arrive(bar(L::kZFull + b));
+        arrive_warp(L::kZFull + b);
       }
       wait_warp(L::kZFull + b, (c >> 1) & 1);
       wait_warp(L::kYFull + h, c & 1);
       tc_fence_after();
       uint8_t* zrow = ztile + row * 128;
-      uint32_t y[32];
-      tmem_ld32(tmem + kTY + h * 64 + lanes + 32 * half, y);
-      tmem_ld_wait();
-      tc_fence_before();
-      mbar_arrive(bar(L::kYFree));
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        uint4* zp = (uint4*)(zrow + (((at0 + e) ^ (row & 7)) << 4));
-        const uint4 zv = *zp;
-        const uint32_t zw[4] = {zv.x, zv.y, zv.z, zv.w};
-        uint32_t o[4];
-#pragma unroll
-        for (int f = 0; f < 4; ++f) {
-          const int i = 8 * e + 2 * f;
-          const float2 z2 = make_float2(__uint_as_float(zw[f] << 16), __uint_as_float(zw[f] & 0xFFFF0000u));
-          const float2 t = mul2(z2, make_float2(-1.44269504088896340736f, -1.44269504088896340736f));
-          const float2 d = add2(make_float2(ex2(t.x), ex2(t.y)), make_float2(1.f, 1.f));
-          const float2 g = mul2(z2, make_float2(rcp(d.x), rcp(d.y)));
-          const float2 r = mul2(make_float2(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), g);
-          o[f] = pack_bf16(r.x, r.y);
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        uint32_t y[32];
+        tmem_ld32(tmem + kTY + h * 64 + lanes + 32 * half, y);
+        tmem_ld_wait();
+        if (half == 1) {
+          tc_fence_before();
+          arrive_warp(L::kYFree);
         }
-        *zp = make_uint4(o[0], o[1], o[2], o[3]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint4* zp = (uint4*)(zrow + (((half * 4 + e) ^ (row & 7)) << 4));
+          const uint4 zv = *zp;
+          const uint32_t zw[4] = {zv.x, zv.y, zv.z, zv.w};
+          uint32_t o[4];
+#pragma unroll
+          for (int f = 0; f < 4; ++f) {
+            const int i = 8 * e + 2 * f;
+            const float2 z2 = make_float2(__uint_as_float(zw[f] << 16), __uint_as_float(zw[f] & 0xFFFF0000u));
+            const float2 t = mul2(z2, make_float2(-1.44269504088896340736f, -1.44269504088896340736f));
+            const float2 d = add2(make_float2(ex2(t.x), ex2(t.y)), make_float2(1.f, 1.f));
+            const float2 g = mul2(z2, make_float2(rcp(d.x), rcp(d.y)));
+            const float2 r = mul2(make_float2(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), g);
+            o[f] = pack_bf16(r.x, r.y);
+          }
+          *zp = make_uint4(o[0], o[1], o[2], o[3]);
+        }
       }
       if (any_bad) {  // tokens up to this one whose x is not finite
 #pragma unroll 1
@@ -638,27 +603,27 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
           if (!(any_bad >> (j >> 5) & 1)) continue;
           const uint16_t* x = p.zx + (first + (size_t)c * kQ + j) * p.zx_stride + di + head * kSsmP;
 #pragma unroll 1
-          for (int e = half * 32; e < half * 32 + 32; ++e)
+          for (int e = 0; e < 64; ++e)
             if ((x[e] & 0x7F80) == 0x7F80) *(uint16_t*)(zrow + (((e >> 3) ^ (row & 7)) << 4) + (e & 7) * 2) = 0x7FC0;
         }
       }
       __syncwarp();
       {
-        const int r0 = quad * 32 + (lane >> 2), at = at0 + (lane & 3);  // eight rows at a time
+        const int r0 = quad * 32 + (lane >> 3), at = lane & 7;  // four rows at a time
         uint16_t* dst = p.out + (first + (size_t)c * kQ + r0) * p.out_stride + head * kSsmP + at * 8;
-#pragma unroll
-        for (int q = 0; q < 4; ++q, dst += 8 * p.out_stride) {
-          const int r = r0 + 8 * q;
+#pragma unroll 4
+        for (int q = 0; q < 8; ++q, dst += 4 * p.out_stride) {
+          const int r = r0 + 4 * q;
           const uint4 v = *(const uint4*)(ztile + r * 128 + ((at ^ (r & 7)) << 4));
           if (r < left) *(uint4*)dst = v;
         }
       }
       fence_proxy_async_smem();  // the next copies into this buffer come by the async proxy
-      mbar_arrive(bar(L::kOut + b));
+      arrive_warp(L::kOut + b);
     }
   } else {
     regs_give<kRegsRest>();
-    if (warp == 24) {
+    if (warp == 16) {
       // ---------------------------------------------------------------- MMAs
       constexpr uint32_t id_g = idesc_16(128, 128, false, false, false), id_y2 = idesc_16(128, 64, false, false, false),
                          id_y = idesc_16(128, 64, false, false, true), id_s = idesc_16(128, 128, false, false, true);
@@ -735,9 +700,8 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
         }
       }
       __syncwarp();
-    } else if (p.tiled) {
-      // -------------------------- copies by tensor maps: x and C, z, B, a warp each
-      const int col = warp == 25 ? di + h0 * kSsmP : warp == 26 ? h0 * kSsmP : 2 * di;
+    } else if (warp < 19) {
+      // ------------------- copies by tensor maps: x, C and B, and z, a warp each
       auto copy = [&](uint32_t dst, int column, int c, int b) {  // two blocks of 64 columns
         if (elect_one()) {
           mbar_arrive_expect_tx(bar(b), kBC);
@@ -747,35 +711,103 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
         __syncwarp();
       };
       int c = 0;
-      for (; c < chunks; ++c) {
+      for (; p.tiled && c < chunks; ++c) {
         const uint32_t parity = ((c >> 1) & 1) ^ 1;
-        if (warp == 25) {
+        if (warp == 17) {
           wait_warp(L::kXEmpty + (c & 1), parity);
           if (!ok) break;
-          copy(sb + L::kX + (c & 1) * 2 * kXT, col, c, L::kXFull + (c & 1));
+          copy(sb + L::kX + (c & 1) * 2 * kXT, di + h0 * kSsmP, c, L::kXFull + (c & 1));
           wait_warp(L::kOut + (c & 1), parity);  // z of two chunks before
           if (!ok) break;
           copy(sb + c_tile(c), 2 * di + kSsmN, c, L::kCFull + (c & 1));
-        } else if (warp == 26) {
-          if (c > 0) wait_warp(L::kY2 + ((c - 1) & 1), ((c - 1) >> 1) & 1);  // C of the chunk before
-          if (!ok) break;
-          copy(sb + z_tile(c), col, c, L::kZFull + (c & 1));
-        } else {
           wait_warp(L::kBEmpty, (c & 1) ^ 1);
           if (!ok) break;
-          copy(sb + L::kB, col, c, L::kBFull);
+          copy(sb + L::kB, 2 * di, c, L::kBFull);
+        } else {
+          if (c > 0) wait_warp(L::kY2 + ((c - 1) & 1), ((c - 1) >> 1) & 1);  // C of the chunk before
+          if (!ok) break;
+          copy(sb + z_tile(c), h0 * kSsmP, c, L::kZFull + (c & 1));
         }
       }
       if (!ok) {  // give-up: the copies in flight land before the shared memory is left
-        const int from = max(0, c - 2);
-        for (int i = from; i <= c; ++i)
-          for (int n = 0; n < (1 << 12); ++n) {
-            const bool x = warp == 25 ? mbar_try_wait(bar(L::kXFull + (i & 1)), (i >> 1) & 1) &&
-                                            mbar_try_wait(bar(L::kCFull + (i & 1)), (i >> 1) & 1)
-                                      : warp == 26 ? mbar_try_wait(bar(L::kZFull + (i & 1)), (i >> 1) & 1)
-                                                   : mbar_try_wait(bar(L::kBFull), i & 1);
-            if (x) break;
+        for (int i = max(0, c - 2); i <= c; ++i)
+          for (int n = 0; n < (1 << 12); ++n)
+            if (warp == 17 ? mbar_try_wait(bar(L::kXFull + (i & 1)), (i >> 1) & 1) &&
+                                 mbar_try_wait(bar(L::kCFull + (i & 1)), (i >> 1) & 1) && mbar_try_wait(bar(L::kBFull), i & 1)
+                           : mbar_try_wait(bar(L::kZFull + (i & 1)), (i >> 1) & 1))
+              break;
+      }
+      __syncwarp();
+    } else {
+      // ------------------------------ the decays, a chunk ahead: lane l has
+      // tokens 4 l .. 4 l + 3 of both heads.  They are summed from the chunk's
+      // end, so that the weights of the state's newest tokens are exact to
+      // fp32 whatever the sum over the chunk is.
+      float rate[2], bias[2];
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        rate[g] = expf(bf(p.prm[h0 + g])) * 1.44269504088896340736f;
+        bias[g] = bf(p.prm[p.Hs + h0 + g]);
+      }
+      const uint16_t* col = p.zx + first * p.zx_stride + 2 * di + 2 * kSsmN + h0;  // two heads: 4 bytes
+      uint32_t raw[4];
+      auto fetch = [&](int c) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int j = c * kQ + 4 * lane + t;
+          raw[t] = j < len ? *(const uint32_t*)(col + (size_t)j * p.zx_stride) : 0;
+        }
+      };
+      fetch(0);
+      for (int c = 0; c < chunks; ++c) {
+        const int left = len - c * kQ;
+        float dt[2][4], after[2][4], last[2];
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          float lam[4];
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            dt[g][t] = softplus((g ? __uint_as_float(raw[t] & 0xFFFF0000u) : __uint_as_float(raw[t] << 16)) + bias[g]);
+            if (4 * lane + t >= left) dt[g][t] = 0.f;
+            // the token's decay in powers of two; 2^-160 is zero in fp32: a larger
+            // step changes nothing, and the cap bounds the rounding of the sums
+            lam[t] = fminf(rate[g] * dt[g][t], 160.f);
           }
+          float down = (lam[0] + lam[1]) + (lam[2] + lam[3]);  // this lane's and the later ones'
+#pragma unroll
+          for (int d = 1; d < 32; d <<= 1) {
+            const float v = __shfl_down_sync(0xffffffffu, down, d);
+            if (lane + d < 32) down += v;
+          }
+          float a = __shfl_down_sync(0xffffffffu, down, 1);
+          if (lane == 31) a = 0.f;
+          last[g] = __shfl_sync(0xffffffffu, down, 0);
+#pragma unroll
+          for (int t = 3; t >= 0; --t) {
+            after[g][t] = a;
+            a += lam[t];
+          }
+        }
+        if (c + 1 < chunks) fetch(c + 1);
+        if (c > 0) {  // the last chunk's have been read
+          wait_warp(L::kWx, (c - 1) & 1);
+          wait_warp(L::kMFull, (c - 1) & 1);
+          if (!ok) break;
+        }
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          *(float4*)(saft + g * kQ + 4 * lane) = make_float4(after[g][0], after[g][1], after[g][2], after[g][3]);
+          *(float4*)(sv + g * kQ + 4 * lane) = make_float4(lg2(dt[g][0]) - after[g][0], lg2(dt[g][1]) - after[g][1],
+                                                           lg2(dt[g][2]) - after[g][2], lg2(dt[g][3]) - after[g][3]);
+          const float end = __shfl_sync(0xffffffffu, after[g][3], lane | 7);  // behind these 32 tokens
+          if (lane < 24)
+            *(float4*)(su + g * 96 + 4 * lane) =
+                make_float4(dt[g][0] * ex2(end - after[g][0]), dt[g][1] * ex2(end - after[g][1]),
+                            dt[g][2] * ex2(end - after[g][2]), dt[g][3] * ex2(end - after[g][3]));
+          if (lane == 0) slast[g] = last[g];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::kScan));
       }
       __syncwarp();
     }
@@ -783,7 +815,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 24) tmem_dealloc(tmem, 512);
+  if (warp == 16) tmem_dealloc(tmem, 512);
 }
 
 }  // namespace wave
