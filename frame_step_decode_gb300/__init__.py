@@ -155,33 +155,49 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+_ARRAYS: dict = {}  # ctypes array types by length
+
+
 def _ints(values):
-    """A host array of int32 (any sequence of integers)."""
-    values = [int(v) for v in values]
-    return (ctypes.c_int32 * max(1, len(values)))(*values), len(values)
+    """A host array of int32 (any sequence of integers), and its length."""
+    n = len(values)
+    t = _ARRAYS.get(n)
+    if t is None:
+        t = _ARRAYS[n] = ctypes.c_int32 * max(1, n)
+    try:
+        return t(*values), n
+    except TypeError:  # elements that are integers, but not Python's
+        return t(*[int(v) for v in values]), n
+
+
+def _types() -> dict:
+    import torch
+    return {torch.float32: WAVE_F32, torch.bfloat16: WAVE_BF16, torch.float16: WAVE_F16}
+
+
+_TYPES: dict = {}
 
 
 def _type_of(t) -> int:
-    import torch
-    return {torch.float32: WAVE_F32, torch.bfloat16: WAVE_BF16, torch.float16: WAVE_F16}.get(t.dtype, -1)
+    if not _TYPES:
+        _TYPES.update(_types())
+    return _TYPES.get(t.dtype, -1)
 
 
-def _rows(t, heads: bool, what: str) -> int:
-    """The row stride in elements of a packed tensor [rows][H][D] (heads) or
+def _rows(t, what: str) -> int:
+    """The row stride in elements of a packed tensor [rows][H][D] or
     [rows][values]; what lies inside a row has to be contiguous."""
-    inner = (t.shape[2], 1) if heads else (1,)
-    if t.dim() != len(inner) + 1 or (t.numel() and any(n > 1 and a != b for n, a, b in zip(t.shape[1:], t.stride()[1:], inner))):
+    shape, stride = t.shape, t.stride()
+    width = shape[-1]
+    fits = stride[-1] == 1 or width == 1
+    if len(shape) == 3:
+        fits = fits and (stride[1] == width or shape[1] == 1)
+        width *= shape[1]
+    elif len(shape) != 2:
+        fits = False
+    if not fits:
         raise ValueError(f"{what}: a packed tensor of rows, contiguous inside a row, is wanted")
-    width = 1
-    for n in t.shape[1:]:
-        width *= n
-    return t.stride(0) if t.shape[0] > 1 else width
-
-
-def _covered(cu, n_cu: int, what: str, *tensors) -> None:
-    """Every packed buffer has the rows that cu names."""
-    if n_cu < 2 or any(t is not None and t.shape[0] < cu[n_cu - 1] for t in tensors):
-        raise ValueError(f"{what}: cu_seqlens names more rows than a buffer has")
+    return stride[0] if shape[0] > 1 else width
 
 
 def _stream(stream) -> int:
@@ -281,18 +297,22 @@ class Wave:
         of one 16-bit type: the rotated q and the k, v that the history now
         holds."""
         (cu, n_cu), (sl, n_sl), (s0, n_s0) = _ints(cu_seqlens), _ints(slots), _ints(starts)
-        if n_sl != n_cu - 1 or n_s0 != n_cu - 1:
+        if n_cu < 2 or n_sl != n_cu - 1 or n_s0 != n_sl:
             raise ValueError("wave_prompt_append: one slot and one start for each sequence")
-        outs = [t for t in (q, k, v) if t is not None]
         H, D = self.cfg.n_heads, self.cfg.head_dim
-        if any(tuple(t.shape[1:]) != (H, D) or not t.is_contiguous() or t.dtype != outs[0].dtype for t in outs):
-            raise ValueError("wave_prompt_append: q, k and v are contiguous [rows][H][D], of one type")
-        if qkv.dim() != 2 or qkv.shape[1] != 3 * H * D:
-            raise ValueError("wave_prompt_append: qkv is [rows][3*H*D]")
-        _covered(cu, n_cu, "wave_prompt_append", qkv, *outs)
-        rc = lib().wave_prompt_append(self.h, layer, n_cu - 1, cu, sl, s0, _ptr(qkv), _type_of(qkv),
-                                      _rows(qkv, False, "qkv"), _ptr(kv), _ptr(kv_scales), _ptr(q), _ptr(k), _ptr(v),
-                                      _type_of(outs[0]) if outs else WAVE_BF16, _stream(stream))
+        rows, out_type = cu[n_sl], -1
+        for t in (q, k, v):
+            if t is None:
+                continue
+            kind = _type_of(t)
+            if t.shape[0] < rows or t.shape[1:] != (H, D) or out_type not in (-1, kind) or not t.is_contiguous():
+                raise ValueError("wave_prompt_append: q, k and v are contiguous [rows][H][D], of one type")
+            out_type = kind
+        if qkv.shape[0] < rows or qkv.shape[1:] != (3 * H * D,):
+            raise ValueError("wave_prompt_append: qkv is [rows][3*H*D], with the rows that cu_seqlens names")
+        rc = lib().wave_prompt_append(self.h, layer, n_sl, cu, sl, s0, _ptr(qkv), _type_of(qkv), _rows(qkv, "qkv"),
+                                      _ptr(kv), _ptr(kv_scales), _ptr(q), _ptr(k), _ptr(v),
+                                      WAVE_BF16 if out_type < 0 else out_type, _stream(stream))
         if check and rc != WAVE_OK:
             raise WaveError(rc, "wave_prompt_append")
         return rc
@@ -303,16 +323,18 @@ class Wave:
         all fp16, rows may be strided; scale defaults to 1/sqrt(D)."""
         cu, n_cu = _ints(cu_seqlens)
         H, D = self.cfg.n_heads, self.cfg.head_dim
-        if any(t.dtype != q.dtype for t in (k, v, out)) or k.shape[1:] != v.shape[1:] or k.shape[-1] != D \
-                or tuple(q.shape[1:]) != (H, D) or tuple(out.shape[1:]) != (H, D):
+        qs, ks, dtype = q.shape, k.shape, q.dtype
+        if k.dtype != dtype or v.dtype != dtype or out.dtype != dtype or qs[1:] != (H, D) or out.shape[1:] != (H, D) \
+                or len(ks) != 3 or ks[2] != D or v.shape[1:] != ks[1:]:
             raise ValueError("wave_prompt_attention: q, out [rows][n_heads][D] and k, v [rows][n_kv_heads][D] of one type")
-        strides = [_rows(t, True, "wave_prompt_attention") for t in (q, k, v, out)]
-        _covered(cu, n_cu, "wave_prompt_attention", q, k, v, out)
-        rc = lib().wave_prompt_attention(self.h, n_cu - 1, cu, k.shape[1], _type_of(q), _ptr(q), strides[0], _ptr(k),
-                                         strides[1], _ptr(v), strides[2], D ** -0.5 if scale is None else scale,
-                                         _ptr(out), strides[3], _stream(stream))
+        if n_cu < 2 or min(qs[0], ks[0], v.shape[0], out.shape[0]) < cu[n_cu - 1]:
+            raise ValueError("wave_prompt_attention: cu_seqlens names more rows than a buffer has")
+        what = "wave_prompt_attention"
+        rc = lib().wave_prompt_attention(self.h, n_cu - 1, cu, ks[1], _type_of(q), _ptr(q), _rows(q, what), _ptr(k),
+                                         _rows(k, what), _ptr(v), _rows(v, what), D ** -0.5 if scale is None else scale,
+                                         _ptr(out), _rows(out, what), _stream(stream))
         if check and rc != WAVE_OK:
-            raise WaveError(rc, "wave_prompt_attention")
+            raise WaveError(rc, what)
         return rc
 
     def sessions_copy(self, src, dst, kv, kv_scales, positions, state=None, move=False, stream=None,
@@ -462,17 +484,18 @@ class HybridWave(Wave):
         [rows][d_inner], rows may be strided; state_in (None when every start
         is 0) and state_out are the fp32 state, which may be one buffer."""
         (cu, n_cu), (sl, n_sl), (s0, n_s0) = _ints(cu_seqlens), _ints(slots), _ints(starts)
-        if n_sl != n_cu - 1 or n_s0 != n_cu - 1:
+        if n_cu < 2 or n_sl != n_cu - 1 or n_s0 != n_sl:
             raise ValueError("wave_hybrid_prompt_state: one slot and one start for each sequence")
         c = self.cfg
         di = c.ssm_heads * c.ssm_head_dim
         if zxbcdt.shape[1:] != (2 * di + 2 * c.ssm_state + c.ssm_heads,) or out.shape[1:] != (di,) \
                 or _type_of(zxbcdt) != WAVE_BF16 or _type_of(out) != WAVE_BF16:
             raise ValueError("wave_hybrid_prompt_state: zxbcdt is bf16 [rows][in_rows], out bf16 [rows][d_inner]")
-        _covered(cu, n_cu, "wave_hybrid_prompt_state", zxbcdt, out)
-        rc = lib().wave_hybrid_prompt_state(self.h, layer, _ptr(weights), n_cu - 1, cu, sl, s0, _ptr(zxbcdt),
-                                            _rows(zxbcdt, False, "zxbcdt"), _ptr(state_in), _ptr(state_out), _ptr(out),
-                                            _rows(out, False, "out"), _stream(stream))
+        if min(zxbcdt.shape[0], out.shape[0]) < cu[n_sl]:
+            raise ValueError("wave_hybrid_prompt_state: cu_seqlens names more rows than a buffer has")
+        rc = lib().wave_hybrid_prompt_state(self.h, layer, _ptr(weights), n_sl, cu, sl, s0, _ptr(zxbcdt),
+                                            _rows(zxbcdt, "zxbcdt"), _ptr(state_in), _ptr(state_out), _ptr(out),
+                                            _rows(out, "out"), _stream(stream))
         if check and rc != WAVE_OK:
             raise WaveError(rc, "wave_hybrid_prompt_state")
         return rc
