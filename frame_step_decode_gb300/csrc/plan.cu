@@ -90,7 +90,9 @@ int device_check(int* dev, int* sms) {
     return WAVE_ECUDA;
   if (major != 10 || minor != 3) return WAVE_EDEVICE;
   if (!encode_fn()) return WAVE_ECUDA;
-  if (configure_step_kernel() != cudaSuccess) return WAVE_ECUDA;
+  if (configure_step_kernel() != cudaSuccess || configure_prompt_attention() != cudaSuccess ||
+      configure_prompt_state() != cudaSuccess)
+    return WAVE_ECUDA;
   int per_sm = 0;
   if (occupancy_per_sm(&per_sm) != cudaSuccess || per_sm < 1) return WAVE_ELAUNCH;
   return WAVE_OK;
@@ -265,6 +267,8 @@ size_t carve_workspace(const Plan& pl, char* base, Workspace* ws) {
       {(void**)&w.zero_pos, (size_t)pl.S_max * 4},
       {(void**)&w.zx, (size_t)(SP * pl.in_rows * 4)},
       {(void**)&w.ssm_out, (size_t)(SP * pl.d_inner * 2)},
+      {(void**)&w.seg_state, pl.hybrid ? (size_t)pl.grid * 2 * kSsmP * kSsmN * 4 : 0},
+      {(void**)&w.seg_decay, pl.hybrid ? (size_t)pl.grid * 2 * 4 : 0},
   };
   size_t o = 0;
   for (const Part& pt : parts) {

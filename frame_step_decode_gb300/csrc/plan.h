@@ -64,6 +64,8 @@ struct Workspace {
   int32_t* zero_pos = nullptr;
   float* zx = nullptr;
   uint16_t* ssm_out = nullptr;
+  float* seg_state = nullptr;  // hybrid: states of prompt segments, one per SM, ...
+  float* seg_decay = nullptr;  // ... and their decays
 };
 
 // Tensor maps of one launch.
@@ -78,6 +80,9 @@ void decoder_layout(const wave_config* c, long long off[6], long long* layer_ele
 // attention block (A), and the offsets inside them.
 void hybrid_layout(const wave_hybrid_config* c, long long* M, long long* A, long long* w_in,
                    long long* w_out, long long* a_log, long long* wqkv, long long* wo);
+// Attributes of the prompt kernels on the current device (prompt_attn.cu, prompt_state.cu).
+cudaError_t configure_prompt_attention();
+cudaError_t configure_prompt_state();
 // The current device, its SM count, and whether it is sm_103 with the driver
 // entry points and kernel attributes the step needs.
 int device_check(int* dev, int* sms);

@@ -573,11 +573,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __gr
 
 template <int D, bool kF16>
 static cudaError_t launch_attention(const AttnParams& p, int grid, cudaStream_t st) {
-  const cudaError_t set = cudaFuncSetAttribute(k_prompt_attention<D, kF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               AttnSmem<D>::kTotal);
-  if (set != cudaSuccess) return set;
-  k_prompt_attention<D, kF16><<<(unsigned)(p.items < grid ? p.items : grid), kAttnThreads, AttnSmem<D>::kTotal, st>>>(p);
+  k_prompt_attention<D, kF16>
+      <<<(unsigned)(p.items < grid ? p.items : grid), kAttnThreads, AttnSmem<D>::kTotal, st>>>(p);
   return cudaGetLastError();
+}
+
+template <int D, bool kF16>
+static cudaError_t configure() {
+  return cudaFuncSetAttribute(k_prompt_attention<D, kF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              AttnSmem<D>::kTotal);
+}
+
+// Once per device, when a handle is made.
+cudaError_t configure_prompt_attention() {
+  const cudaError_t e[4] = {configure<128, false>(), configure<128, true>(), configure<64, false>(), configure<64, true>()};
+  for (cudaError_t x : e)
+    if (x != cudaSuccess) return x;
+  return cudaSuccess;
 }
 
 }  // namespace wave

@@ -33,6 +33,14 @@ struct StateParams {
   float* state_out;
   uint16_t* out;           // [rows][out_stride] bf16
   long long zx_stride, out_stride;
+  // Few sequences and heads leave SMs idle: a long sequence is then cut into
+  // segments of seg_chunks chunks, a CTA each.  A first launch makes every
+  // segment's state from zero, the second begins each segment from those
+  // before it.
+  int seg_chunks;                      // 0: whole sequences
+  int32_t seg_cum[WAVE_MAX_SEQS + 1];  // segments before sequence i
+  float* seg_state;                    // [segment and head pair][128 rows (head, p)][128]
+  float* seg_decay;                    // ... [2]: the decays of the segment, in powers of two
   ErrSink sink;
 };
 
@@ -224,15 +232,38 @@ __device__ __forceinline__ float softplus(float raw) {
   return fmaxf(raw, 0.f) + s * q;
 }
 
+// kLocal: only the state of a segment from zero, into seg_state (the last
+// segment of a sequence has none to give on).
+template <bool kLocal>
 __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_constant__ StateParams p) {
   using L = StateSmem;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int pairs = p.Hs / 2, seq = blockIdx.x / pairs, h0 = (blockIdx.x % pairs) * 2;
-  const size_t first = p.b.begin[seq];
-  const int len = p.b.len(seq), chunks = (len + kQ - 1) / kQ;
-  const bool goes_on = p.b.start[seq] > 0;  // the state begins as state_in, not as zero
+  const int pairs = p.Hs / 2, unit = blockIdx.x / pairs, h0 = (blockIdx.x % pairs) * 2;
+  int seq = unit, seg = 0, len, off = 0;
+  if (p.seg_chunks) {
+    int lo = 0, hi = p.b.n - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (p.seg_cum[mid] <= unit)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    seq = lo;
+    seg = unit - p.seg_cum[seq];
+    off = seg * p.seg_chunks * kQ;
+  }
+  len = p.b.len(seq) - off;
+  const bool last_seg = !p.seg_chunks || len <= p.seg_chunks * kQ;
+  if (!last_seg) len = p.seg_chunks * kQ;
+  if (kLocal && last_seg) return;
+  const size_t first = (size_t)p.b.begin[seq] + off;
+  const int chunks = (len + kQ - 1) / kQ;
+  const bool from_in = !kLocal && p.b.start[seq] > 0;   // the sequence begins from state_in, not from zero
+  const bool goes_on = from_in || (!kLocal && seg > 0);  // this CTA's state does not begin as zero
+  const int seg0 = (int)blockIdx.x - seg * pairs;        // the sequence's first segment, of this head pair
   const int di = p.Hs * kSsmP;
   auto bar = [&](int b) { return sb + L::kBars + b * 8; };
   uint32_t* tmem_word = (uint32_t*)(smem + L::kMisc);
@@ -306,6 +337,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
     // -------------------------------------------------------------- in front
     regs_take<kRegsFront>();
     const float skip = bf(p.prm[2 * p.Hs + head]);
+    float decayed = 0.f;  // kLocal: the decays so far, of head h
     for (int c = 0; c < chunks; ++c) {
       // ---- the state: its bf16 copy for C H^T, and the chunk's decay
       wait_warp(L::kScan, c & 1);
@@ -319,18 +351,32 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
 #pragma unroll 1
         for (int q = 0; q < 4; ++q) {
           uint32_t v[16];
-          if (c == 0) {
+          if (!kLocal && c == 0) {
             const float4* src = (const float4*)(p.state_in + state_at + 16 * q);
+            float4 f[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) f[e] = from_in ? src[e] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+            for (int i = 0; i < seg; ++i) {  // the segments before this one
+              const int cta = seg0 + i * pairs;
+              const float d = ex2(-p.seg_decay[2 * cta + hh]);
+              const float4* part = (const float4*)(p.seg_state + (size_t)cta * (128 * kSsmN) + row * kSsmN + h * 64 + 16 * q);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float4 t = part[e];
+                f[e] = make_float4(fmaf(f[e].x, d, t.x), fmaf(f[e].y, d, t.y), fmaf(f[e].z, d, t.z), fmaf(f[e].w, d, t.w));
+              }
+            }
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float4 f = src[e];
-              v[4 * e] = __float_as_uint(f.x), v[4 * e + 1] = __float_as_uint(f.y);
-              v[4 * e + 2] = __float_as_uint(f.z), v[4 * e + 3] = __float_as_uint(f.w);
+              v[4 * e] = __float_as_uint(f[e].x), v[4 * e + 1] = __float_as_uint(f[e].y);
+              v[4 * e + 2] = __float_as_uint(f[e].z), v[4 * e + 3] = __float_as_uint(f[e].w);
             }
           } else {
             tmem_ld16_nowait(tmem + kTState + lanes + h * 64 + 16 * q, v);
             tmem_ld_wait();
           }
+          if constexpr (!kLocal) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             uint4 w;
@@ -340,6 +386,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
             w.w = pack_bf16(__uint_as_float(v[8 * e + 6]), __uint_as_float(v[8 * e + 7]));
             *(uint4*)(hrow + (((2 * q + e) ^ (pp & 7)) << 4)) = w;
           }
+          }
           scale_regs<16>(v, dec);
           tmem_st16(tmem + kTState + lanes + h * 64 + 16 * q, v);
         }
@@ -347,7 +394,9 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
         fence_proxy_async_smem();
       }
       tc_fence_before();
+      if constexpr (kLocal) decayed += slast[h];
       arrive_warp(L::kHFull);
+      if constexpr (kLocal) continue;
       // ---- M, over G once both heads have read G
       wait_warp(L::kG, c & 1);
       tc_fence_after();
@@ -430,15 +479,17 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
       tc_fence_before();
       arrive_warp(L::kMFull);
     }
+    if (kLocal && row == 0) p.seg_decay[2 * blockIdx.x + h] = decayed;
     // ---- the state after the last token
     wait_warp(L::kS, (chunks - 1) & 1);
     tc_fence_after();
 #pragma unroll 1
-    for (int q = 0; q < 2; ++q) {
+    for (int q = 0; q < 2 && (kLocal || last_seg); ++q) {
       uint32_t v[32];
       tmem_ld32(tmem + kTState + lanes + h * 64 + q * 32, v);
       tmem_ld_wait();
-      float4* dst = (float4*)(p.state_out + state_at + 32 * q);
+      float4* dst = (float4*)(kLocal ? p.seg_state + (size_t)blockIdx.x * (128 * kSsmN) + row * kSsmN + h * 64 + 32 * q
+                                     : p.state_out + state_at + 32 * q);
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         dst[e] = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]), __uint_as_float(v[4 * e + 2]),
@@ -462,8 +513,10 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
           const int n = min(kQ, left);
           wait_warp(L::kXEmpty + b, parity ^ 1);
           copy_tile<2 * kSsmP>(sb + L::kX + b * 2 * kXT, p.zx, p.zx_stride, di + h0 * kSsmP, row0, n);
-          wait_warp(L::kOut + b, parity ^ 1);
-          copy_tile<kSsmN>(sb + c_tile(k), p.zx, p.zx_stride, 2 * di + kSsmN, row0, n);
+          if constexpr (!kLocal) {
+            wait_warp(L::kOut + b, parity ^ 1);
+            copy_tile<kSsmN>(sb + c_tile(k), p.zx, p.zx_stride, 2 * di + kSsmN, row0, n);
+          }
           wait_warp(L::kBEmpty, (k & 1) ^ 1);
           copy_tile<kSsmN>(sb + L::kB, p.zx, p.zx_stride, 2 * di, row0, n);
           asm volatile("cp.async.wait_all;" ::: "memory");
@@ -554,7 +607,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
         tc_fence_before();
         arrive_warp(L::kWx);
       }
-      if (c < 0) continue;
+      if (kLocal || c < 0) continue;
       const int b = c & 1, left = len - c * kQ;
       // ---- the output: y, gated, over z's row and from there to global
       uint8_t* ztile = smem + z_tile(c) + h * kXT;
@@ -632,10 +685,10 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
         const uint32_t ct = sb + c_tile(c), bt = sb + L::kB;
         const bool zero = c == 0 && !goes_on;
         wait_warp(L::kBFull, c & 1);
-        wait_warp(L::kCFull + (c & 1), (c >> 1) & 1);
+        if constexpr (!kLocal) wait_warp(L::kCFull + (c & 1), (c >> 1) & 1);
         if (!ok) break;
         tc_fence_after();
-        if (elect_one()) {  // G = C B^T
+        if (!kLocal && elect_one()) {  // G = C B^T
           const uint32_t cm = sdesc_lo(ct), bm = sdesc_lo(bt);
           mma_ss<false>(tmem + kTG, cm, bm, id_g);
 #pragma unroll
@@ -657,6 +710,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
           tc_commit(bar(L::kBEmpty));
         }
         __syncwarp();
+        if constexpr (!kLocal) {
         if (c > 0) wait_warp(L::kYFree, (c - 1) & 1);
         if (!ok) break;
         tc_fence_after();
@@ -690,6 +744,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
           }
           __syncwarp();
         }
+        }
         if (elect_one()) tc_commit(bar(L::kXEmpty + (c & 1)));
         __syncwarp();
       }
@@ -717,13 +772,15 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
           wait_warp(L::kXEmpty + (c & 1), parity);
           if (!ok) break;
           copy(sb + L::kX + (c & 1) * 2 * kXT, di + h0 * kSsmP, c, L::kXFull + (c & 1));
-          wait_warp(L::kOut + (c & 1), parity);  // z of two chunks before
-          if (!ok) break;
-          copy(sb + c_tile(c), 2 * di + kSsmN, c, L::kCFull + (c & 1));
+          if constexpr (!kLocal) {
+            wait_warp(L::kOut + (c & 1), parity);  // z of two chunks before
+            if (!ok) break;
+            copy(sb + c_tile(c), 2 * di + kSsmN, c, L::kCFull + (c & 1));
+          }
           wait_warp(L::kBEmpty, (c & 1) ^ 1);
           if (!ok) break;
           copy(sb + L::kB, 2 * di, c, L::kBFull);
-        } else {
+        } else if constexpr (!kLocal) {
           if (c > 0) wait_warp(L::kY2 + ((c - 1) & 1), ((c - 1) >> 1) & 1);  // C of the chunk before
           if (!ok) break;
           copy(sb + z_tile(c), h0 * kSsmP, c, L::kZFull + (c & 1));
@@ -791,7 +848,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
         if (c + 1 < chunks) fetch(c + 1);
         if (c > 0) {  // the last chunk's have been read
           wait_warp(L::kWx, (c - 1) & 1);
-          wait_warp(L::kMFull, (c - 1) & 1);
+          wait_warp(kLocal ? L::kHFull : L::kMFull, (c - 1) & 1);
           if (!ok) break;
         }
 #pragma unroll
@@ -816,6 +873,15 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
   __syncthreads();
   tc_fence_after();
   if (warp == 16) tmem_dealloc(tmem, 512);
+}
+
+// Once per device, when a handle is made.
+cudaError_t configure_prompt_state() {
+  const cudaError_t e =
+      cudaFuncSetAttribute(k_prompt_state<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, StateSmem::kTotal);
+  return e != cudaSuccess
+             ? e
+             : cudaFuncSetAttribute(k_prompt_state<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, StateSmem::kTotal);
 }
 
 }  // namespace wave
@@ -873,9 +939,28 @@ extern "C" int wave_hybrid_prompt_state(wave_t* h, int layer, const void* weight
   p.tiled = zx_stride % 8 == 0;
   if (take(true)) {
     if (p.tiled && encode_rows_map(&p.tm, zxbcdt, pl.in_rows, 1, cu_seqlens[n_seq], zx_stride, kQ)) return WAVE_ECUDA;
-    if (cudaFuncSetAttribute(k_prompt_state, cudaFuncAttributeMaxDynamicSharedMemorySize, StateSmem::kTotal) != cudaSuccess)
-      return WAVE_ECUDA;
-    k_prompt_state<<<p.b.n * (Hs / 2), kStateThreads, StateSmem::kTotal, st>>>(p);
+    // Segments: the longest that give no more CTAs than SMs, if that is worth
+    // a second launch.  A chunk of the first costs about half of one of the
+    // second, and a launch about one (2048 tokens of 64 heads, 32 CTAs of 16
+    // chunks: 77 us whole).
+    const int pairs = Hs / 2, sms = pl.grid, longest = (p.b.len(0) + kQ - 1) / kQ;
+    p.seg_chunks = 0;
+    auto segments = [&](int t) {
+      int n = 0;
+      for (int i = 0; i < p.b.n; ++i) n += ((p.b.len(i) + kQ - 1) / kQ + t - 1) / t;
+      return n;
+    };
+    int t = 1;
+    while (t < longest && segments(t) * pairs > sms) ++t;
+    if (3 * t + 4 < 2 * longest && segments(t) * pairs <= sms) p.seg_chunks = t;
+    p.seg_cum[0] = 0;
+    for (int i = 0; i < p.b.n; ++i)
+      p.seg_cum[i + 1] = p.seg_cum[i] + (p.seg_chunks ? ((p.b.len(i) + kQ - 1) / kQ + t - 1) / t : 1);
+    p.seg_state = h->ws.seg_state;
+    p.seg_decay = h->ws.seg_decay;
+    const int ctas = p.seg_cum[p.b.n] * pairs;
+    if (p.seg_chunks) k_prompt_state<true><<<ctas, kStateThreads, StateSmem::kTotal, st>>>(p);
+    k_prompt_state<false><<<ctas, kStateThreads, StateSmem::kTotal, st>>>(p);
   }
   if (take(false)) k_prompt_state_rows<<<dim3(Hs, p.b.n), 256, 0, st>>>(p);
   return cudaGetLastError() == cudaSuccess ? WAVE_OK : WAVE_ECUDA;

@@ -401,6 +401,24 @@ def test_state_lengths(lens, hs):
             assert bool((new[0, s] == 9).all())
 
 
+@pytest.mark.parametrize("hs,lens,starts", [(4, [2600], [0]), (4, [1281], [3]), (8, [1500, 9, 900, 640], [0, 2, 5, 0]),
+                                            (12, [700, 700], [1, 0]), (64, [2048], [0])])
+def test_state_long_sequences_of_few_heads(hs, lens, starts):
+    """Sequences cut into segments over the SMs: the state passes from one to
+    the next, from zero and from an earlier one."""
+    n = len(lens)
+    cu, zx, prm, h0, out = _state_case(lens, hs, starts, seed=hs, S=n)
+    cfg, w = _hybrid(hs, S=n)
+    new = torch.full_like(h0, 9.0)
+    try:
+        for _ in range(2):  # the scratch of one call is no part of the next
+            w.prompt_state(0, _weights(cfg, prm), cu, list(range(n)), starts, zx, h0, new, out)
+        assert w.status() == fsd.WAVE_OK
+    finally:
+        w.close()
+    _check_state(cu, zx, prm, h0, list(range(n)), starts, hs, out, new, n)
+
+
 def test_state_in_place_in_parts_and_left_out():
     """A prompt in one call, and in three calls on the same buffer, each going
     on from the state of the last; a left-out sequence keeps its state."""
