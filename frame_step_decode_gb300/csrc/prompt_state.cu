@@ -18,9 +18,10 @@ using namespace wave;
 
 namespace wave {
 
-// Sequences of at most this many tokens go token by token (a launch of the
-// chunked form costs some microseconds whatever its length).
-constexpr int kRowTokens = 8;
+// Sequences of at most this many tokens go token by token: 0.65 us a token
+// against 13 us for a chunk (one sequence), 2.9 us a token against 48 us (16
+// sequences of 64 heads), whatever the tokens in it.
+constexpr int kRowTokens = 16;
 
 struct StateParams {
   SeqBatch b;
@@ -59,15 +60,34 @@ __global__ void __launch_bounds__(256) k_prompt_state_rows(const __grid_constant
   const float a_neg = -expf(bf(p.prm[h])), bias = bf(p.prm[p.Hs + h]), Dh = bf(p.prm[2 * p.Hs + h]);
   const uint16_t* row = p.zx + (size_t)p.b.begin[i] * p.zx_stride;
   uint16_t* orow = p.out + (size_t)p.b.begin[i] * p.out_stride + h * kSsmP + warp * 8;
-  for (int t = 0; t < n; ++t, row += p.zx_stride, orow += p.out_stride) {
-    const float raw = bf(row[2 * di + 2 * kSsmN + h]) + bias;
+  // lanes with (lane & 3) == 0 finish row 4 b4 + 2 b3 + b2 (their bits 4, 3, 2)
+  const bool h4 = lane & 16, h3 = lane & 8, h2 = lane & 4;
+  const int mine = (h4 ? 4 : 0) + (h3 ? 2 : 0) + (h2 ? 1 : 0);
+  struct Token {  // a token's values, loaded one token ahead
+    uint2 x0, x1, B, C;
+    uint16_t dt, xm, zm;
+  };
+  auto load = [&](const uint16_t* r) {
+    Token k;
+    k.dt = r[2 * di + 2 * kSsmN + h];
+    k.x0 = *(const uint2*)(r + di + h * kSsmP + warp * 8);
+    k.x1 = *(const uint2*)(r + di + h * kSsmP + warp * 8 + 4);
+    k.B = *(const uint2*)(r + 2 * di + 4 * lane);
+    k.C = *(const uint2*)(r + 2 * di + kSsmN + 4 * lane);
+    k.xm = r[di + h * kSsmP + warp * 8 + mine];
+    k.zm = r[h * kSsmP + warp * 8 + mine];
+    return k;
+  };
+  Token next = load(row);
+  for (int t = 0; t < n; ++t, orow += p.out_stride) {
+    const Token k = next;
+    if (t + 1 < n) next = load(row += p.zx_stride);
+    const float raw = bf(k.dt) + bias;
     const float dt = raw > 0.f ? raw + log1pf(expf(-raw)) : log1pf(expf(raw));
     const float a = expf(a_neg * dt);
-    const uint2 x0 = *(const uint2*)(row + di + h * kSsmP + warp * 8), x1 = *(const uint2*)(row + di + h * kSsmP + warp * 8 + 4);
-    const uint2 Bq = *(const uint2*)(row + 2 * di + 4 * lane), Cq = *(const uint2*)(row + 2 * di + kSsmN + 4 * lane);
-    const float4 B = make_float4(bf((uint16_t)Bq.x), bf((uint16_t)(Bq.x >> 16)), bf((uint16_t)Bq.y), bf((uint16_t)(Bq.y >> 16)));
-    const float4 C = make_float4(bf((uint16_t)Cq.x), bf((uint16_t)(Cq.x >> 16)), bf((uint16_t)Cq.y), bf((uint16_t)(Cq.y >> 16)));
-    const uint32_t xw[4] = {x0.x, x0.y, x1.x, x1.y};
+    const float4 B = make_float4(bf((uint16_t)k.B.x), bf((uint16_t)(k.B.x >> 16)), bf((uint16_t)k.B.y), bf((uint16_t)(k.B.y >> 16)));
+    const float4 C = make_float4(bf((uint16_t)k.C.x), bf((uint16_t)(k.C.x >> 16)), bf((uint16_t)k.C.y), bf((uint16_t)(k.C.y >> 16)));
+    const uint32_t xw[4] = {k.x0.x, k.x0.y, k.x1.x, k.x1.y};
     float x[8], y[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -79,8 +99,7 @@ __global__ void __launch_bounds__(256) k_prompt_state_rows(const __grid_constant
       st[j].w = fmaf(a, st[j].w, u * B.w);
       y[j] = st[j].x * C.x + st[j].y * C.y + st[j].z * C.z + st[j].w * C.w;
     }
-    // row sums by recursive halving: lane bits 4, 3, 2 pick the row 4 b4 + 2 b3 + b2
-    const bool h4 = lane & 16, h3 = lane & 8, h2 = lane & 4;
+    // row sums by recursive halving
 #pragma unroll
     for (int j = 0; j < 4; ++j) y[j] = (h4 ? y[j + 4] : y[j]) + __shfl_xor_sync(0xffffffffu, h4 ? y[j] : y[j + 4], 16);
 #pragma unroll
@@ -89,9 +108,8 @@ __global__ void __launch_bounds__(256) k_prompt_state_rows(const __grid_constant
     y[0] += __shfl_xor_sync(0xffffffffu, y[0], 2);
     y[0] += __shfl_xor_sync(0xffffffffu, y[0], 1);
     if ((lane & 3) == 0) {
-      const int j = (h4 ? 4 : 0) + (h3 ? 2 : 0) + (h2 ? 1 : 0);
-      const float xp = bf(row[di + h * kSsmP + warp * 8 + j]), z = bf(row[h * kSsmP + warp * 8 + j]);
-      orow[j] = __bfloat16_as_ushort(__float2bfloat16_rn((y[0] + Dh * xp) * z / (1.0f + expf(-z))));
+      const float xp = bf(k.xm), z = bf(k.zm);
+      orow[mine] = __bfloat16_as_ushort(__float2bfloat16_rn((y[0] + Dh * xp) * z / (1.0f + expf(-z))));
     }
   }
 #pragma unroll
