@@ -6,6 +6,7 @@ is not built, importing the binding's entry points raises.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -159,15 +160,15 @@ _ARRAYS: dict = {}  # ctypes array types by length
 
 
 def _ints(values):
-    """A host array of int32 (any sequence of integers), and its length."""
+    """A host array of int32 (any sequence of integers that fit), and its length."""
     n = len(values)
     t = _ARRAYS.get(n)
     if t is None:
-        t = _ARRAYS[n] = ctypes.c_int32 * max(1, n)
+        t = _ARRAYS[n] = ctypes.c_int32 * n
     try:
-        return t(*values), n
-    except TypeError:  # elements that are integers, but not Python's
-        return t(*[int(v) for v in values]), n
+        return t.from_buffer(array.array("i", values)) if n else t(), n
+    except (OverflowError, TypeError) as e:
+        raise ValueError("a sequence of 32-bit integers is wanted") from e
 
 
 def _types() -> dict:

@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(kAppendThreads) k_prompt_append(const __grid_c
   constexpr int G = D / 4;  // lanes per row: 32 or 16
   const int lane = threadIdx.x % G;
   const int chunks = (p.H + kAppendHeads - 1) / kAppendHeads;
-    const int t = (int)(blockIdx.x / chunks) * (kAppendThreads / G) + (int)threadIdx.x / G;
+  const int t = (int)(blockIdx.x / chunks) * (kAppendThreads / G) + (int)threadIdx.x / G;
   const int h0 = (int)(blockIdx.x % chunks) * kAppendHeads;
   const bool live = t < p.b.cum[p.b.n];  // the shuffles below need whole warps
   const int i = live ? seq_of(p.b, t) : 0;
@@ -166,8 +166,8 @@ extern "C" int wave_prompt_append(wave_t* h, int layer, int n_seq, const int32_t
   if (la < 0 || la >= pl.cfg.n_layers) return WAVE_EINVAL;
   if ((qkv_type != WAVE_F32 && qkv_type != WAVE_BF16) || (out_type != WAVE_BF16 && out_type != WAVE_F16))
     return WAVE_EINVAL;
-  if (row_stride < 3LL * H * D || row_stride % 8 || !aligned16(qkv) || !aligned16(kv_fp8) || !aligned16(kv_scales) ||
-      !aligned16(q) || !aligned16(k) || !aligned16(v))
+  if (row_stride < 3LL * H * D || row_stride % 8 || row_stride > kMaxStride || !aligned16(qkv) || !aligned16(kv_fp8) ||
+      !aligned16(kv_scales) || !aligned16(q) || !aligned16(k) || !aligned16(v))
     return WAVE_EINVAL;
   AppendParams p;
   const int rc = make_batch(&p.b, n_seq, cu_seqlens, slots, starts, pl.S_max);

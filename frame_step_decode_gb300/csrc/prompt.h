@@ -66,6 +66,8 @@ __device__ __forceinline__ int seq_of(const SeqBatch& b, int t) {
   return lo;
 }
 
+constexpr int64_t kMaxStride = (1LL << 31) - 1;  // elements between rows: what a tensor map can describe
+
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
 // Whether the handle's device is the current one (a launch elsewhere would

@@ -22,6 +22,7 @@ namespace wave {
 
 constexpr int kRows = 128;         // query rows of one stream, and keys of one block
 constexpr int kAttnThreads = 384;  // 8 softmax warps (two streams), then copies, MMAs, guard, scheduler
+constexpr int kRegsSoftmax = 208, kRegsRest = 80;  // a row's 128 scores stay in registers
 
 struct AttnParams {
   CUtensorMap tm_q, tm_k, tm_v;
@@ -185,7 +186,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __gr
 
   if (warp < 8) {
     // ---------------------------------------------------------------- softmax
-    regs_take<208>();
+    regs_take<kRegsSoftmax>();
     const int st = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     uint32_t s_it = 0, o_it = 0;
@@ -320,7 +321,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __gr
       if (!live) break;
     }
   } else {
-    regs_give<80>();
+    regs_give<kRegsRest>();
     if (warp == 8) {
       // ------------------------------------------------------------- copies
       if (lane == 0) {
@@ -580,8 +581,8 @@ static cudaError_t launch_attention(const AttnParams& p, int grid, cudaStream_t 
 
 template <int D, bool kF16>
 static cudaError_t configure() {
-  return cudaFuncSetAttribute(k_prompt_attention<D, kF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              AttnSmem<D>::kTotal);
+  return configure_split(k_prompt_attention<D, kF16>, kAttnThreads, 256 * kRegsSoftmax + 128 * kRegsRest,
+                         AttnSmem<D>::kTotal);
 }
 
 // Once per device, when a handle is made.
@@ -605,7 +606,7 @@ extern "C" int wave_prompt_attention(wave_t* h, int n_seq, const int32_t* cu_seq
   const int64_t strides[4] = {q_stride, k_stride, v_stride, out_stride};
   const void* ptrs[4] = {q, k, v, out};
   for (int i = 0; i < 4; ++i)
-    if (strides[i] < least[i] || strides[i] % 8 || strides[i] >= (1LL << 31) || !aligned16(ptrs[i])) return WAVE_EINVAL;
+    if (strides[i] < least[i] || strides[i] % 8 || strides[i] > kMaxStride || !aligned16(ptrs[i])) return WAVE_EINVAL;
   if (!on_device(h)) return WAVE_EINVAL;
   AttnParams p;
   // the sequences that have tokens, longest first

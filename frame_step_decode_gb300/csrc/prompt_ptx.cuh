@@ -2,6 +2,7 @@
 // step kernel's are in ptx.cuh).
 #pragma once
 #include <cuda.h>
+#include <cuda_runtime.h>
 #include <stdint.h>
 
 #include "ptx.cuh"
@@ -159,6 +160,18 @@ __device__ __forceinline__ void regs_take() {
 template <int kRegs>
 __device__ __forceinline__ void regs_give() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+// The attributes of a kernel whose warps divide the registers of the launch
+// among themselves anew: an error if they would ask for more than it has (they
+// would wait for ever).
+template <typename K>
+inline cudaError_t configure_split(K kernel, int threads, int registers, int smem) {
+  cudaFuncAttributes a;
+  const cudaError_t e = cudaFuncGetAttributes(&a, kernel);
+  if (e != cudaSuccess) return e;
+  if (a.numRegs * threads < registers) return cudaErrorInvalidConfiguration;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
 }
 
 // What a kernel with bounded waits reports to: the handle's error word and

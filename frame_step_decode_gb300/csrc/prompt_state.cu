@@ -27,7 +27,7 @@ struct StateParams {
   SeqBatch b;
   CUtensorMap tm;          // the rows of zx as tiles of 64 columns x 128 tokens
   int tiled;               // whether tm is there: a row stride of a multiple of 16 bytes
-  int Hs, S_max;
+  int Hs;
   const uint16_t* zx;      // [rows][zx_stride] bf16: z | x | B | C | dt
   const uint16_t* prm;     // A_log[Hs] | dt_bias[Hs] | D[Hs]
   const float* state_in;   // the layer's [S_max][Hs][64][128]
@@ -37,7 +37,8 @@ struct StateParams {
   // Few sequences and heads leave SMs idle: a long sequence is then cut into
   // segments of seg_chunks chunks, a CTA each.  A first launch makes every
   // segment's state from zero, the second begins each segment from those
-  // before it.
+  // before it.  The last segment's place holds the state that the sequence
+  // begins from: state_out, which the second launch writes, may be state_in.
   int seg_chunks;                      // 0: whole sequences
   int32_t seg_cum[WAVE_MAX_SEQS + 1];  // segments before sequence i
   float* seg_state;                    // [segment and head pair][128 rows (head, p)][128]
@@ -128,31 +129,30 @@ __global__ void __launch_bounds__(256) k_prompt_state_rows(const __grid_constant
 // from TMEM, and the state with (w X)^T read from TMEM and its accumulator,
 // the fp32 state of both heads (row = head, p; column = n), staying in TMEM
 // over the whole sequence.  M and the H of C H^T are rounded to bf16 once
-// (the output is bf16); (w X)^T is split into a bf16 and the bf16 of its
-// remainder (2^-18), since the state is carried on in fp32.
+// (the output is bf16).  The state is fp32, so (w X)^T is the sum of three bf16
+// parts, all of fp32's 24 bits: with two the state was 2.4e-6 off (2-norm),
+// with three 2e-7, the tensor core's own sums.
 //
-// Seven warpgroups: two in front (a head each: the decays, the state's pass
-// between chunks, M), four behind (the weights w, (w X)^T, the gated output),
-// and one warp each for the MMAs, the copies of B, C, x and those of z.  The
-// chain from chunk to chunk is the state's: its pass and its product.
+// Two warpgroups in front (a head each: the state's pass between chunks, M),
+// two behind (a head each: (w X)^T, the gated output), and a warp each for the
+// MMAs, the copies of x, C and B, those of z, and the decays.  The chain from
+// chunk to chunk is the state's: its pass, (w X)^T and its product.
 constexpr int kQ = 128;                 // tokens of a chunk
 constexpr int kStateThreads = 640;      // 2 warpgroups in front, 2 behind, 4 single warps
 constexpr int kBehind = 256;
-// Registers: 640 threads are launched with 96 each (61440).
-constexpr int kRegsFront = 104, kRegsBehind = 104, kRegsRest = 64;
-static_assert(256 * kRegsFront + kBehind * kRegsBehind + 128 * kRegsRest <= kStateThreads * 96, "registers");
+constexpr int kRegsFront = 104, kRegsBehind = 104, kRegsRest = 64;  // 640 threads are launched with 96 each
 constexpr int kBC = kQ * kSsmN * 2;     // bytes of the B (or C) tile
 constexpr int kXT = kQ * kSsmP * 2;     // ... of one head's x (or z) tile
 
 struct StateSmem {
-  // One B; x of two chunks (both heads); three tiles that C and z take turns
-  // with: C_0, z_0, C_1, ...  C's tile is free once its two products are done,
-  // z's once the output has left it (z becomes out in place), so that z is
-  // there a chunk before it is needed and neither waits for the other.
+  // One each of B, C and z (which becomes out in place), x of two chunks: x is
+  // read by the products of two chunks at once.
   static constexpr int kB = 0;
-  static constexpr int kX = kB + kBC;
-  static constexpr int kRing = kX + 2 * 2 * kXT;
-  static constexpr int kH = kRing + 3 * kBC;      // bf16 H of both heads: [2][n / 64][64 rows of 128 B]
+  static constexpr int kC = kB + kBC;
+  static constexpr int kZ = kC + kBC;
+  static constexpr int kX = kZ + kBC;
+  static constexpr int kLo = kX + 2 * 2 * kXT;    // the last part of (w X)^T: [tokens / 64][128 rows (head, p) of 128 B]
+  static constexpr int kH = kLo + kBC;            // bf16 H: [n / 64][128 rows (head, p) of 128 B]
   static constexpr int kAfter = kH + 2 * kXT;     // [head][128] the decays behind token j, to the chunk's end
   static constexpr int kV = kAfter + 2 * kQ * 4;  // [head][128] log2 dt_j - after_j
   static constexpr int kU = kV + 2 * kQ * 4;      // [head][96] dt_j 2^-(the decays behind j in its 32 tokens)
@@ -184,8 +184,8 @@ struct StateSmem {
 };
 static_assert(StateSmem::kTotal <= 232448, "the chunked state form does not fit shared memory");
 
-// TMEM columns: G (the heads' M later, 64 each), (w X)^T (high parts, then
-// remainders), the state, Y of each head.
+// TMEM columns: G (the heads' M later, 64 each), (w X)^T (its first two parts;
+// there is no room for the third), the state, Y of each head.
 constexpr int kTG = 0, kTWx = 128, kTState = 256, kTY = 384;
 
 __device__ __forceinline__ void bar_sync(int id, int threads) {
@@ -276,7 +276,14 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
   len = p.b.len(seq) - off;
   const bool last_seg = !p.seg_chunks || len <= p.seg_chunks * kQ;
   if (!last_seg) len = p.seg_chunks * kQ;
-  if (kLocal && last_seg) return;
+  if (kLocal && last_seg) {
+    if (p.b.start[seq] > 0) {
+      const float4* src = (const float4*)p.state_in + ((size_t)p.b.slot[seq] * p.Hs + h0) * (kSsmP * kSsmN / 4);
+      float4* dst = (float4*)p.seg_state + (size_t)blockIdx.x * (128 * kSsmN / 4);
+      for (int i = threadIdx.x; i < 128 * kSsmN / 4; i += kStateThreads) dst[i] = src[i];
+    }
+    return;
+  }
   const size_t first = (size_t)p.b.begin[seq] + off;
   const int chunks = (len + kQ - 1) / kQ;
   const bool from_in = !kLocal && p.b.start[seq] > 0;   // the sequence begins from state_in, not from zero
@@ -338,8 +345,6 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(b));
   };
-  auto c_tile = [&](int c) { return L::kRing + (2 * c) % 3 * kBC; };
-  auto z_tile = [&](int c) { return L::kRing + (2 * c + 1) % 3 * kBC; };
   const int h = (warp >> 2) & 1, quad = warp & 3, row = quad * 32 + lane;  // a thread per token of head h0 + h
   const uint32_t lanes = (uint32_t)(quad * 32) << 16;
   const int hh = row >> 6, pp = row & 63;  // for the state: row (head hh, p)
@@ -356,6 +361,9 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
     regs_take<kRegsFront>();
     const float skip = bf(p.prm[2 * p.Hs + head]);
     float decayed = 0.f;  // kLocal: the decays so far, of head h
+    const float* begin = p.seg_chunks ? p.seg_state + (size_t)(seg0 + (p.seg_cum[seq + 1] - p.seg_cum[seq] - 1) * pairs) * (128 * kSsmN) +
+                                            row * kSsmN + h * 64
+                                      : p.state_in + state_at;
     for (int c = 0; c < chunks; ++c) {
       // ---- the state: its bf16 copy for C H^T, and the chunk's decay
       wait_warp(L::kScan, c & 1);
@@ -365,12 +373,12 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
       const bool zero = c == 0 && !goes_on;
       if (!zero) {
         const float dec = ex2(-slast[hh]);
-        uint8_t* hrow = smem + L::kH + hh * kXT + h * (64 * 128) + pp * 128;
+        uint8_t* hrow = smem + L::kH + h * (128 * 128) + row * 128;
 #pragma unroll 1
         for (int q = 0; q < 4; ++q) {
           uint32_t v[16];
           if (!kLocal && c == 0) {
-            const float4* src = (const float4*)(p.state_in + state_at + 16 * q);
+            const float4* src = (const float4*)(begin + 16 * q);
             float4 f[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) f[e] = from_in ? src[e] : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -396,14 +404,14 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
           }
           if constexpr (!kLocal) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            uint4 w;
-            w.x = pack_bf16(__uint_as_float(v[8 * e]), __uint_as_float(v[8 * e + 1]));
-            w.y = pack_bf16(__uint_as_float(v[8 * e + 2]), __uint_as_float(v[8 * e + 3]));
-            w.z = pack_bf16(__uint_as_float(v[8 * e + 4]), __uint_as_float(v[8 * e + 5]));
-            w.w = pack_bf16(__uint_as_float(v[8 * e + 6]), __uint_as_float(v[8 * e + 7]));
-            *(uint4*)(hrow + (((2 * q + e) ^ (pp & 7)) << 4)) = w;
-          }
+            for (int e = 0; e < 2; ++e) {
+              uint4 w;
+              w.x = pack_bf16(__uint_as_float(v[8 * e]), __uint_as_float(v[8 * e + 1]));
+              w.y = pack_bf16(__uint_as_float(v[8 * e + 2]), __uint_as_float(v[8 * e + 3]));
+              w.z = pack_bf16(__uint_as_float(v[8 * e + 4]), __uint_as_float(v[8 * e + 5]));
+              w.w = pack_bf16(__uint_as_float(v[8 * e + 6]), __uint_as_float(v[8 * e + 7]));
+              *(uint4*)(hrow + (((2 * q + e) ^ (pp & 7)) << 4)) = w;
+            }
           }
           scale_regs<16>(v, dec);
           tmem_st16(tmem + kTState + lanes + h * 64 + 16 * q, v);
@@ -532,8 +540,8 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
           wait_warp(L::kXEmpty + b, parity ^ 1);
           copy_tile<2 * kSsmP>(sb + L::kX + b * 2 * kXT, p.zx, p.zx_stride, di + h0 * kSsmP, row0, n);
           if constexpr (!kLocal) {
-            wait_warp(L::kOut + b, parity ^ 1);
-            copy_tile<kSsmN>(sb + c_tile(k), p.zx, p.zx_stride, 2 * di + kSsmN, row0, n);
+            if (k > 0) wait_warp(L::kY2 + ((k - 1) & 1), ((k - 1) >> 1) & 1);
+            copy_tile<kSsmN>(sb + L::kC, p.zx, p.zx_stride, 2 * di + kSsmN, row0, n);
           }
           wait_warp(L::kBEmpty, (k & 1) ^ 1);
           copy_tile<kSsmN>(sb + L::kB, p.zx, p.zx_stride, 2 * di, row0, n);
@@ -599,17 +607,27 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
             const float2 r1 = mul2(make_float2(v[4 * e + 2], v[4 * e + 3]), mul2(make_float2(u4.z, u4.w), make_float2(tail, tail)));
             v[4 * e] = r0.x, v[4 * e + 1] = r0.y, v[4 * e + 2] = r1.x, v[4 * e + 3] = r1.y;
           }
-          uint32_t hi[8], lo[8];
+          uint32_t part[3][8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            hi[e] = pack_bf16(v[2 * e], v[2 * e + 1]);
-            const float2 r = sub2(make_float2(v[2 * e], v[2 * e + 1]),
-                                  make_float2(__uint_as_float(hi[e] << 16), __uint_as_float(hi[e] & 0xFFFF0000u)));
-            lo[e] = pack_bf16(r.x, r.y);
+          for (int t = 0; t < 3; ++t) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              part[t][e] = pack_bf16(v[2 * e], v[2 * e + 1]);
+              if (t == 2) continue;
+              const float2 r = sub2(make_float2(v[2 * e], v[2 * e + 1]),
+                                    make_float2(__uint_as_float(part[t][e] << 16), __uint_as_float(part[t][e] & 0xFFFF0000u)));
+              v[2 * e] = r.x, v[2 * e + 1] = r.y;
+            }
           }
-          tmem_st8(tmem + kTWx + lanes + h * 32 + q * 8, hi);
-          tmem_st8(tmem + kTWx + 64 + lanes + h * 32 + q * 8, lo);
+          tmem_st8(tmem + kTWx + lanes + h * 32 + q * 8, part[0]);
+          tmem_st8(tmem + kTWx + 64 + lanes + h * 32 + q * 8, part[1]);
+          uint8_t* lrow = smem + L::kLo + h * (128 * 128) + row * 128;
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            *(uint4*)(lrow + (((2 * q + e) ^ (row & 7)) << 4)) =
+                make_uint4(part[2][4 * e], part[2][4 * e + 1], part[2][4 * e + 2], part[2][4 * e + 3]);
         }
+        fence_proxy_async_smem();
         tmem_st_wait();
         if (*(volatile uint32_t*)sbad >> ((k & 3) * 8) & 0xFFu) {  // seen by every thread or none
           bar_sync(4, kBehind);
@@ -628,11 +646,11 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
       if (kLocal || c < 0) continue;
       const int b = c & 1, left = len - c * kQ;
       // ---- the output: y, gated, over z's row and from there to global
-      uint8_t* ztile = smem + z_tile(c) + h * kXT;
+      uint8_t* ztile = smem + L::kZ + h * kXT;
       const uint32_t any_bad = *(volatile uint32_t*)sbad >> ((c & 3) * 8 + h * 4) & 15u;
       if (!p.tiled) {
-        if (c > 0) wait_warp(L::kY2 + ((c - 1) & 1), ((c - 1) >> 1) & 1);
-        copy_tile<2 * kSsmP>(sb + z_tile(c), p.zx, p.zx_stride, h0 * kSsmP, first + (size_t)c * kQ, min(kQ, left));
+        if (c > 0) wait_warp(L::kOut + ((c - 1) & 1), ((c - 1) >> 1) & 1);
+        copy_tile<2 * kSsmP>(sb + L::kZ, p.zx, p.zx_stride, h0 * kSsmP, first + (size_t)c * kQ, min(kQ, left));
         asm volatile("cp.async.wait_all;" ::: "memory");
         arrive_warp(L::kZFull + b);
       }
@@ -696,11 +714,11 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
     regs_give<kRegsRest>();
     if (warp == 16) {
       // ---------------------------------------------------------------- MMAs
-      constexpr uint32_t id_g = idesc_16(128, 128, false, false, false), id_y2 = idesc_16(128, 64, false, false, false),
-                         id_y = idesc_16(128, 64, false, false, true), id_s = idesc_16(128, 128, false, false, true);
+      constexpr uint32_t id_g = idesc_16(128, 128, false, false, false), id_y = idesc_16(128, 64, false, false, true),
+                         id_s = idesc_16(128, 128, false, false, true);
       constexpr uint32_t kBlk = (kQ * 128) >> 4;  // the next 64 columns of a tile, as a descriptor counts
       for (int c = 0; c < chunks; ++c) {
-        const uint32_t ct = sb + c_tile(c), bt = sb + L::kB;
+        const uint32_t ct = sb + L::kC, bt = sb + L::kB;
         const bool zero = c == 0 && !goes_on;
         wait_warp(L::kBFull, c & 1);
         if constexpr (!kLocal) wait_warp(L::kCFull + (c & 1), (c >> 1) & 1);
@@ -719,49 +737,48 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
         wait_warp(L::kWx, c & 1);
         if (!ok) break;
         tc_fence_after();
-        if (elect_one()) {  // the state += (w X)^T B: the high parts, then the remainders
-          const uint32_t bm = sdesc_lo(bt, kQ * 128);
+        if (elect_one()) {  // the state += (w X)^T B, its three parts
+          const uint32_t bm = sdesc_lo(bt, kQ * 128), lm = sdesc_lo(sb + L::kLo);
 #pragma unroll
           for (int e = 0; e < 16; ++e)
             mma_ts(tmem + kTState, tmem + kTWx + 8 * e, bm + (e % 8) * (2048 >> 4), id_s, e > 0 ? 1u : zero ? 0u : 1u);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            mma_ss<true>(tmem + kTState, lm + (e / 4) * kBlk + (e % 4) * 2, bm + e * (2048 >> 4), id_s);
           tc_commit(bar(L::kS));
           tc_commit(bar(L::kBEmpty));
         }
         __syncwarp();
         if constexpr (!kLocal) {
-        if (c > 0) wait_warp(L::kYFree, (c - 1) & 1);
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {  // Y = C H^T
-          if (!zero) {
-            const uint32_t cm = sdesc_lo(ct), hm = sdesc_lo(sb + L::kH);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              mma_ss<false>(tmem + kTY + h * 64, cm, hm + h * (kXT >> 4), id_y2);
+          if (c > 0) wait_warp(L::kYFree, (c - 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {  // Y = C H^T, of both heads at once
+            if (!zero) {
+              const uint32_t cm = sdesc_lo(ct), hm = sdesc_lo(sb + L::kH);
+              mma_ss<false>(tmem + kTY, cm, hm, id_g);
 #pragma unroll
               for (int e = 1; e < 8; ++e)
-                mma_ss<true>(tmem + kTY + h * 64, cm + (e / 4) * kBlk + (e % 4) * 2,
-                             hm + ((h * kXT + (e / 4) * (64 * 128)) >> 4) + (e % 4) * 2, id_y2);
+                mma_ss<true>(tmem + kTY, cm + (e / 4) * kBlk + (e % 4) * 2, hm + (e / 4) * kBlk + (e % 4) * 2, id_g);
             }
-          }
-          tc_commit(bar(L::kY2 + (c & 1)));
-        }
-        __syncwarp();
-        wait_warp(L::kMFull, c & 1);
-        if (!ok) break;
-        tc_fence_after();
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {  // Y += M X
-          if (elect_one()) {
-            const uint32_t xm = sdesc_lo(sb + L::kX + ((c & 1) * 2 + h) * kXT, kQ * 128);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              mma_ts(tmem + kTY + h * 64, tmem + kTG + (e / 4) * 64 + h * 32 + (e % 4) * 8, xm + e * (2048 >> 4), id_y,
-                     e > 0 ? 1u : zero ? 0u : 1u);
-            tc_commit(bar(L::kYFull + h));
+            tc_commit(bar(L::kY2 + (c & 1)));
           }
           __syncwarp();
-        }
+          wait_warp(L::kMFull, c & 1);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {  // Y += M X
+            if (elect_one()) {
+              const uint32_t xm = sdesc_lo(sb + L::kX + ((c & 1) * 2 + h) * kXT, kQ * 128);
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                mma_ts(tmem + kTY + h * 64, tmem + kTG + (e / 4) * 64 + h * 32 + (e % 4) * 8, xm + e * (2048 >> 4), id_y,
+                       e > 0 ? 1u : zero ? 0u : 1u);
+              tc_commit(bar(L::kYFull + h));
+            }
+            __syncwarp();
+          }
         }
         if (elect_one()) tc_commit(bar(L::kXEmpty + (c & 1)));
         __syncwarp();
@@ -783,34 +800,43 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
         }
         __syncwarp();
       };
-      int c = 0;
-      for (; p.tiled && c < chunks; ++c) {
+      int nx = 0, nc = 0, nb = 0, nz = 0;  // copies begun
+      for (int c = 0; p.tiled && c < chunks; ++c) {
         const uint32_t parity = ((c >> 1) & 1) ^ 1;
         if (warp == 17) {
           wait_warp(L::kXEmpty + (c & 1), parity);
           if (!ok) break;
           copy(sb + L::kX + (c & 1) * 2 * kXT, di + h0 * kSsmP, c, L::kXFull + (c & 1));
-          if constexpr (!kLocal) {
-            wait_warp(L::kOut + (c & 1), parity);  // z of two chunks before
-            if (!ok) break;
-            copy(sb + c_tile(c), 2 * di + kSsmN, c, L::kCFull + (c & 1));
-          }
+          ++nx;
           wait_warp(L::kBEmpty, (c & 1) ^ 1);
           if (!ok) break;
           copy(sb + L::kB, 2 * di, c, L::kBFull);
+          ++nb;
+          if constexpr (!kLocal) {
+            if (c > 0) wait_warp(L::kY2 + ((c - 1) & 1), ((c - 1) >> 1) & 1);  // C of the chunk before
+            if (!ok) break;
+            copy(sb + L::kC, 2 * di + kSsmN, c, L::kCFull + (c & 1));
+            ++nc;
+          }
         } else if constexpr (!kLocal) {
-          if (c > 0) wait_warp(L::kY2 + ((c - 1) & 1), ((c - 1) >> 1) & 1);  // C of the chunk before
+          if (c > 0) wait_warp(L::kOut + ((c - 1) & 1), ((c - 1) >> 1) & 1);
           if (!ok) break;
-          copy(sb + z_tile(c), h0 * kSsmP, c, L::kZFull + (c & 1));
+          copy(sb + L::kZ, h0 * kSsmP, c, L::kZFull + (c & 1));
+          ++nz;
         }
       }
       if (!ok) {  // give-up: the copies in flight land before the shared memory is left
-        for (int i = max(0, c - 2); i <= c; ++i)
-          for (int n = 0; n < (1 << 12); ++n)
-            if (warp == 17 ? mbar_try_wait(bar(L::kXFull + (i & 1)), (i >> 1) & 1) &&
-                                 mbar_try_wait(bar(L::kCFull + (i & 1)), (i >> 1) & 1) && mbar_try_wait(bar(L::kBFull), i & 1)
-                           : mbar_try_wait(bar(L::kZFull + (i & 1)), (i >> 1) & 1))
-              break;
+        auto drain = [&](int b, uint32_t parity) {
+          for (int n = 0; n < (1 << 20) && !mbar_try_wait(bar(b), parity); ++n) {
+          }
+        };
+        auto drain2 = [&](int b, int n) {  // the last two of n copies by turns
+          for (int i = max(0, n - 2); i < n; ++i) drain(b + (i & 1), (i >> 1) & 1);
+        };
+        drain2(L::kXFull, nx);
+        drain2(L::kCFull, nc);
+        drain2(L::kZFull, nz);
+        if (nb) drain(L::kBFull, (nb - 1) & 1);
       }
       __syncwarp();
     } else {
@@ -895,11 +921,10 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
 
 // Once per device, when a handle is made.
 cudaError_t configure_prompt_state() {
-  const cudaError_t e =
-      cudaFuncSetAttribute(k_prompt_state<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, StateSmem::kTotal);
-  return e != cudaSuccess
-             ? e
-             : cudaFuncSetAttribute(k_prompt_state<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, StateSmem::kTotal);
+  constexpr int kSplit = 256 * kRegsFront + kBehind * kRegsBehind + 128 * kRegsRest;
+  cudaError_t e = configure_split(k_prompt_state<false>, kStateThreads, kSplit, StateSmem::kTotal);
+  if (e == cudaSuccess) e = configure_split(k_prompt_state<true>, kStateThreads, kSplit, StateSmem::kTotal);
+  return e;
 }
 
 }  // namespace wave
@@ -912,8 +937,9 @@ extern "C" int wave_hybrid_prompt_state(wave_t* h, int layer, const void* weight
   const Plan& pl = h->pl;
   const int e = pl.hcfg.attn_every;
   if (layer < 0 || layer >= pl.hcfg.n_layers || layer % e == e - 1) return WAVE_EINVAL;
-  if (zx_stride < pl.in_rows || zx_stride % 4 || out_stride < pl.d_inner || out_stride % 8 || !aligned16(weights) ||
-      !aligned16(zxbcdt) || !aligned16(state_in) || !aligned16(state_out) || !aligned16(out))
+  if (zx_stride < pl.in_rows || zx_stride % 4 || out_stride < pl.d_inner || out_stride % 8 || zx_stride > kMaxStride ||
+      out_stride > kMaxStride || !aligned16(weights) || !aligned16(zxbcdt) || !aligned16(state_in) ||
+      !aligned16(state_out) || !aligned16(out))
     return WAVE_EINVAL;
   StateParams p;
   const int rc = make_batch(&p.b, n_seq, cu_seqlens, slots, starts, pl.S_max);
@@ -925,7 +951,6 @@ extern "C" int wave_hybrid_prompt_state(wave_t* h, int layer, const void* weight
   const int Hs = pl.hcfg.ssm_heads, lm = layer - layer / e;
   const size_t per_layer = (size_t)pl.S_max * Hs * kSsmP * kSsmN;
   p.Hs = Hs;
-  p.S_max = pl.S_max;
   p.zx = (const uint16_t*)zxbcdt;
   p.prm = (const uint16_t*)weights + hyb_layer_offset(pl.pk_M, pl.pk_layer, e, layer) + pl.pk_a_log;
   p.state_in = state_in ? state_in + lm * per_layer : nullptr;
@@ -957,7 +982,7 @@ extern "C" int wave_hybrid_prompt_state(wave_t* h, int layer, const void* weight
   p.tiled = zx_stride % 8 == 0;
   if (take(true)) {
     if (p.tiled && encode_rows_map(&p.tm, zxbcdt, pl.in_rows, 1, cu_seqlens[n_seq], zx_stride, kQ)) return WAVE_ECUDA;
-    // Segments: the longest that give no more CTAs than SMs, if that is worth
+    // Segments: the shortest that give no more CTAs than SMs, if that is worth
     // a second launch.  A chunk of the first costs about half of one of the
     // second, and a launch about one (2048 tokens of 64 heads, 32 CTAs of 16
     // chunks: 77 us whole).

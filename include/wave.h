@@ -306,12 +306,16 @@ int wave_fp8_encode(const float* in, int64_t n, uint8_t* out, void* stream);
  * an empty slot of the step) and starts[i] the position of its first token (0
  * for a new session, the session's position for a continuation).
  * 1 <= n_seq <= WAVE_MAX_SEQS; sequences may be empty; no session may be named
- * twice.  Rows outside every sequence are neither read nor written.  Buffers
- * are 16-byte aligned and row strides (in elements) multiples of 8.  Every
- * argument is checked on the host before anything is enqueued: WAVE_EINVAL,
- * or WAVE_EPOS where a token's position would reach T_max; the handle's
- * device has to be the current one.  The calls are asynchronous, allocate
- * nothing, and use the handle as a step does (one stream at a time).
+ * twice.  Rows outside every sequence reach no result, whatever they hold,
+ * and are not written.  Buffers are 16-byte aligned and do not overlap unless
+ * a call says so; row strides (in elements) are multiples of 8 below 2^31.
+ * Every argument is checked on the host before anything is enqueued:
+ * WAVE_EINVAL, or WAVE_EPOS where a token's position would reach T_max; the
+ * handle's device has to be the current one.  The calls are asynchronous,
+ * allocate nothing, and use the handle as a step does: its scratch belongs to
+ * one launch at a time, so the calls and graphs of one handle run one after
+ * another (one stream, or streams that wait for each other).  Waits inside
+ * the kernels are limited by wave_set_timeout_ns and reported by wave_status.
  */
 
 /*
@@ -371,6 +375,13 @@ int wave_prompt_attention(wave_t* h, int n_seq, const int32_t* cu_seqlens, int n
  *             the two may not overlap otherwise).  Sessions that the call does
  *             not name, and those with an empty sequence, are not written.
  *   out       bf16 [rows][out_stride]: bf16(y silu(z)).
+ * The state is carried in fp32.  Sequences of up to 16 tokens run the
+ * recurrence token by token in fp32; longer ones run it in chunks of 128
+ * tokens on the tensor cores, where y's two products take bf16 factors (the
+ * decayed C B^T, and the state before the chunk) and the state's product takes
+ * each weighted x as the sum of three bf16, to fp32's precision.  A token
+ * whose x is not finite makes its own and later tokens of that channel not
+ * finite (NaN in the rest of its chunk).  One to three launches.
  */
 int wave_hybrid_prompt_state(wave_t* h, int layer, const void* weights, int n_seq, const int32_t* cu_seqlens,
                              const int32_t* slots, const int32_t* starts, const void* zxbcdt, int64_t zx_stride,

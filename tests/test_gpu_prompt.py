@@ -209,6 +209,34 @@ def test_attention_is_deterministic_and_replays():
         w.close()
 
 
+def test_attention_batches_of_every_size():
+    """As many sequences as a call takes, and the last of them alone."""
+    g = np.random.default_rng(3)
+    lens = [int(n) for n in g.integers(0, 300, fsd.WAVE_MAX_SEQS)]
+    cu, q, k, v, out = _attention(lens, 4, 2, 64, torch.bfloat16, seed=1, first=2, tail=3)
+    _attend(cu, q, k, v, out)
+    _check_attention(cu, q, k, v, out)
+    one = torch.full_like(out, 7.0)
+    _attend(cu[-2:], q, k, v, one)
+    assert torch.equal(one[cu[-2]:cu[-1]], out[cu[-2]:cu[-1]])
+
+
+def test_attention_offsets_beyond_32_bits():
+    """Rows whose offsets in elements pass 2^31 (slices of a wide buffer)."""
+    H, D, n = 32, 128, 176000
+    cu = [n - 300, n - 170, n - 2]
+    wide = torch.empty(n, 3 * H * D, dtype=torch.bfloat16, device="cuda")
+    out = torch.empty(n, 2 * H * D, dtype=torch.bfloat16, device="cuda")[:, H * D:].unflatten(1, (H, D))
+    g = torch.Generator(device="cuda").manual_seed(1)
+    wide[cu[0]:] = torch.randn(300, 3 * H * D, generator=g, device="cuda").to(torch.bfloat16)
+    out[cu[0]:] = 7
+    q, k, v = (wide[:, i * H * D:(i + 1) * H * D].unflatten(1, (H, D)) for i in range(3))
+    assert cu[0] * wide.stride(0) > 2 ** 31
+    _attend(cu, q, k, v, out)
+    tail = lambda t: t[cu[0]:].contiguous()  # noqa: E731
+    _check_attention([0, 130, 298], tail(q), tail(k), tail(v), tail(out))
+
+
 # --------------------------------------------------------------------- append
 def rope64(x, pos, base=1e4):
     D = x.shape[-1]
@@ -302,6 +330,48 @@ def test_append_equals_the_steps_own_append():
     for s, pos in enumerate(case.pos_h.tolist()):
         assert torch.equal(kv[:, 1, s, :, pos], case.kv[:, 1, s, :, pos])
         assert torch.equal(sc[:, 1, s, :, pos], case.sc[:, 1, s, :, pos])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_append_many_sessions_far_into_the_history(D):
+    """A batch of 128 sessions, replayed from a graph on a stream of its own,
+    into a history whose offsets pass 32 bits: equal to a session at a time."""
+    S, H, T = 128, 32, 4100 * 128 // D
+    g = torch.Generator(device="cuda").manual_seed(D)
+    lens = [int(n) for n in np.random.default_rng(D).integers(0, 9, S)]
+    starts = [T - n for n in lens]
+    cu = _cu(lens)
+    qkv = torch.randn(cu[-1], 3 * H * D, generator=g, device="cuda").to(torch.bfloat16)
+    kv = torch.empty(1, 2, S, H, T, D, dtype=torch.uint8, device="cuda")
+    assert kv.numel() > 2 ** 32
+    sc = torch.empty(1, 2, S, H, T, device="cuda")
+    last = (kv[..., T - 12:, :], sc[..., T - 12:])
+    for t in last:
+        t.fill_(3)
+    q, k = (torch.empty(cu[-1], H, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    w = _wave(H, D, S, T)
+    try:
+        for i in range(S):
+            if lens[i]:
+                w.prompt_append(0, cu[i:i + 2], [i], [starts[i]], qkv, kv, sc, q, k)
+        want = [t.clone() for t in (*last, q, k)]
+        for t in (*last, q, k):
+            t.fill_(3)
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            w.prompt_append(0, cu, list(range(S)), starts, qkv, kv, sc, q, k, stream=s)
+        with torch.cuda.stream(s):
+            graph.replay()
+        torch.cuda.current_stream().wait_stream(s)
+        assert w.status() == fsd.WAVE_OK
+        for a, b in zip((*last, q, k), want):
+            assert torch.equal(a, b)
+        for i in range(S):
+            assert bool((last[0][0, :, i, :, :12 - lens[i]] == 3).all()) and bool((last[1][0, :, i, :, :12 - lens[i]] == 3).all())
+    finally:
+        w.close()
 
 
 # ---------------------------------------------------------------------- state
@@ -419,6 +489,25 @@ def test_state_long_sequences_of_few_heads(hs, lens, starts):
     _check_state(cu, zx, prm, h0, list(range(n)), starts, hs, out, new, n)
 
 
+@pytest.mark.parametrize("lens", [[16], [25], [129], [2048]])
+def test_state_is_carried_in_fp32(lens):
+    """The 2-norm of the state's error, relative to the state: a weight is a
+    product of some six factors and exponentials of 1 to 4 roundings each
+    (10 U in quadrature), and the sums add a rounding a step, those of old
+    tokens decayed (6 U): far below one part of 2^-16, two bf16 of a weight."""
+    hs = 16
+    cu, zx, prm, h0, out = _state_case(lens, hs, [0], seed=lens[0])
+    cfg, w = _hybrid(hs, S=1)
+    new = torch.zeros_like(h0)
+    try:
+        w.prompt_state(0, _weights(cfg, prm), cu, [0], [0], zx, None, new, out)
+        assert w.status() == fsd.WAVE_OK
+    finally:
+        w.close()
+    _, _, states, _ = state_reference(zx, prm, [torch.zeros(hs, P, N, device="cuda")], cu, hs)
+    assert float((new[0, 0].double() - states[0]).norm() / states[0].norm()) <= 16 * U
+
+
 def test_state_in_place_in_parts_and_left_out():
     """A prompt in one call, and in three calls on the same buffer, each going
     on from the state of the last; a left-out sequence keeps its state."""
@@ -487,6 +576,102 @@ def test_state_non_finite_tokens_do_not_reach_earlier_ones():
     assert bool(torch.isnan(out[cu[0] + 140:cu[1]]).all()) and bool(torch.isnan(new[0, 0]).all())
 
 
+@pytest.mark.parametrize("lens", [[17], [127], [128], [129], [64, 0, 1, 200], [385, 16, 15, 18], [255, 257]])
+@pytest.mark.parametrize("hs", [8, 24])
+def test_state_lengths_of_aligned_rows(lens, hs):
+    """Rows of a multiple of 16 bytes, which a tensor map describes."""
+    n = len(lens)
+    starts, slots = [(4 if i % 2 == 0 else 0) for i in range(n)], list(range(n))
+    cu, zx, prm, h0, out = _state_case(lens, hs, starts, seed=sum(lens), first=1, tail=3, S=n)
+    assert zx.stride(0) % 8 == 0
+    cfg, w = _hybrid(hs, S=n)
+    new = torch.full_like(h0, 9.0)
+    try:
+        w.prompt_state(0, _weights(cfg, prm), cu, slots, starts, zx, h0, new, out)
+        assert w.status() == fsd.WAVE_OK
+    finally:
+        w.close()
+    _check_state(cu, zx, prm, h0, slots, starts, hs, out, new, n)
+    assert bool((out[:1] == 7).all()) and bool((out[cu[-1]:] == 7).all())
+
+
+@pytest.mark.parametrize("hs,lens", [(8, [1500, 700]), (4, [1300]), (64, [200, 40, 9])])
+def test_state_in_place_beside_other_work(hs, lens):
+    """In place and elsewhere are the same, with the SMs kept busy by another
+    stream (the CTAs of a sequence's segments do not all run at once)."""
+    n = len(lens)
+    cu, zx, prm, h0, out = _state_case(lens, hs, [1] * n, seed=hs, S=n)
+    cfg, w = _hybrid(hs, S=n)
+    wt = _weights(cfg, prm)
+    a = torch.randn(4096, 4096, device="cuda").to(torch.bfloat16)
+    side = torch.cuda.Stream()
+    try:
+        new, out2 = torch.zeros_like(h0), torch.zeros_like(out)
+        w.prompt_state(0, wt, cu, list(range(n)), [1] * n, zx, h0, new, out)
+        for _ in range(8):
+            state = h0.clone()
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                for _ in range(4):
+                    a @ a
+            w.prompt_state(0, wt, cu, list(range(n)), [1] * n, zx, state, state, out2)
+            assert torch.equal(state, new) and torch.equal(out2, out)
+        assert w.status() == fsd.WAVE_OK
+    finally:
+        w.close()
+
+
+def test_state_batch_replays_from_a_graph():
+    """128 sessions, short and long, captured and replayed with new tokens on
+    a stream of its own."""
+    hs, n = 4, fsd.WAVE_MAX_SEQS
+    lens = [int(x) for x in np.random.default_rng(9).integers(0, 40, n)]
+    lens[5], lens[77] = 300, 129
+    starts = [i % 3 for i in range(n)]
+    cu, zx, prm, h0, out = _state_case(lens, hs, starts, seed=9, S=n)
+    cfg, w = _hybrid(hs, S=n)
+    wt = _weights(cfg, prm)
+    new = torch.full_like(h0, 9.0)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    try:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            w.prompt_state(0, wt, cu, list(range(n)), starts, zx, h0, new, out, stream=s)
+        zx.copy_(zx.flip(0))
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            graph.replay()
+            graph.replay()
+        torch.cuda.current_stream().wait_stream(s)
+        assert w.status() == fsd.WAVE_OK
+    finally:
+        w.close()
+    _check_state(cu, zx, prm, h0, list(range(n)), starts, hs, out, new, n)
+
+
+@pytest.mark.parametrize("pad", [0, 4])
+def test_state_offsets_beyond_32_bits(pad):
+    """Rows whose offsets in elements pass 2^31."""
+    hs, n = 64, 254000
+    lens, starts = [140, 9], [2, 0]
+    width = 2 * hs * P + 2 * N + hs
+    zx = torch.empty(n, width + pad, dtype=torch.bfloat16, device="cuda")[:, :width]
+    out = torch.empty(n, hs * P, dtype=torch.bfloat16, device="cuda")
+    _, small, prm, h0, _ = _state_case(lens, hs, starts, seed=pad)
+    zx[n - 149:] = small
+    cu = [n - 149, n - 9, n]
+    assert cu[0] * zx.stride(0) > 2 ** 31
+    cfg, w = _hybrid(hs, S=2)
+    new = torch.zeros_like(h0)
+    try:
+        w.prompt_state(0, _weights(cfg, prm), cu, [0, 1], starts, zx, h0, new, out)
+        assert w.status() == fsd.WAVE_OK
+    finally:
+        w.close()
+    _check_state([0, 140, 149], small, prm, h0, [0, 1], starts, hs, out[n - 149:], new, 2)
+
+
 # --------------------------------------------------------------------- copies
 def _sessions(hybrid, S=9, T=72, H=3, D=64, hs=4):
     g = torch.Generator(device="cuda").manual_seed(S)
@@ -544,7 +729,59 @@ def test_sessions_copy_long(T, D, pos):
     assert torch.equal(kv, want_kv) and torch.equal(sc, want_sc) and p.tolist() == [pos] * 3
 
 
+def test_sessions_copy_beyond_32_bits_and_replayed():
+    """The last session of a large history to the first slots, from a graph
+    that reads the positions when it runs."""
+    S, H, T, D = 128, 32, 4100, 128
+    kv = torch.empty(1, 2, S, H, T, D, dtype=torch.uint8, device="cuda")
+    sc = torch.empty(1, 2, S, H, T, device="cuda")
+    assert kv.numel() > 2 ** 32
+    for s in (0, 1, 127):
+        kv[:, :, s], sc[:, :, s] = s + 1, s + 1
+    pos = torch.full((S,), -1, dtype=torch.int32, device="cuda")
+    w = _wave(H, D, S, T)
+    try:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            w.sessions_copy([127, 127], [0, 1], kv, sc, pos)
+        pos[127] = 4001
+        graph.replay()
+        assert w.status() == fsd.WAVE_OK
+        for s in (0, 1):
+            assert bool((kv[:, :, s, :, :4001] == 128).all()) and bool((kv[:, :, s, :, 4001:] == s + 1).all())
+            assert bool((sc[:, :, s, :, :4001] == 128).all()) and bool((sc[:, :, s, :, 4001:] == s + 1).all())
+        assert pos[:2].tolist() == [4001, 4001]
+    finally:
+        w.close()
+
+
 # ------------------------------------------------------------------- refusals
+def test_waits_that_run_out_are_reported():
+    """With a limit far below what the kernels take, their waits give up: the
+    launch ends by itself, the status says so once, and the handle goes on."""
+    cu, q, k, v, out = _attention([4100, 300], 4, 4, 128, torch.bfloat16, seed=2)
+    lens, starts = [2600, 700], [0, 3]
+    cs, zx, prm, h0, so = _state_case(lens, 8, starts, seed=1)
+    cfg, w = _hybrid(8, S=2, heads=4, dim=128)
+    wt = _weights(cfg, prm)
+    new = torch.zeros_like(h0)
+    calls = [lambda: w.prompt_attention(cu, q, k, v, out), lambda: w.prompt_state(0, wt, cs, [0, 1], starts, zx, h0, new, so)]
+    try:
+        for c in calls:
+            w.set_timeout_ns(1)
+            c()
+            assert w.status() == fsd.WAVE_ETIMEOUT
+            assert w.status() == fsd.WAVE_OK
+        w.set_timeout_ns(2_000_000_000)
+        for c in calls:
+            c()
+        assert w.status() == fsd.WAVE_OK
+    finally:
+        w.close()
+    _check_attention(cu, q, k, v, out)
+    _check_state(cs, zx, prm, h0, [0, 1], starts, 8, so, new, 2)
+
+
 def test_refusals_before_any_launch():
     """Every bad argument is answered on the host, and nothing is written."""
     L = fsd.lib()
@@ -573,7 +810,7 @@ def test_refusals_before_any_launch():
         for kw in [dict(h=None), dict(layer=-1), dict(layer=2), dict(cu=(0,)), dict(cu=(0, 5, 3)), dict(cu=(-1, 3, 5)),
                    dict(slots=(0, 4)), dict(slots=(1, 1)), dict(starts=(0, -1)), dict(qkv=None), dict(qkv=b + 8), dict(t=2), dict(t=9),
                    dict(stride=376), dict(stride=388), dict(kv=None), dict(kv=b + 4), dict(sc=None), dict(sc=b + 4), dict(q=b + 2),
-                   dict(k=b + 8), dict(v=b + 8), dict(o=0), dict(o=3), many]:
+                   dict(k=b + 8), dict(v=b + 8), dict(o=0), dict(o=3), dict(stride=2 ** 31), many]:
             assert append(**kw) == E, kw
         assert append(starts=(62, 0)) == fsd.WAVE_EPOS and append(starts=(0, 2 ** 31 - 2)) == fsd.WAVE_EPOS
         assert append(h=hw.h, layer=0, stride=192) == E  # a selective-state block has no history
@@ -587,7 +824,7 @@ def test_refusals_before_any_launch():
         for kw in [dict(h=None), dict(h=w.h), dict(layer=1), dict(layer=-1), dict(layer=2), dict(wt=None), dict(wt=b + 8), dict(cu=(0,)),
                    dict(cu=(2, 1)), dict(slots=(0, 4)), dict(slots=(2, 2)), dict(starts=(-1, 0)), dict(starts=(1, 0)), dict(zx=None),
                    dict(zx=b + 8), dict(zs=768), dict(zs=774), dict(so=None), dict(so=b + 8), dict(si=b + 4), dict(out=None),
-                   dict(out=b + 8), dict(os=248), dict(os=260), many]:
+                   dict(out=b + 8), dict(os=248), dict(os=260), dict(zs=2 ** 31), dict(os=2 ** 31), many]:
             assert state(**kw) == E, kw
         assert state(slots=(-1, -1)) == OK
         for kw in [dict(h=None), dict(src=()), dict(src=(4,)), dict(src=(-1,)), dict(dst=(4,)), dict(dst=(-1,)), dict(dst=(0,)),

@@ -60,3 +60,17 @@ def test_shapes_that_do_not_fit_are_refused():
     for i, c in enumerate(bad):
         with pytest.raises(ValueError):
             c()
+
+
+def test_integers_beyond_32_bits_are_refused():
+    w = _decoder()
+    kv, sc, pos = _b(8, dtype=torch.uint8), _b(8, dtype=torch.float32), _b(4, dtype=torch.int32)
+    q, k = _b(3, 2, 64), _b(3, 1, 64)
+    bad = [lambda: w.prompt_append(0, [0, 3], [2 ** 32], [0], _b(3, 384), kv, sc, stream=0),
+           lambda: w.prompt_append(0, [0, 3], [0], [-2 ** 31 - 1], _b(3, 384), kv, sc, stream=0),
+           lambda: w.prompt_attention([2 ** 32, 2 ** 32 + 3], q, k, k, q, stream=0),
+           lambda: w.sessions_copy([0.5], [1], kv, sc, pos, stream=0)]
+    for c in bad:
+        with pytest.raises(ValueError):
+            c()
+    assert list(fsd._ints(torch.tensor([3, -1]))[0]) == [3, -1] and list(fsd._ints([])[0]) == []
