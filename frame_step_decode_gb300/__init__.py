@@ -6,9 +6,9 @@ is not built, importing the binding's entry points raises.
 """
 from __future__ import annotations
 
-import array
 import ctypes
 import os
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libwave.so")
@@ -131,14 +131,14 @@ def lib() -> ctypes.CDLL:
         L.wave_barriers_per_step.restype = i32
         L.wave_phases_per_step.argtypes = [vp]
         L.wave_phases_per_step.restype = i32
-        i32p = ctypes.POINTER(ctypes.c_int32)
-        L.wave_prompt_append.argtypes = [vp, i32, i32, i32p, i32p, i32p, vp, i32, i64, vp, vp, vp, vp, vp, i32, vp]
+        # the host arrays of int32 come as bytes
+        L.wave_prompt_append.argtypes = [vp, i32, i32, vp, vp, vp, vp, i32, i64, vp, vp, vp, vp, vp, i32, vp]
         L.wave_prompt_append.restype = i32
-        L.wave_prompt_attention.argtypes = [vp, i32, i32p, i32, i32, vp, i64, vp, i64, vp, i64, ctypes.c_float, vp, i64, vp]
+        L.wave_prompt_attention.argtypes = [vp, i32, vp, i32, i32, vp, i64, vp, i64, vp, i64, ctypes.c_float, vp, i64, vp]
         L.wave_prompt_attention.restype = i32
-        L.wave_hybrid_prompt_state.argtypes = [vp, i32, vp, i32, i32p, i32p, i32p, vp, i64, vp, vp, vp, i64, vp]
+        L.wave_hybrid_prompt_state.argtypes = [vp, i32, vp, i32, vp, vp, vp, vp, i64, vp, vp, vp, i64, vp]
         L.wave_hybrid_prompt_state.restype = i32
-        L.wave_sessions_copy.argtypes = [vp, i32, i32p, i32p, i32, vp, vp, vp, vp, vp]
+        L.wave_sessions_copy.argtypes = [vp, i32, vp, vp, i32, vp, vp, vp, vp, vp]
         L.wave_sessions_copy.restype = i32
         _lib = L
     return _lib
@@ -156,18 +156,18 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
-_ARRAYS: dict = {}  # ctypes array types by length
+_PACKS: dict = {}  # packers of n int32 by n
 
 
 def _ints(values):
-    """A host array of int32 (any sequence of integers that fit), and its length."""
+    """A host array of int32 (any sequence of integers that fit) as bytes, and its length."""
     n = len(values)
-    t = _ARRAYS.get(n)
-    if t is None:
-        t = _ARRAYS[n] = ctypes.c_int32 * n
+    p = _PACKS.get(n)
+    if p is None:
+        p = _PACKS[n] = struct.Struct(f"{n}i")
     try:
-        return t.from_buffer(array.array("i", values)) if n else t(), n
-    except (OverflowError, TypeError) as e:
+        return p.pack(*values), n
+    except (struct.error, TypeError) as e:
         raise ValueError("a sequence of 32-bit integers is wanted") from e
 
 
@@ -188,17 +188,25 @@ def _type_of(t) -> int:
 def _rows(t, what: str) -> int:
     """The row stride in elements of a packed tensor [rows][H][D] or
     [rows][values]; what lies inside a row has to be contiguous."""
-    shape, stride = t.shape, t.stride()
+    shape = t.shape
+    n = len(shape)
+    if n == 3 and t.is_contiguous():
+        return shape[1] * shape[2]
+    stride = t.stride()
     width = shape[-1]
-    fits = stride[-1] == 1 or width == 1
-    if len(shape) == 3:
+    fits = 2 <= n <= 3 and (stride[-1] == 1 or width == 1)
+    if n == 3:
         fits = fits and (stride[1] == width or shape[1] == 1)
         width *= shape[1]
-    elif len(shape) != 2:
-        fits = False
     if not fits:
         raise ValueError(f"{what}: a packed tensor of rows, contiguous inside a row, is wanted")
     return stride[0] if shape[0] > 1 else width
+
+
+def _is_rows(t, rows: int, H: int, D: int) -> bool:
+    """Whether t is [rows or more][H][D]."""
+    shape = t.shape
+    return len(shape) == 3 and shape[2] == D and shape[1] == H and shape[0] >= rows
 
 
 def _stream(stream) -> int:
@@ -301,15 +309,16 @@ class Wave:
         if n_cu < 2 or n_sl != n_cu - 1 or n_s0 != n_sl:
             raise ValueError("wave_prompt_append: one slot and one start for each sequence")
         H, D = self.cfg.n_heads, self.cfg.head_dim
-        rows, out_type = cu[n_sl], -1
+        rows, out_type = int(cu_seqlens[n_sl]), -1
         for t in (q, k, v):
             if t is None:
                 continue
             kind = _type_of(t)
-            if t.shape[0] < rows or t.shape[1:] != (H, D) or out_type not in (-1, kind) or not t.is_contiguous():
+            if not _is_rows(t, rows, H, D) or out_type not in (-1, kind) or not t.is_contiguous():
                 raise ValueError("wave_prompt_append: q, k and v are contiguous [rows][H][D], of one type")
             out_type = kind
-        if qkv.shape[0] < rows or qkv.shape[1:] != (3 * H * D,):
+        shape = qkv.shape
+        if len(shape) != 2 or shape[1] != 3 * H * D or shape[0] < rows:
             raise ValueError("wave_prompt_append: qkv is [rows][3*H*D], with the rows that cu_seqlens names")
         rc = lib().wave_prompt_append(self.h, layer, n_sl, cu, sl, s0, _ptr(qkv), _type_of(qkv), _rows(qkv, "qkv"),
                                       _ptr(kv), _ptr(kv_scales), _ptr(q), _ptr(k), _ptr(v),
@@ -324,14 +333,15 @@ class Wave:
         all fp16, rows may be strided; scale defaults to 1/sqrt(D)."""
         cu, n_cu = _ints(cu_seqlens)
         H, D = self.cfg.n_heads, self.cfg.head_dim
-        qs, ks, dtype = q.shape, k.shape, q.dtype
-        if k.dtype != dtype or v.dtype != dtype or out.dtype != dtype or qs[1:] != (H, D) or out.shape[1:] != (H, D) \
-                or len(ks) != 3 or ks[2] != D or v.shape[1:] != ks[1:]:
-            raise ValueError("wave_prompt_attention: q, out [rows][n_heads][D] and k, v [rows][n_kv_heads][D] of one type")
-        if n_cu < 2 or min(qs[0], ks[0], v.shape[0], out.shape[0]) < cu[n_cu - 1]:
-            raise ValueError("wave_prompt_attention: cu_seqlens names more rows than a buffer has")
-        what = "wave_prompt_attention"
-        rc = lib().wave_prompt_attention(self.h, n_cu - 1, cu, ks[1], _type_of(q), _ptr(q), _rows(q, what), _ptr(k),
+        what, dtype = "wave_prompt_attention", q.dtype
+        if n_cu < 2:
+            raise ValueError(f"{what}: cu_seqlens has one entry more than there are sequences")
+        rows, Hkv = int(cu_seqlens[n_cu - 1]), k.shape[1] if len(k.shape) == 3 else 0
+        if k.dtype != dtype or v.dtype != dtype or out.dtype != dtype or not _is_rows(q, rows, H, D) \
+                or not _is_rows(out, rows, H, D) or not _is_rows(k, rows, Hkv, D) or not _is_rows(v, rows, Hkv, D):
+            raise ValueError(f"{what}: q, out [rows][n_heads][D] and k, v [rows][n_kv_heads][D] of one type, with the rows "
+                             "that cu_seqlens names")
+        rc = lib().wave_prompt_attention(self.h, n_cu - 1, cu, Hkv, _type_of(q), _ptr(q), _rows(q, what), _ptr(k),
                                          _rows(k, what), _ptr(v), _rows(v, what), D ** -0.5 if scale is None else scale,
                                          _ptr(out), _rows(out, what), _stream(stream))
         if check and rc != WAVE_OK:
@@ -489,10 +499,11 @@ class HybridWave(Wave):
             raise ValueError("wave_hybrid_prompt_state: one slot and one start for each sequence")
         c = self.cfg
         di = c.ssm_heads * c.ssm_head_dim
-        if zxbcdt.shape[1:] != (2 * di + 2 * c.ssm_state + c.ssm_heads,) or out.shape[1:] != (di,) \
+        zs, ys = zxbcdt.shape, out.shape
+        if len(zs) != 2 or len(ys) != 2 or zs[1] != 2 * di + 2 * c.ssm_state + c.ssm_heads or ys[1] != di \
                 or _type_of(zxbcdt) != WAVE_BF16 or _type_of(out) != WAVE_BF16:
             raise ValueError("wave_hybrid_prompt_state: zxbcdt is bf16 [rows][in_rows], out bf16 [rows][d_inner]")
-        if min(zxbcdt.shape[0], out.shape[0]) < cu[n_sl]:
+        if min(zs[0], ys[0]) < int(cu_seqlens[n_sl]):
             raise ValueError("wave_hybrid_prompt_state: cu_seqlens names more rows than a buffer has")
         rc = lib().wave_hybrid_prompt_state(self.h, layer, _ptr(weights), n_sl, cu, sl, s0, _ptr(zxbcdt),
                                             _rows(zxbcdt, "zxbcdt"), _ptr(state_in), _ptr(state_out), _ptr(out),

@@ -1,5 +1,6 @@
 """CPU: the calls on packed prompts and sessions refuse a missing handle and
 badly shaped tensors without touching a device."""
+import numpy as np
 import pytest
 import torch
 
@@ -73,4 +74,5 @@ def test_integers_beyond_32_bits_are_refused():
     for c in bad:
         with pytest.raises(ValueError):
             c()
-    assert list(fsd._ints(torch.tensor([3, -1]))[0]) == [3, -1] and list(fsd._ints([])[0]) == []
+    for values in (torch.tensor([3, -1]), np.array([3, -1]), (3, -1)):
+        assert fsd._ints(values) == (np.array([3, -1], dtype=np.int32).tobytes(), 2)
