@@ -210,9 +210,9 @@ def _is_rows(t, rows: int, H: int, D: int) -> bool:
 
 
 def _stream(stream) -> int:
-    if stream is None:
+    if stream is None:  # the current stream's handle, without a Stream object around it (4 of a call's 12 us)
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
