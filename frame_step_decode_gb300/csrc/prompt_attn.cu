@@ -28,13 +28,13 @@ struct AttnParams {
   CUtensorMap tm_q, tm_k, tm_v;
   int n;                            // sequences, longest first
   int32_t begin[WAVE_MAX_SEQS], len[WAVE_MAX_SEQS];
-  long long items;                  // (pairs of row tiles) x heads
   int Hq, group;                    // query heads, and how many of them share a K/V head
   const uint16_t* v;
   uint16_t* out;
   long long v_stride, out_stride;
   float scale2;                     // scale * log2(e)
   int wide;                         // out's rows are 32-byte aligned
+  int more;                         // more items than SMs
   ErrSink sink;
 };
 
@@ -67,10 +67,12 @@ struct AttnSmem {
     kDone,
     kItemFull,
     kItemEmpty = kItemFull + 2,
-    kCount = kItemEmpty + 2
+    kNext = kItemEmpty + 2,
+    kCount
   };
   static constexpr int kItems = kBars + kCount * 8;
-  static constexpr int kMisc = kItems + 2 * (int)sizeof(AttnItem);
+  static constexpr int kAnswer = (kItems + 2 * (int)sizeof(AttnItem) + 15) / 16 * 16;
+  static constexpr int kMisc = kAnswer + 16;
   static constexpr int kTotal = kMisc + 16 + 1024;  // + alignment
 };
 
@@ -153,6 +155,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __gr
         mbar_init(bar(L::kItemFull + i), 1);
         mbar_init(bar(L::kItemEmpty + i), 11);  // 8 softmax warps, copies, MMAs, guard
       }
+      mbar_init(bar(L::kNext), 1);
       mbar_init(bar(L::kGo), 1);
       mbar_init(bar(L::kOk), 1);
       mbar_init(bar(L::kDone), 1);
@@ -539,19 +542,35 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __gr
       }
     } else {
       // ---------------------------------------------------------- scheduler
+      // The first item is the CTA's own, the later ones those of CTAs that have
+      // not begun: items go to whoever is free next, longest first, and the
+      // copies and first scores of one run under the end of the one before.
       for (uint32_t k = 0; ok; ++k) {
         if (!wait_warp(L::kItemEmpty + (k & 1), ((k >> 1) & 1) ^ 1)) break;
-        // rows of gridDim items, every second one backwards: the CTA with the
-        // longest item of one row gets the shortest of the next
-        const long long idx = (long long)k * gridDim.x + (k & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-        const bool valid = idx < p.items;
+        int idx = blockIdx.x;
+        bool valid = true;
+        if (k > 0) valid = p.more;
+        if (k > 0 && valid) {
+          if (lane == 0) {
+            fence_proxy_async_smem();  // the last answer has been read
+            mbar_arrive_expect_tx(bar(L::kNext), 16);
+            cta_request(sb + L::kAnswer, bar(L::kNext));
+          }
+          __syncwarp();
+          if (!wait_warp(L::kNext, (k - 1) & 1)) {  // give-up: the answer lands before the shared memory is left
+            for (int n = 0; n < (1 << 20) && !mbar_try_wait(bar(L::kNext), (k - 1) & 1); ++n) {
+            }
+            break;
+          }
+          valid = cta_taken(sb + L::kAnswer, idx);
+        }
         int seq = 0, level = 0;
-        if (valid) pair_of_rank(p, (int)(idx / p.Hq), seq, level);
+        if (valid) pair_of_rank(p, idx / p.Hq, seq, level);
         if (lane == 0) {
           AttnItem& it = items[k & 1];
           const int left = p.len[seq] - level * 2 * kRows;
           it.valid = valid;
-          it.head = (int)(idx % p.Hq);
+          it.head = idx % p.Hq;
           it.kv0 = p.begin[seq];
           it.row0 = p.begin[seq] + level * 2 * kRows;
           it.left = left;
@@ -573,16 +592,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __gr
 }
 
 template <int D, bool kF16>
-static cudaError_t launch_attention(const AttnParams& p, int grid, cudaStream_t st) {
-  k_prompt_attention<D, kF16>
-      <<<(unsigned)(p.items < grid ? p.items : grid), kAttnThreads, AttnSmem<D>::kTotal, st>>>(p);
+static cudaError_t launch_attention(const AttnParams& p, long long items, cudaStream_t st) {
+  k_prompt_attention<D, kF16><<<(unsigned)items, kAttnThreads, AttnSmem<D>::kTotal, st>>>(p);
   return cudaGetLastError();
 }
 
 template <int D, bool kF16>
 static cudaError_t configure() {
-  return configure_split(k_prompt_attention<D, kF16>, kAttnThreads, 256 * kRegsSoftmax + 128 * kRegsRest,
-                         AttnSmem<D>::kTotal);
+  return configure_split(k_prompt_attention<D, kF16>, kAttnThreads, 256 * kRegsSoftmax + 128 * kRegsRest, kRegsSoftmax,
+                         kRegsRest, AttnSmem<D>::kTotal);
 }
 
 // Once per device, when a handle is made.
@@ -629,7 +647,9 @@ extern "C" int wave_prompt_attention(wave_t* h, int n_seq, const int32_t* cu_seq
       encode_rows_map(&p.tm_k, k, D, n_kv_heads, rows, k_stride, kRows) ||
       encode_rows_map(&p.tm_v, v, D, n_kv_heads, rows, v_stride, kRows))
     return WAVE_ECUDA;
-  p.items = pairs * H;
+  const long long items = pairs * H;
+  if (items > 0x7fffffff) return WAVE_EINVAL;
+  p.more = items > h->pl.grid;
   p.Hq = H;
   p.group = H / n_kv_heads;
   p.v = (const uint16_t*)v;
@@ -641,11 +661,10 @@ extern "C" int wave_prompt_attention(wave_t* h, int n_seq, const int32_t* cu_seq
   p.sink = make_sink(h->ws.err, h->err_host_dev, h->timeout_ns);
   cudaStream_t st = (cudaStream_t)stream;
   h->last_stream = st;
-  const int grid = h->pl.grid;
   cudaError_t e;
   if (D == 128)
-    e = type == WAVE_F16 ? launch_attention<128, true>(p, grid, st) : launch_attention<128, false>(p, grid, st);
+    e = type == WAVE_F16 ? launch_attention<128, true>(p, items, st) : launch_attention<128, false>(p, items, st);
   else
-    e = type == WAVE_F16 ? launch_attention<64, true>(p, grid, st) : launch_attention<64, false>(p, grid, st);
+    e = type == WAVE_F16 ? launch_attention<64, true>(p, items, st) : launch_attention<64, false>(p, items, st);
   return e == cudaSuccess ? WAVE_OK : WAVE_ECUDA;
 }

@@ -163,15 +163,37 @@ __device__ __forceinline__ void regs_give() {
 }
 
 // The attributes of a kernel whose warps divide the registers of the launch
-// among themselves anew: an error if they would ask for more than it has (they
-// would wait for ever).
+// (`threads` times what it was compiled to) among themselves anew, `registers`
+// in all: an error if that is more than there are (they would wait for ever),
+// if those that take more would end with fewer (`take`), or those that give
+// some with more (`give`).
 template <typename K>
-inline cudaError_t configure_split(K kernel, int threads, int registers, int smem) {
+inline cudaError_t configure_split(K kernel, int threads, int registers, int take, int give, int smem) {
   cudaFuncAttributes a;
   const cudaError_t e = cudaFuncGetAttributes(&a, kernel);
   if (e != cudaSuccess) return e;
-  if (a.numRegs * threads < registers) return cudaErrorInvalidConfiguration;
+  if (a.numRegs * threads < registers || take < a.numRegs || give > a.numRegs) return cudaErrorInvalidConfiguration;
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+}
+
+// Work taken over from CTAs of this launch that have not begun: a request for
+// one of them (its answer, 16 bytes, arrives as bytes on the barrier) and
+// whether there was one, with its index.  No request follows a refused one.
+__device__ __forceinline__ void cta_request(uint32_t answer, uint32_t bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(answer),
+               "r"(bar)
+               : "memory");
+}
+__device__ __forceinline__ bool cta_taken(uint32_t answer, int& cta) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\tld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\tselp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+      : "=r"(ok), "=r"(cta)
+      : "r"(answer)
+      : "memory");
+  return ok != 0;
 }
 
 // What a kernel with bounded waits reports to: the handle's error word and

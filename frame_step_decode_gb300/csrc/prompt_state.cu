@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(256) k_prompt_state_rows(const __grid_constant
 constexpr int kQ = 128;                 // tokens of a chunk
 constexpr int kStateThreads = 640;      // 2 warpgroups in front, 2 behind, 4 single warps
 constexpr int kBehind = 256;
-constexpr int kRegsFront = 104, kRegsBehind = 104, kRegsRest = 64;  // 640 threads are launched with 96 each
+constexpr int kRegsFront = 96, kRegsBehind = 104, kRegsRest = 80;  // 640 threads are launched with 96 each
 constexpr int kBC = kQ * kSsmN * 2;     // bytes of the B (or C) tile
 constexpr int kXT = kQ * kSsmP * 2;     // ... of one head's x (or z) tile
 
@@ -159,7 +159,9 @@ struct StateSmem {
   static constexpr int kLast = kU + 2 * 96 * 4;   // [head] the decays of the whole chunk
   static constexpr int kBad = kLast + 8;  // byte chunk % 4, bit head * 4 + warp: an x that is not finite
   static constexpr int kMisc = kBad + 4;          // TMEM's address
-  static constexpr int kBars = kMisc + 4;
+  static constexpr int kAnswer = kMisc + 4;       // a CTA taken over
+  static constexpr int kUnit = kAnswer + 16;      // ... as the other warps get it
+  static constexpr int kBars = kUnit + 8;
   enum {
     kBFull = 0,
     kBEmpty,
@@ -177,11 +179,15 @@ struct StateSmem {
     kWx,
     kS,
     kScan,
+    kNext,
+    kUnitFull,
+    kUnitEmpty,
     kDone,
     kCount
   };
   static constexpr int kTotal = kBars + kCount * 8;
 };
+static_assert(StateSmem::kAnswer % 16 == 0 && StateSmem::kBars % 8 == 0, "alignment");
 static_assert(StateSmem::kTotal <= 232448, "the chunked state form does not fit shared memory");
 
 // TMEM columns: G (the heads' M later, 64 each), (w X)^T (its first two parts;
@@ -190,6 +196,15 @@ constexpr int kTG = 0, kTWx = 128, kTState = 256, kTY = 384;
 
 __device__ __forceinline__ void bar_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+// Whether it holds for all of them.
+__device__ __forceinline__ bool bar_and(int id, int threads, bool v) {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+               : "=r"(r)
+               : "r"((uint32_t)v), "r"(id), "r"(threads)
+               : "memory");
+  return r != 0;
 }
 // Rows that no tensor map can describe (a stride that is no multiple of 16
 // bytes) are copied by the 256 threads behind, 8 bytes at a time: 128 tokens x
@@ -250,17 +265,39 @@ __device__ __forceinline__ float softplus(float raw) {
   return fmaxf(raw, 0.f) + s * q;
 }
 
+// What a CTA works on: a head pair of a sequence, or of a segment of one.
+struct StateUnit {
+  int seq, h0, first, len;  // first: its first row
+  int chunks;
+};
+
 // kLocal: only the state of a segment from zero, into seg_state (the last
-// segment of a sequence has none to give on).
-template <bool kLocal>
+// segment of a sequence has none to give on).  kOnce: a unit per CTA, whole
+// sequences or segments.  kMore: whole sequences, more of them than SMs; a CTA
+// takes the place of CTAs that have not begun, so that a unit's first copies
+// and products run under the last of the unit before (16 prompts of 9044
+// tokens, 64 heads: 98 us, with a unit per CTA 102 us; a single instance for
+// both took 1.5 us longer for 2048 tokens in segments).
+enum StateMode { kLocal, kOnce, kMore };
+template <StateMode kMode>
 __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_constant__ StateParams p) {
   using L = StateSmem;
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int pairs = p.Hs / 2, unit = blockIdx.x / pairs, h0 = (blockIdx.x % pairs) * 2;
-  int seq = unit, seg = 0, len, off = 0;
-  if (p.seg_chunks) {
+  const int pairs = p.Hs / 2;
+  auto whole = [&](int cta) {  // a CTA's sequence and head pair
+    StateUnit u;
+    u.seq = cta / pairs, u.h0 = cta % pairs * 2;
+    u.len = p.b.len(u.seq), u.first = p.b.begin[u.seq];
+    u.chunks = (u.len + kQ - 1) / kQ;
+    return u;
+  };
+  StateUnit mine;
+  int seg = 0;
+  bool last_seg = true;
+  if (kMode != kMore && p.seg_chunks) {
+    const int unit = blockIdx.x / pairs;
     int lo = 0, hi = p.b.n - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -269,26 +306,25 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
       else
         hi = mid - 1;
     }
-    seq = lo;
-    seg = unit - p.seg_cum[seq];
-    off = seg * p.seg_chunks * kQ;
-  }
-  len = p.b.len(seq) - off;
-  const bool last_seg = !p.seg_chunks || len <= p.seg_chunks * kQ;
-  if (!last_seg) len = p.seg_chunks * kQ;
-  if (kLocal && last_seg) {
-    if (p.b.start[seq] > 0) {
-      const float4* src = (const float4*)p.state_in + ((size_t)p.b.slot[seq] * p.Hs + h0) * (kSsmP * kSsmN / 4);
-      float4* dst = (float4*)p.seg_state + (size_t)blockIdx.x * (128 * kSsmN / 4);
-      for (int i = threadIdx.x; i < 128 * kSsmN / 4; i += kStateThreads) dst[i] = src[i];
+    mine = whole(lo * pairs + blockIdx.x % pairs);
+    seg = unit - p.seg_cum[lo];
+    mine.first += seg * p.seg_chunks * kQ;
+    mine.len -= seg * p.seg_chunks * kQ;
+    last_seg = mine.len <= p.seg_chunks * kQ;
+    if (!last_seg) mine.len = p.seg_chunks * kQ;
+    mine.chunks = (mine.len + kQ - 1) / kQ;
+    if (kMode == kLocal && last_seg) {
+      if (p.b.start[mine.seq] > 0) {
+        const float4* src = (const float4*)p.state_in + ((size_t)p.b.slot[mine.seq] * p.Hs + mine.h0) * (kSsmP * kSsmN / 4);
+        float4* dst = (float4*)p.seg_state + (size_t)blockIdx.x * (128 * kSsmN / 4);
+        for (int i = threadIdx.x; i < 128 * kSsmN / 4; i += kStateThreads) dst[i] = src[i];
+      }
+      return;
     }
-    return;
+  } else {
+    mine = whole(blockIdx.x);
   }
-  const size_t first = (size_t)p.b.begin[seq] + off;
-  const int chunks = (len + kQ - 1) / kQ;
-  const bool from_in = !kLocal && p.b.start[seq] > 0;   // the sequence begins from state_in, not from zero
-  const bool goes_on = from_in || (!kLocal && seg > 0);  // this CTA's state does not begin as zero
-  const int seg0 = (int)blockIdx.x - seg * pairs;        // the sequence's first segment, of this head pair
+  const int seg0 = (int)blockIdx.x - seg * pairs;  // the sequence's first segment, of this head pair
   const int di = p.Hs * kSsmP;
   auto bar = [&](int b) { return sb + L::kBars + b * 8; };
   uint32_t* tmem_word = (uint32_t*)(smem + L::kMisc);
@@ -318,6 +354,9 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
       mbar_init(bar(L::kScan), 1);
       mbar_init(bar(L::kWx), kBehind / 32);
       mbar_init(bar(L::kS), 1);
+      mbar_init(bar(L::kNext), 1);
+      mbar_init(bar(L::kUnitFull), 1);
+      mbar_init(bar(L::kUnitEmpty), 19);  // every warp but the one that writes it
       mbar_init(bar(L::kDone), 1);
       fence_mbar_init();
       fence_proxy_async_smem();
@@ -332,9 +371,9 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
   tc_fence_after();
   const uint32_t tmem = *tmem_word;
 
-  // In the compute warps a wait that gives up leaves the rest of the loop
+  // In the compute warps a wait that gives up leaves the rest of the unit
   // without waits (the named barriers need every warp), with its results
-  // undefined; the other warps leave their loops.
+  // undefined, and then all leave; the other warps leave their loops.
   bool ok = true;
   auto wait_warp = [&](int b, uint32_t parity) {
     if (ok) ok = __all_sync(0xffffffffu, wait_bar(bar(b), parity, p.sink));
@@ -348,203 +387,233 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
   const int h = (warp >> 2) & 1, quad = warp & 3, row = quad * 32 + lane;  // a thread per token of head h0 + h
   const uint32_t lanes = (uint32_t)(quad * 32) << 16;
   const int hh = row >> 6, pp = row & 63;  // for the state: row (head hh, p)
-  const int head = h0 + h;
+  // Whether a unit's sequence begins from state_in, and its state not as zero.
+  auto from_in = [&](const StateUnit& u) { return kMode != kLocal && p.b.start[u.seq] > 0; };
+  auto goes_on = [&](const StateUnit& u) { return kMode != kLocal && (seg > 0 || p.b.start[u.seq] > 0); };
+  // The unit after the n - 1 before it, if there is one: a CTA that has not
+  // begun, taken over by the warp of the decays, so that the first chunk of one
+  // unit runs under the last of the one before.  group: the named barrier of a
+  // group of 256 threads, which goes on together or not at all.
+  auto next_unit = [&](StateUnit& u, uint32_t n, int group = 0) {
+    if (kMode != kMore) return false;
+    wait_warp(L::kUnitFull, (n - 1) & 1);
+    if (group) ok = bar_and(group, 256, ok);
+    if (!ok) return false;
+    const int cta = *(volatile int*)(smem + L::kUnit);
+    arrive_warp(L::kUnitEmpty);
+    if (cta < 0) return false;
+    u = whole(cta);
+    return true;
+  };
   float* sv = (float*)(smem + L::kV);
   float* su = (float*)(smem + L::kU);
   float* saft = (float*)(smem + L::kAfter);
   float* slast = (float*)(smem + L::kLast);
   uint32_t* sbad = (uint32_t*)(smem + L::kBad);
-  const size_t state_at = (((size_t)p.b.slot[seq] * p.Hs + h0) * kSsmP + row) * kSsmN + h * 64;
 
   if (warp < 8) {
     // -------------------------------------------------------------- in front
     regs_take<kRegsFront>();
-    const float skip = bf(p.prm[2 * p.Hs + head]);
     float decayed = 0.f;  // kLocal: the decays so far, of head h
-    const float* begin = p.seg_chunks ? p.seg_state + (size_t)(seg0 + (p.seg_cum[seq + 1] - p.seg_cum[seq] - 1) * pairs) * (128 * kSsmN) +
-                                            row * kSsmN + h * 64
-                                      : p.state_in + state_at;
-    for (int c = 0; c < chunks; ++c) {
-      // ---- the state: its bf16 copy for C H^T, and the chunk's decay
-      wait_warp(L::kScan, c & 1);
-      if (c > 0) wait_warp(L::kS, (c - 1) & 1);
-      tc_fence_after();
-      const float after = saft[h * kQ + row];  // c_j - c_i = after_i - after_j
-      const bool zero = c == 0 && !goes_on;
-      if (!zero) {
-        const float dec = ex2(-slast[hh]);
-        uint8_t* hrow = smem + L::kH + h * (128 * 128) + row * 128;
+    StateUnit u = mine;
+    uint32_t g = 0;  // the CTA's chunks
+    for (uint32_t n = 0; n == 0 || next_unit(u, n, 1); ++n) {
+      const float skip = bf(p.prm[2 * p.Hs + u.h0 + h]);
+      const size_t state_at = (((size_t)p.b.slot[u.seq] * p.Hs + u.h0) * kSsmP + row) * kSsmN + h * 64;
+      const float* begin = kMode != kMore && p.seg_chunks ? p.seg_state +
+                                              (size_t)(seg0 + (p.seg_cum[u.seq + 1] - p.seg_cum[u.seq] - 1) * pairs) * (128 * kSsmN) +
+                                              row * kSsmN + h * 64
+                                        : p.state_in + state_at;
+      for (int c = 0; c < u.chunks; ++c, ++g) {
+        // ---- the state: its bf16 copy for C H^T, and the chunk's decay
+        wait_warp(L::kScan, g & 1);
+        if (g > 0) wait_warp(L::kS, (g - 1) & 1);
+        tc_fence_after();
+        const float after = saft[h * kQ + row];  // c_j - c_i = after_i - after_j
+        const bool zero = c == 0 && !goes_on(u);
+        if (!zero) {
+          const float dec = ex2(-slast[hh]);
+          uint8_t* hrow = smem + L::kH + h * (128 * 128) + row * 128;
 #pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-          uint32_t v[16];
-          if (!kLocal && c == 0) {
-            const float4* src = (const float4*)(begin + 16 * q);
-            float4 f[4];
+          for (int q = 0; q < 4; ++q) {
+            uint32_t v[16];
+            if (kMode != kLocal && c == 0) {
+              const float4* src = (const float4*)(begin + 16 * q);
+              float4 f[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) f[e] = from_in ? src[e] : make_float4(0.f, 0.f, 0.f, 0.f);
+              for (int e = 0; e < 4; ++e) f[e] = from_in(u) ? src[e] : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-            for (int i = 0; i < seg; ++i) {  // the segments before this one
-              const int cta = seg0 + i * pairs;
-              const float d = ex2(-p.seg_decay[2 * cta + hh]);
-              const float4* part = (const float4*)(p.seg_state + (size_t)cta * (128 * kSsmN) + row * kSsmN + h * 64 + 16 * q);
+              for (int i = 0; i < seg; ++i) {  // the segments before this one
+                const int cta = seg0 + i * pairs;
+                const float d = ex2(-p.seg_decay[2 * cta + hh]);
+                const float4* part = (const float4*)(p.seg_state + (size_t)cta * (128 * kSsmN) + row * kSsmN + h * 64 + 16 * q);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float4 t = part[e];
+                  f[e] = make_float4(fmaf(f[e].x, d, t.x), fmaf(f[e].y, d, t.y), fmaf(f[e].z, d, t.z), fmaf(f[e].w, d, t.w));
+                }
+              }
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const float4 t = part[e];
-                f[e] = make_float4(fmaf(f[e].x, d, t.x), fmaf(f[e].y, d, t.y), fmaf(f[e].z, d, t.z), fmaf(f[e].w, d, t.w));
+                v[4 * e] = __float_as_uint(f[e].x), v[4 * e + 1] = __float_as_uint(f[e].y);
+                v[4 * e + 2] = __float_as_uint(f[e].z), v[4 * e + 3] = __float_as_uint(f[e].w);
+              }
+            } else {
+              tmem_ld16_nowait(tmem + kTState + lanes + h * 64 + 16 * q, v);
+              tmem_ld_wait();
+            }
+            if constexpr (kMode != kLocal) {
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                uint4 w;
+                w.x = pack_bf16(__uint_as_float(v[8 * e]), __uint_as_float(v[8 * e + 1]));
+                w.y = pack_bf16(__uint_as_float(v[8 * e + 2]), __uint_as_float(v[8 * e + 3]));
+                w.z = pack_bf16(__uint_as_float(v[8 * e + 4]), __uint_as_float(v[8 * e + 5]));
+                w.w = pack_bf16(__uint_as_float(v[8 * e + 6]), __uint_as_float(v[8 * e + 7]));
+                *(uint4*)(hrow + (((2 * q + e) ^ (pp & 7)) << 4)) = w;
               }
             }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              v[4 * e] = __float_as_uint(f[e].x), v[4 * e + 1] = __float_as_uint(f[e].y);
-              v[4 * e + 2] = __float_as_uint(f[e].z), v[4 * e + 3] = __float_as_uint(f[e].w);
-            }
-          } else {
-            tmem_ld16_nowait(tmem + kTState + lanes + h * 64 + 16 * q, v);
-            tmem_ld_wait();
+            scale_regs<16>(v, dec);
+            tmem_st16(tmem + kTState + lanes + h * 64 + 16 * q, v);
           }
-          if constexpr (!kLocal) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              uint4 w;
-              w.x = pack_bf16(__uint_as_float(v[8 * e]), __uint_as_float(v[8 * e + 1]));
-              w.y = pack_bf16(__uint_as_float(v[8 * e + 2]), __uint_as_float(v[8 * e + 3]));
-              w.z = pack_bf16(__uint_as_float(v[8 * e + 4]), __uint_as_float(v[8 * e + 5]));
-              w.w = pack_bf16(__uint_as_float(v[8 * e + 6]), __uint_as_float(v[8 * e + 7]));
-              *(uint4*)(hrow + (((2 * q + e) ^ (pp & 7)) << 4)) = w;
-            }
-          }
-          scale_regs<16>(v, dec);
-          tmem_st16(tmem + kTState + lanes + h * 64 + 16 * q, v);
-        }
-        tmem_st_wait();
-        fence_proxy_async_smem();
-      }
-      tc_fence_before();
-      if constexpr (kLocal) decayed += slast[h];
-      arrive_warp(L::kHFull);
-      if constexpr (kLocal) continue;
-      // ---- M, over G once both heads have read G
-      wait_warp(L::kG, c & 1);
-      tc_fence_after();
-      // Tokens 64..127 first, then 0..63: once both heads have read that half
-      // of G, its 64 columns take the same half of both heads' M.
-#pragma unroll 1
-      for (int half = 1; half >= 0; --half) {
-        uint32_t m[32];
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int q = 2 * half + t;  // 32 tokens
-          if (q > quad) {              // above the diagonal
-#pragma unroll
-            for (int e = 0; e < 16; ++e) m[16 * t + e] = 0;
-            continue;
-          }
-          uint32_t g[32];
-          tmem_ld32(tmem + kTG + lanes + 32 * q, g);
-          if (q < quad) {
-            // below: the decay from the end of token j's 32 to i is a factor
-            // of the row, that from j to there is in u_j
-            const float r = ex2(after - saft[h * kQ + 32 * q + 31]);
-            const float2 r2 = make_float2(r, r);
-            const float4* uj = (const float4*)(su + h * 96 + 32 * q);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float4 u4 = uj[e];
-              const float2 m0 = mul2(mul2(make_float2(__uint_as_float(g[4 * e]), __uint_as_float(g[4 * e + 1])), r2),
-                                     make_float2(u4.x, u4.y));
-              const float2 m1 = mul2(mul2(make_float2(__uint_as_float(g[4 * e + 2]), __uint_as_float(g[4 * e + 3])), r2),
-                                     make_float2(u4.z, u4.w));
-              m[16 * t + 2 * e] = pack_bf16(m0.x, m0.y);
-              m[16 * t + 2 * e + 1] = pack_bf16(m1.x, m1.y);
-            }
-          } else {
-            // on it; D x_i is added to y_i as D on the diagonal
-            const float2 ai = make_float2(after, after);
-            const float4* vj = (const float4*)(sv + h * kQ + 32 * q);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float4 v4 = vj[e];
-              const float2 t0 = add2(make_float2(v4.x, v4.y), ai), t1 = add2(make_float2(v4.z, v4.w), ai);
-              const float2 m0 = mul2(make_float2(__uint_as_float(g[4 * e]), __uint_as_float(g[4 * e + 1])),
-                                     make_float2(ex2(t0.x), ex2(t0.y)));
-              const float2 m1 = mul2(make_float2(__uint_as_float(g[4 * e + 2]), __uint_as_float(g[4 * e + 3])),
-                                     make_float2(ex2(t1.x), ex2(t1.y)));
-              float f[4] = {m0.x, m0.y, m1.x, m1.y};
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                if (4 * e + k > lane) f[k] = 0.f;
-                if (4 * e + k == lane) f[k] += skip;
-              }
-              m[16 * t + 2 * e] = pack_bf16(f[0], f[1]);
-              m[16 * t + 2 * e + 1] = pack_bf16(f[2], f[3]);
-            }
-          }
+          tmem_st_wait();
+          fence_proxy_async_smem();
         }
         tc_fence_before();
-        bar_sync(1, 256);  // both heads have read this half of G
+        if constexpr (kMode == kLocal) decayed += slast[h];
+        arrive_warp(L::kHFull);
+        if constexpr (kMode == kLocal) continue;
+        // ---- M, over G once both heads have read G
+        wait_warp(L::kG, g & 1);
         tc_fence_after();
-        tmem_st32(tmem + kTG + half * 64 + h * 32 + lanes, m);
-      }
-      // ---- C H^T, scaled in place: M X is added to it
-      wait_warp(L::kY2 + (c & 1), (c >> 1) & 1);
-      tc_fence_after();
-      if (!zero) {
-        const float ei = ex2(after - slast[h]);
+        // Tokens 64..127 first, then 0..63: once both heads have read that half
+        // of G, its 64 columns take the same half of both heads' M.
 #pragma unroll 1
-        for (int q = 0; q < 2; ++q) {
-          uint32_t v[32];
-          tmem_ld32(tmem + kTY + h * 64 + lanes + 32 * q, v);
-          tmem_ld_wait();
-          scale_regs<32>(v, ei);
-          tmem_st32(tmem + kTY + h * 64 + lanes + 32 * q, v);
-        }
-      }
-      tmem_st_wait();
-      tc_fence_before();
-      arrive_warp(L::kMFull);
-    }
-    if (kLocal && row == 0) p.seg_decay[2 * blockIdx.x + h] = decayed;
-    // ---- the state after the last token
-    wait_warp(L::kS, (chunks - 1) & 1);
-    tc_fence_after();
-#pragma unroll 1
-    for (int q = 0; q < 2 && (kLocal || last_seg); ++q) {
-      uint32_t v[32];
-      tmem_ld32(tmem + kTState + lanes + h * 64 + q * 32, v);
-      tmem_ld_wait();
-      float4* dst = (float4*)(kLocal ? p.seg_state + (size_t)blockIdx.x * (128 * kSsmN) + row * kSsmN + h * 64 + 32 * q
-                                     : p.state_out + state_at + 32 * q);
+        for (int half = 1; half >= 0; --half) {
+          uint32_t m[32];
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        dst[e] = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]), __uint_as_float(v[4 * e + 2]),
-                             __uint_as_float(v[4 * e + 3]));
+          for (int t = 0; t < 2; ++t) {
+            const int q = 2 * half + t;  // 32 tokens
+            if (q > quad) {              // above the diagonal
+#pragma unroll
+              for (int e = 0; e < 16; ++e) m[16 * t + e] = 0;
+              continue;
+            }
+            uint32_t gv[32];
+            tmem_ld32(tmem + kTG + lanes + 32 * q, gv);
+            if (q < quad) {
+              // below: the decay from the end of token j's 32 to i is a factor
+              // of the row, that from j to there is in u_j
+              const float r = ex2(after - saft[h * kQ + 32 * q + 31]);
+              const float2 r2 = make_float2(r, r);
+              const float4* uj = (const float4*)(su + h * 96 + 32 * q);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float4 u4 = uj[e];
+                const float2 m0 = mul2(mul2(make_float2(__uint_as_float(gv[4 * e]), __uint_as_float(gv[4 * e + 1])), r2),
+                                       make_float2(u4.x, u4.y));
+                const float2 m1 = mul2(mul2(make_float2(__uint_as_float(gv[4 * e + 2]), __uint_as_float(gv[4 * e + 3])), r2),
+                                       make_float2(u4.z, u4.w));
+                m[16 * t + 2 * e] = pack_bf16(m0.x, m0.y);
+                m[16 * t + 2 * e + 1] = pack_bf16(m1.x, m1.y);
+              }
+            } else {
+              // on it; D x_i is added to y_i as D on the diagonal
+              const float2 ai = make_float2(after, after);
+              const float4* vj = (const float4*)(sv + h * kQ + 32 * q);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float4 v4 = vj[e];
+                const float2 t0 = add2(make_float2(v4.x, v4.y), ai), t1 = add2(make_float2(v4.z, v4.w), ai);
+                const float2 m0 = mul2(make_float2(__uint_as_float(gv[4 * e]), __uint_as_float(gv[4 * e + 1])),
+                                       make_float2(ex2(t0.x), ex2(t0.y)));
+                const float2 m1 = mul2(make_float2(__uint_as_float(gv[4 * e + 2]), __uint_as_float(gv[4 * e + 3])),
+                                       make_float2(ex2(t1.x), ex2(t1.y)));
+                float f[4] = {m0.x, m0.y, m1.x, m1.y};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  if (4 * e + k > lane) f[k] = 0.f;
+                  if (4 * e + k == lane) f[k] += skip;
+                }
+                m[16 * t + 2 * e] = pack_bf16(f[0], f[1]);
+                m[16 * t + 2 * e + 1] = pack_bf16(f[2], f[3]);
+              }
+            }
+          }
+          tc_fence_before();
+          bar_sync(1, 256);  // both heads have read this half of G
+          tc_fence_after();
+          tmem_st32(tmem + kTG + half * 64 + h * 32 + lanes, m);
+        }
+        // ---- C H^T, scaled in place: M X is added to it
+        wait_warp(L::kY2 + (g & 1), (g >> 1) & 1);
+        tc_fence_after();
+        if (!zero) {
+          const float ei = ex2(after - slast[h]);
+#pragma unroll 1
+          for (int q = 0; q < 2; ++q) {
+            uint32_t v[32];
+            tmem_ld32(tmem + kTY + h * 64 + lanes + 32 * q, v);
+            tmem_ld_wait();
+            scale_regs<32>(v, ei);
+            tmem_st32(tmem + kTY + h * 64 + lanes + 32 * q, v);
+          }
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        arrive_warp(L::kMFull);
+      }
+      if (kMode == kLocal && row == 0) p.seg_decay[2 * blockIdx.x + h] = decayed;
+      // ---- the state after the last token
+      wait_warp(L::kS, (g - 1) & 1);
+      tc_fence_after();
+#pragma unroll 1
+      for (int q = 0; q < 2 && (kMode == kLocal || last_seg); ++q) {
+        uint32_t v[32];
+        tmem_ld32(tmem + kTState + lanes + h * 64 + q * 32, v);
+        tmem_ld_wait();
+        float4* dst = (float4*)(kMode == kLocal ? p.seg_state + (size_t)blockIdx.x * (128 * kSsmN) + row * kSsmN + h * 64 + 32 * q
+                                       : p.state_out + state_at + 32 * q);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          dst[e] = make_float4(__uint_as_float(v[4 * e]), __uint_as_float(v[4 * e + 1]), __uint_as_float(v[4 * e + 2]),
+                               __uint_as_float(v[4 * e + 3]));
+      }
     }
   } else if (warp < 16) {
     // ---------------------------------------------------------------- behind
     regs_take<kRegsBehind>();
     // (w X)^T of a chunk is made before the output of the chunk before it: the
     // state's product does not wait for the gate
-    for (int c = -1; c < chunks; ++c) {
-      if (c + 1 < chunks) {
-        const int k = c + 1, b = k & 1, left = len - k * kQ;
+    StateUnit u = mine;
+    uint32_t n = 0, g = 0;  // units; chunks, the next (w X)^T's
+    int c = 0;              // ... and its chunk of u
+    bool weigh = true, gate = false;
+    int out_row = 0;  // the chunk whose output is next: the one before g
+    int out_h0 = 0, out_left = 0;
+    while (weigh || gate) {
+      const int left = u.len - c * kQ;
+      const int row0 = u.first + c * kQ;
+      if (weigh) {
+        const uint32_t k = g;
+        const int b = k & 1;
         // ---- this token's x and B.  Behind the sequence's end lie other rows:
         // theirs become zero.  An x that is not finite would reach earlier
         // tokens as 0 * NaN in M X: it is noted here, becomes zero once the
         // state's weights have been made of it, and is put back at the output.
         const uint32_t parity = (k >> 1) & 1;
         if (!p.tiled) {
-          const size_t row0 = first + (size_t)k * kQ;
-          const int n = min(kQ, left);
+          const int rows = min(kQ, left);
           wait_warp(L::kXEmpty + b, parity ^ 1);
-          copy_tile<2 * kSsmP>(sb + L::kX + b * 2 * kXT, p.zx, p.zx_stride, di + h0 * kSsmP, row0, n);
-          if constexpr (!kLocal) {
+          copy_tile<2 * kSsmP>(sb + L::kX + b * 2 * kXT, p.zx, p.zx_stride, di + u.h0 * kSsmP, row0, rows);
+          if constexpr (kMode != kLocal) {
             if (k > 0) wait_warp(L::kY2 + ((k - 1) & 1), ((k - 1) >> 1) & 1);
-            copy_tile<kSsmN>(sb + L::kC, p.zx, p.zx_stride, 2 * di + kSsmN, row0, n);
+            copy_tile<kSsmN>(sb + L::kC, p.zx, p.zx_stride, 2 * di + kSsmN, row0, rows);
           }
           wait_warp(L::kBEmpty, (k & 1) ^ 1);
-          copy_tile<kSsmN>(sb + L::kB, p.zx, p.zx_stride, 2 * di, row0, n);
+          copy_tile<kSsmN>(sb + L::kB, p.zx, p.zx_stride, 2 * di, row0, rows);
           asm volatile("cp.async.wait_all;" ::: "memory");
           fence_proxy_async_smem();
           arrive_warp(L::kXFull + b);
@@ -643,72 +712,83 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
         tc_fence_before();
         arrive_warp(L::kWx);
       }
-      if (kLocal || c < 0) continue;
-      const int b = c & 1, left = len - c * kQ;
-      // ---- the output: y, gated, over z's row and from there to global
-      uint8_t* ztile = smem + L::kZ + h * kXT;
-      const uint32_t any_bad = *(volatile uint32_t*)sbad >> ((c & 3) * 8 + h * 4) & 15u;
-      if (!p.tiled) {
-        if (c > 0) wait_warp(L::kOut + ((c - 1) & 1), ((c - 1) >> 1) & 1);
-        copy_tile<2 * kSsmP>(sb + L::kZ, p.zx, p.zx_stride, h0 * kSsmP, first + (size_t)c * kQ, min(kQ, left));
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        arrive_warp(L::kZFull + b);
-      }
-      wait_warp(L::kZFull + b, (c >> 1) & 1);
-      wait_warp(L::kYFull + h, c & 1);
-      tc_fence_after();
-      uint8_t* zrow = ztile + row * 128;
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        uint32_t y[32];
-        tmem_ld32(tmem + kTY + h * 64 + lanes + 32 * half, y);
-        tmem_ld_wait();
-        if (half == 1) {
-          tc_fence_before();
-          arrive_warp(L::kYFree);
+      if (kMode != kLocal && gate) {
+        const uint32_t k = g - 1;
+        const int b = k & 1;
+        // ---- the output: y, gated, over z's row and from there to global
+        uint8_t* ztile = smem + L::kZ + h * kXT;
+        const uint32_t any_bad = *(volatile uint32_t*)sbad >> ((k & 3) * 8 + h * 4) & 15u;
+        if (!p.tiled) {
+          if (k > 0) wait_warp(L::kOut + ((k - 1) & 1), ((k - 1) >> 1) & 1);
+          copy_tile<2 * kSsmP>(sb + L::kZ, p.zx, p.zx_stride, out_h0 * kSsmP, out_row, min(kQ, out_left));
+          asm volatile("cp.async.wait_all;" ::: "memory");
+          arrive_warp(L::kZFull + b);
         }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint4* zp = (uint4*)(zrow + (((half * 4 + e) ^ (row & 7)) << 4));
-          const uint4 zv = *zp;
-          const uint32_t zw[4] = {zv.x, zv.y, zv.z, zv.w};
-          uint32_t o[4];
-#pragma unroll
-          for (int f = 0; f < 4; ++f) {
-            const int i = 8 * e + 2 * f;
-            const float2 z2 = make_float2(__uint_as_float(zw[f] << 16), __uint_as_float(zw[f] & 0xFFFF0000u));
-            const float2 t = mul2(z2, make_float2(-1.44269504088896340736f, -1.44269504088896340736f));
-            const float2 d = add2(make_float2(ex2(t.x), ex2(t.y)), make_float2(1.f, 1.f));
-            const float2 g = mul2(z2, make_float2(rcp(d.x), rcp(d.y)));
-            const float2 r = mul2(make_float2(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), g);
-            o[f] = pack_bf16(r.x, r.y);
+        wait_warp(L::kZFull + b, (k >> 1) & 1);
+        wait_warp(L::kYFull + h, k & 1);
+        tc_fence_after();
+        uint8_t* zrow = ztile + row * 128;
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          uint32_t y[32];
+          tmem_ld32(tmem + kTY + h * 64 + lanes + 32 * half, y);
+          tmem_ld_wait();
+          if (half == 1) {
+            tc_fence_before();
+            arrive_warp(L::kYFree);
           }
-          *zp = make_uint4(o[0], o[1], o[2], o[3]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint4* zp = (uint4*)(zrow + (((half * 4 + e) ^ (row & 7)) << 4));
+            const uint4 zv = *zp;
+            const uint32_t zw[4] = {zv.x, zv.y, zv.z, zv.w};
+            uint32_t o[4];
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+              const int i = 8 * e + 2 * f;
+              const float2 z2 = make_float2(__uint_as_float(zw[f] << 16), __uint_as_float(zw[f] & 0xFFFF0000u));
+              const float2 t = mul2(z2, make_float2(-1.44269504088896340736f, -1.44269504088896340736f));
+              const float2 d = add2(make_float2(ex2(t.x), ex2(t.y)), make_float2(1.f, 1.f));
+              const float2 g = mul2(z2, make_float2(rcp(d.x), rcp(d.y)));
+              const float2 r = mul2(make_float2(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), g);
+              o[f] = pack_bf16(r.x, r.y);
+            }
+            *zp = make_uint4(o[0], o[1], o[2], o[3]);
+          }
         }
-      }
-      if (any_bad) {  // tokens up to this one whose x is not finite
+        if (any_bad) {  // tokens up to this one whose x is not finite
 #pragma unroll 1
-        for (int j = 0; j <= row && j < left; ++j) {
-          if (!(any_bad >> (j >> 5) & 1)) continue;
-          const uint16_t* x = p.zx + (first + (size_t)c * kQ + j) * p.zx_stride + di + head * kSsmP;
+          for (int j = 0; j <= row && j < out_left; ++j) {
+            if (!(any_bad >> (j >> 5) & 1)) continue;
+            const uint16_t* x = p.zx + (size_t)(out_row + j) * p.zx_stride + di + (out_h0 + h) * kSsmP;
 #pragma unroll 1
-          for (int e = 0; e < 64; ++e)
-            if ((x[e] & 0x7F80) == 0x7F80) *(uint16_t*)(zrow + (((e >> 3) ^ (row & 7)) << 4) + (e & 7) * 2) = 0x7FC0;
+            for (int e = 0; e < 64; ++e)
+              if ((x[e] & 0x7F80) == 0x7F80) *(uint16_t*)(zrow + (((e >> 3) ^ (row & 7)) << 4) + (e & 7) * 2) = 0x7FC0;
+          }
         }
-      }
-      __syncwarp();
-      {
-        const int r0 = quad * 32 + (lane >> 3), at = lane & 7;  // four rows at a time
-        uint16_t* dst = p.out + (first + (size_t)c * kQ + r0) * p.out_stride + head * kSsmP + at * 8;
+        __syncwarp();
+        {
+          const int r0 = quad * 32 + (lane >> 3), at = lane & 7;  // four rows at a time
+          uint16_t* dst = p.out + (size_t)(out_row + r0) * p.out_stride + (out_h0 + h) * kSsmP + at * 8;
 #pragma unroll 4
-        for (int q = 0; q < 8; ++q, dst += 4 * p.out_stride) {
-          const int r = r0 + 4 * q;
-          const uint4 v = *(const uint4*)(ztile + r * 128 + ((at ^ (r & 7)) << 4));
-          if (r < left) *(uint4*)dst = v;
+          for (int q = 0; q < 8; ++q, dst += 4 * p.out_stride) {
+            const int r = r0 + 4 * q;
+            const uint4 v = *(const uint4*)(ztile + r * 128 + ((at ^ (r & 7)) << 4));
+            if (r < out_left) *(uint4*)dst = v;
+          }
+        }
+        fence_proxy_async_smem();  // the next copies into this buffer come by the async proxy
+        arrive_warp(L::kOut + b);
+      }
+      gate = kMode != kLocal && weigh;
+      if (weigh) {
+        out_row = row0, out_h0 = u.h0, out_left = left;
+        ++g;
+        if (++c == u.chunks) {
+          c = 0;
+          weigh = next_unit(u, ++n, 4);
         }
       }
-      fence_proxy_async_smem();  // the next copies into this buffer come by the async proxy
-      arrive_warp(L::kOut + b);
     }
   } else {
     regs_give<kRegsRest>();
@@ -717,71 +797,75 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
       constexpr uint32_t id_g = idesc_16(128, 128, false, false, false), id_y = idesc_16(128, 64, false, false, true),
                          id_s = idesc_16(128, 128, false, false, true);
       constexpr uint32_t kBlk = (kQ * 128) >> 4;  // the next 64 columns of a tile, as a descriptor counts
-      for (int c = 0; c < chunks; ++c) {
-        const uint32_t ct = sb + L::kC, bt = sb + L::kB;
-        const bool zero = c == 0 && !goes_on;
-        wait_warp(L::kBFull, c & 1);
-        if constexpr (!kLocal) wait_warp(L::kCFull + (c & 1), (c >> 1) & 1);
-        if (!ok) break;
-        tc_fence_after();
-        if (!kLocal && elect_one()) {  // G = C B^T
-          const uint32_t cm = sdesc_lo(ct), bm = sdesc_lo(bt);
-          mma_ss<false>(tmem + kTG, cm, bm, id_g);
-#pragma unroll
-          for (int e = 1; e < 8; ++e)
-            mma_ss<true>(tmem + kTG, cm + (e / 4) * kBlk + (e % 4) * 2, bm + (e / 4) * kBlk + (e % 4) * 2, id_g);
-          tc_commit(bar(L::kG));
-        }
-        __syncwarp();
-        wait_warp(L::kHFull, c & 1);
-        wait_warp(L::kWx, c & 1);
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {  // the state += (w X)^T B, its three parts
-          const uint32_t bm = sdesc_lo(bt, kQ * 128), lm = sdesc_lo(sb + L::kLo);
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            mma_ts(tmem + kTState, tmem + kTWx + 8 * e, bm + (e % 8) * (2048 >> 4), id_s, e > 0 ? 1u : zero ? 0u : 1u);
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            mma_ss<true>(tmem + kTState, lm + (e / 4) * kBlk + (e % 4) * 2, bm + e * (2048 >> 4), id_s);
-          tc_commit(bar(L::kS));
-          tc_commit(bar(L::kBEmpty));
-        }
-        __syncwarp();
-        if constexpr (!kLocal) {
-          if (c > 0) wait_warp(L::kYFree, (c - 1) & 1);
+      StateUnit u = mine;
+      uint32_t g = 0;  // the CTA's chunks
+      for (uint32_t n = 0; ok && (n == 0 || next_unit(u, n)); ++n) {
+        for (int c = 0; c < u.chunks; ++c, ++g) {
+          const uint32_t ct = sb + L::kC, bt = sb + L::kB;
+          const bool zero = c == 0 && !goes_on(u);
+          wait_warp(L::kBFull, g & 1);
+          if constexpr (kMode != kLocal) wait_warp(L::kCFull + (g & 1), (g >> 1) & 1);
           if (!ok) break;
           tc_fence_after();
-          if (elect_one()) {  // Y = C H^T, of both heads at once
-            if (!zero) {
-              const uint32_t cm = sdesc_lo(ct), hm = sdesc_lo(sb + L::kH);
-              mma_ss<false>(tmem + kTY, cm, hm, id_g);
+          if (kMode != kLocal && elect_one()) {  // G = C B^T
+            const uint32_t cm = sdesc_lo(ct), bm = sdesc_lo(bt);
+            mma_ss<false>(tmem + kTG, cm, bm, id_g);
 #pragma unroll
-              for (int e = 1; e < 8; ++e)
-                mma_ss<true>(tmem + kTY, cm + (e / 4) * kBlk + (e % 4) * 2, hm + (e / 4) * kBlk + (e % 4) * 2, id_g);
-            }
-            tc_commit(bar(L::kY2 + (c & 1)));
+            for (int e = 1; e < 8; ++e)
+              mma_ss<true>(tmem + kTG, cm + (e / 4) * kBlk + (e % 4) * 2, bm + (e / 4) * kBlk + (e % 4) * 2, id_g);
+            tc_commit(bar(L::kG));
           }
           __syncwarp();
-          wait_warp(L::kMFull, c & 1);
+          wait_warp(L::kHFull, g & 1);
+          wait_warp(L::kWx, g & 1);
           if (!ok) break;
           tc_fence_after();
+          if (elect_one()) {  // the state += (w X)^T B, its three parts
+            const uint32_t bm = sdesc_lo(bt, kQ * 128), lm = sdesc_lo(sb + L::kLo);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {  // Y += M X
-            if (elect_one()) {
-              const uint32_t xm = sdesc_lo(sb + L::kX + ((c & 1) * 2 + h) * kXT, kQ * 128);
+            for (int e = 0; e < 16; ++e)
+              mma_ts(tmem + kTState, tmem + kTWx + 8 * e, bm + (e % 8) * (2048 >> 4), id_s, e > 0 ? 1u : zero ? 0u : 1u);
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                mma_ts(tmem + kTY + h * 64, tmem + kTG + (e / 4) * 64 + h * 32 + (e % 4) * 8, xm + e * (2048 >> 4), id_y,
-                       e > 0 ? 1u : zero ? 0u : 1u);
-              tc_commit(bar(L::kYFull + h));
+            for (int e = 0; e < 8; ++e)
+              mma_ss<true>(tmem + kTState, lm + (e / 4) * kBlk + (e % 4) * 2, bm + e * (2048 >> 4), id_s);
+            tc_commit(bar(L::kS));
+            tc_commit(bar(L::kBEmpty));
+          }
+          __syncwarp();
+          if constexpr (kMode != kLocal) {
+            if (g > 0) wait_warp(L::kYFree, (g - 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {  // Y = C H^T, of both heads at once
+              if (!zero) {
+                const uint32_t cm = sdesc_lo(ct), hm = sdesc_lo(sb + L::kH);
+                mma_ss<false>(tmem + kTY, cm, hm, id_g);
+#pragma unroll
+                for (int e = 1; e < 8; ++e)
+                  mma_ss<true>(tmem + kTY, cm + (e / 4) * kBlk + (e % 4) * 2, hm + (e / 4) * kBlk + (e % 4) * 2, id_g);
+              }
+              tc_commit(bar(L::kY2 + (g & 1)));
             }
             __syncwarp();
+            wait_warp(L::kMFull, g & 1);
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {  // Y += M X
+              if (elect_one()) {
+                const uint32_t xm = sdesc_lo(sb + L::kX + ((g & 1) * 2 + h) * kXT, kQ * 128);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  mma_ts(tmem + kTY + h * 64, tmem + kTG + (e / 4) * 64 + h * 32 + (e % 4) * 8, xm + e * (2048 >> 4), id_y,
+                         e > 0 ? 1u : zero ? 0u : 1u);
+                tc_commit(bar(L::kYFull + h));
+              }
+              __syncwarp();
+            }
           }
+          if (elect_one()) tc_commit(bar(L::kXEmpty + (g & 1)));
+          __syncwarp();
         }
-        if (elect_one()) tc_commit(bar(L::kXEmpty + (c & 1)));
-        __syncwarp();
       }
       if (!ok) {  // give-up: wait (bounded) for the MMAs issued so far
         if (elect_one()) tc_commit(bar(L::kDone));
@@ -791,38 +875,42 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
       }
       __syncwarp();
     } else if (warp < 19) {
-      // ------------------- copies by tensor maps: x, C and B, and z, a warp each
-      auto copy = [&](uint32_t dst, int column, int c, int b) {  // two blocks of 64 columns
+      // ------------------- copies by tensor maps: x, B and C, and z, a warp each
+      auto copy = [&](uint32_t dst, int column, int r, int b) {  // two blocks of 64 columns
         if (elect_one()) {
           mbar_arrive_expect_tx(bar(b), kBC);
-          tma_load_3d_plain(dst, &p.tm, column, 0, (int)first + c * kQ, bar(b));
-          tma_load_3d_plain(dst + kQ * 128, &p.tm, column + 64, 0, (int)first + c * kQ, bar(b));
+          tma_load_3d_plain(dst, &p.tm, column, 0, r, bar(b));
+          tma_load_3d_plain(dst + kQ * 128, &p.tm, column + 64, 0, r, bar(b));
         }
         __syncwarp();
       };
-      int nx = 0, nc = 0, nb = 0, nz = 0;  // copies begun
-      for (int c = 0; p.tiled && c < chunks; ++c) {
-        const uint32_t parity = ((c >> 1) & 1) ^ 1;
-        if (warp == 17) {
-          wait_warp(L::kXEmpty + (c & 1), parity);
-          if (!ok) break;
-          copy(sb + L::kX + (c & 1) * 2 * kXT, di + h0 * kSsmP, c, L::kXFull + (c & 1));
-          ++nx;
-          wait_warp(L::kBEmpty, (c & 1) ^ 1);
-          if (!ok) break;
-          copy(sb + L::kB, 2 * di, c, L::kBFull);
-          ++nb;
-          if constexpr (!kLocal) {
-            if (c > 0) wait_warp(L::kY2 + ((c - 1) & 1), ((c - 1) >> 1) & 1);  // C of the chunk before
+      StateUnit u = mine;
+      uint32_t g = 0;                          // the CTA's chunks
+      uint32_t nx = 0, nc = 0, nb = 0, nz = 0;  // copies begun
+      for (uint32_t n = 0; ok && (n == 0 || next_unit(u, n)); ++n) {
+        for (int c = 0; p.tiled && c < u.chunks; ++c, ++g) {
+          const int r = u.first + c * kQ;
+          if (warp == 17) {
+            wait_warp(L::kXEmpty + (g & 1), ((g >> 1) & 1) ^ 1);
             if (!ok) break;
-            copy(sb + L::kC, 2 * di + kSsmN, c, L::kCFull + (c & 1));
-            ++nc;
+            copy(sb + L::kX + (g & 1) * 2 * kXT, di + u.h0 * kSsmP, r, L::kXFull + (g & 1));
+            ++nx;
+            wait_warp(L::kBEmpty, (g & 1) ^ 1);
+            if (!ok) break;
+            copy(sb + L::kB, 2 * di, r, L::kBFull);
+            ++nb;
+            if constexpr (kMode != kLocal) {
+              if (g > 0) wait_warp(L::kY2 + ((g - 1) & 1), ((g - 1) >> 1) & 1);  // C of the chunk before
+              if (!ok) break;
+              copy(sb + L::kC, 2 * di + kSsmN, r, L::kCFull + (g & 1));
+              ++nc;
+            }
+          } else if constexpr (kMode != kLocal) {
+            if (g > 0) wait_warp(L::kOut + ((g - 1) & 1), ((g - 1) >> 1) & 1);
+            if (!ok) break;
+            copy(sb + L::kZ, u.h0 * kSsmP, r, L::kZFull + (g & 1));
+            ++nz;
           }
-        } else if constexpr (!kLocal) {
-          if (c > 0) wait_warp(L::kOut + ((c - 1) & 1), ((c - 1) >> 1) & 1);
-          if (!ok) break;
-          copy(sb + L::kZ, h0 * kSsmP, c, L::kZFull + (c & 1));
-          ++nz;
         }
       }
       if (!ok) {  // give-up: the copies in flight land before the shared memory is left
@@ -830,8 +918,8 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
           for (int n = 0; n < (1 << 20) && !mbar_try_wait(bar(b), parity); ++n) {
           }
         };
-        auto drain2 = [&](int b, int n) {  // the last two of n copies by turns
-          for (int i = max(0, n - 2); i < n; ++i) drain(b + (i & 1), (i >> 1) & 1);
+        auto drain2 = [&](int b, uint32_t n) {  // the last two of n copies by turns
+          for (uint32_t i = n > 2 ? n - 2 : 0; i < n; ++i) drain(b + (i & 1), (i >> 1) & 1);
         };
         drain2(L::kXFull, nx);
         drain2(L::kCFull, nc);
@@ -844,71 +932,106 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
       // tokens 4 l .. 4 l + 3 of both heads.  They are summed from the chunk's
       // end, so that the weights of the state's newest tokens are exact to
       // fp32 whatever the sum over the chunk is.
-      float rate[2], bias[2];
+      StateUnit u = mine;
+      uint32_t g = 0;        // the CTA's chunks
+      uint32_t asks = 0;     // requests for another CTA ...
+      bool asked = false;    // ... and whether one is open
+      for (uint32_t n = 0; ok; ++n) {
+        float rate[2], bias[2];
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        rate[g] = expf(bf(p.prm[h0 + g])) * 1.44269504088896340736f;
-        bias[g] = bf(p.prm[p.Hs + h0 + g]);
-      }
-      const uint16_t* col = p.zx + first * p.zx_stride + 2 * di + 2 * kSsmN + h0;  // two heads: 4 bytes
-      uint32_t raw[4];
-      auto fetch = [&](int c) {
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          const int j = c * kQ + 4 * lane + t;
-          raw[t] = j < len ? *(const uint32_t*)(col + (size_t)j * p.zx_stride) : 0;
+        for (int e = 0; e < 2; ++e) {
+          rate[e] = expf(bf(p.prm[u.h0 + e])) * 1.44269504088896340736f;
+          bias[e] = bf(p.prm[p.Hs + u.h0 + e]);
         }
-      };
-      fetch(0);
-      for (int c = 0; c < chunks; ++c) {
-        const int left = len - c * kQ;
-        float dt[2][4], after[2][4], last[2];
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          float lam[4];
+        const uint16_t* col = p.zx + (size_t)u.first * p.zx_stride + 2 * di + 2 * kSsmN + u.h0;  // two heads: 4 bytes
+        uint32_t raw[4];
+        auto fetch = [&](int c) {
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
-            dt[g][t] = softplus((g ? __uint_as_float(raw[t] & 0xFFFF0000u) : __uint_as_float(raw[t] << 16)) + bias[g]);
-            if (4 * lane + t >= left) dt[g][t] = 0.f;
-            // the token's decay in powers of two; 2^-160 is zero in fp32: a larger
-            // step changes nothing, and the cap bounds the rounding of the sums
-            lam[t] = fminf(rate[g] * dt[g][t], 160.f);
+            const int j = c * kQ + 4 * lane + t;
+            raw[t] = j < u.len ? *(const uint32_t*)(col + (size_t)j * p.zx_stride) : 0;
           }
-          float down = (lam[0] + lam[1]) + (lam[2] + lam[3]);  // this lane's and the later ones'
+        };
+        fetch(0);
+        for (int c = 0; c < u.chunks; ++c, ++g) {
+          if (kMode == kMore && c == u.chunks - 1) {
+            if (lane == 0) {
+              fence_proxy_async_smem();  // the last answer has been read
+              mbar_arrive_expect_tx(bar(L::kNext), 16);
+              cta_request(sb + L::kAnswer, bar(L::kNext));
+            }
+            __syncwarp();
+            ++asks, asked = true;
+          }
+          const int left = u.len - c * kQ;
+          float dt[2][4], after[2][4], last[2];
 #pragma unroll
-          for (int d = 1; d < 32; d <<= 1) {
-            const float v = __shfl_down_sync(0xffffffffu, down, d);
-            if (lane + d < 32) down += v;
-          }
-          float a = __shfl_down_sync(0xffffffffu, down, 1);
-          if (lane == 31) a = 0.f;
-          last[g] = __shfl_sync(0xffffffffu, down, 0);
+          for (int e = 0; e < 2; ++e) {
+            float lam[4];
 #pragma unroll
-          for (int t = 3; t >= 0; --t) {
-            after[g][t] = a;
-            a += lam[t];
+            for (int t = 0; t < 4; ++t) {
+              dt[e][t] = softplus((e ? __uint_as_float(raw[t] & 0xFFFF0000u) : __uint_as_float(raw[t] << 16)) + bias[e]);
+              if (4 * lane + t >= left) dt[e][t] = 0.f;
+              // the token's decay in powers of two; 2^-160 is zero in fp32: a larger
+              // step changes nothing, and the cap bounds the rounding of the sums
+              lam[t] = fminf(rate[e] * dt[e][t], 160.f);
+            }
+            float down = (lam[0] + lam[1]) + (lam[2] + lam[3]);  // this lane's and the later ones'
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+              const float v = __shfl_down_sync(0xffffffffu, down, d);
+              if (lane + d < 32) down += v;
+            }
+            float a = __shfl_down_sync(0xffffffffu, down, 1);
+            if (lane == 31) a = 0.f;
+            last[e] = __shfl_sync(0xffffffffu, down, 0);
+#pragma unroll
+            for (int t = 3; t >= 0; --t) {
+              after[e][t] = a;
+              a += lam[t];
+            }
           }
+          if (c + 1 < u.chunks) fetch(c + 1);
+          if (g > 0) {  // the last chunk's have been read
+            wait_warp(L::kWx, (g - 1) & 1);
+            wait_warp(kMode == kLocal ? L::kHFull : L::kMFull, (g - 1) & 1);
+            if (!ok) break;
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            *(float4*)(saft + e * kQ + 4 * lane) = make_float4(after[e][0], after[e][1], after[e][2], after[e][3]);
+            *(float4*)(sv + e * kQ + 4 * lane) = make_float4(lg2(dt[e][0]) - after[e][0], lg2(dt[e][1]) - after[e][1],
+                                                             lg2(dt[e][2]) - after[e][2], lg2(dt[e][3]) - after[e][3]);
+            const float end = __shfl_sync(0xffffffffu, after[e][3], lane | 7);  // behind these 32 tokens
+            if (lane < 24)
+              *(float4*)(su + e * 96 + 4 * lane) =
+                  make_float4(dt[e][0] * ex2(end - after[e][0]), dt[e][1] * ex2(end - after[e][1]),
+                              dt[e][2] * ex2(end - after[e][2]), dt[e][3] * ex2(end - after[e][3]));
+            if (lane == 0) slast[e] = last[e];
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::kScan));
         }
-        if (c + 1 < chunks) fetch(c + 1);
-        if (c > 0) {  // the last chunk's have been read
-          wait_warp(L::kWx, (c - 1) & 1);
-          wait_warp(kLocal ? L::kHFull : L::kMFull, (c - 1) & 1);
-          if (!ok) break;
-        }
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          *(float4*)(saft + g * kQ + 4 * lane) = make_float4(after[g][0], after[g][1], after[g][2], after[g][3]);
-          *(float4*)(sv + g * kQ + 4 * lane) = make_float4(lg2(dt[g][0]) - after[g][0], lg2(dt[g][1]) - after[g][1],
-                                                           lg2(dt[g][2]) - after[g][2], lg2(dt[g][3]) - after[g][3]);
-          const float end = __shfl_sync(0xffffffffu, after[g][3], lane | 7);  // behind these 32 tokens
-          if (lane < 24)
-            *(float4*)(su + g * 96 + 4 * lane) =
-                make_float4(dt[g][0] * ex2(end - after[g][0]), dt[g][1] * ex2(end - after[g][1]),
-                            dt[g][2] * ex2(end - after[g][2]), dt[g][3] * ex2(end - after[g][3]));
-          if (lane == 0) slast[g] = last[g];
+        if (kMode != kMore || !ok) break;
+        // ---- the next unit: asked for with the last chunk of this one
+        wait_warp(L::kNext, n & 1);
+        if (!ok) break;
+        asked = false;
+        int cta;
+        const bool taken = cta_taken(sb + L::kAnswer, cta);
+        wait_warp(L::kUnitEmpty, (n & 1) ^ 1);
+        if (!ok) break;
+        if (lane == 0) {
+          *(volatile int*)(smem + L::kUnit) = taken ? cta : -1;
+          mbar_arrive(bar(L::kUnitFull));
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::kScan));
+        if (!taken) break;
+        u = whole(cta);
+      }
+      if (asked) {  // give-up: the answer lands before the shared memory is left
+        for (int i = 0; i < (1 << 20) && !mbar_try_wait(bar(L::kNext), (asks - 1) & 1); ++i) {
+        }
       }
       __syncwarp();
     }
@@ -922,8 +1045,11 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
 // Once per device, when a handle is made.
 cudaError_t configure_prompt_state() {
   constexpr int kSplit = 256 * kRegsFront + kBehind * kRegsBehind + 128 * kRegsRest;
-  cudaError_t e = configure_split(k_prompt_state<false>, kStateThreads, kSplit, StateSmem::kTotal);
-  if (e == cudaSuccess) e = configure_split(k_prompt_state<true>, kStateThreads, kSplit, StateSmem::kTotal);
+  cudaError_t e = configure_split(k_prompt_state<kLocal>, kStateThreads, kSplit, kRegsFront, kRegsRest, StateSmem::kTotal);
+  if (e == cudaSuccess)
+    e = configure_split(k_prompt_state<kOnce>, kStateThreads, kSplit, kRegsFront, kRegsRest, StateSmem::kTotal);
+  if (e == cudaSuccess)
+    e = configure_split(k_prompt_state<kMore>, kStateThreads, kSplit, kRegsFront, kRegsRest, StateSmem::kTotal);
   return e;
 }
 
@@ -1002,8 +1128,11 @@ extern "C" int wave_hybrid_prompt_state(wave_t* h, int layer, const void* weight
     p.seg_state = h->ws.seg_state;
     p.seg_decay = h->ws.seg_decay;
     const int ctas = p.seg_cum[p.b.n] * pairs;
-    if (p.seg_chunks) k_prompt_state<true><<<ctas, kStateThreads, StateSmem::kTotal, st>>>(p);
-    k_prompt_state<false><<<ctas, kStateThreads, StateSmem::kTotal, st>>>(p);
+    if (p.seg_chunks) k_prompt_state<kLocal><<<ctas, kStateThreads, StateSmem::kTotal, st>>>(p);
+    if (ctas > sms)
+      k_prompt_state<kMore><<<ctas, kStateThreads, StateSmem::kTotal, st>>>(p);
+    else
+      k_prompt_state<kOnce><<<ctas, kStateThreads, StateSmem::kTotal, st>>>(p);
   }
   if (take(false)) k_prompt_state_rows<<<dim3(Hs, p.b.n), 256, 0, st>>>(p);
   return cudaGetLastError() == cudaSuccess ? WAVE_OK : WAVE_ECUDA;
