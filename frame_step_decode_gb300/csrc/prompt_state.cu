@@ -18,10 +18,13 @@ using namespace wave;
 
 namespace wave {
 
-// Sequences of at most this many tokens go token by token: 0.65 us a token
-// against 13 us for a chunk (one sequence), 2.9 us a token against 48 us (16
-// sequences of 64 heads), whatever the tokens in it.
-constexpr int kRowTokens = 16;
+// Sequences of up to so many tokens go token by token, by how many heads they
+// have together.  Up to half as many as SMs: 0.16 us a token and 2.5 to begin
+// with, against 13 us for a chunk with any number of tokens (a sequence of 64
+// heads, 25 tokens: 6.9 against 13.1; 48: 10.8 / 12.9; 64: 13.3 / 12.5).  More:
+// both take their time per head (16 sequences of 64 heads, 16 tokens: 24
+// against 40; 28: 41 / 39; two sequences, 24: 9 / 13; 48: 15 / 13).
+constexpr int kRowTokensFew = 48, kRowTokensMany = 28;
 
 struct StateParams {
   SeqBatch b;
@@ -48,73 +51,118 @@ struct StateParams {
 
 __device__ __forceinline__ float bf(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
 
-// The recurrent form: a CTA per (sequence, head), its 64 x 128 state in
-// registers (warp w: rows 8w..8w+7, lane: states 4 lane..+3).
-__global__ void __launch_bounds__(256) k_prompt_state_rows(const __grid_constant__ StateParams p) {
-  const int h = blockIdx.x, i = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int di = p.Hs * kSsmP, n = p.b.len(i);
-  const size_t base = ((size_t)p.b.slot[i] * p.Hs + h) * (kSsmP * kSsmN) + (size_t)warp * 8 * kSsmN + 4 * lane;
-  float4 st[8];
+// The recurrent form: a CTA per sequence and R rows (p) of a head's state.
+// Sixteen lanes have four rows, eight values of each row in registers, so that
+// a value of B or C read from shared memory serves four rows.  What depends on
+// the token only, or on token and row, is brought in for kRowBatch tokens at
+// once and made fp32 in shared memory (B, C, x, the gate silu(z), dt and the
+// decay); the loads of the next tokens run under the arithmetic of these.  All
+// of it is fp32.  Single tokens are bound by HBM, reading and writing the
+// state (56 sessions of 64 heads: 36.9 us = 6.40 TB/s, with three CTAs to an
+// SM; two 41.1, four 37.9).
+constexpr int kRowBatch = 16;
+
+template <int R>
+__global__ void __launch_bounds__(4 * R, R == 64 ? 3 : 1) k_prompt_state_rows(const __grid_constant__ StateParams p) {
+  constexpr int kUnroll = R == 64 ? 1 : 2;
+  constexpr int kThreads = 4 * R, kParts = kSsmP / R, kLoads = kRowBatch * 2 * kSsmN / 4 / kThreads;
+  __shared__ float4 sbc[kRowBatch][2 * kSsmN / 4];  // B | C
+  __shared__ float4 sx[kRowBatch][R / 4], sgate[kRowBatch][R / 4];
+  __shared__ float2 sda[kRowBatch];                 // dt, decay
+  const int tid = threadIdx.x, i = blockIdx.y, h = blockIdx.x / kParts, row0 = blockIdx.x % kParts * R;
+  const int r = tid >> 4, col = tid & 15, di = p.Hs * kSsmP, n = p.b.len(i);  // rows 4 r .. 4 r + 3
+  const uint16_t* rows = p.zx + (size_t)p.b.begin[i] * p.zx_stride;
+  uint2 vbc[kLoads] = {}, vx = {}, vz = {};
+  uint16_t vdt = 0;
+  const int xt = tid / (R / 4), xc = h * kSsmP + row0 + tid % (R / 4) * 4;  // this thread's token and column of x and z
+  auto load = [&](int t0) {
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int k = j * kThreads + tid, t = k / (2 * kSsmN / 4);
+      if (t0 + t < n) vbc[j] = __ldg((const uint2*)(rows + (size_t)(t0 + t) * p.zx_stride + 2 * di) + k % (2 * kSsmN / 4));
+    }
+    if (t0 + xt < n) {
+      const uint16_t* row = rows + (size_t)(t0 + xt) * p.zx_stride + xc;
+      vx = __ldg((const uint2*)(row + di));
+      vz = __ldg((const uint2*)row);
+    }
+    if (tid < kRowBatch && t0 + tid < n) vdt = rows[(size_t)(t0 + tid) * p.zx_stride + 2 * di + 2 * kSsmN + h];
+  };
+  auto f4 = [&](uint2 v) {
+    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
+                       __uint_as_float(v.y & 0xFFFF0000u));
+  };
+  const size_t base = (((size_t)p.b.slot[i] * p.Hs + h) * kSsmP + row0 + 4 * r) * kSsmN + 4 * col;
+  float4 st[4][2];
 #pragma unroll
   for (int j = 0; j < 8; ++j)
-    st[j] = p.b.start[i] > 0 ? __ldcs((const float4*)(p.state_in + base + j * kSsmN)) : make_float4(0.f, 0.f, 0.f, 0.f);
-  const float a_neg = -expf(bf(p.prm[h])), bias = bf(p.prm[p.Hs + h]), Dh = bf(p.prm[2 * p.Hs + h]);
-  const uint16_t* row = p.zx + (size_t)p.b.begin[i] * p.zx_stride;
-  uint16_t* orow = p.out + (size_t)p.b.begin[i] * p.out_stride + h * kSsmP + warp * 8;
-  // lanes with (lane & 3) == 0 finish row 4 b4 + 2 b3 + b2 (their bits 4, 3, 2)
-  const bool h4 = lane & 16, h3 = lane & 8, h2 = lane & 4;
-  const int mine = (h4 ? 4 : 0) + (h3 ? 2 : 0) + (h2 ? 1 : 0);
-  struct Token {  // a token's values, loaded one token ahead
-    uint2 x0, x1, B, C;
-    uint16_t dt, xm, zm;
-  };
-  auto load = [&](const uint16_t* r) {
-    Token k;
-    k.dt = r[2 * di + 2 * kSsmN + h];
-    k.x0 = *(const uint2*)(r + di + h * kSsmP + warp * 8);
-    k.x1 = *(const uint2*)(r + di + h * kSsmP + warp * 8 + 4);
-    k.B = *(const uint2*)(r + 2 * di + 4 * lane);
-    k.C = *(const uint2*)(r + 2 * di + kSsmN + 4 * lane);
-    k.xm = r[di + h * kSsmP + warp * 8 + mine];
-    k.zm = r[h * kSsmP + warp * 8 + mine];
-    return k;
-  };
-  Token next = load(row);
-  for (int t = 0; t < n; ++t, orow += p.out_stride) {
-    const Token k = next;
-    if (t + 1 < n) next = load(row += p.zx_stride);
-    const float raw = bf(k.dt) + bias;
-    const float dt = raw > 0.f ? raw + log1pf(expf(-raw)) : log1pf(expf(raw));
-    const float a = expf(a_neg * dt);
-    const float4 B = make_float4(bf((uint16_t)k.B.x), bf((uint16_t)(k.B.x >> 16)), bf((uint16_t)k.B.y), bf((uint16_t)(k.B.y >> 16)));
-    const float4 C = make_float4(bf((uint16_t)k.C.x), bf((uint16_t)(k.C.x >> 16)), bf((uint16_t)k.C.y), bf((uint16_t)(k.C.y >> 16)));
-    const uint32_t xw[4] = {k.x0.x, k.x0.y, k.x1.x, k.x1.y};
-    float x[8], y[8];
+    st[j >> 1][j & 1] = p.b.start[i] > 0 ? __ldcs((const float4*)(p.state_in + base + (j >> 1) * kSsmN + (j & 1) * 64))
+                                         : make_float4(0.f, 0.f, 0.f, 0.f);
+  load(0);
+  const float a_neg = -expf(bf(p.prm[h])), bias = bf(p.prm[p.Hs + h]), skip = bf(p.prm[2 * p.Hs + h]);
+  // the sums over a row's lanes end, by recursive halving, with this row's in four of them
+  const bool hi8 = tid & 8, hi4 = tid & 4;
+  const int mine = 4 * r + (hi8 ? 2 : 0) + (hi4 ? 1 : 0);
+  uint16_t* out = p.out + (size_t)p.b.begin[i] * p.out_stride + h * kSsmP + row0 + mine;
+  for (int t0 = 0; t0 < n; t0 += kRowBatch) {
+    if (t0) __syncthreads();  // the tokens before these have been read
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      x[j] = bf((uint16_t)(xw[j / 2] >> (16 * (j & 1))));
-      const float u = dt * x[j];
-      st[j].x = fmaf(a, st[j].x, u * B.x);
-      st[j].y = fmaf(a, st[j].y, u * B.y);
-      st[j].z = fmaf(a, st[j].z, u * B.z);
-      st[j].w = fmaf(a, st[j].w, u * B.w);
-      y[j] = st[j].x * C.x + st[j].y * C.y + st[j].z * C.z + st[j].w * C.w;
+    for (int j = 0; j < kLoads; ++j) {
+      const int k = j * kThreads + tid, t = k / (2 * kSsmN / 4);
+      if (t0 + t < n) sbc[t][k % (2 * kSsmN / 4)] = f4(vbc[j]);
     }
-    // row sums by recursive halving
+    if (t0 + xt < n) {
+      sx[xt][tid % (R / 4)] = f4(vx);
+      const float4 z = f4(vz);
+      sgate[xt][tid % (R / 4)] =
+          make_float4(z.x / (1.f + expf(-z.x)), z.y / (1.f + expf(-z.y)), z.z / (1.f + expf(-z.z)), z.w / (1.f + expf(-z.w)));
+    }
+    if (tid < kRowBatch && t0 + tid < n) {
+      const float raw = bf(vdt) + bias;
+      const float dt = raw > 0.f ? raw + log1pf(expf(-raw)) : log1pf(expf(raw));
+      sda[tid] = make_float2(dt, expf(a_neg * dt));
+    }
+    __syncthreads();
+    if (t0 + kRowBatch < n) load(t0 + kRowBatch);
+    const int m = min(kRowBatch, n - t0);
+#pragma unroll kUnroll
+    for (int t = 0; t < m; ++t, out += p.out_stride) {
+      const float2 da = sda[t], a2 = make_float2(da.y, da.y);
+      const float4 x4 = sx[t][r];
+      const float x[4] = {x4.x, x4.y, x4.z, x4.w};
+      float y[4];
+      float4 B[2], C[2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) y[j] = (h4 ? y[j + 4] : y[j]) + __shfl_xor_sync(0xffffffffu, h4 ? y[j] : y[j + 4], 16);
+      for (int j = 0; j < 2; ++j) B[j] = sbc[t][16 * j + col], C[j] = sbc[t][kSsmN / 4 + 16 * j + col];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) y[j] = (h3 ? y[j + 2] : y[j]) + __shfl_xor_sync(0xffffffffu, h3 ? y[j] : y[j + 2], 8);
-    y[0] = (h2 ? y[1] : y[0]) + __shfl_xor_sync(0xffffffffu, h2 ? y[0] : y[1], 4);
-    y[0] += __shfl_xor_sync(0xffffffffu, y[0], 2);
-    y[0] += __shfl_xor_sync(0xffffffffu, y[0], 1);
-    if ((lane & 3) == 0) {
-      const float xp = bf(k.xm), z = bf(k.zm);
-      orow[mine] = __bfloat16_as_ushort(__float2bfloat16_rn((y[0] + Dh * xp) * z / (1.0f + expf(-z))));
+      for (int e = 0; e < 4; ++e) {
+        const float u = da.x * x[e];
+        const float2 u2 = make_float2(u, u);
+        float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float4& s = st[e][j];
+          const float2 s0 = fma2(a2, make_float2(s.x, s.y), mul2(u2, make_float2(B[j].x, B[j].y)));
+          const float2 s1 = fma2(a2, make_float2(s.z, s.w), mul2(u2, make_float2(B[j].z, B[j].w)));
+          s = make_float4(s0.x, s0.y, s1.x, s1.y);
+          sum = fma2(s0, make_float2(C[j].x, C[j].y), sum);
+          sum = fma2(s1, make_float2(C[j].z, C[j].w), sum);
+        }
+        y[e] = sum.x + sum.y;
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) y[e] = (hi8 ? y[e + 2] : y[e]) + __shfl_xor_sync(0xffffffffu, hi8 ? y[e] : y[e + 2], 8);
+      y[0] = (hi4 ? y[1] : y[0]) + __shfl_xor_sync(0xffffffffu, hi4 ? y[0] : y[1], 4);
+      y[0] += __shfl_xor_sync(0xffffffffu, y[0], 2);
+      y[0] += __shfl_xor_sync(0xffffffffu, y[0], 1);
+      if ((tid & 3) == 0)
+        *out = __bfloat16_as_ushort(
+            __float2bfloat16_rn((y[0] + skip * ((const float*)sx[t])[mine]) * ((const float*)sgate[t])[mine]));
     }
   }
 #pragma unroll
-  for (int j = 0; j < 8; ++j) __stcs((float4*)(p.state_out + base + j * kSsmN), st[j]);
+  for (int j = 0; j < 8; ++j)
+    __stcs((float4*)(p.state_out + base + (j >> 1) * kSsmN + (j & 1) * 64), st[j >> 1][j & 1]);
 }
 
 // ------------------------------------------------------------ chunked form
@@ -1092,11 +1140,23 @@ extern "C" int wave_hybrid_prompt_state(wave_t* h, int layer, const void* weight
   int order[WAVE_MAX_SEQS];
   for (int i = 0; i < all.n; ++i) order[i] = i;
   std::stable_sort(order, order + all.n, [&](int a, int b) { return all.len(a) > all.len(b); });
+  const int pairs = Hs / 2, sms = pl.grid;
+  auto upto = [&](int tokens) {
+    int c = 0;
+    for (int i = 0; i < all.n; ++i) c += all.len(i) <= tokens;
+    return c;
+  };
+  int row_tokens = Hs * upto(kRowTokensFew) <= sms / 2 ? kRowTokensFew : kRowTokensMany;
+  // Where long sequences take the SMs several times over, a few short ones are
+  // run among them: their chunks cost less than a launch of their own (16
+  // prompts of 64 heads, one of them short: 97 against 103 us).
+  const int n_short = upto(row_tokens);
+  if ((all.n - n_short) * pairs > sms && Hs * n_short <= sms) row_tokens = 0;
   auto take = [&](bool chunked) {
     p.b.n = 0;
     for (int k = 0; k < all.n; ++k) {
       const int i = order[k];
-      if ((all.len(i) > kRowTokens) != chunked) continue;
+      if ((all.len(i) > row_tokens) != chunked) continue;
       p.b.begin[p.b.n] = all.begin[i];
       p.b.slot[p.b.n] = all.slot[i];
       p.b.start[p.b.n] = all.start[i];
@@ -1112,7 +1172,7 @@ extern "C" int wave_hybrid_prompt_state(wave_t* h, int layer, const void* weight
     // a second launch.  A chunk of the first costs about half of one of the
     // second, and a launch about one (2048 tokens of 64 heads, 32 CTAs of 16
     // chunks: 77 us whole).
-    const int pairs = Hs / 2, sms = pl.grid, longest = (p.b.len(0) + kQ - 1) / kQ;
+    const int longest = (p.b.len(0) + kQ - 1) / kQ;
     p.seg_chunks = 0;
     auto segments = [&](int t) {
       int n = 0;
@@ -1120,8 +1180,8 @@ extern "C" int wave_hybrid_prompt_state(wave_t* h, int layer, const void* weight
       return n;
     };
     int t = 1;
-    while (t < longest && segments(t) * pairs > sms) ++t;
-    if (3 * t + 4 < 2 * longest && segments(t) * pairs <= sms) p.seg_chunks = t;
+    while (p.b.n * pairs <= sms && t < longest && segments(t) * pairs > sms) ++t;
+    if (p.b.n * pairs <= sms && 3 * t + 4 < 2 * longest) p.seg_chunks = t;
     p.seg_cum[0] = 0;
     for (int i = 0; i < p.b.n; ++i)
       p.seg_cum[i + 1] = p.seg_cum[i] + (p.seg_chunks ? ((p.b.len(i) + kQ - 1) / kQ + t - 1) / t : 1);
@@ -1134,6 +1194,13 @@ extern "C" int wave_hybrid_prompt_state(wave_t* h, int layer, const void* weight
     else
       k_prompt_state<kOnce><<<ctas, kStateThreads, StateSmem::kTotal, st>>>(p);
   }
-  if (take(false)) k_prompt_state_rows<<<dim3(Hs, p.b.n), 256, 0, st>>>(p);
+  if (take(false)) {
+    // Few heads are cut into four CTAs each while all of these run at once (64
+    // heads, 25 tokens: 7.0 against 8.0 us; 256 heads, 16 tokens: 10.3 / 8.3).
+    if (Hs * p.b.n * 4 <= pl.grid * 2)
+      k_prompt_state_rows<16><<<dim3(Hs * 4, p.b.n), 64, 0, st>>>(p);
+    else
+      k_prompt_state_rows<64><<<dim3(Hs, p.b.n), 256, 0, st>>>(p);
+  }
   return cudaGetLastError() == cudaSuccess ? WAVE_OK : WAVE_ECUDA;
 }

@@ -2,7 +2,12 @@
 // batch, or moved into free ones.
 //
 // Bound by HBM: every byte a source holds is read once, however many slots it
-// goes to, and written once per destination.
+// goes to, and written once per destination; a CTA moves pieces of 16 KB, four
+// 16-byte loads of a thread in flight, and the grid (8 CTAs per SM) shares the
+// pieces of all sources and layers evenly whatever the positions, which only
+// the device knows (one session of 1500 positions to 8 slots, eight layers of
+// 32 x 128 heads: 144.6 us = 6.31 TB/s; four hybrid sessions, ten state layers
+// and two of history: 40.4 us = 5.79 TB/s).
 #include <cuda_runtime.h>
 #include <stdint.h>
 

@@ -489,6 +489,27 @@ def test_state_long_sequences_of_few_heads(hs, lens, starts):
     _check_state(cu, zx, prm, h0, list(range(n)), starts, hs, out, new, n)
 
 
+@pytest.mark.parametrize("hs,lens", [(64, [130, 129, 300, 64, 50, 257, 1, 17]), (24, [49 + 5 * i for i in range(30)] + [3]),
+                                     (12, [50 + i % 9 for i in range(64)])])
+def test_state_of_more_sequences_than_sms(hs, lens):
+    """Head pairs of sequences beyond the SMs, a few short sequences among
+    them: the CTAs that run take the others' places."""
+    n = len(lens)
+    starts = [i % 2 for i in range(n)]
+    cu, zx, prm, h0, out = _state_case(lens, hs, starts, seed=hs, S=n)
+    cfg, w = _hybrid(hs, S=n)
+    wt = _weights(cfg, prm)
+    new, again, out2 = torch.full_like(h0, 9.0), h0.clone(), torch.zeros_like(out)
+    try:
+        w.prompt_state(0, wt, cu, list(range(n)), starts, zx, h0, new, out)
+        w.prompt_state(0, wt, cu, list(range(n)), starts, zx, again, again, out2)
+        assert w.status() == fsd.WAVE_OK
+    finally:
+        w.close()
+    assert torch.equal(new, again) and torch.equal(out, out2), "in place, and whoever takes whose place"
+    _check_state(cu, zx, prm, h0, list(range(n)), starts, hs, out, new, n)
+
+
 @pytest.mark.parametrize("lens", [[16], [25], [129], [2048]])
 def test_state_is_carried_in_fp32(lens):
     """The 2-norm of the state's error, relative to the state: a weight is a
