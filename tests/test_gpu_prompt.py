@@ -305,6 +305,45 @@ def test_append(D, H, dtype, out_type):
         assert bool((t[~named] == 7).all())
 
 
+def test_append_rounds_its_quotients_as_a_division_does():
+    """Values a few units in the last place around every midpoint of two codes
+    (where a quotient that is not rounded as the division rounds it would give
+    the other code), at scales from tiny to huge, zeros, infinities and NaN:
+    V's codes and scales are the library's quantiser's, bit for bit."""
+    H, D, S = 2, 128, 1
+    codes = torch.arange(0x7F, dtype=torch.uint8).view(torch.float8_e4m3fn).double()
+    mid = (codes[1:] + codes[:-1]) / 2
+    g = np.random.default_rng(4)
+    rows = []
+    for top in np.concatenate([g.uniform(0.5, 2.0, 60) * 2.0 ** g.integers(-20, 20, 60), 2.0 ** np.arange(-148.0, 125.0, 3.0)]):
+        scale = np.float32(np.float32(top) / np.float32(448.0))
+        v = (mid.numpy() * float(scale)).astype(np.float32)  # 126 midpoints
+        v = (v.view(np.int32) + g.integers(-4, 5, v.shape).astype(np.int32) * (v != 0)).view(np.float32)
+        v = np.concatenate([v, [np.float32(top), 0.0]]).astype(np.float32) * np.where(g.random(128) < 0.5, -1, 1).astype(np.float32)
+        rows.append(np.clip(np.nan_to_num(v), -abs(np.float32(top)), abs(np.float32(top))))
+    rows += [np.zeros(128, np.float32), -np.zeros(128, np.float32)]
+    for bad in (np.inf, -np.inf, np.nan):
+        r = rows[3].copy()
+        r[5] = bad
+        rows.append(r)
+    v = torch.from_numpy(np.stack(rows + rows[:len(rows) % 2])).cuda().reshape(-1, H, D)
+    n = v.shape[0]
+    T = (n + 3) // 4 * 4
+    qkv = torch.cat([torch.zeros(n, 2 * H * D, device="cuda"), v.reshape(n, H * D)], 1)
+    kv = torch.zeros(1, 2, S, H, T, D, dtype=torch.uint8, device="cuda")
+    sc = torch.zeros(1, 2, S, H, T, device="cuda")
+    w = _wave(H, D, S, T)
+    try:
+        w.prompt_append(0, [0, n], [0], [0], qkv, kv, sc)
+        assert w.status() == fsd.WAVE_OK
+    finally:
+        w.close()
+    want, want_sc = torch.empty(n, H, D, dtype=torch.uint8, device="cuda"), torch.empty(n, H, device="cuda")
+    fsd.kv_quantize(v.contiguous(), want, want_sc)
+    assert torch.equal(kv[0, 1, 0, :, :n].transpose(0, 1), want)
+    assert torch.equal(sc[0, 1, 0, :, :n].t().contiguous().view(torch.int32), want_sc.view(torch.int32))
+
+
 def test_append_equals_the_steps_own_append():
     """The rows that a step quantises (its pre-quantisation dump: k rotated,
     v) give, appended as a prompt's v rows, the codes the step wrote."""
