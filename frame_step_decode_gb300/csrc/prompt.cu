@@ -88,7 +88,7 @@ __device__ __forceinline__ uint32_t encode4(const float* v, float sc) {
 // amax/448, code E4M3(v/scale) by an IEEE division), so that a prompt leaves
 // the history that stepping through it would have left.  Bound by HBM: a CTA
 // takes the same few heads of neighbouring tokens, so that the history's rows
-// it writes lie together (16 prompts, 9044 tokens, 32 heads of 128, qkv fp32:
+// it writes lie together (16 prompts, 8005 tokens, 32 heads of 128, qkv fp32:
 // 110 us = 5.97 TB/s; with the heads of one token in a CTA 126 us, with eight
 // divisions a lane and head 111.5 and for 25 tokens 7.0 us instead of 6.3).
 template <int D, typename In, typename Out>

@@ -8,7 +8,7 @@
 // ones with many heads, by latency for a single short one.  Measured (32 heads
 // of 128): a prompt of 8192 tokens 370 to 400 us with the power limit active,
 // 1.38 to 1.49 PFLOP/s of causal work; prompts of 4096, 1 and 2001 tokens, 8
-// K/V heads, fp16, 129 us = 1.32 PFLOP/s; 16 prompts of 1 to 1500 tokens, 9044
+// K/V heads, fp16, 129 us = 1.32 PFLOP/s; 16 prompts of 1 to 1500 tokens, 8005
 // in all, 74 us; a prompt of 25 tokens of 16 heads of 64, 6 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -125,7 +125,7 @@ __device__ __forceinline__ void pair_of_rank(const AttnParams& p, int rank, int&
   seq = rank - at_or_above(lo + 1);
 }
 
-// Flash attention on the tensor cores, a pair of 128-row query tiles per work
+// Attention on the tensor cores, a pair of 128-row query tiles per work
 // item.  One pass over the keys with the softmax's running maximum and sum:
 // S = Q K^T by tcgen05 into TMEM, a thread per row turns S into the weights
 // P (16 bits, written over S), O += P V by tcgen05 with P read from TMEM.  The
