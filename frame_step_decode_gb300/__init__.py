@@ -209,10 +209,15 @@ def _is_rows(t, rows: int, H: int, D: int) -> bool:
     return len(shape) == 3 and shape[2] == D and shape[1] == H and shape[0] >= rows
 
 
+_CURRENT: list = []  # torch's current device, and the current stream's handle on it
+
+
 def _stream(stream) -> int:
-    if stream is None:  # the current stream's handle, without a Stream object around it (4 of a call's 12 us)
-        import torch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if stream is None:  # without a Stream object around the handle (4 of a call's 12 us)
+        if not _CURRENT:
+            import torch
+            _CURRENT.extend((torch.cuda.current_device, torch._C._cuda_getCurrentRawStream))
+        return _CURRENT[1](_CURRENT[0]())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -25,7 +25,6 @@ struct AppendParams {
   void *q, *k, *v;       // [rows][H][D] 16-bit, or null
 };
 
-constexpr int kAppendHeads = 4;  // heads one group of lanes takes, their 12 loads in flight together
 constexpr int kAppendThreads = 128;
 
 template <typename T>
@@ -89,15 +88,14 @@ __device__ __forceinline__ uint32_t encode4(const float* v, float sc) {
 // the history that stepping through it would have left.  Bound by HBM: a CTA
 // takes the same few heads of neighbouring tokens, so that the history's rows
 // it writes lie together (16 prompts, 8005 tokens, 32 heads of 128, qkv fp32:
-// 110 us = 5.97 TB/s; with the heads of one token in a CTA 126 us, with eight
-// divisions a lane and head 111.5 and for 25 tokens 7.0 us instead of 6.3).
-template <int D, typename In, typename Out>
+// 110 us = 5.99 TB/s; with the heads of one token in a CTA 126 us).
+template <int D, int kHeads, typename In, typename Out>
 __global__ void __launch_bounds__(kAppendThreads) k_prompt_append(const __grid_constant__ AppendParams p) {
   constexpr int G = D / 4;  // lanes per row: 32 or 16
   const int lane = threadIdx.x % G;
-  const int chunks = (p.H + kAppendHeads - 1) / kAppendHeads;
+  const int chunks = (p.H + kHeads - 1) / kHeads;
   const int t = (int)(blockIdx.x / chunks) * (kAppendThreads / G) + (int)threadIdx.x / G;
-  const int h0 = (int)(blockIdx.x % chunks) * kAppendHeads;
+  const int h0 = (int)(blockIdx.x % chunks) * kHeads;
   const bool live = t < p.b.cum[p.b.n];  // the shuffles below need whole warps
   const int i = live ? seq_of(p.b, t) : 0;
   const int at = live ? t - p.b.cum[i] : 0;
@@ -112,7 +110,7 @@ __global__ void __launch_bounds__(kAppendThreads) k_prompt_append(const __grid_c
     c[2] = b.x, s[2] = b.y, c[3] = b.z, s[3] = b.w;
   }
 #pragma unroll
-  for (int hh = 0; hh < kAppendHeads; ++hh) {
+  for (int hh = 0; hh < kHeads; ++hh) {
     const int h = h0 + hh;
     const bool on = live && h < p.H;
     float x[3][4];
@@ -156,19 +154,27 @@ __global__ void __launch_bounds__(kAppendThreads) k_prompt_append(const __grid_c
 }
 
 template <int D, typename In, typename Out>
-static void launch_append(const AppendParams& p, cudaStream_t st) {
-  const int per_cta = kAppendThreads / (D / 4);
-  const long long ctas = ((long long)p.b.cum[p.b.n] + per_cta - 1) / per_cta * ((p.H + kAppendHeads - 1) / kAppendHeads);
-  k_prompt_append<D, In, Out><<<(unsigned)ctas, kAppendThreads, 0, st>>>(p);
+static void launch_append(const AppendParams& p, int sms, cudaStream_t st) {
+  // Many tokens: four heads to a group of lanes, their 12 loads in flight
+  // together.  Few: one, a shorter chain (25 tokens of 16 heads of 64: 2.7
+  // against 6.3 us; 32 heads of 128, qkv fp32, 300 tokens: 6.4 / 6.4, 1200:
+  // 20.0 / 18.4, 16 x 511: 141 / 113).
+  constexpr int kHeads = 4;
+  const long long per_cta = kAppendThreads / (D / 4), groups = ((long long)p.b.cum[p.b.n] + per_cta - 1) / per_cta;
+  const long long ctas = groups * ((p.H + kHeads - 1) / kHeads);
+  if (ctas < 4 * sms)
+    k_prompt_append<D, 1, In, Out><<<(unsigned)(groups * p.H), kAppendThreads, 0, st>>>(p);
+  else
+    k_prompt_append<D, kHeads, In, Out><<<(unsigned)ctas, kAppendThreads, 0, st>>>(p);
 }
 
 template <int D>
-static void launch_append_types(const AppendParams& p, int in, int out, cudaStream_t st) {
+static void launch_append_types(const AppendParams& p, int in, int out, int sms, cudaStream_t st) {
   if (in == WAVE_F32)
-    out == WAVE_BF16 ? launch_append<D, float, __nv_bfloat16>(p, st) : launch_append<D, float, __half>(p, st);
+    out == WAVE_BF16 ? launch_append<D, float, __nv_bfloat16>(p, sms, st) : launch_append<D, float, __half>(p, sms, st);
   else
-    out == WAVE_BF16 ? launch_append<D, __nv_bfloat16, __nv_bfloat16>(p, st)
-                     : launch_append<D, __nv_bfloat16, __half>(p, st);
+    out == WAVE_BF16 ? launch_append<D, __nv_bfloat16, __nv_bfloat16>(p, sms, st)
+                     : launch_append<D, __nv_bfloat16, __half>(p, sms, st);
 }
 
 }  // namespace wave
@@ -214,8 +220,8 @@ extern "C" int wave_prompt_append(wave_t* h, int layer, int n_seq, const int32_t
   cudaStream_t st = (cudaStream_t)stream;
   h->last_stream = st;
   if (D == 128)
-    launch_append_types<128>(p, qkv_type, out_type, st);
+    launch_append_types<128>(p, qkv_type, out_type, pl.grid, st);
   else
-    launch_append_types<64>(p, qkv_type, out_type, st);
+    launch_append_types<64>(p, qkv_type, out_type, pl.grid, st);
   return cudaGetLastError() == cudaSuccess ? WAVE_OK : WAVE_ECUDA;
 }

@@ -305,6 +305,37 @@ def test_append(D, H, dtype, out_type):
         assert bool((t[~named] == 7).all())
 
 
+@pytest.mark.parametrize("D,H", [(64, 3), (64, 13), (128, 6), (128, 9)])
+def test_append_of_many_tokens_equals_parts(D, H):
+    """Heads that are no multiple of four, in one call of many tokens and in
+    calls of few: the same bits."""
+    S, T, L = 3, 1600, 1
+    lens, starts = [1500, 1, 1203], [7, 1599, 0]
+    cu = _cu(lens, first=2)
+    g = torch.Generator(device="cuda").manual_seed(H)
+    qkv = torch.randn(cu[-1], 3 * H * D, generator=g, device="cuda")
+    got = []
+    w = _wave(H, D, S, T, L)
+    try:
+        for parts in (1, 20):
+            kv = torch.zeros(L, 2, S, H, T, D, dtype=torch.uint8, device="cuda")
+            sc = torch.zeros(L, 2, S, H, T, device="cuda")
+            q, k, v = (torch.zeros(cu[-1], H, D, dtype=torch.bfloat16, device="cuda") for _ in range(3))
+            if parts == 1:
+                w.prompt_append(0, cu, [0, 1, 2], starts, qkv, kv, sc, q, k, v)
+            else:
+                for s in range(3):
+                    for a in range(0, lens[s], 100):
+                        b = min(lens[s], a + 100)
+                        w.prompt_append(0, [cu[s] + a, cu[s] + b], [s], [starts[s] + a], qkv, kv, sc, q, k, v)
+            got.append((kv, sc, q, k, v))
+        assert w.status() == fsd.WAVE_OK
+    finally:
+        w.close()
+    for x, y in zip(*got):
+        assert torch.equal(x, y)
+
+
 def test_append_rounds_its_quotients_as_a_division_does():
     """Values a few units in the last place around every midpoint of two codes
     (where a quotient that is not rounded as the division rounds it would give
