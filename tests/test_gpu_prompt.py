@@ -221,6 +221,34 @@ def test_attention_batches_of_every_size():
     assert torch.equal(one[cu[-2]:cu[-1]], out[cu[-2]:cu[-1]])
 
 
+@pytest.mark.parametrize("H,Hkv,D", [(16, 4, 64), (12, 12, 128)])
+def test_attention_of_more_items_than_sms(H, Hkv, D):
+    """Items beyond the SMs, eager, on two streams at once and replayed: the
+    same bits whoever takes whose place."""
+    lens = [int(n) for n in np.random.default_rng(H).integers(1, 700, 24)]
+    cu, q, k, v, out = _attention(lens, H, Hkv, D, torch.bfloat16, seed=3)
+    ws = [_wave(H, D) for _ in range(2)]
+    outs = [torch.full_like(out, 7.0) for _ in range(2)]
+    try:
+        ws[0].prompt_attention(cu, q, k, v, out)
+        graph, streams = torch.cuda.CUDAGraph(), [torch.cuda.Stream() for _ in range(2)]
+        with torch.cuda.graph(graph, stream=streams[0]):
+            ws[0].prompt_attention(cu, q, k, v, outs[0], stream=streams[0])
+        for s in streams:
+            s.wait_stream(torch.cuda.current_stream())
+        for _ in range(3):
+            with torch.cuda.stream(streams[0]):
+                graph.replay()
+            ws[1].prompt_attention(cu, q, k, v, outs[1], stream=streams[1])
+        torch.cuda.synchronize()
+        assert ws[0].status() == fsd.WAVE_OK and ws[1].status() == fsd.WAVE_OK
+    finally:
+        for w in ws:
+            w.close()
+    _check_attention(cu, q, k, v, out)
+    assert torch.equal(outs[0], out) and torch.equal(outs[1], out)
+
+
 def test_attention_offsets_beyond_32_bits():
     """Rows whose offsets in elements pass 2^31 (slices of a wide buffer)."""
     H, D, n = 32, 128, 176000
@@ -928,6 +956,30 @@ def test_refusals_before_any_launch():
     finally:
         w.close()
         hw.close()
+
+
+def test_waits_that_run_out_with_more_work_than_sms():
+    """The same where CTAs take the places of others."""
+    cu, q, k, v, out = _attention([600] * 24, 8, 8, 128, torch.bfloat16, seed=2)
+    lens, starts, n = [200] * 6, [0, 3] * 3, 6
+    cs, zx, prm, h0, so = _state_case(lens, 64, starts, seed=1)
+    cfg, w = _hybrid(64, S=n, heads=8, dim=128)
+    wt = _weights(cfg, prm)
+    new = torch.zeros_like(h0)
+    calls = [lambda: w.prompt_attention(cu, q, k, v, out),
+             lambda: w.prompt_state(0, wt, cs, list(range(n)), starts, zx, h0, new, so)]
+    try:
+        for c in calls:
+            w.set_timeout_ns(1)
+            c()
+            assert w.status() == fsd.WAVE_ETIMEOUT
+            w.set_timeout_ns(2_000_000_000)
+            c()
+            assert w.status() == fsd.WAVE_OK
+    finally:
+        w.close()
+    _check_attention(cu, q, k, v, out)
+    _check_state(cs, zx, prm, h0, list(range(n)), starts, 64, so, new, n)
 
 
 # ------------------------------------------------------- the operators together
