@@ -205,7 +205,7 @@ struct ErrSink {
 };
 constexpr uint32_t kTryNs = 1000;  // how long one try may sleep
 inline ErrSink make_sink(int* err, int* err_out, long long timeout_ns) {
-  const long long n = timeout_ns / kTryNs + 1;
+  const long long n = timeout_ns / kTryNs;  // a limit below one try leaves no wait any time
   return {err, err_out, n > 0x7fffffff ? 0x7fffffff : (int)n};
 }
 // Wait for the phase with the given parity; false, and the timeout noted,

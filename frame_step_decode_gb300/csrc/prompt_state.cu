@@ -39,9 +39,10 @@ struct StateParams {
   long long zx_stride, out_stride;
   // Few sequences and heads leave SMs idle: a long sequence is then cut into
   // segments of seg_chunks chunks, a CTA each.  A first launch makes every
-  // segment's state from zero, the second begins each segment from those
-  // before it.  The last segment's place holds the state that the sequence
-  // begins from: state_out, which the second launch writes, may be state_in.
+  // segment's state from zero, a second one from these the states that the
+  // segments begin from, the third goes through the segments again.  The last
+  // segment's place first holds the state that the sequence begins from:
+  // state_out, which the third launch writes, may be state_in.
   int seg_chunks;                      // 0: whole sequences
   int32_t seg_cum[WAVE_MAX_SEQS + 1];  // segments before sequence i
   float* seg_state;                    // [segment and head pair][128 rows (head, p)][128]
@@ -188,9 +189,8 @@ __global__ void __launch_bounds__(4 * R, R == 64 ? 3 : 1) k_prompt_state_rows(co
 // what bounds the kernel: 4.8 us a chunk, 1.7 of them products (16 prompts of
 // 64 heads: tensor cores 24% active, HBM 25%, issue 42%).
 constexpr int kQ = 128;                 // tokens of a chunk
-constexpr int kStateThreads = 640;      // 2 warpgroups in front, 2 behind, 4 single warps
+constexpr int kStateThreads = 640;      // 2 warpgroups in front, 2 behind, 4 single warps; 96 registers each
 constexpr int kBehind = 256;
-constexpr int kRegsFront = 96, kRegsBehind = 104, kRegsRest = 80;  // 640 threads are launched with 96 each
 constexpr int kBC = kQ * kSsmN * 2;     // bytes of the B (or C) tile
 constexpr int kXT = kQ * kSsmP * 2;     // ... of one head's x (or z) tile
 
@@ -315,6 +315,33 @@ __device__ __forceinline__ float softplus(float raw) {
   return fmaxf(raw, 0.f) + s * q;
 }
 
+// The states that segments begin from, in the place of their own states from
+// zero: a thread per four values of a sequence's head pair, eight segments'
+// loads at once (with each CTA adding up those before it, a load after the
+// other, 2048 tokens of 4 heads took 52 us instead of 27).
+__global__ void __launch_bounds__(256) k_segment_states(const __grid_constant__ StateParams p) {
+  const int e = blockIdx.x * 256 + threadIdx.x, pairs = gridDim.y, seq = blockIdx.z;
+  const int first = p.seg_cum[seq], segs = p.seg_cum[seq + 1] - first;
+  auto slot = [&](int i) { return (float4*)p.seg_state + ((size_t)(first + i) * pairs + blockIdx.y) * (128 * kSsmN / 4) + e; };
+  const int hh = e / (kSsmP * kSsmN / 4);
+  float4 now = p.b.start[seq] > 0 ? *slot(segs - 1) : make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = 0; i0 < segs; i0 += 8) {
+    float4 own[8];
+    float d[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (i0 + j + 1 < segs) own[j] = *slot(i0 + j), d[j] = p.seg_decay[2 * ((first + i0 + j) * pairs + blockIdx.y) + hh];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (i0 + j >= segs) break;
+      *slot(i0 + j) = now;
+      const float f = ex2(-d[j]);
+      if (i0 + j + 1 < segs)
+        now = make_float4(fmaf(now.x, f, own[j].x), fmaf(now.y, f, own[j].y), fmaf(now.z, f, own[j].z), fmaf(now.w, f, own[j].w));
+    }
+  }
+}
+
 // What a CTA works on: a head pair of a sequence, or of a segment of one.
 struct StateUnit {
   int seq, h0, first, len;  // first: its first row
@@ -374,7 +401,6 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
   } else {
     mine = whole(blockIdx.x);
   }
-  const int seg0 = (int)blockIdx.x - seg * pairs;  // the sequence's first segment, of this head pair
   const int di = p.Hs * kSsmP;
   auto bar = [&](int b) { return sb + L::kBars + b * 8; };
   uint32_t* tmem_word = (uint32_t*)(smem + L::kMisc);
@@ -437,8 +463,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
   const int h = (warp >> 2) & 1, quad = warp & 3, row = quad * 32 + lane;  // a thread per token of head h0 + h
   const uint32_t lanes = (uint32_t)(quad * 32) << 16;
   const int hh = row >> 6, pp = row & 63;  // for the state: row (head hh, p)
-  // Whether a unit's sequence begins from state_in, and its state not as zero.
-  auto from_in = [&](const StateUnit& u) { return kMode != kLocal && p.b.start[u.seq] > 0; };
+  // Whether a unit's state does not begin as zero.
   auto goes_on = [&](const StateUnit& u) { return kMode != kLocal && (seg > 0 || p.b.start[u.seq] > 0); };
   // The unit after the n - 1 before it, if there is one: a CTA that has not
   // begun, taken over by the warp of the decays, so that the first chunk of one
@@ -463,17 +488,18 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
 
   if (warp < 8) {
     // -------------------------------------------------------------- in front
-    regs_take<kRegsFront>();
     float decayed = 0.f;  // kLocal: the decays so far, of head h
     StateUnit u = mine;
     uint32_t g = 0;  // the CTA's chunks
     for (uint32_t n = 0; n == 0 || next_unit(u, n, 1); ++n) {
       const float skip = bf(p.prm[2 * p.Hs + u.h0 + h]);
       const size_t state_at = (((size_t)p.b.slot[u.seq] * p.Hs + u.h0) * kSsmP + row) * kSsmN + h * 64;
-      const float* begin = kMode != kMore && p.seg_chunks ? p.seg_state +
-                                              (size_t)(seg0 + (p.seg_cum[u.seq + 1] - p.seg_cum[u.seq] - 1) * pairs) * (128 * kSsmN) +
-                                              row * kSsmN + h * 64
-                                        : p.state_in + state_at;
+        const float* begin = kMode != kMore && p.seg_chunks ? p.seg_state + (size_t)blockIdx.x * (128 * kSsmN) + row * kSsmN + h * 64
+                                                          : p.state_in + state_at;
+      if (goes_on(u)) {
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(begin));
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(begin + 32));
+      }
       for (int c = 0; c < u.chunks; ++c, ++g) {
         // ---- the state: its bf16 copy for C H^T, and the chunk's decay
         wait_warp(L::kScan, g & 1);
@@ -491,18 +517,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
               const float4* src = (const float4*)(begin + 16 * q);
               float4 f[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) f[e] = from_in(u) ? src[e] : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-              for (int i = 0; i < seg; ++i) {  // the segments before this one
-                const int cta = seg0 + i * pairs;
-                const float d = ex2(-p.seg_decay[2 * cta + hh]);
-                const float4* part = (const float4*)(p.seg_state + (size_t)cta * (128 * kSsmN) + row * kSsmN + h * 64 + 16 * q);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const float4 t = part[e];
-                  f[e] = make_float4(fmaf(f[e].x, d, t.x), fmaf(f[e].y, d, t.y), fmaf(f[e].z, d, t.z), fmaf(f[e].w, d, t.w));
-                }
-              }
+              for (int e = 0; e < 4; ++e) f[e] = src[e];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
                 v[4 * e] = __float_as_uint(f[e].x), v[4 * e + 1] = __float_as_uint(f[e].y);
@@ -634,7 +649,6 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
     }
   } else if (warp < 16) {
     // ---------------------------------------------------------------- behind
-    regs_take<kRegsBehind>();
     // (w X)^T of a chunk is made before the output of the chunk before it: the
     // state's product does not wait for the gate
     StateUnit u = mine;
@@ -841,7 +855,6 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
       }
     }
   } else {
-    regs_give<kRegsRest>();
     if (warp == 16) {
       // ---------------------------------------------------------------- MMAs
       constexpr uint32_t id_g = idesc_16(128, 128, false, false, false), id_y = idesc_16(128, 64, false, false, true),
@@ -1094,12 +1107,11 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
 
 // Once per device, when a handle is made.
 cudaError_t configure_prompt_state() {
-  constexpr int kSplit = 256 * kRegsFront + kBehind * kRegsBehind + 128 * kRegsRest;
-  cudaError_t e = configure_split(k_prompt_state<kLocal>, kStateThreads, kSplit, kRegsFront, kRegsRest, StateSmem::kTotal);
-  if (e == cudaSuccess)
-    e = configure_split(k_prompt_state<kOnce>, kStateThreads, kSplit, kRegsFront, kRegsRest, StateSmem::kTotal);
-  if (e == cudaSuccess)
-    e = configure_split(k_prompt_state<kMore>, kStateThreads, kSplit, kRegsFront, kRegsRest, StateSmem::kTotal);
+  const void* kernels[3] = {(const void*)k_prompt_state<kLocal>, (const void*)k_prompt_state<kOnce>,
+                            (const void*)k_prompt_state<kMore>};
+  cudaError_t e = cudaSuccess;
+  for (const void* k : kernels)
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, StateSmem::kTotal);
   return e;
 }
 
@@ -1171,9 +1183,9 @@ extern "C" int wave_hybrid_prompt_state(wave_t* h, int layer, const void* weight
   if (take(true)) {
     if (p.tiled && encode_rows_map(&p.tm, zxbcdt, pl.in_rows, 1, cu_seqlens[n_seq], zx_stride, kQ)) return WAVE_ECUDA;
     // Segments: the shortest that give no more CTAs than SMs, if that is worth
-    // a second launch.  A chunk of the first costs about half of one of the
-    // second, and a launch about one (2048 tokens of 64 heads: 77 us as 32 CTAs
-    // of 16 chunks, 51 in segments of 4).
+    // two more launches.  A chunk of the first costs about half of one of the
+    // last, the launches about two (2048 tokens of 64 heads: 77 us as 32 CTAs
+    // of 16 chunks, 50 in segments of 4; of 4 heads 27 in segments of 1).
     const int longest = (p.b.len(0) + kQ - 1) / kQ;
     p.seg_chunks = 0;
     auto segments = [&](int t) {
@@ -1190,7 +1202,10 @@ extern "C" int wave_hybrid_prompt_state(wave_t* h, int layer, const void* weight
     p.seg_state = h->ws.seg_state;
     p.seg_decay = h->ws.seg_decay;
     const int ctas = p.seg_cum[p.b.n] * pairs;
-    if (p.seg_chunks) k_prompt_state<kLocal><<<ctas, kStateThreads, StateSmem::kTotal, st>>>(p);
+    if (p.seg_chunks) {
+      k_prompt_state<kLocal><<<ctas, kStateThreads, StateSmem::kTotal, st>>>(p);
+      k_segment_states<<<dim3(128 * kSsmN / 4 / 256, pairs, p.b.n), 256, 0, st>>>(p);
+    }
     if (ctas > sms)
       k_prompt_state<kMore><<<ctas, kStateThreads, StateSmem::kTotal, st>>>(p);
     else

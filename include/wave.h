@@ -381,7 +381,7 @@ int wave_prompt_attention(wave_t* h, int n_seq, const int32_t* cu_seqlens, int n
  * decayed C B^T, and the state before the chunk) and the state's product takes
  * each weighted x as the sum of three bf16, to fp32's precision.  A token
  * whose x is not finite makes its own and later tokens of that channel not
- * finite (NaN in the rest of its chunk).  One to three launches.
+ * finite (NaN in the rest of its chunk).  One to four launches.
  */
 int wave_hybrid_prompt_state(wave_t* h, int layer, const void* weights, int n_seq, const int32_t* cu_seqlens,
                              const int32_t* slots, const int32_t* starts, const void* zxbcdt, int64_t zx_stride,

@@ -973,6 +973,9 @@ def test_waits_that_run_out_with_more_work_than_sms():
             w.set_timeout_ns(1)
             c()
             assert w.status() == fsd.WAVE_ETIMEOUT
+            w.set_timeout_ns(1000)  # a try each: some run out in the middle of the work
+            c()
+            assert w.status() in (fsd.WAVE_ETIMEOUT, fsd.WAVE_OK)
             w.set_timeout_ns(2_000_000_000)
             c()
             assert w.status() == fsd.WAVE_OK
