@@ -353,8 +353,7 @@ struct StateUnit {
 // sequences or segments.  kMore: whole sequences, more of them than SMs; a CTA
 // takes the place of CTAs that have not begun, so that a unit's first copies
 // and products run under the last of the unit before (16 prompts of 8005
-// tokens, 64 heads: 98 us, with a unit per CTA 102 us; a single instance for
-// both took 1.5 us longer for 2048 tokens in segments).
+// tokens, 64 heads: 97 us, with a unit per CTA 102).
 enum StateMode { kLocal, kOnce, kMore };
 template <StateMode kMode>
 __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_constant__ StateParams p) {
@@ -1000,12 +999,6 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
       uint32_t asks = 0;     // requests for another CTA ...
       bool asked = false;    // ... and whether one is open
       for (uint32_t n = 0; ok; ++n) {
-        float rate[2], bias[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          rate[e] = expf(bf(p.prm[u.h0 + e])) * 1.44269504088896340736f;
-          bias[e] = bf(p.prm[p.Hs + u.h0 + e]);
-        }
         const uint16_t* col = p.zx + (size_t)u.first * p.zx_stride + 2 * di + 2 * kSsmN + u.h0;  // two heads: 4 bytes
         uint32_t raw[4];
         auto fetch = [&](int c) {
@@ -1016,6 +1009,12 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
           }
         };
         fetch(0);
+        float rate[2], bias[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          rate[e] = expf(bf(p.prm[u.h0 + e])) * 1.44269504088896340736f;
+          bias[e] = bf(p.prm[p.Hs + u.h0 + e]);
+        }
         for (int c = 0; c < u.chunks; ++c, ++g) {
           if (kMode == kMore && c == u.chunks - 1) {
             if (lane == 0) {
@@ -1160,17 +1159,31 @@ extern "C" int wave_hybrid_prompt_state(wave_t* h, int layer, const void* weight
     for (int i = 0; i < all.n; ++i) c += all.len(i) <= tokens;
     return c;
   };
-  int row_tokens = Hs * upto(kRowTokensFew) <= sms / 2 ? kRowTokensFew : kRowTokensMany;
-  // Where long sequences take the SMs several times over, a few short ones are
-  // run among them: their chunks cost less than a launch of their own (16
-  // prompts of 64 heads, one of them short: 97 against 103 us).
-  const int n_short = upto(row_tokens);
-  if ((all.n - n_short) * pairs > sms && Hs * n_short <= sms) row_tokens = 0;
-  auto take = [&](bool chunked) {
+  const int n_short = upto(Hs * upto(kRowTokensFew) <= sms / 2 ? kRowTokensFew : kRowTokensMany);
+  int n_long = all.n - n_short;
+  // Segments: the shortest that give no more CTAs than SMs, if that is worth
+  // two more launches.  A chunk of the first costs about half of one of the
+  // last, the launches about two (2048 tokens of 64 heads: 77 us as 32 CTAs
+  // of 16 chunks, 50 in segments of 4; of 4 heads 27 in segments of 1).
+  auto chunks = [&](int k) { return (all.len(order[k]) + kQ - 1) / kQ; };
+  auto segments = [&](int t) {
+    int n = 0;
+    for (int k = 0; k < n_long; ++k) n += (chunks(k) + t - 1) / t;
+    return n;
+  };
+  int t = 1;
+  while (n_long * pairs <= sms && t < chunks(0) && segments(t) * pairs > sms) ++t;
+  const bool cut = n_long && n_long * pairs <= sms && 3 * t + 4 < 2 * chunks(0);
+  // Short sequences go along with long ones where SMs are left for them, and
+  // where long ones take all SMs several times over: a few chunks more cost
+  // less than a launch of their own (16 prompts of 64 heads, three of them
+  // short: 97 against 103 us).
+  const int left = sms - (cut ? segments(t) : n_long) * pairs;
+  if (n_long && (n_short * pairs <= left || (n_long * pairs > sms && Hs * n_short <= sms))) n_long = all.n;
+  auto take = [&](int from, int to) {
     p.b.n = 0;
-    for (int k = 0; k < all.n; ++k) {
+    for (int k = from; k < to; ++k) {
       const int i = order[k];
-      if ((all.len(i) > row_tokens) != chunked) continue;
       p.b.begin[p.b.n] = all.begin[i];
       p.b.slot[p.b.n] = all.slot[i];
       p.b.start[p.b.n] = all.start[i];
@@ -1180,29 +1193,15 @@ extern "C" int wave_hybrid_prompt_state(wave_t* h, int layer, const void* weight
     return p.b.n;
   };
   p.tiled = zx_stride % 8 == 0;
-  if (take(true)) {
+  if (take(0, n_long)) {
     if (p.tiled && encode_rows_map(&p.tm, zxbcdt, pl.in_rows, 1, cu_seqlens[n_seq], zx_stride, kQ)) return WAVE_ECUDA;
-    // Segments: the shortest that give no more CTAs than SMs, if that is worth
-    // two more launches.  A chunk of the first costs about half of one of the
-    // last, the launches about two (2048 tokens of 64 heads: 77 us as 32 CTAs
-    // of 16 chunks, 50 in segments of 4; of 4 heads 27 in segments of 1).
-    const int longest = (p.b.len(0) + kQ - 1) / kQ;
-    p.seg_chunks = 0;
-    auto segments = [&](int t) {
-      int n = 0;
-      for (int i = 0; i < p.b.n; ++i) n += ((p.b.len(i) + kQ - 1) / kQ + t - 1) / t;
-      return n;
-    };
-    int t = 1;
-    while (p.b.n * pairs <= sms && t < longest && segments(t) * pairs > sms) ++t;
-    if (p.b.n * pairs <= sms && 3 * t + 4 < 2 * longest) p.seg_chunks = t;
+    p.seg_chunks = cut ? t : 0;
     p.seg_cum[0] = 0;
-    for (int i = 0; i < p.b.n; ++i)
-      p.seg_cum[i + 1] = p.seg_cum[i] + (p.seg_chunks ? ((p.b.len(i) + kQ - 1) / kQ + t - 1) / t : 1);
+    for (int k = 0; k < n_long; ++k) p.seg_cum[k + 1] = p.seg_cum[k] + (cut ? (chunks(k) + t - 1) / t : 1);
     p.seg_state = h->ws.seg_state;
     p.seg_decay = h->ws.seg_decay;
-    const int ctas = p.seg_cum[p.b.n] * pairs;
-    if (p.seg_chunks) {
+    const int ctas = p.seg_cum[n_long] * pairs;
+    if (cut) {
       k_prompt_state<kLocal><<<ctas, kStateThreads, StateSmem::kTotal, st>>>(p);
       k_segment_states<<<dim3(128 * kSsmN / 4 / 256, pairs, p.b.n), 256, 0, st>>>(p);
     }
@@ -1211,10 +1210,10 @@ extern "C" int wave_hybrid_prompt_state(wave_t* h, int layer, const void* weight
     else
       k_prompt_state<kOnce><<<ctas, kStateThreads, StateSmem::kTotal, st>>>(p);
   }
-  if (take(false)) {
+  if (take(n_long, all.n)) {
     // Few heads are cut into four CTAs each while all of these run at once (64
-    // heads, 25 tokens: 7.0 against 8.0 us; 256 heads, 16 tokens: 10.3 / 8.3).
-    if (Hs * p.b.n * 4 <= pl.grid * 2)
+    // heads, 25 tokens: 6.9 against 8.0 us; 256 heads, 16 tokens: 10.3 / 8.2).
+    if (Hs * p.b.n * 4 <= sms * 2)
       k_prompt_state_rows<16><<<dim3(Hs * 4, p.b.n), 64, 0, st>>>(p);
     else
       k_prompt_state_rows<64><<<dim3(Hs, p.b.n), 256, 0, st>>>(p);
