@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "../../include/wave.h"
 #include "ctx.h"
@@ -184,7 +185,7 @@ __global__ void __launch_bounds__(4 * R, R == 64 ? 3 : 1) k_prompt_state_rows(co
 //
 // Two warpgroups in front (a head each: the state's pass between chunks, M),
 // two behind (a head each: (w X)^T, the gated output), and a warp each for the
-// MMAs, the copies of x, C and B, those of z, and the decays.  The chain from
+// MMAs, the copies of x and B, those of C and z, and the decays.  The chain from
 // chunk to chunk is the state's: its pass, (w X)^T and its product.  It is
 // what bounds the kernel: 4.8 us a chunk, 1.7 of them products (16 prompts of
 // 64 heads: tensor cores 24% active, HBM 25%, issue 42%).
@@ -257,19 +258,23 @@ __device__ __forceinline__ bool bar_and(int id, int threads, bool v) {
   return r != 0;
 }
 // Rows that no tensor map can describe (a stride that is no multiple of 16
-// bytes) are copied by the 256 threads behind, 8 bytes at a time: 128 tokens x
-// kCols values at column `col` of the rows from row0 on, as the same 128-byte
-// swizzled blocks of 64 columns.  Rows from n on repeat row n - 1.
-template <int kCols>
-__device__ __forceinline__ void copy_tile(uint32_t dst, const uint16_t* zx, long long stride, int col, size_t row0, int n) {
-  constexpr int kPer = kCols * 2 / 8;  // pieces of a row
-#pragma unroll 4
-  for (int q = (int)threadIdx.x - 256; q < kQ * kPer; q += kBehind) {
-    const int r = q / kPer, b = (q % kPer) * 8, blk = b >> 7, c = (b >> 4) & 7;
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst + blk * (kQ * 128) + r * 128 + ((c ^ (r & 7)) << 4) + (b & 15)),
-                 "l"(zx + (row0 + min(r, n - 1)) * stride + col + b / 2)
-                 : "memory");
-  }
+// bytes): a warp copies the tile, 128 tokens x 128 columns from (row0, col) on,
+// 8 bytes at a time, as the same 128-byte swizzled blocks of 64 columns.  Rows
+// from n on repeat row n - 1.
+__device__ __forceinline__ void copy_tile(uint32_t dst, const uint16_t* zx, long long stride, int col, int row0, int n) {
+  const int lane = threadIdx.x & 31, blk = lane >> 4, c = (lane >> 1) & 7;
+  const uint16_t* src = zx + (size_t)row0 * stride + col + lane * 4;
+  dst += blk * (kQ * 128) + (lane & 1) * 8;
+#pragma unroll 8
+  for (int r = 0; r < kQ; ++r, src += r < n ? stride : 0)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst + r * 128 + ((c ^ (r & 7)) << 4)), "l"(src) : "memory");
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// Waits for all tiles that this warp has begun to copy but the last kOpen.
+template <int kOpen>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kOpen) : "memory");
+  fence_proxy_async_smem();
 }
 
 __device__ __forceinline__ float lg2(float x) {
@@ -410,17 +415,16 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
 
   if (warp == 16) {
     if (lane == 0) {
-      const int copies = p.tiled ? 1 : kBehind / 32;
       for (int b = 0; b < 2; ++b) {
-        mbar_init(bar(L::kXFull + b), copies);
+        mbar_init(bar(L::kXFull + b), 1);
         mbar_init(bar(L::kXEmpty + b), 1);
-        mbar_init(bar(L::kCFull + b), copies);
-        mbar_init(bar(L::kZFull + b), copies);
+        mbar_init(bar(L::kCFull + b), 1);
+        mbar_init(bar(L::kZFull + b), 1);
         mbar_init(bar(L::kOut + b), kBehind / 32);
         mbar_init(bar(L::kY2 + b), 1);
         mbar_init(bar(L::kYFull + b), 1);
       }
-      mbar_init(bar(L::kBFull), copies);
+      mbar_init(bar(L::kBFull), 1);
       mbar_init(bar(L::kBEmpty), 1);
       mbar_init(bar(L::kMFull), 8);
       mbar_init(bar(L::kG), 1);
@@ -667,22 +671,6 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
         // tokens as 0 * NaN in M X: it is noted here, becomes zero once the
         // state's weights have been made of it, and is put back at the output.
         const uint32_t parity = (k >> 1) & 1;
-        if (!p.tiled) {
-          const int rows = min(kQ, left);
-          wait_warp(L::kXEmpty + b, parity ^ 1);
-          copy_tile<2 * kSsmP>(sb + L::kX + b * 2 * kXT, p.zx, p.zx_stride, di + u.h0 * kSsmP, row0, rows);
-          if constexpr (kMode != kLocal) {
-            if (k > 0) wait_warp(L::kY2 + ((k - 1) & 1), ((k - 1) >> 1) & 1);
-            copy_tile<kSsmN>(sb + L::kC, p.zx, p.zx_stride, 2 * di + kSsmN, row0, rows);
-          }
-          wait_warp(L::kBEmpty, (k & 1) ^ 1);
-          copy_tile<kSsmN>(sb + L::kB, p.zx, p.zx_stride, 2 * di, row0, rows);
-          asm volatile("cp.async.wait_all;" ::: "memory");
-          fence_proxy_async_smem();
-          arrive_warp(L::kXFull + b);
-          arrive_warp(L::kCFull + b);
-          arrive_warp(L::kBFull);
-        }
         wait_warp(L::kXFull + b, parity);
         uint8_t* xrow = smem + L::kX + (b * 2 + h) * kXT + row * 128;
         bool odd = false;
@@ -781,12 +769,6 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
         // ---- the output: y, gated, over z's row and from there to global
         uint8_t* ztile = smem + L::kZ + h * kXT;
         const uint32_t any_bad = *(volatile uint32_t*)sbad >> ((k & 3) * 8 + h * 4) & 15u;
-        if (!p.tiled) {
-          if (k > 0) wait_warp(L::kOut + ((k - 1) & 1), ((k - 1) >> 1) & 1);
-          copy_tile<2 * kSsmP>(sb + L::kZ, p.zx, p.zx_stride, out_h0 * kSsmP, out_row, min(kQ, out_left));
-          asm volatile("cp.async.wait_all;" ::: "memory");
-          arrive_warp(L::kZFull + b);
-        }
         wait_warp(L::kZFull + b, (k >> 1) & 1);
         wait_warp(L::kYFull + h, k & 1);
         tc_fence_after();
@@ -937,45 +919,67 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
       }
       __syncwarp();
     } else if (warp < 19) {
-      // ------------------- copies by tensor maps: x, B and C, and z, a warp each
-      auto copy = [&](uint32_t dst, int column, int r, int b) {  // two blocks of 64 columns
-        if (elect_one()) {
-          mbar_arrive_expect_tx(bar(b), kBC);
-          tma_load_3d_plain(dst, &p.tm, column, 0, r, bar(b));
-          tma_load_3d_plain(dst + kQ * 128, &p.tm, column + 64, 0, r, bar(b));
+      // ----------------------- copies: x and B by one warp, C and z by another
+      auto copy = [&](uint32_t dst, int column, int r, int n, int b) {  // two blocks of 64 columns
+        if (p.tiled) {
+          if (elect_one()) {
+            mbar_arrive_expect_tx(bar(b), kBC);
+            tma_load_3d_plain(dst, &p.tm, column, 0, r, bar(b));
+            tma_load_3d_plain(dst + kQ * 128, &p.tm, column + 64, 0, r, bar(b));
+          }
+          __syncwarp();
+        } else {
+          copy_tile(dst, p.zx, p.zx_stride, column, r, n);
         }
-        __syncwarp();
       };
+      // Without a tensor map the warp itself says when a tile is there: the
+      // first of a chunk's two once the second is under way (the CTA's first
+      // chunk: both buffers are free), or before the second is waited for.
+      auto landed = [&](int b, auto open) {
+        if (p.tiled) return;
+        copy_wait<open.value>();
+        arrive_warp(b);
+      };
+      constexpr std::integral_constant<int, 0> kNone{};
+      constexpr std::integral_constant<int, 1> kOne{};
       StateUnit u = mine;
-      uint32_t g = 0;                          // the CTA's chunks
-      uint32_t nx = 0, nc = 0, nb = 0, nz = 0;  // copies begun
+      uint32_t g = 0;                           // the CTA's chunks
+      uint32_t nx = 0, nb = 0, nc = 0, nz = 0;  // copies begun
       for (uint32_t n = 0; ok && (n == 0 || next_unit(u, n)); ++n) {
-        for (int c = 0; p.tiled && c < u.chunks; ++c, ++g) {
-          const int r = u.first + c * kQ;
+        for (int c = 0; c < u.chunks; ++c, ++g) {
+          const int r = u.first + c * kQ, rows = min(kQ, u.len - c * kQ);
           if (warp == 17) {
             wait_warp(L::kXEmpty + (g & 1), ((g >> 1) & 1) ^ 1);
             if (!ok) break;
-            copy(sb + L::kX + (g & 1) * 2 * kXT, di + u.h0 * kSsmP, r, L::kXFull + (g & 1));
+            copy(sb + L::kX + (g & 1) * 2 * kXT, di + u.h0 * kSsmP, r, rows, L::kXFull + (g & 1));
             ++nx;
+            if (g > 0) landed(L::kXFull + (g & 1), kNone);
             wait_warp(L::kBEmpty, (g & 1) ^ 1);
             if (!ok) break;
-            copy(sb + L::kB, 2 * di, r, L::kBFull);
+            copy(sb + L::kB, 2 * di, r, rows, L::kBFull);
             ++nb;
-            if constexpr (kMode != kLocal) {
-              if (g > 0) wait_warp(L::kY2 + ((g - 1) & 1), ((g - 1) >> 1) & 1);  // C of the chunk before
-              if (!ok) break;
-              copy(sb + L::kC, 2 * di + kSsmN, r, L::kCFull + (g & 1));
-              ++nc;
-            }
+            if (g == 0) landed(L::kXFull, kOne);
+            landed(L::kBFull, kNone);
           } else if constexpr (kMode != kLocal) {
-            if (g > 0) wait_warp(L::kOut + ((g - 1) & 1), ((g - 1) >> 1) & 1);
+            if (g > 0) wait_warp(L::kY2 + ((g - 1) & 1), ((g - 1) >> 1) & 1);  // C of the chunk before
             if (!ok) break;
-            copy(sb + L::kZ, u.h0 * kSsmP, r, L::kZFull + (g & 1));
+            copy(sb + L::kC, 2 * di + kSsmN, r, rows, L::kCFull + (g & 1));
+            ++nc;
+            if (g > 0) {
+              landed(L::kCFull + (g & 1), kNone);
+              wait_warp(L::kOut + ((g - 1) & 1), ((g - 1) >> 1) & 1);
+              if (!ok) break;
+            }
+            copy(sb + L::kZ, u.h0 * kSsmP, r, rows, L::kZFull + (g & 1));
             ++nz;
+            if (g == 0) landed(L::kCFull, kOne);
+            landed(L::kZFull + (g & 1), kNone);
           }
         }
       }
-      if (!ok) {  // give-up: the copies in flight land before the shared memory is left
+      if (!p.tiled) {
+        copy_wait<0>();
+      } else if (!ok) {  // give-up: the copies in flight land before the shared memory is left
         auto drain = [&](int b, uint32_t parity) {
           for (int n = 0; n < (1 << 20) && !mbar_try_wait(bar(b), parity); ++n) {
           }
