@@ -82,6 +82,7 @@ static void free_ctx(wave_ctx* h) {
 
 // Workspace, error mirror and RoPE table of a handle whose plan is set.
 static int build_ctx(wave_ctx* h) {
+  h->pl.prompts = true;
   const size_t total = carve_workspace(h->pl, nullptr, nullptr);
   if (cudaMalloc(&h->ws_block, total) != cudaSuccess) {
     h->ws_block = nullptr;

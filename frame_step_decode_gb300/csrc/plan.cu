@@ -267,8 +267,10 @@ size_t carve_workspace(const Plan& pl, char* base, Workspace* ws) {
       {(void**)&w.zero_pos, (size_t)pl.S_max * 4},
       {(void**)&w.zx, (size_t)(SP * pl.in_rows * 4)},
       {(void**)&w.ssm_out, (size_t)(SP * pl.d_inner * 2)},
-      {(void**)&w.seg_state, pl.hybrid ? (size_t)pl.grid * 2 * kSsmP * kSsmN * 4 : 0},
-      {(void**)&w.seg_decay, pl.hybrid ? (size_t)pl.grid * 2 * 4 : 0},
+      {(void**)&w.part_o, pl.prompts ? (size_t)pl.grid * 256 * D * 4 : 0},
+      {(void**)&w.part_ml, pl.prompts ? (size_t)pl.grid * 256 * 8 : 0},
+      {(void**)&w.seg_state, pl.hybrid && pl.prompts ? (size_t)pl.grid * 2 * kSsmP * kSsmN * 4 : 0},
+      {(void**)&w.seg_decay, pl.hybrid && pl.prompts ? (size_t)pl.grid * 2 * 4 : 0},
   };
   size_t o = 0;
   for (const Part& pt : parts) {

@@ -23,6 +23,7 @@ struct Plan {
   int hybrid = 0;
   wave_hybrid_config hcfg;   // the hybrid shape (hybrid only)
   int S_max = 0, S_pad_max = 0, T_max = 0, grid = 0;
+  bool prompts = false;  // the workspace has room for what the calls on prompts leave between launches
   long long off[6] = {0, 0, 0, 0, 0, 0};  // decoder blob: g_attn, Wqkv, Wo, g_mlp, Wgu, Wdown
   long long layer_elems = 0;              // decoder: one layer; hybrid: one group of layers
   long long hyb_M = 0, hyb_G = 0;         // hybrid: elements of a selective-state block / a group
@@ -64,6 +65,8 @@ struct Workspace {
   int32_t* zero_pos = nullptr;
   float* zx = nullptr;
   uint16_t* ssm_out = nullptr;
+  float* part_o = nullptr;     // attention over prompts: sums of parts of the keys, one per SM, ...
+  float2* part_ml = nullptr;   // ... and their maxima and sums of weights
   float* seg_state = nullptr;  // hybrid: states of prompt segments, one per SM, ...
   float* seg_decay = nullptr;  // ... and their decays
 };

@@ -30,7 +30,12 @@ namespace wave {
 
 constexpr int kRows = 128;         // query rows of one stream, and keys of one block
 constexpr int kAttnThreads = 384;  // 8 softmax warps (two streams), then copies, MMAs, guard, scheduler
+constexpr int kMaxParts = 160;     // items, where keys are divided
 constexpr int kRegsSoftmax = 208, kRegsRest = 80;  // a row's 128 scores stay in registers
+
+// A pair's part `part` of `parts` has the key blocks from part_begin on: even
+// shares, the last (with the diagonal blocks of both tiles) no smaller than two.
+__host__ __device__ inline int part_begin(int blocks, int parts, int part) { return (int)((long long)blocks * part / parts); }
 
 struct AttnParams {
   CUtensorMap tm_q, tm_k, tm_v;
@@ -43,6 +48,13 @@ struct AttnParams {
   float scale2;                     // scale * log2(e)
   int wide;                         // out's rows are 32-byte aligned
   int more;                         // more items than SMs
+  // Few items: the keys of a pair of row tiles are divided among several (see
+  // attention_parts).  Then CTA i works on a part of pair j, where cut_first[j]
+  // <= i, and leaves its sums in place i of the workspace.
+  int cuts;                         // pairs, 0: not divided
+  int32_t cut_first[kMaxParts + 1], cut_seq[kMaxParts], cut_level[kMaxParts];
+  float* part_o;                    // [item][256 rows][D], not divided by the sums of weights
+  float2* part_ml;                  // [item][256 rows]: the maximum and the sum
   ErrSink sink;
 };
 
@@ -50,7 +62,9 @@ struct AttnParams {
 struct AttnItem {
   int valid, head;
   int row0, left;      // first query row of the pair, rows from there to the sequence's end
-  int kv0;             // the sequence's first row
+  int kv0;             // the first row of its keys
+  int diag;            // whether the last key blocks are the tiles' own
+  int part;            // place of its sums in the workspace; -1: it has all keys
   int n0, n1;          // key blocks of stream 0 and 1 (0: no rows)
   uint32_t bad[2][4];  // keys of the last two V blocks that hold a value which is not finite
 };
@@ -136,7 +150,9 @@ __device__ __forceinline__ void pair_of_rank(const AttnParams& p, int rank, int&
 // block j + 1 be issued behind P V of block j although both use the same TMEM
 // columns; a commit covers every MMA issued before it, so s_full of block
 // j + 1 also says that P V of block j is complete.
-template <int D, bool kF16>
+// kCut: with few items, whose keys are divided (a variant of its own: as one
+// with the rest 2% slower for many items).
+template <int D, bool kF16, bool kCut>
 __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __grid_constant__ AttnParams p) {
   using L = AttnSmem<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -206,6 +222,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __gr
       const AttnItem& it = items[k & 1];
       const bool live = it.valid != 0;
       const int n = st ? it.n1 : it.n0;
+      const bool diag = !kCut || it.diag;
       if (live && n > 0) {
         float m = -INFINITY, l = 0.f;
         for (int j = 0; j < n; ++j, ++s_it) {
@@ -215,7 +232,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __gr
 #pragma unroll
           for (int c = 0; c < 4; ++c) tmem_ld32(tS(st) + lanes + 32 * c, s + 32 * c);
           tmem_ld_wait();
-          if (j == n - 1) {  // the diagonal block
+          if (j == n - 1 && diag) {  // the diagonal block
 #pragma unroll
             for (int c = 0; c < 128; ++c)
               if (c > row) s[c] = __float_as_uint(-INFINITY);
@@ -304,6 +321,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __gr
                     if (!isfinite(v)) o[i] = __float_as_uint(__uint_as_float(o[i]) + v);
                   }
                 }
+          }
+          if (kCut && it.part >= 0) {
+            if (st * kRows + row < it.left) {
+              const size_t at = (size_t)it.part * (2 * kRows) + st * kRows + row;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) store32(p.part_o + at * D + 32 * c + 8 * i, o + 8 * i);
+              if (c == 0) p.part_ml[at] = make_float2(m, l);
+            }
+            __syncwarp();
+            continue;
           }
           if (st * kRows + row < it.left) {
             uint32_t w[16];
@@ -424,11 +451,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __gr
           __syncwarp();
         };
         int n0 = 0, n1 = 0;  // key blocks of the streams (0: no item, or no second tile)
+        bool diag = true;
         for (uint32_t k = 0; ok; ++k) {
           if (!wait_warp(L::kItemFull + (k & 1), (k >> 1) & 1)) break;
           {
             const AttnItem& it = items[k & 1];
             n0 = it.valid ? it.n0 : 0, n1 = it.valid ? it.n1 : 0;
+            if constexpr (kCut) diag = it.diag;
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(L::kItemEmpty + (k & 1)));
@@ -447,10 +476,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __gr
           if (!ok) break;
           commit(L::kEmpty + ks);
           int vs = next_tile();
-          if (n0 == 1 && lane == 0) mbar_arrive(bar(L::kGo));
+          if (diag && n0 == 1 && lane == 0) mbar_arrive(bar(L::kGo));
           for (int j = 0; j < nb && ok; ++j) {
             const bool more = j + 1 < nb;
-            bool unchecked = j >= n0 - 1;  // the guard looks over V
+            bool unchecked = diag && j >= n0 - 1;  // the guard looks over V
             int vnext = 0;
 #pragma unroll
             for (int st = 0; st < 2; ++st) {
@@ -476,7 +505,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __gr
               }
               if (st == 0 && more) {
                 vnext = next_tile();
-                if (j + 1 >= n0 - 1 && lane == 0) mbar_arrive(bar(L::kGo));
+                if (diag && j + 1 >= n0 - 1 && lane == 0) mbar_arrive(bar(L::kGo));
               }
             }
             if (ok && more) commit(L::kEmpty + ks);
@@ -502,7 +531,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __gr
         if (!wait_warp(L::kItemFull + (k & 1), (k >> 1) & 1)) break;
         AttnItem& it = items[k & 1];
         const int valid = it.valid, n0 = it.n0, nb = max(it.n0, it.n1);
-        for (int j = n0 - 1; valid && j < nb; ++j) {
+        for (int j = n0 - 1; valid && (!kCut || it.diag) && j < nb; ++j) {
           if (!wait_warp(L::kGo, g_it & 1)) break;
           ++g_it;
           uint8_t* v = smem + L::kRing + ((it_r + 2 * j + 1) % L::kStages) * L::kTile;
@@ -557,7 +586,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __gr
         if (!wait_warp(L::kItemEmpty + (k & 1), ((k >> 1) & 1) ^ 1)) break;
         int idx = blockIdx.x;
         bool valid = true;
-        if (k > 0) valid = p.more;
+        if (k > 0) valid = !kCut && p.more;
         if (k > 0 && valid) {
           if (lane == 0) {
             fence_proxy_async_smem();  // the last answer has been read
@@ -572,18 +601,39 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __gr
           }
           valid = cta_taken(sb + L::kAnswer, idx);
         }
-        int seq = 0, level = 0;
-        if (valid) pair_of_rank(p, idx / p.Hq, seq, level);
+        int seq = 0, level = 0, head = idx % p.Hq, part = 0, parts = 1;
+        if constexpr (!kCut) {
+          if (valid) pair_of_rank(p, idx / p.Hq, seq, level);
+        } else {
+          int lo = 0, hi = p.cuts - 1;
+          while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (p.cut_first[mid] <= idx)
+              lo = mid;
+            else
+              hi = mid - 1;
+          }
+          seq = p.cut_seq[lo], level = p.cut_level[lo];
+          parts = (p.cut_first[lo + 1] - p.cut_first[lo]) / p.Hq;
+          head = (idx - p.cut_first[lo]) / parts, part = (idx - p.cut_first[lo]) % parts;
+        }
         if (lane == 0) {
           AttnItem& it = items[k & 1];
           const int left = p.len[seq] - level * 2 * kRows;
+          const int n0 = 2 * level + 1, n1 = left > kRows ? n0 + 1 : 0;
+          int from = 0, to = max(n0, n1);
+          if constexpr (kCut) {
+            from = part_begin(max(n0, n1), parts, part), to = part_begin(max(n0, n1), parts, part + 1);
+            it.diag = part == parts - 1;
+            it.part = parts > 1 ? idx : -1;
+          }
           it.valid = valid;
-          it.head = idx % p.Hq;
-          it.kv0 = p.begin[seq];
+          it.head = head;
+          it.kv0 = p.begin[seq] + from * kRows;
           it.row0 = p.begin[seq] + level * 2 * kRows;
           it.left = left;
-          it.n0 = 2 * level + 1;
-          it.n1 = left > kRows ? 2 * level + 2 : 0;
+          it.n0 = min(n0, to) - from;
+          it.n1 = n1 ? to - from : 0;
 #pragma unroll
           for (int i = 0; i < 8; ++i) it.bad[i / 4][i % 4] = 0;
           mbar_arrive(bar(L::kItemFull + (k & 1)));
@@ -599,16 +649,84 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __gr
   if (warp == 9) tmem_dealloc(tmem, 512);
 }
 
+// A row's parts joined: a CTA per 32 rows of a tile and head, D / 4 threads to a row.
+template <int D, bool kF16>
+__global__ void __launch_bounds__(256) k_join_parts(const __grid_constant__ AttnParams p) {
+  constexpr int kLanes = D / 4;
+  const int block = blockIdx.x % 8, head = blockIdx.x / 8 % p.Hq, pair = blockIdx.x / 8 / p.Hq;
+  const int parts = (p.cut_first[pair + 1] - p.cut_first[pair]) / p.Hq, col = (int)threadIdx.x % kLanes * 4;
+  if (parts == 1) return;  // written by the attention itself
+  const int seq = p.cut_seq[pair], first = p.cut_level[pair] * 2 * kRows;
+  const size_t item = p.cut_first[pair] + head * parts;
+  for (int r = block * 32 + (int)threadIdx.x / kLanes; r < block * 32 + 32; r += 256 / kLanes) {
+    if (first + r >= p.len[seq]) return;
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < parts; ++i) {
+      const size_t at = (item + i) * (2 * kRows) + r;
+      const float2 ml = p.part_ml[at];
+      const float4 v = *(const float4*)(p.part_o + at * D + col);
+      const float top = fmaxf(m, ml.x);
+      const float a = m == -INFINITY ? 0.f : ex2((m - top) * p.scale2), b = ml.x == -INFINITY ? 0.f : ex2((ml.x - top) * p.scale2);
+      l = l * a + ml.y * b;
+      o = make_float4(o.x * a + v.x * b, o.y * a + v.y * b, o.z * a + v.z * b, o.w * a + v.w * b);
+      m = top;
+    }
+    const float inv = 1.f / l;
+    *(uint2*)(p.out + (size_t)(p.begin[seq] + first + r) * p.out_stride + head * D + col) =
+        make_uint2(pack16<kF16>(o.x * inv, o.y * inv), pack16<kF16>(o.z * inv, o.w * inv));
+  }
+}
+
+// Whether and how the keys are divided: the smallest shares that give no more
+// items than SMs, if the longest then is shorter by more than the join costs
+// (heads of 128: 5500 tokens of one head 28 instead of 69 us, 2000 of 8 heads
+// 24 / 31, 1000 of 4 heads 16.5 / 18.6).
+static int attention_parts(AttnParams& p, int sms) {
+  auto blocks = [&](int seq, int level) {
+    const int left = p.len[seq] - level * 2 * kRows;
+    return left > kRows ? 2 * level + 2 : 2 * level + 1;
+  };
+  auto pairs = [&](int seq) { return (int)((p.len[seq] + 2LL * kRows - 1) / (2 * kRows)); };
+  const int most = blocks(0, pairs(0) - 1), limit = std::min(sms, kMaxParts);
+  auto lay = [&](int share) {  // the table, or false if there are too many items
+    int n = 0, items = 0;
+    p.cut_first[0] = 0;
+    for (int seq = 0; seq < p.n; ++seq)
+      for (int level = 0; level < pairs(seq); ++level) {
+        items += (blocks(seq, level) + share - 1) / share * p.Hq;
+        if (items > limit) return false;
+        p.cut_seq[n] = seq, p.cut_level[n] = level;
+        p.cut_first[++n] = items;
+      }
+    p.cuts = n;
+    return true;
+  };
+  for (int share = 2; share + 3 < most; ++share)
+    if (lay(share)) return p.cut_first[p.cuts];
+  p.cuts = 0;
+  return 0;
+}
+
 template <int D, bool kF16>
 static cudaError_t launch_attention(const AttnParams& p, long long items, cudaStream_t st) {
-  k_prompt_attention<D, kF16><<<(unsigned)items, kAttnThreads, AttnSmem<D>::kTotal, st>>>(p);
+  if (p.cuts) {
+    k_prompt_attention<D, kF16, true><<<(unsigned)items, kAttnThreads, AttnSmem<D>::kTotal, st>>>(p);
+    k_join_parts<D, kF16><<<(unsigned)(p.cuts * p.Hq * 8), 256, 0, st>>>(p);
+  } else {
+    k_prompt_attention<D, kF16, false><<<(unsigned)items, kAttnThreads, AttnSmem<D>::kTotal, st>>>(p);
+  }
   return cudaGetLastError();
 }
 
 template <int D, bool kF16>
 static cudaError_t configure() {
-  return configure_split(k_prompt_attention<D, kF16>, kAttnThreads, 256 * kRegsSoftmax + 128 * kRegsRest, kRegsSoftmax,
-                         kRegsRest, AttnSmem<D>::kTotal);
+  constexpr int kSplit = 256 * kRegsSoftmax + 128 * kRegsRest;
+  const cudaError_t e = configure_split(k_prompt_attention<D, kF16, false>, kAttnThreads, kSplit, kRegsSoftmax, kRegsRest,
+                                        AttnSmem<D>::kTotal);
+  return e != cudaSuccess ? e
+                          : configure_split(k_prompt_attention<D, kF16, true>, kAttnThreads, kSplit, kRegsSoftmax, kRegsRest,
+                                            AttnSmem<D>::kTotal);
 }
 
 // Once per device, when a handle is made.
@@ -655,10 +773,14 @@ extern "C" int wave_prompt_attention(wave_t* h, int n_seq, const int32_t* cu_seq
       encode_rows_map(&p.tm_k, k, D, n_kv_heads, rows, k_stride, kRows) ||
       encode_rows_map(&p.tm_v, v, D, n_kv_heads, rows, v_stride, kRows))
     return WAVE_ECUDA;
-  const long long items = pairs * H;
+  p.Hq = H;
+  p.cuts = 0;
+  const int cut = pairs * H <= h->pl.grid ? attention_parts(p, h->pl.grid) : 0;
+  const long long items = cut ? cut : pairs * H;
+  p.part_o = h->ws.part_o;
+  p.part_ml = h->ws.part_ml;
   if (items > 0x7fffffff) return WAVE_EINVAL;
   p.more = items > h->pl.grid;
-  p.Hq = H;
   p.group = H / n_kv_heads;
   p.v = (const uint16_t*)v;
   p.out = (uint16_t*)out;

@@ -350,7 +350,8 @@ int wave_prompt_append(wave_t* h, int layer, int n_seq, const int32_t* cu_seqlen
  * weights p are rounded to `type` for the second product.  Values at tokens
  * that a row does not attend to never reach it, whatever they are (NaN and
  * infinities included).  out must not overlap q, k or v.  Lengths are not
- * tied to the handle's T_max.
+ * tied to the handle's T_max.  One launch; two where few rows leave SMs idle
+ * and the keys are divided among them (joined in fp32).
  */
 int wave_prompt_attention(wave_t* h, int n_seq, const int32_t* cu_seqlens, int n_kv_heads, int type, const void* q,
                           int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,

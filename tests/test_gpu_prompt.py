@@ -249,6 +249,44 @@ def test_attention_of_more_items_than_sms(H, Hkv, D):
     assert torch.equal(outs[0], out) and torch.equal(outs[1], out)
 
 
+@pytest.mark.parametrize("lens,H,Hkv,D,dtype", [([2000], 1, 1, 128, torch.bfloat16), ([1500, 3, 900], 2, 1, 64, torch.float16),
+                                                ([1281, 1, 640], 4, 4, 64, torch.bfloat16), ([3000, 129], 3, 1, 128, torch.float16),
+                                                ([896, 897], 6, 2, 128, torch.bfloat16)])
+def test_attention_of_few_rows_divides_the_keys(lens, H, Hkv, D, dtype):
+    """Long prompts of few heads, whose keys are divided among CTAs and joined:
+    strided, with rows outside, values that are not finite where no row may see
+    them and where some do, eager and replayed."""
+    cu, q, k, v, out = _attention(lens, H, Hkv, D, dtype, seed=7, first=3, tail=5)
+    wide = torch.full((q.shape[0], H * D + 8), 7.0, dtype=dtype, device="cuda")
+    out = wide[:, :H * D].unflatten(1, (H, D))
+    k[:3], v[:3], k[cu[-1]:], v[cu[-1]:] = float("nan"), float("inf"), float("nan"), float("nan")
+    w = _wave(H, D)
+    try:
+        w.prompt_attention(cu, q, k, v, out)
+        assert w.status() == fsd.WAVE_OK
+        _check_attention(cu, q, k, v, out)
+        assert bool((wide[:, H * D:] == 7).all())
+        once = out.clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            w.prompt_attention(cu, q, k, v, out)
+        wide[3:cu[-1]].fill_(9)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, once)
+        t = cu[0] + lens[0] * 2 // 3  # from this token on, not before
+        v[t, 0, 5] = float("inf")
+        w.prompt_attention(cu, q, k, v, out)
+        assert w.status() == fsd.WAVE_OK
+        own = out[:, :H // Hkv]
+        assert torch.equal(own[:t], once[:t, :H // Hkv]) and not bool(torch.isfinite(own[t:cu[1], :, 5]).any())
+        assert torch.equal(out[cu[1]:], once[cu[1]:]) and torch.equal(out[:, H // Hkv:], once[:, H // Hkv:])
+        keep = [i for i in range(D) if i != 5]
+        assert torch.equal(own[t:cu[1]][..., keep], once[t:cu[1], :H // Hkv][..., keep])
+    finally:
+        w.close()
+
+
 def test_attention_offsets_beyond_32_bits():
     """Rows whose offsets in elements pass 2^31 (slices of a wide buffer)."""
     H, D, n = 32, 128, 176000
