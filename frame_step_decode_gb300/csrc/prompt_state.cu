@@ -323,12 +323,14 @@ __device__ __forceinline__ float softplus(float raw) {
 // The states that segments begin from, in the place of their own states from
 // zero: a thread per four values of a sequence's head pair, eight segments'
 // loads at once (with each CTA adding up those before it, a load after the
-// other, 2048 tokens of 4 heads took 52 us instead of 27).
+// other, 2048 tokens of 4 heads took 52 us instead of 28).
 __global__ void __launch_bounds__(256) k_segment_states(const __grid_constant__ StateParams p) {
   const int e = blockIdx.x * 256 + threadIdx.x, pairs = gridDim.y, seq = blockIdx.z;
   const int first = p.seg_cum[seq], segs = p.seg_cum[seq + 1] - first;
   auto slot = [&](int i) { return (float4*)p.seg_state + ((size_t)(first + i) * pairs + blockIdx.y) * (128 * kSsmN / 4) + e; };
   const int hh = e / (kSsmP * kSsmN / 4);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   float4 now = p.b.start[seq] > 0 ? *slot(segs - 1) : make_float4(0.f, 0.f, 0.f, 0.f);
   for (int i0 = 0; i0 < segs; i0 += 8) {
     float4 own[8];
@@ -366,6 +368,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
   extern __shared__ __align__(1024) uint8_t smem[];
   const uint32_t sb = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if constexpr (kMode == kLocal) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int pairs = p.Hs / 2;
   auto whole = [&](int cta) {  // a CTA's sequence and head pair
     StateUnit u;
@@ -494,6 +497,8 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
     float decayed = 0.f;  // kLocal: the decays so far, of head h
     StateUnit u = mine;
     uint32_t g = 0;  // the CTA's chunks
+    // the states that segments begin from are there, and what state_in held has been read
+    if (kMode == kOnce && p.seg_chunks) asm volatile("griddepcontrol.wait;" ::: "memory");
     for (uint32_t n = 0; n == 0 || next_unit(u, n, 1); ++n) {
       const float skip = bf(p.prm[2 * p.Hs + u.h0 + h]);
       const size_t state_at = (((size_t)p.b.slot[u.seq] * p.Hs + u.h0) * kSsmP + row) * kSsmN + h * 64;
@@ -1108,6 +1113,23 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
   if (warp == 16) tmem_dealloc(tmem, 512);
 }
 
+// A launch whose CTAs may begin (early) when all of the launch before have
+// begun or ended; the kernel itself waits for that launch to be complete.
+template <typename K>
+static cudaError_t launch(K kernel, dim3 grid, int threads, int smem, cudaStream_t st, bool early, const StateParams& p) {
+  cudaLaunchAttribute a;
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = early;
+  cudaLaunchConfig_t c = {};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  c.attrs = &a;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, p);
+}
+
 // Once per device, when a handle is made.
 cudaError_t configure_prompt_state() {
   const void* kernels[3] = {(const void*)k_prompt_state<kLocal>, (const void*)k_prompt_state<kOnce>,
@@ -1168,7 +1190,7 @@ extern "C" int wave_hybrid_prompt_state(wave_t* h, int layer, const void* weight
   // Segments: the shortest that give no more CTAs than SMs, if that is worth
   // two more launches.  A chunk of the first costs about half of one of the
   // last, the launches about two (2048 tokens of 64 heads: 77 us as 32 CTAs
-  // of 16 chunks, 50 in segments of 4; of 4 heads 27 in segments of 1).
+  // of 16 chunks, 50 in segments of 4; of 4 heads 23 in segments of 1).
   auto chunks = [&](int k) { return (all.len(order[k]) + kQ - 1) / kQ; };
   auto segments = [&](int t) {
     int n = 0;
@@ -1206,13 +1228,19 @@ extern "C" int wave_hybrid_prompt_state(wave_t* h, int layer, const void* weight
     p.seg_decay = h->ws.seg_decay;
     const int ctas = p.seg_cum[n_long] * pairs;
     if (cut) {
+      // Where a third of the SMs is free, the CTAs of the second and third
+      // launch begin beside those of the one before and wait for them (2048
+      // tokens of 4 heads 28.4 -> 23.4 us; 128 CTAs 27.1 -> 28.6).
+      const bool early = 3 * ctas <= 2 * sms;
       k_prompt_state<kLocal><<<ctas, kStateThreads, StateSmem::kTotal, st>>>(p);
-      k_segment_states<<<dim3(128 * kSsmN / 4 / 256, pairs, p.b.n), 256, 0, st>>>(p);
-    }
-    if (ctas > sms)
+      if (launch(k_segment_states, dim3(128 * kSsmN / 4 / 256, pairs, p.b.n), 256, 0, st, early, p) != cudaSuccess ||
+          launch(k_prompt_state<kOnce>, dim3(ctas), kStateThreads, StateSmem::kTotal, st, early, p) != cudaSuccess)
+        return WAVE_ECUDA;
+    } else if (ctas > sms) {
       k_prompt_state<kMore><<<ctas, kStateThreads, StateSmem::kTotal, st>>>(p);
-    else
+    } else {
       k_prompt_state<kOnce><<<ctas, kStateThreads, StateSmem::kTotal, st>>>(p);
+    }
   }
   if (take(n_long, all.n)) {
     // Few heads are cut into four CTAs each while all of these run at once (64
