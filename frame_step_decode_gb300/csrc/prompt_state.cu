@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(4 * R, R == 64 ? 3 : 1) k_prompt_state_rows(co
 // over the whole sequence.  M and the H of C H^T are rounded to bf16 once
 // (the output is bf16).  The state is fp32, so (w X)^T is the sum of three bf16
 // parts, all of fp32's 24 bits: with two the state was 2.4e-6 off (2-norm),
-// with three 2e-7, the tensor core's own sums.
+// with three 3e-7.
 //
 // Two warpgroups in front (a head each: the state's pass between chunks, M),
 // two behind (a head each: (w X)^T, the gated output), and a warp each for the
@@ -362,6 +362,7 @@ struct StateUnit {
 // and products run under the last of the unit before (16 prompts of 8005
 // tokens, 64 heads: 97 us, with a unit per CTA 102).
 enum StateMode { kLocal, kOnce, kMore };
+
 template <StateMode kMode>
 __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_constant__ StateParams p) {
   using L = StateSmem;
@@ -502,8 +503,9 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
     for (uint32_t n = 0; n == 0 || next_unit(u, n, 1); ++n) {
       const float skip = bf(p.prm[2 * p.Hs + u.h0 + h]);
       const size_t state_at = (((size_t)p.b.slot[u.seq] * p.Hs + u.h0) * kSsmP + row) * kSsmN + h * 64;
-        const float* begin = kMode != kMore && p.seg_chunks ? p.seg_state + (size_t)blockIdx.x * (128 * kSsmN) + row * kSsmN + h * 64
-                                                          : p.state_in + state_at;
+      const float* begin = kMode != kMore && p.seg_chunks
+                               ? p.seg_state + (size_t)blockIdx.x * (128 * kSsmN) + row * kSsmN + h * 64
+                               : p.state_in + state_at;
       if (goes_on(u)) {
         asm volatile("prefetch.global.L1 [%0];" ::"l"(begin));
         asm volatile("prefetch.global.L1 [%0];" ::"l"(begin + 32));
