@@ -807,6 +807,32 @@ def test_state_batch_replays_from_a_graph():
     _check_state(cu, zx, prm, h0, list(range(n)), starts, hs, out, new, n)
 
 
+@pytest.mark.parametrize("hs,lens,starts", [(4, [1300, 20], [2, 0]), (8, [900], [0]), (24, [1000, 3, 640], [1, 4, 0])])
+def test_state_segments_replay(hs, lens, starts):
+    """Segmented sequences from a graph, in place, again and again: each replay
+    goes on from the state of the one before, as eager calls do."""
+    n = len(lens)
+    cu, zx, prm, h0, out = _state_case(lens, hs, starts, seed=hs + 1, S=n)
+    cfg, w = _hybrid(hs, S=n)
+    wt = _weights(cfg, prm)
+    a, b = h0.clone(), h0.clone()
+    out2 = torch.zeros_like(out)
+    try:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            w.prompt_state(0, wt, cu, list(range(n)), starts, zx, b, b, out2)
+        w.prompt_state(0, wt, cu, list(range(n)), starts, zx, a, a, out)
+        _check_state(cu, zx, prm, h0, list(range(n)), starts, hs, out, a, n)
+        for _ in range(2):
+            w.prompt_state(0, wt, cu, list(range(n)), starts, zx, a, a, out)
+        for _ in range(3):
+            graph.replay()
+        assert w.status() == fsd.WAVE_OK
+        assert torch.equal(a, b) and torch.equal(out, out2)
+    finally:
+        w.close()
+
+
 @pytest.mark.parametrize("pad", [0, 4])
 def test_state_offsets_beyond_32_bits(pad):
     """Rows whose offsets in elements pass 2^31."""
