@@ -374,7 +374,9 @@ int encode_act_maps(const Plan& pl, const Workspace& ws, int S_pad, Maps* m) {
 int encode_rows_map(CUtensorMap* m, const void* base, int D, int heads, long long rows, long long stride,
                     int box_rows) {
   cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)rows};
-  cuuint64_t str[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
+  // strides are multiples of 16 bytes: D * 2 between heads is one, but need not
+  // be where a single head stands for a whole row, and is used for nothing there
+  cuuint64_t str[2] = {(cuuint64_t)(heads > 1 ? D : stride) * 2, (cuuint64_t)stride * 2};
   cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows};
   return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, (void*)base, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B)
              ? WAVE_OK
