@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(4 * R, R == 64 ? 3 : 1) k_prompt_state_rows(co
     if (tid < kRowBatch && t0 + tid < n) {
       const float raw = bf(vdt) + bias;
       const float dt = raw > 0.f ? raw + log1pf(expf(-raw)) : log1pf(expf(raw));
-      sda[tid] = make_float2(dt, expf(a_neg * dt));
+      sda[tid] = make_float2(dt, dt == 0.f ? 1.f : expf(a_neg * dt));  // also at an infinite rate
     }
     __syncthreads();
     if (t0 + kRowBatch < n) load(t0 + kRowBatch);
@@ -1046,8 +1046,9 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
               dt[e][t] = softplus((e ? __uint_as_float(raw[t] & 0xFFFF0000u) : __uint_as_float(raw[t] << 16)) + bias[e]);
               if (4 * lane + t >= left) dt[e][t] = 0.f;
               // the token's decay in powers of two; 2^-160 is zero in fp32: a larger
-              // step changes nothing, and the cap bounds the rounding of the sums
-              lam[t] = fminf(rate[e] * dt[e][t], 160.f);
+              // step changes nothing, and the cap bounds the rounding of the sums.
+              // No step, no decay, also at a rate beyond fp32's range (inf * 0)
+              lam[t] = dt[e][t] == 0.f ? 0.f : fminf(rate[e] * dt[e][t], 160.f);
             }
             float down = (lam[0] + lam[1]) + (lam[2] + lam[3]);  // this lane's and the later ones'
 #pragma unroll

@@ -35,3 +35,21 @@ def test_state_rows_padded_to_16_bytes(hs, lens):
     new = _run_state(hs, case, slots, starts, n)
     _check_state(cu, zx, prm, h0, slots, starts, hs, out, new, n)
     assert bool((out[:2] == 7).all()) and bool((out[cu[-1]:] == 7).all())
+
+
+@pytest.mark.parametrize("a_log", [88.0, 89.0, 3e38])
+@pytest.mark.parametrize("lens", [[25, 28], [129, 384, 200], [1300]])
+def test_state_decays_beyond_fp32(a_log, lens):
+    """exp(A_log) near the end of fp32's range and beyond it: a token with a
+    step forgets all before it, one whose step is zero nothing, and what is not
+    there (the rest of the last chunk) does neither."""
+    hs, n = 4, len(lens)
+    case = _state_case(lens, hs, [3] * n, seed=7, S=n)
+    cu, zx, prm, h0, out = case
+    prm[:hs], prm[hs:2 * hs] = a_log, 3.0
+    if a_log < 1e3:  # softplus(-197) is zero in fp32, and 1e38 of it no decay
+        for b in cu[1:]:
+            zx[b - 7:b:2, -hs:] = -200.0
+    slots, starts = list(range(n)), [3] * n
+    new = _run_state(hs, case, slots, starts, n)
+    _check_state(cu, zx, prm, h0, slots, starts, hs, out, new, n)
