@@ -1025,6 +1025,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
         for (int e = 0; e < 2; ++e) {
           rate[e] = expf(bf(p.prm[u.h0 + e])) * 1.44269504088896340736f;
           bias[e] = bf(p.prm[p.Hs + u.h0 + e]);
+          if (rate[e] != rate[e]) bias[e] = rate[e];  // the cap of the decays would hide a NaN: it goes into dt
         }
         for (int c = 0; c < u.chunks; ++c, ++g) {
           if (kMode == kMore && c == u.chunks - 1) {

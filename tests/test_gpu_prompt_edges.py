@@ -53,3 +53,25 @@ def test_state_decays_beyond_fp32(a_log, lens):
     slots, starts = list(range(n)), [3] * n
     new = _run_state(hs, case, slots, starts, n)
     _check_state(cu, zx, prm, h0, slots, starts, hs, out, new, n)
+
+
+@pytest.mark.parametrize("which", [0, 1, 2])
+@pytest.mark.parametrize("lens", [[25], [129], [1300]])
+def test_state_parameters_that_are_not_a_number(lens, which):
+    """NaN as a head's A_log, dt_bias or D: that head's outputs (and, but for
+    D, its state) are NaN, the other heads of the call are exact."""
+    hs = 4
+    case = _state_case(lens, hs, [3], seed=8, S=1)
+    cu, zx, prm, h0, out = case
+    clean = prm.clone()
+    prm[which * hs + 1] = float("nan")
+    new = _run_state(hs, case, [0], [3], 1)
+    P = h0.shape[3]
+    assert bool(torch.isnan(out[:, P:2 * P]).all())
+    if which < 2:
+        assert bool(torch.isnan(new[0, 0, 1]).all())
+    exact = torch.full_like(out, 7.0)
+    want = _run_state(hs, (cu, zx, clean, h0, exact), [0], [3], 1)
+    rest = [h for h in range(hs) if h != 1 or which == 2]
+    assert torch.equal(new[0, 0, rest], want[0, 0, rest])
+    assert torch.equal(out[:, :P], exact[:, :P]) and torch.equal(out[:, 2 * P:], exact[:, 2 * P:])
