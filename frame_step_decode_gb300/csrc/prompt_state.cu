@@ -66,6 +66,7 @@ constexpr int kRowBatch = 16;
 
 template <int R>
 __global__ void __launch_bounds__(4 * R, R == 64 ? 3 : 1) k_prompt_state_rows(const __grid_constant__ StateParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int kUnroll = R == 64 ? 1 : 2;
   constexpr int kThreads = 4 * R, kParts = kSsmP / R, kLoads = kRowBatch * 2 * kSsmN / 4 / kThreads;
   __shared__ float4 sbc[kRowBatch][2 * kSsmN / 4];  // B | C
@@ -404,6 +405,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
         float4* dst = (float4*)p.seg_state + (size_t)blockIdx.x * (128 * kSsmN / 4);
         for (int i = threadIdx.x; i < 128 * kSsmN / 4; i += kStateThreads) dst[i] = src[i];
       }
+      asm volatile("griddepcontrol.wait;" ::: "memory");  // see the end
       return;
     }
   } else {
@@ -414,6 +416,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
   uint32_t* tmem_word = (uint32_t*)(smem + L::kMisc);
   if (sb & 1023) {  // the tiles' swizzle counts on it, and there is no room to align by hand
     if (threadIdx.x == 0) *(volatile int*)p.sink.err_out = atomicOr(p.sink.err, kErrTimeout) | kErrTimeout;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
 
@@ -1115,6 +1118,7 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
   __syncthreads();
   tc_fence_after();
   if (warp == 16) tmem_dealloc(tmem, 512);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // no launch after this one begins before the rows' is complete
 }
 
 // A launch whose CTAs may begin (early) when all of the launch before have
@@ -1190,6 +1194,7 @@ extern "C" int wave_hybrid_prompt_state(wave_t* h, int layer, const void* weight
     return c;
   };
   const int n_short = upto(Hs * upto(kRowTokensFew) <= sms / 2 ? kRowTokensFew : kRowTokensMany);
+  const int n_between = n_short - upto(kRowTokensMany);  // those that are short in this call only
   int n_long = all.n - n_short;
   // Segments: the shortest that give no more CTAs than SMs, if that is worth
   // two more launches.  A chunk of the first costs about half of one of the
@@ -1204,12 +1209,12 @@ extern "C" int wave_hybrid_prompt_state(wave_t* h, int layer, const void* weight
   int t = 1;
   while (n_long * pairs <= sms && t < chunks(0) && segments(t) * pairs > sms) ++t;
   const bool cut = n_long && n_long * pairs <= sms && 3 * t + 4 < 2 * chunks(0);
-  // Short sequences go along with long ones where SMs are left for them, and
-  // where long ones take all SMs several times over: a few chunks more cost
-  // less than a launch of their own (16 prompts of 64 heads, three of them
-  // short: 97 against 103 us).
+  // What is short in this call only goes along with long ones where SMs are
+  // left for it, and where long ones take all SMs several times over: a few
+  // chunks more cost less than rows of their own.  Up to kRowTokensMany tokens
+  // are always rows: their arithmetic does not depend on who else is there.
   const int left = sms - (cut ? segments(t) : n_long) * pairs;
-  if (n_long && (n_short * pairs <= left || (n_long * pairs > sms && Hs * n_short <= sms))) n_long = all.n;
+  if (n_long && (n_between * pairs <= left || n_long * pairs > sms)) n_long += n_between;
   auto take = [&](int from, int to) {
     p.b.n = 0;
     for (int k = from; k < to; ++k) {
@@ -1222,6 +1227,20 @@ extern "C" int wave_hybrid_prompt_state(wave_t* h, int layer, const void* weight
     }
     return p.b.n;
   };
+  // The rows first: the long ones' CTAs begin beside them (they are other
+  // sessions') and end after them (16 prompts of 64 heads, two of them short:
+  // 96 us, as with those two in chunks; 56 single tokens beside one of 600: 64
+  // instead of 66; seven prompts of 32 heads that leave SMs idle: 36 instead
+  // of 32).
+  const bool rows = take(n_long, all.n);
+  if (rows) {
+    // Few heads are cut into four CTAs each while all of these run at once (64
+    // heads, 25 tokens: 6.9 against 8.0 us; 256 heads, 16 tokens: 10.3 / 8.2).
+    if (Hs * p.b.n * 4 <= sms * 2)
+      k_prompt_state_rows<16><<<dim3(Hs * 4, p.b.n), 64, 0, st>>>(p);
+    else
+      k_prompt_state_rows<64><<<dim3(Hs, p.b.n), 256, 0, st>>>(p);
+  }
   p.tiled = zx_stride % 8 == 0;
   if (take(0, n_long)) {
     if (p.tiled && encode_rows_map(&p.tm, zxbcdt, pl.in_rows, 1, cu_seqlens[n_seq], zx_stride, kQ)) return WAVE_ECUDA;
@@ -1231,28 +1250,21 @@ extern "C" int wave_hybrid_prompt_state(wave_t* h, int layer, const void* weight
     p.seg_state = h->ws.seg_state;
     p.seg_decay = h->ws.seg_decay;
     const int ctas = p.seg_cum[n_long] * pairs;
+    auto long_ones = [&](auto kernel, bool early) {
+      return launch(kernel, dim3(ctas), kStateThreads, StateSmem::kTotal, st, early, p) == cudaSuccess;
+    };
     if (cut) {
       // Where a third of the SMs is free, the CTAs of the second and third
       // launch begin beside those of the one before and wait for them (2048
       // tokens of 4 heads 28.4 -> 23.4 us; 128 CTAs 27.1 -> 28.6).
       const bool early = 3 * ctas <= 2 * sms;
-      k_prompt_state<kLocal><<<ctas, kStateThreads, StateSmem::kTotal, st>>>(p);
-      if (launch(k_segment_states, dim3(128 * kSsmN / 4 / 256, pairs, p.b.n), 256, 0, st, early, p) != cudaSuccess ||
-          launch(k_prompt_state<kOnce>, dim3(ctas), kStateThreads, StateSmem::kTotal, st, early, p) != cudaSuccess)
+      if (!long_ones(k_prompt_state<kLocal>, rows) ||
+          launch(k_segment_states, dim3(128 * kSsmN / 4 / 256, pairs, p.b.n), 256, 0, st, early, p) != cudaSuccess ||
+          !long_ones(k_prompt_state<kOnce>, early))
         return WAVE_ECUDA;
-    } else if (ctas > sms) {
-      k_prompt_state<kMore><<<ctas, kStateThreads, StateSmem::kTotal, st>>>(p);
-    } else {
-      k_prompt_state<kOnce><<<ctas, kStateThreads, StateSmem::kTotal, st>>>(p);
+    } else if (!(ctas > sms ? long_ones(k_prompt_state<kMore>, rows) : long_ones(k_prompt_state<kOnce>, rows))) {
+      return WAVE_ECUDA;
     }
-  }
-  if (take(n_long, all.n)) {
-    // Few heads are cut into four CTAs each while all of these run at once (64
-    // heads, 25 tokens: 6.9 against 8.0 us; 256 heads, 16 tokens: 10.3 / 8.2).
-    if (Hs * p.b.n * 4 <= sms * 2)
-      k_prompt_state_rows<16><<<dim3(Hs * 4, p.b.n), 64, 0, st>>>(p);
-    else
-      k_prompt_state_rows<64><<<dim3(Hs, p.b.n), 256, 0, st>>>(p);
   }
   return cudaGetLastError() == cudaSuccess ? WAVE_OK : WAVE_ECUDA;
 }

@@ -376,8 +376,9 @@ int wave_prompt_attention(wave_t* h, int n_seq, const int32_t* cu_seqlens, int n
  *             the two may not overlap otherwise).  Sessions that the call does
  *             not name, and those with an empty sequence, are not written.
  *   out       bf16 [rows][out_stride]: bf16(y silu(z)).
- * The state is carried in fp32.  Short sequences (up to 28 or 48 tokens) run the
- * recurrence token by token in fp32; longer ones run it in chunks of 128
+ * The state is carried in fp32.  Sequences of up to 28 tokens run the
+ * recurrence token by token in fp32, whoever else is in the call (and those of
+ * up to 48 where few heads are); longer ones run it in chunks of 128
  * tokens on the tensor cores, where y's two products take bf16 factors (the
  * decayed C B^T, and the state before the chunk) and the state's product takes
  * each weighted x as the sum of three bf16, to fp32's precision.  A token

@@ -75,3 +75,30 @@ def test_state_parameters_that_are_not_a_number(lens, which):
     rest = [h for h in range(hs) if h != 1 or which == 2]
     assert torch.equal(new[0, 0, rest], want[0, 0, rest])
     assert torch.equal(out[:, :P], exact[:, :P]) and torch.equal(out[:, 2 * P:], exact[:, 2 * P:])
+
+
+@pytest.mark.parametrize("hs,lens", [(4, [25, 2048]), (64, [1, 300]), (64, [28] + [500] * 12), (32, [7, 300, 20, 129, 600, 40, 260]),
+                                     (64, [1, 600] + [1] * 30), (8, [17, 3000, 5])])
+def test_state_of_a_short_sequence_whoever_else_is_in_the_call(hs, lens):
+    """Sequences of up to 28 tokens, alone and beside long ones: the same bits,
+    of outputs and of the state; in place and called again at once, each call
+    goes on from what the one before left."""
+    n = len(lens)
+    starts, slots = [3] * n, list(range(n))
+    cu, zx, prm, h0, out = _state_case(lens, hs, starts, seed=hs, S=n)
+    cfg, w = _hybrid(hs, S=n)
+    wt = _weights(cfg, prm)
+    together, alone, alone_out = h0.clone(), h0.clone(), torch.full_like(out, 7.0)
+    try:
+        for _ in range(3):
+            w.prompt_state(0, wt, cu, slots, starts, zx, together, together, out)
+        for i in range(n):
+            for _ in range(3 if lens[i] <= 28 else 0):
+                w.prompt_state(0, wt, cu[i:i + 2], [i], [3], zx, alone, alone, alone_out)
+        assert w.status() == fsd.WAVE_OK
+    finally:
+        w.close()
+    for i in range(n):
+        if lens[i] <= 28:
+            assert torch.equal(together[0, i], alone[0, i])
+            assert torch.equal(out[cu[i]:cu[i + 1]], alone_out[cu[i]:cu[i + 1]])
