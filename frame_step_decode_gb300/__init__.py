@@ -389,7 +389,8 @@ class Wave:
         `which` (0 QKV tile, 1 gate/up tile, 2 a head's attention rows, 3 O
         tile, 4 down tile, 5 norm row; hybrid: 6 selective-state
         in-projection tile, 7 a CTA's finished state items, 8 selective-state
-        out-projection tile); index < 0 disables."""
+        out-projection tile; prompts: 9 a CTA's K/V tile of the attention, 10
+        a CTA's chunk of the selective state); index < 0 disables."""
         rc = lib().wave_debug_skip_signal(self.h, which, index)
         if rc != WAVE_OK:
             raise WaveError(rc, "wave_debug_skip_signal")

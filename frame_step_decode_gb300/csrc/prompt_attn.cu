@@ -56,6 +56,7 @@ struct AttnParams {
   float* part_o;                    // [item][256 rows][D], not divided by the sums of weights
   float2* part_ml;                  // [item][256 rows]: the maximum and the sum
   ErrSink sink;
+  int skip;  // testing hook: the copies end before this tile of K and V (-1: off)
 };
 
 // What the scheduler hands to the other warps.
@@ -202,8 +203,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __gr
   auto tS = [&](int st) { return tmem + st * 128; };
   auto tO = [&](int st) { return tmem + 256 + st * D; };
 
-  // Every wait is bounded; a give-up sets the error word, which ends the
-  // other waits, and every warp leaves its loop.  wait: one thread;
+  // Every wait is bounded; a give-up sets the error word and ends the role's
+  // loop, which lets the waits of the others run out too.  wait: one thread;
   // wait_warp: a whole warp, which stays together.
   bool ok = true;
   auto wait = [&](int b, uint32_t parity) { return ok = wait_bar(bar(b), parity, p.sink); };
@@ -385,6 +386,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __gr
           query(0);
           for (int j = 0; j < 2 * nb && ok; ++j, ++it_r) {  // K_0, V_0, K_1, V_1, ...
             const int slot = it_r % L::kStages;
+            if (it_r == (uint32_t)p.skip) {
+              ok = false;
+              break;
+            }
             if (!wait(L::kEmpty + slot, ((it_r / L::kStages) & 1) ^ 1)) break;
             mbar_arrive_expect_tx(bar(L::kFull + slot), L::kTile);
             tile(j & 1 ? &p.tm_v : &p.tm_k, sb + L::kRing + slot * L::kTile, kvh, kv0 + (j >> 1) * kRows,
@@ -789,6 +794,7 @@ extern "C" int wave_prompt_attention(wave_t* h, int n_seq, const int32_t* cu_seq
   p.wide = ((uintptr_t)out & 31) == 0 && out_stride % 16 == 0;
   p.scale2 = scale * 1.44269504088896340736f;
   p.sink = make_sink(h->ws.err, h->err_host_dev, h->timeout_ns);
+  p.skip = h->skip_sig_kind == 9 ? h->skip_sig : -1;
   cudaStream_t st = (cudaStream_t)stream;
   h->last_stream = st;
   cudaError_t e;

@@ -203,9 +203,12 @@ struct ErrSink {
   int* err_out;
   int tries;
 };
-constexpr uint32_t kTryNs = 1000;  // how long one try may sleep
+// How long a try that fails takes: 7920 cycles, whatever time it is given
+// (mbarrier.try_wait's own limit; measured with 1 ns to 1 ms).
+constexpr uint32_t kTryNs = 4000;
 inline ErrSink make_sink(int* err, int* err_out, long long timeout_ns) {
-  const long long n = timeout_ns / kTryNs;  // a limit below one try leaves no wait any time
+  // a limit below a microsecond leaves no wait any time; from there on one try at least
+  const long long n = timeout_ns < 1000 ? 0 : (timeout_ns - 1) / kTryNs + 1;
   return {err, err_out, n > 0x7fffffff ? 0x7fffffff : (int)n};
 }
 // Wait for the phase with the given parity; false, and the timeout noted,

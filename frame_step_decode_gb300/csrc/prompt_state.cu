@@ -49,6 +49,7 @@ struct StateParams {
   float* seg_state;                    // [segment and head pair][128 rows (head, p)][128]
   float* seg_decay;                    // ... [2]: the decays of the segment, in powers of two
   ErrSink sink;
+  int skip;  // testing hook: the copies end before this chunk of a CTA (-1: off)
 };
 
 __device__ __forceinline__ float bf(uint16_t v) { return __uint_as_float((uint32_t)v << 16); }
@@ -958,6 +959,10 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
       for (uint32_t n = 0; ok && (n == 0 || next_unit(u, n)); ++n) {
         for (int c = 0; c < u.chunks; ++c, ++g) {
           const int r = u.first + c * kQ, rows = min(kQ, u.len - c * kQ);
+          if (g == (uint32_t)p.skip) {
+            ok = false;
+            break;
+          }
           if (warp == 17) {
             wait_warp(L::kXEmpty + (g & 1), ((g >> 1) & 1) ^ 1);
             if (!ok) break;
@@ -1182,6 +1187,7 @@ extern "C" int wave_hybrid_prompt_state(wave_t* h, int layer, const void* weight
   cudaStream_t st = (cudaStream_t)stream;
   h->last_stream = st;
   p.sink = make_sink(h->ws.err, h->err_host_dev, h->timeout_ns);
+  p.skip = h->skip_sig_kind == 10 ? h->skip_sig : -1;
   // short sequences go token by token, the others in chunks, longest first
   SeqBatch all = p.b;
   int order[WAVE_MAX_SEQS];

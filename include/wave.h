@@ -432,7 +432,8 @@ int wave_step_static(const wave_config* cfg, int S_max, int T_max, int S, const 
 
 /* ---- testing hooks (fault tests without a GPU fault) ---------------------
  * Limit for every device-side wait of later steps, in nanoseconds (default
- * 2e9).  A wait that runs out sets WAVE_ETIMEOUT and the kernel returns. */
+ * 2e9; the calls on prompts count it in tries of 4 us, and below 1 us a wait
+ * gets none).  A wait that runs out sets WAVE_ETIMEOUT and the kernel returns. */
 int wave_set_timeout_ns(wave_t* h, long long ns);
 /* Make CTA `cta` skip its arrival at grid barrier number `barrier` (0-based)
  * in later steps, so that the others' waits run out; cta < 0 disables. */
@@ -447,7 +448,11 @@ int wave_debug_skip_barrier(wave_t* h, int cta, int barrier);
  * in the hybrid step also 6 the selective-state in-projection tile `index`
  * (the state items wait), 7 the finished state items of CTA `index` (the
  * out-projection waits), 8 the selective-state out-projection tile `index`
- * (the next RMSNorm waits).  index < 0 disables. */
+ * (the next RMSNorm waits).  In the calls on prompts: 9, every CTA of the
+ * attention ends its copies before tile `index` of K and V (0 K, 1 V of its
+ * first block, and so on); 10, every CTA of the chunked selective state ends
+ * its copies before its chunk `index` (the products, and all that is made of
+ * them, wait).  index < 0 disables. */
 int wave_debug_skip_signal(wave_t* h, int which, int index);
 /* Make later steps also write, for every session with a valid position, the
  * fp32 K (after RoPE) and V rows they quantise into dst, a device buffer of

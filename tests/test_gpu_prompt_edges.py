@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import frame_step_decode_gb300 as fsd
-from test_gpu_prompt import _check_state, _hybrid, _state_case, _weights
+from test_gpu_prompt import _attention, _check_attention, _check_state, _hybrid, _state_case, _wave, _weights
 
 pytestmark = pytest.mark.gpu
 
@@ -102,3 +102,39 @@ def test_state_of_a_short_sequence_whoever_else_is_in_the_call(hs, lens):
         if lens[i] <= 28:
             assert torch.equal(together[0, i], alone[0, i])
             assert torch.equal(out[cu[i]:cu[i + 1]], alone_out[cu[i]:cu[i + 1]])
+
+
+def _timed(run):
+    a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    a.record()
+    run()
+    b.record()
+    torch.cuda.synchronize()
+    return a.elapsed_time(b)
+
+
+@pytest.mark.parametrize("ms", [2, 20])
+def test_limits_take_the_time_they_say(ms):
+    """A wait that nothing ends, in the attention and in the chunked state:
+    near its limit (a try is 7920 cycles, counted as 4 us; 2.07 GHz at most)."""
+    cu, q, k, v, out = _attention([300, 1, 700], 2, 2, 128, torch.bfloat16, seed=1)
+    cs, zx, prm, h0, so = _state_case([300], 8, [0], seed=1)
+    cfg, w = _hybrid(8, S=1, heads=2, dim=128)
+    wt = _weights(cfg, prm)
+    new = torch.zeros_like(h0)
+    calls = [(9, lambda: w.prompt_attention(cu, q, k, v, out)), (10, lambda: w.prompt_state(0, wt, cs, [0], [0], zx, h0, new, so))]
+    try:
+        for which, run in calls:
+            run()
+            w.set_timeout_ns(ms * 1_000_000)
+            w.debug_skip_signal(which, 0)
+            took = _timed(run)
+            assert w.status() == fsd.WAVE_ETIMEOUT
+            assert 0.5 * ms < took < 2.5 * ms, took
+            w.debug_skip_signal(which, -1)
+            run()
+            assert w.status() == fsd.WAVE_OK
+    finally:
+        w.close()
+    _check_attention(cu, q, k, v, out)
+    _check_state(cs, zx, prm, h0, [0], [0], 8, so, new, 1)
