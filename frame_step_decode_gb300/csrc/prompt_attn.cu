@@ -196,6 +196,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __gr
     prefetch_tmap(&p.tm_k);
     prefetch_tmap(&p.tm_v);
   }
+  const bool stop = warp == 11 && stopped(p.sink);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -204,7 +205,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __gr
   auto tO = [&](int st) { return tmem + 256 + st * D; };
 
   // Every wait is bounded; a give-up sets the error word and ends the role's
-  // loop, which lets the waits of the others run out too.  wait: one thread;
+  // loop, which lets the waits of the others run out too; CTAs that begin later
+  // find no work.  wait: one thread;
   // wait_warp: a whole warp, which stays together.
   bool ok = true;
   auto wait = [&](int b, uint32_t parity) { return ok = wait_bar(bar(b), parity, p.sink); };
@@ -510,6 +512,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __gr
               }
               if (st == 0 && more) {
                 vnext = next_tile();
+                if (!ok) break;
                 if (diag && j + 1 >= n0 - 1 && lane == 0) mbar_arrive(bar(L::kGo));
               }
             }
@@ -590,7 +593,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) k_prompt_attention(const __gr
       for (uint32_t k = 0; ok; ++k) {
         if (!wait_warp(L::kItemEmpty + (k & 1), ((k >> 1) & 1) ^ 1)) break;
         int idx = blockIdx.x;
-        bool valid = true;
+        bool valid = !stop;
         if (k > 0) valid = !kCut && p.more;
         if (k > 0 && valid) {
           if (lane == 0) {

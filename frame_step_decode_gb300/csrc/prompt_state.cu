@@ -420,6 +420,10 @@ __global__ void __launch_bounds__(kStateThreads, 1) k_prompt_state(const __grid_
     asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
+  if (__syncthreads_or(threadIdx.x == 0 && stopped(p.sink))) {  // a CTA that begins now would run into the same limit
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
 
   if (warp == 16) {
     if (lane == 0) {

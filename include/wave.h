@@ -261,7 +261,9 @@ int wave_hybrid_step(wave_t* h, int S, const void* weights, uint8_t* kv_fp8, flo
  * about (stream or event synchronisation); before that it reports only the
  * launches already finished.  The bits are sticky across launches until
  * read: a non-OK result clears them (host word now, device word by an
- * asynchronous memset enqueued on the handle's last stream).  Returns
+ * asynchronous memset enqueued on the handle's last stream).  Until a timeout
+ * is read, later launches of the handle give up as well, their outputs
+ * undefined.  Returns
  * WAVE_OK, WAVE_ETIMEOUT (a device wait gave up; that step's outputs are
  * undefined, the GPU context stays usable) or WAVE_EPOS; WAVE_ECUDA if the
  * clearing memset could not be enqueued.  This is the step's own failure

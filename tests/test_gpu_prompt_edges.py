@@ -138,3 +138,80 @@ def test_limits_take_the_time_they_say(ms):
         w.close()
     _check_attention(cu, q, k, v, out)
     _check_state(cs, zx, prm, h0, [0], [0], 8, so, new, 1)
+
+
+LIMIT_MS = 20  # of a wait
+
+
+@pytest.mark.parametrize("lens,H,Hkv", [([300] * 96, 8, 2), ([300, 1, 700], 2, 2), ([4100, 300], 4, 1)])  # more items than SMs, fewer, divided keys
+@pytest.mark.parametrize("tile", [0, 1, 3])
+def test_attention_that_is_stuck_ends_after_one_limit(lens, H, Hkv, tile):
+    """Copies that end before a tile: every role's wait runs out, CTAs that
+    begin afterwards leave at once, and the handle goes on."""
+    cu, q, k, v, out = _attention(lens, H, Hkv, 128, torch.bfloat16, seed=tile)
+    w = _wave(H, 128)
+    try:
+        w.set_timeout_ns(LIMIT_MS * 1_000_000)
+        w.debug_skip_signal(9, tile)
+        ms = _timed(lambda: w.prompt_attention(cu, q, k, v, out))
+        assert w.status() == fsd.WAVE_ETIMEOUT
+        assert 0.5 * LIMIT_MS < ms < 2.5 * LIMIT_MS, ms
+        w.debug_skip_signal(9, -1)
+        w.prompt_attention(cu, q, k, v, out)
+        assert w.status() == fsd.WAVE_OK
+    finally:
+        w.close()
+    _check_attention(cu, q, k, v, out)
+
+
+@pytest.mark.parametrize("hs,lens,pad", [(64, [200] * 40, 0), (64, [500] * 6, 0), (8, [600, 129], 0), (8, [2600, 700], 0), (4, [600, 129], 0),
+                                         (4, [600, 20], 4)])
+@pytest.mark.parametrize("chunk", [0, 1])
+def test_state_that_is_stuck_ends_after_one_limit(hs, lens, pad, chunk):
+    """The same of the chunked state, with and without a tensor map, in more
+    units than SMs, fewer, and segments (of one chunk: there is no second)."""
+    n = len(lens)
+    starts, slots = [i % 2 for i in range(n)], list(range(n))
+    cu, zx, prm, h0, out = _state_case(lens, hs, starts, seed=chunk, S=n, pad=pad)
+    cfg, w = _hybrid(hs, S=n)
+    wt = _weights(cfg, prm)
+    new = torch.full_like(h0, 9.0)
+    run = lambda: w.prompt_state(0, wt, cu, slots, starts, zx, h0, new, out)  # noqa: E731
+    try:
+        run()
+        w.set_timeout_ns(LIMIT_MS * 1_000_000)
+        w.debug_skip_signal(10, chunk)
+        ms = _timed(run)
+        if chunk == 0 or hs == 64:
+            assert w.status() == fsd.WAVE_ETIMEOUT
+            assert 0.5 * LIMIT_MS < ms < 2.5 * LIMIT_MS, ms
+        else:
+            assert w.status() in (fsd.WAVE_ETIMEOUT, fsd.WAVE_OK) and ms < 2.5 * LIMIT_MS
+        w.debug_skip_signal(10, -1)
+        run()
+        assert w.status() == fsd.WAVE_OK
+    finally:
+        w.close()
+    _check_state(cu, zx, prm, h0, slots, starts, hs, out, new, n)
+
+
+@pytest.mark.parametrize("ns", [4_000, 12_000])
+def test_attention_gives_up_in_the_middle_of_an_item(ns):
+    """A limit of a few tries, with items of 64 blocks: what waits for an item's
+    end runs out while copies and products are under way.  Launches behind it
+    give up too until the status has been read, and the next one is right."""
+    cu, q, k, v, out = _attention([8192], 8, 1, 128, torch.bfloat16, seed=4)
+    w = _wave(8, 128)
+    try:
+        w.set_timeout_ns(ns)
+        w.prompt_attention(cu, q, k, v, out)
+        w.set_timeout_ns(2_000_000_000)
+        out.fill_(7)
+        w.prompt_attention(cu, q, k, v, out)
+        assert w.status() == fsd.WAVE_ETIMEOUT
+        assert bool((out == 7).all()), "a launch behind one that gave up finds no work"
+        w.prompt_attention(cu, q, k, v, out)
+        assert w.status() == fsd.WAVE_OK
+    finally:
+        w.close()
+    _check_attention(cu, q, k, v, out)
