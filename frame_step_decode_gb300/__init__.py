@@ -209,6 +209,29 @@ def _is_rows(t, rows: int, H: int, D: int) -> bool:
     return len(shape) == 3 and shape[2] == D and shape[1] == H and shape[0] >= rows
 
 
+_DTYPES: dict = {}  # float32 and int32 by name
+
+
+def _held(t, kind, count: int, device: int, what: str) -> None:
+    """Refuse a buffer of the handle's layout (history, state, positions,
+    weights) that a call would read or write beyond its end, as another type
+    (kind: a name in _DTYPES, or the bytes of a value) or on another device.
+    An address (int) or None is the caller's."""
+    if t is None or isinstance(t, int):
+        return
+    fits = t.element_size() == kind if isinstance(kind, int) else t.dtype is _DTYPES[kind]
+    if not fits or t.numel() < count or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{what}: {count} contiguous values ({kind if isinstance(kind, str) else f'{kind} bytes each'}) on device {device} "
+                         f"are wanted, not {t.numel()} of {t.dtype} on device {t.get_device()}")
+
+
+def _here(device: int, what: str, *tensors) -> None:
+    """Refuse tensors that are not on the handle's device."""
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"{what}: a tensor on device {t.get_device()}, the handle's is {device}")
+
+
 _CURRENT: list = []  # torch's current device, and the current stream's handle on it
 
 
@@ -274,6 +297,21 @@ class Wave:
         if rc != WAVE_OK:
             raise WaveError(rc, "wave_create")
         self.h = h
+        self._sizes()
+
+    def _sizes(self) -> None:
+        """What the calls on prompts and sessions compare buffers with: the
+        handle's device, and how many values history, scales, state and packed
+        weights have."""
+        import torch
+        _DTYPES.update(float32=torch.float32, int32=torch.int32)
+        c, hybrid = self.cfg, isinstance(self.cfg, WaveHybridConfig)
+        layers = c.n_layers // c.attn_every if hybrid else c.n_layers
+        self._n_scales = layers * 2 * self.S_max * c.n_heads * self.T_max
+        self._n_codes = self._n_scales * c.head_dim
+        self._n_state = (c.n_layers - layers) * self.S_max * c.ssm_heads * c.ssm_head_dim * c.ssm_state if hybrid else 0
+        self._n_weights = hybrid_packed_weights_bytes(c) // 2 if hybrid else 0
+        self.device = torch.cuda.current_device() if torch.cuda.is_available() else -1
 
     def step(self, S, weights, kv, kv_scales, positions, x, y, stream=None, check=True) -> int:
         rc = lib().wave_step(self.h, S, _ptr(weights), _ptr(kv), _ptr(kv_scales), _ptr(positions),
@@ -325,6 +363,10 @@ class Wave:
         shape = qkv.shape
         if len(shape) != 2 or shape[1] != 3 * H * D or shape[0] < rows:
             raise ValueError("wave_prompt_append: qkv is [rows][3*H*D], with the rows that cu_seqlens names")
+        if self.h:
+            _here(self.device, "wave_prompt_append", qkv, q, k, v)
+            _held(kv, 1, self._n_codes, self.device, "wave_prompt_append: kv")
+            _held(kv_scales, "float32", self._n_scales, self.device, "wave_prompt_append: kv_scales")
         rc = lib().wave_prompt_append(self.h, layer, n_sl, cu, sl, s0, _ptr(qkv), _type_of(qkv), _rows(qkv, "qkv"),
                                       _ptr(kv), _ptr(kv_scales), _ptr(q), _ptr(k), _ptr(v),
                                       WAVE_BF16 if out_type < 0 else out_type, _stream(stream))
@@ -346,6 +388,8 @@ class Wave:
                 or not _is_rows(out, rows, H, D) or not _is_rows(k, rows, Hkv, D) or not _is_rows(v, rows, Hkv, D):
             raise ValueError(f"{what}: q, out [rows][n_heads][D] and k, v [rows][n_kv_heads][D] of one type, with the rows "
                              "that cu_seqlens names")
+        if self.h:
+            _here(self.device, what, q, k, v, out)
         rc = lib().wave_prompt_attention(self.h, n_cu - 1, cu, Hkv, _type_of(q), _ptr(q), _rows(q, what), _ptr(k),
                                          _rows(k, what), _ptr(v), _rows(v, what), D ** -0.5 if scale is None else scale,
                                          _ptr(out), _rows(out, what), _stream(stream))
@@ -361,6 +405,11 @@ class Wave:
         (s, n), (d, n_d) = _ints(src), _ints(dst)
         if n != n_d:
             raise ValueError("wave_sessions_copy: one destination for each source")
+        if self.h:
+            _held(kv, 1, self._n_codes, self.device, "wave_sessions_copy: kv")
+            _held(kv_scales, "float32", self._n_scales, self.device, "wave_sessions_copy: kv_scales")
+            _held(state, "float32", self._n_state, self.device, "wave_sessions_copy: state")
+            _held(positions, "int32", self.S_max, self.device, "wave_sessions_copy: positions")
         rc = lib().wave_sessions_copy(self.h, n, s, d, int(bool(move)), _ptr(kv), _ptr(kv_scales), _ptr(state),
                                       _ptr(positions), _stream(stream))
         if check and rc != WAVE_OK:
@@ -485,6 +534,7 @@ class HybridWave(Wave):
         if rc != WAVE_OK:
             raise WaveError(rc, "wave_hybrid_create")
         self.h = h
+        self._sizes()
 
     def hybrid_step(self, S, weights, kv, kv_scales, ssm_state, positions, x, y, stream=None,
                     check=True) -> int:
@@ -511,6 +561,11 @@ class HybridWave(Wave):
             raise ValueError("wave_hybrid_prompt_state: zxbcdt is bf16 [rows][in_rows], out bf16 [rows][d_inner]")
         if min(zs[0], ys[0]) < int(cu_seqlens[n_sl]):
             raise ValueError("wave_hybrid_prompt_state: cu_seqlens names more rows than a buffer has")
+        if self.h:
+            _here(self.device, "wave_hybrid_prompt_state", zxbcdt, out)
+            _held(weights, 2, self._n_weights, self.device, "wave_hybrid_prompt_state: weights")
+            _held(state_in, "float32", self._n_state, self.device, "wave_hybrid_prompt_state: state_in")
+            _held(state_out, "float32", self._n_state, self.device, "wave_hybrid_prompt_state: state_out")
         rc = lib().wave_hybrid_prompt_state(self.h, layer, _ptr(weights), n_sl, cu, sl, s0, _ptr(zxbcdt),
                                             _rows(zxbcdt, "zxbcdt"), _ptr(state_in), _ptr(state_out), _ptr(out),
                                             _rows(out, "out"), _stream(stream))

@@ -76,3 +76,77 @@ def test_integers_beyond_32_bits_are_refused():
             c()
     for values in (torch.tensor([3, -1]), np.array([3, -1]), (3, -1)):
         assert fsd._ints(values) == (np.array([3, -1], dtype=np.int32).tobytes(), 2)
+
+
+class _Accepts:
+    """A library whose calls all succeed: what reaches it has passed the binding's checks."""
+
+    def __init__(self):
+        self.calls = 0
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls += 1
+            return 0
+        return call
+
+
+def _bound(w, S_max, T_max, monkeypatch):
+    """w as if it had a handle, for buffers on the CPU (device -1), and its calls counted."""
+    fake = _Accepts()
+    w.S_max, w.T_max = S_max, T_max
+    w._sizes()  # of the packed weights by the library itself
+    w.device = -1
+    monkeypatch.setattr(fsd, "lib", lambda: fake)
+    monkeypatch.setattr(type(w), "close", lambda self: None)
+    w.h = 1
+    return w, fake
+
+
+def test_buffers_of_another_size_or_type_are_refused(monkeypatch):
+    """History, scales, state, weights and positions are read and written by
+    slot: too few values, another type, gaps or another device would be out of
+    range or the wrong bytes on the device."""
+    S, T = 4, 64
+    w, fake = _bound(_decoder(), S, T, monkeypatch)
+    kv, sc = _b(1, 2, S, 2, T, 64, dtype=torch.uint8), _b(1, 2, S, 2, T, dtype=torch.float32)
+    pos = _b(S, dtype=torch.int32)
+    qkv, q = _b(3, 384), _b(3, 2, 64)
+    append = lambda kv=kv, sc=sc, **kw: w.prompt_append(0, [0, 3], [0], [0], qkv, kv, sc, stream=0, **kw)  # noqa: E731
+    copy = lambda kv=kv, sc=sc, pos=pos, **kw: w.sessions_copy([0], [1], kv, sc, pos, stream=0, **kw)  # noqa: E731
+    attend = lambda: w.prompt_attention([0, 3], q, q, q, q, stream=0)  # noqa: E731
+    append(), append(q=q), copy(), attend()
+    append(kv=kv.view(torch.float8_e4m3fn), sc=4096)  # codes of any one-byte type; an address is the caller's
+    assert fake.calls == 5
+    bad = [lambda f=f, kw=kw: f(**kw) for f in (append, copy) for kw in
+           (dict(kv=kv.flatten()[:-1]), dict(kv=kv.to(torch.float16)), dict(kv=kv.transpose(3, 4)), dict(sc=sc.flatten()[:-1]),
+            dict(sc=sc.to(torch.bfloat16)), dict(sc=sc.double()), dict(sc=sc.transpose(3, 4)))]
+    bad += [lambda: copy(pos=pos.long()), lambda: copy(pos=pos[:3]), lambda: copy(pos=_b(8, dtype=torch.int32)[::2]),
+            lambda: copy(pos=pos.float())]
+    for c in bad:
+        with pytest.raises(ValueError):
+            c()
+    w.device = 0  # the tensors are elsewhere
+    for c in (append, copy, attend, lambda: append(kv=4096, sc=4096)):
+        with pytest.raises(ValueError):
+            c()
+    assert fake.calls == 5
+
+
+
+def test_state_buffers_of_another_size_or_type_are_refused(monkeypatch):
+    S, T = 4, 64
+    n = fsd.hybrid_packed_weights_bytes(_hybrid().cfg)
+    h, fake = _bound(_hybrid(), S, T, monkeypatch)
+    pos = _b(S, dtype=torch.int32)
+    wt, st, zx, out = _b(n // 2), _b(1, S, 4, 64, 128, dtype=torch.float32), _b(3, 772), _b(3, 256)
+    state = lambda wt=wt, si=st, so=st: h.prompt_state(0, wt, [0, 3], [0], [2], zx, si, so, out, stream=0)  # noqa: E731
+    state(), state(si=None)
+    for kw in (dict(wt=wt[:-1]), dict(wt=wt.float()), dict(si=st.half()), dict(si=st[:, :3]), dict(so=st.to(torch.bfloat16)),
+               dict(so=st.flatten()[:-4]), dict(so=st.transpose(3, 4)), dict(so=st.double())):
+        with pytest.raises(ValueError):
+            state(**kw)
+    for kw in (dict(state=st.half()), dict(state=st.flatten()[1:])):
+        with pytest.raises(ValueError):
+            h.sessions_copy([0], [1], _b(1, 2, S, 1, T, 64, dtype=torch.uint8), _b(1, 2, S, 1, T, dtype=torch.float32), pos, stream=0, **kw)
+    assert fake.calls == 2
