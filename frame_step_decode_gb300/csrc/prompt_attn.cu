@@ -753,7 +753,8 @@ extern "C" int wave_prompt_attention(wave_t* h, int n_seq, const int32_t* cu_seq
   if (!h || !q || !k || !v || !out || !cu_ok(n_seq, cu_seqlens)) return WAVE_EINVAL;
   const int H = h->pl.cfg.n_heads, D = h->pl.cfg.head_dim;
   if (n_kv_heads < 1 || H % n_kv_heads || (type != WAVE_BF16 && type != WAVE_F16)) return WAVE_EINVAL;
-  if (!(scale > 0.f) || !isfinite(scale)) return WAVE_EINVAL;
+  const float scale2 = scale * 1.44269504088896340736f;  // log2(e)
+  if (!(scale > 0.f) || !isfinite(scale2)) return WAVE_EINVAL;
   const int64_t least[4] = {(int64_t)H * D, (int64_t)n_kv_heads * D, (int64_t)n_kv_heads * D, (int64_t)H * D};
   const int64_t strides[4] = {q_stride, k_stride, v_stride, out_stride};
   const void* ptrs[4] = {q, k, v, out};
@@ -795,7 +796,7 @@ extern "C" int wave_prompt_attention(wave_t* h, int n_seq, const int32_t* cu_seq
   p.v_stride = v_stride;
   p.out_stride = out_stride;
   p.wide = ((uintptr_t)out & 31) == 0 && out_stride % 16 == 0;
-  p.scale2 = scale * 1.44269504088896340736f;
+  p.scale2 = scale2;
   p.sink = make_sink(h->ws.err, h->err_host_dev, h->timeout_ns);
   p.skip = h->skip_sig_kind == 9 ? h->skip_sig : -1;
   cudaStream_t st = (cudaStream_t)stream;

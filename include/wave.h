@@ -347,7 +347,7 @@ int wave_prompt_append(wave_t* h, int layer, int n_seq, const int32_t* cu_seqlen
  * n_kv_heads (a divisor of n_heads; head h reads K/V head h / (n_heads /
  * n_kv_heads)); heads are contiguous in a row and rows are *_stride elements
  * apart, so slices of a wider row can be passed.  type is WAVE_BF16 or
- * WAVE_F16, of all four; scale is finite and > 0 (1/sqrt(D) in the step).
+ * WAVE_F16, of all four; scale is > 0 and at most 2.3e38 (1/sqrt(D) in the step).
  * Scores, the softmax's maximum and sum and the output are kept in fp32, the
  * weights p are rounded to `type` for the second product.  Values at tokens
  * that a row does not attend to never reach it, whatever they are (NaN and

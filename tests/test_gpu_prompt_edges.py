@@ -215,3 +215,22 @@ def test_attention_gives_up_in_the_middle_of_an_item(ns):
     finally:
         w.close()
     _check_attention(cu, q, k, v, out)
+
+
+def test_attention_scales_at_the_ends_of_fp32():
+    """Scores of zero are zero at every scale that is taken; one whose
+    logarithm to base 2 leaves fp32 is refused."""
+    cu, q, k, v, out = _attention([300], 2, 1, 64, torch.bfloat16, seed=1)
+    q.zero_()
+    w = _wave(2, 64)
+    try:
+        for scale in (2.3e38, 1e-45):
+            out.fill_(7)
+            w.prompt_attention(cu, q, k, v, out, scale=scale)
+            assert w.status() == fsd.WAVE_OK
+            _check_attention(cu, q, k, v, out, scale=scale)
+        out.fill_(7)
+        assert w.prompt_attention(cu, q, k, v, out, scale=3e38, check=False) == fsd.WAVE_EINVAL
+        assert w.status() == fsd.WAVE_OK and bool((out == 7).all())
+    finally:
+        w.close()
