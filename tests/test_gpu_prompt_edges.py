@@ -234,3 +234,59 @@ def test_attention_scales_at_the_ends_of_fp32():
         assert w.status() == fsd.WAVE_OK and bool((out == 7).all())
     finally:
         w.close()
+
+
+@pytest.mark.parametrize("name", ["TINY", "MID"])
+def test_append_of_a_steps_own_qkv_equals_its_append(name):
+    """The q, k and v that a step dumps before the rotation (fp32), appended as
+    prompts of one token at the sessions' positions: the codes and scales that
+    the step wrote, bit for bit, of K and of V."""
+    import synth
+    from gpu_case import DeviceCase, dump_acts
+    work = getattr(synth, name)
+    case = DeviceCase(work)
+    L, H, D, S, d = work.n_layers, work.n_heads, work.head_dim, case.S, work.d_model
+    w = fsd.Wave(case.cfg, case.S_max, work.T_max)
+    kv, sc = torch.zeros_like(case.kv), torch.zeros_like(case.sc)
+    pos = case.pos_h.tolist()
+    try:
+        acts = torch.from_numpy(dump_acts(w, S, 1, lambda: case.step(w)))[0].cuda()  # [layers][S][record]
+        for l in range(L):
+            w.prompt_append(l, list(range(S + 1)), list(range(S)), pos, acts[l, :, 2 * d:2 * d + 3 * H * D].contiguous(), kv, sc)
+        assert w.status() == fsd.WAVE_OK
+    finally:
+        w.close()
+    for s, p in enumerate(pos):
+        assert torch.equal(kv[:, :, s, :, p], case.kv[:, :, s, :, p])
+        assert torch.equal(sc[:, :, s, :, p], case.sc[:, :, s, :, p])
+
+
+@pytest.mark.parametrize("lens,H,Hkv,D", [([3000], 2, 1, 128), ([900, 40], 4, 4, 64)])
+def test_attention_alone_and_in_a_batch(lens, H, Hkv, D):
+    """Prompts whose keys are divided when they come alone and are not in a
+    larger batch: both within the bound of the definition."""
+    more = lens + [700] * 60
+    cu, q, k, v, out = _attention(more, H, Hkv, D, torch.bfloat16, seed=5)
+    n = sum(lens)
+    mine = cu[:len(lens) + 1]
+    alone = torch.full_like(out, 7.0)
+    w = _wave(H, D)
+    try:
+        w.prompt_attention(cu, q, k, v, out)
+        w.prompt_attention(mine, q, k, v, alone)
+        assert w.status() == fsd.WAVE_OK
+    finally:
+        w.close()
+    assert bool((alone[n:] == 7).all())
+    for got in (out, alone):
+        _check_attention(mine, q[:n], k[:n], v[:n], got[:n])
+
+
+@pytest.mark.parametrize("hs,lens", [(128, [1, 40, 130]), (100, [300, 28]), (768, [2, 129])])
+def test_state_of_many_heads(hs, lens):
+    n = len(lens)
+    starts, slots = [i % 2 for i in range(n)], list(range(n))
+    case = _state_case(lens, hs, starts, seed=hs, S=n)
+    cu, zx, prm, h0, out = case
+    new = _run_state(hs, case, slots, starts, n)
+    _check_state(cu, zx, prm, h0, slots, starts, hs, out, new, n)
