@@ -239,7 +239,8 @@ def _stream(stream) -> int:
     if stream is None:  # without a Stream object around the handle (4 of a call's 12 us)
         if not _CURRENT:
             import torch
-            _CURRENT.extend((torch.cuda.current_device, torch._C._cuda_getCurrentRawStream))
+            raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # not a public name
+            _CURRENT.extend((torch.cuda.current_device, raw or (lambda device: torch.cuda.current_stream(device).cuda_stream)))
         return _CURRENT[1](_CURRENT[0]())
     if isinstance(stream, int):
         return stream

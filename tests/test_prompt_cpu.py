@@ -150,3 +150,20 @@ def test_state_buffers_of_another_size_or_type_are_refused(monkeypatch):
         with pytest.raises(ValueError):
             h.sessions_copy([0], [1], _b(1, 2, S, 1, T, 64, dtype=torch.uint8), _b(1, 2, S, 1, T, dtype=torch.float32), pos, stream=0, **kw)
     assert fake.calls == 2
+
+
+@pytest.mark.parametrize("raw", [True, False])
+def test_the_current_stream_with_and_without_the_raw_getter(monkeypatch, raw):
+    """The handle of torch's current stream, also where torch does not export
+    the function that gives it without a Stream object."""
+    class Stream:
+        cuda_stream = 77
+    monkeypatch.setattr(fsd, "_CURRENT", [])
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device: Stream if device == 3 else None)
+    if raw:
+        monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda device: 77 if device == 3 else 0, raising=False)
+    else:
+        monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    assert fsd._stream(None) == 77 and fsd._stream(None) == 77
+    assert fsd._stream(5) == 5 and fsd._stream(Stream) == 77
