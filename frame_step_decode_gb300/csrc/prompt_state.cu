@@ -1237,6 +1237,8 @@ extern "C" int wave_hybrid_prompt_state(wave_t* h, int layer, const void* weight
     }
     return p.b.n;
   };
+  p.tiled = zx_stride % 8 == 0;
+  if (n_long && p.tiled && encode_rows_map(&p.tm, zxbcdt, pl.in_rows, 1, cu_seqlens[n_seq], zx_stride, kQ)) return WAVE_ECUDA;
   // The rows first: the long ones' CTAs begin beside them (they are other
   // sessions') and end after them (16 prompts of 64 heads, two of them short:
   // 96 us, as with those two in chunks; 56 single tokens beside one of 600: 64
@@ -1251,9 +1253,7 @@ extern "C" int wave_hybrid_prompt_state(wave_t* h, int layer, const void* weight
     else
       k_prompt_state_rows<64><<<dim3(Hs, p.b.n), 256, 0, st>>>(p);
   }
-  p.tiled = zx_stride % 8 == 0;
   if (take(0, n_long)) {
-    if (p.tiled && encode_rows_map(&p.tm, zxbcdt, pl.in_rows, 1, cu_seqlens[n_seq], zx_stride, kQ)) return WAVE_ECUDA;
     p.seg_chunks = cut ? t : 0;
     p.seg_cum[0] = 0;
     for (int k = 0; k < n_long; ++k) p.seg_cum[k + 1] = p.seg_cum[k] + (cut ? (chunks(k) + t - 1) / t : 1);
