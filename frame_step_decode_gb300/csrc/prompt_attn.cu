@@ -5,11 +5,12 @@
 //
 // Bound by the tensor cores for long prompts (4 D flops for a query and a key
 // it attends to; the blocks on the diagonal are done whole), by HBM for short
-// ones with many heads, by latency for a single short one.  Measured (32 heads
-// of 128): a prompt of 8192 tokens 370 to 400 us with the power limit active,
-// 1.38 to 1.49 PFLOP/s of causal work; prompts of 4096, 1 and 2001 tokens, 8
-// K/V heads, fp16, 129 us = 1.32 PFLOP/s; 16 prompts of 1 to 1500 tokens, 8005
-// in all, 74 us; a prompt of 25 tokens of 16 heads of 64, 6 us.
+// ones with many heads, by latency for a single short one.  Measured (captured
+// launches in a row; 32 heads of 128): a prompt of 8192 tokens 370 to 405 us
+// with the power limit active, 1.36 to 1.49 PFLOP/s of causal work; prompts of
+// 4096, 1 and 2001 tokens, 8 K/V heads, fp16, 129 us = 1.32 PFLOP/s; 16 prompts
+// of 1 to 1500 tokens, 8005 in all, 73 to 75 us; 8192 tokens of 16 heads of 64,
+// 162 us = 0.85 PFLOP/s; a prompt of 25 tokens of 16 heads of 64, 6 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

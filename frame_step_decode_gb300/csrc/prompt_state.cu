@@ -180,10 +180,11 @@ __global__ void __launch_bounds__(4 * R, R == 64 ? 3 : 1) k_prompt_state_rows(co
 // two heads of a CTA: B and C are shared by all heads), C H^T, M X with M read
 // from TMEM, and the state with (w X)^T read from TMEM and its accumulator,
 // the fp32 state of both heads (row = head, p; column = n), staying in TMEM
-// over the whole sequence.  M and the H of C H^T are rounded to bf16 once
-// (the output is bf16).  The state is fp32, so (w X)^T is the sum of three bf16
-// parts, all of fp32's 24 bits: with two the state was 2.4e-6 off (2-norm),
-// with three 3e-7.
+// over the whole sequence.  M (with D on its diagonal: D x_i takes part in that
+// rounding; out's error, 2-norm, is 2.3e-3 with it there and with D x apart)
+// and the H of C H^T are rounded to bf16 once (the output is bf16).  The state
+// is fp32, so (w X)^T is the sum of three bf16 parts, all of fp32's 24 bits:
+// with two the state was 2.4e-6 off (2-norm), with three 3e-7.
 //
 // Two warpgroups in front (a head each: the state's pass between chunks, M),
 // two behind (a head each: (w X)^T, the gated output), and a warp each for the
@@ -362,7 +363,7 @@ struct StateUnit {
 // sequences or segments.  kMore: whole sequences, more of them than SMs; a CTA
 // takes the place of CTAs that have not begun, so that a unit's first copies
 // and products run under the last of the unit before (16 prompts of 8005
-// tokens, 64 heads: 97 us, with a unit per CTA 102).
+// tokens, 64 heads: 96 us, with a unit per CTA 102).
 enum StateMode { kLocal, kOnce, kMore };
 
 template <StateMode kMode>
@@ -1209,7 +1210,7 @@ extern "C" int wave_hybrid_prompt_state(wave_t* h, int layer, const void* weight
   // Segments: the shortest that give no more CTAs than SMs, if that is worth
   // two more launches.  A chunk of the first costs about half of one of the
   // last, the launches about two (2048 tokens of 64 heads: 77 us as 32 CTAs
-  // of 16 chunks, 50 in segments of 4; of 4 heads 23 in segments of 1).
+  // of 16 chunks, 49 in segments of 4; of 4 heads 23 in segments of 1).
   auto chunks = [&](int k) { return (all.len(order[k]) + kQ - 1) / kQ; };
   auto segments = [&](int t) {
     int n = 0;

@@ -69,8 +69,10 @@ typedef struct wave_ctx wave_t; /* opaque; owns only its device workspace */
  * context length, and a handle is that profile here.  Allocates the device
  * workspace on the current device (activations, partial sums, the RoPE
  * cos/sin table, barrier words; about 0.5 MB + S_max * (2.1 * d_model + ...)
- * bytes, e.g. ~60 MB for the 7B-class shape at S_max = 128) and one pinned,
- * device-mapped host word for the error status.  Returns WAVE_EINVAL for a
+ * bytes, e.g. ~60 MB for the 7B-class shape at S_max = 128; and what the calls
+ * on prompts leave between their launches, 20 MB for heads of 128, 10 MB for
+ * heads of 64, 10 MB more for a hybrid handle) and one pinned, device-mapped
+ * host word for the error status.  Returns WAVE_EINVAL for a
  * bad shape, WAVE_EDEVICE off sm_103, WAVE_ENOMEM/WAVE_ECUDA on failure;
  * *out is set only on success.
  */
@@ -262,7 +264,7 @@ int wave_hybrid_step(wave_t* h, int S, const void* weights, uint8_t* kv_fp8, flo
  * launches already finished.  The bits are sticky across launches until
  * read: a non-OK result clears them (host word now, device word by an
  * asynchronous memset enqueued on the handle's last stream).  Until a timeout
- * is read, later launches of the handle give up as well, their outputs
+ * is read, later launches of the handle may give up at once, their outputs
  * undefined.  Returns
  * WAVE_OK, WAVE_ETIMEOUT (a device wait gave up; that step's outputs are
  * undefined, the GPU context stays usable) or WAVE_EPOS; WAVE_ECUDA if the
@@ -353,7 +355,11 @@ int wave_prompt_append(wave_t* h, int layer, int n_seq, const int32_t* cu_seqlen
  * that a row does not attend to never reach it, whatever they are (NaN and
  * infinities included).  out must not overlap q, k or v.  Lengths are not
  * tied to the handle's T_max.  One launch; two where few rows leave SMs idle
- * and the keys are divided among them (joined in fp32).
+ * and the keys are divided among them (joined in fp32): a prompt alone and the
+ * same prompt in a larger batch may differ by such roundings.
+ * Prompts are whole: the call reads no history, so it has no counterpart to
+ * the append's starts > 0 (a prompt that goes on from earlier tokens attends
+ * to them in the steps only).
  */
 int wave_prompt_attention(wave_t* h, int n_seq, const int32_t* cu_seqlens, int n_kv_heads, int type, const void* q,
                           int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
@@ -382,8 +388,11 @@ int wave_prompt_attention(wave_t* h, int n_seq, const int32_t* cu_seqlens, int n
  * recurrence token by token in fp32, whoever else is in the call (and those of
  * up to 48 where few heads are); longer ones run it in chunks of 128
  * tokens on the tensor cores, where y's two products take bf16 factors (the
- * decayed C B^T, and the state before the chunk) and the state's product takes
- * each weighted x as the sum of three bf16, to fp32's precision.  A token
+ * decayed C B^T with D on its diagonal, and the state before the chunk) and the
+ * state's product takes each weighted x as the sum of three bf16, to fp32's
+ * precision.  A long sequence alone and in a larger call may differ by these
+ * roundings (where it is cut into segments the state passes between them in
+ * fp32).  A token
  * whose x is not finite makes its own and later tokens of that channel not
  * finite (NaN in the rest of its chunk).  One to four launches.
  */
