@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(4 * R, R == 64 ? 3 : 1) k_prompt_state_rows(co
     if (tid < kRowBatch && t0 + tid < n) {
       const float raw = bf(vdt) + bias;
       const float dt = raw > 0.f ? raw + log1pf(expf(-raw)) : log1pf(expf(raw));
-      sda[tid] = make_float2(dt, dt == 0.f ? 1.f : expf(a_neg * dt));  // also at an infinite rate
+      sda[tid] = make_float2(dt, dt == 0.f && a_neg < 0.f ? 1.f : expf(a_neg * dt));  // an infinite rate too, not a NaN
     }
     __syncthreads();
     if (t0 + kRowBatch < n) load(t0 + kRowBatch);

@@ -75,6 +75,10 @@ def test_state_parameters_that_are_not_a_number(lens, which):
     rest = [h for h in range(hs) if h != 1 or which == 2]
     assert torch.equal(new[0, 0, rest], want[0, 0, rest])
     assert torch.equal(out[:, :P], exact[:, :P]) and torch.equal(out[:, 2 * P:], exact[:, 2 * P:])
+    if which == 0:  # also where no token has a step: NaN times zero
+        zx[:, -hs:] = -200.0
+        new = _run_state(hs, case, [0], [3], 1)
+        assert bool(torch.isnan(out[:, P:2 * P]).all()) and bool(torch.isnan(new[0, 0, 1]).all())
 
 
 @pytest.mark.parametrize("hs,lens", [(4, [25, 2048]), (64, [1, 300]), (64, [28] + [500] * 12), (32, [7, 300, 20, 129, 600, 40, 260]),
@@ -151,6 +155,7 @@ def test_attention_that_is_stuck_ends_after_one_limit(lens, H, Hkv, tile):
     cu, q, k, v, out = _attention(lens, H, Hkv, 128, torch.bfloat16, seed=tile)
     w = _wave(H, 128)
     try:
+        w.prompt_attention(cu, q, k, v, out)
         w.set_timeout_ns(LIMIT_MS * 1_000_000)
         w.debug_skip_signal(9, tile)
         ms = _timed(lambda: w.prompt_attention(cu, q, k, v, out))
