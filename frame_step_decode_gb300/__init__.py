@@ -17,6 +17,8 @@ WAVE_OK, WAVE_EINVAL, WAVE_ECUDA, WAVE_ELAUNCH = 0, -1, -2, -3
 WAVE_ETIMEOUT, WAVE_EPOS, WAVE_EDEVICE, WAVE_ENOMEM = -4, -5, -6, -7
 WAVE_F32, WAVE_BF16, WAVE_F16 = 0, 1, 2
 WAVE_MAX_SEQS = 128
+_ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+_ROPE_SCALINGS = {"none": 0, "linear": 1, "parts": 2}
 
 
 class WaveConfig(ctypes.Structure):
@@ -43,6 +45,18 @@ class WaveHybridConfig(ctypes.Structure):
                    w.ssm_state, w.rms_eps, w.rope_base)
 
 
+class WaveRopeConfig(ctypes.Structure):
+    _fields_ = [("layout", ctypes.c_int), ("dims", ctypes.c_int), ("base", ctypes.c_float), ("scaling", ctypes.c_int),
+                ("factor", ctypes.c_float), ("original", ctypes.c_float), ("fast", ctypes.c_float), ("slow", ctypes.c_float),
+                ("amplitude", ctypes.c_float)]
+
+
+class WaveRope(ctypes.Structure):
+    """A plan of rotary positions (rope_plan)."""
+    _fields_ = [("layout", ctypes.c_int32), ("dims", ctypes.c_int32), ("amplitude", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("turns", ctypes.c_uint64 * 64)]
+
+
 class WaveError(RuntimeError):
     def __init__(self, code: int, what: str):
         super().__init__(f"{what}: {strerror(code)} ({code})")
@@ -58,7 +72,9 @@ EXPORTS = ("wave_create", "wave_destroy", "wave_weights_bytes", "wave_weight_off
            "wave_debug_act_record_floats", "wave_debug_phase_times", "wave_debug_arrival_times",
            "wave_grid_size", "wave_barriers_per_step", "wave_phases_per_step", "wave_hybrid_create", "wave_hybrid_step",
            "wave_hybrid_weights_bytes", "wave_hybrid_layer_offset",
-           "wave_prompt_append", "wave_prompt_attention", "wave_hybrid_prompt_state", "wave_sessions_copy")
+           "wave_prompt_append", "wave_prompt_attention", "wave_hybrid_prompt_state", "wave_sessions_copy",
+           "wave_rope_plan", "wave_rope_apply", "wave_rope_apply_at", "wave_history_append", "wave_history_append_frame",
+           "wave_history_read", "wave_history_attention", "wave_history_attention_frame")
 
 
 def lib() -> ctypes.CDLL:
@@ -140,6 +156,22 @@ def lib() -> ctypes.CDLL:
         L.wave_hybrid_prompt_state.restype = i32
         L.wave_sessions_copy.argtypes = [vp, i32, vp, vp, i32, vp, vp, vp, vp, vp]
         L.wave_sessions_copy.restype = i32
+        L.wave_rope_plan.argtypes = [ctypes.POINTER(WaveRopeConfig), vp]
+        L.wave_rope_plan.restype = i32
+        L.wave_rope_apply.argtypes = [vp, i32, vp, vp, i32, i32, vp, i32, i64, vp, i32, i64, vp]
+        L.wave_rope_apply.restype = i32
+        L.wave_rope_apply_at.argtypes = [vp, i64, vp, i32, i32, vp, i32, i64, vp, i32, i64, vp]
+        L.wave_rope_apply_at.restype = i32
+        L.wave_history_append.argtypes = [vp, i32, i32, vp, vp, vp, vp, vp, i32, i64, vp, vp, i32, i32, vp, i32, vp]
+        L.wave_history_append.restype = i32
+        L.wave_history_append_frame.argtypes = [vp, i32, i32, vp, vp, vp, i32, i64, vp, vp, i32, i32, vp, i32, vp]
+        L.wave_history_append_frame.restype = i32
+        L.wave_history_read.argtypes = [vp, i32, i32, vp, vp, vp, vp, vp, i32, i32, vp, vp, i32, vp]
+        L.wave_history_read.restype = i32
+        L.wave_history_attention.argtypes = [vp, i32, i32, vp, vp, vp, i32, vp, i64, vp, vp, i32, i32, ctypes.c_float, vp, i64, vp]
+        L.wave_history_attention.restype = i32
+        L.wave_history_attention_frame.argtypes = [vp, i32, i32, vp, i32, vp, i64, vp, vp, i32, i32, ctypes.c_float, vp, i64, vp]
+        L.wave_history_attention_frame.restype = i32
         _lib = L
     return _lib
 
@@ -417,6 +449,134 @@ class Wave:
             raise WaveError(rc, "wave_sessions_copy")
         return rc
 
+    def _history(self, what, kv, kv_scales, n_kv_heads, block) -> None:
+        """Refuse buffers that are no history of n_kv_heads heads with a scale for each `block` tokens."""
+        c = self.cfg
+        if n_kv_heads < 1 or c.n_heads % n_kv_heads or block not in (1, 16, 32, 64, 128):
+            raise ValueError(f"{what}: n_kv_heads divides n_heads, and a block is 1, 16, 32, 64 or 128 tokens")
+        if self.h:
+            rows = self._n_scales // (c.n_heads * self.T_max) * n_kv_heads
+            _held(kv, 1, rows * self.T_max * c.head_dim, self.device, f"{what}: kv")
+            _held(kv_scales, "float32", rows * -(-self.T_max // block), self.device, f"{what}: kv_scales")
+
+    def _append_rows(self, what, rows, qkv, n_kv_heads, q) -> None:
+        """Refuse a qkv or a q that does not have the call's rows."""
+        H, D = self.cfg.n_heads, self.cfg.head_dim
+        if len(qkv.shape) != 2 or qkv.shape[1] != (H + 2 * n_kv_heads) * D or qkv.shape[0] < rows:
+            raise ValueError(f"{what}: qkv is [rows][(n_heads + 2 n_kv_heads) * D], with the rows that the call names")
+        if q is not None and (not _is_rows(q, rows, H, D) or not q.is_contiguous()):
+            raise ValueError(f"{what}: q is contiguous [rows][n_heads][D]")
+        if self.h:
+            _here(self.device, what, qkv, q)
+
+    def history_append(self, layer, cu_seqlens, slots, starts, qkv, kv, kv_scales, n_kv_heads, block, rope=None, q=None,
+                       stream=None, check=True) -> int:
+        """wave_history_append: rotary positions (rope: a rope_plan or None),
+        8-bit quantisation and append of packed prompts to layer `layer`'s
+        history of n_kv_heads heads with one scale for each `block` tokens.
+        qkv is [rows][(n_heads + 2 n_kv_heads) * D] (fp32 or bf16, rows may be
+        strided); q, optional, the rotated q, contiguous [rows][n_heads][D]."""
+        what = "wave_history_append"
+        (cu, n_cu), (sl, n_sl), (s0, n_s0) = _ints(cu_seqlens), _ints(slots), _ints(starts)
+        if n_cu < 2 or n_sl != n_cu - 1 or n_s0 != n_sl:
+            raise ValueError(f"{what}: one slot and one start for each sequence")
+        self._append_rows(what, int(cu_seqlens[n_sl]), qkv, n_kv_heads, q)
+        self._history(what, kv, kv_scales, n_kv_heads, block)
+        rc = lib().wave_history_append(self.h, layer, n_sl, cu, sl, s0, _plan(rope), _ptr(qkv), _type_of(qkv), _rows(qkv, what),
+                                       _ptr(kv), _ptr(kv_scales), n_kv_heads, block, _ptr(q),
+                                       WAVE_BF16 if q is None else _type_of(q), _stream(stream))
+        if check and rc != WAVE_OK:
+            raise WaveError(rc, what)
+        return rc
+
+    def history_append_frame(self, layer, positions, qkv, kv, kv_scales, n_kv_heads, block, rope=None, q=None, stream=None,
+                             check=True) -> int:
+        """wave_history_append_frame: the same for one token of each session,
+        row s in slot s at positions[s] (int32 on the device; negative: an
+        empty slot)."""
+        what, S = "wave_history_append_frame", positions.numel()
+        self._append_rows(what, S, qkv, n_kv_heads, q)
+        self._history(what, kv, kv_scales, n_kv_heads, block)
+        if self.h:
+            _held(positions, "int32", S, self.device, f"{what}: positions")
+        rc = lib().wave_history_append_frame(self.h, layer, S, _ptr(positions), _plan(rope), _ptr(qkv), _type_of(qkv),
+                                             _rows(qkv, what), _ptr(kv), _ptr(kv_scales), n_kv_heads, block, _ptr(q),
+                                             WAVE_BF16 if q is None else _type_of(q), _stream(stream))
+        if check and rc != WAVE_OK:
+            raise WaveError(rc, what)
+        return rc
+
+    def history_read(self, layer, cu_seqlens, slots, starts, kv, kv_scales, n_kv_heads, block, k=None, v=None, stream=None,
+                     check=True) -> int:
+        """wave_history_read: positions starts[i] .. of session slots[i] back
+        as contiguous k and v [rows][n_kv_heads][D] (either optional, of one
+        type: fp32, bf16 or fp16)."""
+        what = "wave_history_read"
+        (cu, n_cu), (sl, n_sl), (s0, n_s0) = _ints(cu_seqlens), _ints(slots), _ints(starts)
+        if n_cu < 2 or n_sl != n_cu - 1 or n_s0 != n_sl:
+            raise ValueError(f"{what}: one slot and one start for each sequence")
+        rows, out_type = int(cu_seqlens[n_sl]), -1
+        for t in (k, v):
+            if t is None:
+                continue
+            kind = _type_of(t)
+            if not _is_rows(t, rows, n_kv_heads, self.cfg.head_dim) or out_type not in (-1, kind) or not t.is_contiguous():
+                raise ValueError(f"{what}: k and v are contiguous [rows][n_kv_heads][D], of one type")
+            out_type = kind
+        self._history(what, kv, kv_scales, n_kv_heads, block)
+        if self.h:
+            _here(self.device, what, k, v)
+        rc = lib().wave_history_read(self.h, layer, n_sl, cu, sl, s0, _ptr(kv), _ptr(kv_scales), n_kv_heads, block, _ptr(k), _ptr(v),
+                                     out_type, _stream(stream))
+        if check and rc != WAVE_OK:
+            raise WaveError(rc, what)
+        return rc
+
+    def _attention_rows(self, what, rows, q, out) -> None:
+        """Refuse q and out that do not have the call's rows."""
+        H, D = self.cfg.n_heads, self.cfg.head_dim
+        if out.dtype != q.dtype or not _is_rows(q, rows, H, D) or not _is_rows(out, rows, H, D):
+            raise ValueError(f"{what}: q and out are [rows][n_heads][D] of one type, with the rows that the call names")
+        if self.h:
+            _here(self.device, what, q, out)
+
+    def history_attention(self, layer, cu_seqlens, slots, starts, q, kv, kv_scales, n_kv_heads, block, out, scale=None,
+                          stream=None, check=True) -> int:
+        """wave_history_attention: attention of packed prompts that go on from
+        their sessions' history (append them first).  q and out are
+        [rows][n_heads][D], bf16 or fp16, rows may be strided; scale defaults
+        to 1/sqrt(D)."""
+        what = "wave_history_attention"
+        (cu, n_cu), (sl, n_sl), (s0, n_s0) = _ints(cu_seqlens), _ints(slots), _ints(starts)
+        if n_cu < 2 or n_sl != n_cu - 1 or n_s0 != n_sl:
+            raise ValueError(f"{what}: one slot and one start for each sequence")
+        self._attention_rows(what, int(cu_seqlens[n_sl]), q, out)
+        self._history(what, kv, kv_scales, n_kv_heads, block)
+        rc = lib().wave_history_attention(self.h, layer, n_sl, cu, sl, s0, _type_of(q), _ptr(q), _rows(q, what), _ptr(kv),
+                                          _ptr(kv_scales), n_kv_heads, block, self.cfg.head_dim ** -0.5 if scale is None else scale,
+                                          _ptr(out), _rows(out, what), _stream(stream))
+        if check and rc != WAVE_OK:
+            raise WaveError(rc, what)
+        return rc
+
+    def history_attention_frame(self, layer, positions, q, kv, kv_scales, n_kv_heads, block, out, scale=None, stream=None,
+                                check=True) -> int:
+        """wave_history_attention_frame: the same for one token of each
+        session, row s in slot s at positions[s] (int32 on the device;
+        negative: an empty slot, whose row is left as it is)."""
+        what, S = "wave_history_attention_frame", positions.numel()
+        self._attention_rows(what, S, q, out)
+        self._history(what, kv, kv_scales, n_kv_heads, block)
+        if self.h:
+            _held(positions, "int32", S, self.device, f"{what}: positions")
+        rc = lib().wave_history_attention_frame(self.h, layer, S, _ptr(positions), _type_of(q), _ptr(q), _rows(q, what), _ptr(kv),
+                                                _ptr(kv_scales), n_kv_heads, block,
+                                                self.cfg.head_dim ** -0.5 if scale is None else scale, _ptr(out),
+                                                _rows(out, what), _stream(stream))
+        if check and rc != WAVE_OK:
+            raise WaveError(rc, what)
+        return rc
+
     def status(self, sync: bool = True) -> int:
         """wave_status.  The C call synchronises nothing and reports the
         launches already finished; with sync (the default) the device is
@@ -521,6 +681,65 @@ def fp8_encode(inp, out, stream=None, n: int | None = None) -> None:
     rc = lib().wave_fp8_encode(_ptr(inp), n, _ptr(out), _stream(stream))
     if rc != WAVE_OK:
         raise WaveError(rc, "wave_fp8_encode")
+
+
+def rope_plan(dims: int, base: float = 10000.0, layout: str = "half", scaling: str = "none", factor: float = 1.0,
+              original: float = 0.0, fast: float = 32.0, slow: float = 1.0, amplitude: float = 1.0) -> WaveRope:
+    """wave_rope_plan: rotary positions of the leading `dims` values of a head.
+    layout "half" (pairs (i, i + dims/2)) or "interleaved" ((2i, 2i + 1));
+    scaling "none", "linear" (frequencies / factor) or "parts" (only those of
+    few turns over `original` positions)."""
+    if layout not in _ROPE_LAYOUTS or scaling not in _ROPE_SCALINGS:
+        raise ValueError('wave_rope_plan: layout is "half" or "interleaved", scaling "none", "linear" or "parts"')
+    c = WaveRopeConfig(_ROPE_LAYOUTS[layout], dims, base, _ROPE_SCALINGS[scaling], factor, original, fast, slow, amplitude)
+    plan = WaveRope()
+    rc = lib().wave_rope_plan(ctypes.byref(c), ctypes.addressof(plan))
+    if rc != WAVE_OK:
+        raise WaveError(rc, "wave_rope_plan")
+    return plan
+
+
+def _plan(rope) -> int | None:
+    if rope is None:
+        return None
+    if not isinstance(rope, WaveRope):
+        raise ValueError("a plan made by rope_plan is wanted")
+    return ctypes.addressof(rope)
+
+
+def rope_apply(plan, x, out=None, cu_seqlens=None, starts=None, positions=None, stream=None) -> None:
+    """wave_rope_apply (cu_seqlens and starts: host integers, rows of packed
+    prompts) or wave_rope_apply_at (positions: int32 on the device, one for each
+    row).  x and out are [rows][heads][D] of fp32, bf16 or fp16, rows may be
+    strided; out defaults to x itself."""
+    out = x if out is None else out
+    what = "wave_rope_apply"
+    if len(x.shape) != 3 or x.shape[1:] != out.shape[1:] or (positions is None) == (cu_seqlens is None or starts is None):
+        raise ValueError(f"{what}: x and out are [rows][heads][D]; either cu_seqlens and starts or positions are given")
+    if positions is None:
+        (cu, n_cu), (s0, n_s0) = _ints(cu_seqlens), _ints(starts)
+        if n_cu < 2 or n_s0 != n_cu - 1:
+            raise ValueError(f"{what}: one start for each sequence")
+        rows = int(cu_seqlens[n_s0])
+    else:
+        rows = positions.numel()
+    if x.shape[0] < rows or out.shape[0] < rows:
+        raise ValueError(f"{what}: x and out have the rows that the call names")
+    if x.is_cuda:
+        import torch
+        device = torch.cuda.current_device()
+        _here(device, what, x, out)
+        if positions is not None:
+            _DTYPES.setdefault("int32", torch.int32)
+            _held(positions, "int32", rows, device, f"{what}: positions")
+    heads, D = x.shape[1], x.shape[2]
+    xs = (_ptr(x), _type_of(x), _rows(x, what), _ptr(out), _type_of(out), _rows(out, what), _stream(stream))
+    if positions is None:
+        rc = lib().wave_rope_apply(_plan(plan), n_s0, cu, s0, heads, D, *xs)
+    else:
+        rc = lib().wave_rope_apply_at(_plan(plan), rows, _ptr(positions), heads, D, *xs)
+    if rc != WAVE_OK:
+        raise WaveError(rc, what)
 
 
 class HybridWave(Wave):

@@ -51,6 +51,13 @@ extern "C" {
 #define WAVE_F16 2
 /* Sequences one call on packed prompts takes at most (the largest S_max). */
 #define WAVE_MAX_SEQS 128
+/* Rotary positions: which values of a head are a pair, and how the
+ * frequencies are scaled (wave_rope_config). */
+#define WAVE_ROPE_HALF 0
+#define WAVE_ROPE_INTERLEAVED 1
+#define WAVE_ROPE_PLAIN 0
+#define WAVE_ROPE_LINEAR 1
+#define WAVE_ROPE_PARTS 2
 
 /* Decoder shape.  Constraints checked by wave_create: head_dim is 64 or 128;
  * d_model (at most 8192), n_heads*head_dim and ffn are multiples of 64, 64
@@ -417,6 +424,137 @@ int wave_hybrid_prompt_state(wave_t* h, int layer, const void* weights, int n_se
  */
 int wave_sessions_copy(wave_t* h, int n, const int32_t* src, const int32_t* dst, int move, uint8_t* kv_fp8,
                        float* kv_scales, float* ssm_state, int32_t* positions, void* stream);
+
+/* ---- rotary positions ------------------------------------------------------
+ * The step rotates the pairs (i, i + D/2) of a whole head by pos * base^(-2i/D).
+ * These calls rotate packed rows in the other forms that models use, and the
+ * history's appends below take the same plan.  An interface addition of this
+ * library, as the calls on prompts are.
+ */
+typedef struct {
+  int layout;      /* WAVE_ROPE_HALF: pairs (i, i + dims/2); WAVE_ROPE_INTERLEAVED: (2i, 2i + 1) */
+  int dims;        /* the leading values of a head that are rotated: a multiple of 16, 16..128 */
+  float base;      /* frequency of pair i: base^(-2i/dims), > 0 */
+  int scaling;     /* WAVE_ROPE_PLAIN; _LINEAR: frequency / factor; _PARTS: by turns, below */
+  float factor;    /* > 0 (LINEAR, PARTS) */
+  float original;  /* PARTS: positions the model was trained on, > 0 */
+  float fast;      /* PARTS: pairs of at least this many turns over `original` keep their frequency, ... */
+  float slow;      /* ... those of at most this many get frequency / factor; between the two, linear in the turns; 0 <= slow < fast */
+  float amplitude; /* multiplies cosine and sine (1: none) */
+} wave_rope_config;
+
+/* A plan: plain data, made once on the host and passed to the calls, which
+ * read it before they return.  turns[i] is the frequency of pair i in turns,
+ * times 2^64: the angle of any position is exact modulo a turn. */
+typedef struct {
+  int32_t layout, dims;
+  float amplitude;
+  int32_t reserved;
+  uint64_t turns[64];
+} wave_rope;
+
+/* Make a plan.  Host only, no device needed; frequencies in fp64.  WAVE_EINVAL
+ * for a bad argument (*rope is set only on success). */
+int wave_rope_plan(const wave_rope_config* config, wave_rope* rope);
+
+/*
+ * Rotate packed rows: x and out hold n_heads heads of head_dim (64 or 128, at
+ * least rope->dims) per row, heads contiguous in a row, rows *_stride elements
+ * apart (multiples of 8, below 2^31); type and out_type are WAVE_F32, WAVE_BF16
+ * or WAVE_F16 each.  Values of a head beyond rope->dims are copied.  out may be
+ * x itself (same type and stride); otherwise the two do not overlap.  The
+ * arithmetic is fp32, rounded once at the end; cosine and sine are good to fp32
+ * at every position.
+ *
+ * wave_rope_apply: rows of packed prompts, sequence i at positions starts[i],
+ * starts[i] + 1, ... (host arrays, as the calls on prompts have them); rows
+ * outside every sequence are not written.
+ * wave_rope_apply_at: row r at positions[r], a DEVICE array of `rows` int32; a
+ * row whose position is negative is not written.
+ * Asynchronous, one launch, bound by HBM.
+ */
+int wave_rope_apply(const wave_rope* rope, int n_seq, const int32_t* cu_seqlens, const int32_t* starts, int n_heads,
+                    int head_dim, const void* x, int type, int64_t x_stride, void* out, int out_type, int64_t out_stride,
+                    void* stream);
+int wave_rope_apply_at(const wave_rope* rope, int64_t rows, const int32_t* positions, int n_heads, int head_dim,
+                       const void* x, int type, int64_t x_stride, void* out, int out_type, int64_t out_stride,
+                       void* stream);
+
+/* ---- the history in blocks --------------------------------------------------
+ * The step's history has a scale for each token and as many K/V heads as query
+ * heads.  The calls below work on a history whose layers have n_kv_heads heads
+ * (a divisor of the handle's n_heads; query head h reads K/V head h / (n_heads /
+ * n_kv_heads)) and one scale for each block of `block` tokens and head:
+ *
+ *   kv_fp8     uint8 [L][2][S_max][n_kv_heads][T_max][D]
+ *   kv_scales  float [L][2][S_max][n_kv_heads][ceil(T_max / block)]
+ *
+ * with L, S_max, T_max and D of the handle (L: its attention layers).  block is
+ * 1, 16, 32, 64 or 128.  With block 1 and n_kv_heads = n_heads it is the step's
+ * own history, by the step's own rule (scale = amax / 448): what
+ * wave_prompt_append and the steps write, these calls read, and the other way
+ * round.  So a later prompt of a live session goes on from its history.
+ *
+ * Blocks of 16 and more.  A block's scale is the least power of two s with |v|
+ * <= 448 s for every finite v that it holds (0 if all are 0).  Codes are
+ * floating point, so that a power of two costs no precision, and when a token
+ * is added that needs a larger scale the codes before it are encoded anew by a
+ * change of exponent, which loses nothing above their normal range (2^-6 s).
+ * Infinities are held as +-448 s, NaN as NaN.  The first token that a call
+ * writes to a block at the block's first place begins the block anew; one at a
+ * later place goes on with the scale that the block has.  Slots of a block
+ * behind the last token written keep their codes and mean nothing.
+ *
+ * Prompts (cu_seqlens, slots, starts: HOST arrays) and their rules are those of
+ * the calls on packed prompts.  The _frame forms take one token of each of S
+ * sessions, row s in slot s at positions[s], a DEVICE array [S] as wave_step
+ * has it: they can be captured once and replayed at other positions.  A
+ * negative position is an empty slot, whose row is neither read nor written;
+ * one at or beyond T_max sets WAVE_EPOS, writes no history and gives a zero
+ * attention output.
+ */
+
+/*
+ * Rotate, quantise and append.  qkv is [rows][row_stride], row = q (n_heads*D)
+ * | k (n_kv_heads*D) | v (n_kv_heads*D), of qkv_type WAVE_F32 or WAVE_BF16; q and
+ * k are rotated by `rope` (NULL: not at all); k and v go to slots starts[i] + t
+ * of session slots[i]; the rotated q is rounded to q [rows][n_heads][D] of q_type
+ * (WAVE_BF16 or WAVE_F16; q may be NULL).  One launch, bound by HBM.
+ */
+int wave_history_append(wave_t* h, int layer, int n_seq, const int32_t* cu_seqlens, const int32_t* slots,
+                        const int32_t* starts, const wave_rope* rope, const void* qkv, int qkv_type, int64_t row_stride,
+                        uint8_t* kv_fp8, float* kv_scales, int n_kv_heads, int block, void* q, int q_type, void* stream);
+int wave_history_append_frame(wave_t* h, int layer, int S, const int32_t* positions, const wave_rope* rope,
+                              const void* qkv, int qkv_type, int64_t row_stride, uint8_t* kv_fp8, float* kv_scales,
+                              int n_kv_heads, int block, void* q, int q_type, void* stream);
+
+/*
+ * Read back: positions starts[i] .. of session slots[i], as many as the
+ * sequence has rows, code * scale rounded once, to k and v [rows][n_kv_heads][D]
+ * of out_type (WAVE_F32, WAVE_BF16 or WAVE_F16; either may be NULL).
+ */
+int wave_history_read(wave_t* h, int layer, int n_seq, const int32_t* cu_seqlens, const int32_t* slots,
+                      const int32_t* starts, const uint8_t* kv_fp8, const float* kv_scales, int n_kv_heads, int block,
+                      void* k, void* v, int out_type, void* stream);
+
+/*
+ * Attention over the history: the row of the token at position p of a session
+ * attends to slots 0 .. p of it, its own token (appended before) included,
+ *     out = sum_{t<=p} w_t v_t / sum_{t<=p} w_t,  w_t = exp(scale q . k_t - max).
+ * q and out hold n_heads heads of D per row of `type` (WAVE_BF16 or WAVE_F16),
+ * rows *_stride elements apart; scale is > 0 and at most 2.3e38; n_heads /
+ * n_kv_heads is at most 128.  Codes are exact factors of the products; scores,
+ * the softmax's maximum and sums and the output are kept in fp32, the weights
+ * are rounded to fp16 (11 bits) for the second product.  Slots that a row does not
+ * attend to never reach it, whatever they hold.  out must not overlap q.
+ */
+int wave_history_attention(wave_t* h, int layer, int n_seq, const int32_t* cu_seqlens, const int32_t* slots,
+                           const int32_t* starts, int type, const void* q, int64_t q_stride, const uint8_t* kv_fp8,
+                           const float* kv_scales, int n_kv_heads, int block, float scale, void* out, int64_t out_stride,
+                           void* stream);
+int wave_history_attention_frame(wave_t* h, int layer, int S, const int32_t* positions, int type, const void* q,
+                                 int64_t q_stride, const uint8_t* kv_fp8, const float* kv_scales, int n_kv_heads,
+                                 int block, float scale, void* out, int64_t out_stride, void* stream);
 
 /*
  * wave_step for callers that cannot allocate device memory (inside another
