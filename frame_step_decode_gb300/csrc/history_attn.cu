@@ -10,23 +10,11 @@
 #include <stdint.h>
 
 #include "../../include/wave.h"
-#include "history.h"
+#include "history_attn.h"
 
 using namespace wave;
 
 namespace wave {
-
-struct HistoryAttnParams {
-  SeqBatch b;
-  const int32_t* positions;  // a frame's, on the device; null: the batch's
-  History hist;
-  int heads, group;
-  const uint16_t* q;
-  uint16_t* out;
-  long long q_stride, out_stride;
-  float scale2;              // scale * log2(e)
-  int *err, *err_out;
-};
 
 template <int D, typename T>
 __global__ void __launch_bounds__(256) k_history_attention(const __grid_constant__ HistoryAttnParams p, int tokens) {
@@ -76,6 +64,21 @@ __global__ void __launch_bounds__(256) k_history_attention(const __grid_constant
   for (int e = 0; e < kPer; ++e) out[e] = (T)(acc[e] / l);
 }
 
+// The sequences of `from` that have a length to keep.
+template <typename F>
+static void keep(SeqBatch* to, const SeqBatch from, F want) {
+  to->n = 0;
+  to->cum[0] = 0;
+  for (int i = 0; i < from.n; ++i) {
+    if (!want(from.len(i))) continue;
+    to->begin[to->n] = from.begin[i];
+    to->slot[to->n] = from.slot[i];
+    to->start[to->n] = from.start[i];
+    to->cum[to->n + 1] = to->cum[to->n] + from.len(i);
+    ++to->n;
+  }
+}
+
 static int attention(wave_t* h, HistoryAttnParams& p, int tokens, int type, const void* q, int64_t q_stride, float scale,
                      void* out, int64_t out_stride, void* stream) {
   const int H = h->pl.cfg.n_heads, D = h->pl.cfg.head_dim;
@@ -99,13 +102,32 @@ static int attention(wave_t* h, HistoryAttnParams& p, int tokens, int type, cons
   p.err_out = h->err_host_dev;
   cudaStream_t st = (cudaStream_t)stream;
   h->last_stream = st;
-  const unsigned ctas = (unsigned)(((long long)tokens * H + 7) / 8);
-  if (D == 128)
-    type == WAVE_F16 ? k_history_attention<128, __half><<<ctas, 256, 0, st>>>(p, tokens)
-                     : k_history_attention<128, __nv_bfloat16><<<ctas, 256, 0, st>>>(p, tokens);
-  else
-    type == WAVE_F16 ? k_history_attention<64, __half><<<ctas, 256, 0, st>>>(p, tokens)
-                     : k_history_attention<64, __nv_bfloat16><<<ctas, 256, 0, st>>>(p, tokens);
+  // Sequences whose rows fit one tile of few rows, and the others.
+  HistoryAttnParams many = p;
+  if (p.positions) {
+    p.n = tokens;
+    many.b.n = 0;
+  } else {
+    keep(&p.b, many.b, [&](int len) { return (long long)len * p.group <= kFewRows; });
+    keep(&many.b, many.b, [&](int len) { return (long long)len * p.group > kFewRows; });
+    p.n = p.b.n;
+  }
+  p.part = h->ws.part_o;
+  p.part_cnt = h->ws.hist_cnt;
+  if (p.n) {
+    const cudaError_t e = launch_history_few(p, D, type, h->pl.grid, st);
+    if (e != cudaSuccess) return WAVE_ECUDA;
+  }
+  if (many.b.n) {
+    const int rows = many.b.cum[many.b.n];
+    const unsigned ctas = (unsigned)(((long long)rows * H + 7) / 8);
+    if (D == 128)
+      type == WAVE_F16 ? k_history_attention<128, __half><<<ctas, 256, 0, st>>>(many, rows)
+                       : k_history_attention<128, __nv_bfloat16><<<ctas, 256, 0, st>>>(many, rows);
+    else
+      type == WAVE_F16 ? k_history_attention<64, __half><<<ctas, 256, 0, st>>>(many, rows)
+                       : k_history_attention<64, __nv_bfloat16><<<ctas, 256, 0, st>>>(many, rows);
+  }
   return cudaGetLastError() == cudaSuccess ? WAVE_OK : WAVE_ECUDA;
 }
 

@@ -1,0 +1,34 @@
+// history_attn.h -- what the two kernels of attention over the 8-bit history share.
+#pragma once
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "history.h"
+#include "prompt_ptx.cuh"
+
+namespace wave {
+
+struct HistoryAttnParams {
+  SeqBatch b;
+  const int32_t* positions;  // a frame's, on the device; null: the batch's
+  int n;                     // sequences, or rows of the frame
+  History hist;
+  int heads, group;
+  const uint16_t* q;
+  uint16_t* out;
+  long long q_stride, out_stride;
+  float scale2;              // scale * log2(e)
+  float* part;               // sums of units that several CTAs share, ...
+  int* part_cnt;             // ... and how many have left theirs (0 between launches)
+  int *err, *err_out;
+};
+
+constexpr int kFewRows = 16;  // rows (tokens times heads of a group) of one unit of few rows
+
+// Floats that a CTA leaves for others: two units' rows, their maxima and sums.
+inline size_t few_part_floats(int D) { return 2 * (size_t)kFewRows * (D + 2); }
+
+cudaError_t configure_history_few();
+cudaError_t launch_history_few(const HistoryAttnParams& p, int D, int type, int sms, cudaStream_t st);
+
+}  // namespace wave

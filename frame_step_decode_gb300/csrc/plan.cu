@@ -91,7 +91,7 @@ int device_check(int* dev, int* sms) {
   if (major != 10 || minor != 3) return WAVE_EDEVICE;
   if (!encode_fn()) return WAVE_ECUDA;
   if (configure_step_kernel() != cudaSuccess || configure_prompt_attention() != cudaSuccess ||
-      configure_prompt_state() != cudaSuccess)
+      configure_prompt_state() != cudaSuccess || configure_history_few() != cudaSuccess)
     return WAVE_ECUDA;
   int per_sm = 0;
   if (occupancy_per_sm(&per_sm) != cudaSuccess || per_sm < 1) return WAVE_ELAUNCH;
@@ -269,6 +269,7 @@ size_t carve_workspace(const Plan& pl, char* base, Workspace* ws) {
       {(void**)&w.ssm_out, (size_t)(SP * pl.d_inner * 2)},
       {(void**)&w.part_o, pl.prompts ? (size_t)pl.grid * 256 * D * 4 : 0},
       {(void**)&w.part_ml, pl.prompts ? (size_t)pl.grid * 256 * 8 : 0},
+      {(void**)&w.hist_cnt, pl.prompts ? (size_t)pl.S_max * H * 4 : 0},
       {(void**)&w.seg_state, pl.hybrid && pl.prompts ? (size_t)pl.grid * 2 * kSsmP * kSsmN * 4 : 0},
       {(void**)&w.seg_decay, pl.hybrid && pl.prompts ? (size_t)pl.grid * 2 * 4 : 0},
   };

@@ -67,6 +67,7 @@ struct Workspace {
   uint16_t* ssm_out = nullptr;
   float* part_o = nullptr;     // attention over prompts: sums of parts of the keys, one per SM, ...
   float2* part_ml = nullptr;   // ... and their maxima and sums of weights
+  int* hist_cnt = nullptr;     // attention over the history: CTAs that have left a unit's sums (0 between launches)
   float* seg_state = nullptr;  // hybrid: states of prompt segments, one per SM, ...
   float* seg_decay = nullptr;  // ... and their decays
 };
@@ -86,6 +87,7 @@ void hybrid_layout(const wave_hybrid_config* c, long long* M, long long* A, long
 // Attributes of the prompt kernels on the current device (prompt_attn.cu, prompt_state.cu).
 cudaError_t configure_prompt_attention();
 cudaError_t configure_prompt_state();
+cudaError_t configure_history_few();  // and of attention over the history (history_few.cu)
 // The current device, its SM count, and whether it is sm_103 with the driver
 // entry points and kernel attributes the step needs.
 int device_check(int* dev, int* sms);
