@@ -16,54 +16,6 @@ using namespace wave;
 
 namespace wave {
 
-template <int D, typename T>
-__global__ void __launch_bounds__(256) k_history_attention(const __grid_constant__ HistoryAttnParams p, int tokens) {
-  constexpr int kPer = D / 32;
-  const int lane = threadIdx.x & 31;
-  const long long i = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int t = (int)(i / p.heads), head = (int)(i % p.heads);
-  if (t >= tokens) return;
-  int row, pos, slot;
-  if (p.positions) {
-    row = slot = t;
-    pos = p.positions[t];
-    if (pos < 0) return;
-  } else {
-    const int s = seq_of(p.b, t), n = t - p.b.cum[s];
-    row = p.b.begin[s] + n;
-    pos = p.b.start[s] + n;
-    slot = p.b.slot[s];
-  }
-  T* out = (T*)p.out + (size_t)row * p.out_stride + head * D + lane * kPer;
-  float acc[kPer] = {}, q[kPer], m = -INFINITY, l = 0.f;
-  if (pos >= p.hist.T_max) {
-    if (lane == 0 && head == 0) bad_position(p.err, p.err_out);
-    l = 1.f;
-    pos = -1;
-  }
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) q[e] = (float)((const T*)p.q)[(size_t)row * p.q_stride + head * D + lane * kPer + e];
-  const size_t kr = p.hist.row(0, slot, head / p.group), vr = p.hist.row(1, slot, head / p.group);
-  const uint8_t *kc = p.hist.codes + kr * p.hist.T_max * D, *vc = p.hist.codes + vr * p.hist.T_max * D;
-  const float *ks = p.hist.scales + kr * p.hist.blocks, *vs = p.hist.scales + vr * p.hist.blocks;
-  auto value = [](uint8_t c) { return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3))); };
-  for (int j = 0; j <= pos; ++j) {
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) s += q[e] * value(kc[(size_t)j * D + lane * kPer + e]);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    s *= ks[j >> p.hist.shift] * p.scale2;
-    const float top = fmaxf(m, s), a = exp2f(m - top), w = exp2f(s - top), v = vs[j >> p.hist.shift];
-    m = top;
-    l = l * a + w;
-#pragma unroll
-    for (int e = 0; e < kPer; ++e) acc[e] = acc[e] * a + w * (v * value(vc[(size_t)j * D + lane * kPer + e]));
-  }
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) out[e] = (T)(acc[e] / l);
-}
-
 // The sequences of `from` that have a length to keep.
 template <typename F>
 static void keep(SeqBatch* to, const SeqBatch from, F want) {
@@ -118,17 +70,8 @@ static int attention(wave_t* h, HistoryAttnParams& p, int tokens, int type, cons
     const cudaError_t e = launch_history_few(p, D, type, h->pl.grid, st);
     if (e != cudaSuccess) return WAVE_ECUDA;
   }
-  if (many.b.n) {
-    const int rows = many.b.cum[many.b.n];
-    const unsigned ctas = (unsigned)(((long long)rows * H + 7) / 8);
-    if (D == 128)
-      type == WAVE_F16 ? k_history_attention<128, __half><<<ctas, 256, 0, st>>>(many, rows)
-                       : k_history_attention<128, __nv_bfloat16><<<ctas, 256, 0, st>>>(many, rows);
-    else
-      type == WAVE_F16 ? k_history_attention<64, __half><<<ctas, 256, 0, st>>>(many, rows)
-                       : k_history_attention<64, __nv_bfloat16><<<ctas, 256, 0, st>>>(many, rows);
-  }
-  return cudaGetLastError() == cudaSuccess ? WAVE_OK : WAVE_ECUDA;
+  if (many.b.n && launch_history_many(many, h, type, st) != cudaSuccess) return WAVE_ECUDA;
+  return WAVE_OK;
 }
 
 }  // namespace wave

@@ -25,10 +25,8 @@ struct HistoryAttnParams {
 
 constexpr int kFewRows = 16;  // rows (tokens times heads of a group) of one unit of few rows
 
-// Floats that a CTA leaves for others: two units' rows, their maxima and sums.
-inline size_t few_part_floats(int D) { return 2 * (size_t)kFewRows * (D + 2); }
-
-cudaError_t configure_history_few();
 cudaError_t launch_history_few(const HistoryAttnParams& p, int D, int type, int sms, cudaStream_t st);
+
+cudaError_t launch_history_many(const HistoryAttnParams& p, const wave_ctx* h, int type, cudaStream_t st);
 
 }  // namespace wave

@@ -1,0 +1,838 @@
+// history_many.cu -- attention over the 8-bit history for prompts that go on:
+// more rows than one tile of 16.
+//
+// Bound by the tensor cores (4 D flops for a query head, a query and a key).
+// Rows are (token, head of the group), so that the heads of a K/V head share its
+// tiles; a pair of 128-row tiles is a unit, its two tiles are two streams, and
+// while one stream's weights are computed the tensor core works for the other.
+// S = Q K^T by tcgen05 into TMEM, a thread per row turns S into the weights P
+// (fp16, written over S), O += P V by tcgen05 with P read from TMEM.
+//
+// Four warps bring the codes to fp16 operand tiles: 16 codes a load, held in
+// registers one tile ahead, an exact conversion, and for blocks of 16 to 64 a
+// product with the block's scale relative to the largest of the tile's (a power
+// of two: exact).  The largest itself is a factor of the scores (K) and an
+// offset of the weights' exponents (V).  With a scale for each token the
+// softmax's threads multiply the columns of S and of P in fp32 instead.
+//
+// All units' key blocks are one line, cut evenly among the SMs: a unit's blocks
+// in several CTAs leave fp32 sums, which a second launch joins.
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "history_attn.h"
+
+using namespace wave;
+
+namespace wave {
+
+constexpr int kManyRows = 128;      // rows of a stream, and keys of a block
+constexpr int kManyThreads = 512;   // 8 softmax warps (two streams), 4 that convert, one for MMAs, 3 without work
+constexpr int kMaxCuts = 160;       // CTAs
+constexpr int kRegsRows = 176, kRegsCodes = 96, kRegsMma = 64;
+constexpr float kManyBias = 7.f;    // weights are held times 2^7, see below
+
+// Where a CTA's part of the line begins: key block `block` of a unit.
+struct ManyCut {
+  int32_t seq, level, head, block;
+};
+
+struct ManyParams {
+  HistoryAttnParams a;  // a.b: the sequences
+  int tile_tokens;      // tokens of a 128-row tile: 128 / group
+  int ctas;
+  ManyCut cut[kMaxCuts + 1];
+  float* part_o;        // [2 * CTA + (the unit begins there)][256 rows][D]
+  float2* part_ml;      // their maxima and sums
+  int wide;             // out's rows are 32-byte aligned
+  ErrSink sink;
+  int skip;             // testing hook: no tile of K and V from this one on is made (-1: off)
+};
+
+// A unit's blocks [from, to) in this CTA.
+struct ManyItem {
+  int seq, level, head;
+  int tok0, len;       // first token of stream 0, of the sequence's
+  int n[2];            // key blocks of the streams, from the sequence's begin (0: no rows)
+  int from, to;
+  __host__ __device__ int blocks() const { return n[0] > n[1] ? n[0] : n[1]; }
+  __host__ __device__ bool whole() const { return from == 0 && to == blocks(); }
+};
+
+__host__ __device__ inline void unit_blocks(const SeqBatch& b, int tile_tokens, ManyItem& it) {
+  it.tok0 = it.level * 2 * tile_tokens;
+  it.len = b.len(it.seq);
+  for (int st = 0; st < 2; ++st) {
+    const int first = it.tok0 + st * tile_tokens, last = first + tile_tokens < it.len ? first + tile_tokens : it.len;
+    it.n[st] = first < it.len ? (b.start[it.seq] + last - 1) / kManyRows + 1 : 0;
+  }
+}
+
+// A CTA's walk along its part of the line.
+struct ManyWalk {
+  ManyItem it;
+  __device__ __forceinline__ bool begin(const ManyParams& p) {
+    const ManyCut& c = p.cut[blockIdx.x];
+    it.seq = c.seq, it.level = c.level, it.head = c.head, it.from = c.block;
+    return set(p);
+  }
+  __device__ __forceinline__ bool next(const ManyParams& p) {
+    if (it.to < it.blocks()) return false;  // the rest is another CTA's
+    it.from = 0;
+    if (++it.head == p.a.hist.heads) {
+      it.head = 0;
+      if ((++it.level) * 2 * p.tile_tokens >= it.len) it.level = 0, ++it.seq;
+    }
+    return set(p);
+  }
+  __device__ __forceinline__ bool set(const ManyParams& p) {
+    const ManyCut& e = p.cut[blockIdx.x + 1];
+    const bool last = it.seq == e.seq && it.level == e.level && it.head == e.head;
+    if (it.seq >= p.a.b.n || (last && it.from >= e.block)) return false;
+    unit_blocks(p.a.b, p.tile_tokens, it);
+    it.to = last ? e.block : it.blocks();
+    return true;
+  }
+};
+
+struct BlockMeta {
+  float factor;       // of the scores: the tile's largest K scale, over 2^6
+  float shift;        // of the weights' exponents: log2 of the largest V scale
+  float back;         // 2^-shift
+  float pad;
+  float k[kManyRows], v[kManyRows];  // scales for each token: K's, and V's over 2^shift
+};
+
+template <int D>
+struct ManySmem {
+  static constexpr int kTile = kManyRows * D * 2;
+  static constexpr int kStages = D == 128 ? 4 : 8;
+  static constexpr int kMetas = 4;
+  static constexpr int kRing = 2 * kTile;
+  static constexpr int kMeta = kRing + kStages * kTile;
+  static constexpr int kBad = kMeta + kMetas * (int)sizeof(BlockMeta);  // [2 units][converting warp][D]: the first token whose value is NaN
+  static constexpr int kBars = kBad + 2 * 4 * D * 4;
+  enum {
+    kFull = 0,
+    kEmpty = kFull + kStages,
+    kMetaFull = kEmpty + kStages,
+    kMetaEmpty = kMetaFull + kMetas,
+    kQFull = kMetaEmpty + kMetas,
+    kSFull = kQFull + 2,
+    kPFull = kSFull + 2,
+    kOFull = kPFull + 2,
+    kBadFree = kOFull + 2,
+    kDone = kBadFree + 2,
+    kCount
+  };
+  static constexpr int kMisc = (kBars + kCount * 8 + 15) / 16 * 16;
+  static constexpr int kTotal = kMisc + 48 + 1024;  // + alignment
+};
+static_assert(ManySmem<128>::kTotal <= 232448 && ManySmem<64>::kTotal <= 232448, "shared memory of a CTA");
+
+__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+// The exponent of the least power of two at or above x > 0.
+__device__ __forceinline__ int exponent_up(float x) {
+  const uint32_t u = __float_as_uint(x);
+  return (int)(u >> 23) - 127 + ((u & 0x7FFFFFu) != 0);
+}
+__device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+
+// kTok: a scale for each token.
+template <int D, bool kF16, bool kTok>
+__global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_constant__ ManyParams p) {
+  using L = ManySmem<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t base_raw = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + ((1024 - (base_raw & 1023)) & 1023);
+  const uint32_t sb = smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto bar = [&](int i) { return sb + L::kBars + i * 8; };
+  BlockMeta* metas = (BlockMeta*)(smem + L::kMeta);
+  int* bad = (int*)(smem + L::kBad);
+  uint32_t* tmem_word = (uint32_t*)(smem + L::kMisc);
+  int* leave = (int*)(smem + L::kMisc + 8);
+  int* odd_unit = (int*)(smem + L::kMisc + 16);  // [2 units][converting warp]: it has found NaN values
+
+  if (warp == 12) {
+    if (lane == 0) {
+      for (int i = 0; i < L::kStages; ++i) {
+        mbar_init(bar(L::kFull + i), 4);
+        mbar_init(bar(L::kEmpty + i), 1);
+      }
+      for (int i = 0; i < L::kMetas; ++i) {
+        mbar_init(bar(L::kMetaFull + i), 4);
+        mbar_init(bar(L::kMetaEmpty + i), 8);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(bar(L::kQFull + i), 4);
+        mbar_init(bar(L::kSFull + i), 1);
+        mbar_init(bar(L::kPFull + i), 4);
+        mbar_init(bar(L::kOFull + i), 1);
+        mbar_init(bar(L::kBadFree + i), 8);
+      }
+      mbar_init(bar(L::kDone), 1);
+      fence_mbar_init();
+      fence_proxy_async_smem();
+      *leave = stopped(p.sink);
+    }
+    __syncwarp();
+    tmem_alloc(smem_u32(tmem_word), 512);
+    tmem_relinquish();
+  }
+  for (int i = threadIdx.x; i < 8 * D; i += kManyThreads) bad[i] = INT32_MAX;
+  if (threadIdx.x < 8) odd_unit[threadIdx.x] = 0;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_word;
+  const bool stop = *leave;
+  auto tS = [&](int st) { return tmem + st * 128; };
+  auto tO = [&](int st) { return tmem + 256 + st * D; };
+
+  // Every wait is bounded; a give-up sets the error word and ends the role's
+  // loop, which lets the waits of the others run out too; CTAs that begin
+  // later leave at once.
+  bool ok = true;
+  auto wait_warp = [&](int b, uint32_t parity) {
+    return ok = __all_sync(0xffffffffu, wait_bar(bar(b), parity, p.sink));
+  };
+  ManyWalk walk;
+
+  if (warp < 8) {
+    // ---------------------------------------------------------------- softmax
+    regs_take<kRegsRows>();
+    const int st = warp >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    uint32_t s_it = 0, o_it = 0, m_it = 0, k = 0;
+    // The row's q into the stream's operand tile (128-byte swizzle): fp16, bf16
+    // times a power of two; the factor that its scores get in return.
+    auto bring_q = [&](const ManyItem& it) {
+      const int r = row / p.a.group, tok = it.tok0 + st * p.tile_tokens + r;
+      const bool on = r < p.tile_tokens && tok < it.len;
+      const uint16_t* src = p.a.q + (p.a.b.begin[it.seq] + (on ? tok : it.tok0)) * p.a.q_stride + (it.head * p.a.group + row % p.a.group) * D;
+      uint4 v[D / 8];
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) v[i] = on ? __ldg((const uint4*)src + i) : make_uint4(0, 0, 0, 0);
+      float factor = p.a.scale2, up = 1.f;
+      if constexpr (!kF16) {
+        uint32_t top = 0;  // the largest magnitude: bf16 bits compare as integers
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+          top = __vmaxu2(top, __vmaxu2(__vmaxu2(v[i].x & 0x7FFF7FFFu, v[i].y & 0x7FFF7FFFu), __vmaxu2(v[i].z & 0x7FFF7FFFu, v[i].w & 0x7FFF7FFFu)));
+        top = max(top & 0xFFFFu, top >> 16);
+        const int ex = min(max((int)(top >> 7) - 127, -113), 127);
+        up = power(14 - ex);
+        factor = p.a.scale2 * power(ex) * 0x1p-14f;
+      }
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        if constexpr (!kF16) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) w[c] = half2_of(__uint_as_float(w[c] << 16) * up, __uint_as_float(w[c] & 0xFFFF0000u) * up);
+        }
+        *(uint4*)(smem + st * L::kTile + (i / 8) * (kManyRows * 128) + row * 128 + (((i % 8) ^ (row & 7)) << 4)) =
+            make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::kQFull + st));
+      return factor;
+    };
+    bool live = !stop && walk.begin(p);
+    float factor = live && walk.it.n[st] > walk.it.from ? bring_q(walk.it) : 0.f;
+    for (; live && ok; ++k) {
+      const ManyItem it = walk.it;
+      const int n = min(it.n[st], it.to) - it.from, all = it.to - it.from;  // this stream's blocks, and the unit's
+      const int tok = it.tok0 + st * p.tile_tokens + row / p.a.group;
+      const bool on = row / p.a.group < p.tile_tokens && tok < it.len;
+      const int pos = p.a.b.start[it.seq] + tok;
+      const int cut = (p.a.b.start[it.seq] + it.tok0 + st * p.tile_tokens) / kManyRows;  // from here on some row does not see all keys
+      float m = -INFINITY, l = 0.f, next_factor = 0.f;
+      for (int j = 0; j < all; ++j, ++m_it) {
+        const int mi = m_it % L::kMetas;
+        if (j >= n) {  // the other stream's
+          if (!wait_warp(L::kMetaFull + mi, (m_it / L::kMetas) & 1)) break;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::kMetaEmpty + mi));
+          continue;
+        }
+        if (!wait_warp(L::kMetaFull + mi, (m_it / L::kMetas) & 1)) break;
+        const BlockMeta& meta = metas[mi];
+        const float z = fmaxf(factor * meta.factor, 0x1p-126f), shift = meta.shift, back = meta.back;
+        if (!wait_warp(L::kSFull + st, s_it & 1)) break;
+        ++s_it;
+        tc_fence_after();
+        // 32 columns at a time; the first of them are read again at the end: all
+        // 128 in registers would leave too few for the warps that convert.
+        const bool masked = it.from + j >= cut;
+        const int seen = pos - (it.from + j) * kManyRows;
+        auto ready = [&](int c, uint32_t* s) {  // scaled and masked
+          if constexpr (kTok) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 f = ((const float4*)meta.k)[8 * c + i];
+              const float2 x = mul2(make_float2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), make_float2(f.x, f.y));
+              const float2 y = mul2(make_float2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), make_float2(f.z, f.w));
+              s[4 * i] = __float_as_uint(x.x), s[4 * i + 1] = __float_as_uint(x.y);
+              s[4 * i + 2] = __float_as_uint(y.x), s[4 * i + 3] = __float_as_uint(y.y);
+            }
+          }
+          if (masked) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (32 * c + i > seen) s[i] = __float_as_uint(-INFINITY);
+          }
+        };
+        float mx[2] = {-INFINITY, -INFINITY};
+        auto largest = [&](const uint32_t* s) {
+#pragma unroll
+          for (int i = 0; i < 32; i += 4) {
+            mx[0] = max3(mx[0], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+            mx[1] = max3(mx[1], __uint_as_float(s[i + 2]), __uint_as_float(s[i + 3]));
+          }
+        };
+        uint32_t s0[32], s1[32], s2[32], s3[32];
+        tmem_ld32(tS(st) + lanes, s0);
+        tmem_ld_wait();
+        tmem_ld32(tS(st) + lanes + 32, s1);
+        tmem_ld32(tS(st) + lanes + 64, s2);
+        tmem_ld32(tS(st) + lanes + 96, s3);
+        ready(0, s0);
+        largest(s0);
+        tmem_ld_wait();
+        ready(1, s1);
+        largest(s1);
+        ready(2, s2);
+        largest(s2);
+        ready(3, s3);
+        largest(s3);
+        // The weights' exponents are those of w times the tile's V scale; their
+        // maximum moves only when one would exceed 2^8 of it: O is rescaled
+        // seldom.  fp16 holds them between 2^7 and 2^15 and down to 2^-25, so
+        // that one 2^-32 of the largest is still there.
+        const float top = fmaf(fmaxf(mx[0], mx[1]), z, shift);
+        if (j == 0) {
+          m = top;
+        } else {
+          const bool up = top > m + 8.f;
+          if (__any_sync(0xffffffffu, up)) {
+            const float m2 = up ? top : m;
+            const float a = up ? (m == -INFINITY ? 0.f : ex2(m - m2)) : 1.f;
+            l *= a;
+            m = m2;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(tO(st) + lanes + 32 * c, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
+              tmem_st32(tO(st) + lanes + 32 * c, o);
+            }
+          }
+        }
+        const float neg = (m == -INFINITY ? 0.f : shift - m) + kManyBias;
+        const float2 z2 = make_float2(z, z), neg2 = make_float2(neg, neg);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        uint32_t w[16];
+        auto weights = [&](int c, const uint32_t* s) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 x = fma2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), z2, neg2);
+            float2 e = make_float2(ex2(x.x), ex2(x.y));
+            sum[i & 1] = add2(sum[i & 1], e);
+            if constexpr (kTok) e = mul2(e, ((const float2*)meta.v)[16 * c + i]);
+            w[i] = half2_of(e.x, e.y);
+          }
+        };
+        // P's columns lie over S's first half: its second half first
+        weights(3, s3);
+        tmem_st16(tS(st) + lanes + 48, w);
+        weights(2, s2);
+        tmem_st16(tS(st) + lanes + 32, w);
+        tmem_ld32(tS(st) + lanes, s0);
+        weights(1, s1);
+        tmem_ld_wait();
+        tmem_st16(tS(st) + lanes + 16, w);
+        ready(0, s0);
+        weights(0, s0);
+        tmem_st16(tS(st) + lanes, w);
+        l += ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) * back;
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bar(L::kPFull + st));
+          mbar_arrive(bar(L::kMetaEmpty + mi));
+        }
+      }
+      if (!ok) break;
+      // the next unit's q, before this one's output is waited for (its last scores are done)
+      live = walk.next(p);
+      if (live && walk.it.n[st] > walk.it.from) next_factor = bring_q(walk.it);
+      if (n > 0) {
+        if (!wait_warp(L::kOFull + st, o_it & 1)) break;
+        ++o_it;
+        tc_fence_after();
+        const int4 found = *(const int4*)&odd_unit[(k & 1) * 4];
+        const bool odd = (found.x | found.y | found.z | found.w) != 0;
+        const bool part = !it.whole();
+        const float inv = 1.f / l;
+        const int head = it.head * p.a.group + row % p.a.group;
+        uint16_t* orow = p.a.out + (p.a.b.begin[it.seq] + (on ? tok : it.tok0)) * p.a.out_stride + head * D;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(tO(st) + lanes + 32 * c, o);
+          tmem_ld_wait();
+          if (odd) {  // NaN that was left out of P V: for the rows that see it
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              for (int f = 0; f < 4; ++f)
+                if (pos >= bad[((k & 1) * 4 + f) * D + 32 * c + i]) o[i] = 0x7FC00000u;
+          }
+          if (part) {
+            const size_t at = (size_t)(2 * blockIdx.x + (it.from == 0)) * (2 * kManyRows) + st * kManyRows + row;
+            if (on) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) store32(p.part_o + at * D + 32 * c + 8 * i, o + 8 * i);
+              if (c == 0) p.part_ml[at] = make_float2(m, l);
+            }
+          } else if (on) {
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 v = mul2(make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), make_float2(inv, inv));
+              w[i] = kF16 ? half2_of(v.x, v.y) : pair16<__nv_bfloat16>(v.x, v.y);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if (p.wide)
+                store32(orow + 32 * c + 16 * i, w + 8 * i);
+              else
+#pragma unroll
+                for (int f = 0; f < 2; ++f)
+                  *(uint4*)(orow + 32 * c + 16 * i + 8 * f) =
+                      make_uint4(w[8 * i + 4 * f], w[8 * i + 4 * f + 1], w[8 * i + 4 * f + 2], w[8 * i + 4 * f + 3]);
+            }
+          }
+          __syncwarp();
+        }
+        tc_fence_before();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::kBadFree + (k & 1)));
+      factor = next_factor;
+    }
+  } else if (warp < 12) {
+    // -------------------------------------------------------- codes to tiles
+    regs_give<kRegsCodes>();
+    const int tid = threadIdx.x - 256;
+    constexpr int kRowPieces = D / 16, kPieces = kManyRows * kRowPieces / 128;  // 16-byte pieces of a token; a thread's of a tile
+    constexpr int kRowStep = 128 / kRowPieces;
+    const int prow = tid / kRowPieces, pc = tid % kRowPieces;
+    int* my_bad = bad + (warp - 8) * D;
+    uint32_t tiles = 0, m_it = 0, k = 0;
+    uint4 code[kPieces];
+    float sc[8];  // the block's scales, one block ahead: K's and V's
+    const uint8_t *kc, *vc;
+    const float *ks, *vs;
+    int keys;
+    auto unit = [&](const ManyItem& it) {
+      const size_t kr = p.a.hist.row(0, p.a.b.slot[it.seq], it.head), vr = p.a.hist.row(1, p.a.b.slot[it.seq], it.head);
+      kc = p.a.hist.codes + kr * p.a.hist.T_max * D;
+      vc = p.a.hist.codes + vr * p.a.hist.T_max * D;
+      ks = p.a.hist.scales + kr * p.a.hist.blocks;
+      vs = p.a.hist.scales + vr * p.a.hist.blocks;
+      keys = p.a.b.start[it.seq] + min(it.len, it.tok0 + 2 * p.tile_tokens);
+    };
+    auto piece = [&](const uint8_t* src, int block, int i) {
+      const int t = block * kManyRows + prow + i * kRowStep;
+      return t < keys ? __ldg((const uint4*)(src + (size_t)t * D + pc * 16)) : make_uint4(0, 0, 0, 0);
+    };
+    auto scales = [&](int block) {
+      if constexpr (kTok) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int t = block * kManyRows + lane * 4 + i;
+          sc[i] = t < keys ? __ldg(ks + t) : 0.f;
+          sc[4 + i] = t < keys ? __ldg(vs + t) : 0.f;
+        }
+      } else {  // lanes 0..7 K's, 8..15 V's
+        const int t = block * kManyRows + ((lane & 7) << p.a.hist.shift);
+        sc[0] = lane < 16 && ((lane & 7) << p.a.hist.shift) < kManyRows && t < keys ? __ldg((lane < 8 ? ks : vs) + (t >> p.a.hist.shift)) : 0.f;
+      }
+    };
+    bool live = !stop && walk.begin(p);
+    if (live) {
+      unit(walk.it);
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) code[i] = piece(kc, walk.it.from, i);
+      scales(walk.it.from);
+    }
+    for (; live && ok; ++k) {
+      const ManyItem it = walk.it;
+      const int first_cut = (p.a.b.start[it.seq] + it.tok0) / kManyRows;
+      if (k >= 2) {  // the unit before the last has been written: its list of NaN values is free
+        if (!wait_warp(L::kBadFree + (k & 1), ((k >> 1) - 1) & 1)) break;
+        for (int i = lane; i < D; i += 32) my_bad[(k & 1) * 4 * D + i] = INT32_MAX;
+        if (lane == 0) odd_unit[(k & 1) * 4 + warp - 8] = 0;
+        __syncwarp();
+      }
+      for (int j = it.from; j < it.to && ok; ++j, ++m_it) {
+        const int mi = m_it % L::kMetas;
+        BlockMeta& meta = metas[mi];
+        uint32_t ratio[2];  // kTok: unused; else lane's scale over the tile's, as two fp16
+        if (!wait_warp(L::kMetaEmpty + mi, ((m_it / L::kMetas) & 1) ^ 1)) break;
+        if constexpr (kTok) {
+          // a V scale that is not finite makes all its token's values NaN
+          bool odd = false;
+#pragma unroll
+          for (int i = 4; i < 8; ++i) odd |= !(sc[i] <= 0x1.fffffep127f);
+          if (warp == 8 && __any_sync(0xffffffffu, odd)) {
+            for (int i = 4; i < 8; ++i)
+              if (!(sc[i] <= 0x1.fffffep127f))
+                for (int d = 0; d < D; ++d) atomicMin(&my_bad[(k & 1) * 4 * D + d], j * kManyRows + 4 * lane + i - 4);
+            odd_unit[(k & 1) * 4] = 1;
+          }
+#pragma unroll
+          for (int i = 4; i < 8; ++i) sc[i] = sc[i] <= 0x1.fffffep127f ? sc[i] : 0.f;
+          float top = fmaxf(fmaxf(sc[4], sc[5]), fmaxf(sc[6], sc[7]));
+#pragma unroll
+          for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+          const int e = top > 0.f ? min(max(exponent_up(top), -100), 120) : -100;
+          if (warp == 8) *(float4*)&meta.k[4 * lane] = make_float4(sc[0], sc[1], sc[2], sc[3]);
+          if (warp == 9) {
+            const float r = power(-e);
+            *(float4*)&meta.v[4 * lane] = make_float4(sc[4] * r, sc[5] * r, sc[6] * r, sc[7] * r);
+          }
+          if (warp == 10 && lane == 0) meta.factor = 0x1p-6f, meta.shift = (float)e, meta.back = power(-e);
+          ratio[0] = 0x54005400u;  // 2^6
+          ratio[1] = 0x3C003C00u;  // 1
+        } else {
+          float top = sc[0];
+#pragma unroll
+          for (int d = 4; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+          const int e = top > 0.f ? min(max(exponent_up(top), lane < 8 ? -120 : -100), 120) : -100;
+          const float r = sc[0] * power(-e) * (lane < 8 ? 64.f : 1.f);
+          ratio[0] = half2_of(r, r);
+          const int ek = __shfl_sync(0xffffffffu, e, 0), ev = __shfl_sync(0xffffffffu, e, 8);
+          if (warp == 8 && lane == 0) meta.factor = power(ek) * 0x1p-6f, meta.shift = (float)ev, meta.back = power(-ev);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::kMetaFull + mi));
+#pragma unroll
+        for (int which = 0; which < 2; ++which, ++tiles) {
+          const int slot = tiles % L::kStages;
+          if (tiles == (uint32_t)p.skip) {
+            ok = false;
+            break;
+          }
+          if (!wait_warp(L::kEmpty + slot, ((tiles / L::kStages) & 1) ^ 1)) break;
+          uint8_t* dst = smem + L::kRing + slot * L::kTile;
+          // the tile behind this one, loaded as this one's registers become free
+          const uint8_t* src = which ? kc : vc;
+          int block = j + which;
+          bool more = true;
+          if (which && j + 1 == it.to) {
+            live = walk.next(p);
+            more = live;
+            if (live) {
+              unit(walk.it);
+              src = kc;
+              block = walk.it.from;
+            }
+          }
+          const bool look = which && j >= first_cut;
+          bool odd = false;
+#pragma unroll
+          for (int i = 0; i < kPieces; ++i) {
+            const int row = prow + i * kRowStep;
+            uint32_t c[4] = {code[i].x, code[i].y, code[i].z, code[i].w}, h[8];
+            if (look) {
+#pragma unroll
+              for (int x = 0; x < 4; ++x) odd |= (((c[x] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
+            }
+            uint32_t r;
+            if constexpr (kTok)
+              r = ratio[which];
+            else
+              r = __shfl_sync(0xffffffffu, ratio[0], (row >> p.a.hist.shift) + 8 * which);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) e4m3x4_to_f16x2x2(c[x], h[2 * x], h[2 * x + 1]);
+            if (!kTok || !which) {
+#pragma unroll
+              for (int x = 0; x < 8; ++x) h[x] = mul_half2(h[x], r);
+            }
+            // 16 values: two chunks of a row of 128 bytes; lanes of a row's second half begin with the odd one
+            uint8_t* at = dst + (pc / 4) * (kManyRows * 128) + row * 128;
+            const int c0 = (pc % 4) * 2, flip = pc >> 2;
+            const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+            *(uint4*)(at + (((c0 + flip) ^ (row & 7)) << 4)) = flip ? hi : lo;
+            *(uint4*)(at + (((c0 + (flip ^ 1)) ^ (row & 7)) << 4)) = flip ? lo : hi;
+          }
+          if (__any_sync(0xffffffffu, odd)) {
+            // NaN in a tile that some row does not see all of (0 x NaN would
+            // reach it): out of the tile, and noted for the rows that do
+#pragma unroll 1
+            for (int i = 0; i < kPieces; ++i) {
+              const int row = prow + i * kRowStep;
+              for (int x = 0; x < 16; ++x) {
+                uint16_t* at = (uint16_t*)(dst + (pc / 4) * (kManyRows * 128) + row * 128 + ((((pc % 4) * 2 + x / 8) ^ (row & 7)) << 4)) + x % 8;
+                if ((*at & 0x7FFF) > 0x7C00) {
+                  *at = 0;
+                  atomicMin(&my_bad[(k & 1) * 4 * D + pc * 16 + x], j * kManyRows + row);
+                  odd_unit[(k & 1) * 4 + warp - 8] = 1;
+                }
+              }
+            }
+          }
+          if (more) {
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) code[i] = piece(src, block, i);
+            if (which) scales(block);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(L::kFull + slot));
+        }
+      }
+    }
+  } else {
+    regs_give<kRegsMma>();
+    if (warp == 12) {
+      // --------------------------------------------------------------- MMAs
+      // In issue order on the tensor core, which is what lets Q K^T of block j
+      // + 1 be issued behind P V of block j although both use the same TMEM
+      // columns; a commit covers every MMA issued before it.
+      constexpr uint32_t id_s = idesc_16(128, 128, true, false, false), id_o = idesc_16(128, D, true, false, true);
+      uint32_t p_par[2] = {0, 0}, q_par[2] = {0, 0};
+      int at = 0;           // the next tile of the ring ...
+      uint32_t at_par = 0;  // ... and its parity
+      auto next_tile = [&]() {  // waits for it; its slot
+        wait_warp(L::kFull + at, at_par);
+        const int slot = at;
+        if (++at == L::kStages) at = 0, at_par ^= 1;
+        return slot;
+      };
+      auto commit = [&](int b) {
+        if (elect_one()) tc_commit(bar(b));
+        __syncwarp();
+      };
+      auto scores = [&](int st, int slot) {  // S = Q K^T
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t q = sdesc_lo(sb + st * L::kTile), kt = sdesc_lo(sb + L::kRing + slot * L::kTile);
+#pragma unroll
+          for (int e = 0; e < D / 16; ++e) {
+            const uint32_t o = ((e / 4) * (kManyRows * 128) + (e % 4) * 32) >> 4;
+            if (e == 0)
+              mma_ss<false>(tS(st), q, kt, id_s);
+            else
+              mma_ss<true>(tS(st), q + o, kt + o, id_s);
+          }
+          tc_commit(bar(L::kSFull + st));
+        }
+        __syncwarp();
+      };
+      auto values = [&](int st, int slot, bool first) {  // O += P V
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t vt = sdesc_lo(sb + L::kRing + slot * L::kTile, kManyRows * 128);
+#pragma unroll
+          for (int e = 0; e < kManyRows / 16; ++e)
+            mma_ts(tO(st), tS(st) + 8 * e, vt + e * (2048 >> 4), id_o, e > 0 ? 1u : first ? 0u : 1u);
+        }
+        __syncwarp();
+      };
+      bool live = !stop && walk.begin(p);
+      while (live && ok) {
+        const int n0 = min(walk.it.n[0], walk.it.to) - walk.it.from, n1 = min(walk.it.n[1], walk.it.to) - walk.it.from;
+        const int nb = max(n0, n1);
+        live = walk.next(p);
+        int ks = next_tile();
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+          if (!ok || (st ? n1 : n0) <= 0 || !wait_warp(L::kQFull + st, q_par[st])) continue;
+          q_par[st] ^= 1;
+          scores(st, ks);
+        }
+        if (!ok) break;
+        commit(L::kEmpty + ks);
+        int vsl = next_tile();
+        for (int j = 0; j < nb && ok; ++j) {
+          const bool more = j + 1 < nb;
+          int vnext = 0;
+#pragma unroll
+          for (int st = 0; st < 2; ++st) {
+            const int n = st ? n1 : n0;
+            if (j < n) {
+              if (!wait_warp(L::kPFull + st, p_par[st])) break;
+              p_par[st] ^= 1;
+              values(st, vsl, j == 0);
+            }
+            if (st == 1) commit(L::kEmpty + vsl);
+            if (st == 0 && more) ks = next_tile();
+            if (!ok) break;
+            if (j + 1 < n)
+              scores(st, ks);
+            else if (j + 1 == n)
+              commit(L::kOFull + st);
+            if (st == 0 && more) {
+              vnext = next_tile();
+              if (!ok) break;
+            }
+          }
+          if (ok && more) commit(L::kEmpty + ks);
+          vsl = vnext;
+        }
+      }
+      if (!ok) {  // give-up: wait (bounded) for the MMAs issued so far
+        commit(L::kDone);
+        for (int n = 0; n < (1 << 20) && !mbar_try_wait(bar(L::kDone), 0); ++n) {
+        }
+      }
+      __syncwarp();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 12) tmem_dealloc(tmem, 512);
+}
+
+// A unit's parts joined: a CTA per 32 rows of a unit that is cut, D / 4 threads to a row.
+template <int D, bool kF16>
+__global__ void __launch_bounds__(256) k_join_history(const __grid_constant__ ManyParams p) {
+  constexpr int kLanes = D / 4;
+  const int part = blockIdx.x % 8, c = blockIdx.x / 8 + 1;
+  const ManyCut u = p.cut[c];
+  auto same = [&](int i) { return p.cut[i].seq == u.seq && p.cut[i].level == u.level && p.cut[i].head == u.head && p.cut[i].block > 0; };
+  if (u.block == 0 || (c > 1 && same(c - 1))) return;  // not where a unit is cut first
+  int last = c;  // the last CTA that has a part
+  while (last + 1 < p.ctas && same(last + 1)) ++last;
+  ManyItem it;
+  it.seq = u.seq, it.level = u.level, it.head = u.head;
+  unit_blocks(p.a.b, p.tile_tokens, it);
+  const int col = (int)threadIdx.x % kLanes * 4;
+  for (int r = part * 32 + (int)threadIdx.x / kLanes; r < part * 32 + 32; r += 256 / kLanes) {
+    const int st = r / kManyRows, row = r % kManyRows, tok = it.tok0 + st * p.tile_tokens + row / p.a.group;
+    if (row / p.a.group >= p.tile_tokens || tok >= it.len) continue;
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = c - 1; i <= last; ++i) {
+      const size_t at = (size_t)(2 * i + (i < c)) * (2 * kManyRows) + r;
+      const float2 ml = p.part_ml[at];
+      const float4 v = *(const float4*)(p.part_o + at * D + col);
+      const float top = fmaxf(m, ml.x);
+      const float a = m == -INFINITY ? 0.f : ex2(m - top), b = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
+      l = l * a + ml.y * b;
+      o = make_float4(o.x * a + v.x * b, o.y * a + v.y * b, o.z * a + v.z * b, o.w * a + v.w * b);
+      m = top;
+    }
+    const float inv = 1.f / l;
+    const int head = it.head * p.a.group + row % p.a.group;
+    uint16_t* dst = p.a.out + (p.a.b.begin[it.seq] + tok) * p.a.out_stride + head * D + col;
+    *(uint2*)dst = kF16 ? make_uint2(half2_of(o.x * inv, o.y * inv), half2_of(o.z * inv, o.w * inv))
+                        : make_uint2(pair16<__nv_bfloat16>(o.x * inv, o.y * inv), pair16<__nv_bfloat16>(o.z * inv, o.w * inv));
+  }
+}
+
+// The line cut into even parts, by what its blocks cost: with both streams at
+// work a block takes longer than with one.  A part has three blocks at least.
+// No cut falls before the last block of a unit whose first stream ends a block
+// earlier, so that each stream has a block in every part.
+static bool cut_line(ManyParams& p, int sms) {
+  const SeqBatch& b = p.a.b;
+  const int heads = p.a.hist.heads;
+  auto cost = [](const ManyItem& it) { return it.n[1] ? 4 : 3; };
+  long long total = 0, most = 3;
+  ManyItem it;
+  for (it.seq = 0; it.seq < b.n; ++it.seq)
+    for (it.level = 0; it.level * 2LL * p.tile_tokens < b.len(it.seq); ++it.level) {
+      unit_blocks(b, p.tile_tokens, it);
+      total += (long long)cost(it) * it.blocks() * heads;
+      most = std::max(most, (long long)cost(it));
+    }
+  p.ctas = (int)std::max(1LL, std::min((long long)std::min(sms, kMaxCuts), total / (3 * most)));
+  int c = 0;
+  long long before = 0;  // cost in front of this level's units
+  bool any = false;
+  for (it.seq = 0; it.seq < b.n; ++it.seq)
+    for (it.level = 0; it.level * 2LL * p.tile_tokens < b.len(it.seq); ++it.level) {
+      unit_blocks(b, p.tile_tokens, it);
+      const long long unit = (long long)cost(it) * it.blocks();
+      for (; c < p.ctas; ++c) {
+        const long long at = total * c / p.ctas - before;
+        if (at >= unit * heads) break;
+        int block = (int)(at % unit / cost(it));
+        if (block == it.blocks() - 1 && it.n[1] > it.n[0] && block > 0) --block;
+        p.cut[c] = {it.seq, it.level, (int)(at / unit), block};
+        any |= block > 0;
+      }
+      before += unit * heads;
+    }
+  p.cut[p.ctas] = {b.n, 0, 0, 0};
+  return any;
+}
+
+template <int D, bool kF16, bool kTok>
+static cudaError_t configure() {
+  cudaFuncAttributes a;
+  cudaError_t e = cudaFuncGetAttributes(&a, k_history_many<D, kF16, kTok>);
+  if (e != cudaSuccess) return e;
+  // those that take more registers get them from what the launch had
+  if (a.numRegs * kManyThreads < 256 * kRegsRows + 128 * (kRegsCodes + kRegsMma) || kRegsRows < a.numRegs || kRegsCodes > a.numRegs ||
+      kRegsMma > a.numRegs)
+    return cudaErrorInvalidConfiguration;
+  return cudaFuncSetAttribute(k_history_many<D, kF16, kTok>, cudaFuncAttributeMaxDynamicSharedMemorySize, ManySmem<D>::kTotal);
+}
+
+cudaError_t configure_history_many() {
+  const cudaError_t e[8] = {configure<128, false, false>(), configure<128, false, true>(), configure<128, true, false>(),
+                            configure<128, true, true>(),   configure<64, false, false>(), configure<64, false, true>(),
+                            configure<64, true, false>(),   configure<64, true, true>()};
+  for (cudaError_t x : e)
+    if (x != cudaSuccess) return x;
+  return cudaSuccess;
+}
+
+template <int D, bool kF16>
+static cudaError_t launch(const ManyParams& p, bool join, cudaStream_t st) {
+  if (p.a.hist.block == 1)
+    k_history_many<D, kF16, true><<<p.ctas, kManyThreads, ManySmem<D>::kTotal, st>>>(p);
+  else
+    k_history_many<D, kF16, false><<<p.ctas, kManyThreads, ManySmem<D>::kTotal, st>>>(p);
+  if (join) k_join_history<D, kF16><<<(p.ctas - 1) * 8, 256, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_history_many(const HistoryAttnParams& a, const wave_ctx* h, int type, cudaStream_t st) {
+  ManyParams p;
+  p.a = a;
+  p.tile_tokens = kManyRows / a.group;
+  p.part_o = h->ws.part_o;
+  p.part_ml = h->ws.part_ml;
+  p.wide = ((uintptr_t)a.out & 31) == 0 && a.out_stride % 16 == 0;
+  p.sink = make_sink(h->ws.err, h->err_host_dev, h->timeout_ns);
+  p.skip = h->skip_sig_kind == 11 ? h->skip_sig : -1;
+  const bool join = cut_line(p, h->pl.grid);
+  if (h->pl.cfg.head_dim == 128) return type == WAVE_F16 ? launch<128, true>(p, join, st) : launch<128, false>(p, join, st);
+  return type == WAVE_F16 ? launch<64, true>(p, join, st) : launch<64, false>(p, join, st);
+}
+
+}  // namespace wave

@@ -65,7 +65,7 @@ struct Workspace {
   int32_t* zero_pos = nullptr;
   float* zx = nullptr;
   uint16_t* ssm_out = nullptr;
-  float* part_o = nullptr;     // attention over prompts: sums of parts of the keys, one per SM, ...
+  float* part_o = nullptr;     // attention over prompts: sums of parts of the keys, two per SM, ...
   float2* part_ml = nullptr;   // ... and their maxima and sums of weights
   int* hist_cnt = nullptr;     // attention over the history: CTAs that have left a unit's sums (0 between launches)
   float* seg_state = nullptr;  // hybrid: states of prompt segments, one per SM, ...
@@ -87,7 +87,8 @@ void hybrid_layout(const wave_hybrid_config* c, long long* M, long long* A, long
 // Attributes of the prompt kernels on the current device (prompt_attn.cu, prompt_state.cu).
 cudaError_t configure_prompt_attention();
 cudaError_t configure_prompt_state();
-cudaError_t configure_history_few();  // and of attention over the history (history_few.cu)
+cudaError_t configure_history_few();  // and of attention over the history (history_few.cu, history_many.cu)
+cudaError_t configure_history_many();
 // The current device, its SM count, and whether it is sm_103 with the driver
 // entry points and kernel attributes the step needs.
 int device_check(int* dev, int* sms);
