@@ -8,12 +8,13 @@
 // S = Q K^T by tcgen05 into TMEM, a thread per row turns S into the weights P
 // (fp16, written over S), O += P V by tcgen05 with P read from TMEM.
 //
-// Four warps bring the codes to fp16 operand tiles: 16 codes a load, held in
-// registers one tile ahead, an exact conversion, and for blocks of 16 to 64 a
-// product with the block's scale relative to the largest of the tile's (a power
-// of two: exact).  The largest itself is a factor of the scores (K) and an
-// offset of the weights' exponents (V).  With a scale for each token the
-// softmax's threads multiply the columns of S and of P in fp32 instead.
+// Four warps bring the codes to fp16 operand tiles, an exact conversion: 16
+// codes a load, held in registers one tile ahead.  The K scale of a block of 128
+// is a factor of the scores and the V scale an offset of the weights'
+// exponents, so that neither costs anything an element; in tiles with several
+// scales codes are brought to the largest of them in fp16 (exact for powers of
+// two), and with a scale for each token the softmax's threads multiply the
+// columns of S and of P in fp32.
 //
 // All units' key blocks are one line, cut evenly among the SMs: a unit's blocks
 // in several CTAs leave fp32 sums, which a second launch joins.
@@ -32,8 +33,9 @@ namespace wave {
 constexpr int kManyRows = 128;      // rows of a stream, and keys of a block
 constexpr int kManyThreads = 512;   // 8 softmax warps (two streams), 4 that convert, one for MMAs, 3 without work
 constexpr int kMaxCuts = 160;       // CTAs
-constexpr int kRegsRows = 176, kRegsCodes = 96, kRegsMma = 64;
+constexpr int kRegsRows = 144, kRegsCodes = 128, kRegsMma = 96;
 constexpr float kManyBias = 7.f;    // weights are held times 2^7, see below
+enum { kScaleOfTile, kScaleOfBlock, kScaleOfToken };  // blocks of 128, of 16 to 64, of 1
 
 // Where a CTA's part of the line begins: key block `block` of a unit.
 struct ManyCut {
@@ -58,13 +60,18 @@ struct ManyItem {
   int tok0, len;       // first token of stream 0, of the sequence's
   int n[2];            // key blocks of the streams, from the sequence's begin (0: no rows)
   int from, to;
+  int valid;
+  int start, row0;     // position of the sequence's first token, and its row
   __host__ __device__ int blocks() const { return n[0] > n[1] ? n[0] : n[1]; }
   __host__ __device__ bool whole() const { return from == 0 && to == blocks(); }
+  __host__ __device__ int here(int st) const { return (n[st] < to ? n[st] : to) - from; }  // a stream's blocks in this CTA (or none)
 };
 
 __host__ __device__ inline void unit_blocks(const SeqBatch& b, int tile_tokens, ManyItem& it) {
   it.tok0 = it.level * 2 * tile_tokens;
   it.len = b.len(it.seq);
+  it.start = b.start[it.seq];
+  it.row0 = b.begin[it.seq];
   for (int st = 0; st < 2; ++st) {
     const int first = it.tok0 + st * tile_tokens, last = first + tile_tokens < it.len ? first + tile_tokens : it.len;
     it.n[st] = first < it.len ? (b.start[it.seq] + last - 1) / kManyRows + 1 : 0;
@@ -114,7 +121,8 @@ struct ManySmem {
   static constexpr int kRing = 2 * kTile;
   static constexpr int kMeta = kRing + kStages * kTile;
   static constexpr int kBad = kMeta + kMetas * (int)sizeof(BlockMeta);  // [2 units][converting warp][D]: the first token whose value is NaN
-  static constexpr int kBars = kBad + 2 * 4 * D * 4;
+  static constexpr int kItems = kBad + 2 * 4 * D * 4;
+  static constexpr int kBars = kItems + (2 * (int)sizeof(ManyItem) + 15) / 16 * 16;
   enum {
     kFull = 0,
     kEmpty = kFull + kStages,
@@ -124,8 +132,9 @@ struct ManySmem {
     kSFull = kQFull + 2,
     kPFull = kSFull + 2,
     kOFull = kPFull + 2,
-    kBadFree = kOFull + 2,
-    kDone = kBadFree + 2,
+    kItemFull = kOFull + 2,
+    kItemEmpty = kItemFull + 2,
+    kDone = kItemEmpty + 2,
     kCount
   };
   static constexpr int kMisc = (kBars + kCount * 8 + 15) / 16 * 16;
@@ -150,8 +159,7 @@ __device__ __forceinline__ int exponent_up(float x) {
 }
 __device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
-// kTok: a scale for each token.
-template <int D, bool kF16, bool kTok>
+template <int D, bool kF16, int kScale>
 __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_constant__ ManyParams p) {
   using L = ManySmem<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -162,6 +170,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
   auto bar = [&](int i) { return sb + L::kBars + i * 8; };
   BlockMeta* metas = (BlockMeta*)(smem + L::kMeta);
   int* bad = (int*)(smem + L::kBad);
+  const ManyItem* items = (const ManyItem*)(smem + L::kItems);
   uint32_t* tmem_word = (uint32_t*)(smem + L::kMisc);
   int* leave = (int*)(smem + L::kMisc + 8);
   int* odd_unit = (int*)(smem + L::kMisc + 16);  // [2 units][converting warp]: it has found NaN values
@@ -181,7 +190,8 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
         mbar_init(bar(L::kSFull + i), 1);
         mbar_init(bar(L::kPFull + i), 4);
         mbar_init(bar(L::kOFull + i), 1);
-        mbar_init(bar(L::kBadFree + i), 8);
+        mbar_init(bar(L::kItemFull + i), 1);
+        mbar_init(bar(L::kItemEmpty + i), 13);  // softmax, conversion, MMAs
       }
       mbar_init(bar(L::kDone), 1);
       fence_mbar_init();
@@ -209,20 +219,19 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
   auto wait_warp = [&](int b, uint32_t parity) {
     return ok = __all_sync(0xffffffffu, wait_bar(bar(b), parity, p.sink));
   };
-  ManyWalk walk;
-
   if (warp < 8) {
     // ---------------------------------------------------------------- softmax
     regs_take<kRegsRows>();
     const int st = warp >> 2, row = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    uint32_t s_it = 0, o_it = 0, m_it = 0, k = 0;
+    const int row_tok = row / p.a.group, row_head = row % p.a.group;  // of a tile and of a group
+    uint32_t s_it = 0, o_it = 0, m_it = 0;
     // The row's q into the stream's operand tile (128-byte swizzle): fp16, bf16
     // times a power of two; the factor that its scores get in return.
     auto bring_q = [&](const ManyItem& it) {
-      const int r = row / p.a.group, tok = it.tok0 + st * p.tile_tokens + r;
-      const bool on = r < p.tile_tokens && tok < it.len;
-      const uint16_t* src = p.a.q + (p.a.b.begin[it.seq] + (on ? tok : it.tok0)) * p.a.q_stride + (it.head * p.a.group + row % p.a.group) * D;
+      const int tok = it.tok0 + st * p.tile_tokens + row_tok;
+      const bool on = row_tok < p.tile_tokens && tok < it.len;
+      const uint16_t* src = p.a.q + (it.row0 + (on ? tok : 0)) * p.a.q_stride + (it.head * p.a.group + row_head) * D;
       uint4 v[D / 8];
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) v[i] = on ? __ldg((const uint4*)src + i) : make_uint4(0, 0, 0, 0);
@@ -237,6 +246,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
         up = power(14 - ex);
         factor = p.a.scale2 * power(ex) * 0x1p-14f;
       }
+      uint8_t* dst = smem + st * L::kTile + row * 128;
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) {
         uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
@@ -244,134 +254,126 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
 #pragma unroll
           for (int c = 0; c < 4; ++c) w[c] = half2_of(__uint_as_float(w[c] << 16) * up, __uint_as_float(w[c] & 0xFFFF0000u) * up);
         }
-        *(uint4*)(smem + st * L::kTile + (i / 8) * (kManyRows * 128) + row * 128 + (((i % 8) ^ (row & 7)) << 4)) =
-            make_uint4(w[0], w[1], w[2], w[3]);
+        *(uint4*)(dst + (i / 8) * (kManyRows * 128) + (((i % 8) ^ (row & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::kQFull + st));
       return factor;
     };
-    bool live = !stop && walk.begin(p);
-    float factor = live && walk.it.n[st] > walk.it.from ? bring_q(walk.it) : 0.f;
-    for (; live && ok; ++k) {
-      const ManyItem it = walk.it;
-      const int n = min(it.n[st], it.to) - it.from, all = it.to - it.from;  // this stream's blocks, and the unit's
-      const int tok = it.tok0 + st * p.tile_tokens + row / p.a.group;
-      const bool on = row / p.a.group < p.tile_tokens && tok < it.len;
-      const int pos = p.a.b.start[it.seq] + tok;
-      const int cut = (p.a.b.start[it.seq] + it.tok0 + st * p.tile_tokens) / kManyRows;  // from here on some row does not see all keys
-      float m = -INFINITY, l = 0.f, next_factor = 0.f;
-      for (int j = 0; j < all; ++j, ++m_it) {
+    float factor = 0.f;
+    if (wait_warp(L::kItemFull, 0) && items[0].valid && items[0].here(st) > 0) factor = bring_q(items[0]);
+    for (uint32_t k = 0; ok && items[k & 1].valid; ++k) {
+      const ManyItem& it = items[k & 1];
+      const int n = it.here(st), all = it.to - it.from;  // this stream's blocks, and the unit's
+      const int tile_tok = it.tok0 + st * p.tile_tokens;
+      // what the row sees of the first block, and the first block that some row of the tile does not see all of
+      int seen = it.start + tile_tok + row_tok - it.from * kManyRows;
+      const int cut = (it.start + tile_tok) / kManyRows - it.from;
+      float m = -INFINITY, l = 0.f;
+#pragma unroll 1
+      for (int j = 0; j < all; ++j, ++m_it, seen -= kManyRows) {
         const int mi = m_it % L::kMetas;
+        if (!wait_warp(L::kMetaFull + mi, (m_it / L::kMetas) & 1)) break;
         if (j >= n) {  // the other stream's
-          if (!wait_warp(L::kMetaFull + mi, (m_it / L::kMetas) & 1)) break;
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(L::kMetaEmpty + mi));
           continue;
         }
-        if (!wait_warp(L::kMetaFull + mi, (m_it / L::kMetas) & 1)) break;
         const BlockMeta& meta = metas[mi];
-        const float z = fmaxf(factor * meta.factor, 0x1p-126f), shift = meta.shift, back = meta.back;
+        const float z = fmaxf(factor * meta.factor, 0x1p-126f), shift = meta.shift;
         if (!wait_warp(L::kSFull + st, s_it & 1)) break;
         ++s_it;
         tc_fence_after();
-        // 32 columns at a time; the first of them are read again at the end: all
-        // 128 in registers would leave too few for the warps that convert.
-        const bool masked = it.from + j >= cut;
-        const int seen = pos - (it.from + j) * kManyRows;
-        auto ready = [&](int c, uint32_t* s) {  // scaled and masked
-          if constexpr (kTok) {
+        // 16 columns, scaled and masked; and their largest
+        auto ready = [&](int c, uint32_t* s) {
+          if constexpr (kScale == kScaleOfToken) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float4 f = ((const float4*)meta.k)[8 * c + i];
+            for (int i = 0; i < 4; ++i) {
+              const float4 f = ((const float4*)meta.k)[4 * c + i];
               const float2 x = mul2(make_float2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), make_float2(f.x, f.y));
               const float2 y = mul2(make_float2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), make_float2(f.z, f.w));
               s[4 * i] = __float_as_uint(x.x), s[4 * i + 1] = __float_as_uint(x.y);
               s[4 * i + 2] = __float_as_uint(y.x), s[4 * i + 3] = __float_as_uint(y.y);
             }
           }
-          if (masked) {
+          if (j >= cut) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (32 * c + i > seen) s[i] = __float_as_uint(-INFINITY);
+            for (int i = 0; i < 16; ++i)
+              if (16 * c + i > seen) s[i] = __float_as_uint(-INFINITY);
           }
         };
-        float mx[2] = {-INFINITY, -INFINITY};
+        float mx[2];
         auto largest = [&](const uint32_t* s) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 4) {
+          for (int i = 0; i < 16; i += 4) {
             mx[0] = max3(mx[0], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
             mx[1] = max3(mx[1], __uint_as_float(s[i + 2]), __uint_as_float(s[i + 3]));
           }
         };
-        uint32_t s0[32], s1[32], s2[32], s3[32];
-        tmem_ld32(tS(st) + lanes, s0);
-        tmem_ld_wait();
-        tmem_ld32(tS(st) + lanes + 32, s1);
-        tmem_ld32(tS(st) + lanes + 64, s2);
-        tmem_ld32(tS(st) + lanes + 96, s3);
-        ready(0, s0);
-        largest(s0);
-        tmem_ld_wait();
-        ready(1, s1);
-        largest(s1);
-        ready(2, s2);
-        largest(s2);
-        ready(3, s3);
-        largest(s3);
         // The weights' exponents are those of w times the tile's V scale; their
-        // maximum moves only when one would exceed 2^8 of it: O is rescaled
-        // seldom.  fp16 holds them between 2^7 and 2^15 and down to 2^-25, so
+        // maximum moves only when one would exceed 2^8 of it, so that O is
+        // rescaled seldom and weights are made of S as it is read, with the
+        // maximum of the blocks before; where that was too low they are made
+        // again.  fp16 holds them between 2^7 and 2^15 and down to 2^-25, so
         // that one 2^-32 of the largest is still there.
-        const float top = fmaf(fmaxf(mx[0], mx[1]), z, shift);
         if (j == 0) {
-          m = top;
-        } else {
-          const bool up = top > m + 8.f;
-          if (__any_sync(0xffffffffu, up)) {
-            const float m2 = up ? top : m;
-            const float a = up ? (m == -INFINITY ? 0.f : ex2(m - m2)) : 1.f;
-            l *= a;
-            m = m2;
+          mx[0] = mx[1] = -INFINITY;
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t s[16];
+            tmem_ld16_nowait(tS(st) + lanes + 16 * c, s);
+            tmem_ld_wait();
+            ready(c, s);
+            largest(s);
+          }
+          m = fmaf(fmaxf(mx[0], mx[1]), z, shift);
+        }
+        uint32_t w[64];
+        float2 sum[2];
+#pragma unroll 1
+        while (true) {
+          const float neg = (m == -INFINITY ? 0.f : shift - m) + kManyBias;
+          const float2 z2 = make_float2(z, z), neg2 = make_float2(neg, neg);
+          sum[0] = sum[1] = make_float2(0.f, 0.f);
+          mx[0] = mx[1] = -INFINITY;
+          uint32_t s[2][16];
+          tmem_ld16_nowait(tS(st) + lanes, s[0]);
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t o[32];
-              tmem_ld32(tO(st) + lanes + 32 * c, o);
-              tmem_ld_wait();
+          for (int c = 0; c < 8; ++c) {
+            tmem_ld_wait();
+            if (c < 7) tmem_ld16_nowait(tS(st) + lanes + 16 * (c + 1), s[(c + 1) & 1]);
+            uint32_t* x = s[c & 1];
+            ready(c, x);
+            largest(x);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
-              tmem_st32(tO(st) + lanes + 32 * c, o);
+            for (int i = 0; i < 8; ++i) {
+              const float2 y = fma2(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), z2, neg2);
+              float2 e = make_float2(ex2(y.x), ex2(y.y));
+              sum[i & 1] = add2(sum[i & 1], e);
+              if constexpr (kScale == kScaleOfToken) e = mul2(e, ((const float2*)meta.v)[8 * c + i]);
+              w[8 * c + i] = half2_of(e.x, e.y);
             }
           }
-        }
-        const float neg = (m == -INFINITY ? 0.f : shift - m) + kManyBias;
-        const float2 z2 = make_float2(z, z), neg2 = make_float2(neg, neg);
-        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        uint32_t w[16];
-        auto weights = [&](int c, const uint32_t* s) {
+          const float top = fmaf(fmaxf(mx[0], mx[1]), z, shift);
+          const bool up = top > m + 8.f;
+          if (j == 0 || !__any_sync(0xffffffffu, up)) break;
+          const float a = up ? (m == -INFINITY ? 0.f : ex2(m - top)) : 1.f;
+          l *= a;
+          m = up ? top : m;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tO(st) + lanes + 32 * c, o);
+            tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 x = fma2(make_float2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), z2, neg2);
-            float2 e = make_float2(ex2(x.x), ex2(x.y));
-            sum[i & 1] = add2(sum[i & 1], e);
-            if constexpr (kTok) e = mul2(e, ((const float2*)meta.v)[16 * c + i]);
-            w[i] = half2_of(e.x, e.y);
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
+            tmem_st32(tO(st) + lanes + 32 * c, o);
           }
-        };
-        // P's columns lie over S's first half: its second half first
-        weights(3, s3);
-        tmem_st16(tS(st) + lanes + 48, w);
-        weights(2, s2);
-        tmem_st16(tS(st) + lanes + 32, w);
-        tmem_ld32(tS(st) + lanes, s0);
-        weights(1, s1);
-        tmem_ld_wait();
-        tmem_st16(tS(st) + lanes + 16, w);
-        ready(0, s0);
-        weights(0, s0);
-        tmem_st16(tS(st) + lanes, w);
-        l += ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) * back;
+        }
+        tmem_st32(tS(st) + lanes, w);
+        tmem_st32(tS(st) + lanes + 32, w + 32);
+        l += ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) * meta.back;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -382,19 +384,22 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
       }
       if (!ok) break;
       // the next unit's q, before this one's output is waited for (its last scores are done)
-      live = walk.next(p);
-      if (live && walk.it.n[st] > walk.it.from) next_factor = bring_q(walk.it);
+      if (!wait_warp(L::kItemFull + ((k + 1) & 1), ((k + 1) >> 1) & 1)) break;
+      float next_factor = 0.f;
+      if (items[(k + 1) & 1].valid && items[(k + 1) & 1].here(st) > 0) next_factor = bring_q(items[(k + 1) & 1]);
       if (n > 0) {
         if (!wait_warp(L::kOFull + st, o_it & 1)) break;
         ++o_it;
         tc_fence_after();
         const int4 found = *(const int4*)&odd_unit[(k & 1) * 4];
-        const bool odd = (found.x | found.y | found.z | found.w) != 0;
-        const bool part = !it.whole();
+        const bool odd = (found.x | found.y | found.z | found.w) != 0, part = !it.whole();
+        const int tok = tile_tok + row_tok;
+        const bool on = row_tok < p.tile_tokens && tok < it.len;
         const float inv = 1.f / l;
-        const int head = it.head * p.a.group + row % p.a.group;
-        uint16_t* orow = p.a.out + (p.a.b.begin[it.seq] + (on ? tok : it.tok0)) * p.a.out_stride + head * D;
-#pragma unroll
+        uint16_t* orow = p.a.out + (it.row0 + (on ? tok : 0)) * p.a.out_stride + (it.head * p.a.group + row_head) * D;
+        const size_t at = (size_t)(2 * blockIdx.x + (it.from == 0)) * (2 * kManyRows) + st * kManyRows + row;
+        if (part && on) p.part_ml[at] = make_float2(m, l);
+#pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
           tmem_ld32(tO(st) + lanes + 32 * c, o);
@@ -403,31 +408,29 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               for (int f = 0; f < 4; ++f)
-                if (pos >= bad[((k & 1) * 4 + f) * D + 32 * c + i]) o[i] = 0x7FC00000u;
+                if (it.start + tok >= bad[((k & 1) * 4 + f) * D + 32 * c + i]) o[i] = 0x7FC00000u;
           }
           if (part) {
-            const size_t at = (size_t)(2 * blockIdx.x + (it.from == 0)) * (2 * kManyRows) + st * kManyRows + row;
             if (on) {
 #pragma unroll
               for (int i = 0; i < 4; ++i) store32(p.part_o + at * D + 32 * c + 8 * i, o + 8 * i);
-              if (c == 0) p.part_ml[at] = make_float2(m, l);
             }
           } else if (on) {
-            uint32_t w[16];
+            uint32_t v[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const float2 v = mul2(make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), make_float2(inv, inv));
-              w[i] = kF16 ? half2_of(v.x, v.y) : pair16<__nv_bfloat16>(v.x, v.y);
+              const float2 x = mul2(make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), make_float2(inv, inv));
+              v[i] = kF16 ? half2_of(x.x, x.y) : pair16<__nv_bfloat16>(x.x, x.y);
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               if (p.wide)
-                store32(orow + 32 * c + 16 * i, w + 8 * i);
+                store32(orow + 32 * c + 16 * i, v + 8 * i);
               else
 #pragma unroll
                 for (int f = 0; f < 2; ++f)
                   *(uint4*)(orow + 32 * c + 16 * i + 8 * f) =
-                      make_uint4(w[8 * i + 4 * f], w[8 * i + 4 * f + 1], w[8 * i + 4 * f + 2], w[8 * i + 4 * f + 3]);
+                      make_uint4(v[8 * i + 4 * f], v[8 * i + 4 * f + 1], v[8 * i + 4 * f + 2], v[8 * i + 4 * f + 3]);
             }
           }
           __syncwarp();
@@ -435,37 +438,49 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
         tc_fence_before();
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(L::kBadFree + (k & 1)));
+      if (lane == 0) mbar_arrive(bar(L::kItemEmpty + (k & 1)));
       factor = next_factor;
     }
   } else if (warp < 12) {
     // -------------------------------------------------------- codes to tiles
     regs_give<kRegsCodes>();
-    const int tid = threadIdx.x - 256;
     constexpr int kRowPieces = D / 16, kPieces = kManyRows * kRowPieces / 128;  // 16-byte pieces of a token; a thread's of a tile
-    constexpr int kRowStep = 128 / kRowPieces;
-    const int prow = tid / kRowPieces, pc = tid % kRowPieces;
+    constexpr int kRowStep = 128 / kRowPieces;                                  // rows between them
+    // a thread's row and piece: eight neighbouring lanes take two rows' halves of
+    // 64 values, whose stores meet no bank twice
+    const int prow = (warp - 8) * (kRowStep / 4) + (D == 128 ? (lane >> 2) & 3 : lane >> 2);
+    const int pc = D == 128 ? (lane & 3) | (lane >> 4) << 2 : lane & 3;
+    const uint32_t to = (pc / 4) * (kManyRows * 128) + prow * 128;  // rows are a multiple of 8 apart
+    const uint32_t to0 = to + (((pc % 4 * 2) ^ (prow & 7)) << 4), to1 = to + (((pc % 4 * 2 + 1) ^ (prow & 7)) << 4);
     int* my_bad = bad + (warp - 8) * D;
-    uint32_t tiles = 0, m_it = 0, k = 0;
+    uint32_t tiles = 0, m_it = 0;
     uint4 code[kPieces];
-    float sc[8];  // the block's scales, one block ahead: K's and V's
-    const uint8_t *kc, *vc;
+    float sc[kScale == kScaleOfToken ? 8 : 1];  // the next block's scales
+    const uint8_t *kc, *vc;                     // the thread's piece of the unit's codes
     const float *ks, *vs;
-    int keys;
+    int keys;                                   // what the unit's last row sees
     auto unit = [&](const ManyItem& it) {
-      const size_t kr = p.a.hist.row(0, p.a.b.slot[it.seq], it.head), vr = p.a.hist.row(1, p.a.b.slot[it.seq], it.head);
-      kc = p.a.hist.codes + kr * p.a.hist.T_max * D;
-      vc = p.a.hist.codes + vr * p.a.hist.T_max * D;
+      const int slot = p.a.b.slot[it.seq];
+      const size_t kr = p.a.hist.row(0, slot, it.head), vr = p.a.hist.row(1, slot, it.head);
+      kc = p.a.hist.codes + kr * p.a.hist.T_max * D + prow * D + pc * 16;
+      vc = p.a.hist.codes + vr * p.a.hist.T_max * D + prow * D + pc * 16;
       ks = p.a.hist.scales + kr * p.a.hist.blocks;
       vs = p.a.hist.scales + vr * p.a.hist.blocks;
-      keys = p.a.b.start[it.seq] + min(it.len, it.tok0 + 2 * p.tile_tokens);
+      keys = it.start + min(it.len, it.tok0 + 2 * p.tile_tokens);
     };
-    auto piece = [&](const uint8_t* src, int block, int i) {
-      const int t = block * kManyRows + prow + i * kRowStep;
-      return t < keys ? __ldg((const uint4*)(src + (size_t)t * D + pc * 16)) : make_uint4(0, 0, 0, 0);
+    auto load = [&](const uint8_t* src, int block) {  // of a tile; nothing behind the last key
+      src += (size_t)block * (kManyRows * D);
+      if ((block + 1) * kManyRows <= keys) {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) code[i] = __ldg((const uint4*)(src + i * (kRowStep * D)));
+      } else {
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+          code[i] = block * kManyRows + prow + i * kRowStep < keys ? __ldg((const uint4*)(src + i * (kRowStep * D))) : make_uint4(0, 0, 0, 0);
+      }
     };
     auto scales = [&](int block) {
-      if constexpr (kTok) {
+      if constexpr (kScale == kScaleOfToken) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int t = block * kManyRows + lane * 4 + i;
@@ -473,32 +488,29 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
           sc[4 + i] = t < keys ? __ldg(vs + t) : 0.f;
         }
       } else {  // lanes 0..7 K's, 8..15 V's
-        const int t = block * kManyRows + ((lane & 7) << p.a.hist.shift);
-        sc[0] = lane < 16 && ((lane & 7) << p.a.hist.shift) < kManyRows && t < keys ? __ldg((lane < 8 ? ks : vs) + (t >> p.a.hist.shift)) : 0.f;
+        const int t = (lane & 7) << p.a.hist.shift;
+        sc[0] = lane < 16 && t < kManyRows && block * kManyRows + t < keys ? __ldg((lane < 8 ? ks : vs) + ((block * kManyRows + t) >> p.a.hist.shift)) : 0.f;
       }
     };
-    bool live = !stop && walk.begin(p);
-    if (live) {
-      unit(walk.it);
-#pragma unroll
-      for (int i = 0; i < kPieces; ++i) code[i] = piece(kc, walk.it.from, i);
-      scales(walk.it.from);
+    if (wait_warp(L::kItemFull, 0) && items[0].valid) {
+      unit(items[0]);
+      load(kc, items[0].from);
+      scales(items[0].from);
     }
-    for (; live && ok; ++k) {
-      const ManyItem it = walk.it;
-      const int first_cut = (p.a.b.start[it.seq] + it.tok0) / kManyRows;
-      if (k >= 2) {  // the unit before the last has been written: its list of NaN values is free
-        if (!wait_warp(L::kBadFree + (k & 1), ((k >> 1) - 1) & 1)) break;
-        for (int i = lane; i < D; i += 32) my_bad[(k & 1) * 4 * D + i] = INT32_MAX;
-        if (lane == 0) odd_unit[(k & 1) * 4 + warp - 8] = 0;
-        __syncwarp();
-      }
-      for (int j = it.from; j < it.to && ok; ++j, ++m_it) {
+    for (uint32_t k = 0; ok && items[k & 1].valid; ++k) {
+      const ManyItem& it = items[k & 1];
+      const int first_cut = (it.start + it.tok0) / kManyRows, from = it.from, last = it.to;
+      // the list of NaN values is free: the unit before the last has been written
+      for (int i = lane; i < D; i += 32) my_bad[(k & 1) * 4 * D + i] = INT32_MAX;
+      if (lane == 0) odd_unit[(k & 1) * 4 + warp - 8] = 0;
+      __syncwarp();
+#pragma unroll 1
+      for (int j = from; j < last && ok; ++j, ++m_it) {
         const int mi = m_it % L::kMetas;
         BlockMeta& meta = metas[mi];
-        uint32_t ratio[2];  // kTok: unused; else lane's scale over the tile's, as two fp16
+        uint32_t ratio = 0;  // the lane's scale over the tile's, as two fp16
         if (!wait_warp(L::kMetaEmpty + mi, ((m_it / L::kMetas) & 1) ^ 1)) break;
-        if constexpr (kTok) {
+        if constexpr (kScale == kScaleOfToken) {
           // a V scale that is not finite makes all its token's values NaN
           bool odd = false;
 #pragma unroll
@@ -520,22 +532,31 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
             const float r = power(-e);
             *(float4*)&meta.v[4 * lane] = make_float4(sc[4] * r, sc[5] * r, sc[6] * r, sc[7] * r);
           }
-          if (warp == 10 && lane == 0) meta.factor = 0x1p-6f, meta.shift = (float)e, meta.back = power(-e);
-          ratio[0] = 0x54005400u;  // 2^6
-          ratio[1] = 0x3C003C00u;  // 1
+          if (warp == 10 && lane == 0) meta.factor = 1.f, meta.shift = (float)e, meta.back = power(-e);
         } else {
           float top = sc[0];
+          if constexpr (kScale == kScaleOfBlock) {
 #pragma unroll
-          for (int d = 4; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            for (int d = 4; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+          }
           const int e = top > 0.f ? min(max(exponent_up(top), lane < 8 ? -120 : -100), 120) : -100;
-          const float r = sc[0] * power(-e) * (lane < 8 ? 64.f : 1.f);
-          ratio[0] = half2_of(r, r);
-          const int ek = __shfl_sync(0xffffffffu, e, 0), ev = __shfl_sync(0xffffffffu, e, 8);
-          if (warp == 8 && lane == 0) meta.factor = power(ek) * 0x1p-6f, meta.shift = (float)ev, meta.back = power(-ev);
+          // K's codes have room for 2^6 more in fp16
+          const float r = sc[0] * power(-e) * (kScale == kScaleOfBlock && lane < 8 ? 64.f : 1.f);
+          ratio = half2_of(r, r);
+          const int ev = __shfl_sync(0xffffffffu, e, 8);
+          const float rv = __shfl_sync(0xffffffffu, r, 8);
+          if (warp == 8 && lane == 0) {
+            if constexpr (kScale == kScaleOfBlock) {
+              meta.factor = power(e) * 0x1p-6f, meta.shift = (float)ev, meta.back = power(-ev);
+            } else {  // the scales themselves: a V scale that is no power of two is another factor of the weights
+              meta.factor = sc[0], meta.shift = (float)ev, meta.back = power(-ev);
+            }
+          }
+          if constexpr (kScale == kScaleOfTile) ratio = half2_of(rv, rv);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::kMetaFull + mi));
-#pragma unroll
+#pragma unroll 1
         for (int which = 0; which < 2; ++which, ++tiles) {
           const int slot = tiles % L::kStages;
           if (tiles == (uint32_t)p.skip) {
@@ -544,72 +565,66 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
           }
           if (!wait_warp(L::kEmpty + slot, ((tiles / L::kStages) & 1) ^ 1)) break;
           uint8_t* dst = smem + L::kRing + slot * L::kTile;
-          // the tile behind this one, loaded as this one's registers become free
-          const uint8_t* src = which ? kc : vc;
-          int block = j + which;
-          bool more = true;
-          if (which && j + 1 == it.to) {
-            live = walk.next(p);
-            more = live;
-            if (live) {
-              unit(walk.it);
-              src = kc;
-              block = walk.it.from;
-            }
-          }
           const bool look = which && j >= first_cut;
+          // a product is needed where codes of several scales meet, or the V scale of a block of 128 is no power of two
+          const bool times = kScale == kScaleOfBlock || (kScale == kScaleOfTile && which && ratio != 0x3C003C00u);
           bool odd = false;
 #pragma unroll
           for (int i = 0; i < kPieces; ++i) {
-            const int row = prow + i * kRowStep;
-            uint32_t c[4] = {code[i].x, code[i].y, code[i].z, code[i].w}, h[8];
+            const uint32_t c[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+            uint32_t h[8];
             if (look) {
 #pragma unroll
               for (int x = 0; x < 4; ++x) odd |= (((c[x] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
             }
-            uint32_t r;
-            if constexpr (kTok)
-              r = ratio[which];
-            else
-              r = __shfl_sync(0xffffffffu, ratio[0], (row >> p.a.hist.shift) + 8 * which);
 #pragma unroll
             for (int x = 0; x < 4; ++x) e4m3x4_to_f16x2x2(c[x], h[2 * x], h[2 * x + 1]);
-            if (!kTok || !which) {
+            if (times) {
+              const uint32_t r = kScale == kScaleOfBlock
+                                     ? __shfl_sync(0xffffffffu, ratio, ((prow + i * kRowStep) >> p.a.hist.shift) + 8 * which)
+                                     : ratio;
 #pragma unroll
               for (int x = 0; x < 8; ++x) h[x] = mul_half2(h[x], r);
             }
-            // 16 values: two chunks of a row of 128 bytes; lanes of a row's second half begin with the odd one
-            uint8_t* at = dst + (pc / 4) * (kManyRows * 128) + row * 128;
-            const int c0 = (pc % 4) * 2, flip = pc >> 2;
-            const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-            *(uint4*)(at + (((c0 + flip) ^ (row & 7)) << 4)) = flip ? hi : lo;
-            *(uint4*)(at + (((c0 + (flip ^ 1)) ^ (row & 7)) << 4)) = flip ? lo : hi;
+            *(uint4*)(dst + to0 + i * (kRowStep * 128)) = make_uint4(h[0], h[1], h[2], h[3]);
+            *(uint4*)(dst + to1 + i * (kRowStep * 128)) = make_uint4(h[4], h[5], h[6], h[7]);
           }
-          if (__any_sync(0xffffffffu, odd)) {
+          if (look && __any_sync(0xffffffffu, odd)) {
             // NaN in a tile that some row does not see all of (0 x NaN would
             // reach it): out of the tile, and noted for the rows that do
 #pragma unroll 1
-            for (int i = 0; i < kPieces; ++i) {
-              const int row = prow + i * kRowStep;
+            for (int i = 0; i < kPieces; ++i)
+#pragma unroll 1
               for (int x = 0; x < 16; ++x) {
-                uint16_t* at = (uint16_t*)(dst + (pc / 4) * (kManyRows * 128) + row * 128 + ((((pc % 4) * 2 + x / 8) ^ (row & 7)) << 4)) + x % 8;
+                uint16_t* at = (uint16_t*)(dst + (x < 8 ? to0 : to1) + i * (kRowStep * 128)) + x % 8;
                 if ((*at & 0x7FFF) > 0x7C00) {
                   *at = 0;
-                  atomicMin(&my_bad[(k & 1) * 4 * D + pc * 16 + x], j * kManyRows + row);
+                  atomicMin(&my_bad[(k & 1) * 4 * D + pc * 16 + x], j * kManyRows + prow + i * kRowStep);
                   odd_unit[(k & 1) * 4 + warp - 8] = 1;
                 }
               }
-            }
-          }
-          if (more) {
-#pragma unroll
-            for (int i = 0; i < kPieces; ++i) code[i] = piece(src, block, i);
-            if (which) scales(block);
           }
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(L::kFull + slot));
+          // the tile behind this one
+          if (!which) {
+            load(vc, j);
+          } else if (j + 1 < last) {
+            load(kc, j + 1);
+            scales(j + 1);
+          }
         }
+      }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(L::kItemEmpty + (k & 1)));
+      if (!wait_warp(L::kItemFull + ((k + 1) & 1), ((k + 1) >> 1) & 1)) break;
+      const ManyItem& next = items[(k + 1) & 1];
+      if (next.valid) {
+        unit(next);
+        load(kc, next.from);
+        scales(next.from);
       }
     }
   } else {
@@ -659,11 +674,13 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
         }
         __syncwarp();
       };
-      bool live = !stop && walk.begin(p);
-      while (live && ok) {
-        const int n0 = min(walk.it.n[0], walk.it.to) - walk.it.from, n1 = min(walk.it.n[1], walk.it.to) - walk.it.from;
-        const int nb = max(n0, n1);
-        live = walk.next(p);
+      for (uint32_t k = 0; ok; ++k) {
+        if (!wait_warp(L::kItemFull + (k & 1), (k >> 1) & 1)) break;
+        const bool valid = items[k & 1].valid;
+        const int n0 = items[k & 1].here(0), n1 = items[k & 1].here(1), nb = max(n0, n1);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::kItemEmpty + (k & 1)));
+        if (!valid) break;
         int ks = next_tile();
 #pragma unroll
         for (int st = 0; st < 2; ++st) {
@@ -707,6 +724,21 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
         }
       }
       __syncwarp();
+    } else if (warp == 13) {
+      // ---------------------------------------------------------- scheduler
+      ManyWalk walk;
+      bool live = !stop && walk.begin(p);
+      for (uint32_t k = 0;; ++k) {
+        if (!wait_warp(L::kItemEmpty + (k & 1), ((k >> 1) & 1) ^ 1)) break;
+        if (lane == 0) {
+          walk.it.valid = live;
+          *(ManyItem*)(smem + L::kItems + (k & 1) * sizeof(ManyItem)) = walk.it;
+          mbar_arrive(bar(L::kItemFull + (k & 1)));
+        }
+        __syncwarp();
+        if (!live) break;
+        live = walk.next(p);
+      }
     }
   }
   tc_fence_before();
@@ -790,22 +822,28 @@ static bool cut_line(ManyParams& p, int sms) {
   return any;
 }
 
-template <int D, bool kF16, bool kTok>
+template <int D, bool kF16, int kScale>
 static cudaError_t configure() {
   cudaFuncAttributes a;
-  cudaError_t e = cudaFuncGetAttributes(&a, k_history_many<D, kF16, kTok>);
+  cudaError_t e = cudaFuncGetAttributes(&a, k_history_many<D, kF16, kScale>);
   if (e != cudaSuccess) return e;
   // those that take more registers get them from what the launch had
   if (a.numRegs * kManyThreads < 256 * kRegsRows + 128 * (kRegsCodes + kRegsMma) || kRegsRows < a.numRegs || kRegsCodes > a.numRegs ||
       kRegsMma > a.numRegs)
     return cudaErrorInvalidConfiguration;
-  return cudaFuncSetAttribute(k_history_many<D, kF16, kTok>, cudaFuncAttributeMaxDynamicSharedMemorySize, ManySmem<D>::kTotal);
+  return cudaFuncSetAttribute(k_history_many<D, kF16, kScale>, cudaFuncAttributeMaxDynamicSharedMemorySize, ManySmem<D>::kTotal);
+}
+
+template <int D, bool kF16>
+static cudaError_t configure_all() {
+  const cudaError_t e[3] = {configure<D, kF16, kScaleOfTile>(), configure<D, kF16, kScaleOfBlock>(), configure<D, kF16, kScaleOfToken>()};
+  for (cudaError_t x : e)
+    if (x != cudaSuccess) return x;
+  return cudaSuccess;
 }
 
 cudaError_t configure_history_many() {
-  const cudaError_t e[8] = {configure<128, false, false>(), configure<128, false, true>(), configure<128, true, false>(),
-                            configure<128, true, true>(),   configure<64, false, false>(), configure<64, false, true>(),
-                            configure<64, true, false>(),   configure<64, true, true>()};
+  const cudaError_t e[4] = {configure_all<128, false>(), configure_all<128, true>(), configure_all<64, false>(), configure_all<64, true>()};
   for (cudaError_t x : e)
     if (x != cudaSuccess) return x;
   return cudaSuccess;
@@ -814,9 +852,11 @@ cudaError_t configure_history_many() {
 template <int D, bool kF16>
 static cudaError_t launch(const ManyParams& p, bool join, cudaStream_t st) {
   if (p.a.hist.block == 1)
-    k_history_many<D, kF16, true><<<p.ctas, kManyThreads, ManySmem<D>::kTotal, st>>>(p);
+    k_history_many<D, kF16, kScaleOfToken><<<p.ctas, kManyThreads, ManySmem<D>::kTotal, st>>>(p);
+  else if (p.a.hist.block < kManyRows)
+    k_history_many<D, kF16, kScaleOfBlock><<<p.ctas, kManyThreads, ManySmem<D>::kTotal, st>>>(p);
   else
-    k_history_many<D, kF16, false><<<p.ctas, kManyThreads, ManySmem<D>::kTotal, st>>>(p);
+    k_history_many<D, kF16, kScaleOfTile><<<p.ctas, kManyThreads, ManySmem<D>::kTotal, st>>>(p);
   if (join) k_join_history<D, kF16><<<(p.ctas - 1) * 8, 256, 0, st>>>(p);
   return cudaGetLastError();
 }
