@@ -191,7 +191,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
         mbar_init(bar(L::kPFull + i), 4);
         mbar_init(bar(L::kOFull + i), 1);
         mbar_init(bar(L::kItemFull + i), 1);
-        mbar_init(bar(L::kItemEmpty + i), 13);  // softmax, conversion, MMAs
+        mbar_init(bar(L::kItemEmpty + i), 14);  // softmax, conversion, MMAs, prefetch
       }
       mbar_init(bar(L::kDone), 1);
       fence_mbar_init();
@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
     const uint32_t to0 = to + (((pc % 4 * 2) ^ (prow & 7)) << 4), to1 = to + (((pc % 4 * 2 + 1) ^ (prow & 7)) << 4);
     int* my_bad = bad + (warp - 8) * D;
     uint32_t tiles = 0, m_it = 0;
-    uint4 code[kPieces];
+    uint4 code[2][kPieces];                     // the next K tile and the next V tile
     float sc[kScale == kScaleOfToken ? 8 : 1];  // the next block's scales
     const uint8_t *kc, *vc;                     // the thread's piece of the unit's codes
     const float *ks, *vs;
@@ -468,15 +468,15 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
       vs = p.a.hist.scales + vr * p.a.hist.blocks;
       keys = it.start + min(it.len, it.tok0 + 2 * p.tile_tokens);
     };
-    auto load = [&](const uint8_t* src, int block) {  // of a tile; nothing behind the last key
+    auto load = [&](uint4* c, const uint8_t* src, int block) {  // of a tile; nothing behind the last key
       src += (size_t)block * (kManyRows * D);
       if ((block + 1) * kManyRows <= keys) {
 #pragma unroll
-        for (int i = 0; i < kPieces; ++i) code[i] = __ldg((const uint4*)(src + i * (kRowStep * D)));
+        for (int i = 0; i < kPieces; ++i) c[i] = __ldg((const uint4*)(src + i * (kRowStep * D)));
       } else {
 #pragma unroll
         for (int i = 0; i < kPieces; ++i)
-          code[i] = block * kManyRows + prow + i * kRowStep < keys ? __ldg((const uint4*)(src + i * (kRowStep * D))) : make_uint4(0, 0, 0, 0);
+          c[i] = block * kManyRows + prow + i * kRowStep < keys ? __ldg((const uint4*)(src + i * (kRowStep * D))) : make_uint4(0, 0, 0, 0);
       }
     };
     auto scales = [&](int block) {
@@ -494,8 +494,9 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
     };
     if (wait_warp(L::kItemFull, 0) && items[0].valid) {
       unit(items[0]);
-      load(kc, items[0].from);
+      load(code[0], kc, items[0].from);
       scales(items[0].from);
+      load(code[1], vc, items[0].from);
     }
     for (uint32_t k = 0; ok && items[k & 1].valid; ++k) {
       const ManyItem& it = items[k & 1];
@@ -556,7 +557,11 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::kMetaFull + mi));
-#pragma unroll 1
+        // The tiles behind these are loaded as the registers become free: the
+        // unit's next block, or the first one of the next unit.
+        int ahead = j + 1;
+        bool more = true;
+#pragma unroll
         for (int which = 0; which < 2; ++which, ++tiles) {
           const int slot = tiles % L::kStages;
           if (tiles == (uint32_t)p.skip) {
@@ -571,7 +576,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
           bool odd = false;
 #pragma unroll
           for (int i = 0; i < kPieces; ++i) {
-            const uint32_t c[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+            const uint32_t c[4] = {code[which][i].x, code[which][i].y, code[which][i].z, code[which][i].w};
             uint32_t h[8];
             if (look) {
 #pragma unroll
@@ -607,25 +612,22 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(L::kFull + slot));
-          // the tile behind this one
-          if (!which) {
-            load(vc, j);
-          } else if (j + 1 < last) {
-            load(kc, j + 1);
-            scales(j + 1);
+          if (!which && ahead == last) {
+            if (!wait_warp(L::kItemFull + ((k + 1) & 1), ((k + 1) >> 1) & 1)) break;
+            const ManyItem& next = items[(k + 1) & 1];
+            more = next.valid;
+            if (more) unit(next);
+            ahead = next.from;
+          }
+          if (more) {
+            load(code[which], which ? vc : kc, ahead);
+            if (!which) scales(ahead);
           }
         }
       }
       if (!ok) break;
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::kItemEmpty + (k & 1)));
-      if (!wait_warp(L::kItemFull + ((k + 1) & 1), ((k + 1) >> 1) & 1)) break;
-      const ManyItem& next = items[(k + 1) & 1];
-      if (next.valid) {
-        unit(next);
-        load(kc, next.from);
-        scales(next.from);
-      }
     }
   } else {
     regs_give<kRegsMma>();
@@ -739,6 +741,19 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
         if (!live) break;
         live = walk.next(p);
       }
+    } else if (warp == 14) {
+      // a unit's q on its way to L2 while the unit before is worked on
+      for (uint32_t k = 0;; ++k) {
+        if (!wait_warp(L::kItemFull + (k & 1), (k >> 1) & 1)) break;
+        const ManyItem it = items[k & 1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::kItemEmpty + (k & 1)));
+        if (!it.valid) break;
+        const int tokens = min(2 * p.tile_tokens, it.len - it.tok0), lines = p.a.group * D / 64;  // of 128 bytes, a token
+        const char* q = (const char*)(p.a.q + (it.row0 + it.tok0) * p.a.q_stride + it.head * p.a.group * D);
+        for (int i = lane; i < tokens * lines; i += 32)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(q + (i / lines) * p.a.q_stride * 2 + (i % lines) * 128));
+      }
     }
   }
   tc_fence_before();
@@ -792,12 +807,13 @@ static bool cut_line(ManyParams& p, int sms) {
   const SeqBatch& b = p.a.b;
   const int heads = p.a.hist.heads;
   auto cost = [](const ManyItem& it) { return it.n[1] ? 4 : 3; };
+  constexpr int kUnit = 10;  // what a unit costs beside its blocks
   long long total = 0, most = 3;
   ManyItem it;
   for (it.seq = 0; it.seq < b.n; ++it.seq)
     for (it.level = 0; it.level * 2LL * p.tile_tokens < b.len(it.seq); ++it.level) {
       unit_blocks(b, p.tile_tokens, it);
-      total += (long long)cost(it) * it.blocks() * heads;
+      total += ((long long)cost(it) * it.blocks() + kUnit) * heads;
       most = std::max(most, (long long)cost(it));
     }
   p.ctas = (int)std::max(1LL, std::min((long long)std::min(sms, kMaxCuts), total / (3 * most)));
@@ -807,11 +823,11 @@ static bool cut_line(ManyParams& p, int sms) {
   for (it.seq = 0; it.seq < b.n; ++it.seq)
     for (it.level = 0; it.level * 2LL * p.tile_tokens < b.len(it.seq); ++it.level) {
       unit_blocks(b, p.tile_tokens, it);
-      const long long unit = (long long)cost(it) * it.blocks();
+      const long long unit = (long long)cost(it) * it.blocks() + kUnit;
       for (; c < p.ctas; ++c) {
         const long long at = total * c / p.ctas - before;
         if (at >= unit * heads) break;
-        int block = (int)(at % unit / cost(it));
+        int block = std::min((int)(std::max(at % unit - kUnit, 0LL) / cost(it)), it.blocks() - 1);
         if (block == it.blocks() - 1 && it.n[1] > it.n[0] && block > 0) --block;
         p.cut[c] = {it.seq, it.level, (int)(at / unit), block};
         any |= block > 0;
