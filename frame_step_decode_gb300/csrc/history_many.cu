@@ -285,79 +285,78 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
         if (!wait_warp(L::kSFull + st, s_it & 1)) break;
         ++s_it;
         tc_fence_after();
-        // 16 columns, scaled and masked; and their largest
+        // 32 columns, scaled and masked; and their largest
         auto ready = [&](int c, uint32_t* s) {
           if constexpr (kScale == kScaleOfToken) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float4 f = ((const float4*)meta.k)[4 * c + i];
-              const float2 x = mul2(make_float2(__uint_as_float(s[4 * i]), __uint_as_float(s[4 * i + 1])), make_float2(f.x, f.y));
-              const float2 y = mul2(make_float2(__uint_as_float(s[4 * i + 2]), __uint_as_float(s[4 * i + 3])), make_float2(f.z, f.w));
-              s[4 * i] = __float_as_uint(x.x), s[4 * i + 1] = __float_as_uint(x.y);
-              s[4 * i + 2] = __float_as_uint(y.x), s[4 * i + 3] = __float_as_uint(y.y);
+            for (int i = 0; i < 8; ++i) {
+              const float4 f = ((const float4*)meta.k)[8 * c + i];
+              s[4 * i] = __float_as_uint(__uint_as_float(s[4 * i]) * f.x);
+              s[4 * i + 1] = __float_as_uint(__uint_as_float(s[4 * i + 1]) * f.y);
+              s[4 * i + 2] = __float_as_uint(__uint_as_float(s[4 * i + 2]) * f.z);
+              s[4 * i + 3] = __float_as_uint(__uint_as_float(s[4 * i + 3]) * f.w);
             }
           }
           if (j >= cut) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (16 * c + i > seen) s[i] = __float_as_uint(-INFINITY);
+            for (int i = 0; i < 32; ++i)
+              if (32 * c + i > seen) s[i] = __float_as_uint(-INFINITY);
           }
         };
-        float mx[2];
-        auto largest = [&](const uint32_t* s) {
-#pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            mx[0] = max3(mx[0], __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
-            mx[1] = max3(mx[1], __uint_as_float(s[i + 2]), __uint_as_float(s[i + 3]));
-          }
-        };
-        // The weights' exponents are those of w times the tile's V scale; their
-        // maximum moves only when one would exceed 2^8 of it, so that O is
-        // rescaled seldom and weights are made of S as it is read, with the
-        // maximum of the blocks before; where that was too low they are made
-        // again.  fp16 holds them between 2^7 and 2^15 and down to 2^-25, so
-        // that one 2^-32 of the largest is still there.
-        if (j == 0) {
-          mx[0] = mx[1] = -INFINITY;
+        auto largest = [&]() {
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-          for (int c = 0; c < 8; ++c) {
-            uint32_t s[16];
-            tmem_ld16_nowait(tS(st) + lanes + 16 * c, s);
+          for (int c = 0; c < 4; ++c) {
+            uint32_t s[32];
+            tmem_ld32(tS(st) + lanes + 32 * c, s);
             tmem_ld_wait();
             ready(c, s);
-            largest(s);
-          }
-          m = fmaf(fmaxf(mx[0], mx[1]), z, shift);
-        }
-        uint32_t w[64];
-        float2 sum[2];
-#pragma unroll 1
-        while (true) {
-          const float neg = (m == -INFINITY ? 0.f : shift - m) + kManyBias;
-          const float2 z2 = make_float2(z, z), neg2 = make_float2(neg, neg);
-          sum[0] = sum[1] = make_float2(0.f, 0.f);
-          mx[0] = mx[1] = -INFINITY;
-          uint32_t s[2][16];
-          tmem_ld16_nowait(tS(st) + lanes, s[0]);
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
+            for (int i = 0; i < 32; i += 8)
+#pragma unroll
+              for (int x = 0; x < 4; ++x) mx[x] = max3(mx[x], __uint_as_float(s[i + 2 * x]), __uint_as_float(s[i + 2 * x + 1]));
+          }
+          return fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), z, shift);
+        };
+        // The weights' exponents are those of w times the tile's V scale.  What
+        // they are relative to moves only when the weights of a row's block add
+        // up to more than fp16 holds, so that O is rescaled seldom and weights
+        // are made of S as it is read, with the maximum of the blocks before;
+        // where that was too low they are made again.  The largest is then
+        // between 2^7 and 2^16 and fp16 goes down to 2^-25, so that one 2^-32 of
+        // it is still there.  (One fp32 product at a time: with packed ones the
+        // loop takes 1290 cycles instead of 740 for a warp alone.)
+        if (j == 0) m = largest();
+        uint32_t w[64];
+        float2 sum[4];
+#pragma unroll 1
+        for (bool again = false;; again = true) {
+          const float neg = (m == -INFINITY ? 0.f : shift - m) + kManyBias;
+          sum[0] = sum[1] = sum[2] = sum[3] = make_float2(0.f, 0.f);
+          uint32_t s[2][32];
+          tmem_ld32(tS(st) + lanes, s[0]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
             tmem_ld_wait();
-            if (c < 7) tmem_ld16_nowait(tS(st) + lanes + 16 * (c + 1), s[(c + 1) & 1]);
+            if (c < 3) tmem_ld32(tS(st) + lanes + 32 * (c + 1), s[(c + 1) & 1]);
             uint32_t* x = s[c & 1];
             ready(c, x);
-            largest(x);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float2 y = fma2(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), z2, neg2);
-              float2 e = make_float2(ex2(y.x), ex2(y.y));
-              sum[i & 1] = add2(sum[i & 1], e);
-              if constexpr (kScale == kScaleOfToken) e = mul2(e, ((const float2*)meta.v)[8 * c + i]);
-              w[8 * c + i] = half2_of(e.x, e.y);
+            for (int i = 0; i < 16; ++i) {
+              float2 e = make_float2(ex2(fmaf(__uint_as_float(x[2 * i]), z, neg)), ex2(fmaf(__uint_as_float(x[2 * i + 1]), z, neg)));
+              sum[i & 3] = add2(sum[i & 3], e);
+              if constexpr (kScale == kScaleOfToken) {
+                const float2 v = ((const float2*)meta.v)[16 * c + i];
+                e = make_float2(e.x * v.x, e.y * v.y);
+              }
+              w[16 * c + i] = half2_of(e.x, e.y);
             }
           }
-          const float top = fmaf(fmaxf(mx[0], mx[1]), z, shift);
-          const bool up = top > m + 8.f;
-          if (j == 0 || !__any_sync(0xffffffffu, up)) break;
+          sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+          sum[0].x += sum[0].y;
+          if (j == 0 || again || !__any_sync(0xffffffffu, !(sum[0].x <= 60000.f))) break;
+          const float top = largest();
+          const bool up = top > m;
           const float a = up ? (m == -INFINITY ? 0.f : ex2(m - top)) : 1.f;
           l *= a;
           m = up ? top : m;
@@ -373,7 +372,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
         }
         tmem_st32(tS(st) + lanes, w);
         tmem_st32(tS(st) + lanes + 32, w + 32);
-        l += ((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y)) * meta.back;
+        l += sum[0].x * meta.back;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -692,10 +691,10 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
         }
         if (!ok) break;
         commit(L::kEmpty + ks);
-        int vsl = next_tile();
         for (int j = 0; j < nb && ok; ++j) {
           const bool more = j + 1 < nb;
-          int vnext = 0;
+          const int vsl = next_tile();
+          if (!ok) break;
 #pragma unroll
           for (int st = 0; st < 2; ++st) {
             const int n = st ? n1 : n0;
@@ -711,13 +710,8 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
               scores(st, ks);
             else if (j + 1 == n)
               commit(L::kOFull + st);
-            if (st == 0 && more) {
-              vnext = next_tile();
-              if (!ok) break;
-            }
           }
           if (ok && more) commit(L::kEmpty + ks);
-          vsl = vnext;
         }
       }
       if (!ok) {  // give-up: wait (bounded) for the MMAs issued so far
