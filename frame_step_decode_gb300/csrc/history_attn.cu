@@ -9,6 +9,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "../../include/wave.h"
 #include "history_attn.h"
 
@@ -67,7 +69,9 @@ static int attention(wave_t* h, HistoryAttnParams& p, int tokens, int type, cons
   p.part = h->ws.part_o;
   p.part_cnt = h->ws.hist_cnt;
   if (p.n) {
-    const cudaError_t e = launch_history_few(p, D, type, h->pl.grid, st);
+    int rows = p.group;
+    for (int i = 0; i < p.b.n; ++i) rows = std::max(rows, p.b.len(i) * p.group);
+    const cudaError_t e = launch_history_few(p, D, type, rows, h->pl.grid, st);
     if (e != cudaSuccess) return WAVE_ECUDA;
   }
   if (many.b.n && launch_history_many(many, h, type, st) != cudaSuccess) return WAVE_ECUDA;

@@ -14,18 +14,19 @@ struct HistoryAttnParams {
   int n;                     // sequences, or rows of the frame
   History hist;
   int heads, group;
+  int tiles;                 // few rows: of a K/V head's rows
   const uint16_t* q;
   uint16_t* out;
   long long q_stride, out_stride;
   float scale2;              // scale * log2(e)
-  float* part;               // sums of units that several CTAs share, ...
-  int* part_cnt;             // ... and how many have left theirs (0 between launches)
+  float* part;               // few rows: sums of units that several warps or CTAs share, ...
+  int* part_cnt;             // ... and how many CTAs have left theirs, for each fourth of a unit's rows (0 between launches)
   int *err, *err_out;
 };
 
 constexpr int kFewRows = 16;  // rows (tokens times heads of a group) of one unit of few rows
 
-cudaError_t launch_history_few(const HistoryAttnParams& p, int D, int type, int sms, cudaStream_t st);
+cudaError_t launch_history_few(HistoryAttnParams& p, int D, int type, int rows, int sms, cudaStream_t st);
 
 cudaError_t launch_history_many(const HistoryAttnParams& p, const wave_ctx* h, int type, cudaStream_t st);
 

@@ -9,16 +9,17 @@
 // is joined in shared memory, in several CTAs by the last of them to finish.
 //
 // A chunk's codes are brought into the warp's own ring by cp.async (tokens
-// that no row sees as zeros) and become operands of mma.sync in registers:
-// S = Q K^T with Q's 16 rows as A and eight tokens as B's columns, O += P V with
-// S's registers as A.  The order of a product's inner index is free as long as
-// both operands have it, so that K needs no shuffle: lane (g, t) takes 16
-// bytes of token g, four to an MMA.  V's pairs of tokens are made by byte
-// permutes.  The maxima move only when a weight would exceed 2^8 of them.  A
-// code is an exact f16; the weights, times the V scale of their token, are held
-// in f16 between 2^7 and 2^15 of the largest, so that one 2^-31 of it is still
-// there.  bf16 queries are brought to f16 by a power of two for each row, which
-// loses nothing above 2^-29 of the row's largest value.
+// that no row sees as zeros) and become operands of mma.sync in registers, as A
+// (16 tokens, or 16 dims), so that eight rows are B's columns and 9 to 16 rows
+// two products: S^T = K Q^T, O^T += V^T P^T.  The order of a product's inner
+// index is free as long as both operands have it, so that K needs no shuffle:
+// lane (g, t) takes 16 bytes of token g, four to an MMA.  V's pairs of tokens
+// are made by byte permutes, P is transposed by movmatrix.  The maxima move only
+// when a weight would exceed 2^8 of them.  A code is an exact f16; the weights,
+// times the V scale of their token, are held in f16 between 2^7 and 2^15 of the
+// largest, so that one 2^-31 of it is still there.  bf16 queries are brought to
+// f16 by a power of two for each row, which loses nothing above 2^-29 of the
+// row's largest value.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -28,19 +29,24 @@ using namespace wave;
 
 namespace wave {
 
-constexpr int kFewWarps = 8, kFewThreads = kFewWarps * 32, kFewChunk = 16;
+constexpr int kFewChunk = 16;
 constexpr float kFewBias = 7.f;  // the largest weight is held as 2^7
 
-template <int D>
-struct FewSmem {
-  static constexpr int kStages = 4;
-  static constexpr int kCodes = kFewChunk * D;       // of K, and of V
+// kN: groups of eight rows.  Two take twice the registers: half as many warps.
+template <int D, int kN>
+struct FewShape {
+  static constexpr int kWarps = kN == 1 ? 16 : 8, kThreads = kWarps * 32, kRows = 8 * kN;
+  static constexpr int kStages = kN == 1 ? 3 : 6;
+  static constexpr int kCodes = kFewChunk * D;  // of K, and of V
   static constexpr int kStage = 2 * kCodes + 2 * kFewChunk * 4;
-  static constexpr int kRing = kStages * kStage;     // of a warp
-  static constexpr int kSums = kFewRows * (D + 2) * 4;
-  static_assert(kSums <= kRing, "a warp leaves its last unit's sums in its ring");
-  static constexpr int kFirst = kFewWarps * kRing;   // the warps' first units' sums
-  static constexpr int kTotal = kFirst + kFewWarps * kSums;
+  static constexpr int kRing = kStages * kStage;  // of a warp
+  static constexpr int kSums = kRows * (D + 2);   // floats: a unit's sums, then the rows' maxima and sums of weights
+  static_assert(kSums * 4 <= kRing, "a warp leaves its last unit's sums in its ring");
+  static constexpr int kTotal = kWarps * kRing;
+  // Of the workspace, for each CTA: two units that other CTAs have a part of,
+  // and the warps' first units where another warp has a part.
+  static constexpr int kPart = (2 + kWarps) * kSums;
+  static_assert(kPart <= 2 * 256 * D, "the workspace of a CTA");
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool there) {
@@ -59,6 +65,11 @@ __device__ __forceinline__ float lg2(float x) {
   asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {  // an 8 x 8 tile of 16-bit values
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
 __device__ __forceinline__ bool any_nan_code(uint32_t w) { return (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0; }
 
 // Where a chunk of the line lies.
@@ -72,10 +83,6 @@ struct FewTables {
   int first[WAVE_MAX_SEQS + 1];  // chunks before sequence i
   int keys[WAVE_MAX_SEQS];       // what its last token sees
 };
-
-__device__ __forceinline__ int row_tiles(const HistoryAttnParams& p, int seq) {
-  return ((p.positions ? 1 : p.b.len(seq)) * p.group + kFewRows - 1) / kFewRows;
-}
 
 __device__ __forceinline__ FewPlace place_of(const HistoryAttnParams& p, const FewTables& tab, int at) {
   int lo = 0, hi = p.n - 1;
@@ -99,7 +106,7 @@ __device__ __forceinline__ FewPlace place_of(const HistoryAttnParams& p, const F
 __device__ __forceinline__ void advance(const HistoryAttnParams& p, const FewTables& tab, FewPlace& w) {
   if (++w.chunk < w.chunks) return;
   w.chunk = 0;
-  if (++w.unit < p.hist.heads * row_tiles(p, w.seq)) return;
+  if (++w.unit < p.hist.heads * p.tiles) return;
   w.unit = 0;
   do ++w.seq;
   while (tab.keys[w.seq] == 0);
@@ -107,15 +114,16 @@ __device__ __forceinline__ void advance(const HistoryAttnParams& p, const FewTab
   w.chunks = (w.keys + kFewChunk - 1) / kFewChunk;
 }
 
-// A unit's row r (0..15 of the tile): whether there is one, and the row of q
+// A unit's row r (of the tile): whether there is one, and the row of q
 // and out and the head that it is.
 struct FewRow {
   bool on;
   int head, keys;
   long long row;
 };
+template <int kR>
 __device__ __forceinline__ FewRow row_of(const HistoryAttnParams& p, const FewPlace& w, int r) {
-  const int tiles = row_tiles(p, w.seq), head = w.unit / tiles, i = (w.unit - head * tiles) * kFewRows + r;
+  const int head = w.unit / p.tiles, i = (w.unit - head * p.tiles) * kR + r;
   const int t = i / p.group, len = p.positions ? 1 : p.b.len(w.seq);
   FewRow x;
   x.on = t < len;
@@ -125,26 +133,25 @@ __device__ __forceinline__ FewRow row_of(const HistoryAttnParams& p, const FewPl
   return x;
 }
 
-// Sums of a unit in shared memory: [16 rows][D], then the rows' maxima and
-// sums of weights.  The four values of a row that a lane writes together are
-// moved about so that lanes do not meet in a bank.
+// Where four of a row's sums are among a unit's: moved about so that lanes meet
+// less in a bank.
 template <int D>
 __device__ __forceinline__ int sums_at(int row, int quad) {
-  constexpr int kQuads = D / 16;  // of a lane
-  const int t = quad / kQuads, k = quad % kQuads;
-  return row * (D / 4) + t * kQuads + (k ^ ((2 * t + (row & 1)) & (kQuads - 1)));
+  return row * (D / 4) + (quad ^ (row & 7));
 }
 
-template <int D, bool kF16>
-__global__ void __launch_bounds__(kFewThreads, 1) k_history_few(const __grid_constant__ HistoryAttnParams p) {
-  using L = FewSmem<D>;
+template <int D, bool kF16, int kN>
+__global__ void __launch_bounds__((FewShape<D, kN>::kThreads), 1) k_history_few(const __grid_constant__ HistoryAttnParams p) {
+  using L = FewShape<D, kN>;
+  constexpr int kWarps = L::kWarps, kR = L::kRows;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ FewTables tab;
   __shared__ int scan[WAVE_MAX_SEQS / 32];
   // a warp's units that others have a part of: [0] the one that it goes on with, [1] the one that it leaves unfinished
-  __shared__ FewPlace open[kFewWarps][2];
-  __shared__ int is_open[kFewWarps][2], last_cta;
+  __shared__ FewPlace open[kWarps][2];
+  __shared__ int is_open[kWarps][2];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  float* part = p.part + (size_t)blockIdx.x * L::kPart;
 
   // the line: sequences' chunks
   if (threadIdx.x < WAVE_MAX_SEQS) {
@@ -157,7 +164,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_history_few(const __grid_con
         const int pos = p.positions[s];
         keys = pos < 0 ? 0 : pos >= p.hist.T_max ? -1 : pos + 1;
       }
-      if (keys > 0) mine = (keys + kFewChunk - 1) / kFewChunk * p.hist.heads * row_tiles(p, s);
+      if (keys > 0) mine = (keys + kFewChunk - 1) / kFewChunk * p.hist.heads * p.tiles;
     }
     int sum = mine;
 #pragma unroll
@@ -174,7 +181,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_history_few(const __grid_con
       for (int i = 0; i < p.heads * D / 8; ++i) *(uint4*)(p.out + s * p.out_stride + i * 8) = make_uint4(0, 0, 0, 0);
     }
   }
-  if (threadIdx.x < 2 * kFewWarps) is_open[threadIdx.x >> 1][threadIdx.x & 1] = 0;
+  if (threadIdx.x < 2 * kWarps) is_open[threadIdx.x >> 1][threadIdx.x & 1] = 0;
   if (threadIdx.x == 0) tab.first[0] = 0;
   __syncthreads();
   if (threadIdx.x < WAVE_MAX_SEQS) {
@@ -186,10 +193,10 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_history_few(const __grid_con
   const int total = tab.first[p.n];
   if (total == 0) return;
   // CTAs: no more than there are chunks for their warps
-  const int ctas = min((int)gridDim.x, (total + kFewWarps - 1) / kFewWarps);
+  const int ctas = min((int)gridDim.x, (total + kWarps - 1) / kWarps);
   if ((int)blockIdx.x >= ctas) return;
-  const int w = blockIdx.x * kFewWarps + warp;
-  const int begin = (int)((long long)total * w / (ctas * kFewWarps)), end = (int)((long long)total * (w + 1) / (ctas * kFewWarps));
+  const int w = blockIdx.x * kWarps + warp;
+  const int begin = (int)((long long)total * w / (ctas * kWarps)), end = (int)((long long)total * (w + 1) / (ctas * kWarps));
 
   const uint32_t ring = smem_u32(smem) + warp * L::kRing;
   uint8_t* ring_p = smem + warp * L::kRing;
@@ -201,7 +208,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_history_few(const __grid_con
     const uint8_t *kc = nullptr, *vc = nullptr;
     const float *ks = nullptr, *vs = nullptr;
     auto unit_pointers = [&]() {
-      const int slot = p.positions ? in.seq : p.b.slot[in.seq], head = in.unit / row_tiles(p, in.seq);
+      const int slot = p.positions ? in.seq : p.b.slot[in.seq], head = in.unit / p.tiles;
       const size_t kr = p.hist.row(0, slot, head), vr = p.hist.row(1, slot, head);
       kc = p.hist.codes + kr * p.hist.T_max * D;
       vc = p.hist.codes + vr * p.hist.T_max * D;
@@ -237,43 +244,47 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_history_few(const __grid_con
         if (++issued < end) {
           const int unit = in.unit, seq = in.seq;
           advance(p, tab, in);
-          if (in.unit != unit || in.seq != seq) unit_pointers();
+          if (in.unit != unit || in.seq != seq) {
+            unit_pointers();
+            // its queries, on their way to L1 while the unit at hand is worked on
+#pragma unroll
+            for (int b = 0; b < kN; ++b) {
+              const FewRow r = row_of<kR>(p, in, 8 * b + g);
+              if (r.on && t < kH)
+                asm volatile("prefetch.global.L1 [%0];" ::"l"(p.q + r.row * p.q_stride + r.head * D + t * 64));
+            }
+          }
         }
         if (++slot_in == L::kStages) slot_in = 0;
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
-#pragma unroll
+#pragma unroll 1
     for (int i = 0; i < L::kStages - 1; ++i) issue();
 
     // ---- the unit at hand
     FewPlace at = place_of(p, tab, begin);
-    uint32_t qa[kH * 4][4];
-    float acc[D / 8][4], m[2], e[2], l[2], rf[2];
-    int limit[2];
+    uint32_t qb[kN][kH * 4][2];
+    float acc[kN][D / 16][4], m[kN][2], e[kN][2], l[kN][2], rf[kN][2];  // of rows 2t, 2t + 1 of each eight
+    int limit[kN][2];
     auto begin_unit = [&]() {
-      uint4 raw[2][kH][2];
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const FewRow r = row_of(p, at, g + 8 * x);
-        limit[x] = r.keys;
+      for (int b = 0; b < kN; ++b) {
+        const FewRow r = row_of<kR>(p, at, 8 * b + g);
         const uint16_t* src = p.q + r.row * p.q_stride + r.head * D + t * 16;
+        uint4 raw[kH][2];
 #pragma unroll
         for (int h = 0; h < kH; ++h)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) raw[x][h][i] = r.on ? __ldg((const uint4*)(src + h * 64 + i * 8)) : make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        rf[x] = p.scale2;
-        float up = 1.f;
+          for (int i = 0; i < 2; ++i) raw[h][i] = r.on ? __ldg((const uint4*)(src + h * 64 + i * 8)) : make_uint4(0, 0, 0, 0);
+        float factor = p.scale2, up = 1.f;
         if constexpr (!kF16) {
           uint32_t top = 0;  // the largest magnitude: bf16 bits compare as integers
 #pragma unroll
           for (int h = 0; h < kH; ++h)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const uint4 v = raw[x][h][i];
+              const uint4 v = raw[h][i];
               top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
             }
           top = max(top & 0xFFFFu, top >> 16);
@@ -281,73 +292,75 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_history_few(const __grid_con
           top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
           const int ex = min(max((int)(top >> 7) - 127, -113), 127);  // its exponent
           up = __int_as_float((14 - ex + 127) << 23);
-          rf[x] = p.scale2 * __int_as_float((ex + 127) << 23) * 0x1p-14f;
+          factor = p.scale2 * __int_as_float((ex + 127) << 23) * 0x1p-14f;
         }
 #pragma unroll
         for (int h = 0; h < kH; ++h)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const uint32_t v[4] = {raw[x][h][i].x, raw[x][h][i].y, raw[x][h][i].z, raw[x][h][i].w};
+            const uint32_t v[4] = {raw[h][i].x, raw[h][i].y, raw[h][i].z, raw[h][i].w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               uint32_t z = v[k];
               if constexpr (!kF16) z = half2_of(__uint_as_float(z << 16) * up, __uint_as_float(z & 0xFFFF0000u) * up);
               // word k of 16 bytes: values 2k, 2k + 1 of eight; an MMA takes four values of a lane
-              qa[h * 4 + i * 2 + (k >> 1)][(k & 1) * 2 + x] = z;
+              qb[b][h * 4 + i * 2 + (k >> 1)][k & 1] = z;
             }
           }
-        m[x] = e[x] = -INFINITY;
-        l[x] = 0.f;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          rf[b][x] = __shfl_sync(0xffffffffu, factor, 4 * (2 * t + x));
+          limit[b][x] = __shfl_sync(0xffffffffu, r.keys, 4 * (2 * t + x));
+          m[b][x] = e[b][x] = -INFINITY;
+          l[b][x] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[b][j][k] = 0.f;
       }
+    };
+    auto weights_of = [&](float sum) {  // over the lanes of a row
 #pragma unroll
-      for (int j = 0; j < D / 8; ++j)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) acc[j][k] = 0.f;
+      for (int d = 4; d <= 16; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      return sum;
     };
     // The unit's rows as sums that others join: divided by nothing, relative to the maxima m.
     auto leave_sums = [&](float* dst) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        float sum = l[x];
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        const float f = e[x] == -INFINITY ? 0.f : ex2(e[x] - m[x] - kFewBias);
-        const int row = g + 8 * x;
+      for (int b = 0; b < kN; ++b)
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          float v[4];
+        for (int x = 0; x < 2; ++x) {
+          const float sum = weights_of(l[b][x]), f = e[b][x] == -INFINITY ? 0.f : ex2(e[b][x] - m[b][x] - kFewBias);
+          const int row = 8 * b + 2 * t + x;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int d = 4 * k + i;  // of the lane's D / 4 values
-            v[i] = f * acc[d % (D / 8)][2 * x + d / (D / 8)];
-          }
-          *(float4*)(dst + 4 * sums_at<D>(row, t * (D / 16) + k)) = make_float4(v[0], v[1], v[2], v[3]);
+          for (int k = 0; k < D / 32; ++k)
+            *(float4*)(dst + 4 * sums_at<D>(row, g * (D / 32) + k)) = make_float4(f * acc[b][2 * k][x], f * acc[b][2 * k][2 + x],
+                                                                                f * acc[b][2 * k + 1][x], f * acc[b][2 * k + 1][2 + x]);
+          if (g == 0) *(float2*)(dst + kR * D + 2 * row) = make_float2(m[b][x], sum);
         }
-        if (t == 0) *(float2*)(dst + kFewRows * D + 2 * row) = make_float2(m[x], sum);
-      }
     };
     auto finish_unit = [&]() {
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const FewRow r = row_of(p, at, g + 8 * x);
-        float sum = l[x];
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        if (!r.on) continue;
-        const float f = e[x] == -INFINITY ? 0.f : ex2(e[x] - m[x] - kFewBias), inv = f / sum;
-        uint16_t* dst = p.out + r.row * p.out_stride + r.head * D + t * (D / 4);
+      for (int b = 0; b < kN; ++b)
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k) {
-          uint32_t o[4];
+        for (int x = 0; x < 2; ++x) {
+          const FewRow r = row_of<kR>(p, at, 8 * b + 2 * t + x);
+          const float sum = weights_of(l[b][x]);
+          if (!r.on) continue;
+          const float f = e[b][x] == -INFINITY ? 0.f : ex2(e[b][x] - m[b][x] - kFewBias), inv = f / sum;
+          uint16_t* dst = p.out + r.row * p.out_stride + r.head * D + g * (D / 8);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int d = 8 * k + 2 * i;
-            const float a = acc[d % (D / 8)][2 * x + d / (D / 8)] * inv, b = acc[(d + 1) % (D / 8)][2 * x + d / (D / 8)] * inv;
-            o[i] = kF16 ? pair16<__half>(a, b) : pair16<__nv_bfloat16>(a, b);
+          for (int k = 0; k < D / 64; ++k) {
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float u = acc[b][4 * k + i][x] * inv, v = acc[b][4 * k + i][2 + x] * inv;
+              o[i] = kF16 ? pair16<__half>(u, v) : pair16<__nv_bfloat16>(u, v);
+            }
+            *(uint4*)(dst + 8 * k) = make_uint4(o[0], o[1], o[2], o[3]);
           }
-          *(uint4*)(dst + 8 * k) = make_uint4(o[0], o[1], o[2], o[3]);
         }
-      }
     };
 
     int slot = 0;
@@ -365,85 +378,79 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_history_few(const __grid_con
       if (++slot == L::kStages) slot = 0;
       const float* sc = (const float*)(st + 2 * L::kCodes);
 
-      float s[2][4] = {};
+      float s[kN][4] = {};
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int h = 0; h < kH; ++h) {
+        const int off = D == 128 ? g * 128 + (((t + 4 * h) ^ (4 * (g & 1))) << 4) : g * 64 + (t << 4);
+        const uint4 lo = *(const uint4*)(st + off), hi = *(const uint4*)(st + off + 8 * D);  // tokens g and g + 8
+        const uint32_t lw[4] = {lo.x, lo.y, lo.z, lo.w}, hw[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-        for (int h = 0; h < kH; ++h) {
-          const int row = 8 * i + g;
-          const uint4 k4 = *(const uint4*)(st + (D == 128 ? row * 128 + (((t + 4 * h) ^ (4 * (row & 1))) << 4) : row * 64 + (t << 4)));
-          const uint32_t kw[4] = {k4.x, k4.y, k4.z, k4.w};
+        for (int j = 0; j < 4; ++j) {
+          uint32_t a0, a1, a2, a3;
+          e4m3x4_to_f16x2x2(lw[j], a0, a2);
+          e4m3x4_to_f16x2x2(hw[j], a1, a3);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t b0, b1;
-            e4m3x4_to_f16x2x2(kw[j], b0, b1);
-            mma_f16_16816(s[i], qa[h * 4 + j][0], qa[h * 4 + j][1], qa[h * 4 + j][2], qa[h * 4 + j][3], b0, b1);
-          }
+          for (int b = 0; b < kN; ++b) mma_f16_16816(s[b], a0, a1, a2, a3, qb[b][h * 4 + j][0], qb[b][h * 4 + j][1]);
         }
       }
-      float lv[4];
+      const float k0 = sc[g], k1 = sc[g + 8], lv0 = lg2(sc[16 + g]), lv1 = lg2(sc[24 + g]);
+      const int t0 = at.chunk * kFewChunk;
+      const bool cut = __any_sync(0xffffffffu, t0 + kFewChunk > limit[0][0]);  // some row does not see all of the chunk
+      float top[kN][2], etop[kN][2];
+      bool up = false;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float2 k2 = *(const float2*)(sc + 8 * i + 2 * t), v2 = *(const float2*)(sc + 16 + 8 * i + 2 * t);
-        lv[2 * i] = lg2(v2.x);
-        lv[2 * i + 1] = lg2(v2.y);
+      for (int b = 0; b < kN; ++b)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          s[i][2 * x] *= k2.x * rf[x];
-          s[i][2 * x + 1] *= k2.y * rf[x];
+          s[b][x] *= k0 * rf[b][x];
+          s[b][2 + x] *= k1 * rf[b][x];
+          if (cut) {
+            if (t0 + g >= limit[b][x]) s[b][x] = -INFINITY;
+            if (t0 + g + 8 >= limit[b][x]) s[b][2 + x] = -INFINITY;
+          }
+          top[b][x] = fmaxf(s[b][x], s[b][2 + x]);
+          etop[b][x] = fmaxf(s[b][x] + lv0, s[b][2 + x] + lv1);
+          up |= top[b][x] > m[b][x] + 8.f || etop[b][x] > e[b][x] + 8.f;
         }
-      }
-      const int t0 = at.chunk * kFewChunk;
-      const bool cut = __any_sync(0xffffffffu, t0 + kFewChunk > limit[0]);  // some row does not see all of the chunk
-      if (cut) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (t0 + 8 * i + 2 * t + (k & 1) >= limit[k >> 1]) s[i][k] = -INFINITY;
-      }
-      float top[2], etop[2];
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        top[x] = fmaxf(fmaxf(s[0][2 * x], s[0][2 * x + 1]), fmaxf(s[1][2 * x], s[1][2 * x + 1]));
-        etop[x] = fmaxf(fmaxf(s[0][2 * x] + lv[0], s[0][2 * x + 1] + lv[1]), fmaxf(s[1][2 * x] + lv[2], s[1][2 * x + 1] + lv[3]));
-      }
-      const bool up = top[0] > m[0] + 8.f || top[1] > m[1] + 8.f || etop[0] > e[0] + 8.f || etop[1] > e[1] + 8.f;
       if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
+        for (int b = 0; b < kN; ++b)
 #pragma unroll
-          for (int d = 1; d <= 2; d <<= 1) {
-            top[x] = fmaxf(top[x], __shfl_xor_sync(0xffffffffu, top[x], d));
-            etop[x] = fmaxf(etop[x], __shfl_xor_sync(0xffffffffu, etop[x], d));
-          }
-          const float m2 = fmaxf(m[x], top[x]), e2 = fmaxf(e[x], etop[x]);
-          l[x] *= m[x] == -INFINITY ? 0.f : ex2(m[x] - m2);
-          const float a = e[x] == -INFINITY ? 0.f : ex2(e[x] - e2);
-          m[x] = m2;
-          e[x] = e2;
+          for (int x = 0; x < 2; ++x) {
 #pragma unroll
-          for (int j = 0; j < D / 8; ++j) {
-            acc[j][2 * x] *= a;
-            acc[j][2 * x + 1] *= a;
+            for (int d = 4; d <= 16; d <<= 1) {
+              top[b][x] = fmaxf(top[b][x], __shfl_xor_sync(0xffffffffu, top[b][x], d));
+              etop[b][x] = fmaxf(etop[b][x], __shfl_xor_sync(0xffffffffu, etop[b][x], d));
+            }
+            const float m2 = fmaxf(m[b][x], top[b][x]), e2 = fmaxf(e[b][x], etop[b][x]);
+            l[b][x] *= m[b][x] == -INFINITY ? 0.f : ex2(m[b][x] - m2);
+            const float a = e[b][x] == -INFINITY ? 0.f : ex2(e[b][x] - e2);
+            m[b][x] = m2;
+            e[b][x] = e2;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+              acc[b][j][x] *= a;
+              acc[b][j][2 + x] *= a;
+            }
           }
-        }
       }
-      uint32_t pa[4];
+      uint32_t pb[kN][2];
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const float mm = m[x] == -INFINITY ? 0.f : m[x], ee = (e[x] == -INFINITY ? 0.f : e[x]) - kFewBias;
+      for (int b = 0; b < kN; ++b) {
+        float wt[4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float a = s[i][2 * x], b = s[i][2 * x + 1];
-          l[x] += ex2(a - mm) + ex2(b - mm);
-          float wa = ex2(a + (lv[2 * i] - ee)), wb = ex2(b + (lv[2 * i + 1] - ee));
+        for (int x = 0; x < 2; ++x) {
+          const float mm = m[b][x] == -INFINITY ? 0.f : m[b][x], ee = (e[b][x] == -INFINITY ? 0.f : e[b][x]) - kFewBias;
+          l[b][x] += ex2(s[b][x] - mm) + ex2(s[b][2 + x] - mm);
+          wt[x] = ex2(s[b][x] + (lv0 - ee));
+          wt[2 + x] = ex2(s[b][2 + x] + (lv1 - ee));
           if (cut) {  // a scale behind a row's end counts for nothing there, whatever it is
-            wa = a == -INFINITY ? 0.f : wa;
-            wb = b == -INFINITY ? 0.f : wb;
+            wt[x] = s[b][x] == -INFINITY ? 0.f : wt[x];
+            wt[2 + x] = s[b][2 + x] == -INFINITY ? 0.f : wt[2 + x];
           }
-          pa[2 * i + x] = half2_of(wa, wb);
         }
+        pb[b][0] = transpose8(half2_of(wt[0], wt[1]));
+        pb[b][1] = transpose8(half2_of(wt[2], wt[3]));
       }
       // V: the lane's D / 8 bytes of tokens 2t, 2t + 1, 2t + 8, 2t + 9
       constexpr int kWords = D / 32;
@@ -479,37 +486,33 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_history_few(const __grid_con
       }
 #pragma unroll
       for (int k = 0; k < kWords; ++k) {
-        const uint32_t x0 = prmt(v[0][k], v[1][k], 0x5140), y0 = prmt(v[0][k], v[1][k], 0x7362);
-        const uint32_t x1 = prmt(v[2][k], v[3][k], 0x5140), y1 = prmt(v[2][k], v[3][k], 0x7362);
-        uint32_t a0, a1, b0, b1;
-        e4m3x4_to_f16x2x2(x0, a0, a1);
-        e4m3x4_to_f16x2x2(x1, b0, b1);
-        mma_f16_16816(acc[4 * k], pa[0], pa[1], pa[2], pa[3], a0, b0);
-        mma_f16_16816(acc[4 * k + 1], pa[0], pa[1], pa[2], pa[3], a1, b1);
-        e4m3x4_to_f16x2x2(y0, a0, a1);
-        e4m3x4_to_f16x2x2(y1, b0, b1);
-        mma_f16_16816(acc[4 * k + 2], pa[0], pa[1], pa[2], pa[3], a0, b0);
-        mma_f16_16816(acc[4 * k + 3], pa[0], pa[1], pa[2], pa[3], a1, b1);
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {  // bytes 0, 1 and 2, 3 of a word: dims 4 k + 2 y, 4 k + 2 y + 1 of the lane's
+          uint32_t a0, a1, a2, a3;
+          e4m3x4_to_f16x2x2(prmt(v[0][k], v[1][k], y ? 0x7362 : 0x5140), a0, a1);
+          e4m3x4_to_f16x2x2(prmt(v[2][k], v[3][k], y ? 0x7362 : 0x5140), a2, a3);
+#pragma unroll
+          for (int b = 0; b < kN; ++b) mma_f16_16816(acc[b][2 * k + y], a0, a1, a2, a3, pb[b][0], pb[b][1]);
+        }
       }
       if (odd) {  // the rows that see them get NaN
 #pragma unroll 1
         for (int row = 0; row < kFewChunk; ++row) {
-          // the lane's sums: values t D / 4 .. of its rows
-          uint32_t bad = 0;  // by value
-#pragma unroll
-          for (int d = 0; d < D / 4; ++d) {
-            const int dim = t * (D / 4) + d, pc16 = dim >> 4;
-            const int o = D == 128 ? row * 128 + ((pc16 ^ (((row >> 1) & 3) << 1)) << 4)
-                                   : ((row & ~3) | ((row & 1) << 1) | ((row >> 1) & 1)) * 64 + ((pc16 ^ (((row >> 2) & 1) << 1)) << 4);
+          uint32_t bad = 0;  // of the lane's D / 8 values
+#pragma unroll 1
+          for (int d = 0; d < D / 8; ++d) {
+            const int dim = g * (D / 8) + d, c16 = dim >> 4;
+            const int o = D == 128 ? row * 128 + ((c16 ^ (((row >> 1) & 3) << 1)) << 4)
+                                   : ((row & ~3) | ((row & 1) << 1) | ((row >> 1) & 1)) * 64 + ((c16 ^ (((row >> 2) & 1) << 1)) << 4);
             if ((st[L::kCodes + o + (dim & 15)] & 0x7F) == 0x7F) bad |= 1u << d;
           }
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (t0 + row >= limit[x]) continue;
+          for (int b = 0; b < kN; ++b)
 #pragma unroll
-            for (int d = 0; d < D / 4; ++d)
-              if (bad >> d & 1) acc[d % (D / 8)][2 * x + d / (D / 8)] = __int_as_float(0x7FC00000);
-          }
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+              for (int d = 0; d < D / 8; ++d)
+                if ((bad >> d & 1) && t0 + row < limit[b][x]) acc[b][d / 2][2 * (d & 1) + x] = __int_as_float(0x7FC00000);
         }
       }
       __syncwarp();
@@ -519,7 +522,8 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_history_few(const __grid_con
           finish_unit();
         } else {
           if (c + 1 == end) asm volatile("cp.async.wait_group 0;" ::: "memory");
-          leave_sums(started ? (float*)ring_p : (float*)(smem + L::kFirst + warp * L::kSums));
+          __syncwarp();
+          leave_sums(started ? (float*)ring_p : part + (2 + warp) * L::kSums);
           if (lane == 0) {
             open[warp][started] = at;
             is_open[warp][started] = 1;
@@ -531,118 +535,168 @@ __global__ void __launch_bounds__(kFewThreads, 1) k_history_few(const __grid_con
     }
   }
 
-  // ---- units in several warps: a chain of a CTA's sums, joined by all its threads
+  // ---- units in several warps: a CTA's chains of sums.  A warp joins a fourth of
+  // a chain's rows; where other CTAs have a part of the unit it leaves what it
+  // has for the last of them.
   __syncthreads();
   const int cta_begin = (int)((long long)total * blockIdx.x / ctas), cta_end = (int)((long long)total * (blockIdx.x + 1) / ctas);
-  constexpr int kQuads = kFewRows * D / 4, kEach = kQuads / kFewThreads;
-  for (int k = 0; k < 2 * kFewWarps;) {  // the warps' open units in the line's order
-    if (!is_open[k >> 1][k & 1]) {
-      ++k;
-      continue;
+  constexpr int kQuads = kR * D / 4, kEach = kQuads / 4 / 32;  // four sums at a time: of a unit, and of a lane
+  // the open units in the line's order, and where chains begin
+  uint32_t opens, starts;
+  {
+    const bool there = lane < 2 * kWarps && is_open[(lane >> 1) % kWarps][lane & 1];
+    opens = __ballot_sync(0xffffffffu, there);
+    const uint32_t before = opens & ((1u << lane) - 1);
+    bool first = there;
+    if (there && before) {
+      const int b = 31 - __clz(before);
+      const FewPlace &x = open[b >> 1][b & 1], &y = open[lane >> 1][lane & 1];
+      first = x.seq != y.seq || x.unit != y.unit;
     }
-    const FewPlace u = open[k >> 1][k & 1];
-    int last = k + 1;
-    while (last < 2 * kFewWarps && (!is_open[last >> 1][last & 1] ||
-                                    (open[last >> 1][last & 1].seq == u.seq && open[last >> 1][last & 1].unit == u.unit)))
-      ++last;
+    starts = __ballot_sync(0xffffffffu, first);
+  }
+  for (int task = warp; task < 4 * __popc(starts); task += kWarps) {
+    uint32_t rest = starts;
+    for (int i = 0; i < task / 4; ++i) rest &= rest - 1;
+    const int start = __ffs(rest) - 1;
+    rest &= rest - 1;
+    uint32_t chain = opens & ~((1u << start) - 1) & (rest ? (1u << (__ffs(rest) - 1)) - 1 : 0xffffffffu);
+    const FewPlace u = open[start >> 1][start & 1];
     const int u0 = tab.first[u.seq] + u.unit * u.chunks, u1 = u0 + u.chunks;  // the unit's part of the line
-    const bool here = u0 >= cta_begin && u1 <= cta_end;
+    const int q0 = (task & 3) * (kQuads / 4) + lane;
     float4 o[kEach];
     float mx[kEach], lx[kEach];
-#pragma unroll
-    for (int i = 0; i < kEach; ++i) {
-      const int q = threadIdx.x + i * kFewThreads, row = q / (D / 4), quad = q % (D / 4);
-      o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      mx[i] = -INFINITY;
-      lx[i] = 0.f;
-      for (int j = k; j < last; ++j) {
-        if (!is_open[j >> 1][j & 1]) continue;
-        const float* src = (const float*)(smem + (j & 1 ? (j >> 1) * L::kRing : L::kFirst + (j >> 1) * L::kSums));
-        const float2 ml = *(const float2*)(src + kFewRows * D + 2 * row);
-        const float4 v = *(const float4*)(src + 4 * sums_at<D>(row, quad));
-        const float top = fmaxf(mx[i], ml.x);
-        const float a = mx[i] == -INFINITY ? 0.f : ex2(mx[i] - top), b = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
-        lx[i] = lx[i] * a + ml.y * b;
-        o[i] = make_float4(o[i].x * a + v.x * b, o[i].y * a + v.y * b, o[i].z * a + v.z * b, o[i].w * a + v.w * b);
-        mx[i] = top;
-      }
-    }
-    bool write = here;
-    if (!here) {
-      const int c0 = (int)(((long long)(u0 + 1) * ctas - 1) / total), c1 = (int)(((long long)u1 * ctas - 1) / total);
-      const size_t floats = kFewRows * (D + 2);
-      float* dst = p.part + ((size_t)blockIdx.x * 2 + (u0 >= cta_begin)) * floats;
+    auto clear = [&]() {
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
-        const int q = threadIdx.x + i * kFewThreads, row = q / (D / 4), quad = q % (D / 4);
-        __stcg((float4*)dst + q, o[i]);
-        if (quad == 0) __stcg((float2*)(dst + kFewRows * D) + row, make_float2(mx[i], lx[i]));
+        o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        mx[i] = -INFINITY;
+        lx[i] = 0.f;
       }
-      __threadfence();
-      __syncthreads();
-      int* cnt = p.part_cnt + u.seq * p.heads + u.unit;
-      if (threadIdx.x == 0) last_cta = atomicAdd(cnt, 1) == c1 - c0;
-      __syncthreads();
-      write = last_cta;
-      __syncthreads();
-      if (write) {
-        __threadfence();
-        if (threadIdx.x == 0) *cnt = 0;  // for the next launch
+    };
+    auto add = [&](int i, float2 ml, float4 v) {
+      const float top = fmaxf(mx[i], ml.x);
+      const float a = mx[i] == -INFINITY ? 0.f : ex2(mx[i] - top), b = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
+      lx[i] = lx[i] * a + ml.y * b;
+      o[i] = make_float4(o[i].x * a + v.x * b, o[i].y * a + v.y * b, o[i].z * a + v.z * b, o[i].w * a + v.w * b);
+      mx[i] = top;
+    };
+    constexpr int kBatch = 4;  // sums whose loads are in flight together
+    clear();
+    while (chain) {
+      float2 ml[kBatch][kEach];
+      float4 v[kBatch][kEach];
+#pragma unroll
+      for (int f = 0; f < kBatch; ++f) {
+        const int j = chain ? __ffs(chain) - 1 : -1;
+        chain &= chain - 1;  // 0 stays 0
+        const float* src = j & 1 ? (const float*)(smem + (j >> 1) * L::kRing) : part + (2 + (j >> 1)) * L::kSums;
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
-          const int q = threadIdx.x + i * kFewThreads, row = q / (D / 4);
-          o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-          mx[i] = -INFINITY;
-          lx[i] = 0.f;
-          for (int c = c0; c <= c1; ++c) {
-            const float* src = p.part + ((size_t)c * 2 + (c == c0)) * floats;
-            const float2 ml = __ldcg((const float2*)(src + kFewRows * D) + row);
-            const float4 v = __ldcg((const float4*)src + q);
-            const float top = fmaxf(mx[i], ml.x);
-            const float a = mx[i] == -INFINITY ? 0.f : ex2(mx[i] - top), b = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
-            lx[i] = lx[i] * a + ml.y * b;
-            o[i] = make_float4(o[i].x * a + v.x * b, o[i].y * a + v.y * b, o[i].z * a + v.z * b, o[i].w * a + v.w * b);
-            mx[i] = top;
+          const int row = (q0 + 32 * i) / (D / 4), quad = (q0 + 32 * i) % (D / 4);
+          const float2* sm = (const float2*)(src + kR * D + 2 * row);
+          const float4* so = (const float4*)(src + 4 * sums_at<D>(row, quad));
+          if (j < 0) {
+            ml[f][i] = make_float2(-INFINITY, 0.f);
+            v[f][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+          } else if (j & 1) {
+            ml[f][i] = *sm;
+            v[f][i] = *so;
+          } else {
+            ml[f][i] = __ldcg(sm);
+            v[f][i] = __ldcg(so);
           }
+        }
+      }
+#pragma unroll
+      for (int f = 0; f < kBatch; ++f)
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) add(i, ml[f][i], v[f][i]);
+    }
+    bool write = u0 >= cta_begin && u1 <= cta_end;
+    if (!write) {
+      const int c0 = (int)(((long long)(u0 + 1) * ctas - 1) / total), c1 = (int)(((long long)u1 * ctas - 1) / total);
+      float* dst = part + (u0 >= cta_begin ? L::kSums : 0);
+#pragma unroll
+      for (int i = 0; i < kEach; ++i) {
+        const int q = q0 + 32 * i;
+        __stcg((float4*)dst + q, o[i]);
+        if (q % (D / 4) == 0) __stcg((float2*)(dst + kR * D) + q / (D / 4), make_float2(mx[i], lx[i]));
+      }
+      __threadfence();
+      __syncwarp();
+      int* cnt = p.part_cnt + (u.seq * p.heads + u.unit) * 4 + (task & 3);
+      int there = 0;
+      if (lane == 0) there = atomicAdd(cnt, 1);
+      write = __shfl_sync(0xffffffffu, there, 0) == c1 - c0;
+      if (write) {
+        __threadfence();
+        if (lane == 0) *cnt = 0;  // for the next launch
+        clear();
+        for (int c = c0; c <= c1; c += kBatch) {
+          float2 ml[kBatch][kEach];
+          float4 v[kBatch][kEach];
+#pragma unroll
+          for (int f = 0; f < kBatch; ++f) {
+            const float* src = p.part + (size_t)min(c + f, c1) * L::kPart + (c + f == c0 ? L::kSums : 0);
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+              ml[f][i] = __ldcg((const float2*)(src + kR * D) + (q0 + 32 * i) / (D / 4));
+              v[f][i] = __ldcg((const float4*)src + q0 + 32 * i);
+              if (c + f > c1) ml[f][i].x = -INFINITY;
+            }
+          }
+#pragma unroll
+          for (int f = 0; f < kBatch; ++f)
+#pragma unroll
+            for (int i = 0; i < kEach; ++i)
+              if (c + f <= c1) add(i, ml[f][i], v[f][i]);
         }
       }
     }
     if (write) {
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
-        const int q = threadIdx.x + i * kFewThreads, row = q / (D / 4), quad = q % (D / 4);
-        const FewRow r = row_of(p, u, row);
+        const int row = (q0 + 32 * i) / (D / 4), quad = (q0 + 32 * i) % (D / 4);
+        const FewRow r = row_of<kR>(p, u, row);
         if (!r.on) continue;
         const float inv = 1.f / lx[i];
-        const float4 v = make_float4(o[i].x * inv, o[i].y * inv, o[i].z * inv, o[i].w * inv);
-        const uint2 z = kF16 ? make_uint2(pair16<__half>(v.x, v.y), pair16<__half>(v.z, v.w))
-                             : make_uint2(pair16<__nv_bfloat16>(v.x, v.y), pair16<__nv_bfloat16>(v.z, v.w));
-        *(uint2*)(p.out + r.row * p.out_stride + r.head * D + 4 * quad) = z;
+        *(uint2*)(p.out + r.row * p.out_stride + r.head * D + 4 * quad) =
+            kF16 ? make_uint2(pair16<__half>(o[i].x * inv, o[i].y * inv), pair16<__half>(o[i].z * inv, o[i].w * inv))
+                 : make_uint2(pair16<__nv_bfloat16>(o[i].x * inv, o[i].y * inv), pair16<__nv_bfloat16>(o[i].z * inv, o[i].w * inv));
       }
     }
-    k = last;
   }
 }
 
+template <int D, bool kF16, int kN>
+static cudaError_t configure() {
+  return cudaFuncSetAttribute(k_history_few<D, kF16, kN>, cudaFuncAttributeMaxDynamicSharedMemorySize, FewShape<D, kN>::kTotal);
+}
+
 cudaError_t configure_history_few() {
-  const cudaError_t e[4] = {
-      cudaFuncSetAttribute(k_history_few<128, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, FewSmem<128>::kTotal),
-      cudaFuncSetAttribute(k_history_few<128, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, FewSmem<128>::kTotal),
-      cudaFuncSetAttribute(k_history_few<64, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, FewSmem<64>::kTotal),
-      cudaFuncSetAttribute(k_history_few<64, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, FewSmem<64>::kTotal)};
+  const cudaError_t e[8] = {configure<128, false, 1>(), configure<128, false, 2>(), configure<128, true, 1>(), configure<128, true, 2>(),
+                            configure<64, false, 1>(),  configure<64, false, 2>(),  configure<64, true, 1>(),  configure<64, true, 2>()};
   for (cudaError_t x : e)
     if (x != cudaSuccess) return x;
   return cudaSuccess;
 }
 
-cudaError_t launch_history_few(const HistoryAttnParams& p, int D, int type, int sms, cudaStream_t st) {
-  if (D == 128)
-    type == WAVE_F16 ? k_history_few<128, true><<<sms, kFewThreads, FewSmem<128>::kTotal, st>>>(p)
-                     : k_history_few<128, false><<<sms, kFewThreads, FewSmem<128>::kTotal, st>>>(p);
+template <int D, bool kF16>
+static cudaError_t launch(HistoryAttnParams& p, int rows, int sms, cudaStream_t st) {
+  const int tile = rows <= 8 ? 8 : kFewRows;
+  p.tiles = (rows + tile - 1) / tile;  // more than one for a frame with more than 16 heads to a K/V head
+  if (tile == 8)
+    k_history_few<D, kF16, 1><<<sms, FewShape<D, 1>::kThreads, FewShape<D, 1>::kTotal, st>>>(p);
   else
-    type == WAVE_F16 ? k_history_few<64, true><<<sms, kFewThreads, FewSmem<64>::kTotal, st>>>(p)
-                     : k_history_few<64, false><<<sms, kFewThreads, FewSmem<64>::kTotal, st>>>(p);
+    k_history_few<D, kF16, 2><<<sms, FewShape<D, 2>::kThreads, FewShape<D, 2>::kTotal, st>>>(p);
   return cudaGetLastError();
+}
+
+// rows: the most that a session has for a K/V head.
+cudaError_t launch_history_few(HistoryAttnParams& p, int D, int type, int rows, int sms, cudaStream_t st) {
+  if (D == 128) return type == WAVE_F16 ? launch<128, true>(p, rows, sms, st) : launch<128, false>(p, rows, sms, st);
+  return type == WAVE_F16 ? launch<64, true>(p, rows, sms, st) : launch<64, false>(p, rows, sms, st);
 }
 
 }  // namespace wave
