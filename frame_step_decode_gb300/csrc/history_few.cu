@@ -35,17 +35,16 @@ constexpr float kFewBias = 7.f;  // the largest weight is held as 2^7
 // kN: groups of eight rows.  Two take twice the registers: half as many warps.
 template <int D, int kN>
 struct FewShape {
-  static constexpr int kWarps = kN == 1 ? 16 : 8, kThreads = kWarps * 32, kRows = 8 * kN;
-  static constexpr int kStages = kN == 1 ? 3 : 6;
+  static constexpr int kWarps = kN == 1 ? 12 : 8, kThreads = kWarps * 32, kRows = 8 * kN;
+  static constexpr int kStages = kN == 1 ? 3 : 4;
   static constexpr int kCodes = kFewChunk * D;  // of K, and of V
   static constexpr int kStage = 2 * kCodes + 2 * kFewChunk * 4;
   static constexpr int kRing = kStages * kStage;  // of a warp
   static constexpr int kSums = kRows * (D + 2);   // floats: a unit's sums, then the rows' maxima and sums of weights
   static_assert(kSums * 4 <= kRing, "a warp leaves its last unit's sums in its ring");
-  static constexpr int kTotal = kWarps * kRing;
-  // Of the workspace, for each CTA: two units that other CTAs have a part of,
-  // and the warps' first units where another warp has a part.
-  static constexpr int kPart = (2 + kWarps) * kSums;
+  static constexpr int kFirst = kWarps * kRing;   // the sums of the warps' first units, where another warp has a part
+  static constexpr int kTotal = kFirst + kWarps * kSums * 4;
+  static constexpr int kPart = 2 * kSums;         // of the workspace, for each CTA: two units that other CTAs have a part of
   static_assert(kPart <= 2 * 256 * D, "the workspace of a CTA");
 };
 
@@ -84,20 +83,17 @@ struct FewTables {
   int keys[WAVE_MAX_SEQS];       // what its last token sees
 };
 
-__device__ __forceinline__ FewPlace place_of(const HistoryAttnParams& p, const FewTables& tab, int at) {
-  int lo = 0, hi = p.n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (tab.first[mid] <= at)
-      lo = mid;
-    else
-      hi = mid - 1;
-  }
+__device__ __forceinline__ FewPlace place_of(const HistoryAttnParams& p, const FewTables& tab, int at) {  // by a whole warp
+  const int lane = threadIdx.x & 31;
+  int seq = -1;
+#pragma unroll
+  for (int k = 0; k < WAVE_MAX_SEQS / 32; ++k)
+    seq += __popc(__ballot_sync(0xffffffffu, lane + 32 * k < p.n && tab.first[lane + 32 * k] <= at));
   FewPlace w;
-  w.seq = lo;
-  w.keys = tab.keys[lo];
+  w.seq = seq;
+  w.keys = tab.keys[seq];
   w.chunks = (w.keys + kFewChunk - 1) / kFewChunk;
-  const int in = at - tab.first[lo];
+  const int in = at - tab.first[seq];
   w.unit = in / w.chunks;
   w.chunk = in - w.unit * w.chunks;
   return w;
@@ -202,8 +198,74 @@ __global__ void __launch_bounds__((FewShape<D, kN>::kThreads), 1) k_history_few(
   uint8_t* ring_p = smem + warp * L::kRing;
   constexpr int kH = D / 64;
   if (begin < end) {
+    // ---- the unit at hand; its q is on its way before any key
+    FewPlace at = place_of(p, tab, begin);
+    uint32_t qb[kN][kH * 4][2];
+    float acc[kN][D / 16][4], m[kN][2], e[kN][2], l[kN][2], rf[kN][2];  // of rows 2t, 2t + 1 of each eight
+    int limit[kN][2];
+    uint4 raw[kN][kH][2];
+    auto load_q = [&]() {
+#pragma unroll
+      for (int b = 0; b < kN; ++b) {
+        const FewRow r = row_of<kR>(p, at, 8 * b + g);
+        const uint16_t* src = p.q + r.row * p.q_stride + r.head * D + t * 16;
+#pragma unroll
+        for (int h = 0; h < kH; ++h)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) raw[b][h][i] = r.on ? __ldg((const uint4*)(src + h * 64 + i * 8)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) limit[b][x] = __shfl_sync(0xffffffffu, r.keys, 4 * (2 * t + x));
+      }
+    };
+    auto begin_unit = [&]() {
+#pragma unroll
+      for (int b = 0; b < kN; ++b) {
+        float factor = p.scale2, up = 1.f;
+        if constexpr (!kF16) {
+          uint32_t top = 0;  // the largest magnitude: bf16 bits compare as integers
+#pragma unroll
+          for (int h = 0; h < kH; ++h)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint4 v = raw[b][h][i];
+              top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+            }
+          top = max(top & 0xFFFFu, top >> 16);
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const int ex = min(max((int)(top >> 7) - 127, -113), 127);  // its exponent
+          up = __int_as_float((14 - ex + 127) << 23);
+          factor = p.scale2 * __int_as_float((ex + 127) << 23) * 0x1p-14f;
+        }
+#pragma unroll
+        for (int h = 0; h < kH; ++h)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t v[4] = {raw[b][h][i].x, raw[b][h][i].y, raw[b][h][i].z, raw[b][h][i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              uint32_t z = v[k];
+              if constexpr (!kF16) z = half2_of(__uint_as_float(z << 16) * up, __uint_as_float(z & 0xFFFF0000u) * up);
+              // word k of 16 bytes: values 2k, 2k + 1 of eight; an MMA takes four values of a lane
+              qb[b][h * 4 + i * 2 + (k >> 1)][k & 1] = z;
+            }
+          }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          rf[b][x] = __shfl_sync(0xffffffffu, factor, 4 * (2 * t + x));
+          m[b][x] = e[b][x] = -INFINITY;
+          l[b][x] = 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) acc[b][j][k] = 0.f;
+      }
+    };
+    load_q();
+
     // ---- copies: chunk by chunk along the line, kStages - 1 ahead
-    FewPlace in = place_of(p, tab, begin);
+    FewPlace in = at;
     int issued = begin, slot_in = 0;
     const uint8_t *kc = nullptr, *vc = nullptr;
     const float *ks = nullptr, *vs = nullptr;
@@ -262,64 +324,6 @@ __global__ void __launch_bounds__((FewShape<D, kN>::kThreads), 1) k_history_few(
 #pragma unroll 1
     for (int i = 0; i < L::kStages - 1; ++i) issue();
 
-    // ---- the unit at hand
-    FewPlace at = place_of(p, tab, begin);
-    uint32_t qb[kN][kH * 4][2];
-    float acc[kN][D / 16][4], m[kN][2], e[kN][2], l[kN][2], rf[kN][2];  // of rows 2t, 2t + 1 of each eight
-    int limit[kN][2];
-    auto begin_unit = [&]() {
-#pragma unroll
-      for (int b = 0; b < kN; ++b) {
-        const FewRow r = row_of<kR>(p, at, 8 * b + g);
-        const uint16_t* src = p.q + r.row * p.q_stride + r.head * D + t * 16;
-        uint4 raw[kH][2];
-#pragma unroll
-        for (int h = 0; h < kH; ++h)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) raw[h][i] = r.on ? __ldg((const uint4*)(src + h * 64 + i * 8)) : make_uint4(0, 0, 0, 0);
-        float factor = p.scale2, up = 1.f;
-        if constexpr (!kF16) {
-          uint32_t top = 0;  // the largest magnitude: bf16 bits compare as integers
-#pragma unroll
-          for (int h = 0; h < kH; ++h)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint4 v = raw[h][i];
-              top = __vmaxu2(top, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
-            }
-          top = max(top & 0xFFFFu, top >> 16);
-          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          const int ex = min(max((int)(top >> 7) - 127, -113), 127);  // its exponent
-          up = __int_as_float((14 - ex + 127) << 23);
-          factor = p.scale2 * __int_as_float((ex + 127) << 23) * 0x1p-14f;
-        }
-#pragma unroll
-        for (int h = 0; h < kH; ++h)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t v[4] = {raw[h][i].x, raw[h][i].y, raw[h][i].z, raw[h][i].w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              uint32_t z = v[k];
-              if constexpr (!kF16) z = half2_of(__uint_as_float(z << 16) * up, __uint_as_float(z & 0xFFFF0000u) * up);
-              // word k of 16 bytes: values 2k, 2k + 1 of eight; an MMA takes four values of a lane
-              qb[b][h * 4 + i * 2 + (k >> 1)][k & 1] = z;
-            }
-          }
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          rf[b][x] = __shfl_sync(0xffffffffu, factor, 4 * (2 * t + x));
-          limit[b][x] = __shfl_sync(0xffffffffu, r.keys, 4 * (2 * t + x));
-          m[b][x] = e[b][x] = -INFINITY;
-          l[b][x] = 0.f;
-        }
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) acc[b][j][k] = 0.f;
-      }
-    };
     auto weights_of = [&](float sum) {  // over the lanes of a row
 #pragma unroll
       for (int d = 4; d <= 16; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
@@ -367,6 +371,7 @@ __global__ void __launch_bounds__((FewShape<D, kN>::kThreads), 1) k_history_few(
     bool fresh = true, started = false;
     for (int c = begin; c < end; ++c) {
       if (fresh) {
+        if (c > begin) load_q();
         begin_unit();
         fresh = false;
         started = at.chunk == 0;
@@ -523,7 +528,7 @@ __global__ void __launch_bounds__((FewShape<D, kN>::kThreads), 1) k_history_few(
         } else {
           if (c + 1 == end) asm volatile("cp.async.wait_group 0;" ::: "memory");
           __syncwarp();
-          leave_sums(started ? (float*)ring_p : part + (2 + warp) * L::kSums);
+          leave_sums((float*)(started ? ring_p : smem + L::kFirst + warp * L::kSums * 4));
           if (lane == 0) {
             open[warp][started] = at;
             is_open[warp][started] = 1;
@@ -590,22 +595,12 @@ __global__ void __launch_bounds__((FewShape<D, kN>::kThreads), 1) k_history_few(
       for (int f = 0; f < kBatch; ++f) {
         const int j = chain ? __ffs(chain) - 1 : -1;
         chain &= chain - 1;  // 0 stays 0
-        const float* src = j & 1 ? (const float*)(smem + (j >> 1) * L::kRing) : part + (2 + (j >> 1)) * L::kSums;
+        const float* src = (const float*)(smem + (j & 1 ? (j >> 1) * L::kRing : L::kFirst + (j >> 1) * L::kSums * 4));
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
           const int row = (q0 + 32 * i) / (D / 4), quad = (q0 + 32 * i) % (D / 4);
-          const float2* sm = (const float2*)(src + kR * D + 2 * row);
-          const float4* so = (const float4*)(src + 4 * sums_at<D>(row, quad));
-          if (j < 0) {
-            ml[f][i] = make_float2(-INFINITY, 0.f);
-            v[f][i] = make_float4(0.f, 0.f, 0.f, 0.f);
-          } else if (j & 1) {
-            ml[f][i] = *sm;
-            v[f][i] = *so;
-          } else {
-            ml[f][i] = __ldcg(sm);
-            v[f][i] = __ldcg(so);
-          }
+          ml[f][i] = j < 0 ? make_float2(-INFINITY, 0.f) : *(const float2*)(src + kR * D + 2 * row);
+          v[f][i] = j < 0 ? make_float4(0.f, 0.f, 0.f, 0.f) : *(const float4*)(src + 4 * sums_at<D>(row, quad));
         }
       }
 #pragma unroll
