@@ -35,8 +35,8 @@ constexpr float kFewBias = 7.f;  // the largest weight is held as 2^7
 // kN: groups of eight rows.  Two take twice the registers: half as many warps.
 template <int D, int kN>
 struct FewShape {
-  static constexpr int kWarps = kN == 1 ? 12 : 8, kThreads = kWarps * 32, kRows = 8 * kN;
-  static constexpr int kStages = kN == 1 ? 3 : 4;
+  static constexpr int kWarps = kN == 1 ? 16 : 8, kThreads = kWarps * 32, kRows = 8 * kN;
+  static constexpr int kStages = kN == 1 ? (D == 128 ? 2 : 5) : D == 128 ? 4 : 8;
   static constexpr int kCodes = kFewChunk * D;  // of K, and of V
   static constexpr int kStage = 2 * kCodes + 2 * kFewChunk * 4;
   static constexpr int kRing = kStages * kStage;  // of a warp
