@@ -208,6 +208,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_word;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the launch that joins parts
   const bool stop = *leave;
   auto tS = [&](int st) { return tmem + st * 128; };
   auto tO = [&](int st) { return tmem + 256 + st * D; };
@@ -756,41 +757,48 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
   if (warp == 12) tmem_dealloc(tmem, 512);
 }
 
-// A unit's parts joined: a CTA per 32 rows of a unit that is cut, D / 4 threads to a row.
+// A unit's parts joined: D / 4 threads to a row, a CTA for every 1024 / D rows of
+// each place where the line is cut.  Four parts' loads are in flight together.
 template <int D, bool kF16>
 __global__ void __launch_bounds__(256) k_join_history(const __grid_constant__ ManyParams p) {
-  constexpr int kLanes = D / 4;
-  const int part = blockIdx.x % 8, c = blockIdx.x / 8 + 1;
+  constexpr int kLanes = D / 4, kRowsHere = 256 / kLanes, kCtas = 2 * kManyRows / kRowsHere;
+  const int r = blockIdx.x % kCtas * kRowsHere + (int)threadIdx.x / kLanes, c = blockIdx.x / kCtas + 1;
   const ManyCut u = p.cut[c];
   auto same = [&](int i) { return p.cut[i].seq == u.seq && p.cut[i].level == u.level && p.cut[i].head == u.head && p.cut[i].block > 0; };
   if (u.block == 0 || (c > 1 && same(c - 1))) return;  // not where a unit is cut first
   int last = c;  // the last CTA that has a part
   while (last + 1 < p.ctas && same(last + 1)) ++last;
-  ManyItem it;
-  it.seq = u.seq, it.level = u.level, it.head = u.head;
-  unit_blocks(p.a.b, p.tile_tokens, it);
-  const int col = (int)threadIdx.x % kLanes * 4;
-  for (int r = part * 32 + (int)threadIdx.x / kLanes; r < part * 32 + 32; r += 256 / kLanes) {
-    const int st = r / kManyRows, row = r % kManyRows, tok = it.tok0 + st * p.tile_tokens + row / p.a.group;
-    if (row / p.a.group >= p.tile_tokens || tok >= it.len) continue;
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = c - 1; i <= last; ++i) {
-      const size_t at = (size_t)(2 * i + (i < c)) * (2 * kManyRows) + r;
-      const float2 ml = p.part_ml[at];
-      const float4 v = *(const float4*)(p.part_o + at * D + col);
-      const float top = fmaxf(m, ml.x);
-      const float a = m == -INFINITY ? 0.f : ex2(m - top), b = ml.x == -INFINITY ? 0.f : ex2(ml.x - top);
-      l = l * a + ml.y * b;
-      o = make_float4(o.x * a + v.x * b, o.y * a + v.y * b, o.z * a + v.z * b, o.w * a + v.w * b);
+  const int st = r / kManyRows, row = r % kManyRows, row_tok = row / p.a.group;
+  const int tok = u.level * 2 * p.tile_tokens + st * p.tile_tokens + row_tok, col = (int)threadIdx.x % kLanes * 4;
+  const bool on = row_tok < p.tile_tokens && tok < p.a.b.len(u.seq);
+  uint16_t* dst = p.a.out + (p.a.b.begin[u.seq] + tok) * p.a.out_stride + (u.head * p.a.group + row % p.a.group) * D + col;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are there
+  if (!on) return;
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = c - 1; i <= last; i += 4) {
+    float2 ml[4];
+    float4 v[4];
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      const int k = min(i + f, last);
+      const size_t at = (size_t)(2 * k + (k < c)) * (2 * kManyRows) + r;
+      ml[f] = __ldcg(p.part_ml + at);
+      v[f] = __ldcg((const float4*)(p.part_o + at * D + col));
+    }
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      if (i + f > last) break;
+      const float top = fmaxf(m, ml[f].x);
+      const float a = m == -INFINITY ? 0.f : ex2(m - top), b = ml[f].x == -INFINITY ? 0.f : ex2(ml[f].x - top);
+      l = l * a + ml[f].y * b;
+      o = make_float4(o.x * a + v[f].x * b, o.y * a + v[f].y * b, o.z * a + v[f].z * b, o.w * a + v[f].w * b);
       m = top;
     }
-    const float inv = 1.f / l;
-    const int head = it.head * p.a.group + row % p.a.group;
-    uint16_t* dst = p.a.out + (p.a.b.begin[it.seq] + tok) * p.a.out_stride + head * D + col;
-    *(uint2*)dst = kF16 ? make_uint2(half2_of(o.x * inv, o.y * inv), half2_of(o.z * inv, o.w * inv))
-                        : make_uint2(pair16<__nv_bfloat16>(o.x * inv, o.y * inv), pair16<__nv_bfloat16>(o.z * inv, o.w * inv));
   }
+  const float inv = 1.f / l;
+  *(uint2*)dst = kF16 ? make_uint2(half2_of(o.x * inv, o.y * inv), half2_of(o.z * inv, o.w * inv))
+                      : make_uint2(pair16<__nv_bfloat16>(o.x * inv, o.y * inv), pair16<__nv_bfloat16>(o.z * inv, o.w * inv));
 }
 
 // The line cut into even parts, by what its blocks cost: with both streams at
@@ -867,7 +875,19 @@ static cudaError_t launch(const ManyParams& p, bool join, cudaStream_t st) {
     k_history_many<D, kF16, kScaleOfBlock><<<p.ctas, kManyThreads, ManySmem<D>::kTotal, st>>>(p);
   else
     k_history_many<D, kF16, kScaleOfTile><<<p.ctas, kManyThreads, ManySmem<D>::kTotal, st>>>(p);
-  if (join) k_join_history<D, kF16><<<(p.ctas - 1) * 8, 256, 0, st>>>(p);
+  if (join) {  // its CTAs begin as the parts' end, and wait for all of them
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3((p.ctas - 1) * (2 * kManyRows * D / 1024));
+    c.blockDim = dim3(256);
+    c.stream = st;
+    c.attrs = &early;
+    c.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&c, k_join_history<D, kF16>, p);
+    if (e != cudaSuccess) return e;
+  }
   return cudaGetLastError();
 }
 
