@@ -327,37 +327,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
         // between 2^7 and 2^16 and fp16 goes down to 2^-25, so that one 2^-32 of
         // it is still there.  (One fp32 product at a time: with packed ones the
         // loop takes 1290 cycles instead of 740 for a warp alone.)
-        if (j == 0) m = largest();
-        uint32_t w[64];
-        float2 sum[4];
-#pragma unroll 1
-        for (bool again = false;; again = true) {
-          const float neg = (m == -INFINITY ? 0.f : shift - m) + kManyBias;
-          sum[0] = sum[1] = sum[2] = sum[3] = make_float2(0.f, 0.f);
-          uint32_t s[2][32];
-          tmem_ld32(tS(st) + lanes, s[0]);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            tmem_ld_wait();
-            if (c < 3) tmem_ld32(tS(st) + lanes + 32 * (c + 1), s[(c + 1) & 1]);
-            uint32_t* x = s[c & 1];
-            ready(c, x);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float2 e = make_float2(ex2(fmaf(__uint_as_float(x[2 * i]), z, neg)), ex2(fmaf(__uint_as_float(x[2 * i + 1]), z, neg)));
-              sum[i & 3] = add2(sum[i & 3], e);
-              if constexpr (kScale == kScaleOfToken) {
-                const float2 v = ((const float2*)meta.v)[16 * c + i];
-                e = make_float2(e.x * v.x, e.y * v.y);
-              }
-              w[16 * c + i] = half2_of(e.x, e.y);
-            }
-          }
-          sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
-          sum[0].x += sum[0].y;
-          if (j == 0 || again || !__any_sync(0xffffffffu, !(sum[0].x <= 60000.f))) break;
-          const float top = largest();
-          const bool up = top > m;
+        auto raise = [&](float top, bool up) {  // the maximum moves
           const float a = up ? (m == -INFINITY ? 0.f : ex2(m - top)) : 1.f;
           l *= a;
           m = up ? top : m;
@@ -370,9 +340,75 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
             for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
             tmem_st32(tO(st) + lanes + 32 * c, o);
           }
+        };
+        float2 sum[4];
+        auto weights = [&](int c, uint32_t* x, uint32_t* w, float neg) {  // of 32 columns
+          ready(c, x);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float2 e = make_float2(ex2(fmaf(__uint_as_float(x[2 * i]), z, neg)), ex2(fmaf(__uint_as_float(x[2 * i + 1]), z, neg)));
+            sum[i & 3] = add2(sum[i & 3], e);
+            if constexpr (kScale == kScaleOfToken) {
+              const float2 v = ((const float2*)meta.v)[16 * c + i];
+              e = make_float2(e.x * v.x, e.y * v.y);
+            }
+            w[i] = half2_of(e.x, e.y);
+          }
+        };
+        auto relative = [&]() {
+          sum[0] = sum[1] = sum[2] = sum[3] = make_float2(0.f, 0.f);
+          return (m == -INFINITY ? 0.f : shift - m) + kManyBias;
+        };
+        auto add_up = [&]() {
+          sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+          sum[0].x += sum[0].y;
+        };
+        if (j == 0) m = largest();
+        if constexpr (kScale == kScaleOfToken) {
+          // With a block's scales in registers too, P cannot be held back: the
+          // maximum comes first, and P is written as it is made (over columns of
+          // S that have been read).
+          if (j > 0) {
+            const float top = largest();
+            const bool up = top > m + 8.f;
+            if (__any_sync(0xffffffffu, up)) raise(top, up);
+          }
+          const float neg = relative();
+          uint32_t s[2][32];
+          tmem_ld32(tS(st) + lanes, s[0]);
+#pragma unroll 1
+          for (int c = 0; c < 4; c += 2) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t w[16];
+              tmem_ld_wait();
+              if (c + h < 3) tmem_ld32(tS(st) + lanes + 32 * (c + h + 1), s[1 - h]);
+              weights(c + h, s[h], w, neg);
+              tmem_st16(tS(st) + lanes + 16 * (c + h), w);
+            }
+          }
+          add_up();
+        } else {
+          uint32_t w[64];
+#pragma unroll 1
+          for (bool again = false;; again = true) {
+            const float neg = relative();
+            uint32_t s[2][32];
+            tmem_ld32(tS(st) + lanes, s[0]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              tmem_ld_wait();
+              if (c < 3) tmem_ld32(tS(st) + lanes + 32 * (c + 1), s[(c + 1) & 1]);
+              weights(c, s[c & 1], w + 16 * c, neg);
+            }
+            add_up();
+            if (j == 0 || again || !__any_sync(0xffffffffu, !(sum[0].x <= 60000.f))) break;
+            const float top = largest();
+            raise(top, top > m);
+          }
+          tmem_st32(tS(st) + lanes, w);
+          tmem_st32(tS(st) + lanes + 32, w + 32);
         }
-        tmem_st32(tS(st) + lanes, w);
-        tmem_st32(tS(st) + lanes + 32, w + 32);
         l += sum[0].x * meta.back;
         tmem_st_wait();
         tc_fence_before();
@@ -455,7 +491,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
     int* my_bad = bad + (warp - 8) * D;
     uint32_t tiles = 0, m_it = 0;
     uint4 code[2][kPieces];                     // the next K tile and the next V tile
-    float sc[kScale == kScaleOfToken ? 8 : 1];  // the next block's scales
+    float sc[kScale == kScaleOfToken ? 4 : 1];  // the next block's scales (a scale for each token: warp 8 K's, warp 9 V's)
     const uint8_t *kc, *vc;                     // the thread's piece of the unit's codes
     const float *ks, *vs;
     int keys;                                   // what the unit's last row sees
@@ -481,11 +517,12 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
     };
     auto scales = [&](int block) {
       if constexpr (kScale == kScaleOfToken) {
+        if (warp < 10) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int t = block * kManyRows + lane * 4 + i;
-          sc[i] = t < keys ? __ldg(ks + t) : 0.f;
-          sc[4 + i] = t < keys ? __ldg(vs + t) : 0.f;
+          for (int i = 0; i < 4; ++i) {
+            const int t = block * kManyRows + lane * 4 + i;
+            sc[i] = t < keys ? __ldg((warp == 8 ? ks : vs) + t) : 0.f;
+          }
         }
       } else {  // lanes 0..7 K's, 8..15 V's
         const int t = (lane & 7) << p.a.hist.shift;
@@ -512,28 +549,31 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
         uint32_t ratio = 0;  // the lane's scale over the tile's, as two fp16
         if (!wait_warp(L::kMetaEmpty + mi, ((m_it / L::kMetas) & 1) ^ 1)) break;
         if constexpr (kScale == kScaleOfToken) {
-          // a V scale that is not finite makes all its token's values NaN
-          bool odd = false;
+          if (warp == 8) {
+            *(float4*)&meta.k[4 * lane] = make_float4(sc[0], sc[1], sc[2], sc[3]);
+          } else if (warp == 9) {
+            // a V scale that is not finite makes all its token's values NaN
+            bool odd = false;
 #pragma unroll
-          for (int i = 4; i < 8; ++i) odd |= !(sc[i] <= 0x1.fffffep127f);
-          if (warp == 8 && __any_sync(0xffffffffu, odd)) {
-            for (int i = 4; i < 8; ++i)
-              if (!(sc[i] <= 0x1.fffffep127f))
-                for (int d = 0; d < D; ++d) atomicMin(&my_bad[(k & 1) * 4 * D + d], j * kManyRows + 4 * lane + i - 4);
-            odd_unit[(k & 1) * 4] = 1;
-          }
+            for (int i = 0; i < 4; ++i) odd |= !(sc[i] <= 0x1.fffffep127f);
+            if (__any_sync(0xffffffffu, odd)) {
 #pragma unroll
-          for (int i = 4; i < 8; ++i) sc[i] = sc[i] <= 0x1.fffffep127f ? sc[i] : 0.f;
-          float top = fmaxf(fmaxf(sc[4], sc[5]), fmaxf(sc[6], sc[7]));
+              for (int i = 0; i < 4; ++i)
+                if (!(sc[i] <= 0x1.fffffep127f))
+#pragma unroll 1
+                  for (int d = 0; d < D; ++d) atomicMin(&my_bad[(k & 1) * 4 * D + d], j * kManyRows + 4 * lane + i);
+              odd_unit[(k & 1) * 4 + 1] = 1;
+            }
 #pragma unroll
-          for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-          const int e = top > 0.f ? min(max(exponent_up(top), -100), 120) : -100;
-          if (warp == 8) *(float4*)&meta.k[4 * lane] = make_float4(sc[0], sc[1], sc[2], sc[3]);
-          if (warp == 9) {
+            for (int i = 0; i < 4; ++i) sc[i] = sc[i] <= 0x1.fffffep127f ? sc[i] : 0.f;
+            float top = fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3]));
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            const int e = top > 0.f ? min(max(exponent_up(top), -100), 120) : -100;
             const float r = power(-e);
-            *(float4*)&meta.v[4 * lane] = make_float4(sc[4] * r, sc[5] * r, sc[6] * r, sc[7] * r);
+            *(float4*)&meta.v[4 * lane] = make_float4(sc[0] * r, sc[1] * r, sc[2] * r, sc[3] * r);
+            if (lane == 0) meta.factor = 1.f, meta.shift = (float)e, meta.back = r;
           }
-          if (warp == 10 && lane == 0) meta.factor = 1.f, meta.shift = (float)e, meta.back = power(-e);
         } else {
           float top = sc[0];
           if constexpr (kScale == kScaleOfBlock) {
