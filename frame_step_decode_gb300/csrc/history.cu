@@ -10,8 +10,11 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "../../include/wave.h"
 #include "history.h"
+#include "quotient.cuh"
 
 using namespace wave;
 
@@ -54,14 +57,15 @@ __device__ __forceinline__ void recode(uint8_t* codes, int from, int to, float r
   }
 }
 
-// One token of a head row after another: blocks of 1, and frames.  D / 16
-// lanes to a row, sixteen values each.
+// Single tokens: blocks of 1, and frames.  D / 16 lanes to a head row of a token,
+// sixteen values each, kFew rows of a lane's in flight together while the turns
+// of the token's position are made.
 template <int D, typename In, typename Out>
 __global__ void __launch_bounds__(kAppendThreads2) k_append_tokens(const __grid_constant__ HistoryAppendParams p) {
-  constexpr int kLanes = D / 16;
+  constexpr int kLanes = D / 16, kGroups = kAppendThreads2 / kLanes, kFew = 3;
   __shared__ float4 turns[D / 4];
   const int rows = p.heads + 2 * p.hist.heads, chunks = (rows + p.per_cta - 1) / p.per_cta;
-  const int t = blockIdx.x / chunks, first = (blockIdx.x % chunks) * p.per_cta;
+  const int t = blockIdx.x / chunks, first = (blockIdx.x - t * chunks) * p.per_cta;
   int row, pos, slot;
   if (p.positions) {
     row = slot = t;
@@ -77,82 +81,100 @@ __global__ void __launch_bounds__(kAppendThreads2) k_append_tokens(const __grid_
     pos = p.b.start[s] + n;
     slot = p.b.slot[s];
   }
-  make_turns(p.rope, turns, 0, 1, pos);
-  __syncthreads();
   const int lane = threadIdx.x % kLanes, last = min(first + p.per_cta, rows);
   const uint32_t mates = ((1u << kLanes) - 1) << ((threadIdx.x & 31) / kLanes * kLanes);
-  for (int r = first + (int)threadIdx.x / kLanes; r < last; r += kAppendThreads2 / kLanes) {
-    if (r < p.heads && !p.q) continue;
-    int a, b;
-    bool turned;
-    const bool is_v = r >= p.heads + p.hist.heads;
-    groups_of_item(p.rope, lane, a, b, turned);
-    const In* src = (const In*)p.qkv + (size_t)row * p.stride + r * D;
-    float x[16];
-    load8<In>(src + 8 * a, x);
-    load8<In>(src + 8 * b, x + 8);
-    if (turned && !is_v) turn_item(x, &turns[lane], p.rope.dims / 16, p.rope.layout == WAVE_ROPE_HALF);
-    if (r < p.heads) {
-      Out* dst = (Out*)p.q + ((size_t)row * p.heads + r) * D;
-      store8<Out>(dst + 8 * a, x);
-      store8<Out>(dst + 8 * b, x + 8);
-      continue;
+  const bool half = p.rope.layout == WAVE_ROPE_HALF;
+  int a, b;
+  bool turned;
+  groups_of_item(p.rope, lane, a, b, turned);
+  const In* src = (const In*)p.qkv + (size_t)row * p.stride;
+  for (int r0 = first + (int)threadIdx.x / kLanes, it = 0; it == 0 || r0 - (int)threadIdx.x / kLanes < last; r0 += kFew * kGroups, ++it) {
+    Raw16<In> raw[kFew];
+#pragma unroll
+    for (int f = 0; f < kFew; ++f) {
+      const int r = r0 + f * kGroups;
+      if (r < last && (r >= p.heads || p.q)) raw[f].load(src + r * D, a, b);
     }
-    const size_t hr = p.hist.row(is_v, slot, r - p.heads - (is_v ? p.hist.heads : 0));
-    uint8_t* codes = p.hist.codes + hr * p.hist.T_max * D;
-    float* scales = p.hist.scales + hr * p.hist.blocks;
-    float amax = 0.f;
-    uint2 c0, c1;
-    if (p.hist.block == 1) {
+    if (it == 0) {
+      make_turns(p.rope, turns, 0, 1, pos);
+      __syncthreads();
+    }
 #pragma unroll
-      for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));
-#pragma unroll
-      for (int d = kLanes / 2; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(mates, amax, d));
-      const float sc = __fdiv_rn(amax, 448.0f);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) x[i] = sc == 0.f ? 0.f : __fdiv_rn(x[i], sc);
-      c0 = encode8(x, 1.f), c1 = encode8(x + 8, 1.f);
-      if (lane == 0) scales[pos] = sc;
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) amax = fmaxf(amax, counts(x[i]));
-#pragma unroll
-      for (int d = kLanes / 2; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(mates, amax, d));
-      const int blk = pos >> p.hist.shift, from = blk << p.hist.shift;
-      float sc = block_scale(amax);
-      if (from < pos) {
-        const float old = scales[blk];
-        __syncwarp(mates);  // read before lane 0 writes it
-        if (sc > old)
-          recode<D>(codes, from, pos, old / sc, lane, kLanes);
-        else
-          sc = old;
+    for (int f = 0; f < kFew; ++f) {
+      const int r = r0 + f * kGroups;
+      if (r >= last || (r < p.heads && !p.q)) continue;
+      const bool is_v = r >= p.heads + p.hist.heads;
+      float x[16];
+      raw[f].get(x);
+      if (turned && !is_v) turn_item(x, &turns[lane], p.rope.dims / 16, half);
+      if (r < p.heads) {
+        Out* dst = (Out*)p.q + ((size_t)row * p.heads + r) * D;
+        store8<Out>(dst + 8 * a, x);
+        store8<Out>(dst + 8 * b, x + 8);
+        continue;
       }
-      const float inv = sc == 0.f ? 0.f : __frcp_rn(sc);
-      c0 = encode8(x, inv), c1 = encode8(x + 8, inv);
-      if (lane == 0) scales[blk] = sc;
+      const size_t hr = p.hist.row(is_v, slot, r - p.heads - (is_v ? p.hist.heads : 0));
+      uint8_t* codes = p.hist.codes + hr * p.hist.T_max * D;
+      float* scales = p.hist.scales + hr * p.hist.blocks;
+      float amax = 0.f;
+      uint2 c0, c1;
+      if (p.hist.block == 1) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));
+#pragma unroll
+        for (int d = kLanes / 2; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(mates, amax, d));
+        const float sc = __fdiv_rn(amax, 448.0f);
+        c0 = make_uint2(encode4(x, sc), encode4(x + 4, sc));
+        c1 = make_uint2(encode4(x + 8, sc), encode4(x + 12, sc));
+        if (lane == 0) scales[pos] = sc;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) amax = fmaxf(amax, counts(x[i]));
+#pragma unroll
+        for (int d = kLanes / 2; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(mates, amax, d));
+        const int blk = pos >> p.hist.shift, from = blk << p.hist.shift;
+        float sc = block_scale(amax);
+        if (from < pos) {
+          const float old = scales[blk];
+          __syncwarp(mates);  // read before lane 0 writes it
+          if (sc > old)
+            recode<D>(codes, from, pos, old / sc, lane, kLanes);
+          else
+            sc = old;
+        }
+        const float inv = sc == 0.f ? 0.f : __frcp_rn(sc);
+        c0 = encode8(x, inv), c1 = encode8(x + 8, inv);
+        if (lane == 0) scales[blk] = sc;
+      }
+      uint8_t* dst = codes + (size_t)pos * D;
+      *(uint2*)(dst + 8 * a) = c0;
+      *(uint2*)(dst + 8 * b) = c1;
     }
-    uint8_t* dst = codes + (size_t)pos * D;
-    *(uint2*)(dst + 8 * a) = c0;
-    *(uint2*)(dst + 8 * b) = c1;
   }
 }
 
 // Blocks of 16 to 128 tokens of prompts.  A CTA takes the tokens that the call
 // has of one block, and some of the head rows: one pass over them, values kept
-// in registers between the block's largest magnitude and the codes.  The turns
-// of the block's positions are made once, into shared memory, for all its
-// heads.  kLog: the block is 1 << kLog tokens.
+// in registers between the block's largest magnitude and the codes, the next
+// head row's on their way meanwhile.  The turns of the block's positions are
+// made once, into shared memory, for all its heads.  kLog: the block is 1 <<
+// kLog tokens.
+template <int D, int kLog>
+struct BlockShape {
+  static constexpr int kLanes = D / 16, kItems = (1 << kLog) * kLanes;  // of a head row
+  static constexpr int kThreads = kItems > 512 ? 512 : 256;
+  static constexpr int kPer = kItems > kThreads ? kItems / kThreads : 1;  // items of a thread
+  static constexpr int kGroup = kItems / kPer;                           // threads to a head row
+  static constexpr int kGroups = kThreads / kGroup;                      // head rows at a time
+};
 template <int D, int kLog, typename In, typename Out>
-__global__ void __launch_bounds__(kAppendThreads2) k_append_blocks(const __grid_constant__ HistoryAppendParams p) {
-  constexpr int kBlock = 1 << kLog, kLanes = D / 16, kItems = kBlock * kLanes;
-  constexpr int kPer = kItems > kAppendThreads2 ? kItems / kAppendThreads2 : 1;  // items of a thread
-  constexpr int kGroup = kItems / kPer;                                          // threads to a head row
-  constexpr int kGroups = kAppendThreads2 / kGroup;                              // head rows at a time
+__global__ void __launch_bounds__((BlockShape<D, kLog>::kThreads)) k_append_blocks(const __grid_constant__ HistoryAppendParams p) {
+  using B = BlockShape<D, kLog>;
+  constexpr int kLanes = B::kLanes, kPer = B::kPer, kGroup = B::kGroup, kGroups = B::kGroups;
   extern __shared__ float4 turns[];  // [token][D / 4]
-  __shared__ float most[2][kAppendThreads2 / 32];
+  __shared__ float most[2][B::kThreads / 32];
   const int rows = p.heads + 2 * p.hist.heads, chunks = (rows + p.per_cta - 1) / p.per_cta;
-  const int unit = blockIdx.x / chunks, first = (blockIdx.x % chunks) * p.per_cta, last = min(first + p.per_cta, rows);
+  const int unit = blockIdx.x / chunks, first = (blockIdx.x - unit * chunks) * p.per_cta, last = min(first + p.per_cta, rows);
   int lo = 0, hi = p.b.n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -165,8 +187,6 @@ __global__ void __launch_bounds__(kAppendThreads2) k_append_blocks(const __grid_
   const int blk = (start >> kLog) + unit - p.first_block[lo];
   const int from = max(start, blk << kLog), to = min(end, (blk + 1) << kLog);  // the call's tokens of the block
   const int held = from - (blk << kLog);                                      // what the block holds before them
-  make_turns(p.rope, turns, D / 4, to - from, from);
-  __syncthreads();
   const int g = threadIdx.x / kGroup, in = threadIdx.x % kGroup, lane = in % kLanes, t0 = in / kLanes;
   constexpr int kStep = kGroup / kLanes;  // tokens between a thread's items
   int a, b;
@@ -174,23 +194,29 @@ __global__ void __launch_bounds__(kAppendThreads2) k_append_blocks(const __grid_
   groups_of_item(p.rope, lane, a, b, turned);
   const bool half = p.rope.layout == WAVE_ROPE_HALF;
   const size_t row0 = p.b.begin[lo] + (from - start);
+  Raw16<In> raw[kPer];
+  auto load = [&](int r) {
+    const bool on = r < last && (r >= p.heads || p.q);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int t = t0 + i * kStep;
+      if (on && from + t < to)
+        raw[i].load((const In*)p.qkv + (row0 + t) * p.stride + r * D, a, b);
+      else
+        raw[i].clear();
+    }
+  };
+  load(first + g);
+  make_turns(p.rope, turns, D / 4, to - from, from);
+  __syncthreads();
   for (int it = 0, r0 = first; r0 < last; ++it, r0 += kGroups) {
     const int r = r0 + g;
     const bool is_q = r < p.heads, is_v = r >= p.heads + p.hist.heads, on = r < last && (!is_q || p.q);
     float x[kPer][16];
     float amax = 0.f;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int t = t0 + i * kStep;
-      if (on && from + t < to) {
-        const In* src = (const In*)p.qkv + (row0 + t) * p.stride + r * D;
-        load8<In>(src + 8 * a, x[i]);
-        load8<In>(src + 8 * b, x[i] + 8);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) x[i][e] = 0.f;
-      }
-    }
+    for (int i = 0; i < kPer; ++i) raw[i].get(x[i]);
+    load(r + kGroups);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int t = t0 + i * kStep;
@@ -206,15 +232,15 @@ __global__ void __launch_bounds__(kAppendThreads2) k_append_blocks(const __grid_
       }
     }
     if (r0 + kGroups <= p.heads) continue;  // all of q: the same for the whole CTA
-    const size_t hr = on && !is_q ? p.hist.row(is_v, slot, r - p.heads - (is_v ? p.hist.heads : 0)) : 0;
+    const bool mine = on && !is_q;
+    const size_t hr = mine ? p.hist.row(is_v, slot, r - p.heads - (is_v ? p.hist.heads : 0)) : 0;
     uint8_t* codes = p.hist.codes + hr * p.hist.T_max * D;
     float* scales = p.hist.scales + hr * p.hist.blocks;
-    const bool mine = on && !is_q;
     const float old = mine && held ? scales[blk] : 0.f;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
     if (threadIdx.x % 32 == 0) most[it & 1][threadIdx.x / 32] = amax;
-    __syncthreads();  // the other half of `most` is written before the next one
+    __syncthreads();  // most[it & 1] is written again after the next one, which comes after it has been read
     if (!mine) continue;
 #pragma unroll
     for (int w = 0; w < kGroup / 32; ++w) amax = fmaxf(amax, most[it & 1][g * (kGroup / 32) + w]);
@@ -239,14 +265,20 @@ __global__ void __launch_bounds__(kAppendThreads2) k_append_blocks(const __grid_
 }
 
 template <int D, int kLog, typename In, typename Out>
-static cudaError_t launch_blocks(const HistoryAppendParams& p, int chunks, cudaStream_t st) {
+static cudaError_t launch_blocks(HistoryAppendParams& p, int sms, cudaStream_t st) {
+  using B = BlockShape<D, kLog>;
   constexpr int kSmem = (1 << kLog) * D * 4;
   static_assert(kSmem <= 64 * 1024, "the turns of a block");
   if (kSmem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(k_append_blocks<D, kLog, In, Out>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
   }
-  k_append_blocks<D, kLog, In, Out><<<(unsigned)(p.first_block[p.b.n] * chunks), kAppendThreads2, kSmem, st>>>(p);
+  // head rows of a CTA: up to eight rounds of them, fewer where that leaves SMs without work
+  const int rows = p.heads + 2 * p.hist.heads, units = p.first_block[p.b.n];
+  const long long share = (long long)units * rows / (4LL * sms * B::kGroups);
+  p.per_cta = B::kGroups * (int)std::max(1LL, std::min(8LL, share));
+  const int chunks = (rows + p.per_cta - 1) / p.per_cta;
+  k_append_blocks<D, kLog, In, Out><<<(unsigned)(units * chunks), B::kThreads, kSmem, st>>>(p);
   return cudaGetLastError();
 }
 
@@ -254,7 +286,9 @@ template <int D, typename In, typename Out>
 static cudaError_t launch_history_append(HistoryAppendParams& p, int tokens, int sms, cudaStream_t st) {
   const int rows = p.heads + 2 * p.hist.heads;
   if (p.positions || p.hist.block == 1) {
-    p.per_cta = kAppendThreads2 / (D / 16);
+    // head rows of a CTA: all of them, or one for each group of lanes where tokens are few
+    constexpr int kGroups = kAppendThreads2 / (D / 16);
+    p.per_cta = tokens >= 8 * sms ? rows : kGroups;
     const int chunks = (rows + p.per_cta - 1) / p.per_cta;
     k_append_tokens<D, In, Out><<<(unsigned)((long long)tokens * chunks), kAppendThreads2, 0, st>>>(p);
     return cudaGetLastError();
@@ -263,13 +297,11 @@ static cudaError_t launch_history_append(HistoryAppendParams& p, int tokens, int
   for (int i = 0; i < p.b.n; ++i)
     p.first_block[i + 1] =
         p.first_block[i] + ((p.b.start[i] + p.b.len(i) - 1) >> p.hist.shift) - (p.b.start[i] >> p.hist.shift) + 1;
-  p.per_cta = 8;
-  const int chunks = (rows + p.per_cta - 1) / p.per_cta;
   switch (p.hist.shift) {
-    case 4: return launch_blocks<D, 4, In, Out>(p, chunks, st);
-    case 5: return launch_blocks<D, 5, In, Out>(p, chunks, st);
-    case 6: return launch_blocks<D, 6, In, Out>(p, chunks, st);
-    default: return launch_blocks<D, 7, In, Out>(p, chunks, st);
+    case 4: return launch_blocks<D, 4, In, Out>(p, sms, st);
+    case 5: return launch_blocks<D, 5, In, Out>(p, sms, st);
+    case 6: return launch_blocks<D, 6, In, Out>(p, sms, st);
+    default: return launch_blocks<D, 7, In, Out>(p, sms, st);
   }
 }
 

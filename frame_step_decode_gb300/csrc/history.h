@@ -126,6 +126,28 @@ __device__ __forceinline__ void store8<float>(float* p, const float* x) {
   *(float4*)(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
 }
 
+// Sixteen values of a row as they come from memory, two groups of eight.
+template <typename T>
+struct Raw16 {
+  uint4 v[sizeof(T)];  // 2 for 16-bit types, 4 for fp32
+  __device__ __forceinline__ void load(const T* row, int a, int b) {
+    constexpr int n = sizeof(T) / 2;
+#pragma unroll
+    for (int i = 0; i < n; ++i) {
+      v[i] = *((const uint4*)(row + 8 * a) + i);
+      v[n + i] = *((const uint4*)(row + 8 * b) + i);
+    }
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T); ++i) v[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void get(float* x) const {
+    load8<T>((const T*)v, x);
+    load8<T>((const T*)(v + sizeof(T) / 2), x + 8);
+  }
+};
+
 // ---- the history
 
 // One layer: codes [2][S_max][heads][T_max][D], scales [2][S_max][heads][blocks].

@@ -6,6 +6,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <algorithm>
+
 #include "../../include/wave.h"
 #include "history.h"
 
@@ -18,70 +20,83 @@ struct RopeParams {
   const int32_t* positions;  // rows' positions on the device, or null
   long long tokens;
   wave_rope rope;
-  int heads, rows_per_cta;
+  int heads;
   const void* x;
   void* out;
   long long x_stride, out_stride;
 };
 
-constexpr int kRopeThreads = 256, kRopeRows = 16;
+constexpr int kRopeThreads = 256, kRopeRows = 4;
 
-// Bound by HBM, x read and out written once.  A CTA takes a few rows: the
-// turns of their positions are made once, into shared memory, and serve all
-// heads of a row.
+// Bound by HBM, x read and out written once.  A CTA takes four rows: a thread
+// has the same sixteen values of each, whose loads are in flight while the turns
+// of the rows' positions are made, into shared memory, for all their heads.
 template <int D, typename In, typename Out>
 __global__ void __launch_bounds__(kRopeThreads) k_rope(const __grid_constant__ RopeParams p) {
   __shared__ float4 turns[kRopeRows][D / 4];  // [row][4][dims / 16]: the items' pairs, two by two
-  __shared__ long long at[kRopeRows];         // the row in the buffers, or -1
   const int pairs = p.rope.dims / 2, per = p.rope.dims / 16;
-  const long long first = (long long)blockIdx.x * p.rows_per_cta;
-  const int rows = (int)min((long long)p.rows_per_cta, p.tokens - first);
-  for (int i = threadIdx.x; i < rows * pairs; i += kRopeThreads) {
-    const int r = i / pairs, k = i % pairs;
-    const long long t = first + r;
-    long long row = t;
-    int pos;
+  const long long first = (long long)blockIdx.x * kRopeRows;
+  const int rows = (int)min((long long)kRopeRows, p.tokens - first);
+  long long at[kRopeRows];  // the row in the buffers, or -1
+  int pos[kRopeRows];
+#pragma unroll
+  for (int r = 0; r < kRopeRows; ++r) {
+    at[r] = -1;
+    pos[r] = 0;
+    if (r >= rows) continue;
     if (p.positions) {
-      pos = p.positions[t];
-      if (pos < 0) row = -1;
+      pos[r] = p.positions[first + r];
+      if (pos[r] >= 0) at[r] = first + r;
     } else {
-      const int s = seq_of(p.b, (int)t), n = (int)t - p.b.cum[s];
-      row = p.b.begin[s] + n;
-      pos = p.b.start[s] + n;
+      const int t = (int)first + r, s = seq_of(p.b, t), n = t - p.b.cum[s];
+      at[r] = p.b.begin[s] + n;
+      pos[r] = p.b.start[s] + n;
     }
-    if (k == 0) at[r] = row;
-    ((float2*)turns[r])[(k % 8 / 2 * per + k / 8) * 2 + k % 2] = turn_at(p.rope.turns[k], (uint32_t)max(pos, 0), p.rope.amplitude);
   }
-  __syncthreads();
   constexpr int kItems = D / 16;
   const int items = p.heads * kItems;
   const bool half = p.rope.layout == WAVE_ROPE_HALF;
-  for (int i = threadIdx.x; i < rows * items; i += kRopeThreads) {
-    const int r = i / items, head = (i - r * items) / kItems, item = i % kItems;
-    const long long row = at[r];
-    if (row < 0) continue;
+  for (int i = threadIdx.x; i < (items + (int)blockDim.x - 1) / (int)blockDim.x * (int)blockDim.x; i += blockDim.x) {
+    const int head = i / kItems, item = i % kItems;
     int a, b;
     bool turned;
     groups_of_item(p.rope, item, a, b, turned);
-    const In* src = (const In*)p.x + row * p.x_stride + head * D;
-    Out* dst = (Out*)p.out + row * p.out_stride + head * D;
-    float x[16];
-    load8<In>(src + 8 * a, x);
-    load8<In>(src + 8 * b, x + 8);
-    if (turned) turn_item(x, &turns[r][item], per, half);
-    store8<Out>(dst + 8 * a, x);
-    store8<Out>(dst + 8 * b, x + 8);
+    Raw16<In> raw[kRopeRows];
+    if (i < items) {
+#pragma unroll
+      for (int r = 0; r < kRopeRows; ++r)
+        if (at[r] >= 0) raw[r].load((const In*)p.x + at[r] * p.x_stride + head * D, a, b);
+    }
+    if (i < (int)blockDim.x) {  // once
+      for (int k = threadIdx.x; k < kRopeRows * pairs; k += blockDim.x) {
+        const int r = k / pairs, j = k - r * pairs, t = r == 0 ? pos[0] : r == 1 ? pos[1] : r == 2 ? pos[2] : pos[3];
+        ((float2*)turns[r])[(j % 8 / 2 * per + j / 8) * 2 + j % 2] = turn_at(p.rope.turns[j], (uint32_t)max(t, 0), p.rope.amplitude);
+      }
+      __syncthreads();
+    }
+    if (i >= items) continue;
+#pragma unroll
+    for (int r = 0; r < kRopeRows; ++r) {
+      if (at[r] < 0) continue;
+      float x[16];
+      raw[r].get(x);
+      if (turned) turn_item(x, &turns[r][item], per, half);
+      Out* dst = (Out*)p.out + at[r] * p.out_stride + head * D;
+      store8<Out>(dst + 8 * a, x);
+      store8<Out>(dst + 8 * b, x + 8);
+    }
   }
 }
 
 template <int D, typename In>
 static void launch_rope(const RopeParams& p, int out_type, unsigned ctas, cudaStream_t st) {
+  const unsigned threads = std::min(kRopeThreads, (p.heads * (D / 16) + 31) / 32 * 32);
   if (out_type == WAVE_F32)
-    k_rope<D, In, float><<<ctas, kRopeThreads, 0, st>>>(p);
+    k_rope<D, In, float><<<ctas, threads, 0, st>>>(p);
   else if (out_type == WAVE_BF16)
-    k_rope<D, In, __nv_bfloat16><<<ctas, kRopeThreads, 0, st>>>(p);
+    k_rope<D, In, __nv_bfloat16><<<ctas, threads, 0, st>>>(p);
   else
-    k_rope<D, In, __half><<<ctas, kRopeThreads, 0, st>>>(p);
+    k_rope<D, In, __half><<<ctas, threads, 0, st>>>(p);
 }
 template <int D>
 static void launch_rope_in(const RopeParams& p, int type, int out_type, unsigned ctas, cudaStream_t st) {
@@ -112,8 +127,7 @@ static int apply(RopeParams& p, const wave_rope* rope, int n_heads, int head_dim
   p.out = out;
   p.x_stride = x_stride;
   p.out_stride = out_stride;
-  p.rows_per_cta = 1;
-  const long long ctas = (p.tokens + p.rows_per_cta - 1) / p.rows_per_cta;
+  const long long ctas = (p.tokens + kRopeRows - 1) / kRopeRows;
   if (ctas > 0x7fffffff) return WAVE_EINVAL;
   if (head_dim == 128)
     launch_rope_in<128>(p, type, out_type, (unsigned)ctas, (cudaStream_t)stream);
