@@ -27,7 +27,8 @@ struct HistoryAppendParams {
   History hist;
   wave_rope rope;                          // dims 0: no rotation
   int heads;                               // of q
-  int per_cta;                             // head rows (of q, k and v) that a CTA works on
+  int per_cta;                             // head rows that a CTA works on
+  int kv_ctas, q_team;                     // blocks: the CTAs of K and V; q's are behind them, in teams of so many threads
   long long stride;
   const void* qkv;
   void* q;                                 // [rows][heads][D], or null
@@ -153,12 +154,12 @@ __global__ void __launch_bounds__(kAppendThreads2) k_append_tokens(const __grid_
   }
 }
 
-// Blocks of 16 to 128 tokens of prompts.  A CTA takes the tokens that the call
-// has of one block, and some of the head rows: one pass over them, values kept
-// in registers between the block's largest magnitude and the codes, the next
-// head row's on their way meanwhile.  The turns of the block's positions are
-// made once, into shared memory, for all its heads.  kLog: the block is 1 <<
-// kLog tokens.
+// Blocks of 16 to 128 tokens of prompts.  For K and V a CTA takes the tokens that
+// the call has of one block, and some of the heads: one pass over them, values
+// kept in registers between the block's largest magnitude and the codes, the
+// next head's on their way meanwhile.  For q, which has no blocks, a team of
+// threads takes four tokens with all heads.  So the turns of a position are made for few
+// CTAs (into shared memory), and none for V.  kLog: the block is 1 << kLog tokens.
 template <int D, int kLog>
 struct BlockShape {
   static constexpr int kLanes = D / 16, kItems = (1 << kLog) * kLanes;  // of a head row
@@ -173,8 +174,55 @@ __global__ void __launch_bounds__((BlockShape<D, kLog>::kThreads)) k_append_bloc
   constexpr int kLanes = B::kLanes, kPer = B::kPer, kGroup = B::kGroup, kGroups = B::kGroups;
   extern __shared__ float4 turns[];  // [token][D / 4]
   __shared__ float most[2][B::kThreads / 32];
-  const int rows = p.heads + 2 * p.hist.heads, chunks = (rows + p.per_cta - 1) / p.per_cta;
-  const int unit = blockIdx.x / chunks, first = (blockIdx.x - unit * chunks) * p.per_cta, last = min(first + p.per_cta, rows);
+  const bool half = p.rope.layout == WAVE_ROPE_HALF;
+  if ((int)blockIdx.x >= p.kv_ctas) {  // q
+    constexpr int kTokens = 4;
+    const int team = p.q_team, sub = threadIdx.x / team, tid = threadIdx.x % team, total = p.b.cum[p.b.n];
+    const int first = (((int)blockIdx.x - p.kv_ctas) * (B::kThreads / team) + sub) * kTokens;
+    float4* mine = turns + sub * kTokens * (D / 4);
+    size_t row[kTokens];
+    int pos[kTokens];
+#pragma unroll
+    for (int r = 0; r < kTokens; ++r) {
+      const int t = min(first + r, total - 1), s = seq_of(p.b, t), n = t - p.b.cum[s];
+      row[r] = p.b.begin[s] + n;
+      pos[r] = p.b.start[s] + n;
+    }
+    const int items = p.heads * kLanes;
+    for (int i = tid; i < (items + team - 1) / team * team; i += team) {
+      const int r0 = i / kLanes;
+      int a, b;
+      bool turned;
+      groups_of_item(p.rope, i % kLanes, a, b, turned);
+      Raw16<In> raw[kTokens];
+#pragma unroll
+      for (int r = 0; r < kTokens; ++r)
+        if (i < items && first + r < total) raw[r].load((const In*)p.qkv + row[r] * p.stride + r0 * D, a, b);
+      if (i < team) {  // once
+        const int pairs = p.rope.dims / 2, per = p.rope.dims / 16;
+        for (int k = tid; k < kTokens * pairs; k += team) {
+          const int r = k / pairs, j = k - r * pairs, t = r == 0 ? pos[0] : r == 1 ? pos[1] : r == 2 ? pos[2] : pos[3];
+          ((float2*)(mine + r * (D / 4)))[(j % 8 / 2 * per + j / 8) * 2 + j % 2] = turn_at(p.rope.turns[j], (uint32_t)t, p.rope.amplitude);
+        }
+        __syncthreads();
+      }
+#pragma unroll
+      for (int r = 0; r < kTokens; ++r) {
+        if (i >= items || first + r >= total) continue;
+        float x[16];
+        raw[r].get(x);
+        if (turned) turn_item(x, mine + r * (D / 4) + i % kLanes, p.rope.dims / 16, half);
+        Out* dst = (Out*)p.q + (row[r] * p.heads + r0) * D;
+        store8<Out>(dst + 8 * a, x);
+        store8<Out>(dst + 8 * b, x + 8);
+      }
+    }
+    return;
+  }
+  // K and V: (block, K or V, some heads)
+  const int chunks = (p.hist.heads + p.per_cta - 1) / p.per_cta, unit = blockIdx.x / (2 * chunks);
+  const int which = ((int)blockIdx.x - unit * 2 * chunks) / chunks, first = (blockIdx.x % chunks) * p.per_cta;
+  const int last = min(first + p.per_cta, p.hist.heads);
   int lo = 0, hi = p.b.n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -192,26 +240,26 @@ __global__ void __launch_bounds__((BlockShape<D, kLog>::kThreads)) k_append_bloc
   int a, b;
   bool turned;
   groups_of_item(p.rope, lane, a, b, turned);
-  const bool half = p.rope.layout == WAVE_ROPE_HALF;
+  turned = turned && !which;
   const size_t row0 = p.b.begin[lo] + (from - start);
   Raw16<In> raw[kPer];
   auto load = [&](int r) {
-    const bool on = r < last && (r >= p.heads || p.q);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int t = t0 + i * kStep;
-      if (on && from + t < to)
-        raw[i].load((const In*)p.qkv + (row0 + t) * p.stride + r * D, a, b);
+      if (r < last && from + t < to)
+        raw[i].load((const In*)p.qkv + (row0 + t) * p.stride + (p.heads + which * p.hist.heads + r) * D, a, b);
       else
         raw[i].clear();
     }
   };
   load(first + g);
-  make_turns(p.rope, turns, D / 4, to - from, from);
-  __syncthreads();
+  if (!which) {
+    make_turns(p.rope, turns, D / 4, to - from, from);
+    __syncthreads();
+  }
   for (int it = 0, r0 = first; r0 < last; ++it, r0 += kGroups) {
     const int r = r0 + g;
-    const bool is_q = r < p.heads, is_v = r >= p.heads + p.hist.heads, on = r < last && (!is_q || p.q);
     float x[kPer][16];
     float amax = 0.f;
 #pragma unroll
@@ -220,28 +268,20 @@ __global__ void __launch_bounds__((BlockShape<D, kLog>::kThreads)) k_append_bloc
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int t = t0 + i * kStep;
-      if (!on || from + t >= to) continue;
-      if (turned && !is_v) turn_item(x[i], turns + t * (D / 4) + lane, p.rope.dims / 16, half);
-      if (is_q) {
-        Out* dst = (Out*)p.q + ((row0 + t) * p.heads + r) * D;
-        store8<Out>(dst + 8 * a, x[i]);
-        store8<Out>(dst + 8 * b, x[i] + 8);
-      } else {
+      if (turned && from + t < to) turn_item(x[i], turns + t * (D / 4) + lane, p.rope.dims / 16, half);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) amax = fmaxf(amax, counts(x[i][e]));
-      }
+      for (int e = 0; e < 16; ++e) amax = fmaxf(amax, counts(x[i][e]));  // 0 where there is no token
     }
-    if (r0 + kGroups <= p.heads) continue;  // all of q: the same for the whole CTA
-    const bool mine = on && !is_q;
-    const size_t hr = mine ? p.hist.row(is_v, slot, r - p.heads - (is_v ? p.hist.heads : 0)) : 0;
+    const bool on = r < last;
+    const size_t hr = p.hist.row(which, slot, on ? r : first);
     uint8_t* codes = p.hist.codes + hr * p.hist.T_max * D;
     float* scales = p.hist.scales + hr * p.hist.blocks;
-    const float old = mine && held ? scales[blk] : 0.f;
+    const float old = on && held ? scales[blk] : 0.f;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, d));
     if (threadIdx.x % 32 == 0) most[it & 1][threadIdx.x / 32] = amax;
     __syncthreads();  // most[it & 1] is written again after the next one, which comes after it has been read
-    if (!mine) continue;
+    if (!on) continue;
 #pragma unroll
     for (int w = 0; w < kGroup / 32; ++w) amax = fmaxf(amax, most[it & 1][g * (kGroup / 32) + w]);
     float sc = block_scale(amax);
@@ -273,19 +313,25 @@ static cudaError_t launch_blocks(HistoryAppendParams& p, int sms, cudaStream_t s
     const cudaError_t e = cudaFuncSetAttribute(k_append_blocks<D, kLog, In, Out>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
   }
-  // head rows of a CTA: up to eight rounds of them, fewer where that leaves SMs without work
-  const int rows = p.heads + 2 * p.hist.heads, units = p.first_block[p.b.n];
-  const long long share = (long long)units * rows / (4LL * sms * B::kGroups);
+  // Heads of a CTA: up to eight rounds of them, fewer where that leaves SMs
+  // without work (a CTA of 512 threads has an SM to itself).
+  const int units = p.first_block[p.b.n];
+  const long long share = 2LL * units * p.hist.heads / ((B::kThreads > 256 ? 2LL : 4LL) * sms * B::kGroups);
   p.per_cta = B::kGroups * (int)std::max(1LL, std::min(8LL, share));
-  const int chunks = (rows + p.per_cta - 1) / p.per_cta;
-  k_append_blocks<D, kLog, In, Out><<<(unsigned)(units * chunks), B::kThreads, kSmem, st>>>(p);
+  const int chunks = (p.hist.heads + p.per_cta - 1) / p.per_cta;
+  p.kv_ctas = units * 2 * chunks;
+  p.q_team = 256;
+  while (p.q_team > 64 && p.heads * B::kLanes <= p.q_team / 2) p.q_team /= 2;
+  const int tokens = 4 * (B::kThreads / p.q_team), q_ctas = p.q ? (p.b.cum[p.b.n] + tokens - 1) / tokens : 0;
+  static_assert(4 * B::kThreads / 64 * D * 4 <= kSmem, "q's turns");
+  k_append_blocks<D, kLog, In, Out><<<(unsigned)(p.kv_ctas + q_ctas), B::kThreads, kSmem, st>>>(p);
   return cudaGetLastError();
 }
 
 template <int D, typename In, typename Out>
 static cudaError_t launch_history_append(HistoryAppendParams& p, int tokens, int sms, cudaStream_t st) {
-  const int rows = p.heads + 2 * p.hist.heads;
   if (p.positions || p.hist.block == 1) {
+    const int rows = p.heads + 2 * p.hist.heads;
     // head rows of a CTA: all of them, or one for each group of lanes where tokens are few
     constexpr int kGroups = kAppendThreads2 / (D / 16);
     p.per_cta = tokens >= 8 * sms ? rows : kGroups;
