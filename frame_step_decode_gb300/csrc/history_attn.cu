@@ -56,7 +56,7 @@ static int attention(wave_t* h, HistoryAttnParams& p, int tokens, int type, cons
   p.err_out = h->err_host_dev;
   cudaStream_t st = (cudaStream_t)stream;
   h->last_stream = st;
-  // Sequences whose rows fit one tile of few rows, and the others.
+  // Sequences of few rows, and the others.
   HistoryAttnParams many = p;
   if (p.positions) {
     p.n = tokens;

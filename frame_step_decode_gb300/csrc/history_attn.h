@@ -14,7 +14,7 @@ struct HistoryAttnParams {
   int n;                     // sequences, or rows of the frame
   History hist;
   int heads, group;
-  int tiles;                 // few rows: of a K/V head's rows
+  int tiles;                 // few rows: a frame's, of a K/V head's rows
   const uint16_t* q;
   uint16_t* out;
   long long q_stride, out_stride;
@@ -24,7 +24,9 @@ struct HistoryAttnParams {
   int *err, *err_out;
 };
 
-constexpr int kFewRows = 16;  // rows (tokens times heads of a group) of one unit of few rows
+constexpr int kFewTile = 16;                     // rows (tokens times heads of a group) of a unit of few rows
+constexpr int kFewTiles = 2;                     // units of a prompt and K/V head at most
+constexpr int kFewRows = kFewTile * kFewTiles;
 
 cudaError_t launch_history_few(HistoryAttnParams& p, int D, int type, int rows, int sms, cudaStream_t st);
 

@@ -83,6 +83,12 @@ struct FewTables {
   int keys[WAVE_MAX_SEQS];       // what its last token sees
 };
 
+// Row tiles of a K/V head: the same for all of a frame, by a prompt's length.
+template <int kR>
+__device__ __forceinline__ int tiles_of(const HistoryAttnParams& p, int seq) {
+  return p.positions ? p.tiles : (p.b.len(seq) * p.group + kR - 1) / kR;
+}
+
 __device__ __forceinline__ FewPlace place_of(const HistoryAttnParams& p, const FewTables& tab, int at) {  // by a whole warp
   const int lane = threadIdx.x & 31;
   int seq = -1;
@@ -99,10 +105,11 @@ __device__ __forceinline__ FewPlace place_of(const HistoryAttnParams& p, const F
   return w;
 }
 // The next chunk of the line, which has one.
+template <int kR>
 __device__ __forceinline__ void advance(const HistoryAttnParams& p, const FewTables& tab, FewPlace& w) {
   if (++w.chunk < w.chunks) return;
   w.chunk = 0;
-  if (++w.unit < p.hist.heads * p.tiles) return;
+  if (++w.unit < p.hist.heads * tiles_of<kR>(p, w.seq)) return;
   w.unit = 0;
   do ++w.seq;
   while (tab.keys[w.seq] == 0);
@@ -119,7 +126,7 @@ struct FewRow {
 };
 template <int kR>
 __device__ __forceinline__ FewRow row_of(const HistoryAttnParams& p, const FewPlace& w, int r) {
-  const int head = w.unit / p.tiles, i = (w.unit - head * p.tiles) * kR + r;
+  const int tiles = tiles_of<kR>(p, w.seq), head = w.unit / tiles, i = (w.unit - head * tiles) * kR + r;
   const int t = i / p.group, len = p.positions ? 1 : p.b.len(w.seq);
   FewRow x;
   x.on = t < len;
@@ -160,7 +167,7 @@ __global__ void __launch_bounds__((FewShape<D, kN>::kThreads), 1) k_history_few(
         const int pos = p.positions[s];
         keys = pos < 0 ? 0 : pos >= p.hist.T_max ? -1 : pos + 1;
       }
-      if (keys > 0) mine = (keys + kFewChunk - 1) / kFewChunk * p.hist.heads * p.tiles;
+      if (keys > 0) mine = (keys + kFewChunk - 1) / kFewChunk * p.hist.heads * tiles_of<kR>(p, s);
     }
     int sum = mine;
 #pragma unroll
@@ -270,7 +277,7 @@ __global__ void __launch_bounds__((FewShape<D, kN>::kThreads), 1) k_history_few(
     const uint8_t *kc = nullptr, *vc = nullptr;
     const float *ks = nullptr, *vs = nullptr;
     auto unit_pointers = [&]() {
-      const int slot = p.positions ? in.seq : p.b.slot[in.seq], head = in.unit / p.tiles;
+      const int slot = p.positions ? in.seq : p.b.slot[in.seq], head = in.unit / tiles_of<kR>(p, in.seq);
       const size_t kr = p.hist.row(0, slot, head), vr = p.hist.row(1, slot, head);
       kc = p.hist.codes + kr * p.hist.T_max * D;
       vc = p.hist.codes + vr * p.hist.T_max * D;
@@ -305,7 +312,7 @@ __global__ void __launch_bounds__((FewShape<D, kN>::kThreads), 1) k_history_few(
         cp4(dst + 2 * L::kCodes + lane * 4, (lane < 16 ? ks : vs) + (there ? tok >> p.hist.shift : 0), there);
         if (++issued < end) {
           const int unit = in.unit, seq = in.seq;
-          advance(p, tab, in);
+          advance<kR>(p, tab, in);
           if (in.unit != unit || in.seq != seq) {
             unit_pointers();
             // its queries, on their way to L1 while the unit at hand is worked on
@@ -536,7 +543,7 @@ __global__ void __launch_bounds__((FewShape<D, kN>::kThreads), 1) k_history_few(
         }
         fresh = true;
       }
-      if (c + 1 < end) advance(p, tab, at);
+      if (c + 1 < end) advance<kR>(p, tab, at);
     }
   }
 
@@ -620,7 +627,7 @@ __global__ void __launch_bounds__((FewShape<D, kN>::kThreads), 1) k_history_few(
       }
       __threadfence();
       __syncwarp();
-      int* cnt = p.part_cnt + (u.seq * p.heads + u.unit) * 4 + (task & 3);
+      int* cnt = p.part_cnt + (u.seq * (kFewTiles * p.heads) + u.unit) * 4 + (task & 3);
       int there = 0;
       if (lane == 0) there = atomicAdd(cnt, 1);
       write = __shfl_sync(0xffffffffu, there, 0) == c1 - c0;
@@ -628,11 +635,12 @@ __global__ void __launch_bounds__((FewShape<D, kN>::kThreads), 1) k_history_few(
         __threadfence();
         if (lane == 0) *cnt = 0;  // for the next launch
         clear();
-        for (int c = c0; c <= c1; c += kBatch) {
-          float2 ml[kBatch][kEach];
-          float4 v[kBatch][kEach];
+        constexpr int kFar = 16 / kEach;
+        for (int c = c0; c <= c1; c += kFar) {
+          float2 ml[kFar][kEach];
+          float4 v[kFar][kEach];
 #pragma unroll
-          for (int f = 0; f < kBatch; ++f) {
+          for (int f = 0; f < kFar; ++f) {
             const float* src = p.part + (size_t)min(c + f, c1) * L::kPart + (c + f == c0 ? L::kSums : 0);
 #pragma unroll
             for (int i = 0; i < kEach; ++i) {
@@ -642,7 +650,7 @@ __global__ void __launch_bounds__((FewShape<D, kN>::kThreads), 1) k_history_few(
             }
           }
 #pragma unroll
-          for (int f = 0; f < kBatch; ++f)
+          for (int f = 0; f < kFar; ++f)
 #pragma unroll
             for (int i = 0; i < kEach; ++i)
               if (c + f <= c1) add(i, ml[f][i], v[f][i]);
@@ -679,8 +687,8 @@ cudaError_t configure_history_few() {
 
 template <int D, bool kF16>
 static cudaError_t launch(HistoryAttnParams& p, int rows, int sms, cudaStream_t st) {
-  const int tile = rows <= 8 ? 8 : kFewRows;
-  p.tiles = (rows + tile - 1) / tile;  // more than one for a frame with more than 16 heads to a K/V head
+  const int tile = rows <= 8 ? 8 : kFewTile;
+  p.tiles = (p.group + tile - 1) / tile;  // a frame's
   if (tile == 8)
     k_history_few<D, kF16, 1><<<sms, FewShape<D, 1>::kThreads, FewShape<D, 1>::kTotal, st>>>(p);
   else

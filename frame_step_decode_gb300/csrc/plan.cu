@@ -270,7 +270,7 @@ size_t carve_workspace(const Plan& pl, char* base, Workspace* ws) {
       {(void**)&w.ssm_out, (size_t)(SP * pl.d_inner * 2)},
       {(void**)&w.part_o, pl.prompts ? 2 * (size_t)pl.grid * 256 * D * 4 : 0},
       {(void**)&w.part_ml, pl.prompts ? 2 * (size_t)pl.grid * 256 * 8 : 0},
-      {(void**)&w.hist_cnt, pl.prompts ? (size_t)pl.S_max * H * 16 : 0},
+      {(void**)&w.hist_cnt, pl.prompts ? (size_t)pl.S_max * H * 32 : 0},
       {(void**)&w.seg_state, pl.hybrid && pl.prompts ? (size_t)pl.grid * 2 * kSsmP * kSsmN * 4 : 0},
       {(void**)&w.seg_decay, pl.hybrid && pl.prompts ? (size_t)pl.grid * 2 * 4 : 0},
   };
