@@ -24,6 +24,9 @@ struct HistoryAttnParams {
   int *err, *err_out;
 };
 
+// Whether one of four codes is NaN.
+__device__ __forceinline__ bool any_nan_code(uint32_t w) { return (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0; }
+
 constexpr int kFewTile = 16;                     // rows (tokens times heads of a group) of a unit of few rows
 constexpr int kFewTiles = 2;                     // units of a prompt and K/V head at most
 constexpr int kFewRows = kFewTile * kFewTiles;

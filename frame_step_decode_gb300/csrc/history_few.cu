@@ -69,7 +69,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {  // an 8 x 8 tile o
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
 }
-__device__ __forceinline__ bool any_nan_code(uint32_t w) { return (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0; }
 
 // Where a chunk of the line lies.
 struct FewPlace {

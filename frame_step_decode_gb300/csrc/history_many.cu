@@ -546,7 +546,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
       for (int j = from; j < last && ok; ++j, ++m_it) {
         const int mi = m_it % L::kMetas;
         BlockMeta& meta = metas[mi];
-        uint32_t ratio = 0;  // the lane's scale over the tile's, as two fp16
+        uint32_t ratio = 0;  // the lane's scale over the tile's (a block of 128: V's), as two fp16
         if (!wait_warp(L::kMetaEmpty + mi, ((m_it / L::kMetas) & 1) ^ 1)) break;
         if constexpr (kScale == kScaleOfToken) {
           if (warp == 8) {
@@ -581,19 +581,16 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
             for (int d = 4; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
           }
           const int e = top > 0.f ? min(max(exponent_up(top), lane < 8 ? -120 : -100), 120) : -100;
-          // K's codes have room for 2^6 more in fp16
-          const float r = sc[0] * power(-e) * (kScale == kScaleOfBlock && lane < 8 ? 64.f : 1.f);
+          // K's codes have room for 2^6 more in fp16; the scale of a block of 128 is a factor of K's scores as it is
+          const float r = sc[0] * power(-e) * (lane < 8 ? 64.f : 1.f);
           ratio = half2_of(r, r);
           const int ev = __shfl_sync(0xffffffffu, e, 8);
-          const float rv = __shfl_sync(0xffffffffu, r, 8);
           if (warp == 8 && lane == 0) {
-            if constexpr (kScale == kScaleOfBlock) {
-              meta.factor = power(e) * 0x1p-6f, meta.shift = (float)ev, meta.back = power(-ev);
-            } else {  // the scales themselves: a V scale that is no power of two is another factor of the weights
-              meta.factor = sc[0], meta.shift = (float)ev, meta.back = power(-ev);
-            }
+            meta.factor = kScale == kScaleOfBlock ? power(e) * 0x1p-6f : sc[0];
+            meta.shift = (float)ev;
+            meta.back = power(-ev);
           }
-          if constexpr (kScale == kScaleOfTile) ratio = half2_of(rv, rv);
+          if constexpr (kScale == kScaleOfTile) ratio = __shfl_sync(0xffffffffu, ratio, 8);
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::kMetaFull + mi));
@@ -611,28 +608,36 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
           if (!wait_warp(L::kEmpty + slot, ((tiles / L::kStages) & 1) ^ 1)) break;
           uint8_t* dst = smem + L::kRing + slot * L::kTile;
           const bool look = which && j >= first_cut;
-          // a product is needed where codes of several scales meet, or the V scale of a block of 128 is no power of two
-          const bool times = kScale == kScaleOfBlock || (kScale == kScaleOfTile && which && ratio != 0x3C003C00u);
           bool odd = false;
+          if (look) {  // apart: a branch in the loop below keeps its pieces from being worked on together (5% of the whole)
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i) {
+              const uint32_t c[4] = {code[which][i].x, code[which][i].y, code[which][i].z, code[which][i].w};
+#pragma unroll
+              for (int x = 0; x < 4; ++x) odd |= any_nan_code(c[x]);
+            }
+          }
 #pragma unroll
           for (int i = 0; i < kPieces; ++i) {
             const uint32_t c[4] = {code[which][i].x, code[which][i].y, code[which][i].z, code[which][i].w};
             uint32_t h[8];
-            if (look) {
-#pragma unroll
-              for (int x = 0; x < 4; ++x) odd |= (((c[x] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
-            }
 #pragma unroll
             for (int x = 0; x < 4; ++x) e4m3x4_to_f16x2x2(c[x], h[2 * x], h[2 * x + 1]);
-            if (times) {
-              const uint32_t r = kScale == kScaleOfBlock
-                                     ? __shfl_sync(0xffffffffu, ratio, ((prow + i * kRowStep) >> p.a.hist.shift) + 8 * which)
-                                     : ratio;
+            if constexpr (kScale == kScaleOfBlock) {
+              const uint32_t r = __shfl_sync(0xffffffffu, ratio, ((prow + i * kRowStep) >> p.a.hist.shift) + 8 * which);
 #pragma unroll
               for (int x = 0; x < 8; ++x) h[x] = mul_half2(h[x], r);
             }
             *(uint4*)(dst + to0 + i * (kRowStep * 128)) = make_uint4(h[0], h[1], h[2], h[3]);
             *(uint4*)(dst + to1 + i * (kRowStep * 128)) = make_uint4(h[4], h[5], h[6], h[7]);
+          }
+          if (kScale == kScaleOfTile && which && ratio != 0x3C003C00u) {  // a V scale that is no power of two, or 0
+#pragma unroll 1
+            for (int i = 0; i < 2 * kPieces; ++i) {
+              uint4* at = (uint4*)(dst + (i & 1 ? to1 : to0) + (i >> 1) * (kRowStep * 128));
+              const uint4 h = *at;
+              *at = make_uint4(mul_half2(h.x, ratio), mul_half2(h.y, ratio), mul_half2(h.z, ratio), mul_half2(h.w, ratio));
+            }
           }
           if (look && __any_sync(0xffffffffu, odd)) {
             // NaN in a tile that some row does not see all of (0 x NaN would
