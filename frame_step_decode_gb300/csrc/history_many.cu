@@ -286,6 +286,19 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
         if (!wait_warp(L::kSFull + st, s_it & 1)) break;
         ++s_it;
         tc_fence_after();
+        if (kScale != kScaleOfToken && j >= cut) {  // masked in place: the loop below has no branch
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t s[32];
+            tmem_ld32(tS(st) + lanes + 32 * c, s);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (32 * c + i > seen) s[i] = __float_as_uint(-INFINITY);
+            tmem_st32(tS(st) + lanes + 32 * c, s);
+          }
+          tmem_st_wait();
+        }
         // 32 columns, scaled and masked; and their largest
         auto ready = [&](int c, uint32_t* s) {
           if constexpr (kScale == kScaleOfToken) {
@@ -298,7 +311,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
               s[4 * i + 3] = __float_as_uint(__uint_as_float(s[4 * i + 3]) * f.w);
             }
           }
-          if (j >= cut) {
+          if (kScale == kScaleOfToken && j >= cut) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if (32 * c + i > seen) s[i] = __float_as_uint(-INFINITY);
