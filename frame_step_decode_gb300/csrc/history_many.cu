@@ -23,6 +23,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "history_attn.h"
 
@@ -300,7 +301,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
           tmem_st_wait();
         }
         // 32 columns, scaled and masked; and their largest
-        auto ready = [&](int c, uint32_t* s) {
+        auto ready = [&](int c, uint32_t* s, auto masked) {
           if constexpr (kScale == kScaleOfToken) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -311,20 +312,22 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
               s[4 * i + 3] = __float_as_uint(__uint_as_float(s[4 * i + 3]) * f.w);
             }
           }
-          if (kScale == kScaleOfToken && j >= cut) {
+          if constexpr (masked.value) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if (32 * c + i > seen) s[i] = __float_as_uint(-INFINITY);
           }
         };
-        auto largest = [&]() {
+        constexpr std::true_type kMasked;
+        constexpr std::false_type kAll;
+        auto largest = [&](auto masked) {
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             uint32_t s[32];
             tmem_ld32(tS(st) + lanes + 32 * c, s);
             tmem_ld_wait();
-            ready(c, s);
+            ready(c, s, masked);
 #pragma unroll
             for (int i = 0; i < 32; i += 8)
 #pragma unroll
@@ -355,8 +358,8 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
           }
         };
         float2 sum[4];
-        auto weights = [&](int c, uint32_t* x, uint32_t* w, float neg) {  // of 32 columns
-          ready(c, x);
+        auto weights = [&](int c, uint32_t* x, uint32_t* w, float neg, auto masked) {  // of 32 columns
+          ready(c, x, masked);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             float2 e = make_float2(ex2(fmaf(__uint_as_float(x[2 * i]), z, neg)), ex2(fmaf(__uint_as_float(x[2 * i + 1]), z, neg)));
@@ -376,32 +379,40 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
           sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
           sum[0].x += sum[0].y;
         };
-        if (j == 0) m = largest();
         if constexpr (kScale == kScaleOfToken) {
           // With a block's scales in registers too, P cannot be held back: the
           // maximum comes first, and P is written as it is made (over columns of
           // S that have been read).
-          if (j > 0) {
-            const float top = largest();
-            const bool up = top > m + 8.f;
-            if (__any_sync(0xffffffffu, up)) raise(top, up);
-          }
-          const float neg = relative();
-          uint32_t s[2][32];
-          tmem_ld32(tS(st) + lanes, s[0]);
-#pragma unroll 1
-          for (int c = 0; c < 4; c += 2) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t w[16];
-              tmem_ld_wait();
-              if (c + h < 3) tmem_ld32(tS(st) + lanes + 32 * (c + h + 1), s[1 - h]);
-              weights(c + h, s[h], w, neg);
-              tmem_st16(tS(st) + lanes + 16 * (c + h), w);
+          auto block = [&](auto masked) {
+            const float top = largest(masked);
+            if (j == 0) {
+              m = top;
+            } else {
+              const bool up = top > m + 8.f;
+              if (__any_sync(0xffffffffu, up)) raise(top, up);
             }
-          }
+            const float neg = relative();
+            uint32_t s[2][32];
+            tmem_ld32(tS(st) + lanes, s[0]);
+#pragma unroll 1
+            for (int c = 0; c < 4; c += 2) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint32_t w[16];
+                tmem_ld_wait();
+                if (c + h < 3) tmem_ld32(tS(st) + lanes + 32 * (c + h + 1), s[1 - h]);
+                weights(c + h, s[h], w, neg, masked);
+                tmem_st16(tS(st) + lanes + 16 * (c + h), w);
+              }
+            }
+          };
+          if (j >= cut)
+            block(kMasked);
+          else
+            block(kAll);
           add_up();
         } else {
+          if (j == 0) m = largest(kAll);
           uint32_t w[64];
 #pragma unroll 1
           for (bool again = false;; again = true) {
@@ -412,11 +423,11 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
             for (int c = 0; c < 4; ++c) {
               tmem_ld_wait();
               if (c < 3) tmem_ld32(tS(st) + lanes + 32 * (c + 1), s[(c + 1) & 1]);
-              weights(c, s[c & 1], w + 16 * c, neg);
+              weights(c, s[c & 1], w + 16 * c, neg, kAll);
             }
             add_up();
             if (j == 0 || again || !__any_sync(0xffffffffu, !(sum[0].x <= 60000.f))) break;
-            const float top = largest();
+            const float top = largest(kAll);
             raise(top, top > m);
           }
           tmem_st32(tS(st) + lanes, w);
