@@ -850,3 +850,137 @@ def test_refusals():
             bad()
     assert bool((out == 7).all()) and bool((c.kv == 0x7F).all())
     _done(w)
+
+
+@pytest.mark.parametrize("lens,starts,H,Hkv", [([300] * 20, [40 * i for i in range(20)], 8, 8), ([200, 1, 40, 3, 16, 33, 900], [0, 5, 700, 90, 300, 2, 1], 8, 4),
+                                               ([5, 6, 7, 8, 9, 1], [300] * 6, 16, 4)])
+@pytest.mark.parametrize("D,block", [(128, 1), (64, 64)])
+def test_attention_of_few_and_many_rows_together(lens, starts, H, Hkv, D, block):
+    """More units than SMs; prompts of few rows, of two tiles of them and of many in one call; and each alone, within the bounds."""
+    c, q, out = _attend(lens, starts, H, Hkv, D, block, F16, seed=7, first=1, tail=1)
+
+
+@pytest.mark.parametrize("frame", [False, True])
+@pytest.mark.parametrize("block", [16, 128])
+def test_attention_of_scales_that_are_no_powers_of_two(frame, block):
+    """A history filled by other means: K's and V's scales are then taken to fp16's 11 bits, and so are their products with a
+    code (2^-11 of a key or a value each)."""
+    H, Hkv, D = 4, 2, 64
+    lens, starts = ([1, 1], [300, 1000]) if frame else ([150, 40], [300, 1000])
+    c, cu = _history(lens, [0, 1], starts, 2, Hkv, D, block), _cu(lens)
+    c.sc *= 0.5 + torch.rand(c.sc.shape, generator=_gen(1), device="cuda")
+    q, out = _queries(cu[-1], H, D, BF)
+    w = _wave(H, D, S=2, T=c.T)
+    if frame:
+        w.history_attention_frame(0, torch.tensor(starts, dtype=torch.int32, device="cuda"), q, c.kv, c.sc, Hkv, block, out)
+    else:
+        w.history_attention(0, cu, [0, 1], starts, q, c.kv, c.sc, Hkv, block, out)
+    _done(w)
+    ref, tol = attention_reference(c, q, lens, [0, 1], starts, cu, D ** -0.5)
+    g = H // Hkv
+    for i, (n, s0) in enumerate(zip(lens, starts)):
+        kd, vd = (c.values(which, i, 0, s0 + n).repeat_interleave(g, 0) for which in (0, 1))
+        qd = q[cu[i]:cu[i + 1]].double().transpose(0, 1)
+        later = torch.arange(s0 + n, device="cuda")[None] > s0 + torch.arange(n, device="cuda")[:, None]
+        s = ((qd @ kd.transpose(1, 2)) * D ** -0.5).masked_fill(later, -math.inf)
+        A = torch.softmax(s, -1) @ vd.abs()
+        ds = 2 * 2.0 ** -11 * D ** -0.5 * (qd.abs() @ kd.abs().transpose(1, 2)).masked_fill(later, 0.0).amax(-1, keepdim=True)
+        tol[cu[i]:cu[i + 1]] += ((2 * ds + 2 * 2.0 ** -11) * A * 1.02).transpose(0, 1)
+    assert bool(((out.double() - ref).abs() <= tol).all())
+
+
+def test_history_of_a_hybrid_handle():
+    """The layer is the model's: an attention block's; others are refused."""
+    cfg = fsd.WaveHybridConfig(6, 64, 3, 2, 64, 4, 64, 128, 1e-5, 1e4)
+    w = fsd.HybridWave(cfg, 2, 64)
+    H, D, n, block = 2, 64, 20, 16
+    got = Cache(2, H, 64, D, block, layers=2, layer=1)
+    want = got.clone()
+    x = torch.randn(n, 3 * H * D, generator=_gen(1), device="cuda")
+    for layer in (0, 1, 3, 4, 6):
+        assert w.history_append(layer, [0, n], [1], [0], x, got.kv, got.sc, H, block, check=False) == fsd.WAVE_EINVAL
+    q = torch.zeros(n, H, D, dtype=BF, device="cuda")
+    w.history_append(5, [0, n], [1], [0], x, got.kv, got.sc, H, block, q=q)
+    _, k, v = _split(x, H, H, D)
+    want.write(1, 0, k, v)
+    assert got.same(want)
+    out = torch.zeros_like(q)
+    w.history_attention(5, [0, n], [1], [0], q, got.kv, got.sc, H, block, out)
+    _check(got, q, out, [n], [1], [0], [0, n])
+    _done(w)
+
+
+def test_append_of_128_sequences():
+    H, Hkv, D, T, block = 2, 1, 64, 64, 16
+    lens, starts, slots = [1 + i % 23 for i in range(128)], [(7 * i) % 30 for i in range(128)], [(i * 37) % 128 for i in range(128)]
+    w = _wave(H, D, S=128, T=T)
+    got = Cache(128, Hkv, T, D, block)
+    for s, p in zip(slots, starts):
+        if p:
+            got.write(s, 0, torch.ones(p, Hkv, D, device="cuda"), torch.ones(p, Hkv, D, device="cuda"))
+    want, cu = got.clone(), _cu(lens)
+    x = (4 * torch.randn(cu[-1], (H + 2 * Hkv) * D, generator=_gen(3), device="cuda")).to(BF)
+    w.history_append(0, cu, slots, starts, x, got.kv, got.sc, Hkv, block)
+    _, k, v = _split(x, H, Hkv, D)
+    for i, (n, s, p) in enumerate(zip(lens, slots, starts)):
+        want.write(s, p, k[cu[i]:cu[i + 1]], v[cu[i]:cu[i + 1]])
+    assert got.same(want)
+    _done(w)
+
+
+@pytest.mark.parametrize("index", [0, 1, 5])
+@pytest.mark.parametrize("block", [1, 128])
+def test_attention_whose_tiles_do_not_come(index, block):
+    """The conversion ends before a tile: the waits run out, the launch ends, the status says so once, and the next call on
+    the handle is right."""
+    H, Hkv, D = 4, 2, 128
+    lens, starts = [300, 200], [500, 0]
+    c, cu = _history(lens, [0, 1], starts, 2, Hkv, D, block), _cu(lens)
+    q, out = _queries(cu[-1], H, D, BF)
+    w = _wave(H, D, S=2, T=c.T)
+    call = lambda: w.history_attention(0, cu, [0, 1], starts, q, c.kv, c.sc, Hkv, block, out)  # noqa: E731
+    call()
+    assert w.status() == fsd.WAVE_OK
+    w.set_timeout_ns(20_000_000)
+    w.debug_skip_signal(11, index)
+    call()
+    assert w.status() == fsd.WAVE_ETIMEOUT and w.status() == fsd.WAVE_OK
+    w.debug_skip_signal(11, -1)
+    out.fill_(7)
+    call()
+    _check(c, q, out, lens, [0, 1], starts, cu)
+    w.set_timeout_ns(1)  # no wait gets any time
+    call()
+    assert w.status() == fsd.WAVE_ETIMEOUT
+    w.set_timeout_ns(2_000_000_000)
+    out.fill_(7)
+    call()
+    _check(c, q, out, lens, [0, 1], starts, cu)
+    _done(w)
+
+
+def test_calls_replayed_from_graphs_that_share_a_handle():
+    """Two captured calls of one handle, of few and of many rows, replayed one after another and in either order."""
+    H, Hkv, D, block = 8, 2, 128, 64
+    lens, starts = [[1] * 3, [200, 3, 60]], [[700, 5, 2000], [300, 900, 0]]
+    cs = [_history(n, [0, 1, 2], s, 3, Hkv, D, block, seed=i, T=2004) for i, (n, s) in enumerate(zip(lens, starts))]
+    w = _wave(H, D, S=3, T=2004)
+    qs = [_queries(sum(n), H, D, BF, seed=i) for i, n in enumerate(lens)]
+    graphs = []
+    for (q, out), c, n, s in zip(qs, cs, lens, starts):
+        call = lambda: w.history_attention(0, _cu(n), [0, 1, 2], s, q, c.kv, c.sc, Hkv, block, out)  # noqa: E731
+        call()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        graphs.append(g)
+    for order in ((0, 1), (1, 0), (0, 0), (1, 1, 0)):
+        for q, out in qs:
+            out.fill_(7)
+        for i in order:
+            graphs[i].replay()
+        torch.cuda.synchronize()
+        for i in set(order):
+            _check(cs[i], qs[i][0], qs[i][1], lens[i], [0, 1, 2], starts[i], _cu(lens[i]))
+    _done(w)
