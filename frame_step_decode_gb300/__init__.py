@@ -600,7 +600,8 @@ class Wave:
         tile, 4 down tile, 5 norm row; hybrid: 6 selective-state
         in-projection tile, 7 a CTA's finished state items, 8 selective-state
         out-projection tile; prompts: 9 a CTA's K/V tile of the attention, 10
-        a CTA's chunk of the selective state); index < 0 disables."""
+        a CTA's chunk of the selective state, 11 a CTA's K/V tile of the
+        attention over the history); index < 0 disables."""
         rc = lib().wave_debug_skip_signal(self.h, which, index)
         if rc != WAVE_OK:
             raise WaveError(rc, "wave_debug_skip_signal")

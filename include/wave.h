@@ -77,8 +77,9 @@ typedef struct wave_ctx wave_t; /* opaque; owns only its device workspace */
  * workspace on the current device (activations, partial sums, the RoPE
  * cos/sin table, barrier words; about 0.5 MB + S_max * (2.1 * d_model + ...)
  * bytes, e.g. ~60 MB for the 7B-class shape at S_max = 128; and what the calls
- * on prompts leave between their launches, 20 MB for heads of 128, 10 MB for
- * heads of 64, 10 MB more for a hybrid handle) and one pinned, device-mapped
+ * on prompts and on the history in blocks leave between their launches, 40 MB
+ * for heads of 128, 20 MB for heads of 64, 10 MB more for a hybrid handle) and
+ * one pinned, device-mapped
  * host word for the error status.  Returns WAVE_EINVAL for a
  * bad shape, WAVE_EDEVICE off sm_103, WAVE_ENOMEM/WAVE_ECUDA on failure;
  * *out is set only on success.
@@ -367,7 +368,7 @@ int wave_prompt_append(wave_t* h, int layer, int n_seq, const int32_t* cu_seqlen
  * same prompt in a larger batch may differ by such roundings.
  * Prompts are whole: the call reads no history, so it has no counterpart to
  * the append's starts > 0 (a prompt that goes on from earlier tokens attends
- * to them in the steps only).
+ * to them by wave_history_attention, or in the steps).
  */
 int wave_prompt_attention(wave_t* h, int n_seq, const int32_t* cu_seqlens, int n_kv_heads, int type, const void* q,
                           int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
@@ -495,6 +496,8 @@ int wave_rope_apply_at(const wave_rope* rope, int64_t rows, const int32_t* posit
  * wave_prompt_append and the steps write, these calls read, and the other way
  * round.  So a later prompt of a live session goes on from its history.
  *
+ * wave_sessions_copy and wave_kv_quantize know the step's own form only.
+ *
  * Blocks of 16 and more.  A block's scale is the least power of two s with |v|
  * <= 448 s for every finite v that it holds (0 if all are 0).  Codes are
  * floating point, so that a power of two costs no precision, and when a token
@@ -503,7 +506,9 @@ int wave_rope_apply_at(const wave_rope* rope, int64_t rows, const int32_t* posit
  * Infinities are held as +-448 s, NaN as NaN.  The first token that a call
  * writes to a block at the block's first place begins the block anew; one at a
  * later place goes on with the scale that the block has.  Slots of a block
- * behind the last token written keep their codes and mean nothing.
+ * behind the last token written keep their codes and mean nothing.  (Attention
+ * over blocks filled by other means, with scales that are no powers of two, takes
+ * them and their products with a code to fp16's 11 bits; scales are not negative.)
  *
  * Prompts (cu_seqlens, slots, starts: HOST arrays) and their rules are those of
  * the calls on packed prompts.  The _frame forms take one token of each of S
@@ -545,8 +550,14 @@ int wave_history_read(wave_t* h, int layer, int n_seq, const int32_t* cu_seqlens
  * rows *_stride elements apart; scale is > 0 and at most 2.3e38; n_heads /
  * n_kv_heads is at most 128.  Codes are exact factors of the products; scores,
  * the softmax's maximum and sums and the output are kept in fp32, the weights
- * are rounded to fp16 (11 bits) for the second product.  Slots that a row does not
- * attend to never reach it, whatever they hold.  out must not overlap q.
+ * are rounded to fp16 (11 bits) for the second product, and those below 2^-21 of a
+ * row's largest (each times the V scale of its 128 slots) to 2^-32 of it.  Slots
+ * that a row does not attend to never reach it, whatever they hold.  out must not
+ * overlap q.  Prompts whose tokens make up to 32 rows for a K/V head (tokens times
+ * the heads that share it), and frames, go one way, longer prompts another: one
+ * launch each, and one more where parts of the keys are joined (in fp32).  How the
+ * keys are divided depends on who else is in the call, so that a session alone
+ * and in a batch may differ by the roundings named.
  */
 int wave_history_attention(wave_t* h, int layer, int n_seq, const int32_t* cu_seqlens, const int32_t* slots,
                            const int32_t* starts, int type, const void* q, int64_t q_stride, const uint8_t* kv_fp8,
@@ -602,7 +613,8 @@ int wave_debug_skip_barrier(wave_t* h, int cta, int barrier);
  * attention ends its copies before tile `index` of K and V (0 K, 1 V of its
  * first block, and so on); 10, every CTA of the chunked selective state ends
  * its copies before its chunk `index` (the products, and all that is made of
- * them, wait).  index < 0 disables. */
+ * them, wait); 11, every CTA of the attention over the history for many rows ends
+ * its conversions before tile `index` of K and V.  index < 0 disables. */
 int wave_debug_skip_signal(wave_t* h, int which, int index);
 /* Make later steps also write, for every session with a valid position, the
  * fp32 K (after RoPE) and V rows they quantise into dst, a device buffer of
