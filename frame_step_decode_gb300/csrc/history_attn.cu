@@ -20,7 +20,7 @@ namespace wave {
 
 // The sequences of `from` that have a length to keep.
 template <typename F>
-static void keep(SeqBatch* to, const SeqBatch from, F want) {
+static void keep(SeqBatch* to, const SeqBatch& from, F want) {
   to->n = 0;
   to->cum[0] = 0;
   for (int i = 0; i < from.n; ++i) {
@@ -56,14 +56,31 @@ static int attention(wave_t* h, HistoryAttnParams& p, int tokens, int type, cons
   p.err_out = h->err_host_dev;
   cudaStream_t st = (cudaStream_t)stream;
   h->last_stream = st;
-  // Sequences of few rows, and the others.
+  // Sequences of few rows, and the others.  Where there are others, few rows with
+  // no more than two blocks of 128 keys for each SM go along with them: a launch
+  // of their own costs more (6 us beside 180).
   HistoryAttnParams many = p;
   if (p.positions) {
     p.n = tokens;
     many.b.n = 0;
   } else {
-    keep(&p.b, many.b, [&](int len) { return (long long)len * p.group <= kFewRows; });
-    keep(&many.b, many.b, [&](int len) { return (long long)len * p.group > kFewRows; });
+    auto few = [&](int len) { return (long long)len * p.group <= kFewRows; };
+    long long blocks = 0;
+    bool others = false;
+    for (int i = 0; i < p.b.n; ++i) {
+      const int len = p.b.len(i);
+      if (few(len))
+        blocks += (long long)p.hist.heads * ((p.b.start[i] + len + 127) / 128);
+      else
+        others = true;
+    }
+    if (others && blocks <= 2LL * h->pl.grid) {
+      p.b.n = 0;
+    } else {
+      const SeqBatch all = p.b;
+      keep(&p.b, all, few);
+      keep(&many.b, all, [&](int len) { return !few(len); });
+    }
     p.n = p.b.n;
   }
   p.part = h->ws.part_o;
