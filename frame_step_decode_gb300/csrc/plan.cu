@@ -286,10 +286,11 @@ size_t carve_workspace(const Plan& pl, char* base, Workspace* ws) {
 void rope_table(const Plan& pl, std::vector<float2>* tab) {
   const int D = pl.cfg.head_dim, T = pl.T_max;
   tab->resize((size_t)T * (D / 2));
+  double th[64];
+  for (int i = 0; i < D / 2; ++i) th[i] = pow((double)pl.cfg.rope_base, -2.0 * i / (double)D);
   for (int t = 0; t < T; ++t)
     for (int i = 0; i < D / 2; ++i) {
-      const double th = pow((double)pl.cfg.rope_base, -2.0 * i / (double)D);
-      const double a = (double)t * th;
+      const double a = (double)t * th[i];
       (*tab)[(size_t)t * (D / 2) + i] = make_float2((float)cos(a), (float)sin(a));
     }
 }
