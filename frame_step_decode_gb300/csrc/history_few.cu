@@ -1,11 +1,11 @@
 // history_few.cu -- attention over the 8-bit history for few rows: a frame's
-// single tokens, and prompts of so few tokens that their heads' rows fit one
-// tile of 16.
+// single tokens, and prompts of so few tokens that a K/V head has at most
+// kFewRows rows (tokens times heads of the group), in tiles of 8 or 16.
 //
 // Bound by HBM: every code is read once for all rows of its K/V head.  The
 // keys of all sessions and heads are one line of chunks of 16 tokens, divided
 // evenly among the warps of the GPU whatever the lengths, which only the device
-// knows in a frame; what a unit (session, head, 16 rows) has in several warps
+// knows in a frame; what a unit (session, head, row tile) has in several warps
 // is joined in shared memory, in several CTAs by the last of them to finish.
 //
 // A chunk's codes are brought into the warp's own ring by cp.async (tokens
@@ -20,6 +20,15 @@
 // largest, so that one 2^-31 of it is still there.  bf16 queries are brought to
 // f16 by a power of two for each row, which loses nothing above 2^-29 of the
 // row's largest value.
+//
+// Measured (captured launches in a row): a frame of 80 sessions of up to 3000
+// tokens, 32/8 heads of 128, blocks of 64, 54 us = 4.55 TB/s, of 20 sessions of
+// 6000 tokens 46 us = 5.4 TB/s; 56 sessions of up to 1500 tokens, 32 heads, a scale
+// for each token, 84 us = 4.25 TB/s; one session of 32001 tokens, 32/8 heads,
+// 22.5 us; one after 1500 tokens, 16 x 64, 9.3 us; 25 tokens after 1475, 10.6 us.
+// Of some 80,000 cycles of the frame of 80, about 8,000 are the begin (positions,
+// the line, first loads) and 9,000 the joins; in the loop between the rate is
+// about 5.7 TB/s, what HBM gives.
 #include <cuda_runtime.h>
 #include <stdint.h>
 

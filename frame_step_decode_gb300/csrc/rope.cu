@@ -2,6 +2,9 @@
 // positions on packed rows.
 //
 //   (a, b) -> amplitude (a cos - b sin, a sin + b cos),  angle = position * frequency of the pair
+//
+// Measured (captured launches in a row): 8005 tokens of 40 heads of 128, bf16,
+// 31 us = 5.3 TB/s of mixed reads and writes; 25 tokens of 32 heads of 64, 2.8 us.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
