@@ -984,3 +984,43 @@ def test_calls_replayed_from_graphs_that_share_a_handle():
         for i in set(order):
             _check(cs[i], qs[i][0], qs[i][1], lens[i], [0, 1, 2], starts[i], _cu(lens[i]))
     _done(w)
+
+
+@pytest.mark.parametrize("frame", [False, True])
+@pytest.mark.parametrize("D,block", [(64, 128), (128, 1), (128, 16)])
+def test_attention_of_one_head_shared_by_128(frame, D, block):
+    """The largest group: a tile of 128 rows is one token; a frame has 8 row tiles to a head."""
+    if frame:
+        _attend([1] * 5, [0, 700, 127, 16, 1300], 128, 1, D, block, BF, seed=5, frame=True)
+    else:
+        _attend([3, 1, 70], [300, 0, 129], 128, 1, D, block, BF, seed=6)
+
+
+@pytest.mark.parametrize("D,block", [(128, 128), (64, 128), (128, 1)])
+def test_a_captured_prompt(D, block):
+    """Append, attention and read back of packed prompts captured into one graph, the first use of the handle, and
+    replayed with other inputs: the history, the outputs and what is read back follow them."""
+    H, Hkv, lens, slots, starts = 4, 2, [200, 3], [1, 0], [0, 0]
+    cu, T = _cu(lens), 204
+    w = _wave(H, D, S=2, T=T)
+    plan = fsd.rope_plan(D)
+    c = Cache(2, Hkv, T, D, block)
+    x = torch.zeros(cu[-1], (H + 2 * Hkv) * D, device="cuda")
+    q, out = torch.zeros(cu[-1], H, D, dtype=F16, device="cuda"), torch.zeros(cu[-1], H, D, dtype=F16, device="cuda")
+    k = torch.zeros(cu[-1], Hkv, D, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        w.history_append(0, cu, slots, starts, x, c.kv, c.sc, Hkv, block, rope=plan, q=q)
+        w.history_attention(0, cu, slots, starts, q, c.kv, c.sc, Hkv, block, out)
+        w.history_read(0, cu, slots, starts, c.kv, c.sc, Hkv, block, k)
+    for seed in (1, 2):
+        x.copy_(torch.randn(x.shape, generator=_gen(seed), device="cuda"))
+        want = Cache(2, Hkv, T, D, block)
+        w.history_append(0, cu, slots, starts, x, want.kv, want.sc, Hkv, block, rope=plan)
+        g.replay()
+        torch.cuda.synchronize()
+        assert c.same(want)
+        _check(c, q, out, lens, slots, starts, cu)
+        for i, (n, slot) in enumerate(zip(lens, slots)):
+            assert torch.equal(k[cu[i]:cu[i + 1]].transpose(0, 1), c.values(0, slot, 0, n, torch.float32))
+    _done(w)
