@@ -711,8 +711,8 @@ def _plan(rope) -> int | None:
 def rope_apply(plan, x, out=None, cu_seqlens=None, starts=None, positions=None, stream=None) -> None:
     """wave_rope_apply (cu_seqlens and starts: host integers, rows of packed
     prompts) or wave_rope_apply_at (positions: int32 on the device, one for each
-    row).  x and out are [rows][heads][D] of fp32, bf16 or fp16, rows may be
-    strided; out defaults to x itself."""
+    row).  x and out are [rows][heads][D] of fp32, bf16 or fp16 on the current
+    device, rows may be strided; out defaults to x itself."""
     out = x if out is None else out
     what = "wave_rope_apply"
     if len(x.shape) != 3 or x.shape[1:] != out.shape[1:] or (positions is None) == (cu_seqlens is None or starts is None):
@@ -726,13 +726,14 @@ def rope_apply(plan, x, out=None, cu_seqlens=None, starts=None, positions=None, 
         rows = positions.numel()
     if x.shape[0] < rows or out.shape[0] < rows:
         raise ValueError(f"{what}: x and out have the rows that the call names")
-    if x.is_cuda:
-        import torch
-        device = torch.cuda.current_device()
-        _here(device, what, x, out)
-        if positions is not None:
-            _DTYPES.setdefault("int32", torch.int32)
-            _held(positions, "int32", rows, device, f"{what}: positions")
+    if not x.is_cuda:
+        raise ValueError(f"{what}: tensors on the current device are wanted, not on {x.device}")
+    import torch
+    device = torch.cuda.current_device()
+    _here(device, what, x, out)
+    if positions is not None:
+        _DTYPES.setdefault("int32", torch.int32)
+        _held(positions, "int32", rows, device, f"{what}: positions")
     heads, D = x.shape[1], x.shape[2]
     xs = (_ptr(x), _type_of(x), _rows(x, what), _ptr(out), _type_of(out), _rows(out, what), _stream(stream))
     if positions is None:

@@ -92,6 +92,27 @@ def test_rows_that_do_not_fit_a_rotation_are_refused():
             c()
 
 
+class _NothingIsCalled:
+    def __getattr__(self, name):
+        raise AssertionError(f"{name} was reached")
+
+
+@pytest.mark.parametrize("types", [(torch.bfloat16, torch.bfloat16), (torch.float32, torch.float16)])
+def test_a_rotation_of_the_hosts_tensors_is_refused(types, monkeypatch):
+    """Rows, outputs and positions that fit in all but where they are: no call of the library is made with their addresses."""
+    monkeypatch.setattr(fsd, "_lib", _NothingIsCalled())
+    p, x, out = fsd.WaveRope(0, 64), _b(3, 2, 64, dtype=types[0]), _b(3, 2, 64, dtype=types[1])
+    with pytest.raises(AssertionError):
+        fsd.lib().wave_rope_apply  # the stub stands in for the library
+    pos = torch.zeros(3, dtype=torch.int32)
+    for call in (lambda: fsd.rope_apply(p, x, out, cu_seqlens=[0, 3], starts=[0], stream=0),
+                 lambda: fsd.rope_apply(p, out, cu_seqlens=[0, 3], starts=[0], stream=0),
+                 lambda: fsd.rope_apply(p, x, out, positions=pos, stream=0),
+                 lambda: fsd.rope_apply(p, x, out, positions=pos.long(), stream=0)):
+        with pytest.raises(ValueError):
+            call()
+
+
 @pytest.mark.parametrize("change", [dict(n_heads=0), dict(head_dim=96), dict(head_dim=64, dims=128), dict(type=7), dict(out_type=-1),
                                     dict(x_stride=120), dict(x_stride=132), dict(x_stride=2 ** 31), dict(out_stride=64), dict(x=0), dict(out=0),
                                     dict(x=4104), dict(starts=[-1]), dict(starts=[2 ** 31 - 3]), dict(cu=[3, 0]), dict(cu=[-1, 3]),
