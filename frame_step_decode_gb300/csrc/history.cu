@@ -54,14 +54,15 @@ __device__ __forceinline__ void make_turns(const wave_rope& r, float4* turns, in
 }
 
 // Codes of tokens [from, to) of one head encoded anew under a scale that is
-// 1 / ratio times the one they were made with.
+// 1 / ratio times the one they were made with.  NaN stays NaN, also where the
+// ratio is 0 (a block whose values are not finite has the least scale).
 template <int D>
 __device__ __forceinline__ void recode(uint8_t* codes, int from, int to, float ratio, int lane, int lanes) {
   for (int i = from * (D / 8) + lane; i < to * (D / 8); i += lanes) {
     uint2* c = (uint2*)codes + i;
     float x[8];
     decode8(*c, x);
-    *c = encode8(x, ratio);
+    *c = codes8(x, ratio);
   }
 }
 

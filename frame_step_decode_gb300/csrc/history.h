@@ -208,11 +208,8 @@ __device__ __forceinline__ float counts(float v) {
   return a < __int_as_float(0x7F800000) ? a : 0x1p-126f;
 }
 
-// Eight codes of x / scale.  1 / scale is exact for the powers of two that
-// blocks have.  Infinities saturate, NaN stays NaN; inv is 0 for a scale of 0,
-// whose codes are 0 (without a sign).
-__device__ __forceinline__ uint2 encode8(const float* x, float inv) {
-  if (inv == 0.f) return make_uint2(0, 0);
+// Eight codes of x * inv.  Infinities saturate, NaN stays NaN.
+__device__ __forceinline__ uint2 codes8(const float* x, float inv) {
   uint32_t w[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i)
@@ -221,6 +218,9 @@ __device__ __forceinline__ uint2 encode8(const float* x, float inv) {
                << 16;
   return make_uint2(w[0], w[1]);
 }
+// Eight codes of x / scale.  1 / scale is exact for the powers of two that
+// blocks have; inv is 0 for a scale of 0, whose codes are 0 (without a sign).
+__device__ __forceinline__ uint2 encode8(const float* x, float inv) { return inv == 0.f ? make_uint2(0, 0) : codes8(x, inv); }
 __device__ __forceinline__ void decode8(uint2 c, float* x) {
   const uint32_t w[2] = {c.x, c.y};
 #pragma unroll

@@ -503,7 +503,10 @@ int wave_rope_apply_at(const wave_rope* rope, int64_t rows, const int32_t* posit
  * floating point, so that a power of two costs no precision, and when a token
  * is added that needs a larger scale the codes before it are encoded anew by a
  * change of exponent, which loses nothing above their normal range (2^-6 s).
- * Infinities are held as +-448 s, NaN as NaN.  The first token that a call
+ * NaN is held as NaN, whatever the scale becomes.  An infinity is held as +-448
+ * s of the scale that the block has when it is added (which it does not raise;
+ * where nothing finite but 0 is there, the least ordinary number), and is from
+ * then on that value.  The first token that a call
  * writes to a block at the block's first place begins the block anew; one at a
  * later place goes on with the scale that the block has.  Slots of a block
  * behind the last token written keep their codes and mean nothing.  (Attention
