@@ -57,8 +57,8 @@ struct ManyParams {
   int tile_tokens;      // tokens of a 128-row tile: 128 / group
   int ctas;
   ManyCut cut[kMaxCuts + 1];
-  float* part_o;        // [2 * CTA + (the unit begins there)][256 rows][D]
-  float2* part_ml;      // their maxima and sums
+  float* part_o;        // [2 * CTA + (the unit begins there)][256 rows][D], in the values' own units
+  float2* part_ml;      // the sums of their weights (second) and the power of two that both are relative to
   int wide;             // out's rows are 32-byte aligned
   ErrSink sink;
   int skip;             // testing hook: no tile of K and V from this one on is made (-1: off)
@@ -118,8 +118,7 @@ struct ManyWalk {
 struct BlockMeta {
   float factor;       // of the scores: the tile's largest K scale, over 2^6
   float shift;        // of the weights' exponents: log2 of the largest V scale
-  float back;         // 2^-shift
-  float pad;
+  float pad[2];
   float k[kManyRows], v[kManyRows];  // scales for each token: K's, and V's over 2^shift
 };
 
@@ -281,7 +280,9 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
       // what the row sees of the first block, and the first block that some row of the tile does not see all of
       int seen = it.start + tile_tok + row_tok - it.from * kManyRows;
       const int cut = (it.start + tile_tok) / kManyRows - it.from;
-      float m = -INFINITY, l = 0.f;
+      // what the weights of O are relative to; the sum of the weights without V's
+      // scales, and what it is relative to
+      float m = -INFINITY, l = 0.f, base = 0.f;
 #pragma unroll 1
       for (int j = 0; j < all; ++j, ++m_it, seen -= kManyRows) {
         const int mi = m_it % L::kMetas;
@@ -354,7 +355,6 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
         // loop takes 1290 cycles instead of 740 for a warp alone.)
         auto raise = [&](float top, bool up) {  // the maximum moves
           const float a = up ? (m == -INFINITY ? 0.f : ex2(m - top)) : 1.f;
-          l *= a;
           m = up ? top : m;
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
@@ -380,13 +380,51 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
             w[i] = half2_of(e.x, e.y);
           }
         };
-        auto relative = [&]() {
-          sum[0] = sum[1] = sum[2] = sum[3] = make_float2(0.f, 0.f);
-          return (m == -INFINITY ? 0.f : shift - m) + kManyBias;
-        };
+        auto relative = [&]() { return (m == -INFINITY ? 0.f : shift - m) + kManyBias; };
+        auto clear = [&]() { sum[0] = sum[1] = sum[2] = sum[3] = make_float2(0.f, 0.f); };
         auto add_up = [&]() {
           sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
           sum[0].x += sum[0].y;
+        };
+        // The sum of the weights has a reference of its own: every key counts in
+        // it, also where V's scale is so far below another tile's that the
+        // weights of O are nothing.  Without V's scales this tile's weights are
+        // relative to -neg.  Where that is far above what the sum is relative to
+        // they may all have been cut to 0, and the tile is added apart; where it
+        // is because the maximum has just moved to a score of this tile they are
+        // not, and the sum moves along.
+        bool added = false;
+        auto is_far = [&]() { return -relative() - base > 64.f; };
+        auto add_apart = [&](bool far, auto masked) {
+          float top = -INFINITY, more = 0.f;
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t s[32];
+            tmem_ld32(tS(st) + lanes + 32 * (c & 3), s);
+            tmem_ld_wait();
+            ready(c & 3, s, masked);
+            if (c == 4) top = fmaxf(base, top * z);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              if (c < 4)
+                top = fmaxf(top, __uint_as_float(s[i]));
+              else
+                more += ex2(fmaf(__uint_as_float(s[i]), z, -top));
+            }
+          }
+          l = far ? fmaf(l, ex2(base - top), more) : l;
+          base = far ? top : base;
+          added = far;
+        };
+        auto add_tile = [&](float neg) {
+          const float d = -neg - base;
+          if (added) return;
+          if (d > 64.f) {
+            l = fmaf(l, ex2(-d), sum[0].x);
+            base = -neg;
+          } else {
+            l = fmaf(sum[0].x, ex2(d), l);
+          }
         };
         if constexpr (kScale == kScaleOfToken) {
           // With a block's scales in registers too, P cannot be held back: the
@@ -397,10 +435,15 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
             if (j == 0) {
               m = top;
             } else {
-              const bool up = top > m + 8.f;
-              if (__any_sync(0xffffffffu, up)) raise(top, up);
+              const bool up = top > m + 8.f, far = !up && is_far();
+              if (__any_sync(0xffffffffu, up || far)) {
+                raise(top, up);
+                if (__any_sync(0xffffffffu, far)) add_apart(far, masked);
+              }
             }
             const float neg = relative();
+            if (j == 0) base = -neg;
+            clear();
             uint32_t s[2][32];
             tmem_ld32(tS(st) + lanes, s[0]);
 #pragma unroll 1
@@ -414,18 +457,22 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
                 tmem_st16(tS(st) + lanes + 16 * (c + h), w);
               }
             }
+            add_up();
+            add_tile(neg);
           };
           if (j >= cut)
             block(kMasked);
           else
             block(kAll);
-          add_up();
         } else {
           if (j == 0) m = largest(kAll);
+          float neg = relative();
+          if (j == 0) base = -neg;
+          const bool far = is_far();
           uint32_t w[64];
 #pragma unroll 1
           for (bool again = false;; again = true) {
-            const float neg = relative();
+            clear();
             uint32_t s[2][32];
             tmem_ld32(tS(st) + lanes, s[0]);
 #pragma unroll
@@ -435,14 +482,16 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
               weights(c, s[c & 1], w + 16 * c, neg, kAll);
             }
             add_up();
-            if (j == 0 || again || !__any_sync(0xffffffffu, !(sum[0].x <= 60000.f))) break;
+            if (j == 0 || again || !__any_sync(0xffffffffu, !(sum[0].x <= 60000.f) || far)) break;
+            if (__any_sync(0xffffffffu, far)) add_apart(far, kAll);
             const float top = largest(kAll);
             raise(top, top > m);
+            neg = relative();
           }
           tmem_st32(tS(st) + lanes, w);
           tmem_st32(tS(st) + lanes + 32, w + 32);
+          add_tile(neg);
         }
-        l += sum[0].x * meta.back;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -464,15 +513,26 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
         const bool odd = (found.x | found.y | found.z | found.w) != 0, part = !it.whole();
         const int tok = tile_tok + row_tok;
         const bool on = row_tok < p.tile_tokens && tok < it.len;
-        const float inv = 1.f / l;
+        // the sum of the weights between 1 and 2, and O in the values' own units: times
+        // 2^(m - bias - base), in halves where fp32 does not hold it
+        const int le = l > 0.f && l < INFINITY ? (int)(__float_as_uint(l) >> 23) - 127 : 0;
+        l *= power(-le);
+        base += (float)le;
+        const float units = m - kManyBias - base;
+        const bool wide = __any_sync(0xffffffffu, fabsf(units) > 100.f);  // one factor does for the others
+        const float half = ex2(0.5f * units), factor_o = (wide ? half : ex2(units)) * (part ? 1.f : 1.f / l);
         uint16_t* orow = p.a.out + (it.row0 + (on ? tok : 0)) * p.a.out_stride + (it.head * p.a.group + row_head) * D;
         const size_t at = (size_t)(2 * blockIdx.x + (it.from == 0)) * (2 * kManyRows) + st * kManyRows + row;
-        if (part && on) p.part_ml[at] = make_float2(m, l);
+        if (part && on) p.part_ml[at] = make_float2(l == 0.f ? -INFINITY : base, l);
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
           tmem_ld32(tO(st) + lanes + 32 * c, o);
           tmem_ld_wait();
+          if (wide) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * half);
+          }
           if (odd) {  // NaN that was left out of P V: for the rows that see it
 #pragma unroll
             for (int i = 0; i < 32; ++i)
@@ -480,6 +540,8 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
                 if (it.start + tok >= bad[((k & 1) * 4 + f) * D + 32 * c + i]) o[i] = 0x7FC00000u;
           }
           if (part) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * factor_o);
             if (on) {
 #pragma unroll
               for (int i = 0; i < 4; ++i) store32(p.part_o + at * D + 32 * c + 8 * i, o + 8 * i);
@@ -488,7 +550,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
             uint32_t v[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-              const float2 x = mul2(make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), make_float2(inv, inv));
+              const float2 x = mul2(make_float2(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1])), make_float2(factor_o, factor_o));
               v[i] = kF16 ? half2_of(x.x, x.y) : pair16<__nv_bfloat16>(x.x, x.y);
             }
 #pragma unroll
@@ -571,6 +633,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
     for (uint32_t k = 0; ok && items[k & 1].valid; ++k) {
       const ManyItem& it = items[k & 1];
       const int first_cut = (it.start + it.tok0) / kManyRows, from = it.from, last = it.to;
+      int v_exp = -100;  // of the V scale that the weights are times; a tile whose values are all 0 has the one before it
       // the list of NaN values is free: the unit before the last has been written
       for (int i = lane; i < D; i += 32) my_bad[(k & 1) * 4 * D + i] = INT32_MAX;
       if (lane == 0) odd_unit[(k & 1) * 4 + warp - 8] = 0;
@@ -602,10 +665,10 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
             float top = fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3]));
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-            const int e = top > 0.f ? min(max(exponent_up(top), -100), 120) : -100;
-            const float r = power(-e);
+            if (top > 0.f) v_exp = min(max(exponent_up(top), -100), 120);
+            const float r = power(-v_exp);
             *(float4*)&meta.v[4 * lane] = make_float4(sc[0] * r, sc[1] * r, sc[2] * r, sc[3] * r);
-            if (lane == 0) meta.factor = 1.f, meta.shift = (float)e, meta.back = r;
+            if (lane == 0) meta.factor = 1.f, meta.shift = (float)v_exp;
           }
         } else {
           float top = sc[0];
@@ -613,15 +676,14 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
 #pragma unroll
             for (int d = 4; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
           }
-          const int e = top > 0.f ? min(max(exponent_up(top), lane < 8 ? -120 : -100), 120) : -100;
+          const int e = top > 0.f ? min(max(exponent_up(top), lane < 8 ? -120 : -100), 120) : v_exp;
           // K's codes have room for 2^6 more in fp16; the scale of a block of 128 is a factor of K's scores as it is
           const float r = sc[0] * power(-e) * (lane < 8 ? 64.f : 1.f);
           ratio = half2_of(r, r);
-          const int ev = __shfl_sync(0xffffffffu, e, 8);
+          v_exp = __shfl_sync(0xffffffffu, e, 8);
           if (warp == 8 && lane == 0) {
             meta.factor = kScale == kScaleOfBlock ? power(e) * 0x1p-6f : sc[0];
-            meta.shift = (float)ev;
-            meta.back = power(-ev);
+            meta.shift = (float)v_exp;
           }
           if constexpr (kScale == kScaleOfTile) ratio = __shfl_sync(0xffffffffu, ratio, 8);
         }

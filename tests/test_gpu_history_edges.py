@@ -1,12 +1,101 @@
-"""Blocks that go on, at the edges: values that are not finite."""
+"""Attention over the history, and blocks that go on, at the edges: scales that
+lie far apart, of tokens that a row sees and of tokens that it does not, tiles
+of zeros, the ends of fp32's range, and values that are not finite.  The bound
+on a row's error comes from the slots that the row sees alone."""
 import math
 
 import pytest
 import torch
 
-from test_gpu_history import E4M3, Cache, _done, _gen, _wave
+from test_gpu_history import BF, E4M3, HALF, TINY, U, Cache, _cu, _done, _gen, _queries, _wave
 
 pytestmark = pytest.mark.gpu
+
+
+def seen_reference(c, q, lens, slots, starts, cu, scale):
+    """(out, the bound on |got - out|) in 64 bits.  With w the normalised weights, A = sum w |v| and s the scores: weights are
+    rounded to fp16 (2^-11 A); scores carry at most (D + 8) fp32 roundings of their absolute sum, which enter a weight
+    as a factor exp(2 ds); exponentials and sums 2^-18; a product's sums are cut to fp32 after each 16 keys (2^-23 of A
+    each); the result is rounded once.  Weights below fp16's normal range are off by 2^-25 where 2^7 stands for the
+    largest weight times the largest V scale of its 128 slots, brought up to a power of two; of slots that the row does not
+    see at most 2^4 times the least that it does: 2^-28 of 448 times that a key.  Scales are powers of two (or one a
+    token), so that codes are exact."""
+    H, D = q.shape[1], q.shape[2]
+    g = H // c.Hkv
+    out = torch.zeros(q.shape, dtype=torch.float64, device=q.device)
+    tol = torch.zeros_like(out)
+    for i, (n, slot, s0) in enumerate(zip(lens, slots, starts)):
+        t = s0 + n
+        kd, vd = (c.values(which, slot, 0, t).repeat_interleave(g, 0) for which in (0, 1))
+        vs = c.sc[c.layer, 1, slot][:, torch.arange(t, device=q.device) // c.block].double().repeat_interleave(g, 0)[:, None]
+        qd = q[cu[i]:cu[i + 1]].double().transpose(0, 1)
+        mask = torch.arange(t, device=q.device)[None] > s0 + torch.arange(n, device=q.device)[:, None]
+        s = ((qd @ kd.transpose(1, 2)) * scale).masked_fill(mask, -math.inf)
+        w = torch.softmax(s, -1)
+        A = w @ vd.abs()
+        # the largest seen scale of each 128 slots times the largest seen weight of them
+        per_tile = lambda x: torch.nn.functional.pad(x, (0, -t % 128)).unflatten(-1, (-1, 128)).amax(-1)  # noqa: E731
+        top = (per_tile(w) * 2 * per_tile(vs.expand_as(w).masked_fill(mask, 0.0))).amax(-1, keepdim=True)
+        ds = ((D + 8) * U * scale * (qd.abs() @ kd.abs().transpose(1, 2))).masked_fill(mask, 0.0).amax(-1, keepdim=True)
+        out[cu[i]:cu[i + 1]] = (w @ vd).transpose(0, 1)
+        tol[cu[i]:cu[i + 1]] = (HALF[q.dtype] * (w @ vd).abs() + (2.0 ** -11 + 2.0 * ds + 2.0 ** -18 + t / 16 * 2.0 ** -23) * A * 1.01
+                                + 2.0 ** -28 * 448 * top * t + TINY[q.dtype]).transpose(0, 1)
+    return out, tol
+
+
+def _run(c, q, lens, starts, H, D, frame=False, scale=None):
+    """One call; its output, which is within the bound."""
+    slots, cu, Hkv = list(range(len(lens))), _cu(lens), c.Hkv
+    out = torch.full_like(q, 7.0)
+    w = _wave(H, D, S=len(lens), T=c.T)
+    if frame:
+        w.history_attention_frame(0, torch.tensor(starts, dtype=torch.int32, device="cuda"), q, c.kv, c.sc, Hkv, c.block, out, scale=scale)
+    else:
+        w.history_attention(0, cu, slots, starts, q, c.kv, c.sc, Hkv, c.block, out, scale=scale)
+    _done(w)
+    ref, tol = seen_reference(c, q, lens, slots, starts, cu, D ** -0.5 if scale is None else scale)
+    worst = float(((out.double() - ref).abs() / tol).max())
+    assert worst <= 1.0, worst
+    return out
+
+
+def _rows(n, Hkv, D, seed):
+    return [torch.randn(n, Hkv, D, generator=_gen(seed + j), device="cuda") * (1.5, 1.0)[j] for j in (0, 1)]
+
+
+@pytest.mark.parametrize("frame", [False, True])
+@pytest.mark.parametrize("block", [1, 16, 128])
+@pytest.mark.parametrize("small,large", [(0.0, 2.0 ** 60), (0.0, 1.0), (2.0 ** -100, 2.0 ** 60)])
+@pytest.mark.parametrize("order", ["small first", "large first", "in turns"])
+def test_a_tile_of_values_far_below_anothers(frame, block, small, large, order):
+    """All 128 values of a tile zero, or 2^160 below the next tile's: their weights still count in the sum."""
+    H, D, n, s0 = 2, 64, 1 if frame else 70, 511
+    k, v = _rows(s0 + n, H, D, 5)
+    tile = torch.arange(s0 + n, device="cuda") // 128
+    low = {"small first": tile < 2, "large first": tile >= 2, "in turns": tile % 2 == 0}[order]
+    v = v * torch.where(low, small, large)[:, None, None]
+    c = Cache(1, H, 584, D, block)
+    c.write(0, 0, k, v)
+    for q in (torch.zeros(n, H, D, dtype=BF, device="cuda"), _queries(n, H, D, BF)[0]):
+        _run(c, q, [n], [s0], H, D, frame=frame)
+
+
+@pytest.mark.parametrize("frame", [False, True])
+@pytest.mark.parametrize("block", [1, 16, 128])
+@pytest.mark.parametrize("gap", [60.0, 300.0])
+def test_scores_that_rise_and_fall_far(frame, block, gap):
+    """Scores of whole tiles that differ by hundreds, rising, falling and in turns, with values that do not make up for it."""
+    H, D, n, s0 = 2, 64, 1 if frame else 70, 640
+    base_k, base_v = _rows(s0 + n, H, D, 6)
+    q = _queries(n, H, D, BF)[0]
+    q[..., 0] = 4.0
+    tile = torch.arange(s0 + n, device="cuda") // 128
+    for level in (tile, 5 - tile, tile % 2, (tile * 3) % 5):
+        k, v = base_k.clone(), base_v * 2.0 ** (-9.0 * level.float())[:, None, None]
+        k[..., 0] = level[:, None] * gap * D ** 0.5 / 4.0
+        c = Cache(1, H, 712, D, block)
+        c.write(0, 0, k, v)
+        _run(c, q, [n], [s0], H, D, frame=frame)
 
 
 @pytest.mark.parametrize("block", [16, 64])
