@@ -118,9 +118,22 @@ struct ManyWalk {
 struct BlockMeta {
   float factor;       // of the scores: the tile's largest K scale, over 2^6
   float shift;        // of the weights' exponents: log2 of the largest V scale
-  float pad[2];
-  float k[kManyRows], v[kManyRows];  // scales for each token: K's, and V's over 2^shift
+  int apart;          // the codes are as they are in the tiles, and the scales are
+  float pad;
+  float k[kManyRows], v[kManyRows];  // scales for each token: K's, and V's over 2^shift (apart: log2 of V's); k alone for blocks: 8 of K, 8 of V
 };
+
+// A tile of 128 slots whose scales lie far apart is not brought to the largest
+// of them, for which fp16 would cut the others' codes or weights: its codes stay
+// as they are, its scales meet the scores and the weights token by token in fp32,
+// relative to what a row sees.  Two passes over the scores and two exponentials
+// each: a call of such tiles alone takes 268 us instead of 124 (1024 tokens after
+// 7168, 32 heads of 128, blocks of 64).  How far, in powers of two of the largest
+// scale over the least that is not 0: 8, which leaves codes their bits and weights
+// theirs; of V's, where some row does not see all of the tile, 4, which is what a
+// scale that it does not see may cost it; and there none 64 above the tiles
+// before, whose sums it would leave nothing in fp32.
+constexpr int kApart = 8, kApartCut = 4, kApartRise = 64;
 
 template <int D>
 struct ManySmem {
@@ -167,6 +180,11 @@ __device__ __forceinline__ int exponent_up(float x) {
   return (int)(u >> 23) - 127 + ((u & 0x7FFFFFu) != 0);
 }
 __device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 template <int D, bool kF16, int kScale>
 __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_constant__ ManyParams p) {
@@ -294,22 +312,10 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
         }
         const BlockMeta& meta = metas[mi];
         const float z = fmaxf(factor * meta.factor, 0x1p-126f), shift = meta.shift;
+        const bool apart = kScale != kScaleOfTile && meta.apart, special = j >= cut || apart;
         if (!wait_warp(L::kSFull + st, s_it & 1)) break;
         ++s_it;
         tc_fence_after();
-        if (kScale != kScaleOfToken && j >= cut) {  // masked in place: the loop below has no branch
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t s[32];
-            tmem_ld32(tS(st) + lanes + 32 * c, s);
-            tmem_ld_wait();
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (32 * c + i > seen) s[i] = __float_as_uint(-INFINITY);
-            tmem_st32(tS(st) + lanes + 32 * c, s);
-          }
-          tmem_st_wait();
-        }
         // 32 columns, scaled and masked; and their largest
         auto ready = [&](int c, uint32_t* s, auto masked) {
           if constexpr (kScale == kScaleOfToken) {
@@ -426,6 +432,57 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
             l = fmaf(sum[0].x, ex2(d), l);
           }
         };
+        // A tile apart: its scores times their K scales, in powers of two, and the
+        // weights times their V scales relative to the largest that the row sees.
+        auto apart_tile = [&]() {
+          auto scores = [&](int c, auto use) {  // 16 columns: few at a time keep the code short
+            uint32_t s[16];
+            tmem_ld16_nowait(tS(st) + lanes + 16 * c, s);
+            tmem_ld_wait();
+            const int b = (16 * c) >> p.a.hist.shift;  // of blocks
+            const float bk = kScale == kScaleOfBlock ? factor * meta.k[b] : z, bv = kScale == kScaleOfBlock ? lg2(meta.k[8 + b]) : 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float x = __uint_as_float(s[i]) * bk;
+              if constexpr (kScale == kScaleOfToken) x *= meta.k[16 * c + i];
+              use(i, 16 * c + i > seen ? -INFINITY : x, kScale == kScaleOfToken ? meta.v[16 * c + i] : bv);
+            }
+          };
+          float top = -INFINITY, high = -INFINITY;  // of the scores, and with V's scales
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c)
+            scores(c, [&](int, float x, float v) {
+              top = fmaxf(top, x);
+              high = fmaxf(high, x + v);
+            });
+          if (j == 0) {
+            m = high == -INFINITY ? top - 100.f : high;  // values of 0 alone: as a tile of them
+            base = top == -INFINITY ? 0.f : top;
+          } else {
+            const bool up = high > m;
+            if (__any_sync(0xffffffffu, up)) raise(high, up);
+            const float to = fmaxf(base, top);
+            l *= ex2(base - to);
+            base = to;
+          }
+          const float mm = m == -INFINITY ? 0.f : m - kManyBias;
+          float add = 0.f;
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t w[8];
+            float even = 0.f;
+            scores(c, [&](int i, float x, float v) {
+              add += ex2(x - base);
+              const float e = x == -INFINITY ? 0.f : ex2(x + (v - mm));
+              if (i & 1)
+                w[i / 2] = half2_of(even, e);
+              else
+                even = e;
+            });
+            tmem_st8(tS(st) + lanes + 8 * c, w);  // over scores that have been read
+          }
+          l += add;
+        };
         if constexpr (kScale == kScaleOfToken) {
           // With a block's scales in registers too, P cannot be held back: the
           // maximum comes first, and P is written as it is made (over columns of
@@ -460,37 +517,62 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
             add_up();
             add_tile(neg);
           };
-          if (j >= cut)
-            block(kMasked);
-          else
+          if (special) {  // one branch for tiles of the usual kind: with two, 292 us instead of 287 (2048 after 6144)
+            if (apart)
+              apart_tile();
+            else
+              block(kMasked);
+          } else {
             block(kAll);
-        } else {
-          if (j == 0) m = largest(kAll);
-          float neg = relative();
-          if (j == 0) base = -neg;
-          const bool far = is_far();
-          uint32_t w[64];
-#pragma unroll 1
-          for (bool again = false;; again = true) {
-            clear();
-            uint32_t s[2][32];
-            tmem_ld32(tS(st) + lanes, s[0]);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              tmem_ld_wait();
-              if (c < 3) tmem_ld32(tS(st) + lanes + 32 * (c + 1), s[(c + 1) & 1]);
-              weights(c, s[c & 1], w + 16 * c, neg, kAll);
-            }
-            add_up();
-            if (j == 0 || again || !__any_sync(0xffffffffu, !(sum[0].x <= 60000.f) || far)) break;
-            if (__any_sync(0xffffffffu, far)) add_apart(far, kAll);
-            const float top = largest(kAll);
-            raise(top, top > m);
-            neg = relative();
           }
-          tmem_st32(tS(st) + lanes, w);
-          tmem_st32(tS(st) + lanes + 32, w + 32);
-          add_tile(neg);
+        } else {
+          if (special) {
+            if (apart) {
+              apart_tile();
+              goto made;
+            }
+            // masked in place: the loop below has no branch
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t s[32];
+              tmem_ld32(tS(st) + lanes + 32 * c, s);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (32 * c + i > seen) s[i] = __float_as_uint(-INFINITY);
+              tmem_st32(tS(st) + lanes + 32 * c, s);
+            }
+            tmem_st_wait();
+          }
+          {
+            if (j == 0) m = largest(kAll);
+            float neg = relative();
+            if (j == 0) base = -neg;
+            const bool far = is_far();
+            uint32_t w[64];
+#pragma unroll 1
+            for (bool again = false;; again = true) {
+              clear();
+              uint32_t s[2][32];
+              tmem_ld32(tS(st) + lanes, s[0]);
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                tmem_ld_wait();
+                if (c < 3) tmem_ld32(tS(st) + lanes + 32 * (c + 1), s[(c + 1) & 1]);
+                weights(c, s[c & 1], w + 16 * c, neg, kAll);
+              }
+              add_up();
+              if (j == 0 || again || !__any_sync(0xffffffffu, !(sum[0].x <= 60000.f) || far)) break;
+              if (__any_sync(0xffffffffu, far)) add_apart(far, kAll);
+              const float top = largest(kAll);
+              raise(top, top > m);
+              neg = relative();
+            }
+            tmem_st32(tS(st) + lanes, w);
+            tmem_st32(tS(st) + lanes + 32, w + 32);
+            add_tile(neg);
+          }
+        made:;
         }
         tmem_st_wait();
         tc_fence_before();
@@ -634,6 +716,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
       const ManyItem& it = items[k & 1];
       const int first_cut = (it.start + it.tok0) / kManyRows, from = it.from, last = it.to;
       int v_exp = -100;  // of the V scale that the weights are times; a tile whose values are all 0 has the one before it
+      int v_low = 1000;  // the least exponent of the V scales so far (blocks: lanes 8..15)
       // the list of NaN values is free: the unit before the last has been written
       for (int i = lane; i < D; i += 32) my_bad[(k & 1) * 4 * D + i] = INT32_MAX;
       if (lane == 0) odd_unit[(k & 1) * 4 + warp - 8] = 0;
@@ -643,6 +726,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
         const int mi = m_it % L::kMetas;
         BlockMeta& meta = metas[mi];
         uint32_t ratio = 0;  // the lane's scale over the tile's (a block of 128: V's), as two fp16
+        bool apart = false;
         if (!wait_warp(L::kMetaEmpty + mi, ((m_it / L::kMetas) & 1) ^ 1)) break;
         if constexpr (kScale == kScaleOfToken) {
           if (warp == 8) {
@@ -665,10 +749,18 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
             float top = fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3]));
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            const bool cut = j >= first_cut;
+            const float least = top * power(cut ? -kApartCut : -kApart);
             if (top > 0.f) v_exp = min(max(exponent_up(top), -100), 120);
+            apart = cut && v_exp > v_low + kApartRise;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) apart |= sc[i] > 0.f && sc[i] < least;
+            apart = __any_sync(0xffffffffu, apart);
+            if (top > 0.f) v_low = apart ? -126 : min(v_low, v_exp);
             const float r = power(-v_exp);
-            *(float4*)&meta.v[4 * lane] = make_float4(sc[0] * r, sc[1] * r, sc[2] * r, sc[3] * r);
-            if (lane == 0) meta.factor = 1.f, meta.shift = (float)v_exp;
+            *(float4*)&meta.v[4 * lane] = apart ? make_float4(lg2(sc[0]), lg2(sc[1]), lg2(sc[2]), lg2(sc[3]))
+                                                : make_float4(sc[0] * r, sc[1] * r, sc[2] * r, sc[3] * r);
+            if (lane == 0) meta.factor = 1.f, meta.shift = (float)v_exp, meta.apart = apart;
           }
         } else {
           float top = sc[0];
@@ -677,13 +769,24 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
             for (int d = 4; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
           }
           const int e = top > 0.f ? min(max(exponent_up(top), lane < 8 ? -120 : -100), 120) : v_exp;
+          if constexpr (kScale == kScaleOfBlock) {
+            const bool cut = (lane >= 8) & (j >= first_cut);
+            const float least = top * (cut ? power(-kApartCut) : power(-kApart));
+            const bool far = ((sc[0] > 0.f) & (sc[0] < least)) | (cut & (e > v_low + kApartRise));
+            apart = __any_sync(0xffffffffu, far);
+            v_low = top > 0.f ? (apart ? -126 : min(v_low, e)) : v_low;
+          }
           // K's codes have room for 2^6 more in fp16; the scale of a block of 128 is a factor of K's scores as it is
-          const float r = sc[0] * power(-e) * (lane < 8 ? 64.f : 1.f);
+          const float r = apart ? 1.f : sc[0] * power(-e) * (lane < 8 ? 64.f : 1.f);
           ratio = half2_of(r, r);
           v_exp = __shfl_sync(0xffffffffu, e, 8);
-          if (warp == 8 && lane == 0) {
-            meta.factor = kScale == kScaleOfBlock ? power(e) * 0x1p-6f : sc[0];
-            meta.shift = (float)v_exp;
+          if (warp == 8 && lane < (kScale == kScaleOfBlock ? 16 : 1)) {
+            if (kScale == kScaleOfBlock) meta.k[lane] = sc[0];
+            if (lane == 0) {
+              meta.factor = kScale == kScaleOfTile ? sc[0] : power(e) * 0x1p-6f;
+              meta.shift = (float)v_exp;
+              meta.apart = apart;
+            }
           }
           if constexpr (kScale == kScaleOfTile) ratio = __shfl_sync(0xffffffffu, ratio, 8);
         }

@@ -553,9 +553,11 @@ int wave_history_read(wave_t* h, int layer, int n_seq, const int32_t* cu_seqlens
  * rows *_stride elements apart; scale is > 0 and at most 2.3e38; n_heads /
  * n_kv_heads is at most 128.  Codes are exact factors of the products; scores,
  * the softmax's maximum and sums and the output are kept in fp32, the weights
- * are rounded to fp16 (11 bits) for the second product, and those below 2^-21 of a
- * row's largest (each times the V scale of its 128 slots) to 2^-32 of it.  Slots
- * that a row does not attend to never reach it, whatever they hold.  out must not
+ * are rounded to fp16 (11 bits) for the second product, and those below 2^-17 of a
+ * row's largest (each times the largest V scale of those of its 128 slots that the
+ * row attends to) to 2^-28 of it.  Slots that a row does not attend to never reach
+ * it, whatever they hold, but by the scale of a block that they share with slots
+ * that it does attend to.  out must not
  * overlap q.  Prompts whose tokens make up to 32 rows for a K/V head (tokens times
  * the heads that share it), and frames, go one way, longer prompts another: one
  * launch each, and one more where parts of the keys are joined (in fp32).  How the

@@ -7,7 +7,7 @@ import math
 import pytest
 import torch
 
-from test_gpu_history import BF, E4M3, HALF, TINY, U, Cache, _cu, _done, _gen, _queries, _wave
+from test_gpu_history import BF, E4M3, F16, HALF, TINY, U, Cache, _cu, _done, _far, _gen, _queries, _wave
 
 pytestmark = pytest.mark.gpu
 
@@ -61,6 +61,71 @@ def _run(c, q, lens, starts, H, D, frame=False, scale=None):
 
 def _rows(n, Hkv, D, seed):
     return [torch.randn(n, Hkv, D, generator=_gen(seed + j), device="cuda") * (1.5, 1.0)[j] for j in (0, 1)]
+
+
+# a prompt of few rows, one of many that begins the history, one that goes on, one whose rows lie in two tiles of 128 slots
+PROMPTS = [([12], [70]), ([200], [0]), ([150], [300]), ([90], [1000])]
+
+
+@pytest.mark.parametrize("lens,starts", PROMPTS)
+@pytest.mark.parametrize("block", [1, 16, 64, 128])
+@pytest.mark.parametrize("which", ["k", "v", "both"])
+@pytest.mark.parametrize("large", [1e3, 1e6, 1e12, 1e30])
+def test_later_tokens_do_not_reach_earlier_rows(lens, starts, block, which, large):
+    """Keys and values of the tokens from the middle of a prompt on that are finite and large: the rows before them stay
+    within a bound that knows nothing of them."""
+    H, Hkv, D = 4, 2, 64
+    n, s0 = lens[0], starts[0]
+    k, v = _rows(s0 + n, Hkv, D, 3)
+    at = s0 + n // 2
+    if which in ("k", "both"):
+        k[at:] *= large
+    if which in ("v", "both"):
+        v[at:] *= large
+    c = Cache(1, Hkv, (s0 + n + 3) // 4 * 4, D, block)
+    c.write(0, 0, k, v)
+    q, _ = _queries(n, H, D, BF)
+    # large keys give the rows that see them scores that fp32 does not hold to a part of a unit: rows before them are checked
+    rows = n // 2 if which != "v" else n
+    out = torch.full_like(q, 7.0)
+    w = _wave(H, D, S=1, T=c.T)
+    w.history_attention(0, [0, n], [0], [s0], q, c.kv, c.sc, Hkv, block, out)
+    _done(w)
+    ref, tol = seen_reference(c, q[:rows], [rows], [0], [s0], [0, rows], D ** -0.5)
+    worst = float(((out[:rows].double() - ref).abs() / tol).max())
+    assert worst <= 1.0, worst
+
+
+@pytest.mark.parametrize("block", [1, 16, 32, 128])
+@pytest.mark.parametrize("D,dtype", [(128, BF), (64, BF), (128, F16)])
+def test_one_later_value_far_from_the_others(block, D, dtype):
+    """A single V token 2^30 above (fp16: 2^12) or a run of small ones 2^30 below the others, in and before the prompt."""
+    H, Hkv, n, s0 = 3, 3, 300, 77
+    far = 2.0 ** (30 if dtype is BF else 12)
+    for change in ("later", "earlier", "small"):
+        k, v = _rows(s0 + n, Hkv, D, 8)
+        if change == "later":
+            v[s0 + 140] *= far
+        elif change == "earlier":
+            v[30] *= far
+        else:
+            v[:s0 + 100] /= far
+        c = Cache(1, Hkv, 380, D, block)
+        c.write(0, 0, k, v)
+        _run(c, _queries(n, H, D, dtype)[0], [n], [s0], H, D)
+
+
+@pytest.mark.parametrize("frame", [False, True])
+@pytest.mark.parametrize("block", [1, 16, 128])
+@pytest.mark.parametrize("lo,hi", [(-6, 6), (-40, 40), (-100, -60), (60, 90), (-60, 60)])
+def test_values_of_many_magnitudes(frame, block, lo, hi):
+    """V scales that differ by many powers of two, and runs of zeros, within a bound from the slots that a row sees."""
+    lens, starts = ([1, 1, 1], [500, 39, 1100]) if frame else ([150, 1, 30], [300, 39, 1100])
+    c = Cache(3, 2, 1132, 64, block)
+    for i, (n, s0) in enumerate(zip(lens, starts)):
+        k, v = _rows(n + s0, 2, 64, 20 + i)
+        c.write(i, 0, k, v * _far(lo, hi)(n + s0))
+    _run(c, _queries(sum(lens), 4, 64, BF)[0], lens, starts, 4, 64, frame=frame)
 
 
 @pytest.mark.parametrize("frame", [False, True])
