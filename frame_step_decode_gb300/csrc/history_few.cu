@@ -270,7 +270,7 @@ __global__ void __launch_bounds__((FewShape<D, kN>::kThreads), 1) k_history_few(
           top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
           const int ex = min(max((int)(top >> 7) - 127, -113), 127);  // its exponent
           up = __int_as_float((14 - ex + 127) << 23);
-          factor = p.scale2 * __int_as_float((ex + 127) << 23) * 0x1p-14f;
+          factor = p.scale2 * (__int_as_float((ex + 127) << 23) * 0x1p-14f);
         }
 #pragma unroll
         for (int h = 0; h < kH; ++h)

@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
         top = max(top & 0xFFFFu, top >> 16);
         const int ex = min(max((int)(top >> 7) - 127, -113), 127);
         up = power(14 - ex);
-        factor = p.a.scale2 * power(ex) * 0x1p-14f;
+        factor = p.a.scale2 * (power(ex) * 0x1p-14f);
       }
       uint8_t* dst = smem + st * L::kTile + row * 128;
 #pragma unroll

@@ -557,7 +557,8 @@ int wave_history_read(wave_t* h, int layer, int n_seq, const int32_t* cu_seqlens
  * row's largest (each times the largest V scale of those of its 128 slots that the
  * row attends to) to 2^-28 of it.  Slots that a row does not attend to never reach
  * it, whatever they hold, but by the scale of a block that they share with slots
- * that it does attend to.  out must not
+ * that it does attend to.  (Keys of magnitude 2^105 and more, with block 1, give scores
+ * that are not finite.)  out must not
  * overlap q.  Prompts whose tokens make up to 32 rows for a K/V head (tokens times
  * the heads that share it), and frames, go one way, longer prompts another: one
  * launch each, and one more where parts of the keys are joined (in fp32).  How the

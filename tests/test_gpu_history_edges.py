@@ -163,6 +163,20 @@ def test_scores_that_rise_and_fall_far(frame, block, gap):
         _run(c, q, [n], [s0], H, D, frame=frame)
 
 
+@pytest.mark.parametrize("frame", [False, True])
+@pytest.mark.parametrize("block", [1, 16, 128])
+def test_the_largest_scale_of_scores(frame, block):
+    """scale near its limit with keys that keep the scores moderate: no factor between leaves fp32."""
+    H, D, n, s0 = 4, 64, 1 if frame else 100, 300
+    k, v = _rows(s0 + n, 2, D, 10)
+    c = Cache(1, 2, 404, D, block)
+    q = _queries(n, H, D, BF)[0].float()
+    q = q.sign() * (2.0 + q.abs() / 4)
+    for key, query, scale in ((2.0 ** -130, 1.0, 2.0e38), (2.0 ** -124, 2.0 ** 125, 0.25 / 64)):
+        c.write(0, 0, k * key, v)
+        _run(c, (q * query).to(BF), [n], [s0], H, D, frame=frame, scale=scale)
+
+
 @pytest.mark.parametrize("block", [16, 64])
 @pytest.mark.parametrize("frame", [False, True])
 @pytest.mark.parametrize("sizes", [(-60, 0, 40, 100), (40, 0), (20, 100), (120,)])
