@@ -364,18 +364,21 @@ __global__ void __launch_bounds__((FewShape<D, kN>::kThreads), 1) k_history_few(
       for (int d = 4; d <= 16; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
       return sum;
     };
+    // The sums in the values' own units are times 2^(e - m - bias), which the least
+    // scales take below fp32: twice the root of it.
+    auto half_unit = [&](int b, int x) { return e[b][x] == -INFINITY ? 0.f : ex2(0.5f * (e[b][x] - m[b][x] - kFewBias)); };
     // The unit's rows as sums that others join: divided by nothing, relative to the maxima m.
     auto leave_sums = [&](float* dst) {
 #pragma unroll
       for (int b = 0; b < kN; ++b)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const float sum = weights_of(l[b][x]), f = e[b][x] == -INFINITY ? 0.f : ex2(e[b][x] - m[b][x] - kFewBias);
+          const float sum = weights_of(l[b][x]), f = half_unit(b, x);
           const int row = 8 * b + 2 * t + x;
 #pragma unroll
           for (int k = 0; k < D / 32; ++k)
-            *(float4*)(dst + 4 * sums_at<D>(row, g * (D / 32) + k)) = make_float4(f * acc[b][2 * k][x], f * acc[b][2 * k][2 + x],
-                                                                                f * acc[b][2 * k + 1][x], f * acc[b][2 * k + 1][2 + x]);
+            *(float4*)(dst + 4 * sums_at<D>(row, g * (D / 32) + k)) =
+                make_float4(f * acc[b][2 * k][x] * f, f * acc[b][2 * k][2 + x] * f, f * acc[b][2 * k + 1][x] * f, f * acc[b][2 * k + 1][2 + x] * f);
           if (g == 0) *(float2*)(dst + kR * D + 2 * row) = make_float2(m[b][x], sum);
         }
     };
@@ -387,14 +390,14 @@ __global__ void __launch_bounds__((FewShape<D, kN>::kThreads), 1) k_history_few(
           const FewRow r = row_of<kR>(p, at, 8 * b + 2 * t + x);
           const float sum = weights_of(l[b][x]);
           if (!r.on) continue;
-          const float f = e[b][x] == -INFINITY ? 0.f : ex2(e[b][x] - m[b][x] - kFewBias), inv = f / sum;
+          const float f = half_unit(b, x), inv = f / sum;
           uint16_t* dst = p.out + r.row * p.out_stride + r.head * D + g * (D / 8);
 #pragma unroll
           for (int k = 0; k < D / 64; ++k) {
             uint32_t o[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float u = acc[b][4 * k + i][x] * inv, v = acc[b][4 * k + i][2 + x] * inv;
+              const float u = acc[b][4 * k + i][x] * inv * f, v = acc[b][4 * k + i][2 + x] * inv * f;
               o[i] = kF16 ? pair16<__half>(u, v) : pair16<__nv_bfloat16>(u, v);
             }
             *(uint4*)(dst + 8 * k) = make_uint4(o[0], o[1], o[2], o[3]);

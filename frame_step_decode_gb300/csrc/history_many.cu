@@ -751,7 +751,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
             for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
             const bool cut = j >= first_cut;
             const float least = top * power(cut ? -kApartCut : -kApart);
-            if (top > 0.f) v_exp = min(max(exponent_up(top), -100), 120);
+            if (top > 0.f) v_exp = min(exponent_up(top), 120);
             apart = cut && v_exp > v_low + kApartRise;
 #pragma unroll
             for (int i = 0; i < 4; ++i) apart |= sc[i] > 0.f && sc[i] < least;
@@ -768,7 +768,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
 #pragma unroll
             for (int d = 4; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
           }
-          const int e = top > 0.f ? min(max(exponent_up(top), lane < 8 ? -120 : -100), 120) : v_exp;
+          const int e = top > 0.f ? min(max(exponent_up(top), lane < 8 ? -120 : -126), 120) : v_exp;
           if constexpr (kScale == kScaleOfBlock) {
             const bool cut = (lane >= 8) & (j >= first_cut);
             const float least = top * (cut ? power(-kApartCut) : power(-kApart));

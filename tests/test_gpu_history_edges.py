@@ -165,6 +165,19 @@ def test_scores_that_rise_and_fall_far(frame, block, gap):
 
 @pytest.mark.parametrize("frame", [False, True])
 @pytest.mark.parametrize("block", [1, 16, 128])
+def test_values_at_the_lower_end_of_fp32(frame, block):
+    """V scales of 2^-120 and less, down to the least ordinary number."""
+    H, D, n, s0 = 4, 64, 1 if frame else 100, 300
+    for e in (-108, -114):
+        k, v = _rows(s0 + n, 2, D, 9)
+        c = Cache(1, 2, 400 + 4, D, block)
+        c.write(0, 0, k, v * 2.0 ** e)
+        out = _run(c, _queries(n, H, D, BF)[0], [n], [s0], H, D, frame=frame)
+        assert bool((out != 0).any())
+
+
+@pytest.mark.parametrize("frame", [False, True])
+@pytest.mark.parametrize("block", [1, 16, 128])
 def test_the_largest_scale_of_scores(frame, block):
     """scale near its limit with keys that keep the scores moderate: no factor between leaves fp32."""
     H, D, n, s0 = 4, 64, 1 if frame else 100, 300
