@@ -164,11 +164,6 @@ struct ManySmem {
 };
 static_assert(ManySmem<128>::kTotal <= 232448 && ManySmem<64>::kTotal <= 232448, "shared memory of a CTA");
 
-__device__ __forceinline__ uint32_t half2_of(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 __device__ __forceinline__ uint32_t mul_half2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -180,11 +175,6 @@ __device__ __forceinline__ int exponent_up(float x) {
   return (int)(u >> 23) - 127 + ((u & 0x7FFFFFu) != 0);
 }
 __device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
-__device__ __forceinline__ float lg2(float x) {
-  float y;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 template <int D, bool kF16, int kScale>
 __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_constant__ ManyParams p) {
@@ -1085,14 +1075,8 @@ static bool cut_line(ManyParams& p, int sms) {
 
 template <int D, bool kF16, int kScale>
 static cudaError_t configure() {
-  cudaFuncAttributes a;
-  cudaError_t e = cudaFuncGetAttributes(&a, k_history_many<D, kF16, kScale>);
-  if (e != cudaSuccess) return e;
-  // those that take more registers get them from what the launch had
-  if (a.numRegs * kManyThreads < 256 * kRegsRows + 128 * (kRegsCodes + kRegsMma) || kRegsRows < a.numRegs || kRegsCodes > a.numRegs ||
-      kRegsMma > a.numRegs)
-    return cudaErrorInvalidConfiguration;
-  return cudaFuncSetAttribute(k_history_many<D, kF16, kScale>, cudaFuncAttributeMaxDynamicSharedMemorySize, ManySmem<D>::kTotal);
+  return configure_split(k_history_many<D, kF16, kScale>, kManyThreads, 256 * kRegsRows + 128 * (kRegsCodes + kRegsMma), kRegsRows,
+                         std::max(kRegsCodes, kRegsMma), ManySmem<D>::kTotal);
 }
 
 template <int D, bool kF16>
