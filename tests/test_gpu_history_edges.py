@@ -128,6 +128,30 @@ def test_values_of_many_magnitudes(frame, block, lo, hi):
     _run(c, _queries(sum(lens), 4, 64, BF)[0], lens, starts, 4, 64, frame=frame)
 
 
+@pytest.mark.parametrize("block", [1, 16, 64])
+@pytest.mark.parametrize("D,dtype,lo,hi", [(128, BF, -30, 30), (64, BF, -30, 30), (128, F16, -20, 6), (64, F16, -20, 6)])
+def test_scales_far_apart_in_a_history_that_many_ctas_share(block, D, dtype, lo, hi):
+    """Units whose keys are divided among CTAs, shared heads, two tiles of rows to a unit, K's scales far apart too; and NaN in
+    V behind a row's end, which reaches the rows that attend to it alone."""
+    H, Hkv, lens, starts = 6, 2, [300, 70, 33], [2500, 1100, 0]
+    c, cu = Cache(3, Hkv, 2800, D, block), _cu(lens)
+    for i, (n, s0) in enumerate(zip(lens, starts)):
+        k, v = _rows(n + s0, Hkv, D, 40 + i)
+        c.write(i, 0, k * _far(-12, 1)(n + s0).roll(17, 0), v * _far(lo, hi)(n + s0))
+    q = _queries(cu[-1], H, D, dtype)[0]
+    out = _run(c, q, lens, starts, H, D)
+    c.kv[0, 1, 0, 1, 2500 + 150, 5] = 0x7F
+    c.kv[0, 1, 2, 0, 20, D - 1] = 0xFF
+    again, w = torch.full_like(q, 7.0), _wave(H, D, S=3, T=c.T)
+    w.history_attention(0, cu, [0, 1, 2], starts, q, c.kv, c.sc, Hkv, block, again)
+    _done(w)
+    nan = torch.zeros(q.shape, dtype=torch.bool, device="cuda")
+    nan[150:300, 3:, 5] = True
+    nan[cu[2] + 20:, :3, D - 1] = True
+    assert torch.equal(again.isnan(), nan)
+    assert torch.equal(again[~nan], out[~nan])
+
+
 @pytest.mark.parametrize("frame", [False, True])
 @pytest.mark.parametrize("block", [1, 16, 128])
 @pytest.mark.parametrize("small,large", [(0.0, 2.0 ** 60), (0.0, 1.0), (2.0 ** -100, 2.0 ** 60)])
