@@ -22,10 +22,10 @@
 // row's largest value.
 //
 // Measured (captured launches in a row): a frame of 80 sessions of up to 3000
-// tokens, 32/8 heads of 128, blocks of 64, 54 us = 4.55 TB/s, of 20 sessions of
+// tokens, 32/8 heads of 128, blocks of 64, 54.6 us = 4.5 TB/s, of 20 sessions of
 // 6000 tokens 46 us = 5.4 TB/s; 56 sessions of up to 1500 tokens, 32 heads, a scale
 // for each token, 84 us = 4.25 TB/s; one session of 32001 tokens, 32/8 heads,
-// 22.5 us; one after 1500 tokens, 16 x 64, 9.3 us; 25 tokens after 1475, 10.6 us.
+// 22.8 us; one after 1500 tokens, 16 x 64, 9.4 us; 25 tokens after 1475, 10.6 us.
 // Of some 80,000 cycles of the frame of 80, about 8,000 are the begin (positions,
 // the line, first loads) and 9,000 the joins; in the loop between the rate is
 // about 5.7 TB/s, what HBM gives.

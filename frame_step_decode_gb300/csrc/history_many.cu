@@ -14,19 +14,19 @@
 // exponents, so that neither costs anything an element; in tiles with several
 // scales codes are brought to the largest of them in fp16 (exact for powers of
 // two), and with a scale for each token the softmax's threads multiply the
-// columns of S and of P in fp32.
+// columns of S and of P in fp32; scales that lie far apart go another way (kApart).
 //
 // All units' key blocks are one line, cut evenly among the SMs: a unit's blocks
 // in several CTAs leave fp32 sums, which a second launch joins.
 //
 // Measured (captured launches in a row): 1024 tokens after 7168, 32 heads of 128,
-// fp16, blocks of 128, 112 us = 1.15 PFLOP/s (the join 13 us when profiled alone); 2001 after 4096
-// with 300, 17 and 1 others, 32/8 heads, bf16, blocks of 32, 175 us = 1.0 PFLOP/s;
-// 2048 after 6144, 32 heads, a scale for each token, 283 us = 0.85 PFLOP/s; 8192
-// tokens from the first, 434 to 444 us.  A block of 128 keys and both streams
-// takes about 3500 cycles, 2048 of them the tensor core's (its pipe is active 55%
-// of the time): the MMAs wait for the chain from S to P, and the conversion
-// shares the shared memory with them.
+// fp16, blocks of 128, 113 us = 1.14 PFLOP/s (the join 14 us when profiled alone);
+// 2001 after 4096 with 300, 17 and 1 others, 32/8 heads, bf16, blocks of 32, 177 us =
+// 0.99 PFLOP/s; 2048 after 6144, 32 heads, a scale for each token, 288 us = 0.83
+// PFLOP/s, 16 heads of 64, blocks of 64, 86 us; 8192 tokens from the first, 437 to
+// 447 us.  A block of 128 keys and both streams takes about 3500 cycles, 2048 of
+// them the tensor core's (its pipe is active 55% of the time): the MMAs wait for
+// the chain from S to P, and the conversion shares the shared memory with them.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>

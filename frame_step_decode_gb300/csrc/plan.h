@@ -66,7 +66,7 @@ struct Workspace {
   float* zx = nullptr;
   uint16_t* ssm_out = nullptr;
   float* part_o = nullptr;     // attention over prompts: sums of parts of the keys, two per SM, ...
-  float2* part_ml = nullptr;   // ... and their maxima and sums of weights
+  float2* part_ml = nullptr;   // ... and what they are relative to, and their sums of weights
   int* hist_cnt = nullptr;     // attention over the history: CTAs that have left a unit's sums (0 between launches)
   float* seg_state = nullptr;  // hybrid: states of prompt segments, one per SM, ...
   float* seg_decay = nullptr;  // ... and their decays

@@ -439,7 +439,7 @@ typedef struct {
   int scaling;     /* WAVE_ROPE_PLAIN; _LINEAR: frequency / factor; _PARTS: by turns, below */
   float factor;    /* > 0 (LINEAR, PARTS) */
   float original;  /* PARTS: positions the model was trained on, > 0 */
-  float fast;      /* PARTS: pairs of at least this many turns over `original` keep their frequency, ... */
+  float fast;      /* PARTS: pairs of at least this many turns over `original` keep their frequency (turns, not pairs' numbers), ... */
   float slow;      /* ... those of at most this many get frequency / factor; between the two, linear in the turns; 0 <= slow < fast */
   float amplitude; /* multiplies cosine and sine (1: none) */
 } wave_rope_config;
@@ -490,11 +490,14 @@ int wave_rope_apply_at(const wave_rope* rope, int64_t rows, const int32_t* posit
  *   kv_fp8     uint8 [L][2][S_max][n_kv_heads][T_max][D]
  *   kv_scales  float [L][2][S_max][n_kv_heads][ceil(T_max / block)]
  *
- * with L, S_max, T_max and D of the handle (L: its attention layers).  block is
- * 1, 16, 32, 64 or 128.  With block 1 and n_kv_heads = n_heads it is the step's
- * own history, by the step's own rule (scale = amax / 448): what
- * wave_prompt_append and the steps write, these calls read, and the other way
- * round.  So a later prompt of a live session goes on from its history.
+ * with L, S_max, T_max and D of the handle (L: its attention layers; a handle's
+ * capacity is that of unshared heads, 2 L S_max n_heads T_max < 2^31, whatever
+ * n_kv_heads is).  block is 1, 16, 32, 64 or 128.  With block 1 and n_kv_heads =
+ * n_heads it is the step's own history, by the step's own rule (scale = amax /
+ * 448): what wave_prompt_append and the steps write, these calls read, and the
+ * other way round.  So a later prompt of a live session goes on from its history.
+ * (v has wave_prompt_append's bits; k, turned here for every position and there by
+ * a table of fp32 values, is the same but for those roundings: a code may be the next one.)
  *
  * wave_sessions_copy and wave_kv_quantize know the step's own form only.
  *
@@ -506,10 +509,10 @@ int wave_rope_apply_at(const wave_rope* rope, int64_t rows, const int32_t* posit
  * NaN is held as NaN, whatever the scale becomes.  An infinity is held as +-448
  * s of the scale that the block has when it is added (which it does not raise;
  * where nothing finite but 0 is there, the least ordinary number), and is from
- * then on that value.  The first token that a call
- * writes to a block at the block's first place begins the block anew; one at a
- * later place goes on with the scale that the block has.  Slots of a block
- * behind the last token written keep their codes and mean nothing.  (Attention
+ * then on that value.  The first token that a call writes to a block at the
+ * block's first place begins the block anew; one at a later place goes on with
+ * the scale that the block has.  Slots of a block behind the last token written
+ * keep their codes and mean nothing.  (Attention
  * over blocks filled by other means, with scales that are no powers of two, takes
  * them and their products with a code to fp16's 11 bits; scales are not negative.)
  *
