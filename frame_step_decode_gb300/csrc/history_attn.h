@@ -34,6 +34,15 @@ __device__ __forceinline__ float lg2(float x) {
   asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// Sums that are joined are held over 2^12 of the values' units and relative to
+// their weights' sum brought between 1 and 2, so that the sums of values near
+// fp32's end do not leave it.
+constexpr float kPartBias = 12.f;
+// The exponent of a sum of weights (0 for one that is 0, infinite or NaN) ...
+__device__ __forceinline__ int exponent_of_sum(float l) { return l > 0.f && l < INFINITY ? (int)(__float_as_uint(l) >> 23) - 127 : 0; }
+// ... and the factor that takes joined sums to the output.
+__device__ __forceinline__ float joined_factor(float l) { return 4096.f / l; }
+
 // Whether one of four codes is NaN.
 __device__ __forceinline__ bool any_nan_code(uint32_t w) { return (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0; }
 

@@ -25,7 +25,7 @@
 // tokens, 32/8 heads of 128, blocks of 64, 54.6 us = 4.5 TB/s, of 20 sessions of
 // 6000 tokens 46 us = 5.4 TB/s; 56 sessions of up to 1500 tokens, 32 heads, a scale
 // for each token, 84 us = 4.25 TB/s; one session of 32001 tokens, 32/8 heads,
-// 22.8 us; one after 1500 tokens, 16 x 64, 9.4 us; 25 tokens after 1475, 10.6 us.
+// 23.1 us; one after 1500 tokens, 16 x 64, 9.4 us; 25 tokens after 1475, 10.7 us.
 // Of some 80,000 cycles of the frame of 80, about 8,000 are the begin (positions,
 // the line, first loads) and 9,000 the joins; in the loop between the rate is
 // about 5.7 TB/s, what HBM gives.
@@ -356,20 +356,22 @@ __global__ void __launch_bounds__((FewShape<D, kN>::kThreads), 1) k_history_few(
     };
     // The sums in the values' own units are times 2^(e - m - bias), which the least
     // scales take below fp32: twice the root of it.
-    auto half_unit = [&](int b, int x) { return e[b][x] == -INFINITY ? 0.f : ex2(0.5f * (e[b][x] - m[b][x] - kFewBias)); };
-    // The unit's rows as sums that others join: divided by nothing, relative to the maxima m.
+    auto half_unit = [&](int b, int x, float less) { return e[b][x] == -INFINITY ? 0.f : ex2(0.5f * (e[b][x] - m[b][x] - kFewBias - less)); };
+    // The unit's rows as sums that others join: divided by a power of two, which goes to the maxima m.
     auto leave_sums = [&](float* dst) {
 #pragma unroll
       for (int b = 0; b < kN; ++b)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const float sum = weights_of(l[b][x]), f = half_unit(b, x);
+          const float sum = weights_of(l[b][x]);
+          const int es = exponent_of_sum(sum);
+          const float f = half_unit(b, x, (float)es + kPartBias);
           const int row = 8 * b + 2 * t + x;
 #pragma unroll
           for (int k = 0; k < D / 32; ++k)
             *(float4*)(dst + 4 * sums_at<D>(row, g * (D / 32) + k)) =
                 make_float4(f * acc[b][2 * k][x] * f, f * acc[b][2 * k][2 + x] * f, f * acc[b][2 * k + 1][x] * f, f * acc[b][2 * k + 1][2 + x] * f);
-          if (g == 0) *(float2*)(dst + kR * D + 2 * row) = make_float2(m[b][x], sum);
+          if (g == 0) *(float2*)(dst + kR * D + 2 * row) = make_float2(m[b][x] + (float)es, sum * __int_as_float((127 - es) << 23));
         }
     };
     auto finish_unit = [&]() {
@@ -380,7 +382,7 @@ __global__ void __launch_bounds__((FewShape<D, kN>::kThreads), 1) k_history_few(
           const FewRow r = row_of<kR>(p, at, 8 * b + 2 * t + x);
           const float sum = weights_of(l[b][x]);
           if (!r.on) continue;
-          const float f = half_unit(b, x), inv = f / sum;
+          const float f = half_unit(b, x, 0.f), inv = f / sum;
           uint16_t* dst = p.out + r.row * p.out_stride + r.head * D + g * (D / 8);
 #pragma unroll
           for (int k = 0; k < D / 64; ++k) {
@@ -686,7 +688,7 @@ __global__ void __launch_bounds__((FewShape<D, kN>::kThreads), 1) k_history_few(
         const int row = (q0 + 32 * i) / (D / 4), quad = (q0 + 32 * i) % (D / 4);
         const FewRow r = row_of<kR>(p, u, row);
         if (!r.on) continue;
-        const float inv = 1.f / lx[i];
+        const float inv = joined_factor(lx[i]);
         *(uint2*)(p.out + r.row * p.out_stride + r.head * D + 4 * quad) =
             kF16 ? make_uint2(pair16<__half>(o[i].x * inv, o[i].y * inv), pair16<__half>(o[i].z * inv, o[i].w * inv))
                  : make_uint2(pair16<__nv_bfloat16>(o[i].x * inv, o[i].y * inv), pair16<__nv_bfloat16>(o[i].z * inv, o[i].w * inv));

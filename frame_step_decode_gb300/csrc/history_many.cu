@@ -57,7 +57,7 @@ struct ManyParams {
   int tile_tokens;      // tokens of a 128-row tile: 128 / group
   int ctas;
   ManyCut cut[kMaxCuts + 1];
-  float* part_o;        // [2 * CTA + (the unit begins there)][256 rows][D], in the values' own units
+  float* part_o;        // [2 * CTA + (the unit begins there)][256 rows][D], in the values' own units over 2^kPartBias
   float2* part_ml;      // the sums of their weights (second) and the power of two that both are relative to
   int wide;             // out's rows are 32-byte aligned
   ErrSink sink;
@@ -587,10 +587,10 @@ __global__ void __launch_bounds__(kManyThreads, 1) k_history_many(const __grid_c
         const bool on = row_tok < p.tile_tokens && tok < it.len;
         // the sum of the weights between 1 and 2, and O in the values' own units: times
         // 2^(m - bias - base), in halves where fp32 does not hold it
-        const int le = l > 0.f && l < INFINITY ? (int)(__float_as_uint(l) >> 23) - 127 : 0;
+        const int le = exponent_of_sum(l);
         l *= power(-le);
         base += (float)le;
-        const float units = m - kManyBias - base;
+        const float units = m - kManyBias - base - (part ? kPartBias : 0.f);
         const bool wide = __any_sync(0xffffffffu, fabsf(units) > 100.f);  // one factor does for the others
         const float half = ex2(0.5f * units), factor_o = (wide ? half : ex2(units)) * (part ? 1.f : 1.f / l);
         uint16_t* orow = p.a.out + (it.row0 + (on ? tok : 0)) * p.a.out_stride + (it.head * p.a.group + row_head) * D;
@@ -1029,7 +1029,7 @@ __global__ void __launch_bounds__(256) k_join_history(const __grid_constant__ Ma
       m = top;
     }
   }
-  const float inv = 1.f / l;
+  const float inv = joined_factor(l);
   *(uint2*)dst = kF16 ? make_uint2(half2_of(o.x * inv, o.y * inv), half2_of(o.z * inv, o.w * inv))
                       : make_uint2(pair16<__nv_bfloat16>(o.x * inv, o.y * inv), pair16<__nv_bfloat16>(o.z * inv, o.w * inv));
 }

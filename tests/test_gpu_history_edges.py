@@ -200,6 +200,20 @@ def test_values_at_the_lower_end_of_fp32(frame, block):
         assert bool((out != 0).any())
 
 
+@pytest.mark.parametrize("n,s0", [(1, 9000), (5, 9000), (100, 4000), (300, 0)])
+@pytest.mark.parametrize("block", [1, 16, 128])
+def test_values_at_the_upper_end_of_fp32(n, s0, block):
+    """Thousands of values of one sign near fp32's largest, whose sum leaves it, where warps and CTAs share a row's keys."""
+    H, Hkv, D = 2, 2, 64
+    for big in (2.0 ** 116, 2.0 ** 124):
+        k, v = _rows(s0 + n, Hkv, D, 11)
+        c = Cache(1, Hkv, (s0 + n + 3) // 4 * 4, D, block)
+        c.write(0, 0, k, (1.0 + v.abs()).clamp(max=3.0) * big)
+        for q in (torch.zeros(n, H, D, dtype=BF, device="cuda"), _queries(n, H, D, BF)[0]):
+            out = _run(c, q, [n], [s0], H, D, frame=n == 1)
+            assert bool(out.isfinite().all())
+
+
 @pytest.mark.parametrize("frame", [False, True])
 @pytest.mark.parametrize("block", [1, 16, 128])
 def test_the_largest_scale_of_scores(frame, block):
